@@ -206,8 +206,8 @@ def _run_own(case, state):
     if case["op"] == "gateup":
         return {"h": mx.gateup_silu(state["bank"], state["x"], state["offsets"], state["sorted_pair"], b)}
     if case["op"] == "down":
-        return {"out": mx.down_combine(state["bank"], state["h"], state["w"], state["offsets"], state["sorted_pair"],
-                                       state["pair_pos"], b, shared_gate=state["gate"])}
+        return {"out": mx.down_combine(state["bank"], state["h"], state["w"], state["offsets"], state["pair_pos"], b,
+                                       shared_gate=state["gate"])}
     out = mx.run_layer(state["bank"], state["x"], state["logits"], b, shared_gate=state["gate"])
     return {"out": out, "ids": b.ids, "w": b.w}
 
