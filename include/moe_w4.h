@@ -60,7 +60,7 @@
 extern "C" {
 #endif
 
-#define MOE_W4_ABI_VERSION 4
+#define MOE_W4_ABI_VERSION 5
 
 /* Version of the compiled library.  The Python binding refuses to load a
  * library whose version differs from the header it was written for. */
@@ -559,6 +559,130 @@ moe_status moe_dbg_w4a8_down_partials(
  * MOE_E_DEVICE.
  * ------------------------------------------------------------------- */
 moe_status moe_dbg_dec_stamps(unsigned long long* stamps);
+
+/* =====================================================================
+ * The layer on microscaled 4-bit floating point (MXFP4) weights.
+ *
+ * Format.  A row of C values (C % 32 == 0) is cut into blocks of 32.  A
+ * block is 32 codes of 4 bits (E2M1: sign, two exponent bits, one mantissa
+ * bit; codes 0..7 stand for 0, 0.5, 1, 1.5, 2, 3, 4, 6, codes 8..15 for
+ * their negatives; two codes per byte, the even index in the low nibble, as
+ * in moe_qmat) and one scale byte s (E8M0) that stands for 2^(s - 127); s =
+ * 255 stands for NaN and makes every value of its block NaN.
+ *
+ * Rows are quantised by the rule: a = the block's largest magnitude; s =
+ * floor(log2 a) - 2 + 127, held at 0 from below (a = 0 gives s = 0); each
+ * value / 2^(s - 127) is rounded to the nearest code, a tie to the even
+ * mantissa, and magnitudes above 6 become 6.  A block that holds an inf or
+ * a NaN gets s = 255 and codes 0.
+ *
+ * The layer is the one defined at the top of this file, with these weights
+ * and one of two kinds of activations:
+ *   MOE_A16  bf16 against the weights expanded to bf16 in registers (exact
+ *            for scale bytes 1..251; beyond, bf16's own range), fp32 sums
+ *   MOE_A4   x, and h in bf16, quantised by the rule above inside the call;
+ *            exact products of the codes, fp32 sums
+ * h is bf16 in both (rounded to nearest even), out bf16 or fp32.
+ * inf and NaN pass through: MOE_A16 as in IEEE arithmetic, MOE_A4 a NaN in
+ * every output that the marked block reaches.
+ * Build log "Two 96 GB Ascend cards run Qwen3.8 Flash-Next", section "Keep
+ * low-bit weights packed, do the work on the NPU" (expert weights stay
+ * packed, grouped projections with fused gate/up).
+ *
+ * The calls below take the expert banks as plain arrays, not as descriptor
+ * tables, and the sorted pairs' offsets, not tile lists: tiles are cut
+ * inside.  They keep no state in the workspace; calls that overlap in time
+ * need a workspace each.
+ * ===================================================================== */
+#define MOE_A4 2             /* activations in MXFP4 (moe_mx4_* calls only) */
+
+/* Matrices of one bank (HOST struct, device pointers): codes
+ * [n][N][K/2], scales [n][N][K/32], contiguous.  codes 16-byte, scales
+ * 4-byte aligned. */
+typedef struct moe_mxbank {
+  const uint8_t* codes;
+  const uint8_t* scales;
+} moe_mxbank;
+
+/* ---------------------------------------------------------------------
+ * moe_mx4_quant_rows -- rows to MXFP4 by the rule above (activations, or
+ * the weights of a checkpoint).
+ *   src    [R][ld] bf16 (src_is_f32 = 0) or fp32 (1); the first C entries of
+ *          each row are quantised.  Any ld >= C and any element alignment
+ *          (16-byte aligned rows are faster)
+ *   codes  uint8 [R][C/2] (out), 4-byte aligned;  scales uint8 [R][C/32] (out)
+ * Limits: C % 32 == 0 (else MOE_E_UNSUPPORTED).  R = 0 launches nothing.
+ * ------------------------------------------------------------------- */
+moe_status moe_mx4_quant_rows(const void* src, int src_is_f32, int R, int C, int ld,
+                              uint8_t* codes, uint8_t* scales, void* stream);
+
+/* ---------------------------------------------------------------------
+ * moe_mx4_dequant_rows -- the values that codes [R][C/2] and scales
+ * [R][C/32] stand for, to dst [R][ld] bf16 (dst_is_f32 = 0) or fp32 (1), the
+ * first C entries of each row.  Exact but for magnitudes beyond the type's
+ * largest (inf).  Limits and errors: as moe_mx4_quant_rows.
+ * ------------------------------------------------------------------- */
+moe_status moe_mx4_dequant_rows(const uint8_t* codes, const uint8_t* scales, int R, int C,
+                                void* dst, int dst_is_f32, int ld, void* stream);
+
+/* Workspace of the calls below (device memory, 256-byte aligned, need not
+ * be cleared); 0 for sizes they refuse. */
+size_t moe_mx4_workspace_bytes(int act, int T, int H, int I, int E, int k, int n_shared,
+                               int I_shared);
+
+/* ---------------------------------------------------------------------
+ * moe_mx4_gateup_silu -- grouped gate/up projection with SiLU(g) * u of
+ * every routed pair and every shared-expert token.
+ *   act        MOE_A16 or MOE_A4
+ *   x          bf16 [T][H]
+ *   w13        E matrices [2I][H] (gate rows 0..I-1, up rows I..2I-1)
+ *   w13_shared n_shared matrices [2*I_shared][H] (null when n_shared = 0)
+ *   offsets, sorted_pair: from moe_permute or moe_route_permute
+ *   h          bf16 [T*k + n_shared*T][max(I, I_shared)] (out): row r < T*k is
+ *              sorted row r, row T*k + s*T + t is shared expert s and token
+ *              t.  Rows past offsets[E] and columns past a row's own I (or
+ *              I_shared) are left as they were
+ *   flags      0
+ * Limits: H, I, I_shared multiples of 32, E <= 512, T <= 65535, T*k < 2^24,
+ * T*(k + n_shared)*H < 2^31 (else MOE_E_UNSUPPORTED).  x, h 16-byte aligned.
+ * ------------------------------------------------------------------- */
+moe_status moe_mx4_gateup_silu(int act, const uint16_t* x, int T, int H, int I, int E, int k,
+                               const moe_mxbank* w13, const moe_mxbank* w13_shared, int n_shared,
+                               int I_shared, const int32_t* offsets, const int32_t* sorted_pair,
+                               uint16_t* h, void* workspace, size_t ws_bytes, int flags,
+                               void* stream);
+
+/* ---------------------------------------------------------------------
+ * moe_mx4_down_combine -- grouped down projection of the h rows of
+ * moe_mx4_gateup_silu and the weighted sum into the tokens' outputs.
+ *   h          bf16, as above
+ *   w2         E matrices [H][I];  w2_shared: n_shared matrices [H][I_shared]
+ *   shared_gate, topk_w, pair_pos, out: as in moe_w4_down_combine
+ *   flags      MOE_OUT_F32 or 0
+ * A pair whose pair_pos is -1 adds nothing.  The sum runs in fp32 in the
+ * order j = 0..k-1, then the shared experts.  Limits: as above.
+ * ------------------------------------------------------------------- */
+moe_status moe_mx4_down_combine(int act, const uint16_t* h, int T, int H, int I, int E, int k,
+                                const moe_mxbank* w2, const moe_mxbank* w2_shared, int n_shared,
+                                int I_shared, const float* shared_gate, const float* topk_w,
+                                const int32_t* offsets, const int32_t* pair_pos, void* out,
+                                void* workspace, size_t ws_bytes, int flags, void* stream);
+
+/* ---------------------------------------------------------------------
+ * moe_mx4_layer -- the whole layer: routing of the logits (moe_route_topk),
+ * the sort by expert (moe_permute), moe_mx4_gateup_silu and
+ * moe_mx4_down_combine, with the outputs of all four.
+ *   flags      MOE_OUT_F32 or 0
+ * Limits: those of the parts.
+ * ------------------------------------------------------------------- */
+moe_status moe_mx4_layer(int act, const float* logits, const uint16_t* x, int T, int H, int I,
+                         int E, int k, int renormalize, const moe_mxbank* w13,
+                         const moe_mxbank* w2, const moe_mxbank* w13_shared,
+                         const moe_mxbank* w2_shared, int n_shared, int I_shared,
+                         const float* shared_gate, int32_t* topk_ids, float* topk_w,
+                         int32_t* counts, int32_t* offsets, int32_t* sorted_pair,
+                         int32_t* pair_pos, uint16_t* h, void* out, void* workspace,
+                         size_t ws_bytes, int flags, void* stream);
 
 #ifdef __cplusplus
 }

@@ -14,10 +14,10 @@ from typing import Optional
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe_w4.so")
-ABI_VERSION = 4
+ABI_VERSION = 5
 
 MOE_OK, MOE_E_INVAL, MOE_E_UNSUPPORTED, MOE_E_DEVICE, MOE_E_WORKSPACE = 0, -1, -2, -3, -4
-MOE_A16, MOE_A8 = 0, 1
+MOE_A16, MOE_A8, MOE_A4 = 0, 1, 2
 MOE_PATH_AUTO, MOE_PATH_GEMV, MOE_PATH_MFMA, MOE_PATH_MFMA16 = 0, 1, 2, 3
 MOE_QUANT_SEPARATE = 4
 MOE_X_PREPARED = 64
@@ -101,6 +101,23 @@ _SIGS = {
                                            c_void_p, c_size_t, c_int, c_void_p,
                                            c_int, c_void_p]),
     "moe_dbg_dec_stamps": (c_int, [c_void_p]),
+    "moe_mx4_quant_rows": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_void_p,
+                                   c_void_p]),
+    "moe_mx4_dequant_rows": (c_int, [c_void_p, c_void_p, c_int, c_int, c_void_p, c_int, c_int,
+                                     c_void_p]),
+    "moe_mx4_workspace_bytes": (c_size_t, [c_int] * 8),
+    "moe_mx4_gateup_silu": (c_int, [c_int, c_void_p, c_int, c_int, c_int, c_int, c_int,
+                                    c_void_p, c_void_p, c_int, c_int, c_void_p, c_void_p,
+                                    c_void_p, c_void_p, c_size_t, c_int, c_void_p]),
+    "moe_mx4_down_combine": (c_int, [c_int, c_void_p, c_int, c_int, c_int, c_int, c_int,
+                                     c_void_p, c_void_p, c_int, c_int, c_void_p, c_void_p,
+                                     c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_int,
+                                     c_void_p]),
+    "moe_mx4_layer": (c_int, [c_int, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int,
+                              c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int,
+                              c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                              c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_int,
+                              c_void_p]),
 }
 
 EXPORTED = tuple(_SIGS)
@@ -120,6 +137,11 @@ class QMatDesc(ctypes.Structure):
 
 
 assert ctypes.sizeof(QMatDesc) == 32
+
+
+class MxBankDesc(ctypes.Structure):
+    """struct moe_mxbank (host struct, device pointers)."""
+    _fields_ = [("codes", c_void_p), ("scales", c_void_p)]
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -339,3 +361,49 @@ def moe_dbg_w4a8_down_partials(h, T, H, I, E, k, w2, w2_shared, n_shared,
 def moe_dbg_dec_stamps(stamps, check=True):
     """The decode kernels' phase-stamp buffer (a MOE_DEC_STAMPS build only)."""
     return _call("moe_dbg_dec_stamps", _ptr(stamps), check=check)
+
+
+def _bank(b):
+    """A MxBankDesc by reference, or null."""
+    return None if b is None else ctypes.addressof(b)
+
+
+def moe_mx4_quant_rows(src, src_is_f32, R, C, ld, codes, scales, stream=None, check=True):
+    return _call("moe_mx4_quant_rows", _ptr(src), src_is_f32, R, C, ld, _ptr(codes),
+                 _ptr(scales), _stream(stream), check=check)
+
+
+def moe_mx4_dequant_rows(codes, scales, R, C, dst, dst_is_f32, ld, stream=None, check=True):
+    return _call("moe_mx4_dequant_rows", _ptr(codes), _ptr(scales), R, C, _ptr(dst), dst_is_f32,
+                 ld, _stream(stream), check=check)
+
+
+def moe_mx4_workspace_bytes(act, T, H, I, E, k, n_shared=0, I_shared=0) -> int:
+    return load().moe_mx4_workspace_bytes(act, T, H, I, E, k, n_shared, I_shared)
+
+
+def moe_mx4_gateup_silu(act, x, T, H, I, E, k, w13, w13_shared, n_shared, I_shared, offsets,
+                        sorted_pair, h, workspace, ws_bytes, flags=0, stream=None, check=True):
+    return _call("moe_mx4_gateup_silu", act, _ptr(x), T, H, I, E, k, _bank(w13),
+                 _bank(w13_shared), n_shared, I_shared, _ptr(offsets), _ptr(sorted_pair),
+                 _ptr(h), _ptr(workspace), ws_bytes, flags, _stream(stream), check=check)
+
+
+def moe_mx4_down_combine(act, h, T, H, I, E, k, w2, w2_shared, n_shared, I_shared, topk_w,
+                         offsets, pair_pos, out, workspace, ws_bytes, flags=0, stream=None,
+                         check=True, shared_gate=None):
+    return _call("moe_mx4_down_combine", act, _ptr(h), T, H, I, E, k, _bank(w2),
+                 _bank(w2_shared), n_shared, I_shared, _ptr(shared_gate), _ptr(topk_w),
+                 _ptr(offsets), _ptr(pair_pos), _ptr(out), _ptr(workspace), ws_bytes, flags,
+                 _stream(stream), check=check)
+
+
+def moe_mx4_layer(act, logits, x, T, H, I, E, k, renormalize, w13, w2, w13_shared, w2_shared,
+                  n_shared, I_shared, topk_ids, topk_w, counts, offsets, sorted_pair, pair_pos,
+                  h, out, workspace, ws_bytes, flags=0, stream=None, check=True,
+                  shared_gate=None):
+    return _call("moe_mx4_layer", act, _ptr(logits), _ptr(x), T, H, I, E, k, renormalize,
+                 _bank(w13), _bank(w2), _bank(w13_shared), _bank(w2_shared), n_shared, I_shared,
+                 _ptr(shared_gate), _ptr(topk_ids), _ptr(topk_w), _ptr(counts), _ptr(offsets),
+                 _ptr(sorted_pair), _ptr(pair_pos), _ptr(h), _ptr(out), _ptr(workspace),
+                 ws_bytes, flags, _stream(stream), check=check)

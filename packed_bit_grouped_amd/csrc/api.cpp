@@ -111,6 +111,8 @@ bool use_mfma(int act, int T, int H, int I, int E, int k, int n_shared,
 }  // namespace
 
 namespace moe {
+moe_status device_usable() { return check_device(); }
+
 WsLayout ws_layout(int act, int T, int H, int I, int E, int k, int n_shared,
                    int I_shared) {
   (void)I; (void)E; (void)I_shared;

@@ -30,6 +30,9 @@ struct WsLayout {
 WsLayout ws_layout(int act, int T, int H, int I, int E, int k, int n_shared,
                    int I_shared);
 
+// MOE_OK when the current device is a gfx950, else MOE_E_DEVICE.
+moe_status device_usable();
+
 // Arguments of the grouped projections (both kernels families).
 struct ProjArgs {
   int mode;                    // 0: gate/up (+SiLU*mul), 1: down

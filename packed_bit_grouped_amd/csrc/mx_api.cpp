@@ -1,0 +1,281 @@
+// C ABI of the MXFP4 layer: host-side argument checks, workspace layout and
+// dispatch (the same rules as api.cpp: nothing allocates, synchronizes or
+// reads device memory).
+#include <hip/hip_runtime.h>
+
+#include <cstring>
+
+#include "mx_common.h"
+
+using namespace moe;
+
+namespace {
+
+constexpr int kSortTile = 4096;   // the sort's own tile list is not used
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+moe_status from_hip(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_E_DEVICE; }
+int ld_h_of(int I, int n_shared, int I_shared) {
+  return n_shared > 0 && I_shared > I ? I_shared : I;
+}
+
+moe_status check_shape(int act, int T, int H, int I, int E, int k, int n_shared, int I_shared) {
+  if (act != MOE_A16 && act != MOE_A4) return MOE_E_INVAL;
+  if (T < 0 || H <= 0 || I <= 0 || E <= 0 || k <= 0 || n_shared < 0) return MOE_E_INVAL;
+  if (k > E) return MOE_E_INVAL;
+  if (n_shared > 0 && I_shared <= 0) return MOE_E_INVAL;
+  if (H % kMxBlock || I % kMxBlock || (n_shared > 0 && I_shared % kMxBlock))
+    return MOE_E_UNSUPPORTED;
+  if (E > kPermMaxE || T > 65535 || n_shared > 65535) return MOE_E_UNSUPPORTED;
+  if ((long long)T * k >= (1LL << 24)) return MOE_E_UNSUPPORTED;
+  const long long rows = (long long)T * ((long long)k + n_shared);
+  if (rows * H >= (1LL << 31) || rows * ld_h_of(I, n_shared, I_shared) >= (1LL << 31))
+    return MOE_E_UNSUPPORTED;
+  return MOE_OK;
+}
+
+bool bank_ok(const moe_mxbank* b) {
+  return b && b->codes && b->scales && aligned(b->codes, 16) && aligned(b->scales, 4);
+}
+
+MxWsLayout layout(int act, int T, int H, int I, int E, int k, int n_shared, int I_shared) {
+  MxWsLayout L;
+  const size_t R = (size_t)T * (k + n_shared);
+  const int ld_h = ld_h_of(I, n_shared, I_shared);
+  size_t off = 0;
+  L.qx = off;
+  if (act == MOE_A4) off += up256((size_t)T * (H / 2));
+  L.sx = off;
+  if (act == MOE_A4) off += up256((size_t)T * mx_scale_ld(H));
+  L.qh = off;
+  if (act == MOE_A4) off += up256(R * (ld_h / 2));
+  L.sh = off;
+  if (act == MOE_A4) off += up256(R * mx_scale_ld(ld_h));
+  L.y = off;
+  off += up256(R * H * 4);
+  L.tiles = off;
+  off += 256 + up256((size_t)moe_permute_max_tiles(T, k, E, kSortTile) * 16);
+  L.perm = off;
+  off += up256((size_t)permute_multi_blocks(T * k) * E * 4);
+  L.total = off;
+  return L;
+}
+
+moe_status check_ws(const void* ws, size_t bytes, const MxWsLayout& L) {
+  return ws && aligned(ws, 256) && bytes >= L.total ? MOE_OK : MOE_E_WORKSPACE;
+}
+
+// The projections' launches, every argument checked.
+moe_status gateup(int act, const uint16_t* x, int T, int H, int I, int E, int k,
+                  const moe_mxbank* w13, const moe_mxbank* w13_shared, int n_shared, int I_shared,
+                  const int32_t* offsets, const int32_t* sorted_pair, uint16_t* h, char* ws,
+                  hipStream_t s) {
+  const MxWsLayout L = layout(act, T, H, I, E, k, n_shared, I_shared);
+  MxProj a;
+  std::memset(&a, 0, sizeof(a));
+  a.x = x;
+  a.ld_in = H;
+  if (act == MOE_A4) {
+    uint8_t* q = reinterpret_cast<uint8_t*>(ws + L.qx);
+    uint8_t* sc = reinterpret_cast<uint8_t*>(ws + L.sx);
+    if (launch_mx_quant(x, 0, T, H, H, q, H / 2, sc, mx_scale_ld(H), s) != hipSuccess)
+      return MOE_E_DEVICE;
+    a.q = q;
+    a.s = sc;
+  }
+  a.w = w13->codes;
+  a.ws = w13->scales;
+  if (n_shared > 0) {
+    a.w_sh = w13_shared->codes;
+    a.ws_sh = w13_shared->scales;
+  }
+  a.K = a.K_sh = H;
+  a.U = I;
+  a.U_sh = n_shared > 0 ? I_shared : 0;
+  a.T = T;
+  a.k = k;
+  a.P = T * k;
+  a.E = E;
+  a.n_shared = n_shared;
+  a.offsets = offsets;
+  a.sorted_pair = sorted_pair;
+  a.out = h;
+  a.ld_out = ld_h_of(I, n_shared, I_shared);
+  return from_hip(launch_mx_rows16(a, 0, act == MOE_A4, s));
+}
+
+moe_status down(int act, const uint16_t* h, int T, int H, int I, int E, int k,
+                const moe_mxbank* w2, const moe_mxbank* w2_shared, int n_shared, int I_shared,
+                const float* shared_gate, const float* topk_w, const int32_t* offsets,
+                const int32_t* pair_pos, void* out, int out_f32, char* ws, hipStream_t s) {
+  const MxWsLayout L = layout(act, T, H, I, E, k, n_shared, I_shared);
+  const int ld_h = ld_h_of(I, n_shared, I_shared), P = T * k;
+  float* y = reinterpret_cast<float*>(ws + L.y);
+  MxProj a;
+  std::memset(&a, 0, sizeof(a));
+  a.x = h;
+  a.ld_in = ld_h;
+  if (act == MOE_A4) {
+    uint8_t* q = reinterpret_cast<uint8_t*>(ws + L.qh);
+    uint8_t* sc = reinterpret_cast<uint8_t*>(ws + L.sh);
+    const size_t lds = mx_scale_ld(ld_h);
+    hipError_t e = launch_mx_quant(h, 0, P, I, ld_h, q, ld_h / 2, sc, lds, s);
+    if (e == hipSuccess && n_shared > 0)
+      e = launch_mx_quant(h + (size_t)P * ld_h, 0, n_shared * T, I_shared, ld_h,
+                          q + (size_t)P * (ld_h / 2), ld_h / 2, sc + (size_t)P * lds, lds, s);
+    if (e != hipSuccess) return MOE_E_DEVICE;
+    a.q = q;
+    a.s = sc;
+  }
+  a.w = w2->codes;
+  a.ws = w2->scales;
+  if (n_shared > 0) {
+    a.w_sh = w2_shared->codes;
+    a.ws_sh = w2_shared->scales;
+  }
+  a.K = I;
+  a.K_sh = n_shared > 0 ? I_shared : I;
+  a.U = a.U_sh = H;
+  a.T = T;
+  a.k = k;
+  a.P = P;
+  a.E = E;
+  a.n_shared = n_shared;
+  a.offsets = offsets;
+  a.out = y;
+  a.ld_out = H;
+  if (launch_mx_rows16(a, 1, act == MOE_A4, s) != hipSuccess) return MOE_E_DEVICE;
+  return from_hip(launch_combine(y, H, topk_w, pair_pos, T, k, H, P, n_shared,
+                                 n_shared > 0 ? shared_gate : nullptr, out, out_f32, s));
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_mx4_quant_rows(const void* src, int src_is_f32, int R, int C, int ld,
+                              uint8_t* codes, uint8_t* scales, void* stream) {
+  if (R < 0 || C <= 0 || ld < C) return MOE_E_INVAL;
+  if (src_is_f32 != 0 && src_is_f32 != 1) return MOE_E_INVAL;
+  if (C % kMxBlock) return MOE_E_UNSUPPORTED;
+  if (R == 0) return MOE_OK;
+  if (!src || !codes || !scales) return MOE_E_INVAL;
+  if (!aligned(src, src_is_f32 ? 4 : 2) || !aligned(codes, 4)) return MOE_E_INVAL;
+  const moe_status d = device_usable();
+  if (d != MOE_OK) return d;
+  return from_hip(launch_mx_quant(src, src_is_f32, R, C, ld, codes, C / 2, scales, C / kMxBlock,
+                                  static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_mx4_dequant_rows(const uint8_t* codes, const uint8_t* scales, int R, int C,
+                                void* dst, int dst_is_f32, int ld, void* stream) {
+  if (R < 0 || C <= 0 || ld < C) return MOE_E_INVAL;
+  if (dst_is_f32 != 0 && dst_is_f32 != 1) return MOE_E_INVAL;
+  if (C % kMxBlock) return MOE_E_UNSUPPORTED;
+  if (R == 0) return MOE_OK;
+  if (!dst || !codes || !scales) return MOE_E_INVAL;
+  if (!aligned(dst, dst_is_f32 ? 4 : 2) || !aligned(codes, 4)) return MOE_E_INVAL;
+  const moe_status d = device_usable();
+  if (d != MOE_OK) return d;
+  return from_hip(launch_mx_dequant(codes, scales, R, C, dst, dst_is_f32, ld,
+                                    static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_mx4_workspace_bytes(int act, int T, int H, int I, int E, int k, int n_shared,
+                               int I_shared) {
+  if (check_shape(act, T, H, I, E, k, n_shared, I_shared) != MOE_OK) return 0;
+  return layout(act, T, H, I, E, k, n_shared, I_shared).total;
+}
+
+moe_status moe_mx4_gateup_silu(int act, const uint16_t* x, int T, int H, int I, int E, int k,
+                               const moe_mxbank* w13, const moe_mxbank* w13_shared, int n_shared,
+                               int I_shared, const int32_t* offsets, const int32_t* sorted_pair,
+                               uint16_t* h, void* workspace, size_t ws_bytes, int flags,
+                               void* stream) {
+  moe_status st = check_shape(act, T, H, I, E, k, n_shared, I_shared);
+  if (st != MOE_OK) return st;
+  if (flags) return MOE_E_INVAL;
+  if (T == 0) return MOE_OK;
+  if (!x || !offsets || !sorted_pair || !h || !aligned(x, 16) || !aligned(h, 16))
+    return MOE_E_INVAL;
+  if (!bank_ok(w13) || (n_shared > 0 && !bank_ok(w13_shared))) return MOE_E_INVAL;
+  st = check_ws(workspace, ws_bytes, layout(act, T, H, I, E, k, n_shared, I_shared));
+  if (st != MOE_OK) return st;
+  st = device_usable();
+  if (st != MOE_OK) return st;
+  return gateup(act, x, T, H, I, E, k, w13, w13_shared, n_shared, I_shared, offsets, sorted_pair,
+                h, static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
+}
+
+moe_status moe_mx4_down_combine(int act, const uint16_t* h, int T, int H, int I, int E, int k,
+                                const moe_mxbank* w2, const moe_mxbank* w2_shared, int n_shared,
+                                int I_shared, const float* shared_gate, const float* topk_w,
+                                const int32_t* offsets, const int32_t* pair_pos, void* out,
+                                void* workspace, size_t ws_bytes, int flags, void* stream) {
+  moe_status st = check_shape(act, T, H, I, E, k, n_shared, I_shared);
+  if (st != MOE_OK) return st;
+  if (flags & ~MOE_OUT_F32) return MOE_E_INVAL;
+  if (T == 0) return MOE_OK;
+  if (!h || !topk_w || !offsets || !pair_pos || !out) return MOE_E_INVAL;
+  if (!aligned(h, 16) || !aligned(out, 16)) return MOE_E_INVAL;
+  if (!bank_ok(w2) || (n_shared > 0 && !bank_ok(w2_shared))) return MOE_E_INVAL;
+  st = check_ws(workspace, ws_bytes, layout(act, T, H, I, E, k, n_shared, I_shared));
+  if (st != MOE_OK) return st;
+  st = device_usable();
+  if (st != MOE_OK) return st;
+  return down(act, h, T, H, I, E, k, w2, w2_shared, n_shared, I_shared, shared_gate, topk_w,
+              offsets, pair_pos, out, (flags & MOE_OUT_F32) ? 1 : 0,
+              static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
+}
+
+moe_status moe_mx4_layer(int act, const float* logits, const uint16_t* x, int T, int H, int I,
+                         int E, int k, int renormalize, const moe_mxbank* w13,
+                         const moe_mxbank* w2, const moe_mxbank* w13_shared,
+                         const moe_mxbank* w2_shared, int n_shared, int I_shared,
+                         const float* shared_gate, int32_t* topk_ids, float* topk_w,
+                         int32_t* counts, int32_t* offsets, int32_t* sorted_pair,
+                         int32_t* pair_pos, uint16_t* h, void* out, void* workspace,
+                         size_t ws_bytes, int flags, void* stream) {
+  moe_status st = check_shape(act, T, H, I, E, k, n_shared, I_shared);
+  if (st != MOE_OK) return st;
+  if ((flags & ~MOE_OUT_F32) || (renormalize != 0 && renormalize != 1)) return MOE_E_INVAL;
+  if (T == 0) return MOE_OK;
+  if (!logits || !x || !topk_ids || !topk_w || !counts || !offsets || !sorted_pair || !pair_pos ||
+      !h || !out)
+    return MOE_E_INVAL;
+  if (!aligned(x, 16) || !aligned(h, 16) || !aligned(out, 16)) return MOE_E_INVAL;
+  if (!bank_ok(w13) || !bank_ok(w2)) return MOE_E_INVAL;
+  if (n_shared > 0 && (!bank_ok(w13_shared) || !bank_ok(w2_shared))) return MOE_E_INVAL;
+  const MxWsLayout L = layout(act, T, H, I, E, k, n_shared, I_shared);
+  st = check_ws(workspace, ws_bytes, L);
+  if (st != MOE_OK) return st;
+  st = device_usable();
+  if (st != MOE_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  int32_t* n_tiles = reinterpret_cast<int32_t*>(ws + L.tiles);
+  int32_t* tiles = reinterpret_cast<int32_t*>(ws + L.tiles + 256);
+  const int P = T * k;
+  hipError_t e;
+  if (T <= kFusedRouteMaxT && P <= kFusedRouteMaxP) {
+    e = launch_route_permute(logits, T, E, k, renormalize, kSortTile, topk_ids, topk_w, counts,
+                             offsets, sorted_pair, pair_pos, tiles, n_tiles, s);
+  } else {
+    e = launch_route_topk(logits, T, E, k, renormalize, topk_ids, topk_w, s);
+    if (e == hipSuccess && permute_multi_blocks(P) > 0)
+      e = launch_permute_multi(topk_ids, P, E, kSortTile, counts, offsets, sorted_pair, pair_pos,
+                               tiles, n_tiles, reinterpret_cast<int32_t*>(ws + L.perm), s);
+    else if (e == hipSuccess)
+      e = launch_permute(topk_ids, P, E, kSortTile, counts, offsets, sorted_pair, pair_pos, tiles,
+                         n_tiles, s);
+  }
+  if (e != hipSuccess) return MOE_E_DEVICE;
+  st = gateup(act, x, T, H, I, E, k, w13, w13_shared, n_shared, I_shared, offsets, sorted_pair, h,
+              ws, s);
+  if (st != MOE_OK) return st;
+  return down(act, h, T, H, I, E, k, w2, w2_shared, n_shared, I_shared, shared_gate, topk_w,
+              offsets, pair_pos, out, (flags & MOE_OUT_F32) ? 1 : 0, ws, s);
+}
+
+}  // extern "C"

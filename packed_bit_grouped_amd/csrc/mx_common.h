@@ -1,0 +1,146 @@
+// Shared pieces of the microscaled 4-bit (MXFP4) kernels: E2M1 codes, two a
+// byte with the even index in the low nibble, and one E8M0 scale byte per 32
+// values along K.
+#pragma once
+
+#include "moe_internal.h"
+
+namespace moe {
+
+typedef int mx_i32x4 __attribute__((ext_vector_type(4)));
+typedef int mx_i32x8 __attribute__((ext_vector_type(8)));
+typedef float mx_f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int mx_u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 mx_bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 mx_bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kMxBlock = 32;      // values per scale
+constexpr int kMxNanScale = 255;  // scale byte of a block that held inf or NaN
+
+// Workspace of the projection calls (byte offsets).
+struct MxWsLayout {
+  size_t qx, sx;     // A4: codes [T][H/2], scales [T][scale_ld(H)]
+  size_t qh, sh;     // A4: codes [R][ld_h/2], scales [R][scale_ld(ld_h)]
+  size_t y;          // fp32 [R][H]
+  size_t tiles;      // layer: the sort's tile list and its count
+  size_t perm;       // layer: counts of the sort over many workgroups
+  size_t total;
+};
+
+// Row stride of the scale bytes of quantised activations: whole words, so
+// that the matrix kernels load four scales at once whatever K is.
+inline __host__ __device__ int mx_scale_ld(int K) { return (K / kMxBlock + 3) & ~3; }
+
+// Arguments of the grouped projections.
+struct MxProj {
+  const uint16_t* x;       // A16: bf16 rows (x by token, or h by sorted row)
+  const uint8_t* q;        // A4: their codes
+  const uint8_t* s;        // A4: their scales, row stride mx_scale_ld(ld_in)
+  int ld_in;               // row stride of x in values
+  const uint8_t* w;        // routed experts' codes [E][N][K/2]
+  const uint8_t* ws;       // and scales [E][N][K/32]
+  const uint8_t* w_sh;     // shared experts' [n_shared][N_sh][K_sh/2]
+  const uint8_t* ws_sh;
+  int K, K_sh;
+  int U, U_sh;             // gate/up: I pairs of rows; down: H rows
+  int T, k, P, E, n_shared;
+  const int32_t* offsets;      // [E + 1]
+  const int32_t* sorted_pair;  // [P] (gate/up)
+  void* out;               // gate/up: h bf16; down: y fp32
+  int ld_out;
+};
+
+// fp32 -> bf16 bits, to nearest even, NaN kept.
+__device__ __forceinline__ uint32_t mx_bf16(float f) {
+  return __builtin_bit_cast(uint16_t, (__bf16)f);
+}
+
+// Scale byte of a block from its largest magnitude (as fp32 bits without the
+// sign): floor(log2 a) - 2, held above -127; 255 when a is inf or NaN.
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax_bits) {
+  const uint32_t e = amax_bits >> 23;   // floor(log2 a) + 127 of a normal a
+  if (e == 255) return kMxNanScale;
+  return e > 2 ? e - 2 : 0;             // a below 2^-124, subnormals and 0: 2^-127
+}
+// The scale as the conversion instructions take it: fp32 with the byte as its
+// exponent field (they read that field alone: 0 is 2^-127, 255 is NaN).
+__device__ __forceinline__ float mx_scale_f32(uint32_t byte) {
+  return __uint_as_float(byte << 23);
+}
+
+// Eight codes (one word, K order) to eight bf16: code * 2^(byte - 127), exact
+// for byte >= 1 and below bf16's overflow.
+__device__ __forceinline__ mx_bf16x8 mx_word_to_bf16(uint32_t w, float scale) {
+  const mx_bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0);
+  const mx_bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1);
+  const mx_bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2);
+  const mx_bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3);
+  return mx_bf16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+// 16 rows x 128 K of codes against 128 K x 16 columns of codes, each lane with
+// 32 consecutive codes of its row (lane % 16) and its scale byte in byte J of
+// the scale word: exact products, fp32 sums.
+template <int J>
+__device__ __forceinline__ mx_f32x4 mx_mfma_fp4(mx_u32x4 a, uint32_t sa, mx_u32x4 b, uint32_t sb,
+                                                mx_f32x4 c) {
+  const mx_i32x8 av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+  const mx_i32x8 bv = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+  // formats 4, 4: E2M1 on both sides
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, J, (int)sa, J, (int)sb);
+}
+
+// Tile j (of tiles of TM rows, experts in order, empty experts skipped) of the
+// sorted rows, found by one wave from the offsets alone: lanes count the tiles
+// of 8 experts each (E <= 512), a prefix sum finds the owner.  False past the
+// last tile.  Rows are held inside [0, P] whatever the table says.
+template <int TM>
+__device__ __forceinline__ bool mx_find_tile(const int32_t* __restrict__ offsets, int E, int P,
+                                             int j, int& e, int& r0, int& r1) {
+  const int lane = threadIdx.x & 63;
+  const int per = (E + 63) / 64;   // experts per lane
+  int cnt = 0;
+  for (int i = 0; i < per; ++i) {
+    const int ex = lane * per + i;
+    if (ex < E) {
+      const int n = min(offsets[ex + 1], P) - max(offsets[ex], 0);
+      cnt += n > 0 ? (n + TM - 1) / TM : 0;
+    }
+  }
+  int pre = cnt;   // inclusive prefix over the lanes
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int o = __shfl_up(pre, d);
+    if (lane >= d) pre += o;
+  }
+  const uint64_t past = __ballot(pre > j);
+  if (past == 0) return false;
+  const int owner = __builtin_ctzll(past);
+  int left = j - (__builtin_amdgcn_readlane(pre, owner) - __builtin_amdgcn_readlane(cnt, owner));
+  for (int i = 0; i < per; ++i) {
+    const int ex = owner * per + i;
+    if (ex >= E) return false;
+    const int lo = max(offsets[ex], 0), hi = min(offsets[ex + 1], P);
+    const int nt = hi > lo ? (hi - lo + TM - 1) / TM : 0;
+    if (left < nt) {
+      e = ex;
+      r0 = lo + left * TM;
+      r1 = min(hi, r0 + TM);
+      return true;
+    }
+    left -= nt;
+  }
+  return false;
+}
+
+// Codes, scales: R rows of C values (row stride ld) to codes [R][ldq] bytes and
+// scale bytes [R][lds].
+hipError_t launch_mx_quant(const void* src, int is_f32, int R, int C, int ld, uint8_t* q,
+                           size_t ldq, uint8_t* s, size_t lds, hipStream_t st);
+hipError_t launch_mx_dequant(const uint8_t* q, const uint8_t* s, int R, int C, void* dst,
+                             int is_f32, int ld, hipStream_t st);
+// Grouped projections on tiles of 16 rows, K split over the workgroup's waves;
+// mode 0: gate/up with SiLU*mul to h, 1: down to y.
+hipError_t launch_mx_rows16(const MxProj& a, int mode, int act4, hipStream_t st);
+
+}  // namespace moe

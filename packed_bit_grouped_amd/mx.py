@@ -1,0 +1,234 @@
+"""The MoE FFN layer on microscaled 4-bit (MXFP4) expert weights: rows to the
+format and back, banks, per-step buffers and the layer's calls.
+
+PyTorch serves only as the device allocator and stream provider; every step
+runs in the HIP kernels behind the C ABI (include/moe_w4.h, the format and the
+layer are defined there).
+
+* ``quantize_rows`` / ``dequantize_rows``: bf16 or fp32 rows <-> codes, scales.
+* ``MxBank`` holds the expert matrices of a layer as (codes, scales) pairs of
+  stacked tensors: codes uint8 [n][N][K/2], scales uint8 [n][N][K/32].
+* ``MxBuffers`` preallocates every per-step buffer of one layer shape.
+* ``gateup_silu``, ``down_combine`` and ``run_layer`` issue the calls on the
+  current stream of the tensors' device (or on ``stream``).  The outputs are
+  the buffers' own tensors, overwritten by the next call on them; calls that
+  overlap in time (other streams) need buffers each.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _lib as L
+
+BLOCK = 32
+ACTS = {"a16": L.MOE_A16, "a4": L.MOE_A4, L.MOE_A16: L.MOE_A16, L.MOE_A4: L.MOE_A4}
+
+
+class _On:
+    """The tensors' device made current for a call, where it is not."""
+
+    def __init__(self, t):
+        if not t.is_cuda:
+            raise ValueError(f"expected a tensor on the GPU, got one on {t.device}")
+        d = t.get_device()
+        self.guard = None if d == torch.cuda.current_device() else torch.cuda.device(d)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _want(name, t, dtypes, shape, device=None):
+    """t has one of the dtypes, the shape, no gaps, and lies on the device."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
+        raise TypeError(f"{name}: expected a tensor of {' or '.join(map(str, dtypes))}, got "
+                        f"{getattr(t, 'dtype', type(t))}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: on {t.device}, the buffers are on {device}")
+    return t
+
+
+_BF16 = (torch.bfloat16, torch.int16)   # int16: bf16 bit patterns
+
+
+def quantize_rows(src, codes=None, scales=None, stream=None):
+    """bf16 or fp32 rows [R][C] (unit stride along C, any row stride) to MXFP4:
+    (codes uint8 [R][C/2], scales uint8 [R][C/32]), new unless given."""
+    if src.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"src: expected bfloat16 or float32, got {src.dtype}")
+    if src.dim() != 2:
+        raise ValueError(f"src: expected rows [R][C], got shape {tuple(src.shape)}")
+    R, C = src.shape
+    if C > 1 and R > 0 and src.stride(1) != 1:
+        raise ValueError("src: expected unit stride along C")
+    if C == 0 or C % BLOCK:
+        raise ValueError(f"src: rows of {C} values, expected a multiple of {BLOCK}")
+    ld = src.stride(0) if R > 1 else C
+    if ld < C:
+        raise ValueError("src: rows overlap")
+    if codes is None:
+        codes = torch.empty((R, C // 2), dtype=torch.uint8, device=src.device)
+    if scales is None:
+        scales = torch.empty((R, C // BLOCK), dtype=torch.uint8, device=src.device)
+    _want("codes", codes, (torch.uint8,), (R, C // 2), src.device)
+    _want("scales", scales, (torch.uint8,), (R, C // BLOCK), src.device)
+    with _On(src):
+        L.moe_mx4_quant_rows(src, int(src.dtype == torch.float32), R, C, ld, codes, scales, stream)
+    return codes, scales
+
+
+def dequantize_rows(codes, scales, dtype=torch.bfloat16, stream=None):
+    """The values [R][C] (bf16 or fp32) of codes [R][C/2] and scales [R][C/32]."""
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"dtype: expected bfloat16 or float32, got {dtype}")
+    if codes.dim() != 2:
+        raise ValueError(f"codes: expected rows [R][C/2], got shape {tuple(codes.shape)}")
+    R, C = codes.shape[0], 2 * codes.shape[1]
+    if C == 0 or C % BLOCK:
+        raise ValueError(f"codes: rows of {C} values, expected a multiple of {BLOCK}")
+    _want("codes", codes, (torch.uint8,), (R, C // 2))
+    _want("scales", scales, (torch.uint8,), (R, C // BLOCK), codes.device)
+    dst = torch.empty((R, C), dtype=dtype, device=codes.device)
+    with _On(codes):
+        L.moe_mx4_dequant_rows(codes, scales, R, C, dst, int(dtype == torch.float32), C, stream)
+    return dst
+
+
+def quantize_bank(w, stream=None):
+    """fp32 or bf16 matrices [n][N][K] to one (codes, scales) pair of MxBank."""
+    n, N, K = w.shape
+    codes, scales = quantize_rows(w.reshape(n * N, K), stream=stream)
+    return codes.view(n, N, K // 2), scales.view(n, N, K // BLOCK)
+
+
+class MxBank:
+    """The matrices of one layer: w13 [E][2I][H] and w2 [E][H][I] of the routed
+    experts, w13_shared [n_shared][2*I_shared][H] and w2_shared
+    [n_shared][H][I_shared] of the shared ones, each a (codes, scales) pair.
+    A bank for one of the projections alone holds that projection's pairs."""
+
+    def __init__(self, w13=None, w2=None, w13_shared=None, w2_shared=None):
+        self.pairs, self.desc, self.shape = {}, {}, {}
+        self.device = None
+        for tag, p in (("w13", w13), ("w2", w2), ("w13_shared", w13_shared),
+                       ("w2_shared", w2_shared)):
+            self.pairs[tag], self.desc[tag], self.shape[tag] = p, None, None
+            if p is None:
+                continue
+            codes, scales = p
+            if codes.dim() != 3:
+                raise ValueError(f"{tag}: expected codes [n][N][K/2], got {tuple(codes.shape)}")
+            n, N, K = codes.shape[0], codes.shape[1], 2 * codes.shape[2]
+            _want(tag + " codes", codes, (torch.uint8,), (n, N, K // 2), self.device)
+            self.device = codes.device
+            _want(tag + " scales", scales, (torch.uint8,), (n, N, K // BLOCK), self.device)
+            self.desc[tag] = L.MxBankDesc(codes.data_ptr(), scales.data_ptr())
+            self.shape[tag] = (n, N, K)
+
+    def need(self, tag, n, N, K):
+        """The descriptor of the pair `tag`, whose shape has to be (n, N, K)."""
+        if n == 0:
+            return None
+        if self.shape[tag] != (n, N, K):
+            raise ValueError(f"{tag}: the bank holds {self.shape[tag]} (n, N, K), the buffers "
+                             f"are for {(n, N, K)}")
+        return self.desc[tag]
+
+
+class MxBuffers:
+    """Every per-step buffer of one layer shape, allocated once."""
+
+    def __init__(self, T, H, I, E, k, n_shared=0, I_shared=0, act="a16", device="cuda",
+                 out_f32=False):
+        if act not in ACTS:
+            raise ValueError(f"act: expected 'a16' or 'a4', got {act!r}")
+        self.T, self.H, self.I, self.E, self.k = T, H, I, E, k
+        self.n_shared, self.I_shared, self.act = n_shared, I_shared, ACTS[act]
+        P = T * k
+        self.P, self.R = P, P + n_shared * T
+        self.ld_h = max(I, I_shared if n_shared else 0)
+        self.ws_bytes = L.moe_mx4_workspace_bytes(self.act, T, H, I, E, k, n_shared, I_shared)
+        if self.ws_bytes == 0:
+            raise ValueError(f"unsupported layer shape: T={T} H={H} I={I} E={E} k={k} "
+                             f"n_shared={n_shared} I_shared={I_shared}")
+        dev = torch.device(device)
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.device = dev
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.ids = torch.empty((T, k), **i32)
+        self.w = torch.empty((T, k), dtype=torch.float32, device=dev)
+        self.counts = torch.empty(E, **i32)
+        self.offsets = torch.empty(E + 1, **i32)
+        self.sorted_pair = torch.empty(P, **i32)
+        self.pair_pos = torch.empty(P, **i32)
+        # zeroed once: the columns past a shorter expert's I are never written
+        self.h = torch.zeros((self.R, self.ld_h), dtype=torch.bfloat16, device=dev)
+        self.out_flags = L.MOE_OUT_F32 if out_f32 else 0
+        self.out = torch.empty((T, H), dtype=torch.float32 if out_f32 else torch.bfloat16,
+                               device=dev)
+        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=dev)
+
+
+def _gate(shared_gate, B):
+    if shared_gate is None or not B.n_shared:
+        return None
+    return _want("shared_gate", shared_gate, (torch.float32,), (B.T, B.n_shared), B.device)
+
+
+def gateup_silu(bank, x, offsets, sorted_pair, B, stream=None):
+    """h [T*k + n_shared*T][max(I, I_shared)] in bf16 (B.h) of x bf16 [T][H] and
+    the sort's tables (int32): rows in the order of the sort, then the shared
+    experts' tokens."""
+    _want("x", x, _BF16, (B.T, B.H), B.device)
+    _want("offsets", offsets, (torch.int32,), (B.E + 1,), B.device)
+    _want("sorted_pair", sorted_pair, (torch.int32,), (B.P,), B.device)
+    w13 = bank.need("w13", B.E, 2 * B.I, B.H)
+    sh = bank.need("w13_shared", B.n_shared, 2 * B.I_shared, B.H)
+    with _On(B.h):
+        L.moe_mx4_gateup_silu(B.act, x, B.T, B.H, B.I, B.E, B.k, w13, sh, B.n_shared, B.I_shared,
+                              offsets, sorted_pair, B.h, B.ws, B.ws_bytes, 0, stream)
+    return B.h
+
+
+def down_combine(bank, h, w, offsets, pair_pos, B, shared_gate=None, stream=None):
+    """out [T][H] (B.out) of h (as from gateup_silu), the gate weights w fp32
+    [T][k] and the sort's tables; shared_gate fp32 [T][n_shared]: gate logits of
+    the shared experts (sigmoid), None: weight 1."""
+    _want("h", h, _BF16, (B.R, B.ld_h), B.device)
+    _want("w", w, (torch.float32,), (B.T, B.k), B.device)
+    _want("offsets", offsets, (torch.int32,), (B.E + 1,), B.device)
+    _want("pair_pos", pair_pos, (torch.int32,), (B.P,), B.device)
+    w2 = bank.need("w2", B.E, B.H, B.I)
+    sh = bank.need("w2_shared", B.n_shared, B.H, B.I_shared)
+    with _On(B.h):
+        L.moe_mx4_down_combine(B.act, h, B.T, B.H, B.I, B.E, B.k, w2, sh, B.n_shared, B.I_shared,
+                               w, offsets, pair_pos, B.out, B.ws, B.ws_bytes, B.out_flags, stream,
+                               shared_gate=_gate(shared_gate, B))
+    return B.out
+
+
+def run_layer(bank, x, logits, B, renormalize=1, shared_gate=None, stream=None):
+    """One layer step: out [T][H] (B.out) of x bf16 [T][H] and the router's
+    logits fp32 [T][E]; the routing's results are in B.ids, B.w and the sort's
+    tables of B."""
+    _want("x", x, _BF16, (B.T, B.H), B.device)
+    _want("logits", logits, (torch.float32,), (B.T, B.E), B.device)
+    w13 = bank.need("w13", B.E, 2 * B.I, B.H)
+    w2 = bank.need("w2", B.E, B.H, B.I)
+    s13 = bank.need("w13_shared", B.n_shared, 2 * B.I_shared, B.H)
+    s2 = bank.need("w2_shared", B.n_shared, B.H, B.I_shared)
+    with _On(B.h):
+        L.moe_mx4_layer(B.act, logits, x, B.T, B.H, B.I, B.E, B.k, int(renormalize), w13, w2, s13,
+                        s2, B.n_shared, B.I_shared, B.ids, B.w, B.counts, B.offsets,
+                        B.sorted_pair, B.pair_pos, B.h, B.out, B.ws, B.ws_bytes, B.out_flags,
+                        stream, shared_gate=_gate(shared_gate, B))
+    return B.out

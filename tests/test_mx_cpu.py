@@ -1,0 +1,216 @@
+"""MXFP4 without a GPU: the oracle's format against hand-worked values and a
+search over all codes, and the C ABI's refusals (nothing is launched)."""
+import ctypes
+
+import numpy as np
+import pytest
+
+from oracle import mx_oracle as O
+from packed_bit_grouped_amd import _lib as L
+
+FAKE = 1 << 20
+
+
+def test_hand_worked_block():
+    # largest magnitude 6 = 1.5 * 2^2: scale 2^0; ties to the even mantissa
+    v = np.zeros(32)
+    v[:14] = [6, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5, -0.25, -0.75, -5, 0.26, 4.99, -6]
+    codes, scales = O.quantise(v[None])
+    assert scales[0, 0] == 127
+    assert O.values(codes, scales)[0, :14].tolist() == [
+        6, 0, 1, 1, 2, 2, 4, 4, -0.0, -1, -4, 0.5, 4, -6]
+    # even index in the low nibble: 6 is code 7, 0.25 code 0; -0.25 code 8, -0.75 code 10
+    assert codes[0, 0] == 0x07 and codes[0, 4] == 0xA8
+
+
+@pytest.mark.parametrize("a,byte", [(0.0, 0), (1.0, 125), (7.99, 127), (8.0, 128), (2.0 ** -149, 0),
+                                    (2.0 ** -125, 0), (2.0 ** -124, 1), (3.3e38, 252),
+                                    (np.inf, 255), (np.nan, 255)])
+def test_scale_of_largest_magnitude(a, byte):
+    v = np.zeros(32)
+    v[5] = -a
+    codes, scales = O.quantise(v[None])
+    assert scales[0, 0] == byte
+    if byte == 255:
+        assert not codes.any() and np.isnan(O.values(codes, scales)).all()
+
+
+def test_quantise_is_nearest_of_all_codes():
+    rng = np.random.default_rng(3)
+    v = (rng.standard_normal((64, 96)) * np.exp(rng.standard_normal((64, 1)) * 8)).astype(np.float32)
+    codes, scales = O.quantise(v)
+    got = O.values(codes, scales)
+    unit = np.repeat(np.ldexp(1.0, scales.astype(int) - 127), 32, axis=1)
+    grid = np.concatenate([O.GRID, -O.GRID])
+    best = np.abs(v[..., None] - grid * unit[..., None]).min(-1)
+    assert np.array_equal(np.abs(v - got), best)
+    a = np.abs(v).reshape(64, 3, 32).max(-1)
+    u = unit[:, ::32]
+    assert ((a >= 4 * u) & (a < 8 * u)).all()
+
+
+def test_round_trip_of_every_code():
+    nib = np.tile(np.arange(16, dtype=np.uint8), 2)[None]
+    for s in (1, 100, 127, 250):
+        v = O.values(O.pack(nib), np.array([[s]], dtype=np.uint8))
+        c2, s2 = O.quantise(v)
+        assert s2[0, 0] == s and np.array_equal(O.values(c2, s2), v)
+
+
+def test_one_weight_layer_closed_form():
+    # one nonzero weight in gate, up and down each: h = SiLU(2x) * 3x
+    x = np.zeros((1, 32))
+    x[0, 7] = 1.5
+    w13 = np.zeros((64, 32))
+    w13[0, 7], w13[32, 7] = 2.0, 3.0
+    h, _ = O.gateup(O.activations(x, "a4"), w13, 32)
+    assert h[0, 0] == pytest.approx(3.0 / (1 + np.exp(-3.0)) * 4.5, rel=1e-15)
+    assert not h[0, 1:].any()
+
+
+# ---------------------------------------------------------------------------
+# refusals
+
+
+def _quant(**kw):
+    a = dict(src=FAKE, src_is_f32=0, R=4, C=64, ld=64, codes=FAKE, scales=FAKE)
+    a.update(kw)
+    return L.moe_mx4_quant_rows(*a.values(), stream=0, check=False)
+
+
+def _dequant(**kw):
+    a = dict(codes=FAKE, scales=FAKE, R=4, C=64, dst=FAKE, dst_is_f32=0, ld=64)
+    a.update(kw)
+    return L.moe_mx4_dequant_rows(*a.values(), stream=0, check=False)
+
+
+@pytest.mark.parametrize("call,out", [(_quant, "codes"), (_dequant, "dst")])
+def test_rows_refusals(call, out):
+    kind = "src_is_f32" if call is _quant else "dst_is_f32"
+    far = "src" if call is _quant else "dst"
+    assert call(R=-1) == L.MOE_E_INVAL
+    assert call(C=0) == L.MOE_E_INVAL
+    assert call(ld=63) == L.MOE_E_INVAL
+    assert call(C=48) == L.MOE_E_UNSUPPORTED
+    assert call(**{kind: 2}) == L.MOE_E_INVAL
+    for name in (out, "codes", "scales", far):
+        assert call(**{name: None}) == L.MOE_E_INVAL, name
+    assert call(codes=FAKE + 2) == L.MOE_E_INVAL
+    assert call(**{far: FAKE + 1}) == L.MOE_E_INVAL
+    assert call(**{kind: 1, far: FAKE + 2}) == L.MOE_E_INVAL
+    assert call(R=0, codes=None, scales=None, **{far: None}) == L.MOE_OK
+
+
+BANK = L.MxBankDesc(FAKE, FAKE)
+SHAPE = dict(act=L.MOE_A16, T=4, H=256, I=128, E=8, k=2, n_shared=0, I_shared=0)
+
+
+def _gateup(**kw):
+    a = dict(act=L.MOE_A16, x=FAKE, T=4, H=256, I=128, E=8, k=2, w13=BANK, w13_shared=None,
+             n_shared=0, I_shared=0, offsets=FAKE, sorted_pair=FAKE, h=FAKE, workspace=FAKE,
+             ws_bytes=1 << 30, flags=0)
+    a.update(kw)
+    return L.moe_mx4_gateup_silu(*a.values(), stream=0, check=False)
+
+
+def _down(**kw):
+    a = dict(act=L.MOE_A16, h=FAKE, T=4, H=256, I=128, E=8, k=2, w2=BANK, w2_shared=None,
+             n_shared=0, I_shared=0, topk_w=FAKE, offsets=FAKE, pair_pos=FAKE, out=FAKE,
+             workspace=FAKE, ws_bytes=1 << 30, flags=0)
+    a.update(kw)
+    return L.moe_mx4_down_combine(*a.values(), stream=0, check=False)
+
+
+def _layer(**kw):
+    a = dict(act=L.MOE_A16, logits=FAKE, x=FAKE, T=4, H=256, I=128, E=8, k=2, renormalize=1,
+             w13=BANK, w2=BANK, w13_shared=None, w2_shared=None, n_shared=0, I_shared=0,
+             topk_ids=FAKE, topk_w=FAKE, counts=FAKE, offsets=FAKE, sorted_pair=FAKE,
+             pair_pos=FAKE, h=FAKE, out=FAKE, workspace=FAKE, ws_bytes=1 << 30, flags=0)
+    a.update(kw)
+    return L.moe_mx4_layer(*a.values(), stream=0, check=False)
+
+
+@pytest.mark.parametrize("call", [_gateup, _down, _layer])
+def test_projection_refusals(call):
+    inval = [dict(act=L.MOE_A8), dict(act=7), dict(T=-1), dict(H=0), dict(I=0), dict(E=0), dict(k=0),
+             dict(k=9), dict(n_shared=-1), dict(n_shared=1, I_shared=0), dict(flags=1),
+             dict(flags=L.MOE_W_PREPACKED), dict(offsets=None), dict(n_shared=1, I_shared=128)]
+    unsupported = [dict(H=250), dict(I=100), dict(E=600), dict(T=70000), dict(T=65000, k=512, E=512),
+                   dict(T=60000, k=8, H=1 << 20), dict(n_shared=1, I_shared=100)]
+    if call is not _layer:
+        bank = "w13" if call is _gateup else "w2"
+        inval += [{bank: None}, {bank: L.MxBankDesc(None, FAKE)}, {bank: L.MxBankDesc(FAKE, None)},
+                  {bank: L.MxBankDesc(FAKE + 8, FAKE)}, {bank: L.MxBankDesc(FAKE, FAKE + 2)}]
+    if call is _gateup:
+        inval += [dict(x=None), dict(h=None), dict(sorted_pair=None), dict(x=FAKE + 8),
+                  dict(h=FAKE + 8), dict(flags=L.MOE_OUT_F32)]
+    elif call is _down:
+        inval += [dict(h=None), dict(out=None), dict(topk_w=None), dict(pair_pos=None),
+                  dict(h=FAKE + 8), dict(out=FAKE + 8)]
+    else:
+        inval += [dict(renormalize=2), dict(w13=None), dict(w2=None)]
+        inval += [{n: None} for n in ("logits", "x", "topk_ids", "topk_w", "counts", "sorted_pair",
+                                      "pair_pos", "h", "out")]
+    for kw in inval:
+        assert call(**kw) == L.MOE_E_INVAL, kw
+    for kw in unsupported:
+        assert call(**kw) == L.MOE_E_UNSUPPORTED, kw
+    for kw in (dict(workspace=None), dict(workspace=FAKE + 16), dict(ws_bytes=1)):
+        assert call(**kw) == L.MOE_E_WORKSPACE, kw
+    assert call(T=0) == L.MOE_OK
+
+
+def test_workspace_size_of_refused_shapes_is_zero():
+    def size(**kw):
+        return L.moe_mx4_workspace_bytes(*dict(SHAPE, **kw).values())
+    assert size() >= 4 * 2 * 256 * 4          # the fp32 rows of the down projection
+    assert size(act=L.MOE_A4) > size()
+    for kw in (dict(act=1), dict(H=250), dict(k=9), dict(E=600), dict(T=70000)):
+        assert size(**kw) == 0, kw
+
+
+def test_bank_descriptor_is_two_pointers():
+    assert ctypes.sizeof(L.MxBankDesc) == 16
+
+
+def test_python_front_refuses_before_the_library():
+    torch = pytest.importorskip("torch")
+    from packed_bit_grouped_amd import mx
+    with pytest.raises(TypeError):
+        mx.quantize_rows(torch.zeros(4, 64, dtype=torch.float16))
+    with pytest.raises(ValueError):
+        mx.quantize_rows(torch.zeros(4, 48))
+    with pytest.raises(ValueError):
+        mx.quantize_rows(torch.zeros(64))
+    with pytest.raises(ValueError):
+        mx.quantize_rows(torch.zeros(64, 4).t())
+    with pytest.raises(ValueError):
+        mx.quantize_rows(torch.zeros(1, 64).expand(4, 64))
+    with pytest.raises(ValueError, match="GPU"):
+        mx.quantize_rows(torch.zeros(4, 64))
+    codes = torch.zeros(4, 32, dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        mx.dequantize_rows(codes, torch.zeros(4, 3, dtype=torch.uint8))
+    with pytest.raises(TypeError):
+        mx.dequantize_rows(codes, torch.zeros(4, 2, dtype=torch.uint8), dtype=torch.float16)
+    with pytest.raises(ValueError):
+        mx.MxBank(w13=(codes, codes))
+    pair = (torch.zeros(2, 64, 16, dtype=torch.uint8), torch.zeros(2, 64, 1, dtype=torch.uint8))
+    bank = mx.MxBank(w13=pair)
+    assert bank.need("w13", 2, 64, 32) is not None and bank.need("w13_shared", 0, 64, 32) is None
+    with pytest.raises(ValueError):
+        bank.need("w13", 3, 64, 32)
+    with pytest.raises(ValueError):
+        bank.need("w2", 2, 64, 32)
+    with pytest.raises(ValueError):
+        mx.MxBuffers(4, 250, 32, 4, 2, device="cpu")
+    with pytest.raises(ValueError):
+        mx.MxBuffers(4, 256, 32, 4, 2, act="a8", device="cpu")
+    b = mx.MxBuffers(4, 32, 32, 2, 1, device="cpu")
+    x = torch.zeros(4, 32, dtype=torch.bfloat16)
+    offs, sp = torch.zeros(3, dtype=torch.int32), torch.zeros(4, dtype=torch.int32)
+    for bad in (x.float(), x[:3], x.t().contiguous().t()):
+        with pytest.raises((TypeError, ValueError)):
+            mx.gateup_silu(bank, bad, offs, sp, b)
+    with pytest.raises(TypeError):
+        mx.gateup_silu(bank, x, offs.long(), sp, b)
