@@ -28,7 +28,7 @@ LIB = os.path.join(HERE, "libmoe_w4.so")
 SOURCES = ["api.cpp", "route_permute.hip", "quant_combine.hip",
            "proj_gemv.hip", "proj_decode.hip", "proj_m16.hip",
            "proj_mfma8.hip", "noalloc.hip", "probe.hip", "mx_api.cpp",
-           "mx_quant.hip", "mx_rows16.hip"]
+           "mx_quant.hip", "mx_rows16.hip", "mx_gemm.hip"]
 ARCH = "gfx950"
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
          # packed fp32 VALU forms are kept out of the generated code

@@ -39,19 +39,31 @@ bool bank_ok(const moe_mxbank* b) {
   return b && b->codes && b->scales && aligned(b->codes, 16) && aligned(b->scales, 4);
 }
 
+// A16 rows that are not whole steps of the matrix kernel are copied to padded ones.
+bool pad_x(int H) { return H % 256 != 0; }
+bool pad_h(int I, int n_shared, int I_shared) {
+  return I % 256 != 0 || (n_shared > 0 && I_shared % 256 != 0);
+}
+
+// Tiles of up to 160 rows from this many pairs per expert on, of 16 rows below.
+constexpr long long kGemmRows = 12;
+
 MxWsLayout layout(int act, int T, int H, int I, int E, int k, int n_shared, int I_shared) {
   MxWsLayout L;
   const size_t R = (size_t)T * (k + n_shared);
   const int ld_h = ld_h_of(I, n_shared, I_shared);
   size_t off = 0;
+  const size_t xp = mx_pad_k(H), hp = mx_pad_k(ld_h);
   L.qx = off;
-  if (act == MOE_A4) off += up256((size_t)T * (H / 2));
+  if (act == MOE_A4) off += up256((size_t)T * (xp / 2));
+  else if (pad_x(H)) off += up256((size_t)T * xp * 2);
   L.sx = off;
-  if (act == MOE_A4) off += up256((size_t)T * mx_scale_ld(H));
+  if (act == MOE_A4) off += up256((size_t)T * (xp / kMxBlock));
   L.qh = off;
-  if (act == MOE_A4) off += up256(R * (ld_h / 2));
+  if (act == MOE_A4) off += up256(R * (hp / 2));
+  else if (pad_h(I, n_shared, I_shared)) off += up256(R * hp * 2);
   L.sh = off;
-  if (act == MOE_A4) off += up256(R * mx_scale_ld(ld_h));
+  if (act == MOE_A4) off += up256(R * (hp / kMxBlock));
   L.y = off;
   off += up256(R * H * 4);
   L.tiles = off;
@@ -79,8 +91,7 @@ moe_status gateup(int act, const uint16_t* x, int T, int H, int I, int E, int k,
   if (act == MOE_A4) {
     uint8_t* q = reinterpret_cast<uint8_t*>(ws + L.qx);
     uint8_t* sc = reinterpret_cast<uint8_t*>(ws + L.sx);
-    if (launch_mx_quant(x, 0, T, H, H, q, H / 2, sc, mx_scale_ld(H), s) != hipSuccess)
-      return MOE_E_DEVICE;
+    if (launch_mx_quant(x, 0, T, H, H, q, sc, mx_pad_k(H), s) != hipSuccess) return MOE_E_DEVICE;
     a.q = q;
     a.s = sc;
   }
@@ -102,6 +113,16 @@ moe_status gateup(int act, const uint16_t* x, int T, int H, int I, int E, int k,
   a.sorted_pair = sorted_pair;
   a.out = h;
   a.ld_out = ld_h_of(I, n_shared, I_shared);
+  if ((long long)T * k >= kGemmRows * E &&
+      mx_gemm_ok(act == MOE_A4, T, H, H, H, 2 * I, n_shared > 0 ? 2 * I_shared : 0)) {
+    if (act == MOE_A16 && pad_x(H)) {
+      uint16_t* xp = reinterpret_cast<uint16_t*>(ws + L.qx);
+      if (launch_mx_pad_rows(x, T, H, H, xp, mx_pad_k(H), s) != hipSuccess) return MOE_E_DEVICE;
+      a.x = xp;
+      a.ld_in = mx_pad_k(H);
+    }
+    return from_hip(launch_mx_gemm(a, 0, act == MOE_A4, s));
+  }
   return from_hip(launch_mx_rows16(a, 0, act == MOE_A4, s));
 }
 
@@ -111,6 +132,7 @@ moe_status down(int act, const uint16_t* h, int T, int H, int I, int E, int k,
                 const int32_t* pair_pos, void* out, int out_f32, char* ws, hipStream_t s) {
   const MxWsLayout L = layout(act, T, H, I, E, k, n_shared, I_shared);
   const int ld_h = ld_h_of(I, n_shared, I_shared), P = T * k;
+  const int hp = mx_pad_k(ld_h);
   float* y = reinterpret_cast<float*>(ws + L.y);
   MxProj a;
   std::memset(&a, 0, sizeof(a));
@@ -119,11 +141,10 @@ moe_status down(int act, const uint16_t* h, int T, int H, int I, int E, int k,
   if (act == MOE_A4) {
     uint8_t* q = reinterpret_cast<uint8_t*>(ws + L.qh);
     uint8_t* sc = reinterpret_cast<uint8_t*>(ws + L.sh);
-    const size_t lds = mx_scale_ld(ld_h);
-    hipError_t e = launch_mx_quant(h, 0, P, I, ld_h, q, ld_h / 2, sc, lds, s);
+    hipError_t e = launch_mx_quant(h, 0, P, I, ld_h, q, sc, hp, s);
     if (e == hipSuccess && n_shared > 0)
       e = launch_mx_quant(h + (size_t)P * ld_h, 0, n_shared * T, I_shared, ld_h,
-                          q + (size_t)P * (ld_h / 2), ld_h / 2, sc + (size_t)P * lds, lds, s);
+                          q + (size_t)P * (hp / 2), sc + (size_t)P * (hp / kMxBlock), hp, s);
     if (e != hipSuccess) return MOE_E_DEVICE;
     a.q = q;
     a.s = sc;
@@ -145,7 +166,22 @@ moe_status down(int act, const uint16_t* h, int T, int H, int I, int E, int k,
   a.offsets = offsets;
   a.out = y;
   a.ld_out = H;
-  if (launch_mx_rows16(a, 1, act == MOE_A4, s) != hipSuccess) return MOE_E_DEVICE;
+  if ((long long)T * k >= kGemmRows * E &&
+      mx_gemm_ok(act == MOE_A4, (long long)T * (k + n_shared), ld_h, a.K, a.K_sh, H, n_shared > 0 ? H : 0)) {
+    if (act == MOE_A16 && pad_h(I, n_shared, I_shared)) {
+      uint16_t* pd = reinterpret_cast<uint16_t*>(ws + L.qh);
+      hipError_t e = launch_mx_pad_rows(h, P, I, ld_h, pd, hp, s);
+      if (e == hipSuccess && n_shared > 0)
+        e = launch_mx_pad_rows(h + (size_t)P * ld_h, n_shared * T, I_shared, ld_h,
+                               pd + (size_t)P * hp, hp, s);
+      if (e != hipSuccess) return MOE_E_DEVICE;
+      a.x = pd;
+      a.ld_in = hp;
+    }
+    if (launch_mx_gemm(a, 1, act == MOE_A4, s) != hipSuccess) return MOE_E_DEVICE;
+  } else if (launch_mx_rows16(a, 1, act == MOE_A4, s) != hipSuccess) {
+    return MOE_E_DEVICE;
+  }
   return from_hip(launch_combine(y, H, topk_w, pair_pos, T, k, H, P, n_shared,
                                  n_shared > 0 ? shared_gate : nullptr, out, out_f32, s));
 }
@@ -164,7 +200,7 @@ moe_status moe_mx4_quant_rows(const void* src, int src_is_f32, int R, int C, int
   if (!aligned(src, src_is_f32 ? 4 : 2) || !aligned(codes, 4)) return MOE_E_INVAL;
   const moe_status d = device_usable();
   if (d != MOE_OK) return d;
-  return from_hip(launch_mx_quant(src, src_is_f32, R, C, ld, codes, C / 2, scales, C / kMxBlock,
+  return from_hip(launch_mx_quant(src, src_is_f32, R, C, ld, codes, scales, C,
                                   static_cast<hipStream_t>(stream)));
 }
 

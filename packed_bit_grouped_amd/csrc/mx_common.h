@@ -19,23 +19,24 @@ constexpr int kMxNanScale = 255;  // scale byte of a block that held inf or NaN
 
 // Workspace of the projection calls (byte offsets).
 struct MxWsLayout {
-  size_t qx, sx;     // A4: codes [T][H/2], scales [T][scale_ld(H)]
-  size_t qh, sh;     // A4: codes [R][ld_h/2], scales [R][scale_ld(ld_h)]
+  size_t qx, sx;     // A4: codes and scales of x, rows of mx_pad_k(H) values;
+                     // A16 where rows are not whole steps: qx holds a padded copy of x
+  size_t qh, sh;     // the same of h (rows of mx_pad_k(ld_h))
   size_t y;          // fp32 [R][H]
   size_t tiles;      // layer: the sort's tile list and its count
   size_t perm;       // layer: counts of the sort over many workgroups
   size_t total;
 };
 
-// Row stride of the scale bytes of quantised activations: whole words, so
-// that the matrix kernels load four scales at once whatever K is.
-inline __host__ __device__ int mx_scale_ld(int K) { return (K / kMxBlock + 3) & ~3; }
+// Row length of the activation copies in the workspace: whole steps of the
+// matrix kernels, the rest zeros (codes 0 with scale 0).
+inline __host__ __device__ int mx_pad_k(int K) { return (K + 255) & ~255; }
 
 // Arguments of the grouped projections.
 struct MxProj {
   const uint16_t* x;       // A16: bf16 rows (x by token, or h by sorted row)
-  const uint8_t* q;        // A4: their codes
-  const uint8_t* s;        // A4: their scales, row stride mx_scale_ld(ld_in)
+  const uint8_t* q;        // A4: their codes, rows of mx_pad_k(ld_in) values
+  const uint8_t* s;        // A4: their scales
   int ld_in;               // row stride of x in values
   const uint8_t* w;        // routed experts' codes [E][N][K/2]
   const uint8_t* ws;       // and scales [E][N][K/32]
@@ -133,14 +134,21 @@ __device__ __forceinline__ bool mx_find_tile(const int32_t* __restrict__ offsets
   return false;
 }
 
-// Codes, scales: R rows of C values (row stride ld) to codes [R][ldq] bytes and
-// scale bytes [R][lds].
+// R rows of C values (row stride ld) to rows of CP >= C values, zeros behind
+// the C: codes [R][CP/2] and scale bytes [R][CP/32].
 hipError_t launch_mx_quant(const void* src, int is_f32, int R, int C, int ld, uint8_t* q,
-                           size_t ldq, uint8_t* s, size_t lds, hipStream_t st);
+                           uint8_t* s, int CP, hipStream_t st);
 hipError_t launch_mx_dequant(const uint8_t* q, const uint8_t* s, int R, int C, void* dst,
                              int is_f32, int ld, hipStream_t st);
-// Grouped projections on tiles of 16 rows, K split over the workgroup's waves;
-// mode 0: gate/up with SiLU*mul to h, 1: down to y.
+// R bf16 rows of C values (stride ld, 16-byte aligned) to rows of CP, zeros
+// behind the C.
+hipError_t launch_mx_pad_rows(const uint16_t* src, int R, int C, int ld, uint16_t* dst, int CP,
+                              hipStream_t st);
+// Grouped projections; mode 0: gate/up with SiLU*mul to h, 1: down to y.
+// Tiles of 16 rows, K split over the workgroup's waves:
 hipError_t launch_mx_rows16(const MxProj& a, int mode, int act4, hipStream_t st);
+// Tiles of up to 160 rows (A16: rows of whole steps, K % 256 == 0 or a padded copy):
+bool mx_gemm_ok(int act4, long long rows, int ld, int K, int K_sh, int N, int N_sh);
+hipError_t launch_mx_gemm(const MxProj& a, int mode, int act4, hipStream_t st);
 
 }  // namespace moe

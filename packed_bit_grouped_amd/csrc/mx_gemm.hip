@@ -1,0 +1,562 @@
+// Grouped MXFP4 projections for tiles of many activation rows.
+//
+// The same products as mx_rows16.hip where an expert has tens of rows or
+// more: the packed weights are still read once per tile, and the matrix cores
+// now matter.  Workgroup = one tile (up to 160 sorted rows of one expert, cut
+// evenly) x 128 gate/up units or 256 down rows; 4 waves, one per SIMD (512
+// registers).  Wave w owns 64 weight rows - the gate and the up rows of 32
+// units, so SiLU*mul pairs registers of one lane, or 64 down rows - as four
+// 16-row fragments against all of the tile's rows.
+//
+//  * Weights go from memory into a register ring kD steps of 256 K ahead:
+//    lane (row c = lane % 16, group g = lane / 16) holds blocks 2g and 2g + 1
+//    of the step, so a load instruction covers whole 128-byte runs of 16 rows
+//    and the lane's two scale bytes are one 16-bit load.  Sub-step j multiplies
+//    block 2g + j of every lane (a sum over K does not care which lane holds
+//    which block).
+//  * Activations go from memory straight into a ring of LDS buffers (loads
+//    that write LDS; rows gathered by token).  A4: 128 bytes of codes per row
+//    and step, chunk q of row m in slot q ^ ((m >> 1) & 7); the scale bytes of
+//    the whole tile are staged once.  A16: 256 bytes of bf16 per row and
+//    sub-step, chunk q in slot q ^ (m & 15).  Both spread the 16 lanes that an
+//    LDS access serves at a time over all banks.
+//  * A4 feeds codes and scales to the scaled 16x16x128 instruction; A16
+//    expands a fragment's 8 codes to bf16 by four conversions (exact) for one
+//    16x16x32 step against every row fragment.
+//  * Activation rows are padded to whole steps (codes and scales 0, or bf16
+//    zeros) by the pass that quantises or copies them, so K's tail needs no
+//    cases; the tail's weight scales are cleared, because a stray 255 there
+//    would make NaN of the zeros.
+#include "mx_common.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRowsMax = 160;   // rows per tile
+constexpr int kNF = 4;          // weight fragments of 16 rows per wave
+constexpr int kKS = 256;        // K per weight step
+constexpr int kXcd = 8;
+
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, 0x00020000);
+}
+
+// At most N vector-memory operations of this wave in flight, every LDS access
+// done, then the workgroup barrier; nothing is scheduled across it.
+template <int N>
+__device__ __forceinline__ void vm_barrier() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_barrier();
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+
+struct GemmArgs {
+  MxProj p;
+  int KP, KP_sh;       // K padded to whole steps: row lengths of the activation copy
+  int n_ub;            // workgroups per tile
+  int max_tiles;       // host bound of the routed tiles
+  int sh_per;          // tiles per shared expert
+  int sc_pitch;        // A4: LDS bytes per row of scales
+};
+
+// A4 has one activation stage per weight step, A16 two of 128 K.  kBufs stages
+// of LDS; kD weight steps in registers.
+template <bool ACT4>
+struct Ring {
+  static constexpr int kStages = ACT4 ? 1 : 2;
+  static constexpr int kBufs = 3;
+  static constexpr int kD = ACT4 ? 3 : 2;
+  static constexpr int kRowChunks = ACT4 ? 8 : 16;   // 16-byte chunks per row and stage
+  static constexpr int buf_chunks(int mt) { return kRowChunks * 16 * ((mt + 1) & ~1); }
+};
+
+struct WStep {
+  u32x4 c[kNF][2];
+  uint32_t s[kNF];
+};
+
+struct Tile {
+  const uint8_t* act;   // padded activation rows
+  uint32_t act_bytes;
+  int row_bytes;        // of one padded row
+  int K, U, n_st;
+  int u0;               // first unit / row of this wave
+  int orow;             // first output row
+};
+
+template <int MODE, bool ACT4, int MT, bool SW>
+__device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, __amdgpu_buffer_rsrc_t crs,
+                                     __amdgpu_buffer_rsrc_t srs, u32x4* As, const int* tok,
+                                     const uint8_t* sc, int nrows) {
+  using R = Ring<ACT4>;
+  constexpr int kBuf = R::buf_chunks(MT);
+  constexpr int nA = kBuf / 256;               // activation loads per wave and stage
+  constexpr int kD = R::kD, kBufs = R::kBufs;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const int n_st = t.n_st, n_stage = n_st * R::kStages;
+  const int nblk = t.K / kMxBlock;
+
+  // ---- weight rows of this lane; rows past the end lie past the buffer
+  int coff[kNF], soff[kNF];
+#pragma unroll
+  for (int f = 0; f < kNF; ++f) {
+    int row;
+    bool ok;
+    if (MODE == 0) {
+      const int u = t.u0 + 16 * (f & 1) + c;
+      ok = u < t.U;
+      row = (f >> 1) * t.U + u;
+    } else {
+      row = t.u0 + 16 * f + c;
+      ok = row < t.U;
+    }
+    coff[f] = ok ? row * (t.K / 2) + 32 * g : 0x40000000;
+    soff[f] = ok ? row * nblk + 2 * g : 0x40000000;
+  }
+  // scale bytes of the last step's blocks that exist
+  const int left = nblk - (n_st - 1) * (kKS / kMxBlock) - 2 * g;
+  const uint32_t tail = left >= 2 ? 0xFFFFu : left == 1 ? 0xFFu : 0u;
+
+  auto load_c = [&](int st, int j, WStep& w) {
+    const int o = st < n_st ? st * (kKS / 2) + 16 * j : 0x40000000;   // past the end: nothing is read
+#pragma unroll
+    for (int f = 0; f < kNF; ++f)
+      w.c[f][j] = __builtin_amdgcn_raw_buffer_load_b128(crs, coff[f] + o, 0, 2);
+  };
+  auto load_s = [&](int st, WStep& w) {
+    const int o = st < n_st ? st * (kKS / kMxBlock) : 0x40000000;
+#pragma unroll
+    for (int f = 0; f < kNF; ++f) {
+      if (SW) {
+        w.s[f] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(srs, soff[f] + o, 0, 0);
+      } else {
+        const uint32_t lo = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(srs, soff[f] + o, 0, 0);
+        const uint32_t hi = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(srs, soff[f] + o + 1, 0, 0);
+        w.s[f] = lo | (hi << 8);
+      }
+    }
+  };
+  constexpr int nS = SW ? kNF : 2 * kNF;
+  constexpr int nW = 2 * kNF + nS;             // weight loads per step
+
+  // ---- activation pieces of this lane: LDS slot q of a stage holds the chunk
+  // that the swizzle puts there
+  const __amdgpu_buffer_rsrc_t ars = make_rsrc(t.act, t.act_bytes);
+  int aoff[nA];
+#pragma unroll
+  for (int i = 0; i < nA; ++i) {
+    const int q = (wave * nA + i) * 64 + lane;
+    const int m = q / R::kRowChunks;
+    if (ACT4) {
+      aoff[i] = tok[m] * t.row_bytes + (((q & 7) ^ ((m >> 1) & 7)) * 16);
+    } else {
+      const int ch = (q & 15) ^ (m & 15);      // group ch / 4, 16 bytes ch % 4 of its block
+      aoff[i] = tok[m] * t.row_bytes + (ch >> 2) * 128 + (ch & 3) * 16;
+    }
+  }
+  auto dma = [&](int sg, int buf) {
+    sg = min(sg, n_stage - 1);                 // past the end: the last stage once more
+    const int o = ACT4 ? sg * 128 : (sg >> 1) * 512 + (sg & 1) * 64;
+#pragma unroll
+    for (int i = 0; i < nA; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          ars, (__attribute__((address_space(3))) void*)(As + buf * kBuf + (wave * nA + i) * 64), 16,
+          aoff[i], o, 0, 0);
+  };
+
+  mx_f32x4 acc[kNF][MT];
+#pragma unroll
+  for (int f = 0; f < kNF; ++f)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[f][m] = mx_f32x4{0, 0, 0, 0};
+
+  // Sub-steps of a stage: A4 two of 128 K (block 2g + q of every lane), A16
+  // four of 32 K (word q of block 2g + j).  A row fragment's register is
+  // refilled from LDS for the next sub-step as soon as its four matrix
+  // instructions are issued: the other fragments' instructions (64 cycles
+  // each) cover the read.  A16 expands the next sub-step's weights meanwhile.
+  // Before a stage's last sub-step every wave has read all of its buffer, so
+  // the stage's one barrier stands there: it frees the buffer for the stage
+  // kBufs on, and covers the next stage's loads, which the last sub-step reads.
+  constexpr int kQ = ACT4 ? 2 : 4;
+  const int sw = ACT4 ? (c >> 1) & 7 : c;
+  const u32x4* Ac = As + c * R::kRowChunks;
+  u32x4 x[MT];
+  mx_bf16x8 wv[2][kNF];
+  uint32_t sx[MT];
+  auto x_at = [&](int b, int q) {
+    return Ac + b * kBuf + (((ACT4 ? 2 : 4) * g + q) ^ sw);
+  };
+  auto sx_at = [&](int st) { return sc + c * ga.sc_pitch + min(st, n_st - 1) * 8 + 2 * g; };
+  auto expand = [&](int st, int j, int q, const WStep& w, mx_bf16x8(&v)[kNF]) {
+    const uint32_t keep = st >= n_st - 1 ? tail : 0xFFFFu;
+#pragma unroll
+    for (int f = 0; f < kNF; ++f)
+      v[f] = mx_word_to_bf16(w.c[f][j][q],
+                             __uint_as_float((((w.s[f] & keep) >> (8 * j)) & 255u) << 23));
+  };
+  // issue order of a sub-step: per row fragment four matrix instructions with
+  // the conversions and memory loads between them, then its LDS reads
+  auto spread = [&](auto n_ds, auto n_ld) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int f = 0; f < kNF; ++f) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if (kNF * m + f < n_ld.value) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, ACT4 ? 1 : 2, 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x100, n_ds.value, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  int buf = 0;
+  // After the loads of stage a + 1 (issued behind the barrier of stage a + 1 -
+  // kBufs) and before the barrier of stage a come the weight loads of kBufs - 1
+  // stages (the prologue's: at least as many) and the activation loads of
+  // kBufs - 2.
+  constexpr int kAfter = (kBufs - 2) * nA + (ACT4 ? (kBufs - 1) * nW : nW);
+
+  // stage (st, j) from buffer buf with w; wn holds the next step's weights
+  auto stage = [&](int st, int j, WStep& w, const WStep& wn) {
+    const int a = st * R::kStages + j;
+    const int nb = buf == kBufs - 1 ? 0 : buf + 1;
+    if constexpr (ACT4) {
+      const uint32_t keep = st == n_st - 1 ? tail : 0xFFFFu;
+      uint32_t sws[kNF];
+#pragma unroll
+      for (int f = 0; f < kNF; ++f) sws[f] = w.s[f] & keep;
+      const u32x4* p = x_at(buf, 1);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int f = 0; f < kNF; ++f)
+          acc[f][m] = mx_mfma_fp4<0>(w.c[f][0], sws[f], x[m], sx[m], acc[f][m]);
+        x[m] = p[m * 16 * R::kRowChunks];
+      }
+      spread(Int<1>(), Int<0>());
+      vm_barrier<kAfter>();
+      dma(a + kBufs, buf);
+      load_c(st + kD, 0, w);
+      load_s(st + kD, w);
+      p = x_at(nb, 0);
+      const uint8_t* ps = sx_at(st + 1);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int f = 0; f < kNF; ++f)
+          acc[f][m] = mx_mfma_fp4<1>(w.c[f][1], sws[f], x[m], sx[m], acc[f][m]);
+        x[m] = p[m * 16 * R::kRowChunks];
+        sx[m] = *reinterpret_cast<const uint16_t*>(ps + 16 * m * ga.sc_pitch);
+      }
+      spread(Int<2>(), Int<nA + kNF + nS>());
+      load_c(st + kD, 1, w);
+      __builtin_amdgcn_sched_barrier(0);
+    } else {
+#pragma unroll
+      for (int q = 0; q < kQ; ++q) {
+        const int cur = q & 1, nxt = cur ^ 1;
+        const u32x4* p;
+        if (q < kQ - 1) {
+          p = x_at(buf, q + 1);
+          expand(st, j, q + 1, w, wv[nxt]);
+        } else {
+          vm_barrier<kAfter>();
+          dma(a + kBufs, buf);
+          p = x_at(nb, 0);
+          if (j == 0) expand(st, 1, 0, w, wv[nxt]);
+          else expand(st + 1, 0, 0, wn, wv[nxt]);
+          load_c(st + kD, j, w);
+          if (j == 1) load_s(st + kD, w);
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+#pragma unroll
+          for (int f = 0; f < kNF; ++f)
+            acc[f][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                wv[cur][f], __builtin_bit_cast(mx_bf16x8, x[m]), acc[f][m], 0, 0, 0);
+          x[m] = p[m * 16 * R::kRowChunks];
+        }
+        if (q < kQ - 1) spread(Int<1>(), Int<0>());
+        else if (j == 0) spread(Int<1>(), Int<nA + kNF>());
+        else spread(Int<1>(), Int<nA + kNF + nS>());
+      }
+    }
+    buf = nb;
+  };
+  auto step = [&](int st, WStep& w, const WStep& wn) {
+    stage(st, 0, w, wn);
+    if constexpr (!ACT4) stage(st, 1, w, wn);
+  };
+
+  // Prologue.  A16 loads its third stage before the second step's weights,
+  // so that kAfter holds in the first stages too.
+  WStep w0, w1, w2;
+  auto load_w = [&](int st, WStep& w) {
+    load_c(st, 0, w);
+    load_c(st, 1, w);
+    load_s(st, w);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  dma(0, 0);
+  __builtin_amdgcn_sched_barrier(0);
+  load_w(0, w0);
+  dma(1, 1);
+  __builtin_amdgcn_sched_barrier(0);
+  if constexpr (ACT4) {
+    load_w(1, w1);
+    dma(2, 2);
+    __builtin_amdgcn_sched_barrier(0);
+    load_w(2, w2);
+  } else {
+    dma(2, 2);
+    __builtin_amdgcn_sched_barrier(0);
+    load_w(1, w1);
+  }
+  vm_barrier<2 * nA + kD * nW>();   // stage 0 is in LDS
+  {
+    const u32x4* p = x_at(0, 0);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) x[m] = p[m * 16 * R::kRowChunks];
+    if constexpr (ACT4) {
+      const uint8_t* ps = sx_at(0);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+        sx[m] = *reinterpret_cast<const uint16_t*>(ps + 16 * m * ga.sc_pitch);
+    } else {
+      expand(0, 0, 0, w0, wv[0]);
+    }
+  }
+
+#pragma unroll 1
+  for (int base = 0; base < n_st; base += kD) {
+    step(base, w0, w1);
+    if constexpr (ACT4) {
+      if (base + 1 < n_st) step(base + 1, w1, w2);
+      if (base + 2 < n_st) step(base + 2, w2, w0);
+    } else {
+      if (base + 1 < n_st) step(base + 1, w1, w0);
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(0);   // nothing writes LDS after this
+
+  // ---- lane: row 16 m + c, four consecutive units of every fragment
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int row = 16 * m + c;
+    if (row >= nrows) continue;
+    if (MODE == 0) {
+      uint16_t* h = static_cast<uint16_t*>(ga.p.out) + (size_t)(t.orow + row) * ga.p.ld_out;
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const int u = t.u0 + 16 * f + 4 * g;
+        if (u >= t.U) continue;
+        uint32_t v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = mx_bf16(silu_mul(acc[f][m][i], acc[f + 2][m][i]));
+        *reinterpret_cast<uint2*>(h + u) = make_uint2(v[0] | (v[1] << 16), v[2] | (v[3] << 16));
+      }
+    } else {
+      float* y = static_cast<float*>(ga.p.out) + (size_t)(t.orow + row) * ga.p.ld_out;
+#pragma unroll
+      for (int f = 0; f < kNF; ++f) {
+        const int u = t.u0 + 16 * f + 4 * g;
+        if (u < t.U) __builtin_nontemporal_store(acc[f][m], reinterpret_cast<mx_f32x4*>(y + u));
+      }
+    }
+  }
+}
+
+// Tile j of the routed rows: an expert with n rows has ceil(n / 160) tiles of
+// even size.  Every wave scans the offsets (lanes count 1..8 experts each).
+__device__ __forceinline__ int tiles_of(int n) { return (n + kRowsMax - 1) / kRowsMax; }
+
+template <int MODE, bool ACT4, bool SW>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void mx_gemm_kernel(GemmArgs ga) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  const MxProj& a = ga.p;
+  int* tok = reinterpret_cast<int*>(smem);                   // [kRowsMax]
+  u32x4* As = reinterpret_cast<u32x4*>(smem + kRowsMax * 4);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+  // ---- all tiles: the shared experts', then the routed ones
+  const int per = (a.E + 63) / 64;
+  int cnt = 0;
+  for (int i = 0; i < per; ++i) {
+    const int ex = lane * per + i;
+    if (ex < a.E) cnt += tiles_of(max(min(a.offsets[ex + 1], a.P) - max(a.offsets[ex], 0), 0));
+  }
+  int pre = cnt;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int o = __shfl_up(pre, d);
+    if (lane >= d) pre += o;
+  }
+  const int n_sh = a.n_shared * ga.sh_per;
+  const int n_slots = n_sh + min(__builtin_amdgcn_readlane(pre, 63), ga.max_tiles);
+  // XCD blockIdx % 8 takes a contiguous range of tiles: the workgroups of one
+  // tile share its activation rows in one L2, the tiles of one expert its weights
+  const int b = blockIdx.x, xcd = b % kXcd, li = b / kXcd;
+  const int per_xcd = (n_slots + kXcd - 1) / kXcd;
+  const int local = li / ga.n_ub, ub = li - local * ga.n_ub;
+  const int slot = xcd * per_xcd + local;
+  if (local >= per_xcd || slot >= n_slots) return;
+
+  bool is_sh = false;
+  int e = 0, r0 = 0, r1 = 0;
+  if (slot < n_sh) {
+    is_sh = true;
+    e = slot / ga.sh_per;
+    const int ti = slot - e * ga.sh_per;
+    const int rows = ((a.T + ga.sh_per - 1) / ga.sh_per + 15) & ~15;
+    r0 = min(ti * rows, a.T);
+    r1 = min(r0 + rows, a.T);
+  } else {
+    const int j = slot - n_sh;
+    const uint64_t past = __ballot(pre > j);
+    if (past == 0) return;
+    const int owner = __builtin_ctzll(past);
+    int left = j - (__builtin_amdgcn_readlane(pre, owner) - __builtin_amdgcn_readlane(cnt, owner));
+    for (int i = 0; i < per; ++i) {
+      const int ex = owner * per + i;
+      if (ex >= a.E) break;
+      const int lo = max(a.offsets[ex], 0), hi = min(a.offsets[ex + 1], a.P);
+      const int nt = tiles_of(max(hi - lo, 0));
+      if (left < nt) {
+        e = ex;
+        const int rows = ((hi - lo + nt - 1) / nt + 15) & ~15;
+        r0 = min(lo + left * rows, hi);
+        r1 = min(r0 + rows, hi);
+        break;
+      }
+      left -= nt;
+    }
+  }
+  const int nrows = r1 - r0;
+  if (nrows <= 0) return;
+
+  Tile t;
+  t.K = is_sh ? a.K_sh : a.K;
+  t.U = is_sh ? a.U_sh : a.U;
+  const int KP = is_sh ? ga.KP_sh : ga.KP;
+  t.n_st = (t.K + kKS - 1) / kKS;
+  const int ublk = ub * (MODE == 0 ? 128 : 256);
+  if (ublk >= t.U) return;
+  t.u0 = ublk + wave * (MODE == 0 ? 32 : 64);
+  t.orow = is_sh ? a.P + e * a.T + r0 : r0;
+  // gate/up gathers rows of x by token; down reads its own rows, the shared
+  // experts' behind the routed ones
+  const int arow = MODE == 0 ? 0 : (is_sh ? a.P : 0);
+  const size_t stride = ACT4 ? (size_t)ga.KP / 2 : (size_t)a.ld_in * 2;
+  t.row_bytes = (int)stride;
+  t.act = (ACT4 ? a.q : reinterpret_cast<const uint8_t*>(a.x)) + arow * stride;
+  const int act_rows = MODE == 0 ? a.T : (is_sh ? a.n_shared * a.T : a.P);
+  t.act_bytes = (uint32_t)(act_rows * stride);
+  const int N = MODE == 0 ? 2 * t.U : t.U;
+  const size_t mat = (size_t)N * (t.K / 2);
+  const __amdgpu_buffer_rsrc_t crs = make_rsrc((is_sh ? a.w_sh : a.w) + (size_t)e * mat, (uint32_t)mat);
+  const __amdgpu_buffer_rsrc_t srs =
+      make_rsrc((is_sh ? a.ws_sh : a.ws) + (size_t)e * (mat / 16), (uint32_t)(mat / 16));
+
+  if (tid < kRowsMax) {
+    const int m = tid < nrows ? tid : 0;   // padding rows repeat row 0 (not stored)
+    int row;
+    if (MODE == 1) {
+      row = is_sh ? e * a.T + r0 + m : r0 + m;
+    } else if (is_sh) {
+      row = r0 + m;
+    } else {
+      const int p = a.sorted_pair[r0 + m];
+      row = (unsigned)p < (unsigned)a.P ? p / a.k : 0;
+    }
+    tok[tid] = row;
+  }
+  __syncthreads();
+  const int mt = (nrows + 15) / 16;
+  uint8_t* sc = nullptr;
+  if (ACT4) {
+    // the tile's scale bytes, rows ga.sc_pitch apart (4 bytes more than the
+    // row: 16 rows' words then lie on different banks)
+    sc = smem + kRowsMax * 4 + Ring<true>::kBufs * Ring<true>::buf_chunks(10) * 16;
+    const uint8_t* src = a.s + (size_t)arow * (ga.KP / kMxBlock);
+    const int words = KP / kMxBlock / 4;
+    const int rows = mt * 16;
+    for (int i = tid; i < rows * words; i += kThreads) {
+      const int m = i / words, q = i - m * words;
+      *reinterpret_cast<uint32_t*>(sc + m * ga.sc_pitch + q * 4) =
+          *reinterpret_cast<const uint32_t*>(src + (size_t)tok[m] * (ga.KP / kMxBlock) + q * 4);
+    }
+  }
+#define MX_BODY(MT) body<MODE, ACT4, MT, SW>(ga, t, crs, srs, As, tok, sc, nrows)
+  if (mt <= 2) MX_BODY(2);
+  else if (mt <= 4) MX_BODY(4);
+  else if (mt <= 6) MX_BODY(6);
+  else if (mt <= 8) MX_BODY(8);
+  else MX_BODY(10);
+#undef MX_BODY
+}
+
+template <int MODE, bool ACT4>
+hipError_t launch(const GemmArgs& ga, size_t lds, long long grid, hipStream_t st) {
+  // the two scale bytes of a lane in one load where rows start at even bytes
+  const bool sw = (ga.p.K / kMxBlock) % 2 == 0 &&
+                  (ga.p.n_shared == 0 || (ga.p.K_sh / kMxBlock) % 2 == 0);
+  auto k = sw ? mx_gemm_kernel<MODE, ACT4, true> : mx_gemm_kernel<MODE, ACT4, false>;
+  k<<<(int)grid, kThreads, lds, st>>>(ga);
+  return hipGetLastError();
+}
+
+size_t lds_bytes(bool act4, int KP) {
+  const size_t ring = act4 ? (size_t)Ring<true>::kBufs * Ring<true>::buf_chunks(10) * 16
+                           : (size_t)Ring<false>::kBufs * Ring<false>::buf_chunks(10) * 16;
+  return kRowsMax * 4 + ring + (act4 ? (size_t)kRowsMax * (KP / kMxBlock + 4) : 0);
+}
+
+}  // namespace
+
+bool mx_gemm_ok(int act4, long long rows, int ld, int K, int K_sh, int N, int N_sh) {
+  const int KP = mx_pad_k(K > K_sh ? K : K_sh);
+  if (lds_bytes(act4, KP) > 160 * 1024) return false;
+  // 32-bit offsets into one matrix and into the activation rows
+  const long long stride = act4 ? mx_pad_k(ld) / 2 : 2LL * mx_pad_k(ld);
+  if (rows * stride >= (1LL << 31)) return false;
+  return (long long)N * K / 2 < (1LL << 30) && (long long)N_sh * K_sh / 2 < (1LL << 30);
+}
+
+hipError_t launch_mx_gemm(const MxProj& a, int mode, int act4, hipStream_t st) {
+  GemmArgs ga;
+  ga.p = a;
+  ga.KP = mx_pad_k(a.ld_in);   // row length of the activation copy
+  ga.KP_sh = ga.KP;
+  ga.sh_per = (a.T + kRowsMax - 1) / kRowsMax;
+  ga.max_tiles = moe_permute_max_tiles(a.T, a.k, a.E, kRowsMax);
+  const int step = mode == 0 ? 128 : 256;
+  const int U = a.n_shared > 0 && a.U_sh > a.U ? a.U_sh : a.U;
+  ga.n_ub = (U + step - 1) / step;
+  ga.sc_pitch = ga.KP / kMxBlock + 4;
+  const long long slots = (long long)a.n_shared * ga.sh_per + ga.max_tiles;
+  const long long grid = (slots + kXcd - 1) / kXcd * kXcd * ga.n_ub;
+  if (grid >= (1LL << 31)) return hipErrorInvalidValue;
+  const size_t lds = lds_bytes(act4, ga.KP);
+  if (mode == 0) return act4 ? launch<0, true>(ga, lds, grid, st) : launch<0, false>(ga, lds, grid, st);
+  return act4 ? launch<1, true>(ga, lds, grid, st) : launch<1, false>(ga, lds, grid, st);
+}
+
+}  // namespace moe

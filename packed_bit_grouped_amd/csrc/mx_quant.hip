@@ -21,15 +21,18 @@ constexpr int kQuantThreads = 256;
 // are loaded one by one.  64-bit indices: a bank of experts passes 2^32 bytes.
 template <bool F32, bool VEC>
 __global__ __launch_bounds__(kQuantThreads) void mx_quant_kernel(
-    const void* __restrict__ src, int R, int C8, int ld, uint8_t* __restrict__ q, size_t ldq,
-    uint8_t* __restrict__ s, size_t lds) {
-  const long long n = (long long)R * C8;   // eights of values
+    const void* __restrict__ src, int R, int C8, int ld, uint8_t* __restrict__ q,
+    uint8_t* __restrict__ s, int CP8) {
+  const long long n = (long long)R * CP8;   // eights of values, the padding's too
   for (long long i = (long long)blockIdx.x * kQuantThreads + threadIdx.x; i < n;
        i += (long long)gridDim.x * kQuantThreads) {
-    const long long r = i / C8;
-    const int c = (int)(i - r * C8);   // C8 is a multiple of 4: a block's four lanes stay together
+    const long long r = i / CP8;
+    const int c = (int)(i - r * CP8);   // CP8, C8: multiples of 4, a block's four lanes stay together
     float v[8];
-    if (F32) {
+    if (c >= C8) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+    } else if (F32) {
       const float* p = static_cast<const float*>(src) + r * ld + c * 8;
       if (VEC) {
         const mx_f32x4 a = reinterpret_cast<const mx_f32x4*>(p)[0];
@@ -69,8 +72,8 @@ __global__ __launch_bounds__(kQuantThreads) void mx_quant_kernel(
       w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], sc, 2);
       w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], sc, 3);
     }
-    *reinterpret_cast<uint32_t*>(q + r * ldq + (size_t)c * 4) = w;
-    if ((c & 3) == 0) s[r * lds + (c >> 2)] = (uint8_t)sb;
+    reinterpret_cast<uint32_t*>(q)[i] = w;
+    if ((c & 3) == 0) s[i >> 2] = (uint8_t)sb;
   }
 }
 
@@ -118,6 +121,22 @@ __global__ __launch_bounds__(kQuantThreads) void mx_dequant_kernel(
   }
 }
 
+// bf16 rows to longer ones, 16 bytes per lane.
+__global__ __launch_bounds__(kQuantThreads) void mx_pad_kernel(const uint16_t* __restrict__ src,
+                                                               int R, int C8, int ld,
+                                                               uint16_t* __restrict__ dst,
+                                                               int CP8) {
+  const long long n = (long long)R * CP8;
+  for (long long i = (long long)blockIdx.x * kQuantThreads + threadIdx.x; i < n;
+       i += (long long)gridDim.x * kQuantThreads) {
+    const long long r = i / CP8;
+    const int c = (int)(i - r * CP8);
+    const mx_u32x4 zero = {0, 0, 0, 0};
+    reinterpret_cast<mx_u32x4*>(dst)[i] =
+        c < C8 ? *reinterpret_cast<const mx_u32x4*>(src + r * ld + c * 8) : zero;
+  }
+}
+
 int quant_blocks(long long eights) {
   const long long b = (eights + kQuantThreads - 1) / kQuantThreads;
   return (int)(b < 16384 ? b : 16384);
@@ -130,12 +149,19 @@ bool rows_aligned(const void* p, int ld, int elem) {
 }  // namespace
 
 hipError_t launch_mx_quant(const void* src, int is_f32, int R, int C, int ld, uint8_t* q,
-                           size_t ldq, uint8_t* s, size_t lds, hipStream_t st) {
-  const int blocks = quant_blocks((long long)R * (C / 8));
+                           uint8_t* s, int CP, hipStream_t st) {
+  const int blocks = quant_blocks((long long)R * (CP / 8));
   const bool vec = rows_aligned(src, ld, is_f32 ? 4 : 2);
   auto k = is_f32 ? (vec ? mx_quant_kernel<true, true> : mx_quant_kernel<true, false>)
                   : (vec ? mx_quant_kernel<false, true> : mx_quant_kernel<false, false>);
-  k<<<blocks, kQuantThreads, 0, st>>>(src, R, C / 8, ld, q, ldq, s, lds);
+  k<<<blocks, kQuantThreads, 0, st>>>(src, R, C / 8, ld, q, s, CP / 8);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_pad_rows(const uint16_t* src, int R, int C, int ld, uint16_t* dst, int CP,
+                              hipStream_t st) {
+  mx_pad_kernel<<<quant_blocks((long long)R * (CP / 8)), kQuantThreads, 0, st>>>(src, R, C / 8, ld,
+                                                                                 dst, CP / 8);
   return hipGetLastError();
 }
 

@@ -116,13 +116,11 @@ __global__ __launch_bounds__(kThreads) void mx_rows16_kernel(MxProj a, int n_sh_
     const uint32_t s1 = load_scales<NB, WORDS>(wsc + (size_t)n1 * nblk, b, nblk);
     if (ACT4) {
       mx_u32x4 x[NB];
-      const mx_u32x4* px = reinterpret_cast<const mx_u32x4*>(a.q + xrow * (a.ld_in / 2)) + b;
+      const int KP = mx_pad_k(a.ld_in);
+      const mx_u32x4* px = reinterpret_cast<const mx_u32x4*>(a.q + xrow * (KP / 2)) + b;
 #pragma unroll
       for (int j = 0; j < NB; ++j) x[j] = have && b + j < nblk ? px[j] : zero;
-      uint32_t sx = have ? load_scales<NB, true>(a.s + xrow * mx_scale_ld(a.ld_in), b, nblk) : 0u;
-      // bytes past the last block are whatever the workspace held: a scale
-      // byte of 255 there would make NaN of the zero codes
-      if (nblk - b < NB && nblk > b) sx &= (1u << (8 * (nblk - b))) - 1u;
+      const uint32_t sx = have ? load_scales<NB, true>(a.s + xrow * (KP / kMxBlock), b, nblk) : 0u;
       fp4_steps<NB>(w0, s0, w1, s1, x, sx, a0, a1);
     } else {
       const mx_u32x4* px = reinterpret_cast<const mx_u32x4*>(a.x + xrow * a.ld_in) + b * 4;
