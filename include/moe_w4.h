@@ -589,20 +589,12 @@ moe_status moe_dbg_dec_stamps(unsigned long long* stamps);
  * low-bit weights packed, do the work on the NPU" (expert weights stay
  * packed, grouped projections with fused gate/up).
  *
- * The calls below take the expert banks as plain arrays, not as descriptor
- * tables, and the sorted pairs' offsets, not tile lists: tiles are cut
- * inside.  They keep no state in the workspace; calls that overlap in time
- * need a workspace each.
+ * The projection calls take the expert banks as arrays of tiled matrices
+ * (moe_mx4_tile_bank), not as descriptor tables, and the sorted pairs'
+ * offsets, not tile lists: tiles of rows are cut inside.  They keep no state
+ * in the workspace; calls that overlap in time need a workspace each.
  * ===================================================================== */
 #define MOE_A4 2             /* activations in MXFP4 (moe_mx4_* calls only) */
-
-/* Matrices of one bank (HOST struct, device pointers): codes
- * [n][N][K/2], scales [n][N][K/32], contiguous.  codes 16-byte, scales
- * 4-byte aligned. */
-typedef struct moe_mxbank {
-  const uint8_t* codes;
-  const uint8_t* scales;
-} moe_mxbank;
 
 /* ---------------------------------------------------------------------
  * moe_mx4_quant_rows -- rows to MXFP4 by the rule above (activations, or
@@ -624,6 +616,31 @@ moe_status moe_mx4_quant_rows(const void* src, int src_is_f32, int R, int C, int
  * ------------------------------------------------------------------- */
 moe_status moe_mx4_dequant_rows(const uint8_t* codes, const uint8_t* scales, int R, int C,
                                 void* dst, int dst_is_f32, int ld, void* stream);
+
+/* ---------------------------------------------------------------------
+ * moe_mx4_tile_bank -- n matrices [N][K] of plain rows (codes [n][N][K/2],
+ * scales [n][N][K/32], as moe_mx4_quant_rows writes them) to the layout that
+ * the projections read, once per set of weights: pieces of 16 rows x 128 K of
+ * 1 KB in the order (matrix, 16-row block, piece along K); 16-byte slot 16g + c
+ * of piece s holds block 4s + g of row c.  Scales: 256 bytes per four pieces,
+ * byte j of 4-byte slot 16g + c the scale of block 4(4S + j) + g of row c.
+ * Blocks past K are zeros.
+ *   dst_codes   moe_mx4_bank_code_bytes(n, N, K) bytes, 16-byte aligned
+ *   dst_scales  moe_mx4_bank_scale_bytes(n, N, K) bytes, 4-byte aligned
+ * Limits: N % 16 == 0, K % 32 == 0 (else MOE_E_UNSUPPORTED; the sizes are 0
+ * for what is refused).  codes 16-byte aligned; no overlap.
+ * ------------------------------------------------------------------- */
+size_t moe_mx4_bank_code_bytes(int n, int N, int K);
+size_t moe_mx4_bank_scale_bytes(int n, int N, int K);
+moe_status moe_mx4_tile_bank(const uint8_t* codes, const uint8_t* scales, int n, int N, int K,
+                             uint8_t* dst_codes, uint8_t* dst_scales, void* stream);
+
+/* Tiled matrices of one bank (HOST struct, device pointers): as
+ * moe_mx4_tile_bank wrote them.  codes 16-byte, scales 4-byte aligned. */
+typedef struct moe_mxbank {
+  const uint8_t* codes;
+  const uint8_t* scales;
+} moe_mxbank;
 
 /* Workspace of the calls below (device memory, 256-byte aligned, need not
  * be cleared); 0 for sizes they refuse. */

@@ -105,6 +105,10 @@ _SIGS = {
                                    c_void_p]),
     "moe_mx4_dequant_rows": (c_int, [c_void_p, c_void_p, c_int, c_int, c_void_p, c_int, c_int,
                                      c_void_p]),
+    "moe_mx4_bank_code_bytes": (c_size_t, [c_int, c_int, c_int]),
+    "moe_mx4_bank_scale_bytes": (c_size_t, [c_int, c_int, c_int]),
+    "moe_mx4_tile_bank": (c_int, [c_void_p, c_void_p, c_int, c_int, c_int, c_void_p, c_void_p,
+                                  c_void_p]),
     "moe_mx4_workspace_bytes": (c_size_t, [c_int] * 8),
     "moe_mx4_gateup_silu": (c_int, [c_int, c_void_p, c_int, c_int, c_int, c_int, c_int,
                                     c_void_p, c_void_p, c_int, c_int, c_void_p, c_void_p,
@@ -376,6 +380,19 @@ def moe_mx4_quant_rows(src, src_is_f32, R, C, ld, codes, scales, stream=None, ch
 def moe_mx4_dequant_rows(codes, scales, R, C, dst, dst_is_f32, ld, stream=None, check=True):
     return _call("moe_mx4_dequant_rows", _ptr(codes), _ptr(scales), R, C, _ptr(dst), dst_is_f32,
                  ld, _stream(stream), check=check)
+
+
+def moe_mx4_bank_code_bytes(n, N, K) -> int:
+    return load().moe_mx4_bank_code_bytes(n, N, K)
+
+
+def moe_mx4_bank_scale_bytes(n, N, K) -> int:
+    return load().moe_mx4_bank_scale_bytes(n, N, K)
+
+
+def moe_mx4_tile_bank(codes, scales, n, N, K, dst_codes, dst_scales, stream=None, check=True):
+    return _call("moe_mx4_tile_bank", _ptr(codes), _ptr(scales), n, N, K, _ptr(dst_codes),
+                 _ptr(dst_scales), _stream(stream), check=check)
 
 
 def moe_mx4_workspace_bytes(act, T, H, I, E, k, n_shared=0, I_shared=0) -> int:

@@ -91,7 +91,7 @@ moe_status gateup(int act, const uint16_t* x, int T, int H, int I, int E, int k,
   if (act == MOE_A4) {
     uint8_t* q = reinterpret_cast<uint8_t*>(ws + L.qx);
     uint8_t* sc = reinterpret_cast<uint8_t*>(ws + L.sx);
-    if (launch_mx_quant(x, 0, T, H, H, q, sc, mx_pad_k(H), s) != hipSuccess) return MOE_E_DEVICE;
+    if (launch_mx_quant(x, 0, T, H, H, q, sc, mx_pad_k(H), true, s) != hipSuccess) return MOE_E_DEVICE;
     a.q = q;
     a.s = sc;
   }
@@ -141,10 +141,11 @@ moe_status down(int act, const uint16_t* h, int T, int H, int I, int E, int k,
   if (act == MOE_A4) {
     uint8_t* q = reinterpret_cast<uint8_t*>(ws + L.qh);
     uint8_t* sc = reinterpret_cast<uint8_t*>(ws + L.sh);
-    hipError_t e = launch_mx_quant(h, 0, P, I, ld_h, q, sc, hp, s);
+    hipError_t e = launch_mx_quant(h, 0, P, I, ld_h, q, sc, hp, true, s);
     if (e == hipSuccess && n_shared > 0)
       e = launch_mx_quant(h + (size_t)P * ld_h, 0, n_shared * T, I_shared, ld_h,
-                          q + (size_t)P * (hp / 2), sc + (size_t)P * (hp / kMxBlock), hp, s);
+                          q + (size_t)P * (hp / 2), sc + (size_t)P * (hp / kMxBlock), hp,
+                          true, s);
     if (e != hipSuccess) return MOE_E_DEVICE;
     a.q = q;
     a.s = sc;
@@ -200,7 +201,7 @@ moe_status moe_mx4_quant_rows(const void* src, int src_is_f32, int R, int C, int
   if (!aligned(src, src_is_f32 ? 4 : 2) || !aligned(codes, 4)) return MOE_E_INVAL;
   const moe_status d = device_usable();
   if (d != MOE_OK) return d;
-  return from_hip(launch_mx_quant(src, src_is_f32, R, C, ld, codes, scales, C,
+  return from_hip(launch_mx_quant(src, src_is_f32, R, C, ld, codes, scales, C, false,
                                   static_cast<hipStream_t>(stream)));
 }
 
@@ -216,6 +217,30 @@ moe_status moe_mx4_dequant_rows(const uint8_t* codes, const uint8_t* scales, int
   if (d != MOE_OK) return d;
   return from_hip(launch_mx_dequant(codes, scales, R, C, dst, dst_is_f32, ld,
                                     static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_mx4_bank_code_bytes(int n, int N, int K) {
+  if (n <= 0 || N <= 0 || K <= 0 || N % 16 || K % kMxBlock) return 0;
+  return n * mx_code_bytes(N, K);
+}
+
+size_t moe_mx4_bank_scale_bytes(int n, int N, int K) {
+  if (n <= 0 || N <= 0 || K <= 0 || N % 16 || K % kMxBlock) return 0;
+  return n * mx_scale_bytes(N, K);
+}
+
+moe_status moe_mx4_tile_bank(const uint8_t* codes, const uint8_t* scales, int n, int N, int K,
+                             uint8_t* dst_codes, uint8_t* dst_scales, void* stream) {
+  if (n < 0 || N <= 0 || K <= 0) return MOE_E_INVAL;
+  if (N % 16 || K % kMxBlock) return MOE_E_UNSUPPORTED;
+  if (n == 0) return MOE_OK;
+  if (!codes || !scales || !dst_codes || !dst_scales) return MOE_E_INVAL;
+  if (codes == dst_codes || scales == dst_scales) return MOE_E_INVAL;
+  if (!aligned(codes, 16) || !aligned(dst_codes, 16) || !aligned(dst_scales, 4)) return MOE_E_INVAL;
+  const moe_status d = device_usable();
+  if (d != MOE_OK) return d;
+  return from_hip(launch_mx_tile(codes, scales, n, N, K, dst_codes, dst_scales,
+                                 static_cast<hipStream_t>(stream)));
 }
 
 size_t moe_mx4_workspace_bytes(int act, int T, int H, int I, int E, int k, int n_shared,

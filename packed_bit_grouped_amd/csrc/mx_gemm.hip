@@ -8,12 +8,8 @@
 // units, so SiLU*mul pairs registers of one lane, or 64 down rows - as four
 // 16-row fragments against all of the tile's rows.
 //
-//  * Weights go from memory into a register ring kD steps of 256 K ahead:
-//    lane (row c = lane % 16, group g = lane / 16) holds blocks 2g and 2g + 1
-//    of the step, so a load instruction covers whole 128-byte runs of 16 rows
-//    and the lane's two scale bytes are one 16-bit load.  Sub-step j multiplies
-//    block 2g + j of every lane (a sum over K does not care which lane holds
-//    which block).
+//  * Weights go from memory into a register ring kD steps of 256 K ahead, two
+//    tiled pieces per fragment and step (a contiguous kilobyte per load).
 //  * Activations go from memory straight into a ring of LDS buffers (loads
 //    that write LDS; rows gathered by token).  A4: 128 bytes of codes per row
 //    and step, chunk q of row m in slot q ^ ((m >> 1) & 7); the scale bytes of
@@ -23,10 +19,9 @@
 //  * A4 feeds codes and scales to the scaled 16x16x128 instruction; A16
 //    expands a fragment's 8 codes to bf16 by four conversions (exact) for one
 //    16x16x32 step against every row fragment.
-//  * Activation rows are padded to whole steps (codes and scales 0, or bf16
-//    zeros) by the pass that quantises or copies them, so K's tail needs no
-//    cases; the tail's weight scales are cleared, because a stray 255 there
-//    would make NaN of the zeros.
+//  * Activation rows are whole steps, zeros behind K, by the pass that
+//    quantises or copies them, and the tiles' scales behind K are 0 (never
+//    255), so K's tail needs no cases.
 #include "mx_common.h"
 
 namespace moe {
@@ -97,7 +92,7 @@ struct Tile {
   int orow;             // first output row
 };
 
-template <int MODE, bool ACT4, int MT, bool SW>
+template <int MODE, bool ACT4, int MT>
 __device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, __amdgpu_buffer_rsrc_t crs,
                                      __amdgpu_buffer_rsrc_t srs, u32x4* As, const int* tok,
                                      const uint8_t* sc, int nrows) {
@@ -109,49 +104,31 @@ __device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, __amdgpu
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int n_st = t.n_st, n_stage = n_st * R::kStages;
-  const int nblk = t.K / kMxBlock;
 
-  // ---- weight rows of this lane; rows past the end lie past the buffer
+  // ---- 16-row blocks of this wave; blocks past the end lie past the buffer
+  const int pieces = mx_pieces(t.K), words = (pieces + 3) / 4;
   int coff[kNF], soff[kNF];
 #pragma unroll
   for (int f = 0; f < kNF; ++f) {
-    int row;
-    bool ok;
-    if (MODE == 0) {
-      const int u = t.u0 + 16 * (f & 1) + c;
-      ok = u < t.U;
-      row = (f >> 1) * t.U + u;
-    } else {
-      row = t.u0 + 16 * f + c;
-      ok = row < t.U;
-    }
-    coff[f] = ok ? row * (t.K / 2) + 32 * g : 0x40000000;
-    soff[f] = ok ? row * nblk + 2 * g : 0x40000000;
+    const int u = MODE == 0 ? t.u0 + 16 * (f & 1) : t.u0 + 16 * f;
+    const int rb = ((MODE == 0 && f >= 2 ? t.U : 0) + u) / 16;
+    coff[f] = u < t.U ? rb * pieces * 1024 + lane * 16 : 0x40000000;
+    soff[f] = u < t.U ? rb * words * 256 + lane * 4 : 0x40000000;
   }
-  // scale bytes of the last step's blocks that exist
-  const int left = nblk - (n_st - 1) * (kKS / kMxBlock) - 2 * g;
-  const uint32_t tail = left >= 2 ? 0xFFFFu : left == 1 ? 0xFFu : 0u;
 
   auto load_c = [&](int st, int j, WStep& w) {
-    const int o = st < n_st ? st * (kKS / 2) + 16 * j : 0x40000000;   // past the end: nothing is read
+    const int o = st < n_st ? st * 2048 + j * 1024 : 0x40000000;   // past the end: nothing is read
 #pragma unroll
     for (int f = 0; f < kNF; ++f)
       w.c[f][j] = __builtin_amdgcn_raw_buffer_load_b128(crs, coff[f] + o, 0, 2);
   };
   auto load_s = [&](int st, WStep& w) {
-    const int o = st < n_st ? st * (kKS / kMxBlock) : 0x40000000;
+    const int o = st < n_st ? (st >> 1) * 256 + (st & 1) * 2 : 0x40000000;
 #pragma unroll
-    for (int f = 0; f < kNF; ++f) {
-      if (SW) {
-        w.s[f] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(srs, soff[f] + o, 0, 0);
-      } else {
-        const uint32_t lo = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(srs, soff[f] + o, 0, 0);
-        const uint32_t hi = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(srs, soff[f] + o + 1, 0, 0);
-        w.s[f] = lo | (hi << 8);
-      }
-    }
+    for (int f = 0; f < kNF; ++f)
+      w.s[f] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(srs, soff[f] + o, 0, 0);
   };
-  constexpr int nS = SW ? kNF : 2 * kNF;
+  constexpr int nS = kNF;
   constexpr int nW = 2 * kNF + nS;             // weight loads per step
 
   // ---- activation pieces of this lane: LDS slot q of a stage holds the chunk
@@ -165,13 +142,12 @@ __device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, __amdgpu
     if (ACT4) {
       aoff[i] = tok[m] * t.row_bytes + (((q & 7) ^ ((m >> 1) & 7)) * 16);
     } else {
-      const int ch = (q & 15) ^ (m & 15);      // group ch / 4, 16 bytes ch % 4 of its block
-      aoff[i] = tok[m] * t.row_bytes + (ch >> 2) * 128 + (ch & 3) * 16;
+      aoff[i] = tok[m] * t.row_bytes + (((q & 15) ^ (m & 15)) * 16);
     }
   }
   auto dma = [&](int sg, int buf) {
     sg = min(sg, n_stage - 1);                 // past the end: the last stage once more
-    const int o = ACT4 ? sg * 128 : (sg >> 1) * 512 + (sg & 1) * 64;
+    const int o = sg * (ACT4 ? 128 : 256);
 #pragma unroll
     for (int i = 0; i < nA; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
@@ -200,15 +176,16 @@ __device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, __amdgpu
   mx_bf16x8 wv[2][kNF];
   uint32_t sx[MT];
   auto x_at = [&](int b, int q) {
-    return Ac + b * kBuf + (((ACT4 ? 2 : 4) * g + q) ^ sw);
+    return Ac + b * kBuf + ((ACT4 ? 4 * q + g : 4 * g + q) ^ sw);
   };
-  auto sx_at = [&](int st) { return sc + c * ga.sc_pitch + min(st, n_st - 1) * 8 + 2 * g; };
-  auto expand = [&](int st, int j, int q, const WStep& w, mx_bf16x8(&v)[kNF]) {
-    const uint32_t keep = st >= n_st - 1 ? tail : 0xFFFFu;
+  auto sx_at = [&](int st) {
+    st = min(st, n_st - 1);
+    return sc + c * ga.sc_pitch + (st >> 1) * 16 + 4 * g + (st & 1) * 2;
+  };
+  auto expand = [&](int j, int q, const WStep& w, mx_bf16x8(&v)[kNF]) {
 #pragma unroll
     for (int f = 0; f < kNF; ++f)
-      v[f] = mx_word_to_bf16(w.c[f][j][q],
-                             __uint_as_float((((w.s[f] & keep) >> (8 * j)) & 255u) << 23));
+      v[f] = mx_word_to_bf16(w.c[f][j][q], mx_scale_f32((w.s[f] >> (8 * j)) & 255u));
   };
   // issue order of a sub-step: per row fragment four matrix instructions with
   // the conversions and memory loads between them, then its LDS reads
@@ -237,10 +214,9 @@ __device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, __amdgpu
     const int a = st * R::kStages + j;
     const int nb = buf == kBufs - 1 ? 0 : buf + 1;
     if constexpr (ACT4) {
-      const uint32_t keep = st == n_st - 1 ? tail : 0xFFFFu;
       uint32_t sws[kNF];
 #pragma unroll
-      for (int f = 0; f < kNF; ++f) sws[f] = w.s[f] & keep;
+      for (int f = 0; f < kNF; ++f) sws[f] = w.s[f];
       const u32x4* p = x_at(buf, 1);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
@@ -274,13 +250,13 @@ __device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, __amdgpu
         const u32x4* p;
         if (q < kQ - 1) {
           p = x_at(buf, q + 1);
-          expand(st, j, q + 1, w, wv[nxt]);
+          expand(j, q + 1, w, wv[nxt]);
         } else {
           vm_barrier<kAfter>();
           dma(a + kBufs, buf);
           p = x_at(nb, 0);
-          if (j == 0) expand(st, 1, 0, w, wv[nxt]);
-          else expand(st + 1, 0, 0, wn, wv[nxt]);
+          if (j == 0) expand(1, 0, w, wv[nxt]);
+          else expand(0, 0, wn, wv[nxt]);
           load_c(st + kD, j, w);
           if (j == 1) load_s(st + kD, w);
         }
@@ -339,7 +315,7 @@ __device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, __amdgpu
       for (int m = 0; m < MT; ++m)
         sx[m] = *reinterpret_cast<const uint16_t*>(ps + 16 * m * ga.sc_pitch);
     } else {
-      expand(0, 0, 0, w0, wv[0]);
+      expand(0, 0, w0, wv[0]);
     }
   }
 
@@ -386,7 +362,7 @@ __device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, __amdgpu
 // even size.  Every wave scans the offsets (lanes count 1..8 experts each).
 __device__ __forceinline__ int tiles_of(int n) { return (n + kRowsMax - 1) / kRowsMax; }
 
-template <int MODE, bool ACT4, bool SW>
+template <int MODE, bool ACT4>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void mx_gemm_kernel(GemmArgs ga) {
   extern __shared__ __align__(16) unsigned char smem[];
@@ -470,10 +446,9 @@ void mx_gemm_kernel(GemmArgs ga) {
   const int act_rows = MODE == 0 ? a.T : (is_sh ? a.n_shared * a.T : a.P);
   t.act_bytes = (uint32_t)(act_rows * stride);
   const int N = MODE == 0 ? 2 * t.U : t.U;
-  const size_t mat = (size_t)N * (t.K / 2);
-  const __amdgpu_buffer_rsrc_t crs = make_rsrc((is_sh ? a.w_sh : a.w) + (size_t)e * mat, (uint32_t)mat);
-  const __amdgpu_buffer_rsrc_t srs =
-      make_rsrc((is_sh ? a.ws_sh : a.ws) + (size_t)e * (mat / 16), (uint32_t)(mat / 16));
+  const size_t cb = mx_code_bytes(N, t.K), sb = mx_scale_bytes(N, t.K);
+  const __amdgpu_buffer_rsrc_t crs = make_rsrc((is_sh ? a.w_sh : a.w) + e * cb, (uint32_t)cb);
+  const __amdgpu_buffer_rsrc_t srs = make_rsrc((is_sh ? a.ws_sh : a.ws) + e * sb, (uint32_t)sb);
 
   if (tid < kRowsMax) {
     const int m = tid < nrows ? tid : 0;   // padding rows repeat row 0 (not stored)
@@ -504,7 +479,7 @@ void mx_gemm_kernel(GemmArgs ga) {
           *reinterpret_cast<const uint32_t*>(src + (size_t)tok[m] * (ga.KP / kMxBlock) + q * 4);
     }
   }
-#define MX_BODY(MT) body<MODE, ACT4, MT, SW>(ga, t, crs, srs, As, tok, sc, nrows)
+#define MX_BODY(MT) body<MODE, ACT4, MT>(ga, t, crs, srs, As, tok, sc, nrows)
   if (mt <= 2) MX_BODY(2);
   else if (mt <= 4) MX_BODY(4);
   else if (mt <= 6) MX_BODY(6);
@@ -515,11 +490,7 @@ void mx_gemm_kernel(GemmArgs ga) {
 
 template <int MODE, bool ACT4>
 hipError_t launch(const GemmArgs& ga, size_t lds, long long grid, hipStream_t st) {
-  // the two scale bytes of a lane in one load where rows start at even bytes
-  const bool sw = (ga.p.K / kMxBlock) % 2 == 0 &&
-                  (ga.p.n_shared == 0 || (ga.p.K_sh / kMxBlock) % 2 == 0);
-  auto k = sw ? mx_gemm_kernel<MODE, ACT4, true> : mx_gemm_kernel<MODE, ACT4, false>;
-  k<<<(int)grid, kThreads, lds, st>>>(ga);
+  mx_gemm_kernel<MODE, ACT4><<<(int)grid, kThreads, lds, st>>>(ga);
   return hipGetLastError();
 }
 
@@ -537,7 +508,7 @@ bool mx_gemm_ok(int act4, long long rows, int ld, int K, int K_sh, int N, int N_
   // 32-bit offsets into one matrix and into the activation rows
   const long long stride = act4 ? mx_pad_k(ld) / 2 : 2LL * mx_pad_k(ld);
   if (rows * stride >= (1LL << 31)) return false;
-  return (long long)N * K / 2 < (1LL << 30) && (long long)N_sh * K_sh / 2 < (1LL << 30);
+  return mx_code_bytes(N, K) < (1u << 30) && mx_code_bytes(N_sh, K_sh) < (1u << 30);
 }
 
 hipError_t launch_mx_gemm(const MxProj& a, int mode, int act4, hipStream_t st) {

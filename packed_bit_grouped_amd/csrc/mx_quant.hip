@@ -22,7 +22,7 @@ constexpr int kQuantThreads = 256;
 template <bool F32, bool VEC>
 __global__ __launch_bounds__(kQuantThreads) void mx_quant_kernel(
     const void* __restrict__ src, int R, int C8, int ld, uint8_t* __restrict__ q,
-    uint8_t* __restrict__ s, int CP8) {
+    uint8_t* __restrict__ s, int CP8, int words) {
   const long long n = (long long)R * CP8;   // eights of values, the padding's too
   for (long long i = (long long)blockIdx.x * kQuantThreads + threadIdx.x; i < n;
        i += (long long)gridDim.x * kQuantThreads) {
@@ -73,7 +73,11 @@ __global__ __launch_bounds__(kQuantThreads) void mx_quant_kernel(
       w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], sc, 3);
     }
     reinterpret_cast<uint32_t*>(q)[i] = w;
-    if ((c & 3) == 0) s[i >> 2] = (uint8_t)sb;
+    if ((c & 3) == 0) {
+      long long b = i >> 2;   // block; words: bytes 4j + g of sixteen change places with 4g + j
+      if (words) b = (b & ~15LL) | ((b & 3) << 2) | ((b >> 2) & 3);
+      s[b] = (uint8_t)sb;
+    }
   }
 }
 
@@ -137,6 +141,30 @@ __global__ __launch_bounds__(kQuantThreads) void mx_pad_kernel(const uint16_t* _
   }
 }
 
+// One workgroup wave per piece: lane (c, g) copies block 4s + g of its row; the
+// wave of a word's first piece gathers the four scale bytes of its lanes.
+__global__ __launch_bounds__(kQuantThreads) void mx_tile_kernel(
+    const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, long long n_pieces,
+    int pieces, int nblk, uint8_t* __restrict__ dst, uint8_t* __restrict__ dst_s) {
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  for (long long p = (long long)blockIdx.x * (kQuantThreads / 64) + (threadIdx.x >> 6);
+       p < n_pieces; p += (long long)gridDim.x * (kQuantThreads / 64)) {
+    const long long rb = p / pieces;   // 16-row block, over all matrices
+    const int s = (int)(p - rb * pieces);
+    const long long row = rb * 16 + c;
+    const int b = 4 * s + g;
+    const mx_u32x4 zero = {0, 0, 0, 0};
+    reinterpret_cast<mx_u32x4*>(dst)[p * 64 + lane] =
+        b < nblk ? *reinterpret_cast<const mx_u32x4*>(codes + (row * nblk + b) * 16) : zero;
+    if ((s & 3) == 0) {
+      uint32_t w = 0;
+      for (int j = 0; j < 4; ++j)
+        if (b + 4 * j < nblk) w |= (uint32_t)scales[row * nblk + b + 4 * j] << (8 * j);
+      reinterpret_cast<uint32_t*>(dst_s)[(rb * ((pieces + 3) / 4) + (s >> 2)) * 64 + lane] = w;
+    }
+  }
+}
+
 int quant_blocks(long long eights) {
   const long long b = (eights + kQuantThreads - 1) / kQuantThreads;
   return (int)(b < 16384 ? b : 16384);
@@ -149,12 +177,21 @@ bool rows_aligned(const void* p, int ld, int elem) {
 }  // namespace
 
 hipError_t launch_mx_quant(const void* src, int is_f32, int R, int C, int ld, uint8_t* q,
-                           uint8_t* s, int CP, hipStream_t st) {
+                           uint8_t* s, int CP, bool words, hipStream_t st) {
   const int blocks = quant_blocks((long long)R * (CP / 8));
   const bool vec = rows_aligned(src, ld, is_f32 ? 4 : 2);
   auto k = is_f32 ? (vec ? mx_quant_kernel<true, true> : mx_quant_kernel<true, false>)
                   : (vec ? mx_quant_kernel<false, true> : mx_quant_kernel<false, false>);
-  k<<<blocks, kQuantThreads, 0, st>>>(src, R, C / 8, ld, q, s, CP / 8);
+  k<<<blocks, kQuantThreads, 0, st>>>(src, R, C / 8, ld, q, s, CP / 8, words);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_tile(const uint8_t* codes, const uint8_t* scales, int n, int N, int K,
+                          uint8_t* dst_codes, uint8_t* dst_scales, hipStream_t st) {
+  const int pieces = mx_pieces(K);
+  const long long n_pieces = (long long)n * (N / 16) * pieces;
+  mx_tile_kernel<<<quant_blocks(n_pieces * 64), kQuantThreads, 0, st>>>(
+      codes, scales, n_pieces, pieces, K / kMxBlock, dst_codes, dst_scales);
   return hipGetLastError();
 }
 

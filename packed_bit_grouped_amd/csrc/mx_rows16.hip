@@ -7,14 +7,12 @@
 // weight, read once), so a workgroup is small and loads everything it needs
 // at once.  It owns 16 units (a gate and an up row each, or 2 x 16 down rows)
 // of one tile; its four waves split K and meet in LDS.  Both operands go from
-// memory straight into the matrix instruction's registers: lane (row c = lane
-// % 16, group g = lane / 16) holds NB consecutive 32-value blocks of row c,
-// so its codes are one contiguous run, its scales one word, and step j of a
-// chunk multiplies block j of every lane - the sum over K does not care which
-// lane group holds which block as long as both operands agree.  A16 expands a
-// block to bf16 by the conversion instruction that takes the scale (exact)
-// and runs four 16x16x32 bf16 steps; A4 feeds codes and scale bytes to the
-// scaled 16x16x128 instruction as they are.
+// memory straight into the matrix instruction's registers, the weights as
+// tiled pieces (a contiguous kilobyte per load), the activations as the same
+// blocks of their rows.  A16 expands a block to bf16 by the conversion
+// instruction that takes the scale (exact) and runs four 16x16x32 bf16 steps;
+// A4 feeds codes and scale bytes to the scaled 16x16x128 instruction as they
+// are.
 #include "mx_common.h"
 
 namespace moe {
@@ -26,21 +24,14 @@ constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kPitch = 20;     // LDS words per 16 (4 rows of 20 words: 16 banks apart)
 
-// NB scale bytes of a row from block b on, as one word (absent blocks: 0).
-// WORDS: the row stride is a multiple of NB, so one load serves.
-template <int NB, bool WORDS>
-__device__ __forceinline__ uint32_t load_scales(const uint8_t* __restrict__ row, int b, int nblk) {
-  if (WORDS) {
-    if (b >= nblk) return 0;
-    if (NB == 4) return *reinterpret_cast<const uint32_t*>(row + b);
-    if (NB == 2) return *reinterpret_cast<const uint16_t*>(row + b);
-    return row[b];
-  }
-  uint32_t v = 0;
-#pragma unroll
-  for (int j = 0; j < NB; ++j)
-    if (b + j < nblk) v |= (uint32_t)row[b + j] << (8 * j);
-  return v;
+// The scale bytes of NB pieces from piece s on (s % NB == 0): bytes of the
+// lane's word of four pieces.
+template <int NB>
+__device__ __forceinline__ uint32_t load_scales(const uint8_t* __restrict__ word, int s) {
+  const uint8_t* p = word + (s & 3);
+  if (NB == 4) return *reinterpret_cast<const uint32_t*>(p);
+  if (NB == 2) return *reinterpret_cast<const uint16_t*>(p);
+  return *p;
 }
 
 template <int NB, int J = 0>
@@ -55,7 +46,7 @@ __device__ __forceinline__ void fp4_steps(const mx_u32x4 (&w0)[NB], uint32_t s0,
   }
 }
 
-template <int MODE, bool ACT4, int NB, bool WORDS>
+template <int MODE, bool ACT4, int NB>
 __global__ __launch_bounds__(kThreads) void mx_rows16_kernel(MxProj a, int n_sh_tiles, int n_ub) {
   __shared__ float red[kWaves][2][kTM * kPitch];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -78,13 +69,15 @@ __global__ __launch_bounds__(kThreads) void mx_rows16_kernel(MxProj a, int n_sh_
   const int u0 = ub * (MODE == 0 ? 16 : 32);   // first unit (gate/up) or row (down)
   if (u0 >= U) return;
   const int N = MODE == 0 ? 2 * U : U;
-  const int nblk = K / kMxBlock;
-  const uint8_t* wq = (is_sh ? a.w_sh : a.w) + (size_t)e * N * (K / 2);
-  const uint8_t* wsc = (is_sh ? a.ws_sh : a.ws) + (size_t)e * N * nblk;
-  // weight rows of this lane: rows past the end repeat the last one (their
-  // results are not stored)
-  const int n0 = min(u0 + c, U - 1);
-  const int n1 = MODE == 0 ? U + n0 : min(u0 + 16 + c, U - 1);
+  const int nblk = K / kMxBlock, pieces = mx_pieces(K), words = (pieces + 3) / 4;
+  const uint8_t* wq = (is_sh ? a.w_sh : a.w) + e * mx_code_bytes(N, K);
+  const uint8_t* wsc = (is_sh ? a.ws_sh : a.ws) + e * mx_scale_bytes(N, K);
+  // the two 16-row blocks of this workgroup
+  const size_t rb0 = u0 / 16, rb1 = MODE == 0 ? (U + u0) / 16 : u0 / 16 + 1;
+  const mx_u32x4* q0 = reinterpret_cast<const mx_u32x4*>(wq) + rb0 * pieces * 64 + lane;
+  const mx_u32x4* q1 = reinterpret_cast<const mx_u32x4*>(wq) + rb1 * pieces * 64 + lane;
+  const uint8_t* sw0 = wsc + (rb0 * words * 64 + lane) * 4;
+  const uint8_t* sw1 = wsc + (rb1 * words * 64 + lane) * 4;
 
   // ---- the activation row of this lane's column
   const int orow = is_sh ? a.P + e * a.T + r0 : r0;   // first row of h / y
@@ -104,31 +97,34 @@ __global__ __launch_bounds__(kThreads) void mx_rows16_kernel(MxProj a, int n_sh_
 
   mx_f32x4 a0 = {0, 0, 0, 0}, a1 = {0, 0, 0, 0};
   const mx_u32x4 zero = {0, 0, 0, 0};
-  for (int b = (wave * 4 + g) * NB; b - g * NB < nblk; b += kWaves * 4 * NB) {
+  for (int s = wave * NB; s < pieces; s += kWaves * NB) {
     mx_u32x4 w0[NB], w1[NB];
-    const mx_u32x4* p0 = reinterpret_cast<const mx_u32x4*>(wq + (size_t)n0 * (K / 2)) + b;
-    const mx_u32x4* p1 = reinterpret_cast<const mx_u32x4*>(wq + (size_t)n1 * (K / 2)) + b;
 #pragma unroll
-    for (int j = 0; j < NB; ++j) w0[j] = b + j < nblk ? __builtin_nontemporal_load(p0 + j) : zero;
+    for (int j = 0; j < NB; ++j)
+      w0[j] = s + j < pieces ? __builtin_nontemporal_load(q0 + (s + j) * 64) : zero;
 #pragma unroll
-    for (int j = 0; j < NB; ++j) w1[j] = b + j < nblk ? __builtin_nontemporal_load(p1 + j) : zero;
-    const uint32_t s0 = load_scales<NB, WORDS>(wsc + (size_t)n0 * nblk, b, nblk);
-    const uint32_t s1 = load_scales<NB, WORDS>(wsc + (size_t)n1 * nblk, b, nblk);
+    for (int j = 0; j < NB; ++j)
+      w1[j] = s + j < pieces ? __builtin_nontemporal_load(q1 + (s + j) * 64) : zero;
+    const uint32_t s0 = load_scales<NB>(sw0 + (s >> 2) * 256, s);
+    const uint32_t s1 = load_scales<NB>(sw1 + (s >> 2) * 256, s);
     if (ACT4) {
-      mx_u32x4 x[NB];
+      // rows of whole words, zeros behind K
       const int KP = mx_pad_k(a.ld_in);
-      const mx_u32x4* px = reinterpret_cast<const mx_u32x4*>(a.q + xrow * (KP / 2)) + b;
+      mx_u32x4 x[NB];
+      const mx_u32x4* px = reinterpret_cast<const mx_u32x4*>(a.q + xrow * (KP / 2)) + 4 * s + g;
 #pragma unroll
-      for (int j = 0; j < NB; ++j) x[j] = have && b + j < nblk ? px[j] : zero;
-      const uint32_t sx = have ? load_scales<NB, true>(a.s + xrow * (KP / kMxBlock), b, nblk) : 0u;
+      for (int j = 0; j < NB; ++j) x[j] = have && s + j < pieces ? px[4 * j] : zero;
+      const uint32_t sx =
+          have ? load_scales<NB>(a.s + xrow * (KP / kMxBlock) + (s >> 2) * 16 + 4 * g, s) : 0u;
       fp4_steps<NB>(w0, s0, w1, s1, x, sx, a0, a1);
     } else {
-      const mx_u32x4* px = reinterpret_cast<const mx_u32x4*>(a.x + xrow * a.ld_in) + b * 4;
+      const mx_u32x4* px = reinterpret_cast<const mx_u32x4*>(a.x + xrow * a.ld_in);
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
+        const int b = 4 * (s + j) + g;
         mx_u32x4 x[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) x[t] = have && b + j < nblk ? px[j * 4 + t] : zero;
+        for (int t = 0; t < 4; ++t) x[t] = have && b < nblk ? px[b * 4 + t] : zero;
         const float f0 = mx_scale_f32((s0 >> (8 * j)) & 255u);
         const float f1 = mx_scale_f32((s1 >> (8 * j)) & 255u);
 #pragma unroll
@@ -174,17 +170,13 @@ hipError_t launch(const MxProj& a, hipStream_t st) {
   const long long grid =
       (long long)(n_sh_tiles + moe_permute_max_tiles(a.T, a.k, a.E, kTM)) * n_ub;
   if (grid >= (1LL << 31)) return hipErrorInvalidValue;
-  const int nb = a.K / kMxBlock, nb_sh = a.n_shared > 0 ? a.K_sh / kMxBlock : nb;
-  const int most = nb > nb_sh ? nb : nb_sh;
-#define MX_GO(NB)                                                                             \
-  (nb % NB == 0 && nb_sh % NB == 0                                                            \
-       ? mx_rows16_kernel<MODE, ACT4, NB, true><<<(int)grid, kThreads, 0, st>>>(a, n_sh_tiles, n_ub) \
-       : mx_rows16_kernel<MODE, ACT4, NB, false><<<(int)grid, kThreads, 0, st>>>(a, n_sh_tiles, n_ub))
+  const int K = a.n_shared > 0 && a.K_sh > a.K ? a.K_sh : a.K;
+  const int pieces = mx_pieces(K);
   // the longest run per lane that still gives every wave a chunk of K
-  if (most >= kWaves * 16) MX_GO(4);
-  else if (most >= kWaves * 8) MX_GO(2);
-  else MX_GO(1);
-#undef MX_GO
+  auto kern = pieces >= kWaves * 4   ? mx_rows16_kernel<MODE, ACT4, 4>
+              : pieces >= kWaves * 2 ? mx_rows16_kernel<MODE, ACT4, 2>
+                                     : mx_rows16_kernel<MODE, ACT4, 1>;
+  kern<<<(int)grid, kThreads, 0, st>>>(a, n_sh_tiles, n_ub);
   return hipGetLastError();
 }
 

@@ -6,8 +6,9 @@ runs in the HIP kernels behind the C ABI (include/moe_w4.h, the format and the
 layer are defined there).
 
 * ``quantize_rows`` / ``dequantize_rows``: bf16 or fp32 rows <-> codes, scales.
-* ``MxBank`` holds the expert matrices of a layer as (codes, scales) pairs of
-  stacked tensors: codes uint8 [n][N][K/2], scales uint8 [n][N][K/32].
+* ``MxBank`` lays the expert matrices of a layer out for the projections, once,
+  from (codes, scales) pairs of stacked tensors: codes uint8 [n][N][K/2], scales
+  uint8 [n][N][K/32].
 * ``MxBuffers`` preallocates every per-step buffer of one layer shape.
 * ``gateup_silu``, ``down_combine`` and ``run_layer`` issue the calls on the
   current stream of the tensors' device (or on ``stream``).  The outputs are
@@ -103,7 +104,7 @@ def dequantize_rows(codes, scales, dtype=torch.bfloat16, stream=None):
 
 
 def quantize_bank(w, stream=None):
-    """fp32 or bf16 matrices [n][N][K] to one (codes, scales) pair of MxBank."""
+    """fp32 or bf16 matrices [n][N][K] to one (codes, scales) pair for MxBank."""
     n, N, K = w.shape
     codes, scales = quantize_rows(w.reshape(n * N, K), stream=stream)
     return codes.view(n, N, K // 2), scales.view(n, N, K // BLOCK)
@@ -112,15 +113,17 @@ def quantize_bank(w, stream=None):
 class MxBank:
     """The matrices of one layer: w13 [E][2I][H] and w2 [E][H][I] of the routed
     experts, w13_shared [n_shared][2*I_shared][H] and w2_shared
-    [n_shared][H][I_shared] of the shared ones, each a (codes, scales) pair.
-    A bank for one of the projections alone holds that projection's pairs."""
+    [n_shared][H][I_shared] of the shared ones, each given as a (codes, scales)
+    pair of plain rows and kept tiled (moe_mx4_tile_bank): the pairs are not
+    needed any more.  A bank for one of the projections alone is given that
+    projection's pairs.  A later change of the weights needs a new bank."""
 
-    def __init__(self, w13=None, w2=None, w13_shared=None, w2_shared=None):
-        self.pairs, self.desc, self.shape = {}, {}, {}
+    def __init__(self, w13=None, w2=None, w13_shared=None, w2_shared=None, stream=None):
+        self.tiles, self.desc, self.shape = {}, {}, {}
         self.device = None
         for tag, p in (("w13", w13), ("w2", w2), ("w13_shared", w13_shared),
                        ("w2_shared", w2_shared)):
-            self.pairs[tag], self.desc[tag], self.shape[tag] = p, None, None
+            self.desc[tag] = self.shape[tag] = None
             if p is None:
                 continue
             codes, scales = p
@@ -130,7 +133,15 @@ class MxBank:
             _want(tag + " codes", codes, (torch.uint8,), (n, N, K // 2), self.device)
             self.device = codes.device
             _want(tag + " scales", scales, (torch.uint8,), (n, N, K // BLOCK), self.device)
-            self.desc[tag] = L.MxBankDesc(codes.data_ptr(), scales.data_ptr())
+            nc, ns = L.moe_mx4_bank_code_bytes(n, N, K), L.moe_mx4_bank_scale_bytes(n, N, K)
+            if nc == 0:
+                raise ValueError(f"{tag}: unsupported matrices (n, N, K) = {(n, N, K)}")
+            with _On(codes):
+                tc = torch.empty(nc, dtype=torch.uint8, device=codes.device)
+                ts = torch.empty(ns, dtype=torch.uint8, device=codes.device)
+                L.moe_mx4_tile_bank(codes, scales, n, N, K, tc, ts, stream)
+            self.tiles[tag] = (tc, ts)
+            self.desc[tag] = L.MxBankDesc(tc.data_ptr(), ts.data_ptr())
             self.shape[tag] = (n, N, K)
 
     def need(self, tag, n, N, K):

@@ -138,6 +138,26 @@ def test_rows_past_32_bit_offsets(mx):
     torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("n,N,K", [(1, 16, 32), (2, 48, 128), (3, 32, 352), (2, 64, 2080), (1, 128, 512)])
+def test_tiles_match_their_definition(mx, n, N, K):
+    """The header's layout, built here from plain rows."""
+    rng = np.random.default_rng(K)
+    codes = rng.integers(0, 256, (n, N, K // 2), dtype=np.uint8)
+    scales = rng.integers(0, 256, (n, N, K // 32), dtype=np.uint8)
+    pieces = -(-K // 128)
+    words = -(-pieces // 4)
+    blk = np.zeros((n, N // 16, 16, pieces * 4, 16), dtype=np.uint8)
+    blk[:, :, :, :K // 32] = codes.reshape(n, N // 16, 16, K // 32, 16)
+    want = blk.reshape(n, N // 16, 16, pieces, 4, 16).transpose(0, 1, 3, 4, 2, 5)   # s, g, c
+    sc = np.zeros((n, N // 16, 16, words * 16), dtype=np.uint8)
+    sc[..., :K // 32] = scales.reshape(n, N // 16, 16, K // 32)
+    want_s = sc.reshape(n, N // 16, 16, words, 4, 4).transpose(0, 1, 3, 5, 2, 4)    # S, g, c, j
+    bank = mx.MxBank((torch.from_numpy(codes).to(DEV), torch.from_numpy(scales).to(DEV)))
+    tc, ts = bank.tiles["w13"]
+    assert np.array_equal(tc.cpu().numpy(), want.ravel())
+    assert np.array_equal(ts.cpu().numpy(), want_s.ravel())
+
+
 # ---------------------------------------------------------------------------
 # projections
 
@@ -155,7 +175,7 @@ def make(mx, T, H, I, E, k, n_sh=0, I_sh=0, act="a16", seed=0, skew=0.0, out_f32
     s13, d["v13s"] = matrices(rng, n_sh, 2 * I_sh, H) if n_sh else (None, None)
     s2, d["v2s"] = matrices(rng, n_sh, H, I_sh) if n_sh else (None, None)
     d["gate"] = torch.from_numpy(rng.standard_normal((T, n_sh)).astype(np.float32)).to(DEV) if n_sh else None
-    d["bank"] = mx.MxBank(p13, p2, s13, s2)
+    d["w13"], d["bank"] = p13, mx.MxBank(p13, p2, s13, s2)
     d["B"] = mx.MxBuffers(T, H, I, E, k, n_sh, I_sh if n_sh else 0, act=act, device=DEV, out_f32=out_f32)
     d["B"].ws.fill_(255)     # nothing in the workspace may matter
     return d
@@ -352,7 +372,9 @@ def test_nan_and_inf_stay_in_their_token(mx, act, T):
 def test_marked_weight_block_makes_nan(mx, act, T):
     """A weight block with scale 255 is NaN in its unit and nowhere else."""
     d = make(mx, T, 128, 64, 2, 1, act=act, seed=3)
-    d["bank"].pairs["w13"][1][1, 5, 2] = 255       # expert 1, gate row 5
+    codes, scales = d["w13"]
+    scales[1, 5, 2] = 255                          # expert 1, gate row 5
+    d["bank"] = mx.MxBank((codes, scales))
     ids, w, perm = tables(d)
     h = f64(mx.gateup_silu(d["bank"], d["x"], torch.from_numpy(perm["offsets"]).to(DEV),
                            torch.from_numpy(perm["sorted_pair"]).to(DEV), d["B"]))

@@ -101,6 +101,29 @@ def test_rows_refusals(call, out):
     assert call(R=0, codes=None, scales=None, **{far: None}) == L.MOE_OK
 
 
+def _tile(**kw):
+    a = dict(codes=FAKE, scales=FAKE, n=2, N=64, K=96, dst_codes=2 * FAKE, dst_scales=2 * FAKE)
+    a.update(kw)
+    return L.moe_mx4_tile_bank(*a.values(), stream=0, check=False)
+
+
+def test_tile_refusals():
+    for kw in (dict(n=-1), dict(N=0), dict(K=0), dict(codes=None), dict(scales=None),
+               dict(dst_codes=None), dict(dst_scales=None), dict(dst_codes=FAKE),
+               dict(dst_scales=FAKE), dict(codes=FAKE + 8), dict(dst_codes=2 * FAKE + 8),
+               dict(dst_scales=2 * FAKE + 2)):
+        assert _tile(**kw) == L.MOE_E_INVAL, kw
+    for kw in (dict(N=40), dict(K=48)):
+        assert _tile(**kw) == L.MOE_E_UNSUPPORTED, kw
+    assert _tile(n=0) == L.MOE_OK
+    assert L.moe_mx4_bank_code_bytes(2, 64, 96) == 2 * 4 * 1024
+    assert L.moe_mx4_bank_scale_bytes(2, 64, 96) == 2 * 4 * 256
+    assert L.moe_mx4_bank_code_bytes(3, 32, 2080) == 3 * 2 * 17 * 1024
+    assert L.moe_mx4_bank_scale_bytes(3, 32, 2080) == 3 * 2 * 5 * 256
+    for args in ((0, 64, 96), (2, 40, 96), (2, 64, 48), (2, -16, 96)):
+        assert L.moe_mx4_bank_code_bytes(*args) == L.moe_mx4_bank_scale_bytes(*args) == 0
+
+
 BANK = L.MxBankDesc(FAKE, FAKE)
 SHAPE = dict(act=L.MOE_A16, T=4, H=256, I=128, E=8, k=2, n_shared=0, I_shared=0)
 
@@ -164,7 +187,7 @@ def test_workspace_size_of_refused_shapes_is_zero():
     def size(**kw):
         return L.moe_mx4_workspace_bytes(*dict(SHAPE, **kw).values())
     assert size() >= 4 * 2 * 256 * 4          # the fp32 rows of the down projection
-    assert size(act=L.MOE_A4) > size()
+    assert size(act=L.MOE_A4) >= 4 * 2 * 256 * 4 + 4 * 512 // 2   # and the codes of x
     for kw in (dict(act=1), dict(H=250), dict(k=9), dict(E=600), dict(T=70000)):
         assert size(**kw) == 0, kw
 
@@ -196,10 +219,12 @@ def test_python_front_refuses_before_the_library():
     with pytest.raises(ValueError):
         mx.MxBank(w13=(codes, codes))
     pair = (torch.zeros(2, 64, 16, dtype=torch.uint8), torch.zeros(2, 64, 1, dtype=torch.uint8))
-    bank = mx.MxBank(w13=pair)
-    assert bank.need("w13", 2, 64, 32) is not None and bank.need("w13_shared", 0, 64, 32) is None
-    with pytest.raises(ValueError):
-        bank.need("w13", 3, 64, 32)
+    with pytest.raises(ValueError, match="GPU"):
+        mx.MxBank(w13=pair)
+    with pytest.raises(ValueError, match="unsupported"):
+        mx.MxBank(w13=(pair[0][:, :40].contiguous(), pair[1][:, :40].contiguous()))
+    bank = mx.MxBank()
+    assert bank.need("w13_shared", 0, 64, 32) is None
     with pytest.raises(ValueError):
         bank.need("w2", 2, 64, 32)
     with pytest.raises(ValueError):
@@ -212,5 +237,7 @@ def test_python_front_refuses_before_the_library():
     for bad in (x.float(), x[:3], x.t().contiguous().t()):
         with pytest.raises((TypeError, ValueError)):
             mx.gateup_silu(bank, bad, offs, sp, b)
+    with pytest.raises(ValueError):      # no such matrices in the bank
+        mx.gateup_silu(bank, x, offs, sp, b)
     with pytest.raises(TypeError):
         mx.gateup_silu(bank, x, offs.long(), sp, b)
