@@ -48,6 +48,10 @@ bool pad_h(int I, int n_shared, int I_shared) {
 // Tiles of up to 160 rows from this many pairs per expert on, of 16 rows below.
 constexpr long long kGemmRows = 12;
 
+// A4 on tiles of 16 rows: from this many pairs on the rows are quantised once,
+// by a launch of their own; fewer by every workgroup that reads them.
+constexpr int kCodesPairs = 64;
+
 MxWsLayout layout(int act, int T, int H, int I, int E, int k, int n_shared, int I_shared) {
   MxWsLayout L;
   const size_t R = (size_t)T * (k + n_shared);
@@ -78,52 +82,59 @@ moe_status check_ws(const void* ws, size_t bytes, const MxWsLayout& L) {
   return ws && aligned(ws, 256) && bytes >= L.total ? MOE_OK : MOE_E_WORKSPACE;
 }
 
-// The projections' launches, every argument checked.
-moe_status gateup(int act, const uint16_t* x, int T, int H, int I, int E, int k,
-                  const moe_mxbank* w13, const moe_mxbank* w13_shared, int n_shared, int I_shared,
-                  const int32_t* offsets, const int32_t* sorted_pair, uint16_t* h, char* ws,
-                  hipStream_t s) {
-  const MxWsLayout L = layout(act, T, H, I, E, k, n_shared, I_shared);
+// Arguments shared by the projections; x, w, U and out differ.
+MxProj proj(int T, int E, int k, int n_shared, const moe_mxbank* w, const moe_mxbank* w_sh) {
   MxProj a;
   std::memset(&a, 0, sizeof(a));
-  a.x = x;
-  a.ld_in = H;
-  if (act == MOE_A4) {
-    uint8_t* q = reinterpret_cast<uint8_t*>(ws + L.qx);
-    uint8_t* sc = reinterpret_cast<uint8_t*>(ws + L.sx);
-    if (launch_mx_quant(x, 0, T, H, H, q, sc, mx_pad_k(H), true, s) != hipSuccess) return MOE_E_DEVICE;
-    a.q = q;
-    a.s = sc;
-  }
-  a.w = w13->codes;
-  a.ws = w13->scales;
+  a.w = w->codes;
+  a.ws = w->scales;
   if (n_shared > 0) {
-    a.w_sh = w13_shared->codes;
-    a.ws_sh = w13_shared->scales;
+    a.w_sh = w_sh->codes;
+    a.ws_sh = w_sh->scales;
   }
-  a.K = a.K_sh = H;
-  a.U = I;
-  a.U_sh = n_shared > 0 ? I_shared : 0;
   a.T = T;
   a.k = k;
   a.P = T * k;
   a.E = E;
   a.n_shared = n_shared;
-  a.offsets = offsets;
-  a.sorted_pair = sorted_pair;
+  return a;
+}
+
+MxProj gateup_proj(const uint16_t* x, int T, int H, int I, int E, int k, const moe_mxbank* w13,
+                   const moe_mxbank* w13_shared, int n_shared, int I_shared, uint16_t* h) {
+  MxProj a = proj(T, E, k, n_shared, w13, w13_shared);
+  a.x = x;
+  a.ld_in = H;
+  a.K = a.K_sh = H;
+  a.U = I;
+  a.U_sh = n_shared > 0 ? I_shared : 0;
   a.out = h;
   a.ld_out = ld_h_of(I, n_shared, I_shared);
-  if ((long long)T * k >= kGemmRows * E &&
-      mx_gemm_ok(act == MOE_A4, T, H, H, H, 2 * I, n_shared > 0 ? 2 * I_shared : 0)) {
-    if (act == MOE_A16 && pad_x(H)) {
-      uint16_t* xp = reinterpret_cast<uint16_t*>(ws + L.qx);
-      if (launch_mx_pad_rows(x, T, H, H, xp, mx_pad_k(H), s) != hipSuccess) return MOE_E_DEVICE;
-      a.x = xp;
-      a.ld_in = mx_pad_k(H);
-    }
-    return from_hip(launch_mx_gemm(a, 0, act == MOE_A4, s));
+  return a;
+}
+
+// The projections' launches, every argument checked.
+moe_status gateup(int act, MxProj a, const MxWsLayout& L, const int32_t* offsets,
+                  const int32_t* sorted_pair, char* ws, hipStream_t s) {
+  const int act4 = act == MOE_A4, H = a.K;
+  a.offsets = offsets;
+  a.sorted_pair = sorted_pair;
+  const bool gemm = a.P >= kGemmRows * a.E && mx_gemm_ok(act4, a.T, H, H, H, 2 * a.U, 2 * a.U_sh);
+  hipError_t e = hipSuccess;
+  if (act4 && (gemm || a.P >= kCodesPairs)) {
+    uint8_t* q = reinterpret_cast<uint8_t*>(ws + L.qx);
+    uint8_t* sc = reinterpret_cast<uint8_t*>(ws + L.sx);
+    e = launch_mx_quant(a.x, 0, a.T, H, H, q, sc, mx_pad_k(H), true, s);
+    a.q = q;
+    a.s = sc;
+  } else if (gemm && pad_x(H)) {
+    uint16_t* xp = reinterpret_cast<uint16_t*>(ws + L.qx);
+    e = launch_mx_pad_rows(a.x, a.T, H, H, xp, mx_pad_k(H), s);
+    a.x = xp;
+    a.ld_in = mx_pad_k(H);
   }
-  return from_hip(launch_mx_rows16(a, 0, act == MOE_A4, s));
+  if (e != hipSuccess) return MOE_E_DEVICE;
+  return from_hip(gemm ? launch_mx_gemm(a, 0, act4, s) : launch_mx_rows16(a, 0, act4, s));
 }
 
 moe_status down(int act, const uint16_t* h, int T, int H, int I, int E, int k,
@@ -131,60 +142,46 @@ moe_status down(int act, const uint16_t* h, int T, int H, int I, int E, int k,
                 const float* shared_gate, const float* topk_w, const int32_t* offsets,
                 const int32_t* pair_pos, void* out, int out_f32, char* ws, hipStream_t s) {
   const MxWsLayout L = layout(act, T, H, I, E, k, n_shared, I_shared);
-  const int ld_h = ld_h_of(I, n_shared, I_shared), P = T * k;
-  const int hp = mx_pad_k(ld_h);
-  float* y = reinterpret_cast<float*>(ws + L.y);
-  MxProj a;
-  std::memset(&a, 0, sizeof(a));
+  const int act4 = act == MOE_A4, ld_h = ld_h_of(I, n_shared, I_shared), hp = mx_pad_k(ld_h);
+  const int P = T * k, R_sh = n_shared * T;
+  if (n_shared == 0) shared_gate = nullptr;
+  MxProj a = proj(T, E, k, n_shared, w2, w2_shared);
   a.x = h;
   a.ld_in = ld_h;
-  if (act == MOE_A4) {
-    uint8_t* q = reinterpret_cast<uint8_t*>(ws + L.qh);
-    uint8_t* sc = reinterpret_cast<uint8_t*>(ws + L.sh);
-    hipError_t e = launch_mx_quant(h, 0, P, I, ld_h, q, sc, hp, true, s);
-    if (e == hipSuccess && n_shared > 0)
-      e = launch_mx_quant(h + (size_t)P * ld_h, 0, n_shared * T, I_shared, ld_h,
-                          q + (size_t)P * (hp / 2), sc + (size_t)P * (hp / kMxBlock), hp,
-                          true, s);
-    if (e != hipSuccess) return MOE_E_DEVICE;
-    a.q = q;
-    a.s = sc;
-  }
-  a.w = w2->codes;
-  a.ws = w2->scales;
-  if (n_shared > 0) {
-    a.w_sh = w2_shared->codes;
-    a.ws_sh = w2_shared->scales;
-  }
   a.K = I;
   a.K_sh = n_shared > 0 ? I_shared : I;
   a.U = a.U_sh = H;
-  a.T = T;
-  a.k = k;
-  a.P = P;
-  a.E = E;
-  a.n_shared = n_shared;
   a.offsets = offsets;
+  if (mx_down_combine_ok(a))
+    return from_hip(launch_mx_down_combine(a, act4, topk_w, pair_pos, shared_gate, out, out_f32, s));
+  float* y = reinterpret_cast<float*>(ws + L.y);
   a.out = y;
   a.ld_out = H;
-  if ((long long)T * k >= kGemmRows * E &&
-      mx_gemm_ok(act == MOE_A4, (long long)T * (k + n_shared), ld_h, a.K, a.K_sh, H, n_shared > 0 ? H : 0)) {
-    if (act == MOE_A16 && pad_h(I, n_shared, I_shared)) {
-      uint16_t* pd = reinterpret_cast<uint16_t*>(ws + L.qh);
-      hipError_t e = launch_mx_pad_rows(h, P, I, ld_h, pd, hp, s);
-      if (e == hipSuccess && n_shared > 0)
-        e = launch_mx_pad_rows(h + (size_t)P * ld_h, n_shared * T, I_shared, ld_h,
-                               pd + (size_t)P * hp, hp, s);
-      if (e != hipSuccess) return MOE_E_DEVICE;
-      a.x = pd;
-      a.ld_in = hp;
-    }
-    if (launch_mx_gemm(a, 1, act == MOE_A4, s) != hipSuccess) return MOE_E_DEVICE;
-  } else if (launch_mx_rows16(a, 1, act == MOE_A4, s) != hipSuccess) {
-    return MOE_E_DEVICE;
+  hipError_t e = hipSuccess;
+  const bool gemm = P >= kGemmRows * E &&
+                    mx_gemm_ok(act4, (long long)P + R_sh, ld_h, a.K, a.K_sh, H, H);
+  const uint16_t* h_sh = h + (size_t)P * ld_h;
+  if (act4 && (gemm || P >= kCodesPairs)) {
+    uint8_t* q = reinterpret_cast<uint8_t*>(ws + L.qh);
+    uint8_t* sc = reinterpret_cast<uint8_t*>(ws + L.sh);
+    e = launch_mx_quant(h, 0, P, I, ld_h, q, sc, hp, true, s);
+    if (e == hipSuccess && n_shared > 0)
+      e = launch_mx_quant(h_sh, 0, R_sh, I_shared, ld_h, q + (size_t)P * (hp / 2),
+                          sc + (size_t)P * (hp / kMxBlock), hp, true, s);
+    a.q = q;
+    a.s = sc;
+  } else if (gemm && pad_h(I, n_shared, I_shared)) {
+    uint16_t* pd = reinterpret_cast<uint16_t*>(ws + L.qh);
+    e = launch_mx_pad_rows(h, P, I, ld_h, pd, hp, s);
+    if (e == hipSuccess && n_shared > 0)
+      e = launch_mx_pad_rows(h_sh, R_sh, I_shared, ld_h, pd + (size_t)P * hp, hp, s);
+    a.x = pd;
+    a.ld_in = hp;
   }
-  return from_hip(launch_combine(y, H, topk_w, pair_pos, T, k, H, P, n_shared,
-                                 n_shared > 0 ? shared_gate : nullptr, out, out_f32, s));
+  if (e == hipSuccess) e = gemm ? launch_mx_gemm(a, 1, act4, s) : launch_mx_rows16(a, 1, act4, s);
+  if (e != hipSuccess) return MOE_E_DEVICE;
+  return from_hip(launch_combine(y, H, topk_w, pair_pos, T, k, H, P, n_shared, shared_gate, out,
+                                 out_f32, s));
 }
 
 }  // namespace
@@ -261,12 +258,14 @@ moe_status moe_mx4_gateup_silu(int act, const uint16_t* x, int T, int H, int I, 
   if (!x || !offsets || !sorted_pair || !h || !aligned(x, 16) || !aligned(h, 16))
     return MOE_E_INVAL;
   if (!bank_ok(w13) || (n_shared > 0 && !bank_ok(w13_shared))) return MOE_E_INVAL;
-  st = check_ws(workspace, ws_bytes, layout(act, T, H, I, E, k, n_shared, I_shared));
+  const MxWsLayout L = layout(act, T, H, I, E, k, n_shared, I_shared);
+  st = check_ws(workspace, ws_bytes, L);
   if (st != MOE_OK) return st;
   st = device_usable();
   if (st != MOE_OK) return st;
-  return gateup(act, x, T, H, I, E, k, w13, w13_shared, n_shared, I_shared, offsets, sorted_pair,
-                h, static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
+  return gateup(act, gateup_proj(x, T, H, I, E, k, w13, w13_shared, n_shared, I_shared, h), L,
+                offsets, sorted_pair, static_cast<char*>(workspace),
+                static_cast<hipStream_t>(stream));
 }
 
 moe_status moe_mx4_down_combine(int act, const uint16_t* h, int T, int H, int I, int E, int k,
@@ -315,25 +314,31 @@ moe_status moe_mx4_layer(int act, const float* logits, const uint16_t* x, int T,
   if (st != MOE_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
-  int32_t* n_tiles = reinterpret_cast<int32_t*>(ws + L.tiles);
-  int32_t* tiles = reinterpret_cast<int32_t*>(ws + L.tiles + 256);
-  const int P = T * k;
-  hipError_t e;
-  if (T <= kFusedRouteMaxT && P <= kFusedRouteMaxP) {
-    e = launch_route_permute(logits, T, E, k, renormalize, kSortTile, topk_ids, topk_w, counts,
-                             offsets, sorted_pair, pair_pos, tiles, n_tiles, s);
+  const MxProj a = gateup_proj(x, T, H, I, E, k, w13, w13_shared, n_shared, I_shared, h);
+  if (mx_route_gateup_ok(T, k, E) && a.P < kGemmRows * E) {
+    // a few tokens: routing, sort and gate/up in one launch
+    st = from_hip(launch_mx_route_gateup(a, act == MOE_A4, logits, renormalize, topk_ids, topk_w,
+                                         counts, offsets, sorted_pair, pair_pos, s));
   } else {
-    e = launch_route_topk(logits, T, E, k, renormalize, topk_ids, topk_w, s);
-    if (e == hipSuccess && permute_multi_blocks(P) > 0)
-      e = launch_permute_multi(topk_ids, P, E, kSortTile, counts, offsets, sorted_pair, pair_pos,
-                               tiles, n_tiles, reinterpret_cast<int32_t*>(ws + L.perm), s);
-    else if (e == hipSuccess)
-      e = launch_permute(topk_ids, P, E, kSortTile, counts, offsets, sorted_pair, pair_pos, tiles,
-                         n_tiles, s);
+    int32_t* n_tiles = reinterpret_cast<int32_t*>(ws + L.tiles);
+    int32_t* tiles = reinterpret_cast<int32_t*>(ws + L.tiles + 256);
+    hipError_t e;
+    if (T <= kFusedRouteMaxT && a.P <= kFusedRouteMaxP) {
+      e = launch_route_permute(logits, T, E, k, renormalize, kSortTile, topk_ids, topk_w, counts,
+                               offsets, sorted_pair, pair_pos, tiles, n_tiles, s);
+    } else {
+      e = launch_route_topk(logits, T, E, k, renormalize, topk_ids, topk_w, s);
+      if (e == hipSuccess && permute_multi_blocks(a.P) > 0)
+        e = launch_permute_multi(topk_ids, a.P, E, kSortTile, counts, offsets, sorted_pair,
+                                 pair_pos, tiles, n_tiles,
+                                 reinterpret_cast<int32_t*>(ws + L.perm), s);
+      else if (e == hipSuccess)
+        e = launch_permute(topk_ids, a.P, E, kSortTile, counts, offsets, sorted_pair, pair_pos,
+                           tiles, n_tiles, s);
+    }
+    if (e != hipSuccess) return MOE_E_DEVICE;
+    st = gateup(act, a, L, offsets, sorted_pair, ws, s);
   }
-  if (e != hipSuccess) return MOE_E_DEVICE;
-  st = gateup(act, x, T, H, I, E, k, w13, w13_shared, n_shared, I_shared, offsets, sorted_pair, h,
-              ws, s);
   if (st != MOE_OK) return st;
   return down(act, h, T, H, I, E, k, w2, w2_shared, n_shared, I_shared, shared_gate, topk_w,
               offsets, pair_pos, out, (flags & MOE_OUT_F32) ? 1 : 0, ws, s);

@@ -109,48 +109,54 @@ __device__ __forceinline__ mx_f32x4 mx_mfma_fp4(mx_u32x4 a, uint32_t sa, mx_u32x
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, J, (int)sa, J, (int)sb);
 }
 
-// Tile j (of tiles of TM rows, experts in order, empty experts skipped) of the
-// sorted rows, found by one wave from the offsets alone: lanes count the tiles
-// of 8 experts each (E <= 512), a prefix sum finds the owner.  False past the
-// last tile.  Rows are held inside [0, P] whatever the table says.
-template <int TM>
-__device__ __forceinline__ bool mx_find_tile(const int32_t* __restrict__ offsets, int E, int P,
-                                             int j, int& e, int& r0, int& r1) {
-  const int lane = threadIdx.x & 63;
-  const int per = (E + 63) / 64;   // experts per lane
-  int cnt = 0;
-  for (int i = 0; i < per; ++i) {
-    const int ex = lane * per + i;
-    if (ex < E) {
-      const int n = min(offsets[ex + 1], P) - max(offsets[ex], 0);
-      cnt += n > 0 ? (n + TM - 1) / TM : 0;
-    }
-  }
-  int pre = cnt;   // inclusive prefix over the lanes
+// The sorted rows cut into tiles of at most TM rows, experts in order, empty
+// experts skipped, by one wave from the offsets alone: lane l owns the experts
+// [PER * l, PER * l + PER) (E <= 64 * PER), all its offsets loaded at once, and
+// a prefix sum over the lanes numbers the tiles.  Rows are held inside [0, P]
+// whatever the table says.
+template <int TM, int PER>
+struct MxTiles {
+  int lo[PER], hi[PER], cnt, pre;   // row ranges; tiles of this lane, and up to it
+
+  __device__ __forceinline__ void load(const int32_t* __restrict__ offsets, int E, int P) {
+    const int lane = threadIdx.x & 63;
+    int o[PER + 1];
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int o = __shfl_up(pre, d);
-    if (lane >= d) pre += o;
-  }
-  const uint64_t past = __ballot(pre > j);
-  if (past == 0) return false;
-  const int owner = __builtin_ctzll(past);
-  int left = j - (__builtin_amdgcn_readlane(pre, owner) - __builtin_amdgcn_readlane(cnt, owner));
-  for (int i = 0; i < per; ++i) {
-    const int ex = owner * per + i;
-    if (ex >= E) return false;
-    const int lo = max(offsets[ex], 0), hi = min(offsets[ex + 1], P);
-    const int nt = hi > lo ? (hi - lo + TM - 1) / TM : 0;
-    if (left < nt) {
-      e = ex;
-      r0 = lo + left * TM;
-      r1 = min(hi, r0 + TM);
-      return true;
+    for (int i = 0; i <= PER; ++i) o[i] = offsets[min(lane * PER + i, E)];
+    cnt = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      lo[i] = max(o[i], 0);
+      hi[i] = max(min(o[i + 1], P), lo[i]);   // past the last expert: empty
+      cnt += (hi[i] - lo[i] + TM - 1) / TM;
     }
-    left -= nt;
+    pre = cnt;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int v = __shfl_up(pre, d);
+      if (lane >= d) pre += v;
+    }
   }
-  return false;
-}
+  // Tile j: its expert and rows; false past the last.
+  __device__ __forceinline__ bool find(int j, int& e, int& r0, int& r1) const {
+    const uint64_t past = __ballot(pre > j);
+    if (past == 0) return false;
+    const int owner = __builtin_ctzll(past);
+    int left = j - (__builtin_amdgcn_readlane(pre, owner) - __builtin_amdgcn_readlane(cnt, owner));
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int l = __builtin_amdgcn_readlane(lo[i], owner), h = __builtin_amdgcn_readlane(hi[i], owner);
+      const int nt = (h - l + TM - 1) / TM;
+      if (left >= 0 && left < nt) {
+        e = owner * PER + i;
+        r0 = l + left * TM;
+        r1 = min(h, r0 + TM);
+      }
+      left -= nt;
+    }
+    return true;
+  }
+};
 
 // R rows of C values (row stride ld) to rows of CP >= C values, zeros behind
 // the C: codes [R][CP/2] and scale bytes [R][CP/32]; words: the scale bytes in
@@ -169,6 +175,17 @@ hipError_t launch_mx_pad_rows(const uint16_t* src, int R, int C, int ld, uint16_
 // Grouped projections; mode 0: gate/up with SiLU*mul to h, 1: down to y.
 // Tiles of 16 rows, K split over the workgroup's waves:
 hipError_t launch_mx_rows16(const MxProj& a, int mode, int act4, hipStream_t st);
+// The same for a few tokens with their routing and sort in the launch:
+bool mx_route_gateup_ok(int T, int k, int E);
+hipError_t launch_mx_route_gateup(const MxProj& a, int act4, const float* logits, int renorm,
+                                  int32_t* ids, float* w, int32_t* counts, int32_t* offsets,
+                                  int32_t* sorted_pair, int32_t* pair_pos, hipStream_t st);
+// Down with the weighted sum in the launch, for at most kDnSlots tiles:
+constexpr int kDnSlots = 40;
+bool mx_down_combine_ok(const MxProj& a);
+hipError_t launch_mx_down_combine(const MxProj& a, int act4, const float* topk_w,
+                                  const int32_t* pair_pos, const float* sh_gate, void* out,
+                                  int out_f32, hipStream_t st);
 // Tiles of up to 160 rows (A16: rows of whole steps, K % 256 == 0 or a padded copy):
 bool mx_gemm_ok(int act4, long long rows, int ld, int K, int K_sh, int N, int N_sh);
 hipError_t launch_mx_gemm(const MxProj& a, int mode, int act4, hipStream_t st);

@@ -4,24 +4,32 @@
 //   down:    y[r][n] = h_r . W[n]
 //
 // Few rows per expert: bound by streaming the packed weights (0.53 bytes per
-// weight, read once), so a workgroup is small and loads everything it needs
-// at once.  It owns 16 units (a gate and an up row each, or 2 x 16 down rows)
-// of one tile; its four waves split K and meet in LDS.  Both operands go from
-// memory straight into the matrix instruction's registers, the weights as
+// weight, read once) and, for a handful of tokens, by the latency of that one
+// pass, so everything a workgroup needs is loaded at once.  Both operands go
+// from memory straight into the matrix instruction's registers, the weights as
 // tiled pieces (a contiguous kilobyte per load), the activations as the same
-// blocks of their rows.  A16 expands a block to bf16 by the conversion
-// instruction that takes the scale (exact) and runs four 16x16x32 bf16 steps;
-// A4 feeds codes and scale bytes to the scaled 16x16x128 instruction as they
-// are.
+// blocks of their rows.  A16 expands a block of weights to bf16 by the
+// conversion instruction that takes the scale (exact) and runs four 16x16x32
+// bf16 steps; A4 quantises the block of activations, which one lane holds
+// whole, in registers and feeds codes and scale bytes of both sides to the
+// scaled 16x16x128 instruction.
+//
+//  * mx_rows16_kernel: a workgroup owns 16 units (a gate and an up row each, or
+//    2 x 16 down rows) of one tile; its waves split K and meet in LDS.  With
+//    NV > 0 (a few tokens) every workgroup routes and sorts the batch itself:
+//    that costs less than the launch and the round trip of a routing kernel.
+//  * mx_down_combine_kernel (a few tokens): a workgroup owns 16 output columns
+//    of every token; its waves share the (tile, part of K) products, which meet
+//    in LDS, where the weighted sum of each token is formed: no fp32 rows
+//    through memory and no combine launch.
 #include "mx_common.h"
+#include "route_common.h"
 
 namespace moe {
 
 namespace {
 
 constexpr int kTM = 16;        // rows per tile
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
 constexpr int kPitch = 20;     // LDS words per 16 (4 rows of 20 words: 16 banks apart)
 
 // The scale bytes of NB pieces from piece s on (s % NB == 0): bytes of the
@@ -34,36 +42,211 @@ __device__ __forceinline__ uint32_t load_scales(const uint8_t* __restrict__ word
   return *p;
 }
 
-template <int NB, int J = 0>
-__device__ __forceinline__ void fp4_steps(const mx_u32x4 (&w0)[NB], uint32_t s0,
-                                          const mx_u32x4 (&w1)[NB], uint32_t s1,
-                                          const mx_u32x4 (&x)[NB], uint32_t sx, mx_f32x4& a0,
-                                          mx_f32x4& a1) {
-  if constexpr (J < NB) {
-    a0 = mx_mfma_fp4<J>(w0[J], s0, x[J], sx, a0);
-    a1 = mx_mfma_fp4<J>(w1[J], s1, x[J], sx, a1);
-    fp4_steps<NB, J + 1>(w0, s0, w1, s1, x, sx, a0, a1);
+// 32 bf16 values of one block to codes and scale byte (the rule of
+// mx_quant_kernel, the same instructions).
+__device__ __forceinline__ mx_u32x4 quantise_block(const mx_u32x4 (&x)[4], uint32_t& sb) {
+  uint32_t m = 0;   // two magnitudes per word, compared as 16-bit integers
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t v = x[t][i];
+      m = max(m, max(v & 0x7FFFu, (v >> 16) & 0x7FFFu));
+    }
+  sb = mx_scale_byte(m << 16);
+  const float sc = mx_scale_f32(sb);
+  mx_u32x4 q;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    uint32_t w = 0;
+    const uint32_t v0 = x[t].x, v1 = x[t].y, v2 = x[t].z, v3 = x[t].w;
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(mx_bf16x2, v0), sc, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(mx_bf16x2, v1), sc, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(mx_bf16x2, v2), sc, 2);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(mx_bf16x2, v3), sc, 3);
+    q[t] = w;
+  }
+  return q;
+}
+
+// The lane's block of one piece: 16 rows of weights (codes w, scale byte in
+// byte J of sw) times its activation block x, into acc.
+template <bool ACT4, int J>
+__device__ __forceinline__ mx_f32x4 piece_product(mx_u32x4 w, uint32_t sw, const mx_u32x4 (&x)[4],
+                                                  mx_u32x4 xq, uint32_t sx, mx_f32x4 acc) {
+  if constexpr (ACT4) {
+    const mx_i32x8 av = {(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
+    const mx_i32x8 bv = {(int)xq.x, (int)xq.y, (int)xq.z, (int)xq.w, 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, acc, 4, 4, J, (int)sw, 0,
+                                                            (int)sx);
+  } else {
+    const float f = mx_scale_f32((sw >> (8 * J)) & 255u);
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(mx_word_to_bf16(w[t], f),
+                                                    __builtin_bit_cast(mx_bf16x8, x[t]), acc, 0, 0, 0);
+    return acc;
   }
 }
 
-template <int MODE, bool ACT4, int NB>
-__global__ __launch_bounds__(kThreads) void mx_rows16_kernel(MxProj a, int n_sh_tiles, int n_ub) {
-  __shared__ float red[kWaves][2][kTM * kPitch];
+// NB pieces of F row blocks against the same activation blocks.
+template <bool ACT4, int NB, int F, int J = 0>
+__device__ __forceinline__ void products(const mx_u32x4 (&w)[F][NB], const uint32_t (&sw)[F],
+                                         const mx_u32x4 (&x)[NB][4], mx_f32x4 (&acc)[F]) {
+  if constexpr (J < NB) {
+    mx_u32x4 xq = {0, 0, 0, 0};
+    uint32_t sx = 0;
+    if (ACT4) xq = quantise_block(x[J], sx);
+#pragma unroll
+    for (int f = 0; f < F; ++f)
+      acc[f] = piece_product<ACT4, J>(w[f][J], sw[f], x[J], xq, sx, acc[f]);
+    products<ACT4, NB, F, J + 1>(w, sw, x, acc);
+  }
+}
+
+// The same with the activations' codes x and scale word sx from memory.
+template <int NB, int J = 0>
+__device__ __forceinline__ void code_products(const mx_u32x4 (&w)[2][NB], const uint32_t (&sw)[2],
+                                              const mx_u32x4 (&x)[NB], uint32_t sx,
+                                              mx_f32x4 (&acc)[2]) {
+  if constexpr (J < NB) {
+#pragma unroll
+    for (int f = 0; f < 2; ++f) acc[f] = mx_mfma_fp4<J>(w[f][J], sw[f], x[J], sx, acc[f]);
+    code_products<NB, J + 1>(w, sw, x, sx, acc);
+  }
+}
+
+// Routing outputs of the fused launch (written by workgroup 0 alone).
+struct MxRoute {
+  const float* logits;
+  int renorm;
+  int32_t* ids;
+  float* w;
+  int32_t* counts;
+  int32_t* offsets;
+  int32_t* sorted_pair;
+  int32_t* pair_pos;
+};
+
+constexpr int kRouteT = 16;    // tokens of the fused routing
+constexpr int kRouteP = 64;    // and pairs: one per lane
+
+// One pair per lane (expert id, P pairs): where it stands in the stable sort by
+// expert, from ballots over the id's bits (masks of the pairs that sort before
+// it and of those of its own expert).
+struct PairSort {
+  int id, lt, before, same;   // pairs of smaller experts; of the same one before it; in all
+  uint64_t eq;
+
+  __device__ __forceinline__ void sort(int id_, int P, int E) {
+    const int lane = threadIdx.x & 63;
+    id = id_;
+    const bool in = lane < P;
+    eq = __ballot(in);
+    uint64_t less = 0;
+    for (int b = 31 - __builtin_clz(E | 1); b >= 0; --b) {
+      const bool bit = (id >> b) & 1;
+      const uint64_t ones = __ballot(in && bit);
+      if (bit) less |= eq & ~ones;
+      eq &= bit ? ones : ~ones;
+    }
+    lt = __popcll(less);
+    before = __popcll(eq & (lane == 0 ? 0ull : ~0ull >> (64 - lane)));
+    same = __popcll(eq);
+  }
+  // Tile j of kTM rows, as MxTiles::find; the lane of row r of it has
+  // id == e and before == r - lt.
+  __device__ __forceinline__ bool find(int j, int P, int& e, int& r0, int& r1) const {
+    const int lane = threadIdx.x & 63;
+    const bool start = lane < P && before % kTM == 0;
+    // tile starts before mine: experts smaller than mine, earlier tiles of mine
+    const uint64_t starts = __ballot(start);
+    int idx = 0;
+    for (uint64_t m = starts; m; m &= m - 1) {
+      const int l = __builtin_ctzll(m);
+      const int k = __builtin_amdgcn_readlane(lt + before, l);
+      idx += k < lt + before;
+    }
+    const uint64_t mine = __ballot(start && idx == j);
+    if (mine == 0) return false;
+    const int o = __builtin_ctzll(mine);
+    e = __builtin_amdgcn_readlane(id, o);
+    r0 = __builtin_amdgcn_readlane(lt + before, o);
+    r1 = min(r0 + kTM, __builtin_amdgcn_readlane(lt + same, o));
+    return true;
+  }
+};
+
+// XQ (A4): the activations' codes and scales come from memory; else they are
+// quantised here.  NV: logits per lane of the routing (0: no routing here, the
+// tables come from memory).  WV waves per workgroup.
+template <int MODE, bool ACT4, bool XQ, int NB, int NV, int WV>
+__global__ __launch_bounds__(64 * WV) void mx_rows16_kernel(MxProj a, MxRoute ro, int n_sh_tiles,
+                                                            int n_ub) {
+  constexpr bool ROUTE = NV > 0;
+  __shared__ float red[WV][2][kTM * kPitch];
+  __shared__ int tok_l[WV][kTM];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int slot = blockIdx.x / n_ub, ub = blockIdx.x - slot * n_ub;
+  const int blk = ROUTE ? (int)blockIdx.x - 1 : (int)blockIdx.x;
   const int c = lane & 15, g = lane >> 4;
 
   // ---- the tile: shared experts' first
   bool is_sh = false;
-  int e, r0, r1;
-  const int per = (a.T + kTM - 1) / kTM;
-  if (slot < n_sh_tiles) {
+  int e = 0, r0 = 0, r1 = 0;
+  int pair = -1;   // routed launch: the sorted pair of this lane's column
+  const int slot = blk / n_ub, ub = blk - slot * n_ub;
+  if (blk >= 0 && slot < n_sh_tiles) {
+    const int per = (a.T + kTM - 1) / kTM;
     is_sh = true;
     e = slot / per;
     r0 = (slot - e * per) * kTM;
     r1 = min(a.T, r0 + kTM);
-  } else if (!mx_find_tile<kTM>(a.offsets, a.E, a.P, slot - n_sh_tiles, e, r0, r1)) {
-    return;
+  } else if constexpr (ROUTE) {
+    // workgroup 0 writes the tables of moe_route_topk and moe_permute
+    __shared__ int ids_l[kRouteP];
+    const bool writer = blk < 0;
+    route_tokens<NV, (kRouteT + 4 * WV - 1) / (4 * WV)>(ro.logits, a.T, a.E, a.k, ro.renorm, lane,
+                                                        wave, WV, writer ? ro.ids : nullptr,
+                                                        writer ? ro.w : nullptr, ids_l, nullptr);
+    __syncthreads();
+    PairSort ps;
+    ps.sort(lane < a.P ? ids_l[lane] : 0, a.P, a.E);
+    if (writer) {
+      if (tid < a.P) {
+        ro.sorted_pair[ps.lt + ps.before] = lane;
+        ro.pair_pos[lane] = ps.lt + ps.before;
+      }
+      for (int x = tid; x < a.E; x += 64 * WV) {
+        int n = 0, o = 0;
+        for (int q = 0; q < a.P; ++q) {
+          n += ids_l[q] == x;
+          o += ids_l[q] < x;
+        }
+        ro.counts[x] = n;
+        ro.offsets[x] = o;
+      }
+      if (tid == 0) ro.offsets[a.E] = a.P;
+      return;
+    }
+    if (!ps.find(slot - n_sh_tiles, a.P, e, r0, r1)) return;
+    const int row = ps.lt + ps.before;
+    if (lane < a.P && ps.id == e && row >= r0 && row < r1) tok_l[wave][row - r0] = lane;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");   // the wave's own words
+    if (r0 + c < r1) pair = tok_l[wave][c];
+  } else {
+    // E <= 512: 1, 2, 4 or 8 experts per lane
+    const int j = slot - n_sh_tiles;
+    bool ok;
+    if (a.E <= 128) {
+      MxTiles<kTM, 2> t;
+      t.load(a.offsets, a.E, a.P);
+      ok = t.find(j, e, r0, r1);
+    } else {
+      MxTiles<kTM, 8> t;
+      t.load(a.offsets, a.E, a.P);
+      ok = t.find(j, e, r0, r1);
+    }
+    if (!ok) return;
   }
   const int U = is_sh ? a.U_sh : a.U, K = is_sh ? a.K_sh : a.K;
   const int u0 = ub * (MODE == 0 ? 16 : 32);   // first unit (gate/up) or row (down)
@@ -89,25 +272,26 @@ __global__ __launch_bounds__(kThreads) void mx_rows16_kernel(MxProj a, int n_sh_
     } else if (is_sh) {
       xrow = r0 + c;
     } else {
-      const int p = a.sorted_pair[r0 + c];
+      const int p = ROUTE ? pair : a.sorted_pair[r0 + c];
       have = (unsigned)p < (unsigned)a.P;
       xrow = have ? p / a.k : 0;
     }
   }
 
-  mx_f32x4 a0 = {0, 0, 0, 0}, a1 = {0, 0, 0, 0};
+  mx_f32x4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
   const mx_u32x4 zero = {0, 0, 0, 0};
-  for (int s = wave * NB; s < pieces; s += kWaves * NB) {
-    mx_u32x4 w0[NB], w1[NB];
+  for (int s = wave * NB; s < pieces; s += WV * NB) {
+    mx_u32x4 w[2][NB];
+    uint32_t sw[2];
 #pragma unroll
     for (int j = 0; j < NB; ++j)
-      w0[j] = s + j < pieces ? __builtin_nontemporal_load(q0 + (s + j) * 64) : zero;
+      w[0][j] = s + j < pieces ? __builtin_nontemporal_load(q0 + (s + j) * 64) : zero;
 #pragma unroll
     for (int j = 0; j < NB; ++j)
-      w1[j] = s + j < pieces ? __builtin_nontemporal_load(q1 + (s + j) * 64) : zero;
-    const uint32_t s0 = load_scales<NB>(sw0 + (s >> 2) * 256, s);
-    const uint32_t s1 = load_scales<NB>(sw1 + (s >> 2) * 256, s);
-    if (ACT4) {
+      w[1][j] = s + j < pieces ? __builtin_nontemporal_load(q1 + (s + j) * 64) : zero;
+    sw[0] = load_scales<NB>(sw0 + (s >> 2) * 256, s);
+    sw[1] = load_scales<NB>(sw1 + (s >> 2) * 256, s);
+    if constexpr (XQ) {
       // rows of whole words, zeros behind K
       const int KP = mx_pad_k(a.ld_in);
       mx_u32x4 x[NB];
@@ -116,39 +300,32 @@ __global__ __launch_bounds__(kThreads) void mx_rows16_kernel(MxProj a, int n_sh_
       for (int j = 0; j < NB; ++j) x[j] = have && s + j < pieces ? px[4 * j] : zero;
       const uint32_t sx =
           have ? load_scales<NB>(a.s + xrow * (KP / kMxBlock) + (s >> 2) * 16 + 4 * g, s) : 0u;
-      fp4_steps<NB>(w0, s0, w1, s1, x, sx, a0, a1);
+      code_products<NB>(w, sw, x, sx, acc);
     } else {
+      mx_u32x4 x[NB][4];
       const mx_u32x4* px = reinterpret_cast<const mx_u32x4*>(a.x + xrow * a.ld_in);
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
         const int b = 4 * (s + j) + g;
-        mx_u32x4 x[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) x[t] = have && b < nblk ? px[b * 4 + t] : zero;
-        const float f0 = mx_scale_f32((s0 >> (8 * j)) & 255u);
-        const float f1 = mx_scale_f32((s1 >> (8 * j)) & 255u);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const mx_bf16x8 xv = __builtin_bit_cast(mx_bf16x8, x[t]);
-          a0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(mx_word_to_bf16(w0[j][t], f0), xv, a0, 0, 0, 0);
-          a1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(mx_word_to_bf16(w1[j][t], f1), xv, a1, 0, 0, 0);
-        }
+        for (int t = 0; t < 4; ++t) x[j][t] = have && b < nblk ? px[b * 4 + t] : zero;
       }
+      products<ACT4, NB, 2>(w, sw, x, acc);
     }
   }
 
   // ---- the waves' parts of K meet: word [unit][row]
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    red[wave][0][(4 * g + i) * kPitch + c] = a0[i];
-    red[wave][1][(4 * g + i) * kPitch + c] = a1[i];
+    red[wave][0][(4 * g + i) * kPitch + c] = acc[0][i];
+    red[wave][1][(4 * g + i) * kPitch + c] = acc[1][i];
   }
   __syncthreads();
   const int u = tid & 15, m = tid >> 4;   // unit, row
-  if (r0 + m >= r1) return;
+  if (m >= kTM || r0 + m >= r1) return;
   float v0 = 0.0f, v1 = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
+  for (int w = 0; w < WV; ++w) {
     v0 += red[w][0][u * kPitch + m];
     v1 += red[w][1][u * kPitch + m];
   }
@@ -161,30 +338,232 @@ __global__ __launch_bounds__(kThreads) void mx_rows16_kernel(MxProj a, int n_sh_
   }
 }
 
-template <int MODE, bool ACT4>
-hipError_t launch(const MxProj& a, hipStream_t st) {
+int max_slots(const MxProj& a) {
+  return a.n_shared * ((a.T + kTM - 1) / kTM) + moe_permute_max_tiles(a.T, a.k, a.E, kTM);
+}
+
+template <int MODE, bool ACT4, bool XQ, int NV>
+hipError_t launch(const MxProj& a, const MxRoute& ro, hipStream_t st) {
   const int n_sh_tiles = a.n_shared * ((a.T + kTM - 1) / kTM);
   const int step = MODE == 0 ? 16 : 32;
   const int U = a.n_shared > 0 && a.U_sh > a.U ? a.U_sh : a.U;
   const int n_ub = (U + step - 1) / step;
-  const long long grid =
-      (long long)(n_sh_tiles + moe_permute_max_tiles(a.T, a.k, a.E, kTM)) * n_ub;
+  const long long grid = (long long)max_slots(a) * n_ub + (NV > 0 ? 1 : 0);
   if (grid >= (1LL << 31)) return hipErrorInvalidValue;
   const int K = a.n_shared > 0 && a.K_sh > a.K ? a.K_sh : a.K;
   const int pieces = mx_pieces(K);
-  // the longest run per lane that still gives every wave a chunk of K
-  auto kern = pieces >= kWaves * 4   ? mx_rows16_kernel<MODE, ACT4, 4>
-              : pieces >= kWaves * 2 ? mx_rows16_kernel<MODE, ACT4, 2>
-                                     : mx_rows16_kernel<MODE, ACT4, 1>;
-  kern<<<(int)grid, kThreads, 0, st>>>(a, n_sh_tiles, n_ub);
+  // Up to 64 pairs (a few tokens) eight waves split K, so that each has little
+  // to do behind its loads; else four, with longer runs.  The same rule with
+  // and without the routing: both sum in the same order.
+#define MX_GO(NB, WV) \
+  mx_rows16_kernel<MODE, ACT4, XQ, NB, NV, WV><<<(int)grid, 64 * WV, 0, st>>>(a, ro, n_sh_tiles, n_ub)
+  if (NV > 0 || a.P <= kRouteP) {
+    if (pieces >= 16) MX_GO(2, 8);
+    else MX_GO(1, 8);
+  } else if constexpr (NV == 0) {
+    if (pieces >= 16) MX_GO(4, 4);
+    else if (pieces >= 8) MX_GO(2, 4);
+    else MX_GO(1, 4);
+  }
+#undef MX_GO
   return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------
+constexpr int kDnWaves = 8;
+constexpr int kDnThreads = 64 * kDnWaves;
+constexpr int kDnNB = 2;      // pieces per item
+constexpr int kDnItems = 4;   // items of a wave whose loads are in flight together
+
+struct MxCombine {
+  const float* topk_w;
+  const int32_t* pair_pos;
+  const float* sh_gate;   // or null
+  void* out;
+  int out_f32;
+  int max_tiles;   // routed
+  int n_ch;        // parts of K: items per tile
+};
+
+template <bool ACT4>
+__global__ __launch_bounds__(kDnThreads) void mx_down_combine_kernel(MxProj a, MxCombine cb,
+                                                                     int n_sh_tiles) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int R = a.P + a.n_shared * a.T;
+  float* yb = reinterpret_cast<float*>(smem);                             // [n_ch][R][16]
+  int4* til = reinterpret_cast<int4*>(yb + (size_t)cb.n_ch * R * 16);     // [slots]
+  int* n_til = reinterpret_cast<int*>(til + n_sh_tiles + cb.max_tiles);
+  int* ppos = n_til + 4;                                                  // [P]
+  float* gw = reinterpret_cast<float*>(ppos + a.P);                       // [P]
+  float* sg = gw + a.P;                                                   // [T][n_shared]
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int c = lane & 15, g = lane >> 4;
+  const int n0 = blockIdx.x * 16;
+
+  // ---- tile list (expert, first row, end row, shared) and the gate tables
+  for (int i = tid; i < a.P; i += kDnThreads) {
+    ppos[i] = cb.pair_pos[i];
+    gw[i] = cb.topk_w[i];
+  }
+  const int sh_per = (a.T + kTM - 1) / kTM;
+  for (int i = tid; i < n_sh_tiles; i += kDnThreads) {
+    const int e = i / sh_per, r = (i - e * sh_per) * kTM;
+    til[i] = make_int4(e, a.P + e * a.T + r, a.P + e * a.T + min(a.T, r + kTM), 1);
+  }
+  for (int i = tid; i < a.T * a.n_shared; i += kDnThreads)
+    sg[i] = cb.sh_gate ? shared_gate_weight(cb.sh_gate[i]) : 1.0f;
+  if (wave == kDnWaves - 1) {
+    auto list = [&](auto t) {
+      t.load(a.offsets, a.E, a.P);
+      int at = n_sh_tiles + t.pre - t.cnt;
+      constexpr int PER = sizeof(t.lo) / sizeof(int);
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        for (int r = t.lo[i]; r < t.hi[i] && at < n_sh_tiles + cb.max_tiles; r += kTM)
+          til[at++] = make_int4(lane * PER + i, r, min(t.hi[i], r + kTM), 0);
+      if (lane == 63) *n_til = n_sh_tiles + min(t.pre, cb.max_tiles);
+    };
+    if (a.E <= 128) list(MxTiles<kTM, 2>());
+    else list(MxTiles<kTM, 8>());
+  }
+  __syncthreads();
+
+  // ---- items (tile, part of K), kDnItems per wave at a time
+  const int n_items = *n_til * cb.n_ch;
+  const mx_u32x4 zero = {0, 0, 0, 0};
+  for (int base = wave; base < n_items; base += kDnWaves * kDnItems) {
+    mx_u32x4 w[kDnItems][1][kDnNB], x[kDnItems][kDnNB][4];
+    uint32_t sw[kDnItems][1];
+    int4 tl[kDnItems];
+#pragma unroll
+    for (int i = 0; i < kDnItems; ++i) {
+      const int item = base + i * kDnWaves;
+      const bool ok = item < n_items;
+      const int slot = ok ? item / cb.n_ch : 0, s = ok ? (item - slot * cb.n_ch) * kDnNB : 0;
+      tl[i] = ok ? til[slot] : make_int4(0, 0, 0, 0);
+      const int K = tl[i].w ? a.K_sh : a.K;
+      const int nblk = K / kMxBlock, pieces = mx_pieces(K), words = (pieces + 3) / 4;
+      const uint8_t* wq = (tl[i].w ? a.w_sh : a.w) + tl[i].x * mx_code_bytes(a.U, K);
+      const uint8_t* ws = (tl[i].w ? a.ws_sh : a.ws) + tl[i].x * mx_scale_bytes(a.U, K);
+      const size_t rb = n0 / 16;
+      const mx_u32x4* q = reinterpret_cast<const mx_u32x4*>(wq) + rb * pieces * 64 + lane;
+#pragma unroll
+      for (int j = 0; j < kDnNB; ++j)
+        w[i][0][j] = ok && s + j < pieces ? __builtin_nontemporal_load(q + (s + j) * 64) : zero;
+      sw[i][0] = ok && s < pieces
+                     ? load_scales<kDnNB>(ws + ((rb * words + (s >> 2)) * 64 + lane) * 4, s)
+                     : 0u;
+      const bool have = tl[i].y + c < tl[i].z;
+      const mx_u32x4* px =
+          reinterpret_cast<const mx_u32x4*>(a.x + (size_t)(have ? tl[i].y + c : 0) * a.ld_in);
+#pragma unroll
+      for (int j = 0; j < kDnNB; ++j) {
+        const int b = 4 * (s + j) + g;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) x[i][j][t] = have && b < nblk ? px[b * 4 + t] : zero;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kDnItems; ++i) {
+      const int item = base + i * kDnWaves;
+      if (item >= n_items) break;
+      mx_f32x4 acc[1] = {{0, 0, 0, 0}};
+      products<ACT4, kDnNB, 1>(w[i], sw[i], x[i], acc);
+      const int ch = item % cb.n_ch;
+      if (tl[i].y + c < tl[i].z)
+        *reinterpret_cast<mx_f32x4*>(yb + ((size_t)ch * R + tl[i].y + c) * 16 + 4 * g) = acc[0];
+    }
+  }
+  __syncthreads();
+
+  // ---- out[t][n] = sum_j w_j y_j + sum_s g_s y_s, in that order; the parts of
+  // K of a row first
+  const size_t part = (size_t)R * 16;
+  for (int i = tid; i < a.T * 16; i += kDnThreads) {
+    const int t = i >> 4, n = i & 15;
+    auto row = [&](int r) {
+      float y = yb[(size_t)r * 16 + n];
+      for (int ch = 1; ch < cb.n_ch; ++ch) y += yb[ch * part + (size_t)r * 16 + n];
+      return y;
+    };
+    // four pairs at a time: their LDS reads, then the sum in order
+    float o = 0.0f;
+    for (int j0 = 0; j0 < a.k; j0 += 4) {
+      float y[4], w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int q = t * a.k + min(j0 + j, a.k - 1), p = ppos[q];
+        w[j] = gw[q];
+        const bool on = j0 + j < a.k && p >= 0;
+        y[j] = row(on ? p : 0);
+        if (!on) w[j] = y[j] = 0.0f;   // + 0: the sum as if it were skipped
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o = fmaf(w[j], y[j], o);
+    }
+    for (int s = 0; s < a.n_shared; ++s)
+      o = fmaf(sg[t * a.n_shared + s], row(a.P + s * a.T + t), o);
+    if (cb.out_f32) static_cast<float*>(cb.out)[(size_t)t * a.U + n0 + n] = o;
+    else static_cast<uint16_t*>(cb.out)[(size_t)t * a.U + n0 + n] = (uint16_t)mx_bf16(o);
+  }
+}
+
+int dn_parts(const MxProj& a) {
+  const int K = a.n_shared > 0 && a.K_sh > a.K ? a.K_sh : a.K;
+  return (mx_pieces(K) + kDnNB - 1) / kDnNB;
+}
+
+size_t dn_lds(const MxProj& a, int max_tiles, int n_sh_tiles) {
+  const size_t R = (size_t)a.P + (size_t)a.n_shared * a.T;
+  return dn_parts(a) * R * 64 + (size_t)(n_sh_tiles + max_tiles) * 16 + 16 + (size_t)a.P * 8 +
+         (size_t)a.T * a.n_shared * 4;
 }
 
 }  // namespace
 
 hipError_t launch_mx_rows16(const MxProj& a, int mode, int act4, hipStream_t st) {
-  if (mode == 0) return act4 ? launch<0, true>(a, st) : launch<0, false>(a, st);
-  return act4 ? launch<1, true>(a, st) : launch<1, false>(a, st);
+  const MxRoute none = {};
+  const bool xq = act4 && a.q != nullptr;
+  if (mode == 0)
+    return xq ? launch<0, true, true, 0>(a, none, st)
+              : act4 ? launch<0, true, false, 0>(a, none, st) : launch<0, false, false, 0>(a, none, st);
+  return xq ? launch<1, true, true, 0>(a, none, st)
+            : act4 ? launch<1, true, false, 0>(a, none, st) : launch<1, false, false, 0>(a, none, st);
+}
+
+bool mx_route_gateup_ok(int T, int k, int E) {
+  return T <= kRouteT && T * k <= kRouteP && E <= kPermMaxE;
+}
+
+hipError_t launch_mx_route_gateup(const MxProj& a, int act4, const float* logits, int renorm,
+                                  int32_t* ids, float* w, int32_t* counts, int32_t* offsets,
+                                  int32_t* sorted_pair, int32_t* pair_pos, hipStream_t st) {
+  const MxRoute ro = {logits, renorm, ids, w, counts, offsets, sorted_pair, pair_pos};
+#define MX_NV(NV) \
+  (act4 ? launch<0, true, false, NV>(a, ro, st) : launch<0, false, false, NV>(a, ro, st))
+  if (a.E <= 64) return MX_NV(1);
+  if (a.E <= 128) return MX_NV(2);
+  if (a.E <= 256) return MX_NV(4);
+  return MX_NV(8);
+#undef MX_NV
+}
+
+bool mx_down_combine_ok(const MxProj& a) {
+  const int max_tiles = moe_permute_max_tiles(a.T, a.k, a.E, kTM);
+  const int n_sh_tiles = a.n_shared * ((a.T + kTM - 1) / kTM);
+  return n_sh_tiles + max_tiles <= kDnSlots && dn_lds(a, max_tiles, n_sh_tiles) <= 64 * 1024;
+}
+
+hipError_t launch_mx_down_combine(const MxProj& a, int act4, const float* topk_w,
+                                  const int32_t* pair_pos, const float* sh_gate, void* out,
+                                  int out_f32, hipStream_t st) {
+  MxCombine cb = {topk_w, pair_pos, sh_gate, out, out_f32,
+                  moe_permute_max_tiles(a.T, a.k, a.E, kTM), dn_parts(a)};
+  const int n_sh_tiles = a.n_shared * ((a.T + kTM - 1) / kTM);
+  const size_t lds = dn_lds(a, cb.max_tiles, n_sh_tiles);
+  auto kern = act4 ? mx_down_combine_kernel<true> : mx_down_combine_kernel<false>;
+  kern<<<a.U / 16, kDnThreads, lds, st>>>(a, cb, n_sh_tiles);
+  return hipGetLastError();
 }
 
 }  // namespace moe

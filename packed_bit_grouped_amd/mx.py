@@ -17,6 +17,8 @@ layer are defined there).
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import _lib as L
@@ -25,64 +27,78 @@ BLOCK = 32
 ACTS = {"a16": L.MOE_A16, "a4": L.MOE_A4, L.MOE_A16: L.MOE_A16, L.MOE_A4: L.MOE_A4}
 
 
-class _On:
-    """The tensors' device made current for a call, where it is not."""
-
-    def __init__(self, t):
-        if not t.is_cuda:
-            raise ValueError(f"expected a tensor on the GPU, got one on {t.device}")
-        d = t.get_device()
-        self.guard = None if d == torch.cuda.current_device() else torch.cuda.device(d)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _launch(name, dev, stream, *args):
+    """The C call on the device with index dev, on the stream (None: that
+    device's current one)."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _launch(name, dev, stream, *args)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    st = getattr(L._lib or L.load(), name)(*args, stream)
+    if st:
+        raise L.MoeError(name, st, L.status_str(st))
 
 
-def _want(name, t, dtypes, shape, device=None):
-    """t has one of the dtypes, the shape, no gaps, and lies on the device."""
+def _want(name, t, dtypes, shape, dev=None):
+    """t has one of the dtypes, the shape, no gaps, and lies on the device with
+    index dev (None: any); returns its address."""
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape
+            and t.is_contiguous() and (dev is None or t.get_device() == dev)):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
         raise TypeError(f"{name}: expected a tensor of {' or '.join(map(str, dtypes))}, got "
                         f"{getattr(t, 'dtype', type(t))}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name}: on {t.device}, the buffers are on {device}")
-    return t
+    raise ValueError(f"{name}: on {t.device}, expected it on the device of the other tensors")
 
 
 _BF16 = (torch.bfloat16, torch.int16)   # int16: bf16 bit patterns
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
+_U8 = (torch.uint8,)
+
+
+def _gpu(t):
+    if not t.is_cuda:
+        raise ValueError(f"expected a tensor on the GPU, got one on {t.device}")
+    return t.get_device()
 
 
 def quantize_rows(src, codes=None, scales=None, stream=None):
     """bf16 or fp32 rows [R][C] (unit stride along C, any row stride) to MXFP4:
     (codes uint8 [R][C/2], scales uint8 [R][C/32]), new unless given."""
-    if src.dtype not in (torch.bfloat16, torch.float32):
+    f32 = src.dtype is torch.float32
+    if not f32 and src.dtype is not torch.bfloat16:
         raise TypeError(f"src: expected bfloat16 or float32, got {src.dtype}")
     if src.dim() != 2:
         raise ValueError(f"src: expected rows [R][C], got shape {tuple(src.shape)}")
     R, C = src.shape
-    if C > 1 and R > 0 and src.stride(1) != 1:
-        raise ValueError("src: expected unit stride along C")
     if C == 0 or C % BLOCK:
         raise ValueError(f"src: rows of {C} values, expected a multiple of {BLOCK}")
-    ld = src.stride(0) if R > 1 else C
+    ld, unit = src.stride()
+    if R <= 1:
+        ld = C
+    if R > 0 and unit != 1:
+        raise ValueError("src: expected unit stride along C")
     if ld < C:
         raise ValueError("src: rows overlap")
+    dev = _gpu(src)
     if codes is None:
         codes = torch.empty((R, C // 2), dtype=torch.uint8, device=src.device)
+    else:
+        _want("codes", codes, _U8, (R, C // 2), dev)
     if scales is None:
         scales = torch.empty((R, C // BLOCK), dtype=torch.uint8, device=src.device)
-    _want("codes", codes, (torch.uint8,), (R, C // 2), src.device)
-    _want("scales", scales, (torch.uint8,), (R, C // BLOCK), src.device)
-    with _On(src):
-        L.moe_mx4_quant_rows(src, int(src.dtype == torch.float32), R, C, ld, codes, scales, stream)
+    else:
+        _want("scales", scales, _U8, (R, C // BLOCK), dev)
+    _launch("moe_mx4_quant_rows", dev, stream, src.data_ptr(), f32, R, C, ld, codes.data_ptr(),
+            scales.data_ptr())
     return codes, scales
 
 
@@ -92,14 +108,16 @@ def dequantize_rows(codes, scales, dtype=torch.bfloat16, stream=None):
         raise TypeError(f"dtype: expected bfloat16 or float32, got {dtype}")
     if codes.dim() != 2:
         raise ValueError(f"codes: expected rows [R][C/2], got shape {tuple(codes.shape)}")
-    R, C = codes.shape[0], 2 * codes.shape[1]
+    R, C = codes.shape
+    C *= 2
     if C == 0 or C % BLOCK:
         raise ValueError(f"codes: rows of {C} values, expected a multiple of {BLOCK}")
-    _want("codes", codes, (torch.uint8,), (R, C // 2))
-    _want("scales", scales, (torch.uint8,), (R, C // BLOCK), codes.device)
+    pc = _want("codes", codes, _U8, (R, C // 2))
+    ps = _want("scales", scales, _U8, (R, C // BLOCK), codes.get_device())
+    dev = _gpu(codes)
     dst = torch.empty((R, C), dtype=dtype, device=codes.device)
-    with _On(codes):
-        L.moe_mx4_dequant_rows(codes, scales, R, C, dst, int(dtype == torch.float32), C, stream)
+    _launch("moe_mx4_dequant_rows", dev, stream, pc, ps, R, C, dst.data_ptr(),
+            dtype is torch.float32, C)
     return dst
 
 
@@ -119,39 +137,43 @@ class MxBank:
     projection's pairs.  A later change of the weights needs a new bank."""
 
     def __init__(self, w13=None, w2=None, w13_shared=None, w2_shared=None, stream=None):
-        self.tiles, self.desc, self.shape = {}, {}, {}
+        self.tiles, self.desc, self.addr, self.shape = {}, {}, {}, {}
         self.device = None
         for tag, p in (("w13", w13), ("w2", w2), ("w13_shared", w13_shared),
                        ("w2_shared", w2_shared)):
-            self.desc[tag] = self.shape[tag] = None
+            self.shape[tag] = None
             if p is None:
                 continue
             codes, scales = p
             if codes.dim() != 3:
                 raise ValueError(f"{tag}: expected codes [n][N][K/2], got {tuple(codes.shape)}")
             n, N, K = codes.shape[0], codes.shape[1], 2 * codes.shape[2]
-            _want(tag + " codes", codes, (torch.uint8,), (n, N, K // 2), self.device)
-            self.device = codes.device
-            _want(tag + " scales", scales, (torch.uint8,), (n, N, K // BLOCK), self.device)
+            _want(tag + " codes", codes, _U8, (n, N, K // 2), self.device)
+            self.device = codes.get_device()
+            _want(tag + " scales", scales, _U8, (n, N, K // BLOCK), self.device)
             nc, ns = L.moe_mx4_bank_code_bytes(n, N, K), L.moe_mx4_bank_scale_bytes(n, N, K)
             if nc == 0:
                 raise ValueError(f"{tag}: unsupported matrices (n, N, K) = {(n, N, K)}")
-            with _On(codes):
-                tc = torch.empty(nc, dtype=torch.uint8, device=codes.device)
-                ts = torch.empty(ns, dtype=torch.uint8, device=codes.device)
-                L.moe_mx4_tile_bank(codes, scales, n, N, K, tc, ts, stream)
+            tc = torch.empty(nc, dtype=torch.uint8, device=codes.device)
+            ts = torch.empty(ns, dtype=torch.uint8, device=codes.device)
+            _launch("moe_mx4_tile_bank", _gpu(codes), stream, codes.data_ptr(), scales.data_ptr(),
+                    n, N, K, tc.data_ptr(), ts.data_ptr())
             self.tiles[tag] = (tc, ts)
             self.desc[tag] = L.MxBankDesc(tc.data_ptr(), ts.data_ptr())
+            self.addr[tag] = ctypes.addressof(self.desc[tag])
             self.shape[tag] = (n, N, K)
 
-    def need(self, tag, n, N, K):
-        """The descriptor of the pair `tag`, whose shape has to be (n, N, K)."""
-        if n == 0:
+    def need(self, tag, shape, dev):
+        """The address of the descriptor of `tag`, whose matrices have to be of
+        that shape (n, N, K) and on the device with index dev."""
+        if shape[0] == 0:
             return None
-        if self.shape[tag] != (n, N, K):
+        if self.shape[tag] != shape:
             raise ValueError(f"{tag}: the bank holds {self.shape[tag]} (n, N, K), the buffers "
-                             f"are for {(n, N, K)}")
-        return self.desc[tag]
+                             f"are for {shape}")
+        if self.device != dev:
+            raise ValueError(f"{tag}: the bank and the buffers are on different devices")
+        return self.addr[tag]
 
 
 class MxBuffers:
@@ -174,6 +196,10 @@ class MxBuffers:
         if dev.type == "cuda" and dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
         self.device = dev
+        self._dev = dev.index if dev.type == "cuda" else -1
+        # the matrices that a bank has to hold for these buffers
+        self.mats = {"w13": (E, 2 * I, H), "w2": (E, H, I), "w13_shared": (n_shared, 2 * I_shared, H),
+                     "w2_shared": (n_shared, H, I_shared)}
         i32 = dict(dtype=torch.int32, device=dev)
         self.ids = torch.empty((T, k), **i32)
         self.w = torch.empty((T, k), dtype=torch.float32, device=dev)
@@ -192,21 +218,21 @@ class MxBuffers:
 def _gate(shared_gate, B):
     if shared_gate is None or not B.n_shared:
         return None
-    return _want("shared_gate", shared_gate, (torch.float32,), (B.T, B.n_shared), B.device)
+    return _want("shared_gate", shared_gate, _F32, (B.T, B.n_shared), B._dev)
 
 
 def gateup_silu(bank, x, offsets, sorted_pair, B, stream=None):
     """h [T*k + n_shared*T][max(I, I_shared)] in bf16 (B.h) of x bf16 [T][H] and
     the sort's tables (int32): rows in the order of the sort, then the shared
     experts' tokens."""
-    _want("x", x, _BF16, (B.T, B.H), B.device)
-    _want("offsets", offsets, (torch.int32,), (B.E + 1,), B.device)
-    _want("sorted_pair", sorted_pair, (torch.int32,), (B.P,), B.device)
-    w13 = bank.need("w13", B.E, 2 * B.I, B.H)
-    sh = bank.need("w13_shared", B.n_shared, 2 * B.I_shared, B.H)
-    with _On(B.h):
-        L.moe_mx4_gateup_silu(B.act, x, B.T, B.H, B.I, B.E, B.k, w13, sh, B.n_shared, B.I_shared,
-                              offsets, sorted_pair, B.h, B.ws, B.ws_bytes, 0, stream)
+    dev = B._dev
+    px = _want("x", x, _BF16, (B.T, B.H), dev)
+    po = _want("offsets", offsets, _I32, (B.E + 1,), dev)
+    pp = _want("sorted_pair", sorted_pair, _I32, (B.P,), dev)
+    need, mats = bank.need, B.mats
+    w13, sh = need("w13", mats["w13"], dev), need("w13_shared", mats["w13_shared"], dev)
+    _launch("moe_mx4_gateup_silu", dev, stream, B.act, px, B.T, B.H, B.I, B.E, B.k, w13, sh,
+            B.n_shared, B.I_shared, po, pp, B.h.data_ptr(), B.ws.data_ptr(), B.ws_bytes, 0)
     return B.h
 
 
@@ -214,16 +240,16 @@ def down_combine(bank, h, w, offsets, pair_pos, B, shared_gate=None, stream=None
     """out [T][H] (B.out) of h (as from gateup_silu), the gate weights w fp32
     [T][k] and the sort's tables; shared_gate fp32 [T][n_shared]: gate logits of
     the shared experts (sigmoid), None: weight 1."""
-    _want("h", h, _BF16, (B.R, B.ld_h), B.device)
-    _want("w", w, (torch.float32,), (B.T, B.k), B.device)
-    _want("offsets", offsets, (torch.int32,), (B.E + 1,), B.device)
-    _want("pair_pos", pair_pos, (torch.int32,), (B.P,), B.device)
-    w2 = bank.need("w2", B.E, B.H, B.I)
-    sh = bank.need("w2_shared", B.n_shared, B.H, B.I_shared)
-    with _On(B.h):
-        L.moe_mx4_down_combine(B.act, h, B.T, B.H, B.I, B.E, B.k, w2, sh, B.n_shared, B.I_shared,
-                               w, offsets, pair_pos, B.out, B.ws, B.ws_bytes, B.out_flags, stream,
-                               shared_gate=_gate(shared_gate, B))
+    dev = B._dev
+    ph = _want("h", h, _BF16, (B.R, B.ld_h), dev)
+    pw = _want("w", w, _F32, (B.T, B.k), dev)
+    po = _want("offsets", offsets, _I32, (B.E + 1,), dev)
+    pp = _want("pair_pos", pair_pos, _I32, (B.P,), dev)
+    need, mats = bank.need, B.mats
+    w2, sh = need("w2", mats["w2"], dev), need("w2_shared", mats["w2_shared"], dev)
+    _launch("moe_mx4_down_combine", dev, stream, B.act, ph, B.T, B.H, B.I, B.E, B.k, w2, sh,
+            B.n_shared, B.I_shared, _gate(shared_gate, B), pw, po, pp, B.out.data_ptr(),
+            B.ws.data_ptr(), B.ws_bytes, B.out_flags)
     return B.out
 
 
@@ -231,15 +257,15 @@ def run_layer(bank, x, logits, B, renormalize=1, shared_gate=None, stream=None):
     """One layer step: out [T][H] (B.out) of x bf16 [T][H] and the router's
     logits fp32 [T][E]; the routing's results are in B.ids, B.w and the sort's
     tables of B."""
-    _want("x", x, _BF16, (B.T, B.H), B.device)
-    _want("logits", logits, (torch.float32,), (B.T, B.E), B.device)
-    w13 = bank.need("w13", B.E, 2 * B.I, B.H)
-    w2 = bank.need("w2", B.E, B.H, B.I)
-    s13 = bank.need("w13_shared", B.n_shared, 2 * B.I_shared, B.H)
-    s2 = bank.need("w2_shared", B.n_shared, B.H, B.I_shared)
-    with _On(B.h):
-        L.moe_mx4_layer(B.act, logits, x, B.T, B.H, B.I, B.E, B.k, int(renormalize), w13, w2, s13,
-                        s2, B.n_shared, B.I_shared, B.ids, B.w, B.counts, B.offsets,
-                        B.sorted_pair, B.pair_pos, B.h, B.out, B.ws, B.ws_bytes, B.out_flags,
-                        stream, shared_gate=_gate(shared_gate, B))
+    dev = B._dev
+    px = _want("x", x, _BF16, (B.T, B.H), dev)
+    pl = _want("logits", logits, _F32, (B.T, B.E), dev)
+    need, mats = bank.need, B.mats
+    w13, w2 = need("w13", mats["w13"], dev), need("w2", mats["w2"], dev)
+    s13, s2 = need("w13_shared", mats["w13_shared"], dev), need("w2_shared", mats["w2_shared"], dev)
+    _launch("moe_mx4_layer", dev, stream, B.act, pl, px, B.T, B.H, B.I, B.E, B.k,
+            int(renormalize), w13, w2, s13, s2, B.n_shared, B.I_shared, _gate(shared_gate, B),
+            B.ids.data_ptr(), B.w.data_ptr(), B.counts.data_ptr(), B.offsets.data_ptr(),
+            B.sorted_pair.data_ptr(), B.pair_pos.data_ptr(), B.h.data_ptr(), B.out.data_ptr(),
+            B.ws.data_ptr(), B.ws_bytes, B.out_flags)
     return B.out

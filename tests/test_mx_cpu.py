@@ -224,9 +224,9 @@ def test_python_front_refuses_before_the_library():
     with pytest.raises(ValueError, match="unsupported"):
         mx.MxBank(w13=(pair[0][:, :40].contiguous(), pair[1][:, :40].contiguous()))
     bank = mx.MxBank()
-    assert bank.need("w13_shared", 0, 64, 32) is None
+    assert bank.need("w13_shared", (0, 64, 32), 0) is None
     with pytest.raises(ValueError):
-        bank.need("w2", 2, 64, 32)
+        bank.need("w2", (2, 64, 32), 0)
     with pytest.raises(ValueError):
         mx.MxBuffers(4, 250, 32, 4, 2, device="cpu")
     with pytest.raises(ValueError):
