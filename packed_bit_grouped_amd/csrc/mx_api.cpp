@@ -164,8 +164,10 @@ moe_status down(int act, const uint16_t* h, int T, int H, int I, int E, int k,
   if (act4 && (gemm || P >= kCodesPairs)) {
     uint8_t* q = reinterpret_cast<uint8_t*>(ws + L.qh);
     uint8_t* sc = reinterpret_cast<uint8_t*>(ws + L.sh);
-    e = launch_mx_quant(h, 0, P, I, ld_h, q, sc, hp, true, s);
-    if (e == hipSuccess && n_shared > 0)
+    // rows of one length are one launch
+    const bool one = n_shared == 0 || I_shared == I;
+    e = launch_mx_quant(h, 0, one ? P + R_sh : P, I, ld_h, q, sc, hp, true, s);
+    if (e == hipSuccess && !one)
       e = launch_mx_quant(h_sh, 0, R_sh, I_shared, ld_h, q + (size_t)P * (hp / 2),
                           sc + (size_t)P * (hp / kMxBlock), hp, true, s);
     a.q = q;

@@ -109,6 +109,13 @@ __device__ __forceinline__ mx_f32x4 mx_mfma_fp4(mx_u32x4 a, uint32_t sa, mx_u32x
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, J, (int)sa, J, (int)sb);
 }
 
+// Keeps v's computation before this point.  A matrix instruction reads all lanes'
+// registers whatever the execution mask, but the compiler may move a scaled one
+// (and the conversions that feed it) into a branch that only some lanes take,
+// if only those use its result: whatever stands before such a branch is kept
+// before it by this.
+__device__ __forceinline__ void mx_keep(mx_f32x4& v) { __asm__ volatile("" : "+v"(v)); }
+
 // The sorted rows cut into tiles of at most TM rows, experts in order, empty
 // experts skipped, by one wave from the offsets alone: lane l owns the experts
 // [PER * l, PER * l + PER) (E <= 64 * PER), all its offsets loaded at once, and

@@ -335,6 +335,8 @@ __device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, __amdgpu
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int row = 16 * m + c;
+#pragma unroll
+    for (int f = 0; f < kNF; ++f) mx_keep(acc[f][m]);
     if (row >= nrows) continue;
     if (MODE == 0) {
       uint16_t* h = static_cast<uint16_t*>(ga.p.out) + (size_t)(t.orow + row) * ga.p.ld_out;

@@ -128,64 +128,168 @@ struct MxRoute {
   int32_t* pair_pos;
 };
 
-constexpr int kRouteT = 16;    // tokens of the fused routing
-constexpr int kRouteP = 64;    // and pairs: one per lane
+// Up to this many tokens and pairs route inside the gate/up launch.  (Fewer
+// than kRouteRowMinT tokens: their gate weights are summed over 64 lanes, as
+// the routing kernels do for them.)
+constexpr int kRouteT = 4;
+constexpr int kRouteP = 64;
+static_assert(kRouteT < kRouteRowMinT, "the order of the gate weights' sum");
 
-// One pair per lane (expert id, P pairs): where it stands in the stable sort by
-// expert, from ballots over the id's bits (masks of the pairs that sort before
-// it and of those of its own expert).
-struct PairSort {
-  int id, lt, before, same;   // pairs of smaller experts; of the same one before it; in all
-  uint64_t eq;
-
-  __device__ __forceinline__ void sort(int id_, int P, int E) {
-    const int lane = threadIdx.x & 63;
-    id = id_;
-    const bool in = lane < P;
-    eq = __ballot(in);
-    uint64_t less = 0;
-    for (int b = 31 - __builtin_clz(E | 1); b >= 0; --b) {
-      const bool bit = (id >> b) & 1;
-      const uint64_t ones = __ballot(in && bit);
-      if (bit) less |= eq & ~ones;
-      eq &= bit ? ones : ~ones;
-    }
-    lt = __popcll(less);
-    before = __popcll(eq & (lane == 0 ? 0ull : ~0ull >> (64 - lane)));
-    same = __popcll(eq);
+// LDS of the routing of T tokens (dynamic): order keys [T][E4], ranks [T][E],
+// chosen ids [P], masks of the chosen experts [T][W].
+struct RouteLds {
+  uint32_t* ord;
+  int* rank;
+  int* ids;
+  uint64_t* mask;
+  int E4, W;
+  static __host__ __device__ size_t bytes(int T, int E) {
+    return (size_t)T * ((E + 3) / 4 * 4 + E) * 4 + kRouteP * 4 + (size_t)T * ((E + 63) / 64) * 8 + 8;
   }
-  // Tile j of kTM rows, as MxTiles::find; the lane of row r of it has
-  // id == e and before == r - lt.
-  __device__ __forceinline__ bool find(int j, int P, int& e, int& r0, int& r1) const {
-    const int lane = threadIdx.x & 63;
-    const bool start = lane < P && before % kTM == 0;
-    // tile starts before mine: experts smaller than mine, earlier tiles of mine
-    const uint64_t starts = __ballot(start);
-    int idx = 0;
-    for (uint64_t m = starts; m; m &= m - 1) {
-      const int l = __builtin_ctzll(m);
-      const int k = __builtin_amdgcn_readlane(lt + before, l);
-      idx += k < lt + before;
-    }
-    const uint64_t mine = __ballot(start && idx == j);
-    if (mine == 0) return false;
-    const int o = __builtin_ctzll(mine);
-    e = __builtin_amdgcn_readlane(id, o);
-    r0 = __builtin_amdgcn_readlane(lt + before, o);
-    r1 = min(r0 + kTM, __builtin_amdgcn_readlane(lt + same, o));
-    return true;
+  __device__ RouteLds(unsigned char* p, int T, int E) : E4((E + 3) & ~3), W((E + 63) / 64) {
+    ord = reinterpret_cast<uint32_t*>(p);
+    rank = reinterpret_cast<int*>(ord + T * E4);
+    ids = rank + T * E;
+    mask = reinterpret_cast<uint64_t*>(
+        (reinterpret_cast<uintptr_t>(ids + kRouteP) + 7) & ~uintptr_t(7));
   }
 };
 
+// Top-k of T tokens by the whole workgroup: the rank of an expert is the number
+// of experts that beat it (larger key, or an equal one with a smaller index),
+// counted by all threads at once - for a handful of tokens about half the time
+// of k arg-max rounds in one wave per token - and the chosen ones are those
+// with rank < k, kept as bit masks.
+template <int THREADS>
+__device__ __forceinline__ void route_masks(const MxProj& a, const float* __restrict__ logits,
+                                            const RouteLds& L) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int E = a.E, n = a.T * E;
+  for (int i = tid; i < a.T * L.E4; i += THREADS) {
+    const int t = a.T == 1 ? 0 : i / L.E4, e = i - t * L.E4;
+    L.ord[i] = e < E ? route_ord(logits[t * E + e]) : 0u;   // 0: beats nothing
+  }
+  for (int i = tid; i < n; i += THREADS) L.rank[i] = 0;
+  __syncthreads();
+  // few keys: several threads share one, each counting a part of the experts
+  const int parts = n < THREADS ? THREADS / n : 1;
+  const int run = (L.E4 / 4 + parts - 1) / parts;   // quads per part
+  for (int i = tid; i < n * parts; i += THREADS) {
+    const int part = parts == 1 ? 0 : i / n, r = i - part * n;
+    const int t = a.T == 1 ? 0 : r / E, e = r - t * E;
+    const uint32_t* row = L.ord + t * L.E4;
+    const uint32_t my = row[e];
+    const int q1 = min((part + 1) * run, L.E4 / 4);
+    int cnt = 0;
+#pragma unroll 4
+    for (int q = part * run; q < q1; ++q) {
+      const mx_u32x4 v = *reinterpret_cast<const mx_u32x4*>(row + 4 * q);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) cnt += v[j] > my || (v[j] == my && 4 * q + j < e);
+    }
+    if (parts == 1) L.rank[r] = cnt;
+    else atomicAdd(&L.rank[r], cnt);   // integers: any order
+  }
+  __syncthreads();
+  for (int i = wave; i < a.T * L.W; i += THREADS / 64) {
+    const int t = a.T == 1 ? 0 : i / L.W, e = (i - t * L.W) * 64 + lane;
+    const uint64_t m = __ballot(e < E && L.rank[t * E + min(e, E - 1)] < a.k);
+    if (lane == 0) L.mask[i] = m;
+  }
+  __syncthreads();
+}
+
+// The workgroup that writes the tables of moe_route_topk and moe_permute.
+template <int THREADS>
+__device__ __forceinline__ void write_routing(const MxProj& a, const MxRoute& ro,
+                                              const RouteLds& L) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int E = a.E, k = a.k;
+  // pairs of experts before e, and of e by tokens before t
+  auto place = [&](int e, int t) {
+    const uint64_t below = (1ull << (e & 63)) - 1;
+    int o = 0;
+    for (int u = 0; u < a.T; ++u) {
+      for (int w = 0; w < e / 64; ++w) o += __popcll(L.mask[u * L.W + w]);
+      o += __popcll(L.mask[u * L.W + e / 64] & below);
+      if (u < t) o += (int)(L.mask[u * L.W + e / 64] >> (e & 63)) & 1;
+    }
+    return o;
+  };
+  for (int i = tid; i < a.T * E; i += THREADS) {
+    const int t = i / E, e = i - t * E, r = L.rank[i];
+    if (r < k) {
+      const int p = t * k + r, pos = place(e, t);
+      L.ids[p] = e;
+      ro.ids[p] = e;
+      ro.pair_pos[p] = pos;
+      ro.sorted_pair[pos] = p;
+    }
+  }
+  for (int e = tid; e < E; e += THREADS) {
+    int c = 0;
+    for (int u = 0; u < a.T; ++u) c += (int)(L.mask[u * L.W + e / 64] >> (e & 63)) & 1;
+    ro.counts[e] = c;
+    ro.offsets[e] = place(e, 0);
+  }
+  if (tid == 0) ro.offsets[E] = a.P;
+  __syncthreads();
+  // gate weights: one wave per token, choice r in lane r (k <= 64), the sums of
+  // route_group_vals
+  for (int t = wave; t < a.T; t += THREADS / 64) {
+    const float v = lane < k ? route_unord(L.ord[t * L.E4 + L.ids[t * k + lane]]) : 0.0f;
+    const float top = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 0));
+    const float ex = lane < k ? expf(v - top) : 0.0f;
+    float sum = ex;
+    if (!ro.renorm) {
+      sum = 0.0f;
+      for (int e = lane; e < E; e += 64) sum += expf(route_unord(L.ord[t * L.E4 + e]) - top);
+    }
+    const float denom = wave_sum(sum);
+    if (lane < k) ro.w[t * k + lane] = ex / denom;
+  }
+}
+
+// Tile j of the routed experts (each has at most T <= 16 rows: one tile): its
+// expert, rows, and the token of this lane's row (-1: none).
+__device__ __forceinline__ bool find_masked(const MxProj& a, const RouteLds& L, int j, int& e,
+                                            int& r0, int& r1, int& token) {
+  const int c = threadIdx.x & 15;
+  r0 = 0;
+  for (int w = 0; w < L.W; ++w) {
+    uint64_t any = 0;
+    for (int t = 0; t < a.T; ++t) any |= L.mask[t * L.W + w];
+    const int n = __popcll(any);
+    if (j < n) {
+      for (; j > 0; --j) any &= any - 1;
+      const int b = __builtin_ctzll(any);
+      e = 64 * w + b;
+      int rows = 0;
+      token = -1;
+      for (int t = 0; t < a.T; ++t) {
+        const uint64_t m = L.mask[t * L.W + w];
+        r0 += __popcll(m & ((1ull << b) - 1));
+        if ((m >> b) & 1) {
+          if (rows == c) token = t;
+          ++rows;
+        }
+      }
+      r1 = r0 + rows;
+      return true;
+    }
+    j -= n;
+    for (int t = 0; t < a.T; ++t) r0 += __popcll(L.mask[t * L.W + w]);
+  }
+  return false;
+}
+
 // XQ (A4): the activations' codes and scales come from memory; else they are
-// quantised here.  NV: logits per lane of the routing (0: no routing here, the
-// tables come from memory).  WV waves per workgroup.
-template <int MODE, bool ACT4, bool XQ, int NB, int NV, int WV>
+// quantised here.  ROUTE: the workgroup routes the tokens itself, and workgroup
+// 0 writes the tables; else the tables come from memory.  WV waves.
+template <int MODE, bool ACT4, bool XQ, int NB, bool ROUTE, int WV>
 __global__ __launch_bounds__(64 * WV) void mx_rows16_kernel(MxProj a, MxRoute ro, int n_sh_tiles,
                                                             int n_ub) {
-  constexpr bool ROUTE = NV > 0;
   __shared__ float red[WV][2][kTM * kPitch];
-  __shared__ int tok_l[WV][kTM];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int blk = ROUTE ? (int)blockIdx.x - 1 : (int)blockIdx.x;
   const int c = lane & 15, g = lane >> 4;
@@ -193,7 +297,7 @@ __global__ __launch_bounds__(64 * WV) void mx_rows16_kernel(MxProj a, MxRoute ro
   // ---- the tile: shared experts' first
   bool is_sh = false;
   int e = 0, r0 = 0, r1 = 0;
-  int pair = -1;   // routed launch: the sorted pair of this lane's column
+  int token = -1;   // routed launch: the token of this lane's column
   const int slot = blk / n_ub, ub = blk - slot * n_ub;
   if (blk >= 0 && slot < n_sh_tiles) {
     const int per = (a.T + kTM - 1) / kTM;
@@ -202,39 +306,16 @@ __global__ __launch_bounds__(64 * WV) void mx_rows16_kernel(MxProj a, MxRoute ro
     r0 = (slot - e * per) * kTM;
     r1 = min(a.T, r0 + kTM);
   } else if constexpr (ROUTE) {
-    // workgroup 0 writes the tables of moe_route_topk and moe_permute
-    __shared__ int ids_l[kRouteP];
-    const bool writer = blk < 0;
-    route_tokens<NV, (kRouteT + 4 * WV - 1) / (4 * WV)>(ro.logits, a.T, a.E, a.k, ro.renorm, lane,
-                                                        wave, WV, writer ? ro.ids : nullptr,
-                                                        writer ? ro.w : nullptr, ids_l, nullptr);
-    __syncthreads();
-    PairSort ps;
-    ps.sort(lane < a.P ? ids_l[lane] : 0, a.P, a.E);
-    if (writer) {
-      if (tid < a.P) {
-        ro.sorted_pair[ps.lt + ps.before] = lane;
-        ro.pair_pos[lane] = ps.lt + ps.before;
-      }
-      for (int x = tid; x < a.E; x += 64 * WV) {
-        int n = 0, o = 0;
-        for (int q = 0; q < a.P; ++q) {
-          n += ids_l[q] == x;
-          o += ids_l[q] < x;
-        }
-        ro.counts[x] = n;
-        ro.offsets[x] = o;
-      }
-      if (tid == 0) ro.offsets[a.E] = a.P;
+    extern __shared__ __align__(16) unsigned char route_smem[];
+    const RouteLds L(route_smem, a.T, a.E);
+    route_masks<64 * WV>(a, ro.logits, L);
+    if (blk < 0) {
+      write_routing<64 * WV>(a, ro, L);
       return;
     }
-    if (!ps.find(slot - n_sh_tiles, a.P, e, r0, r1)) return;
-    const int row = ps.lt + ps.before;
-    if (lane < a.P && ps.id == e && row >= r0 && row < r1) tok_l[wave][row - r0] = lane;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");   // the wave's own words
-    if (r0 + c < r1) pair = tok_l[wave][c];
+    if (!find_masked(a, L, slot - n_sh_tiles, e, r0, r1, token)) return;
   } else {
-    // E <= 512: 1, 2, 4 or 8 experts per lane
+    // E <= 512: two or eight experts per lane
     const int j = slot - n_sh_tiles;
     bool ok;
     if (a.E <= 128) {
@@ -271,8 +352,10 @@ __global__ __launch_bounds__(64 * WV) void mx_rows16_kernel(MxProj a, MxRoute ro
       xrow = orow + c;
     } else if (is_sh) {
       xrow = r0 + c;
+    } else if (ROUTE) {
+      xrow = token;
     } else {
-      const int p = ROUTE ? pair : a.sorted_pair[r0 + c];
+      const int p = a.sorted_pair[r0 + c];
       have = (unsigned)p < (unsigned)a.P;
       xrow = have ? p / a.k : 0;
     }
@@ -314,6 +397,8 @@ __global__ __launch_bounds__(64 * WV) void mx_rows16_kernel(MxProj a, MxRoute ro
     }
   }
 
+  mx_keep(acc[0]);
+  mx_keep(acc[1]);
   // ---- the waves' parts of K meet: word [unit][row]
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -342,25 +427,27 @@ int max_slots(const MxProj& a) {
   return a.n_shared * ((a.T + kTM - 1) / kTM) + moe_permute_max_tiles(a.T, a.k, a.E, kTM);
 }
 
-template <int MODE, bool ACT4, bool XQ, int NV>
+template <int MODE, bool ACT4, bool XQ, bool ROUTE>
 hipError_t launch(const MxProj& a, const MxRoute& ro, hipStream_t st) {
   const int n_sh_tiles = a.n_shared * ((a.T + kTM - 1) / kTM);
   const int step = MODE == 0 ? 16 : 32;
   const int U = a.n_shared > 0 && a.U_sh > a.U ? a.U_sh : a.U;
   const int n_ub = (U + step - 1) / step;
-  const long long grid = (long long)max_slots(a) * n_ub + (NV > 0 ? 1 : 0);
+  const long long grid = (long long)max_slots(a) * n_ub + (ROUTE ? 1 : 0);
   if (grid >= (1LL << 31)) return hipErrorInvalidValue;
   const int K = a.n_shared > 0 && a.K_sh > a.K ? a.K_sh : a.K;
   const int pieces = mx_pieces(K);
+  const size_t lds = ROUTE ? RouteLds::bytes(a.T, a.E) : 0;
   // Up to 64 pairs (a few tokens) eight waves split K, so that each has little
   // to do behind its loads; else four, with longer runs.  The same rule with
   // and without the routing: both sum in the same order.
-#define MX_GO(NB, WV) \
-  mx_rows16_kernel<MODE, ACT4, XQ, NB, NV, WV><<<(int)grid, 64 * WV, 0, st>>>(a, ro, n_sh_tiles, n_ub)
-  if (NV > 0 || a.P <= kRouteP) {
+#define MX_GO(NB, WV)                                                                         \
+  mx_rows16_kernel<MODE, ACT4, XQ, NB, ROUTE, WV><<<(int)grid, 64 * WV, lds, st>>>(a, ro, n_sh_tiles, \
+                                                                                   n_ub)
+  if (ROUTE || a.P <= kRouteP) {
     if (pieces >= 16) MX_GO(2, 8);
     else MX_GO(1, 8);
-  } else if constexpr (NV == 0) {
+  } else if constexpr (!ROUTE) {
     if (pieces >= 16) MX_GO(4, 4);
     else if (pieces >= 8) MX_GO(2, 4);
     else MX_GO(1, 4);
@@ -385,20 +472,24 @@ struct MxCombine {
   int n_ch;        // parts of K: items per tile
 };
 
-template <bool ACT4>
+// COLS: 16 output columns per workgroup, or 8 (half the rows of a piece: 128-byte
+// runs of it) where 16 would leave compute units without a workgroup - one of
+// them draws about 23 GB/s, so a token's 7 MB want all 256.
+template <bool ACT4, int COLS>
 __global__ __launch_bounds__(kDnThreads) void mx_down_combine_kernel(MxProj a, MxCombine cb,
                                                                      int n_sh_tiles) {
   extern __shared__ __align__(16) unsigned char smem[];
   const int R = a.P + a.n_shared * a.T;
-  float* yb = reinterpret_cast<float*>(smem);                             // [n_ch][R][16]
-  int4* til = reinterpret_cast<int4*>(yb + (size_t)cb.n_ch * R * 16);     // [slots]
+  float* yb = reinterpret_cast<float*>(smem);                             // [n_ch][R][COLS]
+  int4* til = reinterpret_cast<int4*>(yb + (size_t)cb.n_ch * R * COLS);   // [slots]
   int* n_til = reinterpret_cast<int*>(til + n_sh_tiles + cb.max_tiles);
   int* ppos = n_til + 4;                                                  // [P]
   float* gw = reinterpret_cast<float*>(ppos + a.P);                       // [P]
   float* sg = gw + a.P;                                                   // [T][n_shared]
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int c = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.x * 16;
+  const int n0 = blockIdx.x * COLS;
+  const bool wrow = COLS == 16 || (c >> 3) == ((n0 >> 3) & 1);   // this lane's weight row is wanted
 
   // ---- tile list (expert, first row, end row, shared) and the gate tables
   for (int i = tid; i < a.P; i += kDnThreads) {
@@ -449,7 +540,7 @@ __global__ __launch_bounds__(kDnThreads) void mx_down_combine_kernel(MxProj a, M
       const mx_u32x4* q = reinterpret_cast<const mx_u32x4*>(wq) + rb * pieces * 64 + lane;
 #pragma unroll
       for (int j = 0; j < kDnNB; ++j)
-        w[i][0][j] = ok && s + j < pieces ? __builtin_nontemporal_load(q + (s + j) * 64) : zero;
+        w[i][0][j] = ok && wrow && s + j < pieces ? __builtin_nontemporal_load(q + (s + j) * 64) : zero;
       sw[i][0] = ok && s < pieces
                      ? load_scales<kDnNB>(ws + ((rb * words + (s >> 2)) * 64 + lane) * 4, s)
                      : 0u;
@@ -469,40 +560,56 @@ __global__ __launch_bounds__(kDnThreads) void mx_down_combine_kernel(MxProj a, M
       if (item >= n_items) break;
       mx_f32x4 acc[1] = {{0, 0, 0, 0}};
       products<ACT4, kDnNB, 1>(w[i], sw[i], x[i], acc);
+      mx_keep(acc[0]);
       const int ch = item % cb.n_ch;
-      if (tl[i].y + c < tl[i].z)
-        *reinterpret_cast<mx_f32x4*>(yb + ((size_t)ch * R + tl[i].y + c) * 16 + 4 * g) = acc[0];
+      // lane: row c, weight rows 4g .. 4g + 3
+      if (tl[i].y + c < tl[i].z && (COLS == 16 || (g >> 1) == ((n0 >> 3) & 1)))
+        *reinterpret_cast<mx_f32x4*>(yb + ((size_t)ch * R + tl[i].y + c) * COLS +
+                                     (4 * g & (COLS - 1))) = acc[0];
     }
   }
   __syncthreads();
 
-  // ---- out[t][n] = sum_j w_j y_j + sum_s g_s y_s, in that order; the parts of
-  // K of a row first
-  const size_t part = (size_t)R * 16;
-  for (int i = tid; i < a.T * 16; i += kDnThreads) {
-    const int t = i >> 4, n = i & 15;
-    auto row = [&](int r) {
-      float y = yb[(size_t)r * 16 + n];
-      for (int ch = 1; ch < cb.n_ch; ++ch) y += yb[ch * part + (size_t)r * 16 + n];
-      return y;
-    };
-    // four pairs at a time: their LDS reads, then the sum in order
-    float o = 0.0f;
-    for (int j0 = 0; j0 < a.k; j0 += 4) {
-      float y[4], w[4];
+  // ---- the parts of K of every row (rows that no tile wrote are not read below)
+  const int part = R * COLS;
+  if (cb.n_ch > 1) {
+    for (int i = tid; i < part; i += kDnThreads) {
+      float y = yb[i];
+      for (int c0 = 1; c0 < cb.n_ch; c0 += 4) {
+        float v[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int q = t * a.k + min(j0 + j, a.k - 1), p = ppos[q];
+        for (int q = 0; q < 4; ++q) v[q] = yb[min(c0 + q, cb.n_ch - 1) * part + i];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (c0 + q < cb.n_ch) y += v[q];
+      }
+      yb[i] = y;
+    }
+    __syncthreads();
+  }
+
+  // ---- out[t][n] = sum_j w_j y_j + sum_s g_s y_s, in that order
+  for (int i = tid; i < a.T * COLS; i += kDnThreads) {
+    const int t = i / COLS, n = i & (COLS - 1);
+    // eight pairs at a time: their LDS reads, then the sum in order
+    float o = 0.0f;
+    for (int j0 = 0; j0 < a.k; j0 += 8) {
+      int p[8];
+      float y[8], w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int q = t * a.k + min(j0 + j, a.k - 1);
+        p[j] = j0 + j < a.k ? ppos[q] : -1;
         w[j] = gw[q];
-        const bool on = j0 + j < a.k && p >= 0;
-        y[j] = row(on ? p : 0);
-        if (!on) w[j] = y[j] = 0.0f;   // + 0: the sum as if it were skipped
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o = fmaf(w[j], y[j], o);
+      for (int j = 0; j < 8; ++j) y[j] = yb[max(p[j], 0) * COLS + n];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (p[j] >= 0) o = fmaf(w[j], y[j], o);
     }
     for (int s = 0; s < a.n_shared; ++s)
-      o = fmaf(sg[t * a.n_shared + s], row(a.P + s * a.T + t), o);
+      o = fmaf(sg[t * a.n_shared + s], yb[(a.P + s * a.T + t) * COLS + n], o);
     if (cb.out_f32) static_cast<float*>(cb.out)[(size_t)t * a.U + n0 + n] = o;
     else static_cast<uint16_t*>(cb.out)[(size_t)t * a.U + n0 + n] = (uint16_t)mx_bf16(o);
   }
@@ -513,9 +620,11 @@ int dn_parts(const MxProj& a) {
   return (mx_pieces(K) + kDnNB - 1) / kDnNB;
 }
 
+int dn_cols(const MxProj& a) { return a.U / 16 < 256 ? 8 : 16; }
+
 size_t dn_lds(const MxProj& a, int max_tiles, int n_sh_tiles) {
   const size_t R = (size_t)a.P + (size_t)a.n_shared * a.T;
-  return dn_parts(a) * R * 64 + (size_t)(n_sh_tiles + max_tiles) * 16 + 16 + (size_t)a.P * 8 +
+  return dn_parts(a) * R * dn_cols(a) * 4 + (size_t)(n_sh_tiles + max_tiles) * 16 + 16 + (size_t)a.P * 8 +
          (size_t)a.T * a.n_shared * 4;
 }
 
@@ -524,11 +633,12 @@ size_t dn_lds(const MxProj& a, int max_tiles, int n_sh_tiles) {
 hipError_t launch_mx_rows16(const MxProj& a, int mode, int act4, hipStream_t st) {
   const MxRoute none = {};
   const bool xq = act4 && a.q != nullptr;
-  if (mode == 0)
-    return xq ? launch<0, true, true, 0>(a, none, st)
-              : act4 ? launch<0, true, false, 0>(a, none, st) : launch<0, false, false, 0>(a, none, st);
-  return xq ? launch<1, true, true, 0>(a, none, st)
-            : act4 ? launch<1, true, false, 0>(a, none, st) : launch<1, false, false, 0>(a, none, st);
+#define MX_L(MODE)                                              \
+  (xq     ? launch<MODE, true, true, false>(a, none, st)        \
+   : act4 ? launch<MODE, true, false, false>(a, none, st)       \
+          : launch<MODE, false, false, false>(a, none, st))
+  return mode == 0 ? MX_L(0) : MX_L(1);
+#undef MX_L
 }
 
 bool mx_route_gateup_ok(int T, int k, int E) {
@@ -539,13 +649,7 @@ hipError_t launch_mx_route_gateup(const MxProj& a, int act4, const float* logits
                                   int32_t* ids, float* w, int32_t* counts, int32_t* offsets,
                                   int32_t* sorted_pair, int32_t* pair_pos, hipStream_t st) {
   const MxRoute ro = {logits, renorm, ids, w, counts, offsets, sorted_pair, pair_pos};
-#define MX_NV(NV) \
-  (act4 ? launch<0, true, false, NV>(a, ro, st) : launch<0, false, false, NV>(a, ro, st))
-  if (a.E <= 64) return MX_NV(1);
-  if (a.E <= 128) return MX_NV(2);
-  if (a.E <= 256) return MX_NV(4);
-  return MX_NV(8);
-#undef MX_NV
+  return act4 ? launch<0, true, false, true>(a, ro, st) : launch<0, false, false, true>(a, ro, st);
 }
 
 bool mx_down_combine_ok(const MxProj& a) {
@@ -561,8 +665,10 @@ hipError_t launch_mx_down_combine(const MxProj& a, int act4, const float* topk_w
                   moe_permute_max_tiles(a.T, a.k, a.E, kTM), dn_parts(a)};
   const int n_sh_tiles = a.n_shared * ((a.T + kTM - 1) / kTM);
   const size_t lds = dn_lds(a, cb.max_tiles, n_sh_tiles);
-  auto kern = act4 ? mx_down_combine_kernel<true> : mx_down_combine_kernel<false>;
-  kern<<<a.U / 16, kDnThreads, lds, st>>>(a, cb, n_sh_tiles);
+  const bool half = dn_cols(a) == 8;
+  auto kern = act4 ? (half ? mx_down_combine_kernel<true, 8> : mx_down_combine_kernel<true, 16>)
+                   : (half ? mx_down_combine_kernel<false, 8> : mx_down_combine_kernel<false, 16>);
+  kern<<<a.U / dn_cols(a), kDnThreads, lds, st>>>(a, cb, n_sh_tiles);
   return hipGetLastError();
 }
 
