@@ -317,7 +317,7 @@ moe_status moe_mx4_layer(int act, const float* logits, const uint16_t* x, int T,
   hipStream_t s = static_cast<hipStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
   const MxProj a = gateup_proj(x, T, H, I, E, k, w13, w13_shared, n_shared, I_shared, h);
-  if (mx_route_gateup_ok(T, k, E) && a.P < kGemmRows * E) {
+  if (mx_route_gateup_ok(T, k, E, H) && a.P < kGemmRows * E) {
     // a few tokens: routing, sort and gate/up in one launch
     st = from_hip(launch_mx_route_gateup(a, act == MOE_A4, logits, renormalize, topk_ids, topk_w,
                                          counts, offsets, sorted_pair, pair_pos, s));

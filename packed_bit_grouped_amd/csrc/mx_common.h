@@ -183,7 +183,7 @@ hipError_t launch_mx_pad_rows(const uint16_t* src, int R, int C, int ld, uint16_
 // Tiles of 16 rows, K split over the workgroup's waves:
 hipError_t launch_mx_rows16(const MxProj& a, int mode, int act4, hipStream_t st);
 // The same for a few tokens with their routing and sort in the launch:
-bool mx_route_gateup_ok(int T, int k, int E);
+bool mx_route_gateup_ok(int T, int k, int E, int H);
 hipError_t launch_mx_route_gateup(const MxProj& a, int act4, const float* logits, int renorm,
                                   int32_t* ids, float* w, int32_t* counts, int32_t* offsets,
                                   int32_t* sorted_pair, int32_t* pair_pos, hipStream_t st);

@@ -135,66 +135,84 @@ constexpr int kRouteT = 4;
 constexpr int kRouteP = 64;
 static_assert(kRouteT < kRouteRowMinT, "the order of the gate weights' sum");
 
-// LDS of the routing of T tokens (dynamic): order keys [T][E4], ranks [T][E],
-// chosen ids [P], masks of the chosen experts [T][W].
+// LDS of the routed launch (dynamic): masks of the chosen experts [T][W], then
+// (workgroup 0) the chosen ids and their order keys [P], and the tokens' rows,
+// 16 bytes apart beyond their length.
 struct RouteLds {
-  uint32_t* ord;
-  int* rank;
-  int* ids;
   uint64_t* mask;
-  int E4, W;
-  static __host__ __device__ size_t bytes(int T, int E) {
-    return (size_t)T * ((E + 3) / 4 * 4 + E) * 4 + kRouteP * 4 + (size_t)T * ((E + 63) / 64) * 8 + 8;
+  int* ids;
+  uint32_t* key;
+  unsigned char* x;
+  int W, pitch;
+  static __host__ __device__ size_t head(int T, int E) {
+    return ((size_t)T * ((E + 63) / 64) * 8 + kRouteP * 8 + 15) / 16 * 16;
   }
-  __device__ RouteLds(unsigned char* p, int T, int E) : E4((E + 3) & ~3), W((E + 63) / 64) {
-    ord = reinterpret_cast<uint32_t*>(p);
-    rank = reinterpret_cast<int*>(ord + T * E4);
-    ids = rank + T * E;
-    mask = reinterpret_cast<uint64_t*>(
-        (reinterpret_cast<uintptr_t>(ids + kRouteP) + 7) & ~uintptr_t(7));
+  static __host__ __device__ size_t bytes(int T, int E, int H) {
+    return head(T, E) + (size_t)T * (H * 2 + 16);
+  }
+  __device__ RouteLds(unsigned char* p, int T, int E, int H) : W((E + 63) / 64), pitch(H * 2 + 16) {
+    mask = reinterpret_cast<uint64_t*>(p);
+    ids = reinterpret_cast<int*>(mask + T * W);
+    key = reinterpret_cast<uint32_t*>(ids + kRouteP);
+    x = p + head(T, E);
   }
 };
 
-// Top-k of T tokens by the whole workgroup: the rank of an expert is the number
-// of experts that beat it (larger key, or an equal one with a smaller index),
-// counted by all threads at once - for a handful of tokens about half the time
-// of k arg-max rounds in one wave per token - and the chosen ones are those
-// with rank < k, kept as bit masks.
-template <int THREADS>
-__device__ __forceinline__ void route_masks(const MxProj& a, const float* __restrict__ logits,
-                                            const RouteLds& L) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int E = a.E, n = a.T * E;
-  for (int i = tid; i < a.T * L.E4; i += THREADS) {
-    const int t = a.T == 1 ? 0 : i / L.E4, e = i - t * L.E4;
-    L.ord[i] = e < E ? route_ord(logits[t * E + e]) : 0u;   // 0: beats nothing
-  }
-  for (int i = tid; i < n; i += THREADS) L.rank[i] = 0;
-  __syncthreads();
-  // few keys: several threads share one, each counting a part of the experts
-  const int parts = n < THREADS ? THREADS / n : 1;
-  const int run = (L.E4 / 4 + parts - 1) / parts;   // quads per part
-  for (int i = tid; i < n * parts; i += THREADS) {
-    const int part = parts == 1 ? 0 : i / n, r = i - part * n;
-    const int t = a.T == 1 ? 0 : r / E, e = r - t * E;
-    const uint32_t* row = L.ord + t * L.E4;
-    const uint32_t my = row[e];
-    const int q1 = min((part + 1) * run, L.E4 / 4);
-    int cnt = 0;
-#pragma unroll 4
-    for (int q = part * run; q < q1; ++q) {
-      const mx_u32x4 v = *reinterpret_cast<const mx_u32x4*>(row + 4 * q);
+// One wave, one token: the mask of the k experts with the largest order keys
+// (of equal keys the smaller index).  The k-th largest key is found from the top
+// two bits at a time, counting the keys not below a candidate by ballots; that
+// takes half the time of k arg-max rounds, whose order only workgroup 0 needs.
+template <int NV>
+__device__ __forceinline__ void select_topk(const float* __restrict__ logits, int E, int k,
+                                            uint64_t* mask) {
+  const int lane = threadIdx.x & 63;
+  uint32_t key[NV];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) cnt += v[j] > my || (v[j] == my && 4 * q + j < e);
-    }
-    if (parts == 1) L.rank[r] = cnt;
-    else atomicAdd(&L.rank[r], cnt);   // integers: any order
+  for (int j = 0; j < NV; ++j) key[j] = __float_as_uint(logits[min(lane + 64 * j, E - 1)]);
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+    key[j] = lane + 64 * j < E ? route_ord(__uint_as_float(key[j])) : 0u;
+  uint32_t thr = 0;
+  for (int b = 30; b >= 0; b -= 2) {
+    int n[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int q = 1; q < 4; ++q)
+#pragma unroll
+      for (int j = 0; j < NV; ++j) n[q] += __popcll(__ballot(key[j] >= (thr | ((uint32_t)q << b))));
+    thr |= (n[3] >= k ? 3u : n[2] >= k ? 2u : n[1] >= k ? 1u : 0u) << b;
   }
-  __syncthreads();
-  for (int i = wave; i < a.T * L.W; i += THREADS / 64) {
-    const int t = a.T == 1 ? 0 : i / L.W, e = (i - t * L.W) * 64 + lane;
-    const uint64_t m = __ballot(e < E && L.rank[t * E + min(e, E - 1)] < a.k);
-    if (lane == 0) L.mask[i] = m;
+  int need = k;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) need -= __popcll(__ballot(key[j] > thr));
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    uint64_t m = __ballot(key[j] > thr), eq = __ballot(key[j] == thr);
+    for (; need > 0 && eq; --need) {
+      m |= eq & (0 - eq);
+      eq &= eq - 1;
+    }
+    if (lane == 0 && 64 * j < E) mask[j] = m;
+  }
+}
+
+// Waves 0 .. T-1 of the workgroup route a token each, the others bring the
+// tokens' rows into LDS.
+template <int WV>
+__device__ __forceinline__ void route_and_stage(const MxProj& a, const float* __restrict__ logits,
+                                                bool route, const RouteLds& L) {
+  const int wave = threadIdx.x >> 6;
+  const int first = route ? a.T : 0;
+  if (wave < first) {
+    uint64_t* m = L.mask + wave * L.W;
+    const float* row = logits + wave * a.E;
+    if (a.E <= 128) select_topk<2>(row, a.E, a.k, m);
+    else select_topk<8>(row, a.E, a.k, m);
+  } else {
+    const int n = a.ld_in / 8;   // 16-byte chunks per row
+    for (int t = 0; t < a.T; ++t)
+      for (int i = threadIdx.x - 64 * first; i < n; i += 64 * (WV - first))
+        *reinterpret_cast<mx_u32x4*>(L.x + t * L.pitch + i * 16) =
+            *reinterpret_cast<const mx_u32x4*>(a.x + (size_t)t * a.ld_in + i * 8);
   }
   __syncthreads();
 }
@@ -204,49 +222,65 @@ template <int THREADS>
 __device__ __forceinline__ void write_routing(const MxProj& a, const MxRoute& ro,
                                               const RouteLds& L) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int E = a.E, k = a.k;
-  // pairs of experts before e, and of e by tokens before t
-  auto place = [&](int e, int t) {
-    const uint64_t below = (1ull << (e & 63)) - 1;
-    int o = 0;
-    for (int u = 0; u < a.T; ++u) {
-      for (int w = 0; w < e / 64; ++w) o += __popcll(L.mask[u * L.W + w]);
-      o += __popcll(L.mask[u * L.W + e / 64] & below);
-      if (u < t) o += (int)(L.mask[u * L.W + e / 64] >> (e & 63)) & 1;
-    }
+  const int E = a.E, k = a.k, W = L.W;
+  auto chosen = [&](int t, int e) { return (int)(L.mask[t * W + e / 64] >> (e & 63)) & 1; };
+  // token t's chosen experts below e
+  auto below = [&](int t, int e) {
+    int o = __popcll(L.mask[t * W + e / 64] & ((1ull << (e & 63)) - 1));
+    for (int w = 0; w < e / 64; ++w) o += __popcll(L.mask[t * W + w]);
     return o;
   };
   for (int i = tid; i < a.T * E; i += THREADS) {
-    const int t = i / E, e = i - t * E, r = L.rank[i];
-    if (r < k) {
-      const int p = t * k + r, pos = place(e, t);
+    const int t = i / E, e = i - t * E;
+    if (chosen(t, e)) {
+      const int p = t * k + below(t, e);
       L.ids[p] = e;
-      ro.ids[p] = e;
-      ro.pair_pos[p] = pos;
-      ro.sorted_pair[pos] = p;
+      L.key[p] = route_ord(ro.logits[i]);
     }
   }
   for (int e = tid; e < E; e += THREADS) {
-    int c = 0;
-    for (int u = 0; u < a.T; ++u) c += (int)(L.mask[u * L.W + e / 64] >> (e & 63)) & 1;
+    int c = 0, o = 0;
+    for (int t = 0; t < a.T; ++t) {
+      c += chosen(t, e);
+      o += below(t, e);
+    }
     ro.counts[e] = c;
-    ro.offsets[e] = place(e, 0);
+    ro.offsets[e] = o;
   }
   if (tid == 0) ro.offsets[E] = a.P;
   __syncthreads();
-  // gate weights: one wave per token, choice r in lane r (k <= 64), the sums of
-  // route_group_vals
-  for (int t = wave; t < a.T; t += THREADS / 64) {
-    const float v = lane < k ? route_unord(L.ord[t * L.E4 + L.ids[t * k + lane]]) : 0.0f;
+  // pair tid: the rank of its expert among the token's chosen ones, its place in
+  // the stable sort (smaller experts of every token, the same one of earlier
+  // tokens), and its gate weight
+  const int t = tid / k, i0 = t * k;
+  int e = 0, rank = 0;
+  uint32_t key = 0;
+  if (tid < a.P) {
+    e = L.ids[tid];
+    key = L.key[tid];
+    for (int q = i0; q < i0 + k; ++q) rank += L.key[q] > key || (L.key[q] == key && q < tid);
+    int pos = 0;
+    for (int u = 0; u < a.T; ++u) pos += below(u, e) + (u < t ? chosen(u, e) : 0);
+    const int p = i0 + rank;
+    ro.ids[p] = e;
+    ro.pair_pos[p] = pos;
+    ro.sorted_pair[pos] = p;
+  }
+  __syncthreads();
+  if (tid < a.P) L.key[i0 + rank] = key;   // in order of rank from here on
+  __syncthreads();
+  // one wave per token, choice r in lane r, the sums of route_group_vals
+  for (int u = wave; u < a.T; u += THREADS / 64) {
+    const float v = lane < k ? route_unord(L.key[u * k + lane]) : 0.0f;
     const float top = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 0));
     const float ex = lane < k ? expf(v - top) : 0.0f;
     float sum = ex;
     if (!ro.renorm) {
       sum = 0.0f;
-      for (int e = lane; e < E; e += 64) sum += expf(route_unord(L.ord[t * L.E4 + e]) - top);
+      for (int x = lane; x < E; x += 64) sum += expf(ro.logits[u * E + x] - top);
     }
     const float denom = wave_sum(sum);
-    if (lane < k) ro.w[t * k + lane] = ex / denom;
+    if (lane < k) ro.w[u * k + lane] = ex / denom;
   }
 }
 
@@ -299,6 +333,9 @@ __global__ __launch_bounds__(64 * WV) void mx_rows16_kernel(MxProj a, MxRoute ro
   int e = 0, r0 = 0, r1 = 0;
   int token = -1;   // routed launch: the token of this lane's column
   const int slot = blk / n_ub, ub = blk - slot * n_ub;
+  extern __shared__ __align__(16) unsigned char route_smem[];
+  const RouteLds L(route_smem, ROUTE ? a.T : 0, a.E, ROUTE ? a.ld_in : 0);
+  if constexpr (ROUTE) route_and_stage<WV>(a, ro.logits, blk < 0 || slot >= n_sh_tiles, L);
   if (blk >= 0 && slot < n_sh_tiles) {
     const int per = (a.T + kTM - 1) / kTM;
     is_sh = true;
@@ -306,9 +343,6 @@ __global__ __launch_bounds__(64 * WV) void mx_rows16_kernel(MxProj a, MxRoute ro
     r0 = (slot - e * per) * kTM;
     r1 = min(a.T, r0 + kTM);
   } else if constexpr (ROUTE) {
-    extern __shared__ __align__(16) unsigned char route_smem[];
-    const RouteLds L(route_smem, a.T, a.E);
-    route_masks<64 * WV>(a, ro.logits, L);
     if (blk < 0) {
       write_routing<64 * WV>(a, ro, L);
       return;
@@ -386,7 +420,8 @@ __global__ __launch_bounds__(64 * WV) void mx_rows16_kernel(MxProj a, MxRoute ro
       code_products<NB>(w, sw, x, sx, acc);
     } else {
       mx_u32x4 x[NB][4];
-      const mx_u32x4* px = reinterpret_cast<const mx_u32x4*>(a.x + xrow * a.ld_in);
+      const mx_u32x4* px = ROUTE ? reinterpret_cast<const mx_u32x4*>(L.x + xrow * L.pitch)
+                                 : reinterpret_cast<const mx_u32x4*>(a.x + xrow * a.ld_in);
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
         const int b = 4 * (s + j) + g;
@@ -437,7 +472,7 @@ hipError_t launch(const MxProj& a, const MxRoute& ro, hipStream_t st) {
   if (grid >= (1LL << 31)) return hipErrorInvalidValue;
   const int K = a.n_shared > 0 && a.K_sh > a.K ? a.K_sh : a.K;
   const int pieces = mx_pieces(K);
-  const size_t lds = ROUTE ? RouteLds::bytes(a.T, a.E) : 0;
+  const size_t lds = ROUTE ? RouteLds::bytes(a.T, a.E, a.ld_in) : 0;
   // Up to 64 pairs (a few tokens) eight waves split K, so that each has little
   // to do behind its loads; else four, with longer runs.  The same rule with
   // and without the routing: both sum in the same order.
@@ -641,8 +676,9 @@ hipError_t launch_mx_rows16(const MxProj& a, int mode, int act4, hipStream_t st)
 #undef MX_L
 }
 
-bool mx_route_gateup_ok(int T, int k, int E) {
-  return T <= kRouteT && T * k <= kRouteP && E <= kPermMaxE;
+bool mx_route_gateup_ok(int T, int k, int E, int H) {
+  return T <= kRouteT && T * k <= kRouteP && E <= kPermMaxE &&
+         RouteLds::bytes(T, E, H) <= 40 * 1024;
 }
 
 hipError_t launch_mx_route_gateup(const MxProj& a, int act4, const float* logits, int renorm,
