@@ -14,8 +14,8 @@
 //    that write LDS; rows gathered by token).  A4: 128 bytes of codes per row
 //    and step, chunk q of row m in slot q ^ ((m >> 1) & 7); the scale bytes of
 //    the whole tile are staged once.  A16: 256 bytes of bf16 per row and
-//    sub-step, chunk q in slot q ^ (m & 15).  Both spread the 16 lanes that an
-//    LDS access serves at a time over all banks.
+//    sub-step, chunk q in slot q ^ swizzle16(m).  Both spread the 16 lanes that
+//    an LDS access serves at a time over all banks.
 //  * A4 feeds codes and scales to the scaled 16x16x128 instruction; A16
 //    expands a fragment's 8 codes to bf16 by four conversions (exact) for one
 //    16x16x32 step against every row fragment.
@@ -57,6 +57,14 @@ template <int N>
 struct Int {
   static constexpr int value = N;
 };
+
+// A16: chunk q of row m of a stage lies in slot q ^ swizzle16(m) of its 16.  A
+// 128-bit LDS access serves 16 lanes at a time, but not 16 in a row: lanes 0-3
+// and 12-15 of one quarter of the wave go with 4-11 of the next, so the two
+// quarters (chunks 4g + q and 4g + 4 + q) have to differ in the low two bits
+// for those rows.  (With slot q ^ (m & 15) half of the LDS cycles were
+// conflicts.)
+__device__ __forceinline__ int swizzle16(int m) { return ((m & 3) << 2) | ((m >> 2) & 3); }
 
 struct GemmArgs {
   MxProj p;
@@ -142,7 +150,7 @@ __device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, __amdgpu
     if (ACT4) {
       aoff[i] = tok[m] * t.row_bytes + (((q & 7) ^ ((m >> 1) & 7)) * 16);
     } else {
-      aoff[i] = tok[m] * t.row_bytes + (((q & 15) ^ (m & 15)) * 16);
+      aoff[i] = tok[m] * t.row_bytes + (((q & 15) ^ swizzle16(m)) * 16);
     }
   }
   auto dma = [&](int sg, int buf) {
@@ -170,7 +178,7 @@ __device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, __amdgpu
   // the stage's one barrier stands there: it frees the buffer for the stage
   // kBufs on, and covers the next stage's loads, which the last sub-step reads.
   constexpr int kQ = ACT4 ? 2 : 4;
-  const int sw = ACT4 ? (c >> 1) & 7 : c;
+  const int sw = ACT4 ? (c >> 1) & 7 : swizzle16(c);
   const u32x4* Ac = As + c * R::kRowChunks;
   u32x4 x[MT];
   mx_bf16x8 wv[2][kNF];
@@ -485,7 +493,9 @@ void mx_gemm_kernel(GemmArgs ga) {
   if (mt <= 2) MX_BODY(2);
   else if (mt <= 4) MX_BODY(4);
   else if (mt <= 6) MX_BODY(6);
-  else if (mt <= 8) MX_BODY(8);
+  else if (mt == 7) MX_BODY(7);
+  else if (mt == 8) MX_BODY(8);
+  else if (mt == 9) MX_BODY(9);
   else MX_BODY(10);
 #undef MX_BODY
 }
