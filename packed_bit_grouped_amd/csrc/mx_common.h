@@ -74,6 +74,14 @@ __device__ __forceinline__ uint32_t mx_bf16(float f) {
   return __builtin_bit_cast(uint16_t, (__bf16)f);
 }
 
+// SiLU(g) * u with the hardware's exp2 and reciprocal: a few units of fp32 of
+// relative error (|g| of them in the exponential where SiLU is tiny), far below
+// the rounding to bf16 behind it; 8 instructions instead of about 40.
+__device__ __forceinline__ float mx_silu_mul(float g, float u) {
+  const float e = __builtin_amdgcn_exp2f(-1.4426950408889634f * g);
+  return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
+}
+
 // Scale byte of a block from its largest magnitude (as fp32 bits without the
 // sign): floor(log2 a) - 2, held above -127; 255 when a is inf or NaN.
 __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax_bits) {
@@ -144,8 +152,9 @@ struct MxTiles {
       if (lane >= d) pre += v;
     }
   }
-  // Tile j: its expert and rows; false past the last.
-  __device__ __forceinline__ bool find(int j, int& e, int& r0, int& r1) const {
+  // Tile j: its expert, the expert's rows, and which of its tiles it is; false
+  // past the last.
+  __device__ __forceinline__ bool find(int j, int& e, int& first, int& end, int& k) const {
     const uint64_t past = __ballot(pre > j);
     if (past == 0) return false;
     const int owner = __builtin_ctzll(past);
@@ -156,11 +165,20 @@ struct MxTiles {
       const int nt = (h - l + TM - 1) / TM;
       if (left >= 0 && left < nt) {
         e = owner * PER + i;
-        r0 = l + left * TM;
-        r1 = min(h, r0 + TM);
+        first = l;
+        end = h;
+        k = left;
       }
       left -= nt;
     }
+    return true;
+  }
+  // The same as rows [r0, r1) of full tiles.
+  __device__ __forceinline__ bool find(int j, int& e, int& r0, int& r1) const {
+    int l, h, k;
+    if (!find(j, e, l, h, k)) return false;
+    r0 = l + k * TM;
+    r1 = min(h, r0 + TM);
     return true;
   }
 };

@@ -68,7 +68,7 @@ __device__ __forceinline__ int swizzle16(int m) { return ((m & 3) << 2) | ((m >>
 
 struct GemmArgs {
   MxProj p;
-  int KP, KP_sh;       // K padded to whole steps: row lengths of the activation copy
+  int KP;              // row length of the activation copy
   int n_ub;            // workgroups per tile
   int max_tiles;       // host bound of the routed tiles
   int sh_per;          // tiles per shared expert
@@ -100,10 +100,57 @@ struct Tile {
   int orow;             // first output row
 };
 
+// The wave's weights: four 16-row blocks; blocks past the end lie past the
+// buffer, where nothing is read.
+constexpr int kNone = 0x40000000;
+constexpr int nS = kNF;
+constexpr int nW = 2 * kNF + nS;   // weight loads per step
+
+struct Weights {
+  __amdgpu_buffer_rsrc_t crs, srs;
+  int coff[kNF], soff[kNF], n_st;
+
+  template <int MODE>
+  __device__ __forceinline__ void init(const Tile& t, const uint8_t* w, const uint8_t* ws, int e) {
+    const int lane = threadIdx.x & 63;
+    const int N = MODE == 0 ? 2 * t.U : t.U;
+    const size_t cb = mx_code_bytes(N, t.K), sb = mx_scale_bytes(N, t.K);
+    crs = make_rsrc(w + e * cb, (uint32_t)cb);
+    srs = make_rsrc(ws + e * sb, (uint32_t)sb);
+    n_st = t.n_st;
+    const int pieces = mx_pieces(t.K), words = (pieces + 3) / 4;
+#pragma unroll
+    for (int f = 0; f < kNF; ++f) {
+      const int u = MODE == 0 ? t.u0 + 16 * (f & 1) : t.u0 + 16 * f;
+      const int rb = ((MODE == 0 && f >= 2 ? t.U : 0) + u) / 16;
+      coff[f] = u < t.U ? rb * pieces * 1024 + lane * 16 : kNone;
+      soff[f] = u < t.U ? rb * words * 256 + lane * 4 : kNone;
+    }
+  }
+  __device__ __forceinline__ void load_c(int st, int j, WStep& w) const {
+    const int o = st < n_st ? st * 2048 + j * 1024 : kNone;
+#pragma unroll
+    for (int f = 0; f < kNF; ++f)
+      w.c[f][j] = __builtin_amdgcn_raw_buffer_load_b128(crs, coff[f] + o, 0, 2);
+  }
+  __device__ __forceinline__ void load_s(int st, WStep& w) const {
+    const int o = st < n_st ? (st >> 1) * 256 + (st & 1) * 2 : kNone;
+#pragma unroll
+    for (int f = 0; f < kNF; ++f)
+      w.s[f] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(srs, soff[f] + o, 0, 0);
+  }
+  __device__ __forceinline__ void load(int st, WStep& w) const {
+    load_c(st, 0, w);
+    load_c(st, 1, w);
+    load_s(st, w);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+};
+
+// w0: the weights of the first step, already on their way.
 template <int MODE, bool ACT4, int MT>
-__device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, __amdgpu_buffer_rsrc_t crs,
-                                     __amdgpu_buffer_rsrc_t srs, u32x4* As, const int* tok,
-                                     const uint8_t* sc, int nrows) {
+__device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, const Weights& wt, WStep& w0,
+                                     u32x4* As, const int* tok, const uint8_t* sc, int nrows) {
   using R = Ring<ACT4>;
   constexpr int kBuf = R::buf_chunks(MT);
   constexpr int nA = kBuf / 256;               // activation loads per wave and stage
@@ -112,32 +159,8 @@ __device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, __amdgpu
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int n_st = t.n_st, n_stage = n_st * R::kStages;
-
-  // ---- 16-row blocks of this wave; blocks past the end lie past the buffer
-  const int pieces = mx_pieces(t.K), words = (pieces + 3) / 4;
-  int coff[kNF], soff[kNF];
-#pragma unroll
-  for (int f = 0; f < kNF; ++f) {
-    const int u = MODE == 0 ? t.u0 + 16 * (f & 1) : t.u0 + 16 * f;
-    const int rb = ((MODE == 0 && f >= 2 ? t.U : 0) + u) / 16;
-    coff[f] = u < t.U ? rb * pieces * 1024 + lane * 16 : 0x40000000;
-    soff[f] = u < t.U ? rb * words * 256 + lane * 4 : 0x40000000;
-  }
-
-  auto load_c = [&](int st, int j, WStep& w) {
-    const int o = st < n_st ? st * 2048 + j * 1024 : 0x40000000;   // past the end: nothing is read
-#pragma unroll
-    for (int f = 0; f < kNF; ++f)
-      w.c[f][j] = __builtin_amdgcn_raw_buffer_load_b128(crs, coff[f] + o, 0, 2);
-  };
-  auto load_s = [&](int st, WStep& w) {
-    const int o = st < n_st ? (st >> 1) * 256 + (st & 1) * 2 : 0x40000000;
-#pragma unroll
-    for (int f = 0; f < kNF; ++f)
-      w.s[f] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(srs, soff[f] + o, 0, 0);
-  };
-  constexpr int nS = kNF;
-  constexpr int nW = 2 * kNF + nS;             // weight loads per step
+  auto load_c = [&](int st, int j, WStep& w) { wt.load_c(st, j, w); };
+  auto load_s = [&](int st, WStep& w) { wt.load_s(st, w); };
 
   // ---- activation pieces of this lane: LDS slot q of a stage holds the chunk
   // that the swizzle puts there
@@ -288,31 +311,23 @@ __device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, __amdgpu
     if constexpr (!ACT4) stage(st, 1, w, wn);
   };
 
-  // Prologue.  A16 loads its third stage before the second step's weights,
-  // so that kAfter holds in the first stages too.
-  WStep w0, w1, w2;
-  auto load_w = [&](int st, WStep& w) {
-    load_c(st, 0, w);
-    load_c(st, 1, w);
-    load_s(st, w);
-    __builtin_amdgcn_sched_barrier(0);
-  };
+  // Prologue: the loads in an order for which kAfter holds in the first stages
+  // too (the first step's weights went before).
+  WStep w1, w2;
   dma(0, 0);
-  __builtin_amdgcn_sched_barrier(0);
-  load_w(0, w0);
   dma(1, 1);
   __builtin_amdgcn_sched_barrier(0);
   if constexpr (ACT4) {
-    load_w(1, w1);
+    wt.load(1, w1);
     dma(2, 2);
     __builtin_amdgcn_sched_barrier(0);
-    load_w(2, w2);
+    wt.load(2, w2);
   } else {
     dma(2, 2);
     __builtin_amdgcn_sched_barrier(0);
-    load_w(1, w1);
+    wt.load(1, w1);
   }
-  vm_barrier<2 * nA + kD * nW>();   // stage 0 is in LDS
+  vm_barrier<2 * nA + (kD - 1) * nW>();   // stage 0 (and the scales) in LDS
   {
     const u32x4* p = x_at(0, 0);
 #pragma unroll
@@ -327,16 +342,25 @@ __device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, __amdgpu
     }
   }
 
+  // Whole turns of the ring, then the steps that are left (a condition inside
+  // the turn would keep two sets of accumulators alive).  The weight loads of
+  // those last steps have no reader and may be dropped: the barriers that count
+  // them are the first of the rest, whose loads went out in the turns before,
+  // and the last, which nothing needs to wait for.
+  int base = 0;
 #pragma unroll 1
-  for (int base = 0; base < n_st; base += kD) {
+  for (; base + kD <= n_st; base += kD) {
     step(base, w0, w1);
     if constexpr (ACT4) {
-      if (base + 1 < n_st) step(base + 1, w1, w2);
-      if (base + 2 < n_st) step(base + 2, w2, w0);
+      step(base + 1, w1, w2);
+      step(base + 2, w2, w0);
     } else {
-      if (base + 1 < n_st) step(base + 1, w1, w0);
+      step(base + 1, w1, w0);
     }
   }
+  if (base < n_st) step(base, w0, w1);
+  if constexpr (ACT4)
+    if (base + 1 < n_st) step(base + 1, w1, w2);
   __builtin_amdgcn_s_waitcnt(0);   // nothing writes LDS after this
 
   // ---- lane: row 16 m + c, four consecutive units of every fragment
@@ -354,7 +378,7 @@ __device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, __amdgpu
         if (u >= t.U) continue;
         uint32_t v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = mx_bf16(silu_mul(acc[f][m][i], acc[f + 2][m][i]));
+        for (int i = 0; i < 4; ++i) v[i] = mx_bf16(mx_silu_mul(acc[f][m][i], acc[f + 2][m][i]));
         *reinterpret_cast<uint2*>(h + u) = make_uint2(v[0] | (v[1] << 16), v[2] | (v[3] << 16));
       }
     } else {
@@ -362,15 +386,45 @@ __device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, __amdgpu
 #pragma unroll
       for (int f = 0; f < kNF; ++f) {
         const int u = t.u0 + 16 * f + 4 * g;
-        if (u < t.U) __builtin_nontemporal_store(acc[f][m], reinterpret_cast<mx_f32x4*>(y + u));
+        if (u < t.U) *reinterpret_cast<mx_f32x4*>(y + u) = acc[f][m];
       }
     }
   }
 }
 
-// Tile j of the routed rows: an expert with n rows has ceil(n / 160) tiles of
-// even size.  Every wave scans the offsets (lanes count 1..8 experts each).
-__device__ __forceinline__ int tiles_of(int n) { return (n + kRowsMax - 1) / kRowsMax; }
+// Routed rows: an expert with n rows has ceil(n / 160) tiles of even size.
+__device__ __forceinline__ void cut(int first, int end, int n, int k, int& r0, int& r1) {
+  const int rows = ((end - first + n - 1) / n + 15) & ~15;
+  r0 = min(first + k * rows, end);
+  r1 = min(r0 + rows, end);
+}
+
+template <int PER>
+__device__ __forceinline__ bool pick_tile(const GemmArgs& ga, bool& is_sh, int& e, int& r0, int& r1,
+                                          int& ub) {
+  const MxProj& a = ga.p;
+  MxTiles<kRowsMax, PER> tl;
+  tl.load(a.offsets, a.E, a.P);
+  const int n_sh = a.n_shared * ga.sh_per;
+  const int n_slots = n_sh + min(__builtin_amdgcn_readlane(tl.pre, 63), ga.max_tiles);
+  // XCD blockIdx % 8 takes a contiguous range of tiles: the workgroups of one
+  // tile share its activation rows in one L2, the tiles of one expert its weights
+  const int b = blockIdx.x, xcd = b % kXcd, li = b / kXcd;
+  const int per_xcd = (n_slots + kXcd - 1) / kXcd;
+  const int local = li / ga.n_ub, slot = xcd * per_xcd + local;
+  ub = li - local * ga.n_ub;
+  if (local >= per_xcd || slot >= n_slots) return false;
+  is_sh = slot < n_sh;
+  if (is_sh) {
+    e = slot / ga.sh_per;
+    cut(0, a.T, ga.sh_per, slot - e * ga.sh_per, r0, r1);
+    return r0 < r1;
+  }
+  int first, end, k;
+  if (!tl.find(slot - n_sh, e, first, end, k)) return false;
+  cut(first, end, (end - first + kRowsMax - 1) / kRowsMax, k, r0, r1);
+  return r0 < r1;
+}
 
 template <int MODE, bool ACT4>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
@@ -381,67 +435,15 @@ void mx_gemm_kernel(GemmArgs ga) {
   u32x4* As = reinterpret_cast<u32x4*>(smem + kRowsMax * 4);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-
-  // ---- all tiles: the shared experts', then the routed ones
-  const int per = (a.E + 63) / 64;
-  int cnt = 0;
-  for (int i = 0; i < per; ++i) {
-    const int ex = lane * per + i;
-    if (ex < a.E) cnt += tiles_of(max(min(a.offsets[ex + 1], a.P) - max(a.offsets[ex], 0), 0));
-  }
-  int pre = cnt;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int o = __shfl_up(pre, d);
-    if (lane >= d) pre += o;
-  }
-  const int n_sh = a.n_shared * ga.sh_per;
-  const int n_slots = n_sh + min(__builtin_amdgcn_readlane(pre, 63), ga.max_tiles);
-  // XCD blockIdx % 8 takes a contiguous range of tiles: the workgroups of one
-  // tile share its activation rows in one L2, the tiles of one expert its weights
-  const int b = blockIdx.x, xcd = b % kXcd, li = b / kXcd;
-  const int per_xcd = (n_slots + kXcd - 1) / kXcd;
-  const int local = li / ga.n_ub, ub = li - local * ga.n_ub;
-  const int slot = xcd * per_xcd + local;
-  if (local >= per_xcd || slot >= n_slots) return;
-
-  bool is_sh = false;
-  int e = 0, r0 = 0, r1 = 0;
-  if (slot < n_sh) {
-    is_sh = true;
-    e = slot / ga.sh_per;
-    const int ti = slot - e * ga.sh_per;
-    const int rows = ((a.T + ga.sh_per - 1) / ga.sh_per + 15) & ~15;
-    r0 = min(ti * rows, a.T);
-    r1 = min(r0 + rows, a.T);
-  } else {
-    const int j = slot - n_sh;
-    const uint64_t past = __ballot(pre > j);
-    if (past == 0) return;
-    const int owner = __builtin_ctzll(past);
-    int left = j - (__builtin_amdgcn_readlane(pre, owner) - __builtin_amdgcn_readlane(cnt, owner));
-    for (int i = 0; i < per; ++i) {
-      const int ex = owner * per + i;
-      if (ex >= a.E) break;
-      const int lo = max(a.offsets[ex], 0), hi = min(a.offsets[ex + 1], a.P);
-      const int nt = tiles_of(max(hi - lo, 0));
-      if (left < nt) {
-        e = ex;
-        const int rows = ((hi - lo + nt - 1) / nt + 15) & ~15;
-        r0 = min(lo + left * rows, hi);
-        r1 = min(r0 + rows, hi);
-        break;
-      }
-      left -= nt;
-    }
-  }
+  bool is_sh;
+  int e, r0, r1, ub;
+  if (!(a.E <= 128 ? pick_tile<2>(ga, is_sh, e, r0, r1, ub) : pick_tile<8>(ga, is_sh, e, r0, r1, ub)))
+    return;
   const int nrows = r1 - r0;
-  if (nrows <= 0) return;
 
   Tile t;
   t.K = is_sh ? a.K_sh : a.K;
   t.U = is_sh ? a.U_sh : a.U;
-  const int KP = is_sh ? ga.KP_sh : ga.KP;
   t.n_st = (t.K + kKS - 1) / kKS;
   const int ublk = ub * (MODE == 0 ? 128 : 256);
   if (ublk >= t.U) return;
@@ -455,10 +457,12 @@ void mx_gemm_kernel(GemmArgs ga) {
   t.act = (ACT4 ? a.q : reinterpret_cast<const uint8_t*>(a.x)) + arow * stride;
   const int act_rows = MODE == 0 ? a.T : (is_sh ? a.n_shared * a.T : a.P);
   t.act_bytes = (uint32_t)(act_rows * stride);
-  const int N = MODE == 0 ? 2 * t.U : t.U;
-  const size_t cb = mx_code_bytes(N, t.K), sb = mx_scale_bytes(N, t.K);
-  const __amdgpu_buffer_rsrc_t crs = make_rsrc((is_sh ? a.w_sh : a.w) + e * cb, (uint32_t)cb);
-  const __amdgpu_buffer_rsrc_t srs = make_rsrc((is_sh ? a.ws_sh : a.ws) + e * sb, (uint32_t)sb);
+  // the first step's weights need only the tile: on their way before its rows
+  // are looked up
+  Weights wt;
+  wt.init<MODE>(t, is_sh ? a.w_sh : a.w, is_sh ? a.ws_sh : a.ws, e);
+  WStep w0;
+  wt.load(0, w0);
 
   if (tid < kRowsMax) {
     const int m = tid < nrows ? tid : 0;   // padding rows repeat row 0 (not stored)
@@ -477,19 +481,23 @@ void mx_gemm_kernel(GemmArgs ga) {
   const int mt = (nrows + 15) / 16;
   uint8_t* sc = nullptr;
   if (ACT4) {
-    // the tile's scale bytes, rows ga.sc_pitch apart (4 bytes more than the
-    // row: 16 rows' words then lie on different banks)
+    // the tile's scale bytes, by loads that write LDS, ahead of every activation
+    // load: rows of an odd number of 16-byte chunks, so that 16 rows' words lie
+    // on different banks (an even number is followed by a chunk that is not read)
     sc = smem + kRowsMax * 4 + Ring<true>::kBufs * Ring<true>::buf_chunks(10) * 16;
-    const uint8_t* src = a.s + (size_t)arow * (ga.KP / kMxBlock);
-    const int words = KP / kMxBlock / 4;
-    const int rows = mt * 16;
-    for (int i = tid; i < rows * words; i += kThreads) {
-      const int m = i / words, q = i - m * words;
-      *reinterpret_cast<uint32_t*>(sc + m * ga.sc_pitch + q * 4) =
-          *reinterpret_cast<const uint32_t*>(src + (size_t)tok[m] * (ga.KP / kMxBlock) + q * 4);
+    const int row = ga.KP / kMxBlock, chunks = ga.sc_pitch / 16;
+    const __amdgpu_buffer_rsrc_t rs =
+        make_rsrc(a.s + (size_t)arow * row, (uint32_t)((size_t)act_rows * row));
+    const int n = mt * 16 * chunks;
+    for (int i = wave * 64; i < n; i += kThreads) {
+      const int q = min(i + lane, n - 1), m = q / chunks, ch = min(q - m * chunks, row / 16 - 1);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rs, (__attribute__((address_space(3))) void*)(sc + i * 16), 16, tok[m] * row + ch * 16, 0, 0,
+          0);
     }
+    __builtin_amdgcn_sched_barrier(0);
   }
-#define MX_BODY(MT) body<MODE, ACT4, MT>(ga, t, crs, srs, As, tok, sc, nrows)
+#define MX_BODY(MT) body<MODE, ACT4, MT>(ga, t, wt, w0, As, tok, sc, nrows)
   if (mt <= 2) MX_BODY(2);
   else if (mt <= 4) MX_BODY(4);
   else if (mt <= 6) MX_BODY(6);
@@ -506,10 +514,12 @@ hipError_t launch(const GemmArgs& ga, size_t lds, long long grid, hipStream_t st
   return hipGetLastError();
 }
 
+int sc_pitch(int KP) { return (KP / kMxBlock) | 16; }   // KP / 32 is a multiple of 16
+
 size_t lds_bytes(bool act4, int KP) {
   const size_t ring = act4 ? (size_t)Ring<true>::kBufs * Ring<true>::buf_chunks(10) * 16
                            : (size_t)Ring<false>::kBufs * Ring<false>::buf_chunks(10) * 16;
-  return kRowsMax * 4 + ring + (act4 ? (size_t)kRowsMax * (KP / kMxBlock + 4) : 0);
+  return kRowsMax * 4 + ring + (act4 ? (size_t)kRowsMax * sc_pitch(KP) + 1024 : 0);
 }
 
 }  // namespace
@@ -527,13 +537,12 @@ hipError_t launch_mx_gemm(const MxProj& a, int mode, int act4, hipStream_t st) {
   GemmArgs ga;
   ga.p = a;
   ga.KP = mx_pad_k(a.ld_in);   // row length of the activation copy
-  ga.KP_sh = ga.KP;
   ga.sh_per = (a.T + kRowsMax - 1) / kRowsMax;
   ga.max_tiles = moe_permute_max_tiles(a.T, a.k, a.E, kRowsMax);
   const int step = mode == 0 ? 128 : 256;
   const int U = a.n_shared > 0 && a.U_sh > a.U ? a.U_sh : a.U;
   ga.n_ub = (U + step - 1) / step;
-  ga.sc_pitch = ga.KP / kMxBlock + 4;
+  ga.sc_pitch = sc_pitch(ga.KP);
   const long long slots = (long long)a.n_shared * ga.sh_per + ga.max_tiles;
   const long long grid = (slots + kXcd - 1) / kXcd * kXcd * ga.n_ub;
   if (grid >= (1LL << 31)) return hipErrorInvalidValue;
