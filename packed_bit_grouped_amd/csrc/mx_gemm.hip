@@ -70,7 +70,6 @@ struct GemmArgs {
   MxProj p;
   int KP;              // row length of the activation copy
   int n_ub;            // workgroups per tile
-  int n_blk;           // blocks of 128 units (256 rows) per workgroup
   int max_tiles;       // host bound of the routed tiles
   int sh_per;          // tiles per shared expert
   int sc_pitch;        // A4: LDS bytes per row of scales
@@ -147,40 +146,6 @@ struct Weights {
     __builtin_amdgcn_sched_barrier(0);
   }
 };
-
-// Results of a wave's four fragments; lane: row 16 m + c, four consecutive units
-// of each.
-template <int MODE, int MT>
-__device__ __forceinline__ void store(const GemmArgs& ga, const Tile& t, mx_f32x4 (&acc)[kNF][MT],
-                                      int nrows) {
-  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int row = 16 * m + c;
-#pragma unroll
-    for (int f = 0; f < kNF; ++f) mx_keep(acc[f][m]);
-    if (row >= nrows) continue;
-    if (MODE == 0) {
-      uint16_t* h = static_cast<uint16_t*>(ga.p.out) + (size_t)(t.orow + row) * ga.p.ld_out;
-#pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        const int u = t.u0 + 16 * f + 4 * g;
-        if (u >= t.U) continue;
-        uint32_t v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = mx_bf16(mx_silu_mul(acc[f][m][i], acc[f + 2][m][i]));
-        *reinterpret_cast<uint2*>(h + u) = make_uint2(v[0] | (v[1] << 16), v[2] | (v[3] << 16));
-      }
-    } else {
-      float* y = static_cast<float*>(ga.p.out) + (size_t)(t.orow + row) * ga.p.ld_out;
-#pragma unroll
-      for (int f = 0; f < kNF; ++f) {
-        const int u = t.u0 + 16 * f + 4 * g;
-        if (u < t.U) *reinterpret_cast<mx_f32x4*>(y + u) = acc[f][m];
-      }
-    }
-  }
-}
 
 // w0: the weights of the first step, already on their way.
 template <int MODE, bool ACT4, int MT>
@@ -398,21 +363,47 @@ __device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, const We
     if (base + 1 < n_st) step(base + 1, w1, w2);
   __builtin_amdgcn_s_waitcnt(0);   // nothing writes LDS after this
 
-  store<MODE, MT>(ga, t, acc, nrows);
+  // ---- lane: row 16 m + c, four consecutive units of every fragment
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int row = 16 * m + c;
+#pragma unroll
+    for (int f = 0; f < kNF; ++f) mx_keep(acc[f][m]);
+    if (row >= nrows) continue;
+    if (MODE == 0) {
+      uint16_t* h = static_cast<uint16_t*>(ga.p.out) + (size_t)(t.orow + row) * ga.p.ld_out;
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const int u = t.u0 + 16 * f + 4 * g;
+        if (u >= t.U) continue;
+        uint32_t v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = mx_bf16(mx_silu_mul(acc[f][m][i], acc[f + 2][m][i]));
+        *reinterpret_cast<uint2*>(h + u) = make_uint2(v[0] | (v[1] << 16), v[2] | (v[3] << 16));
+      }
+    } else {
+      float* y = static_cast<float*>(ga.p.out) + (size_t)(t.orow + row) * ga.p.ld_out;
+#pragma unroll
+      for (int f = 0; f < kNF; ++f) {
+        const int u = t.u0 + 16 * f + 4 * g;
+        if (u < t.U) *reinterpret_cast<mx_f32x4*>(y + u) = acc[f][m];
+      }
+    }
+  }
 }
 
-// Routed rows: an expert with n rows has ceil(n / TM) tiles of even size.
+// Routed rows: an expert with n rows has ceil(n / 160) tiles of even size.
 __device__ __forceinline__ void cut(int first, int end, int n, int k, int& r0, int& r1) {
   const int rows = ((end - first + n - 1) / n + 15) & ~15;
   r0 = min(first + k * rows, end);
   r1 = min(r0 + rows, end);
 }
 
-template <int TM, int PER>
+template <int PER>
 __device__ __forceinline__ bool pick_tile(const GemmArgs& ga, bool& is_sh, int& e, int& r0, int& r1,
                                           int& ub) {
   const MxProj& a = ga.p;
-  MxTiles<TM, PER> tl;
+  MxTiles<kRowsMax, PER> tl;
   tl.load(a.offsets, a.E, a.P);
   const int n_sh = a.n_shared * ga.sh_per;
   const int n_slots = n_sh + min(__builtin_amdgcn_readlane(tl.pre, 63), ga.max_tiles);
@@ -431,42 +422,48 @@ __device__ __forceinline__ bool pick_tile(const GemmArgs& ga, bool& is_sh, int& 
   }
   int first, end, k;
   if (!tl.find(slot - n_sh, e, first, end, k)) return false;
-  cut(first, end, (end - first + TM - 1) / TM, k, r0, r1);
+  cut(first, end, (end - first + kRowsMax - 1) / kRowsMax, k, r0, r1);
   return r0 < r1;
 }
 
-// What both kernels do first: the tile, its first weights, its rows.
-template <int MODE, bool ACT4, int TM>
-__device__ __forceinline__ bool set_up(const GemmArgs& ga, Tile& t, Weights& wt, WStep& w0, int* tok,
-                                       int& nrows, int& arow, int& act_rows) {
+template <int MODE, bool ACT4>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void mx_gemm_kernel(GemmArgs ga) {
+  extern __shared__ __align__(16) unsigned char smem[];
   const MxProj& a = ga.p;
-  const int tid = threadIdx.x;
+  int* tok = reinterpret_cast<int*>(smem);                   // [kRowsMax]
+  u32x4* As = reinterpret_cast<u32x4*>(smem + kRowsMax * 4);
+  const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   bool is_sh;
   int e, r0, r1, ub;
-  if (!(a.E <= 128 ? pick_tile<TM, 2>(ga, is_sh, e, r0, r1, ub)
-                   : pick_tile<TM, 8>(ga, is_sh, e, r0, r1, ub)))
-    return false;
-  nrows = r1 - r0;
+  if (!(a.E <= 128 ? pick_tile<2>(ga, is_sh, e, r0, r1, ub) : pick_tile<8>(ga, is_sh, e, r0, r1, ub)))
+    return;
+  const int nrows = r1 - r0;
+
+  Tile t;
   t.K = is_sh ? a.K_sh : a.K;
   t.U = is_sh ? a.U_sh : a.U;
   t.n_st = (t.K + kKS - 1) / kKS;
-  const int ublk = ub * ga.n_blk * (MODE == 0 ? 128 : 256);
-  if (ublk >= t.U) return false;
+  const int ublk = ub * (MODE == 0 ? 128 : 256);
+  if (ublk >= t.U) return;
   t.u0 = ublk + wave * (MODE == 0 ? 32 : 64);
   t.orow = is_sh ? a.P + e * a.T + r0 : r0;
   // gate/up gathers rows of x by token; down reads its own rows, the shared
   // experts' behind the routed ones
-  arow = MODE == 0 ? 0 : (is_sh ? a.P : 0);
+  const int arow = MODE == 0 ? 0 : (is_sh ? a.P : 0);
   const size_t stride = ACT4 ? (size_t)ga.KP / 2 : (size_t)a.ld_in * 2;
   t.row_bytes = (int)stride;
   t.act = (ACT4 ? a.q : reinterpret_cast<const uint8_t*>(a.x)) + arow * stride;
-  act_rows = MODE == 0 ? a.T : (is_sh ? a.n_shared * a.T : a.P);
+  const int act_rows = MODE == 0 ? a.T : (is_sh ? a.n_shared * a.T : a.P);
   t.act_bytes = (uint32_t)(act_rows * stride);
   // the first step's weights need only the tile: on their way before its rows
   // are looked up
+  Weights wt;
   wt.init<MODE>(t, is_sh ? a.w_sh : a.w, is_sh ? a.ws_sh : a.ws, e);
+  WStep w0;
   wt.load(0, w0);
+
   if (tid < kRowsMax) {
     const int m = tid < nrows ? tid : 0;   // padding rows repeat row 0 (not stored)
     int row;
@@ -481,44 +478,24 @@ __device__ __forceinline__ bool set_up(const GemmArgs& ga, Tile& t, Weights& wt,
     tok[tid] = row;
   }
   __syncthreads();
-  return true;
-}
-
-// A4: the tile's scale bytes to sc by loads that write LDS, ahead of every
-// activation load: rows of an odd number of 16-byte chunks, so that 16 rows'
-// words lie on different banks (an even number is followed by one not used).
-__device__ __forceinline__ void stage_scales(const GemmArgs& ga, const int* tok, uint8_t* sc,
-                                             int rows, int arow, int act_rows) {
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int row = ga.KP / kMxBlock, chunks = ga.sc_pitch / 16;
-  const __amdgpu_buffer_rsrc_t rs =
-      make_rsrc(ga.p.s + (size_t)arow * row, (uint32_t)((size_t)act_rows * row));
-  const int n = rows * chunks;
-  for (int i = wave * 64; i < n; i += kThreads) {
-    const int q = min(i + lane, n - 1), m = q / chunks, ch = min(q - m * chunks, row / 16 - 1);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        rs, (__attribute__((address_space(3))) void*)(sc + i * 16), 16, tok[m] * row + ch * 16, 0, 0, 0);
-  }
-  __builtin_amdgcn_sched_barrier(0);
-}
-
-template <int MODE, bool ACT4>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
-void mx_gemm_kernel(GemmArgs ga) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  int* tok = reinterpret_cast<int*>(smem);                   // [kRowsMax]
-  u32x4* As = reinterpret_cast<u32x4*>(smem + kRowsMax * 4);
-  Tile t;
-  Weights wt;
-  WStep w0;
-  int nrows, arow, act_rows;
-  if (!set_up<MODE, ACT4, kRowsMax>(ga, t, wt, w0, tok, nrows, arow, act_rows)) return;
   const int mt = (nrows + 15) / 16;
   uint8_t* sc = nullptr;
   if (ACT4) {
+    // the tile's scale bytes, by loads that write LDS, ahead of every activation
+    // load: rows of an odd number of 16-byte chunks, so that 16 rows' words lie
+    // on different banks (an even number is followed by a chunk that is not read)
     sc = smem + kRowsMax * 4 + Ring<true>::kBufs * Ring<true>::buf_chunks(10) * 16;
-    stage_scales(ga, tok, sc, mt * 16, arow, act_rows);
+    const int row = ga.KP / kMxBlock, chunks = ga.sc_pitch / 16;
+    const __amdgpu_buffer_rsrc_t rs =
+        make_rsrc(a.s + (size_t)arow * row, (uint32_t)((size_t)act_rows * row));
+    const int n = mt * 16 * chunks;
+    for (int i = wave * 64; i < n; i += kThreads) {
+      const int q = min(i + lane, n - 1), m = q / chunks, ch = min(q - m * chunks, row / 16 - 1);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rs, (__attribute__((address_space(3))) void*)(sc + i * 16), 16, tok[m] * row + ch * 16, 0, 0,
+          0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
   }
 #define MX_BODY(MT) body<MODE, ACT4, MT>(ga, t, wt, w0, As, tok, sc, nrows)
   if (mt <= 2) MX_BODY(2);
@@ -528,167 +505,6 @@ void mx_gemm_kernel(GemmArgs ga) {
   else if (mt == 8) MX_BODY(8);
   else if (mt == 9) MX_BODY(9);
   else MX_BODY(10);
-#undef MX_BODY
-}
-
-// ---------------------------------------------------------------------
-// A4 with rows short enough that a tile's codes stay in LDS whole (K up to 2048:
-// 128 to 160 rows): a workgroup stages them once and then walks several blocks
-// of weight rows.  The activations pass once per walk instead of once per
-// block, the waves need no barrier any more, and the weight ring runs on from
-// block to block, so nothing waits between them.
-// (TM only makes the kernels' bodies distinct functions.)
-template <int MODE, int MT, int D, int TM>
-__device__ __forceinline__ void body_res(const GemmArgs& ga, Tile& t, const Weights& wt, WStep& w0,
-                                         u32x4* As, const int* tok, const uint8_t* sc, int nrows) {
-  constexpr int kBuf = Ring<true>::buf_chunks(MT);
-  constexpr int nA = kBuf / 256;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int c = lane & 15, g = lane >> 4;
-  const int n_st = t.n_st;
-  const int left = (t.U - (t.u0 - wave * (MODE == 0 ? 32 : 64)) + (MODE == 0 ? 127 : 255)) /
-                   (MODE == 0 ? 128 : 256);
-  const int n_blk = min(ga.n_blk, left);
-  const int cblk = (MODE == 0 ? 8 : 16) * mx_pieces(t.K) * 1024;              // bytes per block
-  const int sblk = (MODE == 0 ? 8 : 16) * ((mx_pieces(t.K) + 3) / 4) * 256;
-
-  const __amdgpu_buffer_rsrc_t ars = make_rsrc(t.act, t.act_bytes);
-  int aoff[nA];
-#pragma unroll
-  for (int i = 0; i < nA; ++i) {
-    const int q = (wave * nA + i) * 64 + lane, m = q / 8;
-    aoff[i] = tok[m] * t.row_bytes + (((q & 7) ^ ((m >> 1) & 7)) * 16);
-  }
-  for (int st = 0; st < n_st; ++st)
-#pragma unroll
-    for (int i = 0; i < nA; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          ars, (__attribute__((address_space(3))) void*)(As + st * kBuf + (wave * nA + i) * 64), 16,
-          aoff[i], st * 128, 0, 0);
-
-  // weights of step st of block b (past the last block: nothing is read)
-  auto load_c = [&](int b, int st, int j, WStep& w) {
-    const int o = b < n_blk ? b * cblk + st * 2048 + j * 1024 : kNone;
-#pragma unroll
-    for (int f = 0; f < kNF; ++f)
-      w.c[f][j] = __builtin_amdgcn_raw_buffer_load_b128(wt.crs, wt.coff[f] + o, 0, 2);
-  };
-  auto load_s = [&](int b, int st, WStep& w) {
-    const int o = b < n_blk ? b * sblk + (st >> 1) * 256 + (st & 1) * 2 : kNone;
-#pragma unroll
-    for (int f = 0; f < kNF; ++f)
-      w.s[f] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(wt.srs, wt.soff[f] + o, 0, 0);
-  };
-  WStep w1, w2, w3;
-#pragma unroll
-  for (int i = 1; i < D; ++i) {
-    WStep& w = i == 1 ? w1 : i == 2 ? w2 : w3;
-    load_c(0, i, 0, w);
-    load_c(0, i, 1, w);
-    load_s(0, i, w);
-  }
-  vm_barrier<0>();   // the tile is in LDS
-
-  const int sw = (c >> 1) & 7;
-  const u32x4* Ac = As + c * 8;
-  mx_f32x4 acc[kNF][MT];
-  u32x4 x[MT];
-  uint32_t sx[MT];
-  auto x_at = [&](int st, int q) { return Ac + st * kBuf + ((4 * q + g) ^ sw); };
-  auto sx_at = [&](int st) { return sc + c * ga.sc_pitch + (st >> 1) * 16 + 4 * g + (st & 1) * 2; };
-  auto spread = [&](auto n_ds, auto n_ld) {
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-#pragma unroll
-      for (int f = 0; f < kNF; ++f) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        if (kNF * m + f < n_ld.value) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, 1, 0);
-      }
-      __builtin_amdgcn_sched_group_barrier(0x100, n_ds.value, 0);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  {
-    const u32x4* p = x_at(0, 0);
-    const uint8_t* ps = sx_at(0);
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      x[m] = p[m * 128];
-      sx[m] = *reinterpret_cast<const uint16_t*>(ps + 16 * m * ga.sc_pitch);
-    }
-  }
-  auto step = [&](int b, int st, WStep& w) {
-    const bool over = st + D >= n_st;   // the ring runs on into the next block
-    const int rb = over ? b + 1 : b, rs = over ? st + D - n_st : st + D;
-    const int nx = st + 1 == n_st ? 0 : st + 1;
-    const u32x4* p = x_at(st, 1);
-    uint32_t sws[kNF];
-#pragma unroll
-    for (int f = 0; f < kNF; ++f) sws[f] = w.s[f];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-#pragma unroll
-      for (int f = 0; f < kNF; ++f)
-        acc[f][m] = mx_mfma_fp4<0>(w.c[f][0], sws[f], x[m], sx[m], acc[f][m]);
-      x[m] = p[m * 128];
-    }
-    spread(Int<1>(), Int<0>());
-    load_c(rb, rs, 0, w);
-    load_s(rb, rs, w);
-    p = x_at(nx, 0);
-    const uint8_t* ps = sx_at(nx);
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-#pragma unroll
-      for (int f = 0; f < kNF; ++f)
-        acc[f][m] = mx_mfma_fp4<1>(w.c[f][1], sws[f], x[m], sx[m], acc[f][m]);
-      x[m] = p[m * 128];
-      sx[m] = *reinterpret_cast<const uint16_t*>(ps + 16 * m * ga.sc_pitch);
-    }
-    spread(Int<2>(), Int<kNF + nS>());
-    load_c(rb, rs, 1, w);
-    __builtin_amdgcn_sched_barrier(0);
-  };
-#pragma unroll 1
-  for (int b = 0; b < n_blk; ++b) {
-#pragma unroll
-    for (int f = 0; f < kNF; ++f)
-#pragma unroll
-      for (int m = 0; m < MT; ++m) acc[f][m] = mx_f32x4{0, 0, 0, 0};
-#pragma unroll 1
-    for (int st = 0; st < n_st; st += D) {
-      step(b, st, w0);
-      if constexpr (D > 1) step(b, st + 1, w1);
-      if constexpr (D > 2) step(b, st + 2, w2);
-      if constexpr (D > 3) step(b, st + 3, w3);
-    }
-    store<MODE, MT>(ga, t, acc, nrows);
-    t.u0 += MODE == 0 ? 128 : 256;
-  }
-}
-
-template <int MODE, int TM, int D>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
-void mx_gemm_res_kernel(GemmArgs ga) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  int* tok = reinterpret_cast<int*>(smem);                   // [kRowsMax]
-  Tile t;
-  Weights wt;
-  WStep w0;
-  int nrows, arow, act_rows;
-  if (!set_up<MODE, true, TM>(ga, t, wt, w0, tok, nrows, arow, act_rows)) return;
-  const int mt = (nrows + 15) / 16;
-  uint8_t* sc = smem + kRowsMax * 4;
-  u32x4* As = reinterpret_cast<u32x4*>(sc + TM * ga.sc_pitch + 1024);
-  stage_scales(ga, tok, sc, mt * 16, arow, act_rows);
-#define MX_BODY(MT) body_res<MODE, MT, D, TM>(ga, t, wt, w0, As, tok, sc, nrows)
-  if (mt <= 2) MX_BODY(2);
-  else if (mt <= 4) MX_BODY(4);
-  else if (mt <= 6) MX_BODY(6);
-  else if (TM == 128 || mt <= 8) MX_BODY(8);
-  else if constexpr (TM > 128) MX_BODY(10);
 #undef MX_BODY
 }
 
@@ -717,60 +533,19 @@ bool mx_gemm_ok(int act4, long long rows, int ld, int K, int K_sh, int N, int N_
   return mx_code_bytes(N, K) < (1u << 30) && mx_code_bytes(N_sh, K_sh) < (1u << 30);
 }
 
-// K of the kernel that keeps a tile in LDS: rows per tile and ring depth (a
-// divisor of the steps, so that a block is whole turns); 0 rows: not for this K.
-static void res_plan(int KP, int K, int& rows, int& depth) {
-  const int n_st = (K + kKS - 1) / kKS;
-  depth = n_st % 3 == 0 ? 3 : n_st % 4 == 0 ? 4 : n_st % 2 == 0 ? 2 : 1;
-  rows = 0;
-  if (depth == 1) return;
-  for (int r : {160, 128}) {
-    const size_t lds = kRowsMax * 4 + (size_t)r * sc_pitch(KP) + 1024 + (size_t)n_st * r * 128;
-    if (rows == 0 && lds <= 160 * 1024) rows = r;
-  }
-}
-
 hipError_t launch_mx_gemm(const MxProj& a, int mode, int act4, hipStream_t st) {
   GemmArgs ga;
   ga.p = a;
   ga.KP = mx_pad_k(a.ld_in);   // row length of the activation copy
-  ga.sc_pitch = sc_pitch(ga.KP);
-  ga.n_blk = 1;
+  ga.sh_per = (a.T + kRowsMax - 1) / kRowsMax;
+  ga.max_tiles = moe_permute_max_tiles(a.T, a.k, a.E, kRowsMax);
   const int step = mode == 0 ? 128 : 256;
   const int U = a.n_shared > 0 && a.U_sh > a.U ? a.U_sh : a.U;
-  const int blocks = (U + step - 1) / step;
-  int rows = 0, depth = 0;
-  if (act4 && (a.n_shared == 0 || a.K_sh == a.K)) res_plan(ga.KP, a.K, rows, depth);
-  const int tm = rows ? rows : kRowsMax;
-  ga.sh_per = (a.T + tm - 1) / tm;
-  ga.max_tiles = moe_permute_max_tiles(a.T, a.k, a.E, tm);
+  ga.n_ub = (U + step - 1) / step;
+  ga.sc_pitch = sc_pitch(ga.KP);
   const long long slots = (long long)a.n_shared * ga.sh_per + ga.max_tiles;
-  if (rows) {
-    // several blocks per workgroup while that leaves about four workgroups per
-    // compute unit
-    const long long per = slots * blocks / 1024;
-    ga.n_blk = (int)(per < 1 ? 1 : per > blocks ? blocks : per);
-  }
-  ga.n_ub = (blocks + ga.n_blk - 1) / ga.n_blk;
   const long long grid = (slots + kXcd - 1) / kXcd * kXcd * ga.n_ub;
   if (grid >= (1LL << 31)) return hipErrorInvalidValue;
-  if (rows) {
-    const int n_st = (a.K + kKS - 1) / kKS;
-    const size_t lds = kRowsMax * 4 + (size_t)rows * ga.sc_pitch + 1024 + (size_t)n_st * rows * 128;
-#define MX_RES(MODE, TM, D) mx_gemm_res_kernel<MODE, TM, D><<<(int)grid, kThreads, lds, st>>>(ga)
-#define MX_RES_D(MODE, TM)                 \
-  if (depth == 3) MX_RES(MODE, TM, 3);     \
-  else if (depth == 4) MX_RES(MODE, TM, 4); \
-  else MX_RES(MODE, TM, 2)
-    if (mode == 0) {
-      if (rows == 160) { MX_RES_D(0, 160); } else { MX_RES_D(0, 128); }
-    } else {
-      if (rows == 160) { MX_RES_D(1, 160); } else { MX_RES_D(1, 128); }
-    }
-#undef MX_RES_D
-#undef MX_RES
-    return hipGetLastError();
-  }
   const size_t lds = lds_bytes(act4, ga.KP);
   if (mode == 0) return act4 ? launch<0, true>(ga, lds, grid, st) : launch<0, false>(ga, lds, grid, st);
   return act4 ? launch<1, true>(ga, lds, grid, st) : launch<1, false>(ga, lds, grid, st);
