@@ -45,12 +45,62 @@ bool pad_h(int I, int n_shared, int I_shared) {
   return I % 256 != 0 || (n_shared > 0 && I_shared % 256 != 0);
 }
 
-// Tiles of up to 160 rows from this many pairs per expert on, of 16 rows below.
-constexpr long long kGemmRows = 12;
+// Whether a projection runs on tiles of up to 160 rows or of 16.  A tile of 160
+// costs its workgroup a long pass whatever its rows (so there have to be enough
+// of them to fill the chip: the first test, in pieces of weights, an expert's
+// last tile counted as half), one of 16 reads the weights anew for every 16 rows
+// and converts them for 16.
+//  * A16 expands the weights on the vector units, so it is the work that decides:
+//    rows x blocks of columns x pieces of K.  us, 16 rows / 160 rows, H 2048,
+//    I 768, 128 experts, k 8: gate/up of 16 tokens 34/41, of 32 47/44, of 256
+//    87/46; down of 64 tokens 33/36, of 128 38/37, of 256 55/41.  H 4096, I 1536,
+//    8 experts, k 2: gate/up of 32 tokens 18/23, of 64 28/22; down of 32 13/15,
+//    of 64 18/16, of 128 26/20.
+//  * A4 takes codes on both sides and gains from the rows of an expert alone.
+//    The same sizes: gate/up of 128 tokens (8 rows an expert) 41/44, of 256
+//    56/45; down of 192 tokens 36/39, of 256 41/41; 8 experts, 128 tokens
+//    (32 rows) gate/up 26/23, down 20/19.
+//  * Few workgroups: H 1056, I 352, 8 experts, k 3, A16 gate/up of 512 tokens
+//    (351 pieces) 19/21, of 1024 (621) 29/26.
+bool large_tiles(const MxProj& a, bool act4, int mode) {
+  const long long n_ub = mode == 0 ? (a.U + 127) / 128 : (a.U + 255) / 256;
+  const long long work = n_ub * mx_pieces(a.K);
+  const long long tiles = a.P / 160 + (a.E < a.P ? a.E : a.P) / 2;
+  if (tiles * work < 500) return false;
+  if (act4 ? a.P < 16LL * a.E : a.P * work < (mode == 0 ? 24576 : 40960)) return false;
+  const long long rows = mode == 0 ? a.T : (long long)a.P + (long long)a.n_shared * a.T;
+  return mx_gemm_ok(act4, rows, a.ld_in, a.K, a.K_sh, mode == 0 ? 2 * a.U : a.U,
+                    mode == 0 ? 2 * a.U_sh : a.U_sh);
+}
 
-// A4 on tiles of 16 rows: from this many pairs on the rows are quantised once,
-// by a launch of their own; fewer by every workgroup that reads them.
-constexpr int kCodesPairs = 64;
+// Pieces of weight blocks that all workgroups on tiles of 16 rows pass, at most:
+// what quantising the rows in each of them costs.
+long long rows16_work(const MxProj& a, int mode) {
+  const long long n_ub = mode == 0 ? (a.U + 15) / 16 : (a.U + 31) / 32;
+  const long long slots = a.n_shared * ((a.T + 15LL) / 16) + moe_permute_max_tiles(a.T, a.k, a.E, 16);
+  return slots * n_ub * mx_pieces(a.K);
+}
+
+// A4 on tiles of 16 rows: whether the rows are quantised once, by a launch of
+// their own, or by every workgroup that reads them (the same codes).  us, in the
+// workgroups / by a launch: H 2048, I 768, 128 experts, k 8, gate/up of 1 token
+// (work 6144) 6.8/7.2, of 2 (12288) 9.4/9.4, of 4 15.9/13.3, of 16 38/28; down of
+// 2 tokens (6144) 8.7/9.7, of 4 (12288) 12.3/12.2, of 16 24.7/21.1; H 1024,
+// I 512, 64 experts, k 4, gate/up of 8 tokens (8192) 6.5/7.7, of 16 10.8/10.5.
+constexpr long long kCodesWork = 12288;
+
+bool codes_first(const MxProj& a, int mode) { return rows16_work(a, mode) > kCodesWork; }
+
+// Whether a few tokens are routed and sorted by every workgroup of gate/up: one
+// or two launches less, for the passes over the logits in each and, A4, the
+// quantisation there.  Layer, us, by a launch / in the workgroups: H 2048, I 768,
+// 128 experts, k 8, one shared, A16 1 token 19.0/14.7, 3 tokens 29.6/26.7, A4 the
+// same 20.7/16.3, 28.9/27.8; H 4096, I 1536, 256 experts, A16 1 token 31.4/31.0
+// (work 24576), 2 tokens 47.9/47.1, 3 tokens 63.4/66.3, A4 1 token 31.0/32.3.
+bool route_inside(const MxProj& a, bool act4) {
+  return mx_route_gateup_ok(a.T, a.k, a.E, a.ld_in) && !large_tiles(a, act4, 0) &&
+         rows16_work(a, 0) < (act4 ? 2 : 5) * kCodesWork;
+}
 
 MxWsLayout layout(int act, int T, int H, int I, int E, int k, int n_shared, int I_shared) {
   MxWsLayout L;
@@ -119,9 +169,9 @@ moe_status gateup(int act, MxProj a, const MxWsLayout& L, const int32_t* offsets
   const int act4 = act == MOE_A4, H = a.K;
   a.offsets = offsets;
   a.sorted_pair = sorted_pair;
-  const bool gemm = a.P >= kGemmRows * a.E && mx_gemm_ok(act4, a.T, H, H, H, 2 * a.U, 2 * a.U_sh);
+  const bool gemm = large_tiles(a, act4, 0);
   hipError_t e = hipSuccess;
-  if (act4 && (gemm || a.P >= kCodesPairs)) {
+  if (act4 && (gemm || codes_first(a, 0))) {
     uint8_t* q = reinterpret_cast<uint8_t*>(ws + L.qx);
     uint8_t* sc = reinterpret_cast<uint8_t*>(ws + L.sx);
     e = launch_mx_quant(a.x, 0, a.T, H, H, q, sc, mx_pad_k(H), true, s);
@@ -152,16 +202,13 @@ moe_status down(int act, const uint16_t* h, int T, int H, int I, int E, int k,
   a.K_sh = n_shared > 0 ? I_shared : I;
   a.U = a.U_sh = H;
   a.offsets = offsets;
-  if (mx_down_combine_ok(a))
-    return from_hip(launch_mx_down_combine(a, act4, topk_w, pair_pos, shared_gate, out, out_f32, s));
   float* y = reinterpret_cast<float*>(ws + L.y);
   a.out = y;
   a.ld_out = H;
   hipError_t e = hipSuccess;
-  const bool gemm = P >= kGemmRows * E &&
-                    mx_gemm_ok(act4, (long long)P + R_sh, ld_h, a.K, a.K_sh, H, H);
+  const bool gemm = large_tiles(a, act4, 1);
   const uint16_t* h_sh = h + (size_t)P * ld_h;
-  if (act4 && (gemm || P >= kCodesPairs)) {
+  if (act4 && (gemm || codes_first(a, 1))) {
     uint8_t* q = reinterpret_cast<uint8_t*>(ws + L.qh);
     uint8_t* sc = reinterpret_cast<uint8_t*>(ws + L.sh);
     // rows of one length are one launch
@@ -317,7 +364,7 @@ moe_status moe_mx4_layer(int act, const float* logits, const uint16_t* x, int T,
   hipStream_t s = static_cast<hipStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
   const MxProj a = gateup_proj(x, T, H, I, E, k, w13, w13_shared, n_shared, I_shared, h);
-  if (mx_route_gateup_ok(T, k, E, H) && a.P < kGemmRows * E) {
+  if (route_inside(a, act == MOE_A4)) {
     // a few tokens: routing, sort and gate/up in one launch
     st = from_hip(launch_mx_route_gateup(a, act == MOE_A4, logits, renormalize, topk_ids, topk_w,
                                          counts, offsets, sorted_pair, pair_pos, s));

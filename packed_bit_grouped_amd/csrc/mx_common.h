@@ -205,12 +205,6 @@ bool mx_route_gateup_ok(int T, int k, int E, int H);
 hipError_t launch_mx_route_gateup(const MxProj& a, int act4, const float* logits, int renorm,
                                   int32_t* ids, float* w, int32_t* counts, int32_t* offsets,
                                   int32_t* sorted_pair, int32_t* pair_pos, hipStream_t st);
-// Down with the weighted sum in the launch, for at most kDnSlots tiles:
-constexpr int kDnSlots = 40;
-bool mx_down_combine_ok(const MxProj& a);
-hipError_t launch_mx_down_combine(const MxProj& a, int act4, const float* topk_w,
-                                  const int32_t* pair_pos, const float* sh_gate, void* out,
-                                  int out_f32, hipStream_t st);
 // Tiles of up to 160 rows (A16: rows of whole steps, K % 256 == 0 or a padded copy):
 bool mx_gemm_ok(int act4, long long rows, int ld, int K, int K_sh, int N, int N_sh);
 hipError_t launch_mx_gemm(const MxProj& a, int mode, int act4, hipStream_t st);

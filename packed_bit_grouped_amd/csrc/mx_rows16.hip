@@ -14,14 +14,10 @@
 // whole, in registers and feeds codes and scale bytes of both sides to the
 // scaled 16x16x128 instruction.
 //
-//  * mx_rows16_kernel: a workgroup owns 16 units (a gate and an up row each, or
-//    2 x 16 down rows) of one tile; its waves split K and meet in LDS.  With
-//    NV > 0 (a few tokens) every workgroup routes and sorts the batch itself:
-//    that costs less than the launch and the round trip of a routing kernel.
-//  * mx_down_combine_kernel (a few tokens): a workgroup owns 16 output columns
-//    of every token; its waves share the (tile, part of K) products, which meet
-//    in LDS, where the weighted sum of each token is formed: no fp32 rows
-//    through memory and no combine launch.
+// A workgroup owns 16 units (a gate and an up row each, or 2 x 16 down rows) of
+// one tile; its waves split K and meet in LDS.  With ROUTE (a few tokens) every
+// workgroup routes and sorts the batch itself: that costs less than the launch
+// and the round trip of a routing kernel.
 #include "mx_common.h"
 #include "route_common.h"
 
@@ -30,6 +26,8 @@ namespace moe {
 namespace {
 
 constexpr int kTM = 16;        // rows per tile
+constexpr int kWaves = 4;      // share K
+constexpr int kThreads = 64 * kWaves;
 constexpr int kPitch = 20;     // LDS words per 16 (4 rows of 20 words: 16 banks apart)
 
 // The scale bytes of NB pieces from piece s on (s % NB == 0): bytes of the
@@ -131,9 +129,10 @@ struct MxRoute {
 // Up to this many tokens and pairs route inside the gate/up launch.  (Fewer
 // than kRouteRowMinT tokens: their gate weights are summed over 64 lanes, as
 // the routing kernels do for them.)
-constexpr int kRouteT = 4;
+constexpr int kRouteT = 3;
 constexpr int kRouteP = 64;
 static_assert(kRouteT < kRouteRowMinT, "the order of the gate weights' sum");
+static_assert(kRouteT < kWaves, "a wave is left to stage the rows");
 
 // LDS of the routed launch (dynamic): masks of the chosen experts [T][W], then
 // (workgroup 0) the chosen ids and their order keys [P], and the tokens' rows,
@@ -197,7 +196,6 @@ __device__ __forceinline__ void select_topk(const float* __restrict__ logits, in
 
 // Waves 0 .. T-1 of the workgroup route a token each, the others bring the
 // tokens' rows into LDS.
-template <int WV>
 __device__ __forceinline__ void route_and_stage(const MxProj& a, const float* __restrict__ logits,
                                                 bool route, const RouteLds& L) {
   const int wave = threadIdx.x >> 6;
@@ -210,7 +208,7 @@ __device__ __forceinline__ void route_and_stage(const MxProj& a, const float* __
   } else {
     const int n = a.ld_in / 8;   // 16-byte chunks per row
     for (int t = 0; t < a.T; ++t)
-      for (int i = threadIdx.x - 64 * first; i < n; i += 64 * (WV - first))
+      for (int i = threadIdx.x - 64 * first; i < n; i += 64 * (kWaves - first))
         *reinterpret_cast<mx_u32x4*>(L.x + t * L.pitch + i * 16) =
             *reinterpret_cast<const mx_u32x4*>(a.x + (size_t)t * a.ld_in + i * 8);
   }
@@ -218,7 +216,6 @@ __device__ __forceinline__ void route_and_stage(const MxProj& a, const float* __
 }
 
 // The workgroup that writes the tables of moe_route_topk and moe_permute.
-template <int THREADS>
 __device__ __forceinline__ void write_routing(const MxProj& a, const MxRoute& ro,
                                               const RouteLds& L) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -230,7 +227,7 @@ __device__ __forceinline__ void write_routing(const MxProj& a, const MxRoute& ro
     for (int w = 0; w < e / 64; ++w) o += __popcll(L.mask[t * W + w]);
     return o;
   };
-  for (int i = tid; i < a.T * E; i += THREADS) {
+  for (int i = tid; i < a.T * E; i += kThreads) {
     const int t = i / E, e = i - t * E;
     if (chosen(t, e)) {
       const int p = t * k + below(t, e);
@@ -238,7 +235,7 @@ __device__ __forceinline__ void write_routing(const MxProj& a, const MxRoute& ro
       L.key[p] = route_ord(ro.logits[i]);
     }
   }
-  for (int e = tid; e < E; e += THREADS) {
+  for (int e = tid; e < E; e += kThreads) {
     int c = 0, o = 0;
     for (int t = 0; t < a.T; ++t) {
       c += chosen(t, e);
@@ -270,7 +267,7 @@ __device__ __forceinline__ void write_routing(const MxProj& a, const MxRoute& ro
   if (tid < a.P) L.key[i0 + rank] = key;   // in order of rank from here on
   __syncthreads();
   // one wave per token, choice r in lane r, the sums of route_group_vals
-  for (int u = wave; u < a.T; u += THREADS / 64) {
+  for (int u = wave; u < a.T; u += kThreads / 64) {
     const float v = lane < k ? route_unord(L.key[u * k + lane]) : 0.0f;
     const float top = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 0));
     const float ex = lane < k ? expf(v - top) : 0.0f;
@@ -319,11 +316,11 @@ __device__ __forceinline__ bool find_masked(const MxProj& a, const RouteLds& L, 
 
 // XQ (A4): the activations' codes and scales come from memory; else they are
 // quantised here.  ROUTE: the workgroup routes the tokens itself, and workgroup
-// 0 writes the tables; else the tables come from memory.  WV waves.
-template <int MODE, bool ACT4, bool XQ, int NB, bool ROUTE, int WV>
-__global__ __launch_bounds__(64 * WV) void mx_rows16_kernel(MxProj a, MxRoute ro, int n_sh_tiles,
+// 0 writes the tables; else the tables come from memory.
+template <int MODE, bool ACT4, bool XQ, int NB, bool ROUTE>
+__global__ __launch_bounds__(kThreads) void mx_rows16_kernel(MxProj a, MxRoute ro, int n_sh_tiles,
                                                             int n_ub) {
-  __shared__ float red[WV][2][kTM * kPitch];
+  __shared__ float red[kWaves][2][kTM * kPitch];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int blk = ROUTE ? (int)blockIdx.x - 1 : (int)blockIdx.x;
   const int c = lane & 15, g = lane >> 4;
@@ -335,7 +332,7 @@ __global__ __launch_bounds__(64 * WV) void mx_rows16_kernel(MxProj a, MxRoute ro
   const int slot = blk / n_ub, ub = blk - slot * n_ub;
   extern __shared__ __align__(16) unsigned char route_smem[];
   const RouteLds L(route_smem, ROUTE ? a.T : 0, a.E, ROUTE ? a.ld_in : 0);
-  if constexpr (ROUTE) route_and_stage<WV>(a, ro.logits, blk < 0 || slot >= n_sh_tiles, L);
+  if constexpr (ROUTE) route_and_stage(a, ro.logits, blk < 0 || slot >= n_sh_tiles, L);
   if (blk >= 0 && slot < n_sh_tiles) {
     const int per = (a.T + kTM - 1) / kTM;
     is_sh = true;
@@ -344,7 +341,7 @@ __global__ __launch_bounds__(64 * WV) void mx_rows16_kernel(MxProj a, MxRoute ro
     r1 = min(a.T, r0 + kTM);
   } else if constexpr (ROUTE) {
     if (blk < 0) {
-      write_routing<64 * WV>(a, ro, L);
+      write_routing(a, ro, L);
       return;
     }
     if (!find_masked(a, L, slot - n_sh_tiles, e, r0, r1, token)) return;
@@ -397,7 +394,7 @@ __global__ __launch_bounds__(64 * WV) void mx_rows16_kernel(MxProj a, MxRoute ro
 
   mx_f32x4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
   const mx_u32x4 zero = {0, 0, 0, 0};
-  for (int s = wave * NB; s < pieces; s += WV * NB) {
+  for (int s = wave * NB; s < pieces; s += kWaves * NB) {
     mx_u32x4 w[2][NB];
     uint32_t sw[2];
 #pragma unroll
@@ -442,10 +439,10 @@ __global__ __launch_bounds__(64 * WV) void mx_rows16_kernel(MxProj a, MxRoute ro
   }
   __syncthreads();
   const int u = tid & 15, m = tid >> 4;   // unit, row
-  if (m >= kTM || r0 + m >= r1) return;
+  if (r0 + m >= r1) return;
   float v0 = 0.0f, v1 = 0.0f;
 #pragma unroll
-  for (int w = 0; w < WV; ++w) {
+  for (int w = 0; w < kWaves; ++w) {
     v0 += red[w][0][u * kPitch + m];
     v1 += red[w][1][u * kPitch + m];
   }
@@ -473,194 +470,17 @@ hipError_t launch(const MxProj& a, const MxRoute& ro, hipStream_t st) {
   const int K = a.n_shared > 0 && a.K_sh > a.K ? a.K_sh : a.K;
   const int pieces = mx_pieces(K);
   const size_t lds = ROUTE ? RouteLds::bytes(a.T, a.E, a.ld_in) : 0;
-  // Up to 64 pairs (a few tokens) eight waves split K, so that each has little
-  // to do behind its loads; else four, with longer runs.  The same rule with
-  // and without the routing: both sum in the same order.
-#define MX_GO(NB, WV)                                                                         \
-  mx_rows16_kernel<MODE, ACT4, XQ, NB, ROUTE, WV><<<(int)grid, 64 * WV, lds, st>>>(a, ro, n_sh_tiles, \
-                                                                                   n_ub)
-  if (ROUTE || a.P <= kRouteP) {
-    if (pieces >= 16) MX_GO(2, 8);
-    else MX_GO(1, 8);
-  } else if constexpr (!ROUTE) {
-    if (pieces >= 16) MX_GO(4, 4);
-    else if (pieces >= 8) MX_GO(2, 4);
-    else MX_GO(1, 4);
-  }
+  // Pieces per wave and turn, so that the four waves pass K in few turns: each
+  // turn is a trip to memory (down of one token, K 768, NB 1 7.6 us, 2 7.3; A4
+  // of 64 tokens 31.3, 29.4).  At K between 1024 and 2048 NB 4 would leave waves
+  // idle (K 1408, 12 tokens: 14.3 us, NB 2 12.8).
+#define MX_GO(NB) \
+  mx_rows16_kernel<MODE, ACT4, XQ, NB, ROUTE><<<(int)grid, kThreads, lds, st>>>(a, ro, n_sh_tiles, n_ub)
+  if (pieces >= 16) MX_GO(4);
+  else if (pieces > 4) MX_GO(2);
+  else MX_GO(1);
 #undef MX_GO
   return hipGetLastError();
-}
-
-// ---------------------------------------------------------------------
-constexpr int kDnWaves = 8;
-constexpr int kDnThreads = 64 * kDnWaves;
-constexpr int kDnNB = 2;      // pieces per item
-constexpr int kDnItems = 4;   // items of a wave whose loads are in flight together
-
-struct MxCombine {
-  const float* topk_w;
-  const int32_t* pair_pos;
-  const float* sh_gate;   // or null
-  void* out;
-  int out_f32;
-  int max_tiles;   // routed
-  int n_ch;        // parts of K: items per tile
-};
-
-// COLS: 16 output columns per workgroup, or 8 (half the rows of a piece: 128-byte
-// runs of it) where 16 would leave compute units without a workgroup - one of
-// them draws about 23 GB/s, so a token's 7 MB want all 256.
-template <bool ACT4, int COLS>
-__global__ __launch_bounds__(kDnThreads) void mx_down_combine_kernel(MxProj a, MxCombine cb,
-                                                                     int n_sh_tiles) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  const int R = a.P + a.n_shared * a.T;
-  float* yb = reinterpret_cast<float*>(smem);                             // [n_ch][R][COLS]
-  int4* til = reinterpret_cast<int4*>(yb + (size_t)cb.n_ch * R * COLS);   // [slots]
-  int* n_til = reinterpret_cast<int*>(til + n_sh_tiles + cb.max_tiles);
-  int* ppos = n_til + 4;                                                  // [P]
-  float* gw = reinterpret_cast<float*>(ppos + a.P);                       // [P]
-  float* sg = gw + a.P;                                                   // [T][n_shared]
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int c = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.x * COLS;
-  const bool wrow = COLS == 16 || (c >> 3) == ((n0 >> 3) & 1);   // this lane's weight row is wanted
-
-  // ---- tile list (expert, first row, end row, shared) and the gate tables
-  for (int i = tid; i < a.P; i += kDnThreads) {
-    ppos[i] = cb.pair_pos[i];
-    gw[i] = cb.topk_w[i];
-  }
-  const int sh_per = (a.T + kTM - 1) / kTM;
-  for (int i = tid; i < n_sh_tiles; i += kDnThreads) {
-    const int e = i / sh_per, r = (i - e * sh_per) * kTM;
-    til[i] = make_int4(e, a.P + e * a.T + r, a.P + e * a.T + min(a.T, r + kTM), 1);
-  }
-  for (int i = tid; i < a.T * a.n_shared; i += kDnThreads)
-    sg[i] = cb.sh_gate ? shared_gate_weight(cb.sh_gate[i]) : 1.0f;
-  if (wave == kDnWaves - 1) {
-    auto list = [&](auto t) {
-      t.load(a.offsets, a.E, a.P);
-      int at = n_sh_tiles + t.pre - t.cnt;
-      constexpr int PER = sizeof(t.lo) / sizeof(int);
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        for (int r = t.lo[i]; r < t.hi[i] && at < n_sh_tiles + cb.max_tiles; r += kTM)
-          til[at++] = make_int4(lane * PER + i, r, min(t.hi[i], r + kTM), 0);
-      if (lane == 63) *n_til = n_sh_tiles + min(t.pre, cb.max_tiles);
-    };
-    if (a.E <= 128) list(MxTiles<kTM, 2>());
-    else list(MxTiles<kTM, 8>());
-  }
-  __syncthreads();
-
-  // ---- items (tile, part of K), kDnItems per wave at a time
-  const int n_items = *n_til * cb.n_ch;
-  const mx_u32x4 zero = {0, 0, 0, 0};
-  for (int base = wave; base < n_items; base += kDnWaves * kDnItems) {
-    mx_u32x4 w[kDnItems][1][kDnNB], x[kDnItems][kDnNB][4];
-    uint32_t sw[kDnItems][1];
-    int4 tl[kDnItems];
-#pragma unroll
-    for (int i = 0; i < kDnItems; ++i) {
-      const int item = base + i * kDnWaves;
-      const bool ok = item < n_items;
-      const int slot = ok ? item / cb.n_ch : 0, s = ok ? (item - slot * cb.n_ch) * kDnNB : 0;
-      tl[i] = ok ? til[slot] : make_int4(0, 0, 0, 0);
-      const int K = tl[i].w ? a.K_sh : a.K;
-      const int nblk = K / kMxBlock, pieces = mx_pieces(K), words = (pieces + 3) / 4;
-      const uint8_t* wq = (tl[i].w ? a.w_sh : a.w) + tl[i].x * mx_code_bytes(a.U, K);
-      const uint8_t* ws = (tl[i].w ? a.ws_sh : a.ws) + tl[i].x * mx_scale_bytes(a.U, K);
-      const size_t rb = n0 / 16;
-      const mx_u32x4* q = reinterpret_cast<const mx_u32x4*>(wq) + rb * pieces * 64 + lane;
-#pragma unroll
-      for (int j = 0; j < kDnNB; ++j)
-        w[i][0][j] = ok && wrow && s + j < pieces ? __builtin_nontemporal_load(q + (s + j) * 64) : zero;
-      sw[i][0] = ok && s < pieces
-                     ? load_scales<kDnNB>(ws + ((rb * words + (s >> 2)) * 64 + lane) * 4, s)
-                     : 0u;
-      const bool have = tl[i].y + c < tl[i].z;
-      const mx_u32x4* px =
-          reinterpret_cast<const mx_u32x4*>(a.x + (size_t)(have ? tl[i].y + c : 0) * a.ld_in);
-#pragma unroll
-      for (int j = 0; j < kDnNB; ++j) {
-        const int b = 4 * (s + j) + g;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) x[i][j][t] = have && b < nblk ? px[b * 4 + t] : zero;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kDnItems; ++i) {
-      const int item = base + i * kDnWaves;
-      if (item >= n_items) break;
-      mx_f32x4 acc[1] = {{0, 0, 0, 0}};
-      products<ACT4, kDnNB, 1>(w[i], sw[i], x[i], acc);
-      mx_keep(acc[0]);
-      const int ch = item % cb.n_ch;
-      // lane: row c, weight rows 4g .. 4g + 3
-      if (tl[i].y + c < tl[i].z && (COLS == 16 || (g >> 1) == ((n0 >> 3) & 1)))
-        *reinterpret_cast<mx_f32x4*>(yb + ((size_t)ch * R + tl[i].y + c) * COLS +
-                                     (4 * g & (COLS - 1))) = acc[0];
-    }
-  }
-  __syncthreads();
-
-  // ---- the parts of K of every row (rows that no tile wrote are not read below)
-  const int part = R * COLS;
-  if (cb.n_ch > 1) {
-    for (int i = tid; i < part; i += kDnThreads) {
-      float y = yb[i];
-      for (int c0 = 1; c0 < cb.n_ch; c0 += 4) {
-        float v[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = yb[min(c0 + q, cb.n_ch - 1) * part + i];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (c0 + q < cb.n_ch) y += v[q];
-      }
-      yb[i] = y;
-    }
-    __syncthreads();
-  }
-
-  // ---- out[t][n] = sum_j w_j y_j + sum_s g_s y_s, in that order
-  for (int i = tid; i < a.T * COLS; i += kDnThreads) {
-    const int t = i / COLS, n = i & (COLS - 1);
-    // eight pairs at a time: their LDS reads, then the sum in order
-    float o = 0.0f;
-    for (int j0 = 0; j0 < a.k; j0 += 8) {
-      int p[8];
-      float y[8], w[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int q = t * a.k + min(j0 + j, a.k - 1);
-        p[j] = j0 + j < a.k ? ppos[q] : -1;
-        w[j] = gw[q];
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = yb[max(p[j], 0) * COLS + n];
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (p[j] >= 0) o = fmaf(w[j], y[j], o);
-    }
-    for (int s = 0; s < a.n_shared; ++s)
-      o = fmaf(sg[t * a.n_shared + s], yb[(a.P + s * a.T + t) * COLS + n], o);
-    if (cb.out_f32) static_cast<float*>(cb.out)[(size_t)t * a.U + n0 + n] = o;
-    else static_cast<uint16_t*>(cb.out)[(size_t)t * a.U + n0 + n] = (uint16_t)mx_bf16(o);
-  }
-}
-
-int dn_parts(const MxProj& a) {
-  const int K = a.n_shared > 0 && a.K_sh > a.K ? a.K_sh : a.K;
-  return (mx_pieces(K) + kDnNB - 1) / kDnNB;
-}
-
-int dn_cols(const MxProj& a) { return a.U / 16 < 256 ? 8 : 16; }
-
-size_t dn_lds(const MxProj& a, int max_tiles, int n_sh_tiles) {
-  const size_t R = (size_t)a.P + (size_t)a.n_shared * a.T;
-  return dn_parts(a) * R * dn_cols(a) * 4 + (size_t)(n_sh_tiles + max_tiles) * 16 + 16 + (size_t)a.P * 8 +
-         (size_t)a.T * a.n_shared * 4;
 }
 
 }  // namespace
@@ -686,26 +506,6 @@ hipError_t launch_mx_route_gateup(const MxProj& a, int act4, const float* logits
                                   int32_t* sorted_pair, int32_t* pair_pos, hipStream_t st) {
   const MxRoute ro = {logits, renorm, ids, w, counts, offsets, sorted_pair, pair_pos};
   return act4 ? launch<0, true, false, true>(a, ro, st) : launch<0, false, false, true>(a, ro, st);
-}
-
-bool mx_down_combine_ok(const MxProj& a) {
-  const int max_tiles = moe_permute_max_tiles(a.T, a.k, a.E, kTM);
-  const int n_sh_tiles = a.n_shared * ((a.T + kTM - 1) / kTM);
-  return n_sh_tiles + max_tiles <= kDnSlots && dn_lds(a, max_tiles, n_sh_tiles) <= 64 * 1024;
-}
-
-hipError_t launch_mx_down_combine(const MxProj& a, int act4, const float* topk_w,
-                                  const int32_t* pair_pos, const float* sh_gate, void* out,
-                                  int out_f32, hipStream_t st) {
-  MxCombine cb = {topk_w, pair_pos, sh_gate, out, out_f32,
-                  moe_permute_max_tiles(a.T, a.k, a.E, kTM), dn_parts(a)};
-  const int n_sh_tiles = a.n_shared * ((a.T + kTM - 1) / kTM);
-  const size_t lds = dn_lds(a, cb.max_tiles, n_sh_tiles);
-  const bool half = dn_cols(a) == 8;
-  auto kern = act4 ? (half ? mx_down_combine_kernel<true, 8> : mx_down_combine_kernel<true, 16>)
-                   : (half ? mx_down_combine_kernel<false, 8> : mx_down_combine_kernel<false, 16>);
-  kern<<<a.U / dn_cols(a), kDnThreads, lds, st>>>(a, cb, n_sh_tiles);
-  return hipGetLastError();
 }
 
 }  // namespace moe

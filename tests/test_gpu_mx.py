@@ -491,3 +491,162 @@ def test_quantised_layer_end_to_end(mx):
     ids, w, perm = tables(d)
     check_h(d, d["B"].h, perm)
     check_out(d, out, d["B"].h, perm, f64(d["B"].w), np.ones((T, 0)))
+
+
+# ---------------------------------------------------------------------------
+# many rows: tiles of up to 160
+
+LARGE = [
+    # T, H, I, E, k, n_shared, I_shared
+    (507, 2080, 352, 20, 3, 1, 224),     # padded rows, shared experts of their own length
+    (320, 2048, 512, 24, 4, 0, 0),       # whole steps of K
+    (1210, 64, 2080, 60, 2, 0, 0),       # K of half a piece; one block of columns in down
+    (1030, 1024, 256, 150, 5, 0, 0),     # more than 128 experts
+    (2500, 1056, 416, 3, 2, 2, 32),      # many tiles an expert
+]
+MANY = (640, 1056, 416, 24, 4, 1, 416)
+
+
+def on_large_tiles(shape, act):
+    """The library's rule, so that a shape that it no longer sends there is noticed."""
+    T, H, I, E, k = shape[:5]
+    P = T * k
+    tiles = P // 160 + min(E, P) // 2
+    gu, dn = -(-I // 128) * -(-H // 128), -(-H // 256) * -(-I // 128)
+    rows = P >= 16 * E if act == "a4" else P * gu >= 24576 and P * dn >= 40960
+    return tiles * min(gu, dn) >= 500 and rows
+
+
+@pytest.mark.parametrize("act", ["a16", "a4"])
+@pytest.mark.parametrize("shape", LARGE, ids=str)
+def test_many_rows(mx, shape, act):
+    assert on_large_tiles(shape, act)
+    test_layer(mx, shape, act)
+
+
+@pytest.mark.parametrize("act", ["a16", "a4"])
+def test_many_rows_with_unrouted_pairs(mx, act):
+    """Pairs that no expert took: their rows of h stay as they were, nothing of
+    them reaches the outputs, and a token without any gives zeros."""
+    T, H, I, E, k = MANY[:5]
+    assert on_large_tiles(MANY, act)
+    d = make(mx, T, H, I, E, k, act=act, seed=31)
+    ids, w, _ = tables(d)
+    gone = np.zeros((T, k), dtype=bool)
+    gone[::3, 1] = True
+    gone[1] = True
+    flat = np.where(gone, -1, ids).ravel()
+    order = np.argsort(np.where(flat < 0, 999, flat), kind="stable")
+    n = int((flat >= 0).sum())
+    pos = np.full(k * T, -1, dtype=np.int32)
+    pos[order[:n]] = np.arange(n)
+    sp = np.full(k * T, -1, dtype=np.int32)
+    sp[:n] = order[:n]
+    off = np.concatenate([[0], np.cumsum(np.bincount(flat[flat >= 0], minlength=E))]).astype(np.int32)
+    perm = {"offsets": off, "sorted_pair": sp, "pair_pos": pos}
+    B = d["B"]
+    B.h.fill_(3.0)
+    h = mx.gateup_silu(d["bank"], d["x"], torch.from_numpy(off).to(DEV), torch.from_numpy(sp).to(DEV), B)
+    check_h(d, h, perm)
+    assert (h[n:] == 3.0).all()
+    h[n:] = float("nan")
+    w32 = torch.from_numpy(w.astype(np.float32)).to(DEV)
+    out = mx.down_combine(d["bank"], h, w32, torch.from_numpy(off).to(DEV), torch.from_numpy(pos).to(DEV), B)
+    assert (out[1] == 0).all()
+    hz = h.clone()
+    hz[n:] = 0
+    check_out(d, out, hz, perm, f64(w32), np.ones((T, 0)))
+
+
+@pytest.mark.parametrize("act", ["a16", "a4"])
+def test_many_rows_nan_and_inf_stay_in_their_token(mx, act):
+    assert on_large_tiles(MANY, act)
+    d = make(mx, *MANY, act=act, seed=8)
+    d["x"][1, 37] = float("nan")
+    d["x"][3, 5] = float("inf")
+    out = f64(mx.run_layer(d["bank"], d["x"], d["logits"], d["B"], shared_gate=d["gate"]))
+    bad = np.zeros(MANY[0], dtype=bool)
+    bad[[1, 3]] = True
+    assert np.isfinite(out[~bad]).all()
+    assert np.isnan(out[1]).all()
+    assert np.isnan(out[3]).all() if act == "a4" else not np.isfinite(out[3]).any()
+    x0 = d["x"].clone()
+    x0[1] = x0[3] = 0
+    keep = mx.run_layer(d["bank"], x0, d["logits"], d["B"], shared_gate=d["gate"])
+    assert np.array_equal(f64(keep)[~bad], out[~bad])
+
+
+@pytest.mark.parametrize("act", ["a16", "a4"])
+def test_many_rows_marked_weight_block_makes_nan(mx, act):
+    T, H, I, E, k = MANY[:5]
+    d = make(mx, T, H, I, E, k, act=act, seed=3)
+    codes, scales = d["w13"]
+    scales[1, 5, 2] = 255                          # expert 1, gate row 5
+    scales[2, I + 33, H // 32 - 1] = 255           # expert 2, up row 33, the last block
+    d["bank"] = mx.MxBank((codes, scales))
+    ids, w, perm = tables(d)
+    h = f64(mx.gateup_silu(d["bank"], d["x"], torch.from_numpy(perm["offsets"]).to(DEV),
+                           torch.from_numpy(perm["sorted_pair"]).to(DEV), d["B"]))
+    off = perm["offsets"]
+    want = np.zeros(h.shape, dtype=bool)
+    want[off[1]:off[2], 5] = True
+    want[off[2]:off[3], 33] = True
+    assert np.array_equal(np.isnan(h), want)
+
+
+@pytest.mark.parametrize("act", ["a16", "a4"])
+def test_many_rows_repeat_and_replay_bit_identical(mx, act):
+    d = make(mx, *MANY, act=act, seed=77)
+    B = d["B"]
+    ref = mx.run_layer(d["bank"], d["x"], d["logits"], B, shared_gate=d["gate"]).clone()
+    for fill in (0, 255):
+        B.ws.fill_(fill)
+        assert torch.equal(mx.run_layer(d["bank"], d["x"], d["logits"], B, shared_gate=d["gate"]), ref)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mx.run_layer(d["bank"], d["x"], d["logits"], B, shared_gate=d["gate"])
+    eager = mx.MxBuffers(*MANY, act=act, device=DEV)
+    rng = np.random.default_rng(6)
+    for step in range(3):
+        d["x"].copy_(bf16_rows(rng, MANY[0], MANY[1]))
+        d["logits"].copy_(torch.from_numpy(rng.standard_normal((MANY[0], MANY[3])).astype(np.float32)))
+        want = mx.run_layer(d["bank"], d["x"], d["logits"], eager, shared_gate=d["gate"])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(B.out, want), step
+
+
+# ---------------------------------------------------------------------------
+# a few tokens: routing in the gate/up launch
+
+
+@pytest.mark.parametrize("act", ["a16", "a4"])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 512, 64), (2, 130, 32), (3, 65, 20), (3, 64, 21), (2, 5, 5)])
+def test_few_tokens_route_as_the_routing_calls(mx, act, T, E, k):
+    """The tables and weights of the routed launch are those of the framework's
+    routing and sort, ties, infinities and NaN among the logits too."""
+    d = make(mx, T, 64, 32, E, k, act=act, seed=E + k)
+    B = d["B"]
+    rng = np.random.default_rng(E)
+    for kind in ("plain", "ties", "special"):
+        lg = rng.standard_normal((T, E)).astype(np.float32)
+        if kind == "ties":
+            lg = np.round(lg)
+        if kind == "special" and E > 4:
+            lg[0, 0], lg[0, E // 2], lg[T - 1, E - 1] = -np.inf, -np.inf, -3e38
+        logits = torch.from_numpy(lg).to(DEV)
+        for renorm in (0, 1):
+            out = mx.run_layer(d["bank"], d["x"], logits, B, renormalize=renorm)
+            ids, w = oracle.route_topk(lg, k, renorm)
+            perm = oracle.permute(ids, E, 16)
+            assert np.array_equal(B.ids.cpu().numpy(), ids), kind
+            for name in ("counts", "offsets", "sorted_pair", "pair_pos"):
+                assert np.array_equal(getattr(B, name).cpu().numpy(), perm[name]), (kind, name)
+            # logit - max below 16 in size is rounded by at most 8 eps, which the
+            # exponential turns into 8 eps relative, and adds 2 of its own; the
+            # sum has the same and 14 additions (8 per lane, 6 over lanes), the
+            # quotient one: 8 + 2 + 8 + 2 + 14 + 1 = 35 (-inf and -3e38 give 0)
+            assert (np.abs(f64(B.w) - w) <= 40 * O.EPS32 * w).all()
+            check_h(d, B.h, perm)
+            check_out(d, out, B.h, perm, f64(B.w), np.ones((T, 0)))
