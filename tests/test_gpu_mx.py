@@ -650,3 +650,56 @@ def test_few_tokens_route_as_the_routing_calls(mx, act, T, E, k):
             assert (np.abs(f64(B.w) - w) <= 40 * O.EPS32 * w).all()
             check_h(d, B.h, perm)
             check_out(d, out, B.h, perm, f64(B.w), np.ones((T, 0)))
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 128, 8), (3, 130, 5), (2, 20, 20)])
+def test_few_tokens_route_nan_logits_as_the_routing_calls(mx, T, E, k):
+    """NaN logits have no order of their own: the routed launch takes the one
+    that moe_route_topk and moe_permute take, and gives the same bits."""
+    from packed_bit_grouped_amd import _lib as L
+    d = make(mx, T, 64, 32, E, k, seed=E)
+    B = d["B"]
+    rng = np.random.default_rng(7)
+    for vals in ((np.nan,), (-np.nan, np.inf), (np.nan, -np.inf, np.inf, -0.0, 0.0)):
+        lg = rng.standard_normal((T, E)).astype(np.float32)
+        for i, v in enumerate(vals):
+            lg[i % T, 3 * i], lg[(i + 1) % T, E - 1 - i] = v, -v
+        logits = torch.from_numpy(lg).to(DEV)
+        for renorm in (0, 1):
+            mx.run_layer(d["bank"], d["x"], logits, B, renormalize=renorm)
+            i32 = dict(dtype=torch.int32, device=DEV)
+            ids, w = torch.empty((T, k), **i32), torch.empty((T, k), device=DEV)
+            n = L.load().moe_permute_max_tiles(T, k, E, 16)
+            t = [torch.empty(m, **i32) for m in (E, E + 1, T * k, T * k, 4 * n, 1)]
+            L.moe_route_topk(logits, T, E, k, renorm, ids, w)
+            L.moe_permute(ids, T, k, E, 16, *t)
+            assert torch.equal(B.ids, ids)
+            assert torch.equal(B.w.view(torch.int32), w.view(torch.int32))
+            for got, want in zip((B.counts, B.offsets, B.sorted_pair, B.pair_pos), t):
+                assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("act", ["a16", "a4"])
+@pytest.mark.parametrize("shape", [
+    (80, 40960, 128, 4, 1, 0, 0),    # rows whose scales do not fit beside a tile
+    (2, 49152, 32, 2, 1, 0, 0),      # tokens too long to be staged while they are routed
+    (5, 64, 32, 512, 40, 0, 0),      # every expert a lane can hold
+    (1, 64, 32, 128, 100, 1, 32),    # more pairs than the routed launch takes
+    (33, 32, 4096, 2, 2, 3, 32),     # shared experts shorter than the routed ones
+], ids=str)
+def test_far_sizes(mx, shape, act):
+    test_layer(mx, shape, act)
+
+
+def test_a_pair_without_a_place_adds_nothing(mx):
+    T, H, I, E, k = 6, 64, 32, 4, 2
+    d = make(mx, T, H, I, E, k, seed=5)
+    ids, w, perm = tables(d)
+    B = d["B"]
+    h = bf16_rows(np.random.default_rng(1), B.R, B.ld_h).to(DEV)
+    w32 = torch.from_numpy(w.astype(np.float32)).to(DEV)
+    off = torch.from_numpy(perm["offsets"]).to(DEV)
+    pos = perm["pair_pos"].copy()
+    pos[3] = -1
+    want = mx.down_combine(d["bank"], h, w32, off, torch.from_numpy(pos).to(DEV), B).clone()
+    check_out(d, want, h, dict(perm, pair_pos=pos), f64(w32), np.ones((T, 0)))
