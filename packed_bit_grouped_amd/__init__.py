@@ -2,7 +2,8 @@
 
 The compute lives in libmoe_w4.so (hand-written HIP kernels behind the C
 ABI of include/moe_w4.h); this package is its Python binding (`_lib`), the
-device-resident layer driver (`layer`) and the build script (`build`).
+device-resident layer driver (`layer`), the MXFP4 operators (`mx`) and the
+build script (`build`).
 """
 from . import _lib  # noqa: F401
 from ._lib import (MOE_A16, MOE_A8, MOE_PATH_AUTO, MOE_PATH_GEMV,  # noqa: F401

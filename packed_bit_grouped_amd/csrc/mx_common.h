@@ -34,8 +34,8 @@ struct MxWsLayout {
 // the scale bytes of four pieces as one word per lane, byte j the lane's block
 // of piece 4S + j.  Blocks past K hold code 0 and scale 0.  A wave's load is
 // then one contiguous kilobyte; from plain rows (16 runs of 128 bytes a load)
-// the gate/up product of 4096 tokens with MXFP4 activations took 716 us
-// instead of 478.
+// the gate/up product of 4096 tokens with MXFP4 activations (H 4096, I 1536,
+// 256 experts, k 8) took 716 us where the tiles took 478 (398 now).
 constexpr int kMxPieceK = 128;
 inline __host__ __device__ int mx_pieces(int K) { return (K + kMxPieceK - 1) / kMxPieceK; }
 inline __host__ __device__ size_t mx_code_bytes(int N, int K) {

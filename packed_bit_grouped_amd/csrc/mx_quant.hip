@@ -6,7 +6,10 @@
 // power of two is exact, so the only rounding is the one to the code, done by
 // the conversion instruction (all 2^16 bf16 inputs and the codes' midpoints
 // were compared with the definition at 12 scales).  Bound by memory: 2 or 4
-// bytes read and 0.53 written per value, no reuse.
+// bytes read and 0.53 written per value, no reuse.  Measured: 201 M fp32 weights
+// to codes 201 us (4.5 TB/s read and written together), back to bf16 83 us (6.1
+// TB/s); 4096 rows of 4096 bf16 values 8.8 us each way (4.8 TB/s); 12 rows of
+// 2048 2.5 us, the launch.
 #include "mx_common.h"
 
 namespace moe {
