@@ -6,7 +6,8 @@
 // evenly) x 128 gate/up units or 256 down rows; 4 waves, one per SIMD (512
 // registers).  Wave w owns 64 weight rows - the gate and the up rows of 32
 // units, so SiLU*mul pairs registers of one lane, or 64 down rows - as four
-// 16-row fragments against all of the tile's rows.
+// 16-row fragments (NF) against all of the tile's rows.  A4 with few rows per
+// expert: tiles of 144, two fragments per wave, two workgroups per compute unit.
 //
 //  * Weights go from memory into a register ring kD steps of 256 K ahead, two
 //    tiled pieces per fragment and step (a contiguous kilobyte per load).
@@ -27,16 +28,21 @@
 //  * A16 gate/up 739 us, 1.12 PFLOP/s: the matrix pipes are busy 54% of the
 //    cycles, the conversions of the weights share the issue slots.  A library
 //    bf16 product of 8192^3 random values reaches 1.20.
-//  * A4 gate/up 390-400 us, 1.71 GB of weights at 4.3 TB/s; matrix pipes 25%
-//    busy.  One workgroup per compute unit: its start and its stores overlap
-//    with nothing.  A4 down 340 us: 0.86 GB of weights, 0.54 GB of y.
+//  * A4 gate/up 389 us, 1.71 GB of weights at 4.4 TB/s, matrix pipes 25% busy;
+//    down 340 us, 0.86 GB of weights and 0.54 GB of y.  By clock stamps the loop
+//    reads at 6.3 TB/s (22.7 of a workgroup's 30.6 us, down 9.6 of 20.0): the
+//    rest is finding the tile (1.6), its rows (0.5 to 1.4), the first loads (2.6
+//    to 4.2) and the stores (2.0 to 3.8), which one workgroup per compute unit
+//    does not overlap.  32 rows an expert, two workgroups: 6.1 TB/s.
 //  * A tile of 160 rows reads the weights once for nearly every expert here; with
 //    tiles of 128 an expert in two needs a second pass.
 //  * Tried: a tile's codes kept in LDS while several blocks of weights pass
 //    (A4 down here 343 -> 305 us, but 32 experts 211 -> 255, gate/up with K 1024
 //    75 -> 114); columns of down in parts, so that y stays in the cache (460 ->
 //    522 us for parts of 1024); a grid of the likely tiles whose workgroups walk
-//    to further ones (398 -> 418 us).
+//    to further ones (398 -> 418 us); several blocks of columns per workgroup, the
+//    next one's first loads before the stores (397 -> 434 us: the accumulators
+//    then move between the register files in every turn).
 #include "mx_common.h"
 
 namespace moe {
@@ -44,8 +50,8 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRowsMax = 160;   // rows per tile
-constexpr int kNF = 4;          // weight fragments of 16 rows per wave
+constexpr int kRowsMax = 160;      // rows per tile
+constexpr int kRowsNarrow = 144;   // of the kernel with two workgroups per compute unit
 constexpr int kKS = 256;        // K per weight step
 constexpr int kXcd = 8;
 
@@ -98,12 +104,21 @@ struct Ring {
   static constexpr int kBufs = 3;
   static constexpr int kD = ACT4 ? 3 : 2;
   static constexpr int kRowChunks = ACT4 ? 8 : 16;   // 16-byte chunks per row and stage
-  static constexpr int buf_chunks(int mt) { return kRowChunks * 16 * ((mt + 1) & ~1); }
+  // a stage's chunks; the waves load them 64 at a time, an equal number each:
+  // what goes past an odd number of fragments lands behind the ring (spill), or
+  // where LDS is not short, in a buffer rounded up
+  static constexpr int buf_chunks(int mt, int nf) {
+    return kRowChunks * 16 * (nf == 2 ? mt : (mt + 1) & ~1);
+  }
+  static constexpr int spill(int nf) { return nf == 2 ? 128 : 0; }
+  static constexpr int chunks(int mt_max, int nf) { return kBufs * buf_chunks(mt_max, nf) + spill(nf); }
 };
 
+// NF: weight fragments of 16 rows per wave.
+template <int NF>
 struct WStep {
-  u32x4 c[kNF][2];
-  uint32_t s[kNF];
+  u32x4 c[NF][2];
+  uint32_t s[NF];
 };
 
 struct Tile {
@@ -118,12 +133,11 @@ struct Tile {
 // The wave's weights: four 16-row blocks; blocks past the end lie past the
 // buffer, where nothing is read.
 constexpr int kNone = 0x40000000;
-constexpr int nS = kNF;
-constexpr int nW = 2 * kNF + nS;   // weight loads per step
 
+template <int NF>
 struct Weights {
   __amdgpu_buffer_rsrc_t crs, srs;
-  int coff[kNF], soff[kNF], n_st;
+  int coff[NF], soff[NF], n_st;
 
   template <int MODE>
   __device__ __forceinline__ void init(const Tile& t, const uint8_t* w, const uint8_t* ws, int e) {
@@ -135,26 +149,26 @@ struct Weights {
     n_st = t.n_st;
     const int pieces = mx_pieces(t.K), words = (pieces + 3) / 4;
 #pragma unroll
-    for (int f = 0; f < kNF; ++f) {
-      const int u = MODE == 0 ? t.u0 + 16 * (f & 1) : t.u0 + 16 * f;
-      const int rb = ((MODE == 0 && f >= 2 ? t.U : 0) + u) / 16;
+    for (int f = 0; f < NF; ++f) {
+      const int u = MODE == 0 ? t.u0 + 16 * (f % (NF / 2)) : t.u0 + 16 * f;
+      const int rb = ((MODE == 0 && f >= NF / 2 ? t.U : 0) + u) / 16;
       coff[f] = u < t.U ? rb * pieces * 1024 + lane * 16 : kNone;
       soff[f] = u < t.U ? rb * words * 256 + lane * 4 : kNone;
     }
   }
-  __device__ __forceinline__ void load_c(int st, int j, WStep& w) const {
+  __device__ __forceinline__ void load_c(int st, int j, WStep<NF>& w) const {
     const int o = st < n_st ? st * 2048 + j * 1024 : kNone;
 #pragma unroll
-    for (int f = 0; f < kNF; ++f)
+    for (int f = 0; f < NF; ++f)
       w.c[f][j] = __builtin_amdgcn_raw_buffer_load_b128(crs, coff[f] + o, 0, 2);
   }
-  __device__ __forceinline__ void load_s(int st, WStep& w) const {
+  __device__ __forceinline__ void load_s(int st, WStep<NF>& w) const {
     const int o = st < n_st ? (st >> 1) * 256 + (st & 1) * 2 : kNone;
 #pragma unroll
-    for (int f = 0; f < kNF; ++f)
+    for (int f = 0; f < NF; ++f)
       w.s[f] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(srs, soff[f] + o, 0, 0);
   }
-  __device__ __forceinline__ void load(int st, WStep& w) const {
+  __device__ __forceinline__ void load(int st, WStep<NF>& w) const {
     load_c(st, 0, w);
     load_c(st, 1, w);
     load_s(st, w);
@@ -163,19 +177,22 @@ struct Weights {
 };
 
 // w0: the weights of the first step, already on their way.
-template <int MODE, bool ACT4, int MT>
-__device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, const Weights& wt, WStep& w0,
+template <int MODE, bool ACT4, int NF, int TM, int MT>
+__device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, const Weights<NF>& wt, WStep<NF>& w0,
                                      u32x4* As, const int* tok, const uint8_t* sc, int nrows) {
   using R = Ring<ACT4>;
-  constexpr int kBuf = R::buf_chunks(MT);
-  constexpr int nA = kBuf / 256;               // activation loads per wave and stage
+  constexpr int kBuf = R::buf_chunks(MT, NF);
+  constexpr int nA = (kBuf + 255) / 256;       // activation loads per wave and stage
+  constexpr int kSpill = R::kBufs * R::buf_chunks((TM + 15) / 16, NF);
+  static_assert(nA * 256 - kBuf <= R::spill(NF), "the loads' last chunks");
   constexpr int kD = R::kD, kBufs = R::kBufs;
+  constexpr int nS = NF, nW = 2 * NF + nS;      // weight loads per step
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int n_st = t.n_st, n_stage = n_st * R::kStages;
-  auto load_c = [&](int st, int j, WStep& w) { wt.load_c(st, j, w); };
-  auto load_s = [&](int st, WStep& w) { wt.load_s(st, w); };
+  auto load_c = [&](int st, int j, WStep<NF>& w) { wt.load_c(st, j, w); };
+  auto load_s = [&](int st, WStep<NF>& w) { wt.load_s(st, w); };
 
   // ---- activation pieces of this lane: LDS slot q of a stage holds the chunk
   // that the swizzle puts there
@@ -195,15 +212,17 @@ __device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, const We
     sg = min(sg, n_stage - 1);                 // past the end: the last stage once more
     const int o = sg * (ACT4 ? 128 : 256);
 #pragma unroll
-    for (int i = 0; i < nA; ++i)
+    for (int i = 0; i < nA; ++i) {
+      const int q = (wave * nA + i) * 64;
+      const int to = nA * 256 == kBuf || q < kBuf ? buf * kBuf + q : kSpill + q - kBuf;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          ars, (__attribute__((address_space(3))) void*)(As + buf * kBuf + (wave * nA + i) * 64), 16,
-          aoff[i], o, 0, 0);
+          ars, (__attribute__((address_space(3))) void*)(As + to), 16, aoff[i], o, 0, 0);
+    }
   };
 
-  mx_f32x4 acc[kNF][MT];
+  mx_f32x4 acc[NF][MT];
 #pragma unroll
-  for (int f = 0; f < kNF; ++f)
+  for (int f = 0; f < NF; ++f)
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[f][m] = mx_f32x4{0, 0, 0, 0};
 
@@ -219,7 +238,7 @@ __device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, const We
   const int sw = ACT4 ? (c >> 1) & 7 : swizzle16(c);
   const u32x4* Ac = As + c * R::kRowChunks;
   u32x4 x[MT];
-  mx_bf16x8 wv[2][kNF];
+  mx_bf16x8 wv[2][NF];
   uint32_t sx[MT];
   auto x_at = [&](int b, int q) {
     return Ac + b * kBuf + ((ACT4 ? 4 * q + g : 4 * g + q) ^ sw);
@@ -228,9 +247,9 @@ __device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, const We
     st = min(st, n_st - 1);
     return sc + c * ga.sc_pitch + (st >> 1) * 16 + 4 * g + (st & 1) * 2;
   };
-  auto expand = [&](int j, int q, const WStep& w, mx_bf16x8(&v)[kNF]) {
+  auto expand = [&](int j, int q, const WStep<NF>& w, mx_bf16x8(&v)[NF]) {
 #pragma unroll
-    for (int f = 0; f < kNF; ++f)
+    for (int f = 0; f < NF; ++f)
       v[f] = mx_word_to_bf16(w.c[f][j][q], mx_scale_f32((w.s[f] >> (8 * j)) & 255u));
   };
   // issue order of a sub-step: per row fragment four matrix instructions with
@@ -239,9 +258,9 @@ __device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, const We
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
 #pragma unroll
-      for (int f = 0; f < kNF; ++f) {
+      for (int f = 0; f < NF; ++f) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        if (kNF * m + f < n_ld.value) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        if (NF * m + f < n_ld.value) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
         __builtin_amdgcn_sched_group_barrier(0x002, ACT4 ? 1 : 2, 0);
       }
       __builtin_amdgcn_sched_group_barrier(0x100, n_ds.value, 0);
@@ -256,18 +275,18 @@ __device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, const We
   constexpr int kAfter = (kBufs - 2) * nA + (ACT4 ? (kBufs - 1) * nW : nW);
 
   // stage (st, j) from buffer buf with w; wn holds the next step's weights
-  auto stage = [&](int st, int j, WStep& w, const WStep& wn) {
+  auto stage = [&](int st, int j, WStep<NF>& w, const WStep<NF>& wn) {
     const int a = st * R::kStages + j;
     const int nb = buf == kBufs - 1 ? 0 : buf + 1;
     if constexpr (ACT4) {
-      uint32_t sws[kNF];
+      uint32_t sws[NF];
 #pragma unroll
-      for (int f = 0; f < kNF; ++f) sws[f] = w.s[f];
+      for (int f = 0; f < NF; ++f) sws[f] = w.s[f];
       const u32x4* p = x_at(buf, 1);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
 #pragma unroll
-        for (int f = 0; f < kNF; ++f)
+        for (int f = 0; f < NF; ++f)
           acc[f][m] = mx_mfma_fp4<0>(w.c[f][0], sws[f], x[m], sx[m], acc[f][m]);
         x[m] = p[m * 16 * R::kRowChunks];
       }
@@ -281,12 +300,12 @@ __device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, const We
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
 #pragma unroll
-        for (int f = 0; f < kNF; ++f)
+        for (int f = 0; f < NF; ++f)
           acc[f][m] = mx_mfma_fp4<1>(w.c[f][1], sws[f], x[m], sx[m], acc[f][m]);
         x[m] = p[m * 16 * R::kRowChunks];
         sx[m] = *reinterpret_cast<const uint16_t*>(ps + 16 * m * ga.sc_pitch);
       }
-      spread(Int<2>(), Int<nA + kNF + nS>());
+      spread(Int<2>(), Int<nA + NF + nS>());
       load_c(st + kD, 1, w);
       __builtin_amdgcn_sched_barrier(0);
     } else {
@@ -309,26 +328,26 @@ __device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, const We
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
 #pragma unroll
-          for (int f = 0; f < kNF; ++f)
+          for (int f = 0; f < NF; ++f)
             acc[f][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                 wv[cur][f], __builtin_bit_cast(mx_bf16x8, x[m]), acc[f][m], 0, 0, 0);
           x[m] = p[m * 16 * R::kRowChunks];
         }
         if (q < kQ - 1) spread(Int<1>(), Int<0>());
-        else if (j == 0) spread(Int<1>(), Int<nA + kNF>());
-        else spread(Int<1>(), Int<nA + kNF + nS>());
+        else if (j == 0) spread(Int<1>(), Int<nA + NF>());
+        else spread(Int<1>(), Int<nA + NF + nS>());
       }
     }
     buf = nb;
   };
-  auto step = [&](int st, WStep& w, const WStep& wn) {
+  auto step = [&](int st, WStep<NF>& w, const WStep<NF>& wn) {
     stage(st, 0, w, wn);
     if constexpr (!ACT4) stage(st, 1, w, wn);
   };
 
   // Prologue: the loads in an order for which kAfter holds in the first stages
   // too (the first step's weights went before).
-  WStep w1, w2;
+  WStep<NF> w1, w2;
   dma(0, 0);
   dma(1, 1);
   __builtin_amdgcn_sched_barrier(0);
@@ -383,23 +402,23 @@ __device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, const We
   for (int m = 0; m < MT; ++m) {
     const int row = 16 * m + c;
 #pragma unroll
-    for (int f = 0; f < kNF; ++f) mx_keep(acc[f][m]);
+    for (int f = 0; f < NF; ++f) mx_keep(acc[f][m]);
     if (row >= nrows) continue;
     if (MODE == 0) {
       uint16_t* h = static_cast<uint16_t*>(ga.p.out) + (size_t)(t.orow + row) * ga.p.ld_out;
 #pragma unroll
-      for (int f = 0; f < 2; ++f) {
+      for (int f = 0; f < NF / 2; ++f) {
         const int u = t.u0 + 16 * f + 4 * g;
         if (u >= t.U) continue;
         uint32_t v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = mx_bf16(mx_silu_mul(acc[f][m][i], acc[f + 2][m][i]));
+        for (int i = 0; i < 4; ++i) v[i] = mx_bf16(mx_silu_mul(acc[f][m][i], acc[f + NF / 2][m][i]));
         *reinterpret_cast<uint2*>(h + u) = make_uint2(v[0] | (v[1] << 16), v[2] | (v[3] << 16));
       }
     } else {
       float* y = static_cast<float*>(ga.p.out) + (size_t)(t.orow + row) * ga.p.ld_out;
 #pragma unroll
-      for (int f = 0; f < kNF; ++f) {
+      for (int f = 0; f < NF; ++f) {
         const int u = t.u0 + 16 * f + 4 * g;
         if (u < t.U) *reinterpret_cast<mx_f32x4*>(y + u) = acc[f][m];
       }
@@ -407,18 +426,18 @@ __device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, const We
   }
 }
 
-// Routed rows: an expert with n rows has ceil(n / 160) tiles of even size.
+// Routed rows: an expert with n rows has ceil(n / TM) tiles of even size.
 __device__ __forceinline__ void cut(int first, int end, int n, int k, int& r0, int& r1) {
   const int rows = ((end - first + n - 1) / n + 15) & ~15;
   r0 = min(first + k * rows, end);
   r1 = min(r0 + rows, end);
 }
 
-template <int PER>
+template <int TM, int PER>
 __device__ __forceinline__ bool pick_tile(const GemmArgs& ga, bool& is_sh, int& e, int& r0, int& r1,
                                           int& ub) {
   const MxProj& a = ga.p;
-  MxTiles<kRowsMax, PER> tl;
+  MxTiles<TM, PER> tl;
   tl.load(a.offsets, a.E, a.P);
   const int n_sh = a.n_shared * ga.sh_per;
   const int n_slots = n_sh + min(__builtin_amdgcn_readlane(tl.pre, 63), ga.max_tiles);
@@ -437,12 +456,12 @@ __device__ __forceinline__ bool pick_tile(const GemmArgs& ga, bool& is_sh, int& 
   }
   int first, end, k;
   if (!tl.find(slot - n_sh, e, first, end, k)) return false;
-  cut(first, end, (end - first + kRowsMax - 1) / kRowsMax, k, r0, r1);
+  cut(first, end, (end - first + TM - 1) / TM, k, r0, r1);
   return r0 < r1;
 }
 
-template <int MODE, bool ACT4>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
+template <int MODE, bool ACT4, int NF, int TM>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4 / NF, 4 / NF)))
 void mx_gemm_kernel(GemmArgs ga) {
   extern __shared__ __align__(16) unsigned char smem[];
   const MxProj& a = ga.p;
@@ -452,7 +471,7 @@ void mx_gemm_kernel(GemmArgs ga) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   bool is_sh;
   int e, r0, r1, ub;
-  if (!(a.E <= 128 ? pick_tile<2>(ga, is_sh, e, r0, r1, ub) : pick_tile<8>(ga, is_sh, e, r0, r1, ub)))
+  if (!(a.E <= 128 ? pick_tile<TM, 2>(ga, is_sh, e, r0, r1, ub) : pick_tile<TM, 8>(ga, is_sh, e, r0, r1, ub)))
     return;
   const int nrows = r1 - r0;
 
@@ -460,9 +479,9 @@ void mx_gemm_kernel(GemmArgs ga) {
   t.K = is_sh ? a.K_sh : a.K;
   t.U = is_sh ? a.U_sh : a.U;
   t.n_st = (t.K + kKS - 1) / kKS;
-  const int ublk = ub * (MODE == 0 ? 128 : 256);
+  const int ublk = ub * (MODE == 0 ? 32 : 64) * NF;
   if (ublk >= t.U) return;
-  t.u0 = ublk + wave * (MODE == 0 ? 32 : 64);
+  t.u0 = ublk + wave * (MODE == 0 ? 8 : 16) * NF;
   t.orow = is_sh ? a.P + e * a.T + r0 : r0;
   // gate/up gathers rows of x by token; down reads its own rows, the shared
   // experts' behind the routed ones
@@ -474,9 +493,9 @@ void mx_gemm_kernel(GemmArgs ga) {
   t.act_bytes = (uint32_t)(act_rows * stride);
   // the first step's weights need only the tile: on their way before its rows
   // are looked up
-  Weights wt;
-  wt.init<MODE>(t, is_sh ? a.w_sh : a.w, is_sh ? a.ws_sh : a.ws, e);
-  WStep w0;
+  Weights<NF> wt;
+  wt.template init<MODE>(t, is_sh ? a.w_sh : a.w, is_sh ? a.ws_sh : a.ws, e);
+  WStep<NF> w0;
   wt.load(0, w0);
 
   if (tid < kRowsMax) {
@@ -499,7 +518,7 @@ void mx_gemm_kernel(GemmArgs ga) {
     // the tile's scale bytes, by loads that write LDS, ahead of every activation
     // load: rows of an odd number of 16-byte chunks, so that 16 rows' words lie
     // on different banks (an even number is followed by a chunk that is not read)
-    sc = smem + kRowsMax * 4 + Ring<true>::kBufs * Ring<true>::buf_chunks(10) * 16;
+    sc = smem + kRowsMax * 4 + Ring<true>::chunks((TM + 15) / 16, NF) * 16;
     const int row = ga.KP / kMxBlock, chunks = ga.sc_pitch / 16;
     const __amdgpu_buffer_rsrc_t rs =
         make_rsrc(a.s + (size_t)arow * row, (uint32_t)((size_t)act_rows * row));
@@ -512,36 +531,29 @@ void mx_gemm_kernel(GemmArgs ga) {
     }
     __builtin_amdgcn_sched_barrier(0);
   }
-#define MX_BODY(MT) body<MODE, ACT4, MT>(ga, t, wt, w0, As, tok, sc, nrows)
+#define MX_BODY(MT) body<MODE, ACT4, NF, TM, MT>(ga, t, wt, w0, As, tok, sc, nrows)
   if (mt <= 2) MX_BODY(2);
   else if (mt <= 4) MX_BODY(4);
   else if (mt <= 6) MX_BODY(6);
   else if (mt == 7) MX_BODY(7);
   else if (mt == 8) MX_BODY(8);
-  else if (mt == 9) MX_BODY(9);
-  else MX_BODY(10);
+  else if (TM <= 144 || mt == 9) MX_BODY(9);
+  else if constexpr (TM > 144) MX_BODY(10);
 #undef MX_BODY
-}
-
-template <int MODE, bool ACT4>
-hipError_t launch(const GemmArgs& ga, size_t lds, long long grid, hipStream_t st) {
-  mx_gemm_kernel<MODE, ACT4><<<(int)grid, kThreads, lds, st>>>(ga);
-  return hipGetLastError();
 }
 
 int sc_pitch(int KP) { return (KP / kMxBlock) | 16; }   // KP / 32 is a multiple of 16
 
-size_t lds_bytes(bool act4, int KP) {
-  const size_t ring = act4 ? (size_t)Ring<true>::kBufs * Ring<true>::buf_chunks(10) * 16
-                           : (size_t)Ring<false>::kBufs * Ring<false>::buf_chunks(10) * 16;
-  return kRowsMax * 4 + ring + (act4 ? (size_t)kRowsMax * sc_pitch(KP) + 1024 : 0);
+size_t lds_bytes(bool act4, int KP, int tm, int nf) {
+  const size_t ring = act4 ? Ring<true>::chunks((tm + 15) / 16, nf) : Ring<false>::chunks((tm + 15) / 16, nf);
+  return kRowsMax * 4 + ring * 16 + (act4 ? (size_t)tm * sc_pitch(KP) + 1024 : 0);
 }
 
 }  // namespace
 
 bool mx_gemm_ok(int act4, long long rows, int ld, int K, int K_sh, int N, int N_sh) {
   const int KP = mx_pad_k(K > K_sh ? K : K_sh);
-  if (lds_bytes(act4, KP) > 160 * 1024) return false;
+  if (lds_bytes(act4, KP, kRowsMax, 4) > 160 * 1024) return false;
   // 32-bit offsets into one matrix and into the activation rows
   const long long stride = act4 ? mx_pad_k(ld) / 2 : 2LL * mx_pad_k(ld);
   if (rows * stride >= (1LL << 31)) return false;
@@ -552,18 +564,39 @@ hipError_t launch_mx_gemm(const MxProj& a, int mode, int act4, hipStream_t st) {
   GemmArgs ga;
   ga.p = a;
   ga.KP = mx_pad_k(a.ld_in);   // row length of the activation copy
-  ga.sh_per = (a.T + kRowsMax - 1) / kRowsMax;
-  ga.max_tiles = moe_permute_max_tiles(a.T, a.k, a.E, kRowsMax);
-  const int step = mode == 0 ? 128 : 256;
+  ga.sc_pitch = sc_pitch(ga.KP);
+  // Two workgroups per compute unit, each with half the weight rows per wave: one's
+  // start and stores pass behind the other's loop (by clock stamps 8 of 31 us of a
+  // gate/up workgroup, 10 of 20 of down, whose loop alone reads 6.3 TB/s), but the
+  // activations are read twice as often.  A4, us, one / two workgroups, by rows
+  // per expert.  H 4096, I 1536: 8 experts, 64 rows, gate/up 25/19, down 23/19,
+  // 256 rows 32/47, 34/35; 256 experts, 32 rows 296/278, 241/231, 64 rows 321/308,
+  // 311/289, 128 rows 389/400, 460/436 (with the sum).  H 2048, I 768, 128
+  // experts: 16 rows 45/42, 41/38, 64 rows 53/52, 62/61, 128 rows 63/68, 89/93.
+  const bool narrow = act4 && a.P <= 96LL * a.E && lds_bytes(true, ga.KP, kRowsNarrow, 2) <= 80 * 1024;
+  const int tm = narrow ? kRowsNarrow : kRowsMax, nf = narrow ? 2 : 4;
+  ga.sh_per = (a.T + tm - 1) / tm;
+  ga.max_tiles = moe_permute_max_tiles(a.T, a.k, a.E, tm);
+  const int step = (mode == 0 ? 32 : 64) * nf;
   const int U = a.n_shared > 0 && a.U_sh > a.U ? a.U_sh : a.U;
   ga.n_ub = (U + step - 1) / step;
-  ga.sc_pitch = sc_pitch(ga.KP);
   const long long slots = (long long)a.n_shared * ga.sh_per + ga.max_tiles;
   const long long grid = (slots + kXcd - 1) / kXcd * kXcd * ga.n_ub;
   if (grid >= (1LL << 31)) return hipErrorInvalidValue;
-  const size_t lds = lds_bytes(act4, ga.KP);
-  if (mode == 0) return act4 ? launch<0, true>(ga, lds, grid, st) : launch<0, false>(ga, lds, grid, st);
-  return act4 ? launch<1, true>(ga, lds, grid, st) : launch<1, false>(ga, lds, grid, st);
+  const size_t lds = lds_bytes(act4, ga.KP, tm, nf);
+#define MX_GO(MODE, ACT4, NF, TM) mx_gemm_kernel<MODE, ACT4, NF, TM><<<(int)grid, kThreads, lds, st>>>(ga)
+  if (narrow) {
+    if (mode == 0) MX_GO(0, true, 2, kRowsNarrow);
+    else MX_GO(1, true, 2, kRowsNarrow);
+  } else if (act4) {
+    if (mode == 0) MX_GO(0, true, 4, kRowsMax);
+    else MX_GO(1, true, 4, kRowsMax);
+  } else {
+    if (mode == 0) MX_GO(0, false, 4, kRowsMax);
+    else MX_GO(1, false, 4, kRowsMax);
+  }
+#undef MX_GO
+  return hipGetLastError();
 }
 
 }  // namespace moe

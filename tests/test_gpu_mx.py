@@ -703,3 +703,27 @@ def test_a_pair_without_a_place_adds_nothing(mx):
     pos[3] = -1
     want = mx.down_combine(d["bank"], h, w32, off, torch.from_numpy(pos).to(DEV), B).clone()
     check_out(d, want, h, dict(perm, pair_pos=pos), f64(w32), np.ones((T, 0)))
+
+
+# fewer rows an expert, A4: two workgroups share a compute unit
+FEWER = (560, 1056, 416, 24, 4, 1, 416)
+
+
+@pytest.mark.parametrize("check", [
+    test_many_rows_with_unrouted_pairs, test_many_rows_nan_and_inf_stay_in_their_token,
+    test_many_rows_marked_weight_block_makes_nan, test_many_rows_repeat_and_replay_bit_identical,
+], ids=lambda f: f.__name__[15:])
+def test_fewer_rows(mx, monkeypatch, check):
+    T, H, I, E, k = FEWER[:5]
+    assert on_large_tiles(FEWER, "a4") and T * k <= 96 * E < MANY[0] * MANY[4]
+    monkeypatch.setitem(globals(), "MANY", FEWER)
+    check(mx, "a4")
+
+
+@pytest.mark.parametrize("shape", [
+    (400, 6144, 128, 24, 1, 0, 0),     # rows too long for two workgroups' LDS
+    (1150, 4608, 160, 12, 1, 1, 96),   # the longest that fit
+    (2000, 512, 2304, 12, 1, 0, 0),    # more rows an expert than the rule takes
+], ids=str)
+def test_rows_on_either_side_of_the_two_workgroup_rule(mx, shape):
+    test_layer(mx, shape, "a4")
