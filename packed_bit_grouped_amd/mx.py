@@ -14,6 +14,15 @@ layer are defined there).
   current stream of the tensors' device (or on ``stream``).  The outputs are
   the buffers' own tensors, overwritten by the next call on them; calls that
   overlap in time (other streams) need buffers each.
+
+``stream`` (a torch stream, or a stream handle as a number, which has to live
+as long as the tensors it was used with): inputs, a bank and buffers have to be
+ready on it, and whoever reads the results elsewhere waits for it.  What a call
+allocates or copies itself it does on that stream, and the new tensors belong
+to it.  ``quantize_rows``, ``quantize_bank``, ``dequantize_rows`` and ``MxBank``
+may be given tensors that are dropped at once; the step calls' tensors, bank
+and buffers are kept until their work is done (``MxBuffers`` and ``MxBank`` fill
+their tensors on the stream that they are made on: other streams wait for it).
 """
 from __future__ import annotations
 
@@ -40,6 +49,35 @@ def _launch(name, dev, stream, *args):
     st = getattr(L._lib or L.load(), name)(*args, stream)
     if st:
         raise L.MoeError(name, st, L.status_str(st))
+
+
+def _side(dev, stream):
+    """`stream` as a torch stream of the device with index dev; None: the
+    current one there, on which torch allocates and copies anyway."""
+    if stream is None:
+        return None
+    if not isinstance(stream, int):
+        return stream
+    if stream == 0:
+        return torch.cuda.default_stream(dev)
+    return torch.cuda.ExternalStream(stream, device=dev)
+
+
+def _empty(shape, dtype, device, side):
+    """Memory of the stream `side`: what was freed there earlier is free there,
+    while the current stream's pool may hand out what queued work still uses."""
+    if side is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(side):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _used_on(side, *tensors):
+    """The tensors' memory is given to nothing else before the work that is
+    queued on `side` by now is done, even if the caller drops them at once."""
+    if side is not None:
+        for t in tensors:
+            t.record_stream(side)
 
 
 def _want(name, t, dtypes, shape, dev=None):
@@ -89,16 +127,18 @@ def quantize_rows(src, codes=None, scales=None, stream=None):
     if ld < C:
         raise ValueError("src: rows overlap")
     dev = _gpu(src)
+    side = _side(dev, stream)
     if codes is None:
-        codes = torch.empty((R, C // 2), dtype=torch.uint8, device=src.device)
+        codes = _empty((R, C // 2), torch.uint8, src.device, side)
     else:
         _want("codes", codes, _U8, (R, C // 2), dev)
     if scales is None:
-        scales = torch.empty((R, C // BLOCK), dtype=torch.uint8, device=src.device)
+        scales = _empty((R, C // BLOCK), torch.uint8, src.device, side)
     else:
         _want("scales", scales, _U8, (R, C // BLOCK), dev)
     _launch("moe_mx4_quant_rows", dev, stream, src.data_ptr(), f32, R, C, ld, codes.data_ptr(),
             scales.data_ptr())
+    _used_on(side, src, codes, scales)
     return codes, scales
 
 
@@ -115,16 +155,25 @@ def dequantize_rows(codes, scales, dtype=torch.bfloat16, stream=None):
     pc = _want("codes", codes, _U8, (R, C // 2))
     ps = _want("scales", scales, _U8, (R, C // BLOCK), codes.get_device())
     dev = _gpu(codes)
-    dst = torch.empty((R, C), dtype=dtype, device=codes.device)
+    side = _side(dev, stream)
+    dst = _empty((R, C), dtype, codes.device, side)
     _launch("moe_mx4_dequant_rows", dev, stream, pc, ps, R, C, dst.data_ptr(),
             dtype is torch.float32, C)
+    _used_on(side, codes, scales)
     return dst
 
 
 def quantize_bank(w, stream=None):
     """fp32 or bf16 matrices [n][N][K] to one (codes, scales) pair for MxBank."""
     n, N, K = w.shape
-    codes, scales = quantize_rows(w.reshape(n * N, K), stream=stream)
+    side = _side(_gpu(w), stream)
+    if side is None:
+        rows = w.reshape(n * N, K)
+    else:   # matrices that are not contiguous are copied: in front of the call that reads the copy
+        with torch.cuda.stream(side):
+            rows = w.reshape(n * N, K)
+        _used_on(side, w)
+    codes, scales = quantize_rows(rows, stream=stream)
     return codes.view(n, N, K // 2), scales.view(n, N, K // BLOCK)
 
 
@@ -154,10 +203,12 @@ class MxBank:
             nc, ns = L.moe_mx4_bank_code_bytes(n, N, K), L.moe_mx4_bank_scale_bytes(n, N, K)
             if nc == 0:
                 raise ValueError(f"{tag}: unsupported matrices (n, N, K) = {(n, N, K)}")
-            tc = torch.empty(nc, dtype=torch.uint8, device=codes.device)
-            ts = torch.empty(ns, dtype=torch.uint8, device=codes.device)
-            _launch("moe_mx4_tile_bank", _gpu(codes), stream, codes.data_ptr(), scales.data_ptr(),
+            side = _side(_gpu(codes), stream)
+            tc = _empty(nc, torch.uint8, codes.device, side)
+            ts = _empty(ns, torch.uint8, codes.device, side)
+            _launch("moe_mx4_tile_bank", self.device, stream, codes.data_ptr(), scales.data_ptr(),
                     n, N, K, tc.data_ptr(), ts.data_ptr())
+            _used_on(side, codes, scales)
             self.tiles[tag] = (tc, ts)
             self.desc[tag] = L.MxBankDesc(tc.data_ptr(), ts.data_ptr())
             self.addr[tag] = ctypes.addressof(self.desc[tag])

@@ -1,0 +1,139 @@
+"""The MXFP4 operators where their other tests do not go: calls on another
+stream than the current one."""
+import numpy as np
+import pytest
+
+from oracle import mx_oracle as O
+
+torch = pytest.importorskip("torch")
+from test_gpu_mx import DEV, bf16_rows, f64, mx  # noqa: E402,F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------
+# another stream than the current one: the other one is held up where the call's
+# own work has to be in order, the current one where it must not matter
+
+HOLD = 50_000_000     # clock ticks of a spinning kernel: tens of milliseconds
+
+
+def hold(stream):
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(HOLD)
+
+
+def other_stream(kind):
+    """(a side stream that has seen the work queued so far, the argument for it)"""
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    return s, (s if kind == "stream" else s.cuda_stream)
+
+
+@pytest.mark.parametrize("kind", ["stream", "handle"])
+def test_transposed_bank_is_copied_on_the_call_s_stream(mx, kind):
+    """The copy that quantize_bank makes of matrices that are not contiguous is
+    in front of the quantiser, whatever the current stream is busy with, and
+    its memory is not given away while the quantiser reads it."""
+    w = torch.randn((3, 128, 96), generator=torch.Generator(DEV).manual_seed(1), device=DEV)
+    want = mx.quantize_bank(w.transpose(1, 2))
+    torch.cuda.synchronize()
+    s, arg = other_stream(kind)
+    hold(torch.cuda.current_stream())     # a copy queued here would come late
+    got = mx.quantize_bank(w.transpose(1, 2), stream=arg)
+    s.synchronize()
+    with torch.cuda.stream(s):
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    torch.cuda.synchronize()
+    hold(s)                               # the copy's memory has to last
+    got = mx.quantize_bank(w.transpose(1, 2), stream=arg)
+    noise = [torch.full((3 * 96, 128), 7.0, device=DEV) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    del noise
+
+
+@pytest.mark.parametrize("kind", ["stream", "handle"])
+@pytest.mark.parametrize("made_on", ["current", "other"])
+def test_pairs_may_be_dropped_behind_the_bank(mx, made_on, kind):
+    w = torch.randn((4, 64, 256), generator=torch.Generator(DEV).manual_seed(2), device=DEV)
+    want = mx.MxBank(mx.quantize_bank(w)).tiles["w13"]
+    torch.cuda.synchronize()
+    if made_on == "current":
+        pair = mx.quantize_bank(w)
+        s, arg = other_stream(kind)
+        hold(s)
+        bank = mx.MxBank(pair, stream=arg)
+        shapes = [t.shape for t in pair]
+        del pair
+    else:
+        s, arg = other_stream(kind)
+        hold(s)
+        bank = mx.MxBank(mx.quantize_bank(w, stream=arg), stream=arg)
+        shapes = [(4, 64, 128), (4, 64, 8)]
+    noise = [torch.full(sh, 255, dtype=torch.uint8, device=DEV) for sh in shapes for _ in range(4)]
+    torch.cuda.synchronize()
+    for got, ref in zip(bank.tiles["w13"], want):
+        assert torch.equal(got, ref)
+    del noise
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_may_be_dropped_behind_the_call(mx, dtype):
+    src = bf16_rows(np.random.default_rng(3), 96, 512).to(DEV).to(dtype)
+    want_c, want_s = O.quantise(f64(src))
+    want_v = torch.from_numpy(O.values(want_c, want_s)).float()
+    torch.cuda.synchronize()
+    s, arg = other_stream("stream")
+    hold(s)
+    codes, scales = mx.quantize_rows(src.clone(), stream=arg)
+    noise = [torch.full_like(src, 9.0) for _ in range(4)]
+    torch.cuda.synchronize()
+    c2, s2 = codes.clone(), scales.clone()
+    s.wait_stream(torch.cuda.current_stream())
+    hold(s)
+    back = mx.dequantize_rows(c2, s2, dtype, stream=arg)
+    del c2, s2
+    noise += [torch.full_like(t, 255) for t in (codes, scales) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert np.array_equal(codes.cpu().numpy(), want_c) and np.array_equal(scales.cpu().numpy(), want_s)
+    assert torch.equal(back.cpu().float(), want_v)
+    del noise
+
+
+@pytest.mark.parametrize("kind", ["stream", "handle"])
+def test_results_do_not_lie_where_the_current_stream_still_writes(mx, kind):
+    """Memory that was freed on the current stream behind queued work may be
+    handed out there again at once, not to a call on another stream."""
+    src = bf16_rows(np.random.default_rng(4), 64, 512).to(DEV)
+    w = src.float().view(2, 32, 512)
+    codes, scales = mx.quantize_rows(src)
+    back = mx.dequantize_rows(codes, scales)
+    tiles = mx.MxBank(mx.quantize_bank(w)).tiles["w13"]
+    torch.cuda.synchronize()
+    s, arg = other_stream(kind)
+    hold(torch.cuda.current_stream())
+    for t in (codes, scales, back, *tiles):      # written late, given back at once
+        for _ in range(2):
+            junk = torch.full_like(t, 77)
+            del junk
+    c2, s2 = mx.quantize_rows(src, stream=arg)
+    b2 = mx.dequantize_rows(c2, s2, stream=arg)
+    t2 = mx.MxBank(mx.quantize_bank(w, stream=arg), stream=arg).tiles["w13"]
+    torch.cuda.synchronize()
+    for got, ref in zip((c2, s2, b2, *t2), (codes, scales, back, *tiles)):
+        assert torch.equal(got, ref)
+
+
+def test_default_stream_as_a_handle(mx):
+    """Handle 0 is the default stream."""
+    w = torch.randn((2, 64, 48), generator=torch.Generator(DEV).manual_seed(5), device=DEV)
+    want = mx.quantize_bank(w.transpose(1, 2))
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = mx.quantize_bank(w.transpose(1, 2), stream=0)
+        tiles = mx.MxBank(got, stream=0).tiles["w13"]
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for a, b in zip(tiles, mx.MxBank(want).tiles["w13"]):
+        assert torch.equal(a, b)
