@@ -36,16 +36,23 @@ BLOCK = 32
 ACTS = {"a16": L.MOE_A16, "a4": L.MOE_A4, L.MOE_A16: L.MOE_A16, L.MOE_A4: L.MOE_A4}
 
 
+def _here(dev, stream):
+    """The torch stream, which has to be one of the device with index dev."""
+    if stream.device_index != dev:
+        raise ValueError(f"stream: of device {stream.device_index}, the tensors are on device {dev}")
+    return stream
+
+
 def _launch(name, dev, stream, *args):
     """The C call on the device with index dev, on the stream (None: that
     device's current one)."""
+    if stream is not None and not isinstance(stream, int):
+        stream = _here(dev, stream).cuda_stream
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return _launch(name, dev, stream, *args)
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(dev)
-    elif not isinstance(stream, int):
-        stream = stream.cuda_stream
     st = getattr(L._lib or L.load(), name)(*args, stream)
     if st:
         raise L.MoeError(name, st, L.status_str(st))
@@ -57,7 +64,7 @@ def _side(dev, stream):
     if stream is None:
         return None
     if not isinstance(stream, int):
-        return stream
+        return _here(dev, stream)
     if stream == 0:
         return torch.cuda.default_stream(dev)
     return torch.cuda.ExternalStream(stream, device=dev)

@@ -6,7 +6,7 @@ import pytest
 from oracle import mx_oracle as O
 
 torch = pytest.importorskip("torch")
-from test_gpu_mx import DEV, bf16_rows, f64, mx  # noqa: E402,F401
+from test_gpu_mx import DEV, bf16_rows, f64, make, mx  # noqa: E402,F401
 
 pytestmark = pytest.mark.gpu
 
@@ -137,3 +137,19 @@ def test_default_stream_as_a_handle(mx):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     for a, b in zip(tiles, mx.MxBank(want).tiles["w13"]):
         assert torch.equal(a, b)
+
+
+def test_stream_of_another_device_is_refused(mx):
+    class StreamOfDevice1:
+        device_index, cuda_stream = 1, 0
+    s = StreamOfDevice1()
+    d = make(mx, 2, 64, 32, 2, 1)
+    B, w = d["B"], torch.zeros((1, 32, 64), device=DEV)
+    codes, scales = mx.quantize_rows(w[0])
+    for call in (lambda: mx.quantize_rows(w[0], stream=s), lambda: mx.dequantize_rows(codes, scales, stream=s),
+                 lambda: mx.quantize_bank(w, stream=s), lambda: mx.MxBank(mx.quantize_bank(w), stream=s),
+                 lambda: mx.run_layer(d["bank"], d["x"], d["logits"], B, stream=s),
+                 lambda: mx.gateup_silu(d["bank"], d["x"], B.offsets, B.sorted_pair, B, stream=s),
+                 lambda: mx.down_combine(d["bank"], B.h, B.w, B.offsets, B.pair_pos, B, stream=s)):
+        with pytest.raises(ValueError, match="device 1"):
+            call()

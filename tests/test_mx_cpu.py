@@ -241,3 +241,16 @@ def test_python_front_refuses_before_the_library():
         mx.gateup_silu(bank, x, offs, sp, b)
     with pytest.raises(TypeError):
         mx.gateup_silu(bank, x, offs.long(), sp, b)
+
+
+class StreamOfDevice1:
+    device_index, cuda_stream = 1, 0
+
+
+def test_stream_of_another_device_is_refused_before_the_library():
+    pytest.importorskip("torch")
+    from packed_bit_grouped_amd import mx
+    for call in (lambda: mx._side(0, StreamOfDevice1()),
+                 lambda: mx._launch("moe_mx4_quant_rows", 0, StreamOfDevice1(), None, 0, 0, 32, 32, None, None)):
+        with pytest.raises(ValueError, match="device 1"):
+            call()
