@@ -406,13 +406,20 @@ __device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, const We
     if (row >= nrows) continue;
     if (MODE == 0) {
       uint16_t* h = static_cast<uint16_t*>(ga.p.out) + (size_t)(t.orow + row) * ga.p.ld_out;
+      float gv[2 * NF], uv[2 * NF], hv[2 * NF];
+#pragma unroll
+      for (int i = 0; i < 2 * NF; ++i) {
+        gv[i] = acc[i / 4][m][i % 4];
+        uv[i] = acc[i / 4 + NF / 2][m][i % 4];
+      }
+      mx_silu_mul(gv, uv, hv);
 #pragma unroll
       for (int f = 0; f < NF / 2; ++f) {
         const int u = t.u0 + 16 * f + 4 * g;
         if (u >= t.U) continue;
         uint32_t v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = mx_bf16(mx_silu_mul(acc[f][m][i], acc[f + NF / 2][m][i]));
+        for (int i = 0; i < 4; ++i) v[i] = mx_bf16(hv[4 * f + i]);
         *reinterpret_cast<uint2*>(h + u) = make_uint2(v[0] | (v[1] << 16), v[2] | (v[3] << 16));
       }
     } else {

@@ -459,7 +459,10 @@ __global__ __launch_bounds__(kThreads) void mx_rows16_kernel(MxProj a, MxRoute r
   }
   const size_t o = (size_t)(orow + m) * a.ld_out + u0 + u;
   if (MODE == 0) {
-    if (u0 + u < U) static_cast<uint16_t*>(a.out)[o] = (uint16_t)mx_bf16(mx_silu_mul(v0, v1));
+    const float gv[1] = {v0}, uv[1] = {v1};
+    float hv[1];
+    mx_silu_mul(gv, uv, hv);
+    if (u0 + u < U) static_cast<uint16_t*>(a.out)[o] = (uint16_t)mx_bf16(hv[0]);
   } else {
     if (u0 + u < U) static_cast<float*>(a.out)[o] = v0;
     if (u0 + 16 + u < U) static_cast<float*>(a.out)[o + 16] = v1;

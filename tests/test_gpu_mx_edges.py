@@ -1,8 +1,9 @@
 """The MXFP4 operators where their other tests do not go: calls on another
-stream than the current one."""
+stream than the current one, SiLU far below zero."""
 import numpy as np
 import pytest
 
+import oracle
 from oracle import mx_oracle as O
 
 torch = pytest.importorskip("torch")
@@ -153,3 +154,49 @@ def test_stream_of_another_device_is_refused(mx):
                  lambda: mx.down_combine(d["bank"], B.h, B.w, B.offsets, B.pair_pos, B, stream=s)):
         with pytest.raises(ValueError, match="device 1"):
             call()
+
+
+# ---------------------------------------------------------------------------
+# the ends of the ranges
+
+# One expert, 16-row tiles; four experts, tiles of up to 160 rows.
+FEW_ROWS, MANY_ROWS = (80, 64, 32, 1), (2560, 2048, 256, 4)
+
+
+@pytest.mark.parametrize("act", ["a16", "a4"])
+@pytest.mark.parametrize("dims", [FEW_ROWS, MANY_ROWS], ids=["few", "many"])
+def test_silu_far_below_zero(mx, dims, act):
+    """h = SiLU(g) * u where SiLU(g) is below fp32's smallest number and u
+    brings the product back: one weight of 1 each for g and u, so that both
+    are exact."""
+    T, H, I, E = dims
+    w = np.zeros((E, 2 * I, H))
+    w[:, :I, 0] = 1.0
+    w[:, I:, 32] = 1.0
+    codes, scales = O.quantise(w)
+    bank = mx.MxBank((torch.from_numpy(codes).to(DEV), torch.from_numpy(scales).to(DEV)))
+    if act == "a4":   # a code and a scale hold these exactly
+        g = -np.array([0.5, 4, 12, 48, 64, 96, 128, 192, 256])
+    else:
+        g = -np.array([0.5, 4, 12, 48, 63.5, 64.5, 80, 86, 87.5, 88, 89, 104, 128, 160, 176, 182, 186])
+    u = 2.0 ** np.array([0, 20, 90, 126])
+    pairs = np.array([(a, b) for a in g for b in u])
+    x = np.zeros((T, H), dtype=np.float32)
+    x[:, [0, 32]] = pairs[np.arange(T) % len(pairs)]
+    B = mx.MxBuffers(T, H, I, E, 1, act=act, device=DEV)
+    ids = (np.arange(T) % E).astype(np.int32)[:, None]
+    perm = oracle.permute(ids, E, 16)
+    xt = torch.from_numpy(x).bfloat16().to(DEV)
+    h = f64(mx.gateup_silu(bank, xt, torch.from_numpy(perm["offsets"]).to(DEV),
+                           torch.from_numpy(perm["sorted_pair"]).to(DEV), B))
+    xv = O.activations(f64(xt), act)[perm["sorted_pair"]]
+    gv, uv = xv[:, 0], xv[:, 32]
+    want = gv / (1 + np.exp(-gv)) * uv
+    # the exponential's argument is rounded by |g| * 1.45 half units, which it
+    # turns into |g| units of relative error at most; with a factor below 2^-126
+    # that fp32 holds in steps of 2^-149 (e^(g/2) >= e^-93.5 = 2^-134.9: 2^-15);
+    # a few units for the products; then half a step of bf16 and its smallest step
+    rel = (2 * np.abs(gv) + 16) * O.EPS32 + 2.0 ** -14
+    bound = (rel + 2.0 ** -8 * (1 + rel)) * np.abs(want) + 2.0 ** -133
+    assert (np.abs(h - want[:, None]) <= bound[:, None]).all(), sorted(
+        {(float(a), float(b)) for a, b, bad in zip(gv, uv, (np.abs(h - want[:, None]) > bound[:, None]).any(1)) if bad})
