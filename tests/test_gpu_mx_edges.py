@@ -1,5 +1,6 @@
 """The MXFP4 operators where their other tests do not go: calls on another
-stream than the current one, SiLU far below zero."""
+stream than the current one, SiLU far below zero, scale
+bytes next to the ends."""
 import numpy as np
 import pytest
 
@@ -7,7 +8,7 @@ import oracle
 from oracle import mx_oracle as O
 
 torch = pytest.importorskip("torch")
-from test_gpu_mx import DEV, bf16_rows, f64, make, mx  # noqa: E402,F401
+from test_gpu_mx import DEV, bf16_rows, check_h, f64, make, mx, tables  # noqa: E402,F401
 
 pytestmark = pytest.mark.gpu
 
@@ -200,3 +201,25 @@ def test_silu_far_below_zero(mx, dims, act):
     bound = (rel + 2.0 ** -8 * (1 + rel)) * np.abs(want) + 2.0 ** -133
     assert (np.abs(h - want[:, None]) <= bound[:, None]).all(), sorted(
         {(float(a), float(b)) for a, b, bad in zip(gv, uv, (np.abs(h - want[:, None]) > bound[:, None]).any(1)) if bad})
+
+
+@pytest.mark.parametrize("act", ["a16", "a4"])
+@pytest.mark.parametrize("dims", [(20, 256, 64, 3), (2560, 2048, 256, 4)], ids=["few", "many"])
+@pytest.mark.parametrize("byte,unit", [(1, 122), (2, 121), (250, -124), (251, -125)])
+def test_scale_bytes_next_to_the_ends(mx, dims, act, byte, unit):
+    """Weights of one scale byte next to the smallest or the largest, every
+    code among them, with x of the size that brings the sums back to order 1."""
+    T, H, I, E = dims
+    rng = np.random.default_rng(byte)
+    d = make(mx, T, H, I, E, 1, act=act, seed=byte)
+    codes = rng.integers(0, 256, (E, 2 * I, H // 2), dtype=np.uint8)
+    scales = np.full((E, 2 * I, H // 32), byte, dtype=np.uint8)
+    d["v13"] = O.values(codes, scales)
+    d["bank"] = mx.MxBank((torch.from_numpy(codes).to(DEV), torch.from_numpy(scales).to(DEV)))
+    x = np.ldexp(rng.standard_normal((T, H)) / np.sqrt(H), unit)
+    d["x"] = torch.from_numpy(x.astype(np.float32)).bfloat16().to(DEV)
+    ids, w, perm = tables(d)
+    h = mx.gateup_silu(d["bank"], d["x"], torch.from_numpy(perm["offsets"]).to(DEV),
+                       torch.from_numpy(perm["sorted_pair"]).to(DEV), d["B"])
+    assert np.abs(f64(h)).max() > 0.1
+    check_h(d, h, perm)
