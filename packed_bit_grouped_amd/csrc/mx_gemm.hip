@@ -130,14 +130,17 @@ struct Tile {
   int orow;             // first output row
 };
 
-// The wave's weights: four 16-row blocks; blocks past the end lie past the
-// buffer, where nothing is read.
-constexpr int kNone = 0x40000000;
+// The wave's weights: four 16-row blocks; blocks and steps past the end lie past
+// the buffer (at most 2^30 bytes), where nothing is read.  Offsets are unsigned:
+// a step past the end of a block past the end is twice kNone.
+constexpr uint32_t kNone = 0x40000000;
+static_assert(2ull * kNone <= UINT32_MAX, "no offset comes round to a valid one");
 
 template <int NF>
 struct Weights {
   __amdgpu_buffer_rsrc_t crs, srs;
-  int coff[NF], soff[NF], n_st;
+  uint32_t coff[NF], soff[NF];
+  int n_st;
 
   template <int MODE>
   __device__ __forceinline__ void init(const Tile& t, const uint8_t* w, const uint8_t* ws, int e) {
@@ -157,16 +160,16 @@ struct Weights {
     }
   }
   __device__ __forceinline__ void load_c(int st, int j, WStep<NF>& w) const {
-    const int o = st < n_st ? st * 2048 + j * 1024 : kNone;
+    const uint32_t o = st < n_st ? st * 2048 + j * 1024 : kNone;
 #pragma unroll
     for (int f = 0; f < NF; ++f)
-      w.c[f][j] = __builtin_amdgcn_raw_buffer_load_b128(crs, coff[f] + o, 0, 2);
+      w.c[f][j] = __builtin_amdgcn_raw_buffer_load_b128(crs, (int)(coff[f] + o), 0, 2);
   }
   __device__ __forceinline__ void load_s(int st, WStep<NF>& w) const {
-    const int o = st < n_st ? (st >> 1) * 256 + (st & 1) * 2 : kNone;
+    const uint32_t o = st < n_st ? (st >> 1) * 256 + (st & 1) * 2 : kNone;
 #pragma unroll
     for (int f = 0; f < NF; ++f)
-      w.s[f] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(srs, soff[f] + o, 0, 0);
+      w.s[f] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(srs, (int)(soff[f] + o), 0, 0);
   }
   __device__ __forceinline__ void load(int st, WStep<NF>& w) const {
     load_c(st, 0, w);
