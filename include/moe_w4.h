@@ -628,7 +628,7 @@ moe_status moe_mx4_dequant_rows(const uint8_t* codes, const uint8_t* scales, int
  *   dst_codes   moe_mx4_bank_code_bytes(n, N, K) bytes, 16-byte aligned
  *   dst_scales  moe_mx4_bank_scale_bytes(n, N, K) bytes, 4-byte aligned
  * Limits: N % 16 == 0, K % 32 == 0 (else MOE_E_UNSUPPORTED; the sizes are 0
- * for what is refused).  codes 16-byte aligned; no overlap.
+ * for what is refused and for more than 2^64 bytes).  codes 16-byte aligned; no overlap.
  * ------------------------------------------------------------------- */
 size_t moe_mx4_bank_code_bytes(int n, int N, int K);
 size_t moe_mx4_bank_scale_bytes(int n, int N, int K);
@@ -660,8 +660,11 @@ size_t moe_mx4_workspace_bytes(int act, int T, int H, int I, int E, int k, int n
  *              t.  Rows past offsets[E] and columns past a row's own I (or
  *              I_shared) are left as they were
  *   flags      0
- * Limits: H, I, I_shared multiples of 32, E <= 512, T <= 65535, T*k < 2^24,
- * T*(k + n_shared)*H < 2^31 (else MOE_E_UNSUPPORTED).  x, h 16-byte aligned.
+ * Limits: H, I, I_shared multiples of 32 and below 2^30, E <= 512, T and
+ * n_shared <= 65535, T*k < 2^24, T*(k + n_shared)*H and that with I or I_shared
+ * < 2^31, (T*k/16 + min(E, T*k) + n_shared*ceil(T/16)) * max(I, I_shared) < 2^28
+ * and the same with H < 2^29 (workgroups of a launch; more work where larger
+ * tiles take it); else MOE_E_UNSUPPORTED.  x, h 16-byte aligned.
  * ------------------------------------------------------------------- */
 moe_status moe_mx4_gateup_silu(int act, const uint16_t* x, int T, int H, int I, int E, int k,
                                const moe_mxbank* w13, const moe_mxbank* w13_shared, int n_shared,

@@ -20,19 +20,36 @@ int ld_h_of(int I, int n_shared, int I_shared) {
   return n_shared > 0 && I_shared > I ? I_shared : I;
 }
 
-moe_status check_shape(int act, int T, int H, int I, int E, int k, int n_shared, int I_shared) {
-  if (act != MOE_A16 && act != MOE_A4) return MOE_E_INVAL;
-  if (T < 0 || H <= 0 || I <= 0 || E <= 0 || k <= 0 || n_shared < 0) return MOE_E_INVAL;
-  if (k > E) return MOE_E_INVAL;
-  if (n_shared > 0 && I_shared <= 0) return MOE_E_INVAL;
-  if (H % kMxBlock || I % kMxBlock || (n_shared > 0 && I_shared % kMxBlock))
-    return MOE_E_UNSUPPORTED;
-  if (E > kPermMaxE || T > 65535 || n_shared > 65535) return MOE_E_UNSUPPORTED;
-  if ((long long)T * k >= (1LL << 24)) return MOE_E_UNSUPPORTED;
-  const long long rows = (long long)T * ((long long)k + n_shared);
-  if (rows * H >= (1LL << 31) || rows * ld_h_of(I, n_shared, I_shared) >= (1LL << 31))
-    return MOE_E_UNSUPPORTED;
-  return MOE_OK;
+// Sizes of the projections (pointers null).
+MxProj gateup_dims(int T, int H, int I, int E, int k, int n_shared, int I_shared) {
+  MxProj a;
+  std::memset(&a, 0, sizeof(a));
+  a.T = T;
+  a.k = k;
+  a.P = T * k;
+  a.E = E;
+  a.n_shared = n_shared;
+  a.ld_in = H;
+  a.K = a.K_sh = H;
+  a.U = I;
+  a.U_sh = n_shared > 0 ? I_shared : 0;
+  a.ld_out = ld_h_of(I, n_shared, I_shared);
+  return a;
+}
+
+MxProj down_dims(int T, int H, int I, int E, int k, int n_shared, int I_shared) {
+  MxProj a = gateup_dims(T, H, I, E, k, n_shared, I_shared);
+  a.ld_in = ld_h_of(I, n_shared, I_shared);
+  a.K = I;
+  a.K_sh = n_shared > 0 ? I_shared : I;
+  a.U = a.U_sh = a.ld_out = H;
+  return a;
+}
+
+// n matrices of one size, 0 beyond any memory (a matrix has fewer than 2^62 bytes).
+size_t bank_bytes(int n, size_t one) {
+  size_t all;
+  return __builtin_mul_overflow((size_t)n, one, &all) ? 0 : all;
 }
 
 bool bank_ok(const moe_mxbank* b) {
@@ -68,9 +85,7 @@ bool large_tiles(const MxProj& a, bool act4, int mode) {
   const long long tiles = a.P / 160 + (a.E < a.P ? a.E : a.P) / 2;
   if (tiles * work < 500) return false;
   if (act4 ? a.P < 16LL * a.E : a.P * work < (mode == 0 ? 24576 : 40960)) return false;
-  const long long rows = mode == 0 ? a.T : (long long)a.P + (long long)a.n_shared * a.T;
-  return mx_gemm_ok(act4, rows, a.ld_in, a.K, a.K_sh, mode == 0 ? 2 * a.U : a.U,
-                    mode == 0 ? 2 * a.U_sh : a.U_sh);
+  return mx_gemm_ok(a, mode, act4);
 }
 
 // Pieces of weight blocks that all workgroups on tiles of 16 rows pass, at most:
@@ -100,6 +115,30 @@ bool codes_first(const MxProj& a, int mode) { return rows16_work(a, mode) > kCod
 bool route_inside(const MxProj& a, bool act4) {
   return mx_route_gateup_ok(a.T, a.k, a.E, a.ld_in) && !large_tiles(a, act4, 0) &&
          rows16_work(a, 0) < (act4 ? 2 : 5) * kCodesWork;
+}
+
+moe_status check_shape(int act, int T, int H, int I, int E, int k, int n_shared, int I_shared) {
+  if (act != MOE_A16 && act != MOE_A4) return MOE_E_INVAL;
+  if (T < 0 || H <= 0 || I <= 0 || E <= 0 || k <= 0 || n_shared < 0) return MOE_E_INVAL;
+  if (k > E) return MOE_E_INVAL;
+  if (n_shared > 0 && I_shared <= 0) return MOE_E_INVAL;
+  if (H % kMxBlock || I % kMxBlock || (n_shared > 0 && I_shared % kMxBlock))
+    return MOE_E_UNSUPPORTED;
+  if (H >= kMxMaxLen || I >= kMxMaxLen || (n_shared > 0 && I_shared >= kMxMaxLen))
+    return MOE_E_UNSUPPORTED;
+  if (E > kPermMaxE || T > 65535 || n_shared > 65535) return MOE_E_UNSUPPORTED;
+  if ((long long)T * k >= (1LL << 24)) return MOE_E_UNSUPPORTED;
+  const long long rows = (long long)T * ((long long)k + n_shared);
+  if (rows * H >= (1LL << 31) || rows * ld_h_of(I, n_shared, I_shared) >= (1LL << 31))
+    return MOE_E_UNSUPPORTED;
+  // more workgroups than a launch holds (the routed launch has one more than counted)
+  const int act4 = act == MOE_A4;
+  const MxProj g = gateup_dims(T, H, I, E, k, n_shared, I_shared);
+  const MxProj d = down_dims(T, H, I, E, k, n_shared, I_shared);
+  if ((mx_rows16_grid(g, 0) >= kMxMaxGrid && !large_tiles(g, act4, 0)) ||
+      (mx_rows16_grid(d, 1) >= kMxMaxGrid && !large_tiles(d, act4, 1)))
+    return MOE_E_UNSUPPORTED;
+  return MOE_OK;
 }
 
 MxWsLayout layout(int act, int T, int H, int I, int E, int k, int n_shared, int I_shared) {
@@ -132,35 +171,13 @@ moe_status check_ws(const void* ws, size_t bytes, const MxWsLayout& L) {
   return ws && aligned(ws, 256) && bytes >= L.total ? MOE_OK : MOE_E_WORKSPACE;
 }
 
-// Arguments shared by the projections; x, w, U and out differ.
-MxProj proj(int T, int E, int k, int n_shared, const moe_mxbank* w, const moe_mxbank* w_sh) {
-  MxProj a;
-  std::memset(&a, 0, sizeof(a));
+void set_banks(MxProj& a, const moe_mxbank* w, const moe_mxbank* w_sh) {
   a.w = w->codes;
   a.ws = w->scales;
-  if (n_shared > 0) {
+  if (a.n_shared > 0) {
     a.w_sh = w_sh->codes;
     a.ws_sh = w_sh->scales;
   }
-  a.T = T;
-  a.k = k;
-  a.P = T * k;
-  a.E = E;
-  a.n_shared = n_shared;
-  return a;
-}
-
-MxProj gateup_proj(const uint16_t* x, int T, int H, int I, int E, int k, const moe_mxbank* w13,
-                   const moe_mxbank* w13_shared, int n_shared, int I_shared, uint16_t* h) {
-  MxProj a = proj(T, E, k, n_shared, w13, w13_shared);
-  a.x = x;
-  a.ld_in = H;
-  a.K = a.K_sh = H;
-  a.U = I;
-  a.U_sh = n_shared > 0 ? I_shared : 0;
-  a.out = h;
-  a.ld_out = ld_h_of(I, n_shared, I_shared);
-  return a;
 }
 
 // The projections' launches, every argument checked.
@@ -195,16 +212,12 @@ moe_status down(int act, const uint16_t* h, int T, int H, int I, int E, int k,
   const int act4 = act == MOE_A4, ld_h = ld_h_of(I, n_shared, I_shared), hp = mx_pad_k(ld_h);
   const int P = T * k, R_sh = n_shared * T;
   if (n_shared == 0) shared_gate = nullptr;
-  MxProj a = proj(T, E, k, n_shared, w2, w2_shared);
+  MxProj a = down_dims(T, H, I, E, k, n_shared, I_shared);
+  set_banks(a, w2, w2_shared);
   a.x = h;
-  a.ld_in = ld_h;
-  a.K = I;
-  a.K_sh = n_shared > 0 ? I_shared : I;
-  a.U = a.U_sh = H;
   a.offsets = offsets;
   float* y = reinterpret_cast<float*>(ws + L.y);
   a.out = y;
-  a.ld_out = H;
   hipError_t e = hipSuccess;
   const bool gemm = large_tiles(a, act4, 1);
   const uint16_t* h_sh = h + (size_t)P * ld_h;
@@ -267,12 +280,12 @@ moe_status moe_mx4_dequant_rows(const uint8_t* codes, const uint8_t* scales, int
 
 size_t moe_mx4_bank_code_bytes(int n, int N, int K) {
   if (n <= 0 || N <= 0 || K <= 0 || N % 16 || K % kMxBlock) return 0;
-  return n * mx_code_bytes(N, K);
+  return bank_bytes(n, mx_code_bytes(N, K));
 }
 
 size_t moe_mx4_bank_scale_bytes(int n, int N, int K) {
   if (n <= 0 || N <= 0 || K <= 0 || N % 16 || K % kMxBlock) return 0;
-  return n * mx_scale_bytes(N, K);
+  return bank_bytes(n, mx_scale_bytes(N, K));
 }
 
 moe_status moe_mx4_tile_bank(const uint8_t* codes, const uint8_t* scales, int n, int N, int K,
@@ -312,8 +325,11 @@ moe_status moe_mx4_gateup_silu(int act, const uint16_t* x, int T, int H, int I, 
   if (st != MOE_OK) return st;
   st = device_usable();
   if (st != MOE_OK) return st;
-  return gateup(act, gateup_proj(x, T, H, I, E, k, w13, w13_shared, n_shared, I_shared, h), L,
-                offsets, sorted_pair, static_cast<char*>(workspace),
+  MxProj a = gateup_dims(T, H, I, E, k, n_shared, I_shared);
+  set_banks(a, w13, w13_shared);
+  a.x = x;
+  a.out = h;
+  return gateup(act, a, L, offsets, sorted_pair, static_cast<char*>(workspace),
                 static_cast<hipStream_t>(stream));
 }
 
@@ -363,7 +379,10 @@ moe_status moe_mx4_layer(int act, const float* logits, const uint16_t* x, int T,
   if (st != MOE_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
-  const MxProj a = gateup_proj(x, T, H, I, E, k, w13, w13_shared, n_shared, I_shared, h);
+  MxProj a = gateup_dims(T, H, I, E, k, n_shared, I_shared);
+  set_banks(a, w13, w13_shared);
+  a.x = x;
+  a.out = h;
   if (route_inside(a, act == MOE_A4)) {
     // a few tokens: routing, sort and gate/up in one launch
     st = from_hip(launch_mx_route_gateup(a, act == MOE_A4, logits, renormalize, topk_ids, topk_w,

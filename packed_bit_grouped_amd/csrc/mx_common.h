@@ -16,6 +16,8 @@ typedef __bf16 mx_bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kMxBlock = 32;      // values per scale
 constexpr int kMxNanScale = 255;  // scale byte of a block that held inf or NaN
+constexpr int kMxMaxLen = 1 << 30;  // H, I, I_shared: 2 I rows and padded rows are ints
+constexpr long long kMxMaxGrid = (1LL << 24) - 1;  // workgroups of 256: below 2^32 threads a launch
 
 // Workspace of the projection calls (byte offsets).
 struct MxWsLayout {
@@ -37,7 +39,7 @@ struct MxWsLayout {
 // the gate/up product of 4096 tokens with MXFP4 activations (H 4096, I 1536,
 // 256 experts, k 8) took 716 us where the tiles took 478 (398 now).
 constexpr int kMxPieceK = 128;
-inline __host__ __device__ int mx_pieces(int K) { return (K + kMxPieceK - 1) / kMxPieceK; }
+inline __host__ __device__ int mx_pieces(int K) { return (int)(((uint32_t)K + kMxPieceK - 1) / kMxPieceK); }
 inline __host__ __device__ size_t mx_code_bytes(int N, int K) {
   return (size_t)(N / 16) * mx_pieces(K) * 1024;
 }
@@ -220,6 +222,7 @@ hipError_t launch_mx_pad_rows(const uint16_t* src, int R, int C, int ld, uint16_
                               hipStream_t st);
 // Grouped projections; mode 0: gate/up with SiLU*mul to h, 1: down to y.
 // Tiles of 16 rows, K split over the workgroup's waves:
+long long mx_rows16_grid(const MxProj& a, int mode);   // its workgroups, at most kMxMaxGrid
 hipError_t launch_mx_rows16(const MxProj& a, int mode, int act4, hipStream_t st);
 // The same for a few tokens with their routing and sort in the launch:
 bool mx_route_gateup_ok(int T, int k, int E, int H);
@@ -227,7 +230,7 @@ hipError_t launch_mx_route_gateup(const MxProj& a, int act4, const float* logits
                                   int32_t* ids, float* w, int32_t* counts, int32_t* offsets,
                                   int32_t* sorted_pair, int32_t* pair_pos, hipStream_t st);
 // Tiles of up to 160 rows (A16: rows of whole steps, K % 256 == 0 or a padded copy):
-bool mx_gemm_ok(int act4, long long rows, int ld, int K, int K_sh, int N, int N_sh);
+bool mx_gemm_ok(const MxProj& a, int mode, int act4);
 hipError_t launch_mx_gemm(const MxProj& a, int mode, int act4, hipStream_t st);
 
 }  // namespace moe

@@ -559,22 +559,16 @@ size_t lds_bytes(bool act4, int KP, int tm, int nf) {
   return kRowsMax * 4 + ring * 16 + (act4 ? (size_t)tm * sc_pitch(KP) + 1024 : 0);
 }
 
-}  // namespace
+// The launch's tiles and grid.
+struct Plan {
+  bool narrow;
+  int KP, tm, sh_per, max_tiles, n_ub;
+  long long grid;
+};
 
-bool mx_gemm_ok(int act4, long long rows, int ld, int K, int K_sh, int N, int N_sh) {
-  const int KP = mx_pad_k(K > K_sh ? K : K_sh);
-  if (lds_bytes(act4, KP, kRowsMax, 4) > 160 * 1024) return false;
-  // 32-bit offsets into one matrix and into the activation rows
-  const long long stride = act4 ? mx_pad_k(ld) / 2 : 2LL * mx_pad_k(ld);
-  if (rows * stride >= (1LL << 31)) return false;
-  return mx_code_bytes(N, K) < (1u << 30) && mx_code_bytes(N_sh, K_sh) < (1u << 30);
-}
-
-hipError_t launch_mx_gemm(const MxProj& a, int mode, int act4, hipStream_t st) {
-  GemmArgs ga;
-  ga.p = a;
-  ga.KP = mx_pad_k(a.ld_in);   // row length of the activation copy
-  ga.sc_pitch = sc_pitch(ga.KP);
+Plan plan(const MxProj& a, int mode, int act4) {
+  Plan p;
+  p.KP = mx_pad_k(a.ld_in);   // row length of the activation copy
   // Two workgroups per compute unit, each with half the weight rows per wave: one's
   // start and stores pass behind the other's loop (by clock stamps 8 of 31 us of a
   // gate/up workgroup, 10 of 20 of down, whose loop alone reads 6.3 TB/s), but the
@@ -583,19 +577,39 @@ hipError_t launch_mx_gemm(const MxProj& a, int mode, int act4, hipStream_t st) {
   // 256 rows 32/47, 34/35; 256 experts, 32 rows 296/278, 241/231, 64 rows 321/308,
   // 311/289, 128 rows 389/400, 460/436 (with the sum).  H 2048, I 768, 128
   // experts: 16 rows 45/42, 41/38, 64 rows 53/52, 62/61, 128 rows 63/68, 89/93.
-  const bool narrow = act4 && a.P <= 96LL * a.E && lds_bytes(true, ga.KP, kRowsNarrow, 2) <= 80 * 1024;
-  const int tm = narrow ? kRowsNarrow : kRowsMax, nf = narrow ? 2 : 4;
-  ga.sh_per = (a.T + tm - 1) / tm;
-  ga.max_tiles = moe_permute_max_tiles(a.T, a.k, a.E, tm);
-  const int step = (mode == 0 ? 32 : 64) * nf;
+  p.narrow = act4 && a.P <= 96LL * a.E && lds_bytes(true, p.KP, kRowsNarrow, 2) <= 80 * 1024;
+  p.tm = p.narrow ? kRowsNarrow : kRowsMax;
+  p.sh_per = (a.T + p.tm - 1) / p.tm;
+  p.max_tiles = moe_permute_max_tiles(a.T, a.k, a.E, p.tm);
+  const int step = (mode == 0 ? 32 : 64) * (p.narrow ? 2 : 4);
   const int U = a.n_shared > 0 && a.U_sh > a.U ? a.U_sh : a.U;
-  ga.n_ub = (U + step - 1) / step;
-  const long long slots = (long long)a.n_shared * ga.sh_per + ga.max_tiles;
-  const long long grid = (slots + kXcd - 1) / kXcd * kXcd * ga.n_ub;
-  if (grid >= (1LL << 31)) return hipErrorInvalidValue;
-  const size_t lds = lds_bytes(act4, ga.KP, tm, nf);
-#define MX_GO(MODE, ACT4, NF, TM) mx_gemm_kernel<MODE, ACT4, NF, TM><<<(int)grid, kThreads, lds, st>>>(ga)
-  if (narrow) {
+  p.n_ub = (U + step - 1) / step;
+  const long long slots = (long long)a.n_shared * p.sh_per + p.max_tiles;
+  p.grid = (slots + kXcd - 1) / kXcd * kXcd * p.n_ub;
+  return p;
+}
+
+}  // namespace
+
+bool mx_gemm_ok(const MxProj& a, int mode, int act4) {
+  const int KP = mx_pad_k(a.K > a.K_sh ? a.K : a.K_sh);
+  if (lds_bytes(act4, KP, kRowsMax, 4) > 160 * 1024) return false;
+  // 32-bit offsets into one matrix and into the activation rows
+  const long long rows = mode == 0 ? a.T : (long long)a.P + (long long)a.n_shared * a.T;
+  const long long stride = act4 ? mx_pad_k(a.ld_in) / 2 : 2LL * mx_pad_k(a.ld_in);
+  if (rows * stride >= (1LL << 31)) return false;
+  const int per = mode == 0 ? 2 : 1;
+  return mx_code_bytes(per * a.U, a.K) < (1u << 30) && mx_code_bytes(per * a.U_sh, a.K_sh) < (1u << 30) &&
+         plan(a, mode, act4).grid <= kMxMaxGrid;
+}
+
+hipError_t launch_mx_gemm(const MxProj& a, int mode, int act4, hipStream_t st) {
+  const Plan p = plan(a, mode, act4);
+  const GemmArgs ga = {a, p.KP, p.n_ub, p.max_tiles, p.sh_per, sc_pitch(p.KP)};
+  const size_t lds = lds_bytes(act4, p.KP, p.tm, p.narrow ? 2 : 4);
+#define MX_GO(MODE, ACT4, NF, TM) \
+  mx_gemm_kernel<MODE, ACT4, NF, TM><<<(int)p.grid, kThreads, lds, st>>>(ga)
+  if (p.narrow) {
     if (mode == 0) MX_GO(0, true, 2, kRowsNarrow);
     else MX_GO(1, true, 2, kRowsNarrow);
   } else if (act4) {

@@ -469,18 +469,19 @@ __global__ __launch_bounds__(kThreads) void mx_rows16_kernel(MxProj a, MxRoute r
   }
 }
 
-int max_slots(const MxProj& a) {
-  return a.n_shared * ((a.T + kTM - 1) / kTM) + moe_permute_max_tiles(a.T, a.k, a.E, kTM);
+// Blocks of columns: of 16 units, or of 32 down rows.
+int col_blocks(const MxProj& a, int mode) {
+  const int step = mode == 0 ? 16 : 32;
+  const int U = a.n_shared > 0 && a.U_sh > a.U ? a.U_sh : a.U;
+  return (U + step - 1) / step;
 }
 
 template <int MODE, bool ACT4, bool XQ, bool ROUTE>
 hipError_t launch(const MxProj& a, const MxRoute& ro, hipStream_t st) {
   const int n_sh_tiles = a.n_shared * ((a.T + kTM - 1) / kTM);
-  const int step = MODE == 0 ? 16 : 32;
-  const int U = a.n_shared > 0 && a.U_sh > a.U ? a.U_sh : a.U;
-  const int n_ub = (U + step - 1) / step;
-  const long long grid = (long long)max_slots(a) * n_ub + (ROUTE ? 1 : 0);
-  if (grid >= (1LL << 31)) return hipErrorInvalidValue;
+  const int n_ub = col_blocks(a, MODE);
+  const long long grid = mx_rows16_grid(a, MODE) + (ROUTE ? 1 : 0);
+  if (grid > kMxMaxGrid) return hipErrorInvalidValue;
   const int K = a.n_shared > 0 && a.K_sh > a.K ? a.K_sh : a.K;
   const int pieces = mx_pieces(K);
   const size_t lds = ROUTE ? RouteLds::bytes(a.T, a.E, a.ld_in) : 0;
@@ -498,6 +499,12 @@ hipError_t launch(const MxProj& a, const MxRoute& ro, hipStream_t st) {
 }
 
 }  // namespace
+
+long long mx_rows16_grid(const MxProj& a, int mode) {
+  const long long slots =
+      a.n_shared * ((a.T + kTM - 1LL) / kTM) + moe_permute_max_tiles(a.T, a.k, a.E, kTM);
+  return slots * col_blocks(a, mode);
+}
 
 hipError_t launch_mx_rows16(const MxProj& a, int mode, int act4, hipStream_t st) {
   const MxRoute none = {};

@@ -254,3 +254,23 @@ def test_stream_of_another_device_is_refused_before_the_library():
                  lambda: mx._launch("moe_mx4_quant_rows", 0, StreamOfDevice1(), None, 0, 0, 32, 32, None, None)):
         with pytest.raises(ValueError, match="device 1"):
             call()
+
+
+def test_sizes_next_to_the_range_of_int():
+    """Sums and products of sizes near 2^31 come out right or are refused
+    before anything is launched."""
+    K = 2 ** 31 - 32
+    assert L.moe_mx4_bank_code_bytes(1, 16, K) == (2 ** 31 // 128) * 1024
+    assert L.moe_mx4_bank_scale_bytes(1, 16, K) == (2 ** 31 // 512) * 256
+    assert L.moe_mx4_bank_code_bytes(3, 2 ** 31 - 16, 32) == 3 * (2 ** 27 - 1) * 1024
+    assert L.moe_mx4_bank_code_bytes(2 ** 31 - 1, 2 ** 31 - 16, K) == 0
+    # 2 I rows, and padded rows, are ints
+    for kw in (dict(T=0, H=K), dict(T=0, I=K), dict(T=1, k=1, I=2 ** 30), dict(T=1, k=1, H=2 ** 30),
+               dict(T=0, n_shared=1, I_shared=K)):
+        assert L.moe_mx4_workspace_bytes(*dict(SHAPE, **kw).values()) == 0, kw
+    # more threads than a launch holds: many experts of very many units, many shared experts
+    for kw in (dict(T=1, H=32, I=1 << 23, E=512, k=128), dict(T=1, H=32, I=32, n_shared=32768, I_shared=16384)):
+        assert L.moe_mx4_workspace_bytes(*dict(SHAPE, **kw).values()) == 0, kw
+        a = dict(kw, w13_shared=BANK if "n_shared" in kw else None)
+        assert _gateup(**a) == L.MOE_E_UNSUPPORTED, kw
+    assert L.moe_mx4_workspace_bytes(*dict(SHAPE, T=1, H=32, I=32, n_shared=8192, I_shared=16384).values()) > 0
