@@ -60,7 +60,7 @@
 extern "C" {
 #endif
 
-#define MOE_W4_ABI_VERSION 5
+#define MOE_W4_ABI_VERSION 6
 
 /* Version of the compiled library.  The Python binding refuses to load a
  * library whose version differs from the header it was written for. */
@@ -646,6 +646,11 @@ typedef struct moe_mxbank {
  * be cleared); 0 for sizes they refuse. */
 size_t moe_mx4_workspace_bytes(int act, int T, int H, int I, int E, int k, int n_shared,
                                int I_shared);
+
+/* Most rows of a tile with which the gate/up (down = 0) or the down call (1)
+ * of these sizes runs: 16, 144 or 160 (host only); 0 for sizes they refuse. */
+int moe_mx4_tile_rows(int act, int T, int H, int I, int E, int k, int n_shared, int I_shared,
+                      int down);
 
 /* ---------------------------------------------------------------------
  * moe_mx4_gateup_silu -- grouped gate/up projection with SiLU(g) * u of

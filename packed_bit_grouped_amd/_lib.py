@@ -14,7 +14,7 @@ from typing import Optional
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe_w4.so")
-ABI_VERSION = 5
+ABI_VERSION = 6
 
 MOE_OK, MOE_E_INVAL, MOE_E_UNSUPPORTED, MOE_E_DEVICE, MOE_E_WORKSPACE = 0, -1, -2, -3, -4
 MOE_A16, MOE_A8, MOE_A4 = 0, 1, 2
@@ -110,6 +110,7 @@ _SIGS = {
     "moe_mx4_tile_bank": (c_int, [c_void_p, c_void_p, c_int, c_int, c_int, c_void_p, c_void_p,
                                   c_void_p]),
     "moe_mx4_workspace_bytes": (c_size_t, [c_int] * 8),
+    "moe_mx4_tile_rows": (c_int, [c_int] * 9),
     "moe_mx4_gateup_silu": (c_int, [c_int, c_void_p, c_int, c_int, c_int, c_int, c_int,
                                     c_void_p, c_void_p, c_int, c_int, c_void_p, c_void_p,
                                     c_void_p, c_void_p, c_size_t, c_int, c_void_p]),
@@ -397,6 +398,10 @@ def moe_mx4_tile_bank(codes, scales, n, N, K, dst_codes, dst_scales, stream=None
 
 def moe_mx4_workspace_bytes(act, T, H, I, E, k, n_shared=0, I_shared=0) -> int:
     return load().moe_mx4_workspace_bytes(act, T, H, I, E, k, n_shared, I_shared)
+
+
+def moe_mx4_tile_rows(act, T, H, I, E, k, n_shared=0, I_shared=0, down=0) -> int:
+    return load().moe_mx4_tile_rows(act, T, H, I, E, k, n_shared, I_shared, down)
 
 
 def moe_mx4_gateup_silu(act, x, T, H, I, E, k, w13, w13_shared, n_shared, I_shared, offsets,

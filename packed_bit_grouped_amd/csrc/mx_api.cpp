@@ -308,6 +308,16 @@ size_t moe_mx4_workspace_bytes(int act, int T, int H, int I, int E, int k, int n
   return layout(act, T, H, I, E, k, n_shared, I_shared).total;
 }
 
+int moe_mx4_tile_rows(int act, int T, int H, int I, int E, int k, int n_shared, int I_shared,
+                      int down) {
+  if (check_shape(act, T, H, I, E, k, n_shared, I_shared) != MOE_OK) return 0;
+  if (down != 0 && down != 1) return 0;
+  const int act4 = act == MOE_A4;
+  const MxProj a = down ? down_dims(T, H, I, E, k, n_shared, I_shared)
+                        : gateup_dims(T, H, I, E, k, n_shared, I_shared);
+  return large_tiles(a, act4, down) ? mx_gemm_tile_rows(a, down, act4) : 16;
+}
+
 moe_status moe_mx4_gateup_silu(int act, const uint16_t* x, int T, int H, int I, int E, int k,
                                const moe_mxbank* w13, const moe_mxbank* w13_shared, int n_shared,
                                int I_shared, const int32_t* offsets, const int32_t* sorted_pair,

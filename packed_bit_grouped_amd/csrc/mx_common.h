@@ -231,6 +231,7 @@ hipError_t launch_mx_route_gateup(const MxProj& a, int act4, const float* logits
                                   int32_t* sorted_pair, int32_t* pair_pos, hipStream_t st);
 // Tiles of up to 160 rows (A16: rows of whole steps, K % 256 == 0 or a padded copy):
 bool mx_gemm_ok(const MxProj& a, int mode, int act4);
+int mx_gemm_tile_rows(const MxProj& a, int mode, int act4);   // 144 or 160
 hipError_t launch_mx_gemm(const MxProj& a, int mode, int act4, hipStream_t st);
 
 }  // namespace moe

@@ -603,6 +603,8 @@ bool mx_gemm_ok(const MxProj& a, int mode, int act4) {
          plan(a, mode, act4).grid <= kMxMaxGrid;
 }
 
+int mx_gemm_tile_rows(const MxProj& a, int mode, int act4) { return plan(a, mode, act4).tm; }
+
 hipError_t launch_mx_gemm(const MxProj& a, int mode, int act4, hipStream_t st) {
   const Plan p = plan(a, mode, act4);
   const GemmArgs ga = {a, p.KP, p.n_ub, p.max_tiles, p.sh_per, sc_pitch(p.KP)};

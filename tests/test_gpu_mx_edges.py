@@ -1,13 +1,15 @@
 """The MXFP4 operators where their other tests do not go: calls on another
-stream than the current one, SiLU far below zero, scale
-bytes next to the ends."""
+stream than the current one, SiLU far below zero, scale bytes next to the
+ends, shared experts longer than the routed ones."""
 import numpy as np
 import pytest
 
 import oracle
 from oracle import mx_oracle as O
+from packed_bit_grouped_amd import _lib as L
 
 torch = pytest.importorskip("torch")
+import test_gpu_mx as G  # noqa: E402
 from test_gpu_mx import DEV, bf16_rows, check_h, f64, make, mx, tables  # noqa: E402,F401
 
 pytestmark = pytest.mark.gpu
@@ -223,3 +225,47 @@ def test_scale_bytes_next_to_the_ends(mx, dims, act, byte, unit):
                        torch.from_numpy(perm["sorted_pair"]).to(DEV), d["B"])
     assert np.abs(f64(h)).max() > 0.1
     check_h(d, h, perm)
+
+
+# ---------------------------------------------------------------------------
+# shared experts longer than the routed ones, on large tiles
+
+# T, H, I, E, k, n_shared, I_shared: whole steps of K and not, with more rows an
+# expert than A4's kernel with two workgroups per compute unit takes, and with fewer
+LONG_WIDE = [(1300, 4096, 256, 24, 2, 1, 768), (1300, 2080, 160, 24, 2, 2, 416)]
+LONG_NARROW = [(1300, 2048, 256, 48, 2, 1, 768), (1300, 2080, 224, 40, 2, 1, 512),
+               (1300, 2080, 256, 48, 2, 1, 352)]
+
+
+@pytest.mark.parametrize("act", ["a16", "a4"])
+@pytest.mark.parametrize("shape", LONG_WIDE + LONG_NARROW, ids=str)
+def test_long_shared_experts_on_large_tiles(mx, shape, act):
+    """The layer and its parts; the columns of h past a routed row's own are
+    not read, whatever they hold, and not written."""
+    T, H, I, E, k, n_sh, I_sh = shape
+    for down in (0, 1):
+        assert L.moe_mx4_tile_rows(mx.ACTS[act], *shape, down) > 16
+    G.test_layer(mx, shape, act)
+    d = make(mx, *shape, act=act, seed=1)
+    B = d["B"]
+    want = mx.run_layer(d["bank"], d["x"], d["logits"], B, shared_gate=d["gate"]).clone()
+    assert (B.h[:T * k, I:] == 0).all()
+    B.h.fill_(float("nan"))
+    assert torch.equal(mx.run_layer(d["bank"], d["x"], d["logits"], B, shared_gate=d["gate"]), want)
+    assert torch.isnan(B.h[:T * k, I:]).all() and torch.isfinite(B.h[:T * k, :I]).all()
+    assert torch.isfinite(B.h[T * k:]).all()
+
+
+@pytest.mark.parametrize("act", ["a16", "a4"])
+@pytest.mark.parametrize("T", [2, 33])
+@pytest.mark.parametrize("I,I_sh", [(96, 224), (224, 96)])
+def test_columns_past_a_row_s_own_are_not_read(mx, T, I, I_sh, act):
+    """The same on 16 rows, the shared experts' columns too."""
+    d = make(mx, T, 288, I, 6, 2, 1, I_sh, act=act, seed=T)
+    B = d["B"]
+    want = mx.run_layer(d["bank"], d["x"], d["logits"], B, shared_gate=d["gate"]).clone()
+    B.h.fill_(float("nan"))
+    assert torch.equal(mx.run_layer(d["bank"], d["x"], d["logits"], B, shared_gate=d["gate"]), want)
+    P = 2 * T
+    assert torch.isfinite(B.h[:P, :I]).all() and torch.isnan(B.h[:P, I:]).all()
+    assert torch.isfinite(B.h[P:, :I_sh]).all() and torch.isnan(B.h[P:, I_sh:]).all()

@@ -274,3 +274,30 @@ def test_sizes_next_to_the_range_of_int():
         a = dict(kw, w13_shared=BANK if "n_shared" in kw else None)
         assert _gateup(**a) == L.MOE_E_UNSUPPORTED, kw
     assert L.moe_mx4_workspace_bytes(*dict(SHAPE, T=1, H=32, I=32, n_shared=8192, I_shared=16384).values()) > 0
+
+
+def test_shapes_of_the_gpu_tests_run_on_the_tiles_that_they_are_for():
+    """The library's own choice of kernel for every shape that a GPU test has
+    for the larger tiles."""
+    pytest.importorskip("torch")
+    import test_gpu_mx as G
+    import test_gpu_mx_edges as X
+
+    def rows(shape, act, calls=(0, 1)):
+        return {L.moe_mx4_tile_rows(act, *shape, d) for d in calls}
+
+    for shape in G.LARGE + [G.MANY] + X.LONG_WIDE + X.LONG_NARROW:
+        assert rows(shape, L.MOE_A16) == {160}, shape
+    for shape in [G.FEWER] + X.LONG_NARROW:
+        assert rows(shape, L.MOE_A4) == {144}, shape
+    assert rows((1150, 4608, 160, 12, 1, 1, 96), L.MOE_A4, [0]) == {144}
+    for shape in [G.MANY, (2000, 512, 2304, 12, 1, 0, 0)] + X.LONG_WIDE:
+        assert rows(shape, L.MOE_A4) == {160}, shape
+    assert rows((400, 6144, 128, 24, 1, 0, 0), L.MOE_A4, [0]) == {160}
+    for shape in G.LARGE:
+        assert rows(shape, L.MOE_A4) <= {144, 160}, shape
+    for shape in ((1, 2048, 768, 128, 8, 1, 768), (64, 2048, 768, 128, 8, 0, 0), (80, 40960, 128, 4, 1, 0, 0)):
+        assert rows(shape, L.MOE_A16) == rows(shape, L.MOE_A4) == {16}, shape
+    assert L.moe_mx4_tile_rows(L.MOE_A8, 64, 2048, 768, 128, 8) == 0
+    assert L.moe_mx4_tile_rows(L.MOE_A16, 64, 2050, 768, 128, 8) == 0
+    assert L.moe_mx4_tile_rows(L.MOE_A16, 64, 2048, 768, 128, 8, down=2) == 0
