@@ -69,14 +69,28 @@ bool pad_h(int I, int n_shared, int I_shared) {
 // and converts them for 16.
 //  * A16 expands the weights on the vector units, so it is the work that decides:
 //    rows x blocks of columns x pieces of K.  us, 16 rows / 160 rows, H 2048,
-//    I 768, 128 experts, k 8: gate/up of 16 tokens 34/41, of 32 47/44, of 256
-//    87/46; down of 64 tokens 33/36, of 128 38/37, of 256 55/41.  H 4096, I 1536,
-//    8 experts, k 2: gate/up of 32 tokens 18/23, of 64 28/22; down of 32 13/15,
-//    of 64 18/16, of 128 26/20.
+//    I 768, 128 experts, k 8: gate/up of 16 tokens 34/40, of 24 41/41, of 32
+//    45/42, of 256 88/45; down of 64 tokens 33/35, of 128 38/37, of 256 55/40.
+//    H 4096, I 1536, 256 experts, k 8: gate/up of 4 tokens 46/47, of 8 (one row
+//    an expert) 83/77, of 16 132/121, of 64 296/257; down of 16 84/77, of 64
+//    187/167.
+//    But not with fewer workgroups than half the compute units (the experts that
+//    P pairs are likely to touch, about E P / (E + P), x blocks of columns) until
+//    an expert's rows fill a tile of 16: H 4096, I 1536, 8 experts, k 2: gate/up
+//    of 32 tokens (8 rows) 17/22, of 48 20/22, of 64 26/22; down of 48 14/15, of
+//    64 18/16.  H 8192, I 2048: gate/up of 24 tokens 34/39, of 48 41/39; down,
+//    with twice the blocks, of 24 24/19.  H 4096, I 14336: down of 24 tokens
+//    55/65, of 48 72/67.
+//    (Measured slower still, up to 1.2x: 16 tokens on 64 experts, whose 41 tiles
+//    take a third round of the chip; two shared experts of H 2048 and I 1408,
+//    down of 80 tokens; experts chosen by a Zipf prior, down of 128 tokens.  The
+//    rule knows neither how tiles fall on the chip nor how rows on the experts.)
 //  * A4 takes codes on both sides and gains from the rows of an expert alone.
-//    The same sizes: gate/up of 128 tokens (8 rows an expert) 41/44, of 256
-//    56/45; down of 192 tokens 36/39, of 256 41/41; 8 experts, 128 tokens
-//    (32 rows) gate/up 26/23, down 20/19.
+//    The same sizes: gate/up of 128 tokens (8 rows an expert) 41/42, of 256
+//    54/43; down of 192 tokens 35/36, of 256 41/38; 8 experts, 32 tokens (8 rows)
+//    gate/up 14/16, down 12/13, 64 tokens 18/17, 16/14; 256 experts, 256 tokens
+//    (8 rows) 287/260, 214/187, 512 tokens 434/262, 293/202 (with that many
+//    experts the larger tiles win from 6 rows an expert on, which the rule leaves).
 //  * Few workgroups: H 1056, I 352, 8 experts, k 3, A16 gate/up of 512 tokens
 //    (351 pieces) 19/21, of 1024 (621) 29/26.
 bool large_tiles(const MxProj& a, bool act4, int mode) {
@@ -84,7 +98,13 @@ bool large_tiles(const MxProj& a, bool act4, int mode) {
   const long long work = n_ub * mx_pieces(a.K);
   const long long tiles = a.P / 160 + (a.E < a.P ? a.E : a.P) / 2;
   if (tiles * work < 500) return false;
-  if (act4 ? a.P < 16LL * a.E : a.P * work < (mode == 0 ? 24576 : 40960)) return false;
+  if (act4) {
+    if (a.P < 16LL * a.E) return false;
+  } else {
+    const long long touched = (long long)a.E * a.P / (a.E + a.P);
+    if (a.P * work < (mode == 0 ? 24576 : 40960)) return false;
+    if (touched * n_ub < 128 && a.P < 12LL * a.E) return false;
+  }
   return mx_gemm_ok(a, mode, act4);
 }
 

@@ -302,3 +302,22 @@ def test_shapes_of_the_gpu_tests_run_on_the_tiles_that_they_are_for():
     assert L.moe_mx4_tile_rows(L.MOE_A8, 64, 2048, 768, 128, 8) == 0
     assert L.moe_mx4_tile_rows(L.MOE_A16, 64, 2050, 768, 128, 8) == 0
     assert L.moe_mx4_tile_rows(L.MOE_A16, 64, 2048, 768, 128, 8, down=2) == 0
+
+
+def test_tiles_where_both_were_measured():
+    """A16 takes the larger tiles where they were measured faster: with few
+    experts not before their rows fill a tile of 16, with many from the first
+    rows on."""
+    def gateup(T, *layer):
+        return L.moe_mx4_tile_rows(L.MOE_A16, T, *layer)
+
+    def down(T, *layer):
+        return L.moe_mx4_tile_rows(L.MOE_A16, T, *layer, 0, 0, 1)
+
+    few, many, wide = (4096, 1536, 8, 2), (4096, 1536, 256, 8), (8192, 2048, 8, 2)
+    assert [gateup(T, *few) for T in (16, 32, 40, 64, 96)] == [16, 16, 16, 160, 160]
+    assert [gateup(T, *wide) for T in (16, 32, 64)] == [16, 16, 160]
+    assert [down(T, 4096, 14336, 8, 2) for T in (16, 32, 64)] == [16, 16, 160]
+    assert [gateup(T, *many) for T in (4, 8, 16, 64)] == [16, 160, 160, 160]
+    assert [gateup(T, 2048, 768, 128, 8) for T in (16, 32, 64)] == [16, 160, 160]
+    assert [down(T, 2048, 768, 128, 8) for T in (64, 128)] == [16, 160]
