@@ -269,3 +269,31 @@ def test_columns_past_a_row_s_own_are_not_read(mx, T, I, I_sh, act):
     P = 2 * T
     assert torch.isfinite(B.h[:P, :I]).all() and torch.isnan(B.h[:P, I:]).all()
     assert torch.isfinite(B.h[P:, :I_sh]).all() and torch.isnan(B.h[P:, I_sh:]).all()
+
+
+def test_calls_on_a_stream_of_their_own_are_captured(mx):
+    """The copy and the memory that the calls make belong to the captured
+    stream, given as such or as the current one; replays give the eager bits."""
+    w = torch.empty((2, 64, 96), device=DEV)
+
+    def calls(stream):
+        codes, scales = mx.quantize_bank(w.transpose(1, 2), stream=stream)
+        tiles = mx.MxBank((codes, scales), stream=stream).tiles["w13"]
+        rows = mx.dequantize_rows(codes.view(-1, 32), scales.view(-1, 2), stream=stream)
+        return codes, scales, *tiles, rows
+
+    w.copy_(torch.randn(w.shape, generator=torch.Generator(DEV).manual_seed(0), device=DEV))
+    calls(None)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s = torch.cuda.current_stream()
+        got = [calls(s), calls(s.cuda_stream), calls(None)]
+    for seed in range(3):
+        w.copy_(torch.randn(w.shape, generator=torch.Generator(DEV).manual_seed(seed + 1), device=DEV))
+        want = calls(None)
+        graph.replay()
+        torch.cuda.synchronize()
+        for outs in got:
+            for a, b in zip(outs, want):
+                assert torch.equal(a, b), seed
