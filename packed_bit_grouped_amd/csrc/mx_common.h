@@ -37,7 +37,7 @@ struct MxWsLayout {
 // of piece 4S + j.  Blocks past K hold code 0 and scale 0.  A wave's load is
 // then one contiguous kilobyte; from plain rows (16 runs of 128 bytes a load)
 // the gate/up product of 4096 tokens with MXFP4 activations (H 4096, I 1536,
-// 256 experts, k 8) took 716 us where the tiles took 478 (398 now).
+// 256 experts, k 8) took 716 us where the tiles took 478 (392 now).
 constexpr int kMxPieceK = 128;
 inline __host__ __device__ int mx_pieces(int K) { return (int)(((uint32_t)K + kMxPieceK - 1) / kMxPieceK); }
 inline __host__ __device__ size_t mx_code_bytes(int N, int K) {

@@ -16,7 +16,9 @@
 //    and step, chunk q of row m in slot q ^ ((m >> 1) & 7); the scale bytes of
 //    the whole tile are staged once.  A16: 256 bytes of bf16 per row and
 //    sub-step, chunk q in slot q ^ swizzle16(m).  Both spread the 16 lanes that
-//    an LDS access serves at a time over all banks.
+//    a 128-bit LDS access serves at a time over all banks; the counters show no
+//    conflicts for A16, and conflicts in 16% of A4's LDS cycles, which reads the
+//    scales by two bytes a lane as well (not separated by a measurement).
 //  * A4 feeds codes and scales to the scaled 16x16x128 instruction; A16
 //    expands a fragment's 8 codes to bf16 by four conversions (exact) for one
 //    16x16x32 step against every row fragment.
@@ -24,16 +26,19 @@
 //    quantises or copies them, and the tiles' scales behind K are 0 (never
 //    255), so K's tail needs no cases.
 //
-// Measured (4096 tokens, H 4096, I 1536, 256 experts, k 8: 128 rows an expert):
-//  * A16 gate/up 739 us, 1.12 PFLOP/s: the matrix pipes are busy 54% of the
-//    cycles, the conversions of the weights share the issue slots.  A library
-//    bf16 product of 8192^3 random values reaches 1.20.
-//  * A4 gate/up 389 us, 1.71 GB of weights at 4.4 TB/s, matrix pipes 25% busy;
-//    down 340 us, 0.86 GB of weights and 0.54 GB of y.  By clock stamps the loop
+// Measured (4096 tokens, H 4096, I 1536, 256 experts, k 8: 128 rows an expert;
+// kernel trace, median and fastest of 30 calls on three sets of weights):
+//  * A16 gate/up 768 / 745 us (739 a call in a row of calls: 1.12 PFLOP/s): the
+//    matrix pipes are busy 54% of the cycles, the conversions of the weights share
+//    the issue slots.  A library bf16 product of 8192^3 random values reaches 1.20.
+//    Down 519 / 497, pipes 36% busy: half the work, and 0.54 GB of y.
+//  * A4 gate/up 392 / 387 us, 1.71 GB of weights at 4.4 TB/s, matrix pipes 24% busy;
+//    down 338 / 334 us, 0.86 GB of weights and 0.54 GB of y.  By clock stamps the loop
 //    reads at 6.3 TB/s (22.7 of a workgroup's 30.6 us, down 9.6 of 20.0): the
 //    rest is finding the tile (1.6), its rows (0.5 to 1.4), the first loads (2.6
 //    to 4.2) and the stores (2.0 to 3.8), which one workgroup per compute unit
-//    does not overlap.  32 rows an expert, two workgroups: 6.1 TB/s.
+//    does not overlap.  64 rows an expert, two workgroups: gate/up 333 / 319 us,
+//    down 243 / 239, pipes 17% and 11% busy.
 //  * A tile of 160 rows reads the weights once for nearly every expert here; with
 //    tiles of 128 an expert in two needs a second pass.
 //  * Tried: a tile's codes kept in LDS while several blocks of weights pass
@@ -572,11 +577,16 @@ Plan plan(const MxProj& a, int mode, int act4) {
   // Two workgroups per compute unit, each with half the weight rows per wave: one's
   // start and stores pass behind the other's loop (by clock stamps 8 of 31 us of a
   // gate/up workgroup, 10 of 20 of down, whose loop alone reads 6.3 TB/s), but the
-  // activations are read twice as often.  A4, us, one / two workgroups, by rows
-  // per expert.  H 4096, I 1536: 8 experts, 64 rows, gate/up 25/19, down 23/19,
-  // 256 rows 32/47, 34/35; 256 experts, 32 rows 296/278, 241/231, 64 rows 321/308,
-  // 311/289, 128 rows 389/400, 460/436 (with the sum).  H 2048, I 768, 128
-  // experts: 16 rows 45/42, 41/38, 64 rows 53/52, 62/61, 128 rows 63/68, 89/93.
+  // activations are read twice as often.  A4 calls (down with the sum), us, one /
+  // two workgroups, by rows per expert.  H 4096, I 1536: 256 experts, 12 rows gate/up
+  // 280/264, down 206/195, 32 rows 295/279, 243/231, 64 rows 322/309, 309/289, 80 rows
+  // 340/326, 350/323; 32 experts, 96 rows 57/54, 53/52; 8 experts, 96 rows 28/21,
+  // 26/22.  H 2048, I 768, 128 experts: 32 rows 48/47, 49/46, 96 rows 59/58, 76/75.
+  // In eight layers with 12 to 96 rows it was never more than 1% slower.  Beyond 96
+  // the two win in turn, gate/up and down alike, as the tiles fall into rounds of the
+  // chip: 256 experts, 128 rows 398/400, 460/437; 32 experts, 192 rows 87/91, 84/93;
+  // 8 experts, 128 rows 31/33, 30/30, 384 rows 55/48, 50/47; H 2048, 128 experts, 128
+  // rows 65/68, 89/95; I 14336, 8 experts, 128 rows gate/up 124/182.
   p.narrow = act4 && a.P <= 96LL * a.E && lds_bytes(true, p.KP, kRowsNarrow, 2) <= 80 * 1024;
   p.tm = p.narrow ? kRowsNarrow : kRowsMax;
   p.sh_per = (a.T + p.tm - 1) / p.tm;

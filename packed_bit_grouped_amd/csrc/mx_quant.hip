@@ -6,10 +6,11 @@
 // power of two is exact, so the only rounding is the one to the code, done by
 // the conversion instruction (all 2^16 bf16 inputs and the codes' midpoints
 // were compared with the definition at 12 scales).  Bound by memory: 2 or 4
-// bytes read and 0.53 written per value, no reuse.  Measured: 201 M fp32 weights
-// to codes 201 us (4.5 TB/s read and written together), back to bf16 83 us (6.1
-// TB/s); 4096 rows of 4096 bf16 values 8.8 us each way (4.8 TB/s); 12 rows of
-// 2048 2.5 us, the launch.
+// bytes read and 0.53 written per value, no reuse.  Measured (kernel trace, medians
+// of 30): 201 M fp32 weights to codes 206 us (4.4 TB/s read and written together),
+// back to bf16 85 us (6.0 TB/s), to fp32 248 us (3.7 TB/s, 7/8 of it written); 4096
+// rows of 4096 bf16 values 9.4 us and 8.8 back (4.5 and 4.8 TB/s, partly the cache),
+// to fp32 15.4; 12 rows of 2048 2.5 us, the launch.
 #include "mx_common.h"
 
 namespace moe {

@@ -5,7 +5,7 @@
 //
 // Few rows per expert: bound by streaming the packed weights (0.53 bytes per
 // weight, read once) and, for a handful of tokens, by the latency of that one
-// pass, so everything a workgroup needs is loaded at once.  Both operands go
+// pass: a turn's weights, scales and activations are loaded at once.  Both operands go
 // from memory straight into the matrix instruction's registers, the weights as
 // tiled pieces (a contiguous kilobyte per load), the activations as the same
 // blocks of their rows.  A16 expands a block of weights to bf16 by the
@@ -19,10 +19,18 @@
 // workgroup routes and sorts the batch itself: that costs less than the launch
 // and the round trip of a routing kernel.
 //
-// Measured (H 2048, I 768, 128 experts, k 8): A4 gate/up of 64 tokens 34.6 us =
-// 6.1 TB/s of codes and scales (a plain read reaches 6.3); A16 of one token with
-// a shared expert 6.1 us, of 15 MB: three dependent trips to memory (offsets,
-// token, rows) and the reduction; routed inside 7.0; down of one token 3.8.
+// Measured (H 2048, I 768, 128 experts, k 8; kernel trace, median and fastest of 30
+// calls on three sets of weights): A4 gate/up of 64 tokens 35.0 / 33.9 us = 6.1
+// TB/s of codes and scales (a plain read reaches 6.3); A16 of one token with a
+// shared expert 6.4 / 5.2 us, of 15 MB; routed inside 7.6 / 7.2; down of one token
+// 5.1 / 3.9, of 12 tokens 11.3 / 10.2, of 64 29.6 / 28.9.  What a short gate/up
+// pass waits for is trips to memory one behind the other: the offsets, the row's
+// pair (the loop's first loads, weights too, stand behind it and behind the
+// division that makes a token of it, though the weights need the tile alone),
+// then rows and weights, then the reduction; a second turn's loads (K above 2048)
+// start when the first turn's products are done.  A16 gate/up of 8 tokens 22.6 us
+// against 13.7 for its bytes, of 16 33.4 against 22: every weight is converted for
+// 16 columns of which one or two are used.
 // Four waves: with eight, each with half the K, gate/up of one token took 0.7 us
 // longer, of 8 tokens 27.4 against 22.6 - more waves to start and to join for the
 // same loads in flight.  A kernel that joined down and the weighted sum (a
@@ -488,7 +496,9 @@ hipError_t launch(const MxProj& a, const MxRoute& ro, hipStream_t st) {
   // Pieces per wave and turn, so that the four waves pass K in few turns: each
   // turn is a trip to memory (down of one token, K 768, NB 1 7.6 us, 2 7.3; A4
   // of 64 tokens 31.3, 29.4).  At K between 1024 and 2048 NB 4 would leave waves
-  // idle (K 1408, 12 tokens: 14.3 us, NB 2 12.8).
+  // idle (K 1408, 12 tokens: 14.3 us, NB 2 12.8).  NB 2 leaves one of the four idle
+  // at K 640 and 768 (five and six pieces), NB 1 at K 352, and K 1408 and 1536 (11
+  // and 12) go 2, 2, 1, 1: K of 768 in down costs its workgroup a turn for 13 KB.
 #define MX_GO(NB) \
   mx_rows16_kernel<MODE, ACT4, XQ, NB, ROUTE><<<(int)grid, kThreads, lds, st>>>(a, ro, n_sh_tiles, n_ub)
   if (pieces >= 16) MX_GO(4);
