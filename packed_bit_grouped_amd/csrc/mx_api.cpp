@@ -81,10 +81,13 @@ bool pad_h(int I, int n_shared, int I_shared) {
 //    64 18/16.  H 8192, I 2048: gate/up of 24 tokens 34/39, of 48 41/39; down,
 //    with twice the blocks, of 24 24/19.  H 4096, I 14336: down of 24 tokens
 //    55/65, of 48 72/67.
-//    (Measured slower still, up to 1.2x: 16 tokens on 64 experts, whose 41 tiles
-//    take a third round of the chip; two shared experts of H 2048 and I 1408,
-//    down of 80 tokens; experts chosen by a Zipf prior, down of 128 tokens.  The
-//    rule knows neither how tiles fall on the chip nor how rows on the experts.)
+//    (Of 448 sizes measured 69 still run more than 5% longer than on the other
+//    kernel: 1.1x to 1.2x for 16 tokens on 64 experts, whose 41 tiles take a third
+//    round of the chip, two shared experts of H 2048 and I 1408, down of 80 tokens,
+//    experts chosen by a Zipf prior, down of 128; 1.4x for gate/up of 4 tokens with
+//    I 14336 and for down of 96 to 192 tokens on 8 or 32 experts; 1.4x to 1.8x at
+//    short K, H 512, 512 experts, 16 to 64 tokens.  The rule knows neither how tiles
+//    fall on the chip nor how rows on the experts.)
 //  * A4 takes codes on both sides and gains from the rows of an expert alone.
 //    The same sizes: gate/up of 128 tokens (8 rows an expert) 41/42, of 256
 //    54/43; down of 192 tokens 35/36, of 256 41/38; 8 experts, 32 tokens (8 rows)

@@ -297,3 +297,20 @@ def test_calls_on_a_stream_of_their_own_are_captured(mx):
         for outs in got:
             for a, b in zip(outs, want):
                 assert torch.equal(a, b), seed
+
+
+# ---------------------------------------------------------------------------
+# the most tokens, choices and units
+
+
+@pytest.mark.parametrize("act", ["a16", "a4"])
+@pytest.mark.parametrize("shape", [
+    (65535, 32, 32, 4, 1, 0, 0),      # tokens
+    (9, 32, 32, 512, 512, 0, 0),      # choices: more pairs than one routing launch takes
+    (1, 64, 32, 512, 512, 1, 64),
+    (300, 32, 32768, 2, 1, 0, 0),     # units: a single step of K on large tiles, and a long K behind it
+    (2, 32, 65536, 2, 1, 1, 32),
+], ids=str)
+def test_largest_of_each(mx, shape, act):
+    G.test_layer(mx, shape, act)
+
