@@ -60,7 +60,7 @@
 extern "C" {
 #endif
 
-#define MOE_W4_ABI_VERSION 6
+#define MOE_W4_ABI_VERSION 7
 
 /* Version of the compiled library.  The Python binding refuses to load a
  * library whose version differs from the header it was written for. */
@@ -147,6 +147,39 @@ moe_status moe_router_topk(const uint16_t* x, int T, int H,
 moe_status moe_route_topk(const float* logits, int T, int E, int k,
                           int renormalize, int32_t* topk_ids, float* topk_w,
                           void* stream);
+
+/* ---------------------------------------------------------------------
+ * moe_route_scored -- router top-k on scores: softmax or sigmoid scores, a
+ * bias for balance, groups of experts (same build log and section as
+ * moe_router_topk: tokens are scored and routed on the device).
+ *   logits     fp32 [T][E]
+ *   score      MOE_SCORE_SOFTMAX: s = softmax of the token's E logits;
+ *              MOE_SCORE_SIGMOID: s = 1 / (1 + exp(-logit))
+ *   bias       fp32 [E], finite or -inf, or null (0): the choice goes by
+ *              c = s + bias, the weights by s
+ *   n_group    the experts are n_group groups of E / n_group neighbours; a
+ *              group counts the sum of its group_best (1 or 2) largest c, and
+ *              the topk_group best groups stay (topk_group = n_group: all;
+ *              ties to the lower group)
+ *   topk_ids   int32 [T][k] (out): the k experts of those groups with the
+ *              largest c in descending order, ties to the lower index
+ *   topk_w     fp32 [T][k] (out): s of the chosen, divided by their sum where
+ *              renormalize is 1, times scale
+ * Scores, choice values, sums and weights are computed in 64 bits; a weight is
+ * rounded once.  A logit of -inf has score 0, also in a softmax of nothing
+ * else; chosen scores that sum to 0 give weights of 0.  A choice value that is
+ * NaN counts as -inf; NaN, or +inf under a softmax, reaches the weights of its
+ * token alone, and its ids are k different experts all the same.
+ * Limits: 1 <= E <= 1024, n_group <= 64 divides E, k <= topk_group * E /
+ * n_group, T < 2^26.  T = 0 launches nothing.  Errors: MOE_E_INVAL
+ * (arguments), MOE_E_UNSUPPORTED (E, n_group above 64, T), MOE_E_DEVICE.
+ * ------------------------------------------------------------------- */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+moe_status moe_route_scored(const float* logits, int T, int E, int k, int score,
+                            const float* bias, int n_group, int topk_group, int group_best,
+                            int renormalize, float scale, int32_t* topk_ids, float* topk_w,
+                            void* stream);
 
 /* ---------------------------------------------------------------------
  * moe_permute -- stable counting sort of the T*k (token, expert) pairs by

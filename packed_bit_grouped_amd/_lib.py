@@ -14,7 +14,7 @@ from typing import Optional
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe_w4.so")
-ABI_VERSION = 6
+ABI_VERSION = 7
 
 MOE_OK, MOE_E_INVAL, MOE_E_UNSUPPORTED, MOE_E_DEVICE, MOE_E_WORKSPACE = 0, -1, -2, -3, -4
 MOE_A16, MOE_A8, MOE_A4 = 0, 1, 2
@@ -25,8 +25,10 @@ MOE_LAYER_ONE_LAUNCH = 8
 MOE_OUT_F32 = 16
 MOE_W_PREPACKED = 32
 MOE_NOALLOC_SCRATCH_BYTES = 32 << 20
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 
 c_int, c_size_t, c_void_p = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
+c_float = ctypes.c_float
 
 # name -> (restype, argtypes), mirroring include/moe_w4.h
 _SIGS = {
@@ -123,6 +125,8 @@ _SIGS = {
                               c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                               c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_int,
                               c_void_p]),
+    "moe_route_scored": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_int, c_int,
+                                 c_int, c_int, c_float, c_void_p, c_void_p, c_void_p]),
 }
 
 EXPORTED = tuple(_SIGS)
@@ -228,6 +232,13 @@ def moe_route_topk(logits, T, E, k, renormalize, topk_ids, topk_w,
 
 def moe_router_workspace_bytes(T, H, E) -> int:
     return load().moe_router_workspace_bytes(T, H, E)
+
+
+def moe_route_scored(logits, T, E, k, score, bias, n_group, topk_group, group_best, renormalize,
+                     scale, topk_ids, topk_w, stream=None, check=True):
+    return _call("moe_route_scored", _ptr(logits), T, E, k, score, _ptr(bias), n_group, topk_group,
+                 group_best, renormalize, scale, _ptr(topk_ids), _ptr(topk_w), _stream(stream),
+                 check=check)
 
 
 def moe_router_topk(x, T, H, router_w, prior, E, k, renormalize, logits, topk_ids,

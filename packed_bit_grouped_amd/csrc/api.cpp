@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstring>
 
 #include "moe_internal.h"
@@ -204,6 +205,27 @@ moe_status moe_route_topk(const float* logits, int T, int E, int k,
                           int renormalize, int32_t* topk_ids, float* topk_w,
                           void* stream) {
   return route_topk_impl(logits, T, E, k, renormalize, topk_ids, topk_w, stream, nullptr);
+}
+
+moe_status moe_route_scored(const float* logits, int T, int E, int k, int score,
+                            const float* bias, int n_group, int topk_group, int group_best,
+                            int renormalize, float scale, int32_t* topk_ids, float* topk_w,
+                            void* stream) {
+  if (T < 0 || E <= 0 || k <= 0 || n_group <= 0 || topk_group <= 0) return MOE_E_INVAL;
+  if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return MOE_E_INVAL;
+  if (renormalize != 0 && renormalize != 1) return MOE_E_INVAL;
+  if (group_best != 1 && group_best != 2) return MOE_E_INVAL;
+  if (E % n_group || topk_group > n_group) return MOE_E_INVAL;
+  if (!std::isfinite(scale)) return MOE_E_INVAL;
+  if (k > (long long)topk_group * (E / n_group)) return MOE_E_INVAL;
+  if (E > kRouteMaxE || n_group > kScoredMaxGroups || T >= (1 << 26)) return MOE_E_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!logits || !topk_ids || !topk_w) return MOE_E_INVAL;
+  const moe_status st = check_device();
+  if (st != MOE_OK) return st;
+  const ScoredArgs a = {logits, bias, T, E, k, score, n_group, topk_group, group_best,
+                        renormalize, scale, topk_ids, topk_w};
+  return from_hip(launch_route_scored(a, static_cast<hipStream_t>(stream)));
 }
 
 size_t moe_router_workspace_bytes(int T, int H, int E) {

@@ -8,6 +8,7 @@ namespace moe {
 constexpr int kPermMaxE = 512;      // permute: experts per launch
 constexpr int kPermIdBits = 9;      // bits of an expert id below kPermMaxE
 constexpr int kRouteMaxE = 1024;    // route: 16 logits per lane
+constexpr int kScoredMaxGroups = 64;   // scored routing: a lane or more per group
 constexpr int kFusedRouteMaxT = 64; // fused route+permute: tokens per launch
 constexpr int kFusedRouteMaxP = 4096;  // fused route+permute: pairs per launch
 constexpr int kLayerFlags = 1024;   // one-launch layer: barrier flags (and max grid)
@@ -121,6 +122,17 @@ hipError_t launch_route_permute(const float* logits, int T, int E, int k,
 hipError_t launch_route_topk(const float* logits, int T, int E, int k,
                              int renorm, int32_t* ids, float* w, hipStream_t st,
                              const XPrep* xp = nullptr);
+// Routing by scores (moe_route_scored).
+struct ScoredArgs {
+  const float* logits;
+  const float* bias;           // [E] or null
+  int T, E, k;
+  int score, n_group, topk_group, group_best, renorm;
+  float scale;
+  int32_t* ids;
+  float* w;
+};
+hipError_t launch_route_scored(const ScoredArgs& a, hipStream_t st);
 // Rows [R][C] (row stride ld) to int8 rows of stride ldq and fp32 scales.
 hipError_t launch_quant_a8(const void* src, int is_f32, int R, int C, int ld,
                            int8_t* q, int ldq, float* s, hipStream_t st);
