@@ -294,6 +294,13 @@ size_t moe_workspace_bytes(int act, int T, int H, int I, int E, int k,
                               /* without it out is bf16, the round-to-      */
                               /* nearest-even of exactly that value         */
 
+#define MOE_GU_F32 256        /* moe_w4_gateup_silu / moe_mx4_gateup_silu: h */
+                              /* is fp32 [R][2*ld_h], a row's gate sums and, */
+                              /* from column ld_h on, its up sums, without   */
+                              /* SiLU: what moe_lora_gateup_silu joins with  */
+                              /* the requests' adapters.  Other calls refuse */
+                              /* it; not on the vector-ALU decode path       */
+
 /* Tile height to pass as moe_permute's tile_m: 160 (the MFMA path's row
  * chunk: an expert with up to 160 pairs streams its weights once) when
  * T*k >= 32*E with A16, else 16.  Both paths accept any tile_m; the MFMA
@@ -697,7 +704,7 @@ int moe_mx4_tile_rows(int act, int T, int H, int I, int E, int k, int n_shared, 
  *              sorted row r, row T*k + s*T + t is shared expert s and token
  *              t.  Rows past offsets[E] and columns past a row's own I (or
  *              I_shared) are left as they were
- *   flags      0
+ *   flags      0 or MOE_GU_F32 (h fp32 [...][2*max(I, I_shared)])
  * Limits: H, I, I_shared multiples of 32 and below 2^30, E <= 512, T and
  * n_shared <= 65535, T*k < 2^24, T*(k + n_shared)*H and that with I or I_shared
  * < 2^31, (T*k/16 + min(E, T*k) + n_shared*ceil(T/16)) * max(I, I_shared) < 2^28
@@ -741,6 +748,104 @@ moe_status moe_mx4_layer(int act, const float* logits, const uint16_t* x, int T,
                          int32_t* counts, int32_t* offsets, int32_t* sorted_pair,
                          int32_t* pair_pos, uint16_t* h, void* out, void* workspace,
                          size_t ws_bytes, int flags, void* stream);
+
+/* =====================================================================
+ * Low-rank adapters of many requests beside the experts' projections.
+ *
+ * Build log "Two 96 GB Ascend cards run Qwen3.8 Flash-Next", sections "Keep
+ * low-bit weights packed, do the work on the NPU" (adapters cannot be merged
+ * into packed weights) and "Optimise serving, not isolated kernels" (one batch
+ * of many requests).  The expert weights are shared by all requests; a request
+ * may have an adapter: for an expert a pair of matrices (A, B) and a scale for
+ * its gate/up and one for its down projection.
+ *
+ *   h(t, e) = SiLU(g + s Bg (Ag x_t)) * (u + s Bu (Au x_t))   g, u: the shared sums
+ *   out[t]  = base[t] + sum over the token's experts of w s B (A h(t, e))
+ *
+ * A layer runs as: routing (moe_route_scored, moe_route_topk, ...), moe_permute,
+ * moe_w4_gateup_silu or moe_mx4_gateup_silu with MOE_GU_F32 -> gu,
+ * moe_lora_gateup_silu -> h, moe_w4_down_combine or moe_mx4_down_combine with
+ * MOE_OUT_F32 -> base, moe_lora_down_combine -> out.
+ * ===================================================================== */
+
+/* An adapter's matrices for one projection of one expert; tables of these live
+ * in DEVICE memory, as [n_adapters][E + n_shared] (shared experts behind the
+ * routed ones).
+ *   gate/up: a bf16 [2*rank][K] (the gate's rows, then up's), K = H;
+ *            b bf16 [N][rank], N = 2I (gate rows, then up rows)
+ *   down:    a bf16 [rank][K], K = I;  b bf16 [N][rank], N = H
+ * (I_shared for shared experts.)  rank: a multiple of 8, 0 where the adapter
+ * leaves the expert alone; ranks may differ from entry to entry.  a, b 16-byte
+ * aligned.  An entry that the calls cannot use (other N or K, rank above
+ * max_rank or no multiple of 8, null or misaligned matrices) counts as rank 0
+ * and sets bit 0 of the workspace's error word. */
+typedef struct moe_lora {
+  const uint16_t* a;
+  const uint16_t* b;
+  int32_t rank;
+  float scale;
+  int32_t N;
+  int32_t K;
+} moe_lora;                 /* 32 bytes */
+
+/* Workspace of the two calls below (device memory, 256-byte aligned); 0 for
+ * sizes they refuse.  Its first 4 bytes are the error word, which the caller
+ * zeroes once and reads when it wants to; nothing else is kept between calls.
+ * Calls that overlap in time need a workspace each. */
+size_t moe_lora_workspace_bytes(int T, int k, int n_shared, int max_rank);
+
+/* ---------------------------------------------------------------------
+ * moe_lora_gateup_silu -- h of every routed pair and shared-expert token from
+ * the shared projection's sums and the tokens' adapters.
+ *   x          bf16 [T][H]
+ *   adapter    int32 [T]: the token's adapter, outside [0, n_adapters): none
+ *   table      device table [n_adapters][E + n_shared] of gate/up entries
+ *              (may be null when n_adapters = 0)
+ *   topk_ids   int32 [T*k];  sorted_pair int32 [T*k] from moe_permute
+ *   gu         fp32 [T*k + n_shared*T][2*max(I, I_shared)], as written with
+ *              MOE_GU_F32
+ *   h          (out) rows as in moe_w4_gateup_silu, [...][max(I, I_shared)]:
+ *              bf16, or fp32 with MOE_H_F32 in flags (A8).  Rows past
+ *              offsets[E] and columns past a row's own I (I_shared) are left
+ *              as they were.  Not overlapping gu
+ *   flags      MOE_H_F32 or 0
+ * All sums are fp32 and nothing but h is rounded to fewer bits.
+ * inf and NaN stay in the rows and columns that they reach; an inf in B (and, with
+ * MOE_H_F32, in down's A) may come out as NaN.
+ * Limits: H, I, I_shared multiples of 32 and at most 2^20, E <= 1024, n_shared
+ * <= 65535, n_adapters * (E + n_shared) < 2^31, max_rank a multiple of 8 up to
+ * 128, T*k < 2^24, T*(k + n_shared) times H or max(I, I_shared) < 2^31; else
+ * MOE_E_UNSUPPORTED.  x, gu, h 16-byte aligned.  T = 0 launches nothing.
+ * ------------------------------------------------------------------- */
+#define MOE_H_F32 512        /* moe_lora_* calls: h is fp32 (A8 layers) */
+moe_status moe_lora_gateup_silu(const uint16_t* x, int T, int H, int I, int E, int k,
+                                int n_shared, int I_shared, const int32_t* adapter,
+                                int n_adapters, int max_rank, const moe_lora* table,
+                                const int32_t* topk_ids, const int32_t* sorted_pair,
+                                const float* gu, void* h, void* workspace, size_t ws_bytes,
+                                int flags, void* stream);
+
+/* ---------------------------------------------------------------------
+ * moe_lora_down_combine -- the tokens' outputs from the shared down projection's
+ * and the adapters' weighted sum.
+ *   h          as written by moe_lora_gateup_silu (bf16, or fp32 with MOE_H_F32)
+ *   adapter, topk_ids, sorted_pair: as above;  table: of down entries
+ *   offsets, pair_pos: from moe_permute;  topk_w, shared_gate: as in
+ *              moe_w4_down_combine
+ *   base       fp32 [T][H], moe_*_down_combine's out with MOE_OUT_F32
+ *   out        bf16 [T][H] (out), or fp32 with MOE_OUT_F32 (may be base itself)
+ *   flags      MOE_H_F32, MOE_OUT_F32, both or 0
+ * A pair whose pair_pos is -1 adds nothing.  Sums are fp32, in a fixed order.
+ * Limits: as above.
+ * ------------------------------------------------------------------- */
+moe_status moe_lora_down_combine(const void* h, int T, int H, int I, int E, int k,
+                                 int n_shared, int I_shared, const int32_t* adapter,
+                                 int n_adapters, int max_rank, const moe_lora* table,
+                                 const float* shared_gate, const float* topk_w,
+                                 const int32_t* topk_ids, const int32_t* offsets,
+                                 const int32_t* sorted_pair, const int32_t* pair_pos,
+                                 const float* base, void* out, void* workspace,
+                                 size_t ws_bytes, int flags, void* stream);
 
 #ifdef __cplusplus
 }

@@ -24,6 +24,8 @@ MOE_X_PREPARED = 64
 MOE_LAYER_ONE_LAUNCH = 8
 MOE_OUT_F32 = 16
 MOE_W_PREPACKED = 32
+MOE_GU_F32 = 256
+MOE_H_F32 = 512
 MOE_NOALLOC_SCRATCH_BYTES = 32 << 20
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 
@@ -127,6 +129,14 @@ _SIGS = {
                               c_void_p]),
     "moe_route_scored": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_int, c_int,
                                  c_int, c_int, c_float, c_void_p, c_void_p, c_void_p]),
+    "moe_lora_workspace_bytes": (c_size_t, [c_int] * 4),
+    "moe_lora_gateup_silu": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
+                                     c_void_p, c_int, c_int, c_void_p, c_void_p, c_void_p,
+                                     c_void_p, c_void_p, c_void_p, c_size_t, c_int, c_void_p]),
+    "moe_lora_down_combine": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
+                                      c_void_p, c_int, c_int, c_void_p, c_void_p, c_void_p,
+                                      c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                      c_void_p, c_size_t, c_int, c_void_p]),
 }
 
 EXPORTED = tuple(_SIGS)
@@ -151,6 +161,15 @@ assert ctypes.sizeof(QMatDesc) == 32
 class MxBankDesc(ctypes.Structure):
     """struct moe_mxbank (host struct, device pointers)."""
     _fields_ = [("codes", c_void_p), ("scales", c_void_p)]
+
+
+class LoraDesc(ctypes.Structure):
+    """struct moe_lora (32 bytes)."""
+    _fields_ = [("a", c_void_p), ("b", c_void_p), ("rank", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("N", ctypes.c_int32), ("K", ctypes.c_int32)]
+
+
+assert ctypes.sizeof(LoraDesc) == 32
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -440,3 +459,25 @@ def moe_mx4_layer(act, logits, x, T, H, I, E, k, renormalize, w13, w2, w13_share
                  _ptr(shared_gate), _ptr(topk_ids), _ptr(topk_w), _ptr(counts), _ptr(offsets),
                  _ptr(sorted_pair), _ptr(pair_pos), _ptr(h), _ptr(out), _ptr(workspace),
                  ws_bytes, flags, _stream(stream), check=check)
+
+
+def moe_lora_workspace_bytes(T, k, n_shared, max_rank) -> int:
+    return load().moe_lora_workspace_bytes(T, k, n_shared, max_rank)
+
+
+def moe_lora_gateup_silu(x, T, H, I, E, k, n_shared, I_shared, adapter, n_adapters, max_rank,
+                         table, topk_ids, sorted_pair, gu, h, workspace, ws_bytes, flags=0,
+                         stream=None, check=True):
+    return _call("moe_lora_gateup_silu", _ptr(x), T, H, I, E, k, n_shared, I_shared, _ptr(adapter),
+                 n_adapters, max_rank, _ptr(table), _ptr(topk_ids), _ptr(sorted_pair), _ptr(gu),
+                 _ptr(h), _ptr(workspace), ws_bytes, flags, _stream(stream), check=check)
+
+
+def moe_lora_down_combine(h, T, H, I, E, k, n_shared, I_shared, adapter, n_adapters, max_rank,
+                          table, topk_w, topk_ids, offsets, sorted_pair, pair_pos, base, out,
+                          workspace, ws_bytes, flags=0, stream=None, check=True,
+                          shared_gate=None):
+    return _call("moe_lora_down_combine", _ptr(h), T, H, I, E, k, n_shared, I_shared,
+                 _ptr(adapter), n_adapters, max_rank, _ptr(table), _ptr(shared_gate), _ptr(topk_w),
+                 _ptr(topk_ids), _ptr(offsets), _ptr(sorted_pair), _ptr(pair_pos), _ptr(base),
+                 _ptr(out), _ptr(workspace), ws_bytes, flags, _stream(stream), check=check)

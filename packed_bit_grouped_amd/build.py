@@ -4,8 +4,8 @@ Usage: python -m packed_bit_grouped_amd.build [-j N] [--host-check OUT.so]
                                                [--stamps OUT.so]
 Every call recompiles every source (the build check wants a real compile).
 --host-check also builds a copy of the library whose host code at the C ABI
-(argument checks, workspace carving, launch set-up: api.cpp, mx_api.cpp and
-the entry points of noalloc.hip and probe.hip) carries AddressSanitizer and
+(argument checks, workspace carving, launch set-up: api.cpp, mx_api.cpp,
+lora_api.cpp and the entry points of noalloc.hip and probe.hip) carries AddressSanitizer and
 UndefinedBehaviorSanitizer; device code is not instrumented.  It is for
 CPU-side checks only (load it with the ASan runtime preloaded).
 --stamps also builds a copy whose decode kernels write phase clock stamps
@@ -28,7 +28,8 @@ LIB = os.path.join(HERE, "libmoe_w4.so")
 SOURCES = ["api.cpp", "route_permute.hip", "quant_combine.hip",
            "proj_gemv.hip", "proj_decode.hip", "proj_m16.hip",
            "proj_mfma8.hip", "noalloc.hip", "probe.hip", "mx_api.cpp",
-           "mx_quant.hip", "mx_rows16.hip", "mx_gemm.hip", "route_scored.hip"]
+           "mx_quant.hip", "mx_rows16.hip", "mx_gemm.hip", "route_scored.hip",
+           "lora_api.cpp", "lora.hip"]
 ARCH = "gfx950"
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
          # packed fp32 VALU forms are kept out of the generated code
@@ -56,7 +57,7 @@ def _compile(src: str, objdir: str) -> str:
 
 
 # sources whose host code is instrumented in the host-check build
-HOST_CHECK_SOURCES = ["api.cpp", "mx_api.cpp", "noalloc.hip", "probe.hip"]
+HOST_CHECK_SOURCES = ["api.cpp", "mx_api.cpp", "lora_api.cpp", "noalloc.hip", "probe.hip"]
 # host-side sanitizers only: each flag goes to the host compilation
 SAN_FLAGS = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
              "-Xarch_host", "-fno-sanitize-recover=undefined",

@@ -325,7 +325,7 @@ static moe_status gateup_impl(int act, const uint16_t* x, int T, int H, int I,
                               const int32_t* n_tiles, int tile_m, void* h,
                               void* workspace, size_t ws_bytes, int flags,
                               int32_t* partials, int ng_ld, void* stream,
-                              bool stage_h16 = false) {
+                              bool stage_h16 = false, bool raw = false) {
   moe_status st = check_layer(act, T, H, I, E, k, n_shared, I_shared, tile_m, flags);
   if (st != MOE_OK) return st;
   if (T == 0) return MOE_OK;
@@ -367,7 +367,8 @@ static moe_status gateup_impl(int act, const uint16_t* x, int T, int H, int I,
   a.n_tiles = n_tiles;
   a.max_tiles = moe_permute_max_tiles(T, k, E, tile_m);
   a.out = h;
-  a.ld_out = ld_h;
+  a.raw = raw;
+  a.ld_out = raw ? 2 * ld_h : ld_h;
   a.err = reinterpret_cast<int32_t*>(ws + L.err);
   a.partials = partials;
   a.ng_ld = ng_ld;
@@ -384,7 +385,7 @@ static moe_status gateup_impl(int act, const uint16_t* x, int T, int H, int I,
     return from_hip(launch_proj_mfma8(a, x16, pp, s));
   }
   if (pp) return MOE_E_UNSUPPORTED;   // the prepacked layout is read by the matrix-core path only
-  const bool dec = act == MOE_A16 && !partials && dec_gateup_ok(T, H, tile_m);
+  const bool dec = act == MOE_A16 && !partials && !raw && dec_gateup_ok(T, H, tile_m);
   const bool on_m16 = path == MOE_PATH_MFMA16 ||
                       (path == MOE_PATH_AUTO && m16 && !(dec && (long long)T * k <= kDecPairs));
   a.in_bf16 = x;
@@ -542,7 +543,8 @@ moe_status moe_w4_gateup_silu(int act, const uint16_t* x, int T, int H, int I,
                               size_t ws_bytes, int flags, void* stream) {
   return gateup_impl(act, x, T, H, I, E, k, w13, w13_shared, n_shared, I_shared,
                      offsets, sorted_pair, tiles, n_tiles, tile_m, h, workspace,
-                     ws_bytes, flags, nullptr, 0, stream);
+                     ws_bytes, flags & ~MOE_GU_F32, nullptr, 0, stream, false,
+                     (flags & MOE_GU_F32) != 0);
 }
 
 moe_status moe_w4_route_gateup_silu(int act, const float* logits, const uint16_t* x, int T,

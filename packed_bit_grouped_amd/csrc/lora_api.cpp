@@ -1,0 +1,163 @@
+// C ABI of the low-rank adapters: host-side argument checks, workspace layout
+// and dispatch (the same rules as api.cpp: nothing allocates, synchronizes or
+// reads device memory).
+#include <hip/hip_runtime.h>
+
+#include <cstring>
+
+#include "lora_common.h"
+
+using namespace moe;
+
+namespace {
+
+constexpr int kLoraMaxLen = 1 << 20;   // H, I, I_shared
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+moe_status from_hip(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_E_DEVICE; }
+int ld_h_of(int I, int n_shared, int I_shared) {
+  return n_shared > 0 && I_shared > I ? I_shared : I;
+}
+
+size_t v_bytes(int R, int halves, int max_rank) {
+  int splits;
+  bool large;
+  lora_plan(R, halves, max_rank, splits, large);
+  return (size_t)splits * R * halves * max_rank * 4;
+}
+
+size_t workspace_bytes(int R, int max_rank) {
+  const size_t up = v_bytes(R, 2, max_rank), down = v_bytes(R, 1, max_rank);
+  return 256 + (up > down ? up : down);
+}
+
+moe_status check_rows(int T, int k, int n_shared, int max_rank) {
+  if (T < 0 || k <= 0 || n_shared < 0 || max_rank <= 0) return MOE_E_INVAL;
+  if (max_rank % 8) return MOE_E_INVAL;
+  if (max_rank > kLoraMaxRank || n_shared > 65535) return MOE_E_UNSUPPORTED;
+  if ((long long)T * k >= (1LL << 24)) return MOE_E_UNSUPPORTED;
+  if ((long long)T * ((long long)k + n_shared) >= (1LL << 26)) return MOE_E_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status check_shape(int T, int H, int I, int E, int k, int n_shared, int I_shared,
+                       int n_adapters, int max_rank) {
+  const moe_status st = check_rows(T, k, n_shared, max_rank);
+  if (st != MOE_OK && st != MOE_E_UNSUPPORTED) return st;
+  if (H <= 0 || I <= 0 || E <= 0 || k > E || n_adapters < 0) return MOE_E_INVAL;
+  if (n_shared > 0 && I_shared <= 0) return MOE_E_INVAL;
+  if (st != MOE_OK) return st;
+  if (H % 32 || I % 32 || (n_shared > 0 && I_shared % 32)) return MOE_E_UNSUPPORTED;
+  if (H > kLoraMaxLen || I > kLoraMaxLen || (n_shared > 0 && I_shared > kLoraMaxLen))
+    return MOE_E_UNSUPPORTED;
+  if (E > kRouteMaxE) return MOE_E_UNSUPPORTED;
+  if ((long long)n_adapters * ((long long)E + n_shared) >= (1LL << 31)) return MOE_E_UNSUPPORTED;
+  const long long rows = (long long)T * ((long long)k + n_shared);
+  if (rows * H >= (1LL << 31) || rows * ld_h_of(I, n_shared, I_shared) >= (1LL << 31))
+    return MOE_E_UNSUPPORTED;
+  return MOE_OK;
+}
+
+LoraArgs args_of(int T, int H, int I, int E, int k, int n_shared, int I_shared,
+                 const int32_t* adapter, int n_adapters, int max_rank, const moe_lora* table,
+                 const int32_t* topk_ids, const int32_t* sorted_pair, char* ws, int halves) {
+  LoraArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.T = T;
+  a.k = k;
+  a.P = T * k;
+  a.R = T * (k + n_shared);
+  a.E = E;
+  a.n_shared = n_shared;
+  a.n = n_adapters;
+  a.max_rank = max_rank;
+  a.adapter = adapter;
+  a.topk_ids = topk_ids;
+  a.sorted_pair = sorted_pair;
+  a.table = table;
+  a.halves = halves;
+  a.H = H;
+  a.I = I;
+  a.I_sh = n_shared > 0 ? I_shared : I;
+  a.ld_h = ld_h_of(I, n_shared, I_shared);
+  a.err = reinterpret_cast<int32_t*>(ws);
+  a.v = reinterpret_cast<float*>(ws + 256);
+  lora_plan(a.R, halves, max_rank, a.splits, a.large);
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_lora_workspace_bytes(int T, int k, int n_shared, int max_rank) {
+  if (check_rows(T, k, n_shared, max_rank) != MOE_OK) return 0;
+  return workspace_bytes(T * (k + n_shared), max_rank);
+}
+
+moe_status moe_lora_gateup_silu(const uint16_t* x, int T, int H, int I, int E, int k,
+                                int n_shared, int I_shared, const int32_t* adapter,
+                                int n_adapters, int max_rank, const moe_lora* table,
+                                const int32_t* topk_ids, const int32_t* sorted_pair,
+                                const float* gu, void* h, void* workspace, size_t ws_bytes,
+                                int flags, void* stream) {
+  moe_status st = check_shape(T, H, I, E, k, n_shared, I_shared, n_adapters, max_rank);
+  if (st != MOE_OK) return st;
+  if (flags & ~MOE_H_F32) return MOE_E_INVAL;
+  if (T == 0) return MOE_OK;
+  if (!x || !adapter || !topk_ids || !sorted_pair || !gu || !h || gu == h) return MOE_E_INVAL;
+  if (n_adapters > 0 && (!table || !aligned(table, 8))) return MOE_E_INVAL;
+  if (!aligned(x, 16) || !aligned(gu, 16) || !aligned(h, 16)) return MOE_E_INVAL;
+  if (!workspace || !aligned(workspace, 256) ||
+      ws_bytes < workspace_bytes(T * (k + n_shared), max_rank))
+    return MOE_E_WORKSPACE;
+  st = device_usable();
+  if (st != MOE_OK) return st;
+  LoraArgs a = args_of(T, H, I, E, k, n_shared, I_shared, adapter, n_adapters, max_rank, table,
+                       topk_ids, sorted_pair, static_cast<char*>(workspace), 2);
+  a.in = x;
+  a.gu = gu;
+  a.out = h;
+  a.out_f32 = (flags & MOE_H_F32) ? 1 : 0;
+  return from_hip(launch_lora_gateup(a, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_lora_down_combine(const void* h, int T, int H, int I, int E, int k,
+                                 int n_shared, int I_shared, const int32_t* adapter,
+                                 int n_adapters, int max_rank, const moe_lora* table,
+                                 const float* shared_gate, const float* topk_w,
+                                 const int32_t* topk_ids, const int32_t* offsets,
+                                 const int32_t* sorted_pair, const int32_t* pair_pos,
+                                 const float* base, void* out, void* workspace,
+                                 size_t ws_bytes, int flags, void* stream) {
+  moe_status st = check_shape(T, H, I, E, k, n_shared, I_shared, n_adapters, max_rank);
+  if (st != MOE_OK) return st;
+  if (flags & ~(MOE_H_F32 | MOE_OUT_F32)) return MOE_E_INVAL;
+  if (T == 0) return MOE_OK;
+  if (!h || !adapter || !topk_w || !topk_ids || !offsets || !sorted_pair || !pair_pos || !base ||
+      !out)
+    return MOE_E_INVAL;
+  if (out == base && !(flags & MOE_OUT_F32)) return MOE_E_INVAL;
+  if (n_adapters > 0 && (!table || !aligned(table, 8))) return MOE_E_INVAL;
+  if (!aligned(h, 16) || !aligned(base, 16) || !aligned(out, (flags & MOE_OUT_F32) ? 16 : 8))
+    return MOE_E_INVAL;
+  if (!workspace || !aligned(workspace, 256) ||
+      ws_bytes < workspace_bytes(T * (k + n_shared), max_rank))
+    return MOE_E_WORKSPACE;
+  st = device_usable();
+  if (st != MOE_OK) return st;
+  LoraArgs a = args_of(T, H, I, E, k, n_shared, I_shared, adapter, n_adapters, max_rank, table,
+                       topk_ids, sorted_pair, static_cast<char*>(workspace), 1);
+  a.in = h;
+  a.in_f32 = (flags & MOE_H_F32) ? 1 : 0;
+  a.offsets = offsets;
+  a.pair_pos = pair_pos;
+  a.topk_w = topk_w;
+  a.shared_gate = n_shared > 0 ? shared_gate : nullptr;
+  a.base = base;
+  a.out = out;
+  a.out_f32 = (flags & MOE_OUT_F32) ? 1 : 0;
+  return from_hip(launch_lora_down(a, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

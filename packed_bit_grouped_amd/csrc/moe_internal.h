@@ -62,8 +62,9 @@ struct ProjArgs {
   int n_rb;                    // work items per tile (MFMA path)
   int res_rows;                // rows of one result buffer in LDS (GEMV path)
   // outputs
-  void* out;                   // gate/up: h (bf16 or fp32); down: y fp32
+  void* out;                   // gate/up: h (bf16 or fp32), or its fp32 sums (raw); down: y fp32
   int ld_out;
+  int raw;                     // gate/up: rows of 2 ld_h fp32, the gate sums, then the up sums
   int32_t* err;
   // down with the combine fused (decode kernels): gate weights and the
   // sorted row of every pair

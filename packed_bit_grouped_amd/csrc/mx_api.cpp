@@ -348,7 +348,7 @@ moe_status moe_mx4_gateup_silu(int act, const uint16_t* x, int T, int H, int I, 
                                void* stream) {
   moe_status st = check_shape(act, T, H, I, E, k, n_shared, I_shared);
   if (st != MOE_OK) return st;
-  if (flags) return MOE_E_INVAL;
+  if (flags & ~MOE_GU_F32) return MOE_E_INVAL;
   if (T == 0) return MOE_OK;
   if (!x || !offsets || !sorted_pair || !h || !aligned(x, 16) || !aligned(h, 16))
     return MOE_E_INVAL;
@@ -362,6 +362,10 @@ moe_status moe_mx4_gateup_silu(int act, const uint16_t* x, int T, int H, int I, 
   set_banks(a, w13, w13_shared);
   a.x = x;
   a.out = h;
+  if (flags & MOE_GU_F32) {
+    a.raw = 1;
+    a.ld_out *= 2;
+  }
   return gateup(act, a, L, offsets, sorted_pair, static_cast<char*>(workspace),
                 static_cast<hipStream_t>(stream));
 }

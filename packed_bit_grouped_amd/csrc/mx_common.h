@@ -67,8 +67,9 @@ struct MxProj {
   int T, k, P, E, n_shared;
   const int32_t* offsets;      // [E + 1]
   const int32_t* sorted_pair;  // [P] (gate/up)
-  void* out;               // gate/up: h bf16; down: y fp32
+  void* out;               // gate/up: h bf16, or its fp32 sums (raw); down: y fp32
   int ld_out;
+  int raw;                 // gate/up: rows of 2 ld_h fp32, the gate sums, then the up sums
 };
 
 // fp32 -> bf16 bits, to nearest even, NaN kept.

@@ -150,7 +150,7 @@ struct Weights {
   template <int MODE>
   __device__ __forceinline__ void init(const Tile& t, const uint8_t* w, const uint8_t* ws, int e) {
     const int lane = threadIdx.x & 63;
-    const int N = MODE == 0 ? 2 * t.U : t.U;
+    const int N = MODE != 1 ? 2 * t.U : t.U;
     const size_t cb = mx_code_bytes(N, t.K), sb = mx_scale_bytes(N, t.K);
     crs = make_rsrc(w + e * cb, (uint32_t)cb);
     srs = make_rsrc(ws + e * sb, (uint32_t)sb);
@@ -158,8 +158,8 @@ struct Weights {
     const int pieces = mx_pieces(t.K), words = (pieces + 3) / 4;
 #pragma unroll
     for (int f = 0; f < NF; ++f) {
-      const int u = MODE == 0 ? t.u0 + 16 * (f % (NF / 2)) : t.u0 + 16 * f;
-      const int rb = ((MODE == 0 && f >= NF / 2 ? t.U : 0) + u) / 16;
+      const int u = MODE != 1 ? t.u0 + 16 * (f % (NF / 2)) : t.u0 + 16 * f;
+      const int rb = ((MODE != 1 && f >= NF / 2 ? t.U : 0) + u) / 16;
       coff[f] = u < t.U ? rb * pieces * 1024 + lane * 16 : kNone;
       soff[f] = u < t.U ? rb * words * 256 + lane * 4 : kNone;
     }
@@ -430,6 +430,15 @@ __device__ __forceinline__ void body(const GemmArgs& ga, const Tile& t, const We
         for (int i = 0; i < 4; ++i) v[i] = mx_bf16(hv[4 * f + i]);
         *reinterpret_cast<uint2*>(h + u) = make_uint2(v[0] | (v[1] << 16), v[2] | (v[3] << 16));
       }
+    } else if (MODE == 2) {
+      // the gate and up sums as they are, up behind the row's first half
+      float* y = static_cast<float*>(ga.p.out) + (size_t)(t.orow + row) * ga.p.ld_out;
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        const int u = t.u0 + 16 * (f % (NF / 2)) + 4 * g;
+        if (u < t.U)
+          *reinterpret_cast<mx_f32x4*>(y + u + (f < NF / 2 ? 0 : ga.p.ld_out / 2)) = acc[f][m];
+      }
     } else {
       float* y = static_cast<float*>(ga.p.out) + (size_t)(t.orow + row) * ga.p.ld_out;
 #pragma unroll
@@ -494,17 +503,17 @@ void mx_gemm_kernel(GemmArgs ga) {
   t.K = is_sh ? a.K_sh : a.K;
   t.U = is_sh ? a.U_sh : a.U;
   t.n_st = (t.K + kKS - 1) / kKS;
-  const int ublk = ub * (MODE == 0 ? 32 : 64) * NF;
+  const int ublk = ub * (MODE != 1 ? 32 : 64) * NF;
   if (ublk >= t.U) return;
-  t.u0 = ublk + wave * (MODE == 0 ? 8 : 16) * NF;
+  t.u0 = ublk + wave * (MODE != 1 ? 8 : 16) * NF;
   t.orow = is_sh ? a.P + e * a.T + r0 : r0;
   // gate/up gathers rows of x by token; down reads its own rows, the shared
   // experts' behind the routed ones
-  const int arow = MODE == 0 ? 0 : (is_sh ? a.P : 0);
+  const int arow = MODE != 1 ? 0 : (is_sh ? a.P : 0);
   const size_t stride = ACT4 ? (size_t)ga.KP / 2 : (size_t)a.ld_in * 2;
   t.row_bytes = (int)stride;
   t.act = (ACT4 ? a.q : reinterpret_cast<const uint8_t*>(a.x)) + arow * stride;
-  const int act_rows = MODE == 0 ? a.T : (is_sh ? a.n_shared * a.T : a.P);
+  const int act_rows = MODE != 1 ? a.T : (is_sh ? a.n_shared * a.T : a.P);
   t.act_bytes = (uint32_t)(act_rows * stride);
   // the first step's weights need only the tile: on their way before its rows
   // are looked up
@@ -621,7 +630,11 @@ hipError_t launch_mx_gemm(const MxProj& a, int mode, int act4, hipStream_t st) {
   const size_t lds = lds_bytes(act4, p.KP, p.tm, p.narrow ? 2 : 4);
 #define MX_GO(MODE, ACT4, NF, TM) \
   mx_gemm_kernel<MODE, ACT4, NF, TM><<<(int)p.grid, kThreads, lds, st>>>(ga)
-  if (p.narrow) {
+  if (mode == 0 && a.raw) {
+    if (p.narrow) MX_GO(2, true, 2, kRowsNarrow);
+    else if (act4) MX_GO(2, true, 4, kRowsMax);
+    else MX_GO(2, false, 4, kRowsMax);
+  } else if (p.narrow) {
     if (mode == 0) MX_GO(0, true, 2, kRowsNarrow);
     else MX_GO(1, true, 2, kRowsNarrow);
   } else if (act4) {

@@ -466,7 +466,12 @@ __global__ __launch_bounds__(kThreads) void mx_rows16_kernel(MxProj a, MxRoute r
     v1 += red[w][1][u * kPitch + m];
   }
   const size_t o = (size_t)(orow + m) * a.ld_out + u0 + u;
-  if (MODE == 0) {
+  if (MODE == 0 && a.raw) {
+    if (u0 + u < U) {
+      static_cast<float*>(a.out)[o] = v0;
+      static_cast<float*>(a.out)[o + a.ld_out / 2] = v1;
+    }
+  } else if (MODE == 0) {
     const float gv[1] = {v0}, uv[1] = {v1};
     float hv[1];
     mx_silu_mul(gv, uv, hv);

@@ -253,8 +253,13 @@ __global__ __launch_bounds__(kGemvThreads) void proj_gemv_kernel(ProjArgs a) {
               gv *= xsc[m];
               uv *= xsc[m];
             }
-            const float hv = silu_mul(gv, uv);
             const size_t o = (size_t)(orow_base + m) * a.ld_out + unit0 + ub + i;
+            if (a.raw) {
+              static_cast<float*>(a.out)[o] = gv;
+              static_cast<float*>(a.out)[o + a.ld_out / 2] = uv;
+              continue;
+            }
+            const float hv = silu_mul(gv, uv);
             if (ACT == MOE_A16) static_cast<uint16_t*>(a.out)[o] = (uint16_t)f32_to_bf16(hv);
             else static_cast<float*>(a.out)[o] = hv;
           }

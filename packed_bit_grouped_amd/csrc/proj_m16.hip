@@ -577,8 +577,13 @@ __device__ __forceinline__ void m16_tile(const ProjArgs& a, const moe_qmat& q, b
             gv *= xsc[t];
             uv *= xsc[t];
           }
-          const float hv = silu_mul(gv, uv);
           const size_t o = (size_t)(orow0 + t) * a.ld_out + unit;
+          if (a.raw) {
+            static_cast<float*>(a.out)[o] = gv;
+            static_cast<float*>(a.out)[o + a.ld_out / 2] = uv;
+            continue;
+          }
+          const float hv = silu_mul(gv, uv);
           if (ACT == MOE_A16) static_cast<uint16_t*>(a.out)[o] = (uint16_t)f32_to_bf16(hv);
           else static_cast<float*>(a.out)[o] = hv;
         }

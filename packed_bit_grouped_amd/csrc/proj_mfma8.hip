@@ -293,7 +293,7 @@ __device__ __forceinline__ void chunk(const ProjArgs& a, const Tile& t, const La
   int r = 0;
   if (tid < kRowsMax) {
     const int mm = tid < nrows ? tid : 0;   // padding rows re-read row 0 (discarded)
-    if (MODE == 0) r = t.is_sh ? mc + mm : a.sorted_pair[mc + mm];
+    if (MODE != 1) r = t.is_sh ? mc + mm : a.sorted_pair[mc + mm];
     else r = t.is_sh ? a.P + t.e * a.T + mc + mm : mc + mm;
   }
   BReg<BITS> b0, b1, b2, b3, b4, b5, b6, b7;
@@ -307,7 +307,7 @@ __device__ __forceinline__ void chunk(const ProjArgs& a, const Tile& t, const La
     load_b(4, b4); load_b(5, b5); load_b(6, b6); load_b(7, b7);
   }
   __syncthreads();   // previous chunk's readers of tok are done
-  if (tid < kRowsMax) tok[tid] = (MODE == 0 && !t.is_sh) ? r / a.k : r;
+  if (tid < kRowsMax) tok[tid] = (MODE != 1 && !t.is_sh) ? r / a.k : r;
   __syncthreads();
   // activations: piece q = (wave * MBA + i) * 64 + lane of a step (row q >>
   // 3, LDS slot q & 7) holds global chunk (q & 7) ^ ((row >> 1) & 7) of the
@@ -574,7 +574,8 @@ __device__ __forceinline__ void chunk(const ProjArgs& a, const Tile& t, const La
       }
     }
   } else {
-    // y tile of one part [rows][32] fp32, row stride 160 bytes
+    // y tile of one part [rows][32] fp32, row stride 160 bytes; the gate and
+    // up sums (mode 2) the same way, up behind the row's first half
     constexpr int kRowB = 160;
     unsigned char* stg = reinterpret_cast<unsigned char*>(As) + wave * (kRowsMax * kRowB);
 #pragma unroll
@@ -597,7 +598,8 @@ __device__ __forceinline__ void chunk(const ProjArgs& a, const Tile& t, const La
       }
       __syncthreads();   // lanes read what other lanes wrote
       const int q = lane & 7;
-      const int col = ln_.wrow[p] - lc + 4 * q;
+      const int col = MODE == 1 ? ln_.wrow[p] - lc + 4 * q
+                                : ln_.wrow[0] - lc + 4 * q + p * (a.ld_out / 2);
 #pragma unroll
       for (int i = 0; i < (MBT * 32 + HT * 16 + 7) / 8; ++i) {
         const int m = 8 * i + (lane >> 3);
@@ -622,12 +624,12 @@ __device__ __forceinline__ void tile(const ProjArgs& a, const Tile& t, u32x4_v* 
   const int K = t.K, U = t.U;
   const int ng = K / t.group;
   const int row_bytes = K * BITS / 8;
-  const int n_wrows = MODE == 0 ? 2 * U : U;
+  const int n_wrows = MODE != 1 ? 2 * U : U;
 
   Lane L;
   L.n_st = K / kKS;
   int brow[2];   // this lane's weight rows
-  if (MODE == 0) {
+  if (MODE != 1) {
     const int unit = t.u0 + 32 * n + lc;
     L.wval[0] = L.wval[1] = unit < U;
     L.wrow[0] = L.wrow[1] = unit;
@@ -653,7 +655,7 @@ __device__ __forceinline__ void tile(const ProjArgs& a, const Tile& t, u32x4_v* 
   if (PP) {
     // gate/up: [unit block of 32][step][gate, up][64 lane slots]; down:
     // [row block of 32][step][64 lane slots]
-    if (MODE == 0) {
+    if (MODE != 1) {
       const int blk = t.u0 / 32 + n;
       L.cstride = 2 * 64 * kLaneBytes;
 #pragma unroll
@@ -681,7 +683,7 @@ __device__ __forceinline__ void tile(const ProjArgs& a, const Tile& t, u32x4_v* 
     // barrier (it waits for an activation load issued later) covers them
     uint32_t* sw = reinterpret_cast<uint32_t*>(As + kABufs * kABuf) + kRowsMax +
                    n * (kSclGroupsMax * 32);
-    const int sblk = MODE == 0 ? t.u0 / 32 + n : (t.u0 + 64 * n) / 64;
+    const int sblk = MODE != 1 ? t.u0 / 32 + n : (t.u0 + 64 * n) / 64;
     const int nld = (ng * 128 + 1023) / 1024;
     for (int i = 0; i < nld; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
@@ -758,10 +760,10 @@ void proj_mfma8_kernel(ProjArgs a, const uint16_t* x16) {
   }
   t.K = t.is_sh ? a.K_sh : a.K;
   t.U = t.is_sh ? a.U_sh : a.U;
-  t.u0 = nb * (MODE == 0 ? kUnits : 2 * kUnits);
+  t.u0 = nb * (MODE != 1 ? kUnits : 2 * kUnits);
   if (t.u0 >= t.U) return;
   const moe_qmat q = t.is_sh ? a.w_sh[t.e] : a.w[t.e];
-  if (!qmat_usable(q, MODE == 0 ? 2 * t.U : t.U, t.K) || t.K % (2 * kKS) != 0 ||
+  if (!qmat_usable(q, MODE != 1 ? 2 * t.U : t.U, t.K) || t.K % (2 * kKS) != 0 ||
       (PP && (t.K / q.group > kSclGroupsMax ||
               (reinterpret_cast<uintptr_t>(q.scales) & 15) != 0))) {
     if (tid == 0) atomicOr(a.err, 1);
@@ -771,8 +773,8 @@ void proj_mfma8_kernel(ProjArgs a, const uint16_t* x16) {
   t.scales = q.scales;
   t.group = q.group;
   // rows the activation source holds: T token rows, or every h row
-  t.a_bytes = (uint32_t)((size_t)(MODE == 0 ? a.T : a.P + a.n_shared * a.T) * a.ld_in * 2);
-  t.asrc = MODE == 0 ? x16 : a.in_bf16;
+  t.a_bytes = (uint32_t)((size_t)(MODE != 1 ? a.T : a.P + a.n_shared * a.T) * a.ld_in * 2);
+  t.asrc = MODE != 1 ? x16 : a.in_bf16;
   if (q.bits == 4) tile<MODE, 4, PP>(a, t, As, tok);
   else tile<MODE, 2, PP>(a, t, As, tok);
 }
@@ -828,7 +830,10 @@ hipError_t launch_proj_mfma8(const ProjArgs& a_in, uint16_t* a16, bool prepacked
                      (prepacked ? (size_t)4 * kSclGroupsMax * 32 * 4 : 0);
   if (lds > 160 * 1024) return hipErrorInvalidValue;
   const dim3 g((unsigned)blocks), blk(kThreads);
-  if (a.mode == 0) {
+  if (a.mode == 0 && a.raw) {
+    if (prepacked) proj_mfma8_kernel<2, true><<<g, blk, lds, st>>>(a, a16);
+    else proj_mfma8_kernel<2, false><<<g, blk, lds, st>>>(a, a16);
+  } else if (a.mode == 0) {
     if (prepacked) proj_mfma8_kernel<0, true><<<g, blk, lds, st>>>(a, a16);
     else proj_mfma8_kernel<0, false><<<g, blk, lds, st>>>(a, a16);
   } else {

@@ -279,25 +279,30 @@ def _gate(shared_gate, B):
     return _want("shared_gate", shared_gate, _F32, (B.T, B.n_shared), B._dev)
 
 
-def gateup_silu(bank, x, offsets, sorted_pair, B, stream=None):
+def gateup_silu(bank, x, offsets, sorted_pair, B, stream=None, gu=None):
     """h [T*k + n_shared*T][max(I, I_shared)] in bf16 (B.h) of x bf16 [T][H] and
     the sort's tables (int32): rows in the order of the sort, then the shared
-    experts' tokens."""
+    experts' tokens.  With gu, fp32 [...][2*max(I, I_shared)], the gate and up
+    sums go there as they are (MOE_GU_F32, see lora.py), and gu is returned."""
     dev = B._dev
     px = _want("x", x, _BF16, (B.T, B.H), dev)
     po = _want("offsets", offsets, _I32, (B.E + 1,), dev)
     pp = _want("sorted_pair", sorted_pair, _I32, (B.P,), dev)
     need, mats = bank.need, B.mats
     w13, sh = need("w13", mats["w13"], dev), need("w13_shared", mats["w13_shared"], dev)
+    if gu is None:
+        to, flags = B.h.data_ptr(), 0
+    else:
+        to, flags = _want("gu", gu, _F32, (B.R, 2 * B.ld_h), dev), L.MOE_GU_F32
     _launch("moe_mx4_gateup_silu", dev, stream, B.act, px, B.T, B.H, B.I, B.E, B.k, w13, sh,
-            B.n_shared, B.I_shared, po, pp, B.h.data_ptr(), B.ws.data_ptr(), B.ws_bytes, 0)
-    return B.h
+            B.n_shared, B.I_shared, po, pp, to, B.ws.data_ptr(), B.ws_bytes, flags)
+    return B.h if gu is None else gu
 
 
-def down_combine(bank, h, w, offsets, pair_pos, B, shared_gate=None, stream=None):
-    """out [T][H] (B.out) of h (as from gateup_silu), the gate weights w fp32
-    [T][k] and the sort's tables; shared_gate fp32 [T][n_shared]: gate logits of
-    the shared experts (sigmoid), None: weight 1."""
+def down_combine(bank, h, w, offsets, pair_pos, B, shared_gate=None, stream=None, out=None):
+    """out [T][H] (B.out, or `out` in fp32 if given) of h (as from gateup_silu),
+    the gate weights w fp32 [T][k] and the sort's tables; shared_gate fp32
+    [T][n_shared]: gate logits of the shared experts (sigmoid), None: weight 1."""
     dev = B._dev
     ph = _want("h", h, _BF16, (B.R, B.ld_h), dev)
     pw = _want("w", w, _F32, (B.T, B.k), dev)
@@ -305,10 +310,14 @@ def down_combine(bank, h, w, offsets, pair_pos, B, shared_gate=None, stream=None
     pp = _want("pair_pos", pair_pos, _I32, (B.P,), dev)
     need, mats = bank.need, B.mats
     w2, sh = need("w2", mats["w2"], dev), need("w2_shared", mats["w2_shared"], dev)
+    if out is None:
+        to, flags = B.out.data_ptr(), B.out_flags
+    else:
+        to, flags = _want("out", out, _F32, (B.T, B.H), dev), L.MOE_OUT_F32
     _launch("moe_mx4_down_combine", dev, stream, B.act, ph, B.T, B.H, B.I, B.E, B.k, w2, sh,
-            B.n_shared, B.I_shared, _gate(shared_gate, B), pw, po, pp, B.out.data_ptr(),
-            B.ws.data_ptr(), B.ws_bytes, B.out_flags)
-    return B.out
+            B.n_shared, B.I_shared, _gate(shared_gate, B), pw, po, pp, to, B.ws.data_ptr(),
+            B.ws_bytes, flags)
+    return B.out if out is None else out
 
 
 def run_layer(bank, x, logits, B, renormalize=1, shared_gate=None, stream=None):
