@@ -792,7 +792,8 @@ typedef struct moe_lora {
  * sizes they refuse.  Its first 4 bytes are the error word, which the caller
  * zeroes once and reads when it wants to; nothing else is kept between calls.
  * Calls that overlap in time need a workspace each. */
-size_t moe_lora_workspace_bytes(int T, int k, int n_shared, int max_rank);
+size_t moe_lora_workspace_bytes(int T, int H, int I, int E, int k, int n_shared, int I_shared,
+                                int max_rank);
 
 /* ---------------------------------------------------------------------
  * moe_lora_gateup_silu -- h of every routed pair and shared-expert token from
@@ -814,8 +815,8 @@ size_t moe_lora_workspace_bytes(int T, int k, int n_shared, int max_rank);
  * MOE_H_F32, in down's A) may come out as NaN.
  * Limits: H, I, I_shared multiples of 32 and at most 2^20, E <= 1024, n_shared
  * <= 65535, n_adapters * (E + n_shared) < 2^31, max_rank a multiple of 8 up to
- * 128, T*k < 2^24, T*(k + n_shared) times H or max(I, I_shared) < 2^31; else
- * MOE_E_UNSUPPORTED.  x, gu, h 16-byte aligned.  T = 0 launches nothing.
+ * 128, T*k < 2^24, T*(k + n_shared) < 2^26 and times H or max(I, I_shared) <
+ * 2^31; else MOE_E_UNSUPPORTED.  x, gu, h 16-byte aligned.  T = 0 launches nothing.
  * ------------------------------------------------------------------- */
 #define MOE_H_F32 512        /* moe_lora_* calls: h is fp32 (A8 layers) */
 moe_status moe_lora_gateup_silu(const uint16_t* x, int T, int H, int I, int E, int k,

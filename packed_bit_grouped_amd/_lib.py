@@ -129,7 +129,7 @@ _SIGS = {
                               c_void_p]),
     "moe_route_scored": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_int, c_int,
                                  c_int, c_int, c_float, c_void_p, c_void_p, c_void_p]),
-    "moe_lora_workspace_bytes": (c_size_t, [c_int] * 4),
+    "moe_lora_workspace_bytes": (c_size_t, [c_int] * 8),
     "moe_lora_gateup_silu": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
                                      c_void_p, c_int, c_int, c_void_p, c_void_p, c_void_p,
                                      c_void_p, c_void_p, c_void_p, c_size_t, c_int, c_void_p]),
@@ -461,8 +461,8 @@ def moe_mx4_layer(act, logits, x, T, H, I, E, k, renormalize, w13, w2, w13_share
                  ws_bytes, flags, _stream(stream), check=check)
 
 
-def moe_lora_workspace_bytes(T, k, n_shared, max_rank) -> int:
-    return load().moe_lora_workspace_bytes(T, k, n_shared, max_rank)
+def moe_lora_workspace_bytes(T, H, I, E, k, n_shared=0, I_shared=0, max_rank=16) -> int:
+    return load().moe_lora_workspace_bytes(T, H, I, E, k, n_shared, I_shared, max_rank)
 
 
 def moe_lora_gateup_silu(x, T, H, I, E, k, n_shared, I_shared, adapter, n_adapters, max_rank,

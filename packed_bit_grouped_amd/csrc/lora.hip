@@ -71,12 +71,15 @@ __device__ __forceinline__ void split3(const float (&f)[8], u32x4 (&s)[3]) {
 // of places without a row.
 constexpr int kBaseShared = -1, kBaseRouted = -2, kNoRow = -3;
 
-// A lane's row of the window: its token, width and number in the adapters' table.
+// A lane's row of the window: its token and number in the adapters' table, and
+// (WEIGHT) what its output joins the token's with.
 struct Row {
   int token, key;
+  float weight;
 };
+template <bool WEIGHT>
 __device__ __forceinline__ Row window_row(const LoraArgs& a, int r, bool in) {
-  Row w = {0, kNoRow};
+  Row w = {0, kNoRow, 1.0f};
   if (!in || r >= a.R) return w;
   int e;
   if (r < a.P) {
@@ -85,10 +88,13 @@ __device__ __forceinline__ Row window_row(const LoraArgs& a, int r, bool in) {
     e = a.topk_ids[p];
     if ((unsigned)e >= (unsigned)a.E) return w;
     w.token = p / a.k;
+    if (WEIGHT) w.weight = a.topk_w[p];
   } else {
     const int q = r - a.P, s = q / a.T;
     w.token = q - s * a.T;
     e = a.E + s;
+    if (WEIGHT && a.shared_gate)
+      w.weight = shared_gate_weight(a.shared_gate[(size_t)w.token * a.n_shared + s]);
   }
   const int d = a.adapter[w.token];
   w.key = (unsigned)d < (unsigned)a.n ? d * (a.E + a.n_shared) + e
@@ -104,15 +110,17 @@ struct Pair {
   int rank;
   float scale;
 };
+__device__ __forceinline__ bool entry_ok(const LoraArgs& a, const moe_lora& d, int N, int K) {
+  return d.rank > 0 && d.rank <= a.max_rank && d.rank % 8 == 0 && d.N == N && d.K == K &&
+         d.a != nullptr && d.b != nullptr &&
+         ((reinterpret_cast<uintptr_t>(d.a) | reinterpret_cast<uintptr_t>(d.b)) & 15) == 0;
+}
 __device__ __forceinline__ Pair pair_of(const LoraArgs& a, int key, int N, int K) {
   Pair p = {nullptr, nullptr, 0, 0.0f};
   if (key < 0) return p;
   const moe_lora d = a.table[key];
   if (d.rank == 0) return p;
-  const bool ok = d.rank > 0 && d.rank <= a.max_rank && d.rank % 8 == 0 && d.N == N && d.K == K &&
-                  d.a != nullptr && d.b != nullptr &&
-                  ((reinterpret_cast<uintptr_t>(d.a) | reinterpret_cast<uintptr_t>(d.b)) & 15) == 0;
-  if (!ok) {
+  if (!entry_ok(a, d, N, K)) {
     if (threadIdx.x == 0) atomicOr(a.err, 1);
     return p;
   }
@@ -158,10 +166,14 @@ __device__ __forceinline__ int list_rows(uint64_t rows, int* list) {
 // The workgroup's waves (and, for few rows, `splits` workgroups) share K; a
 // wave's fragments go from memory to registers, 16 bytes per lane, since every
 // byte of A and of the rows is read by one wave only.
-template <int NF, int CT, bool F32>
+//
+// PARTS: v goes out times the row's weight, as three bf16 parts (the accumulating
+// kernel's operand: it would else be split once per slab of columns).
+template <int NF, int CT, bool F32, bool PARTS>
 __device__ __forceinline__ void shrink_group(const LoraArgs& a, const Pair& p, int K, int C, int ct0,
                                              int split, const void* const (&rows)[NF],
-                                             const int (&row)[NF], int n, float* red) {
+                                             const int (&row)[NF], const float (&weight)[NF], int n,
+                                             float* red) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = lane & 15, g = lane >> 4;
   const int steps = K >> 5, workers = kWaves * a.splits, me = split * kWaves + wave;
@@ -244,21 +256,182 @@ __device__ __forceinline__ void shrink_group(const LoraArgs& a, const Pair& p, i
       for (int w = 0; w < kWaves; ++w)
         t += *reinterpret_cast<const f32x4*>(red + ((w * NF * CT + f * CT + j) * 64 + lane) * 4);
       const int col = 16 * (ct0 + j) + 4 * g;
-      if (16 * f + c < n && col < C)
-        *reinterpret_cast<f32x4*>(v + (size_t)row[f] * VL + col) = t * p.scale;
+      if (16 * f + c >= n) continue;
+      if (col >= C) continue;
+      t *= p.scale;
+      if constexpr (PARTS) {
+        uint32_t q[4][3];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split3(t[i] * weight[f], q[i][0], q[i][1], q[i][2]);
+        // a piece of 8 ranks of neighbouring rows is contiguous: what a fragment loads
+        uint16_t* o = a.parts + ((size_t)(col >> 3) * a.R + row[f]) * 8 + (col & 7);
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+          *reinterpret_cast<uint2*>(o + (size_t)e * a.R * a.max_rank) =
+              make_uint2(q[0][e] | (q[1][e] << 16), q[2][e] | (q[3][e] << 16));
+      } else {
+        *reinterpret_cast<f32x4*>(v + (size_t)row[f] * VL + col) = t;
+      }
     }
 }
 
-template <int NW, int CT, bool F32>
-__global__ __launch_bounds__(kThreads) void lora_shrink_kernel(LoraArgs a, int slots) {
+// First of [lo, hi) whose pair is at least p (an expert's rows are in the order
+// of their pairs).
+__device__ __forceinline__ int first_pair(const int32_t* sorted_pair, int lo, int hi, int p) {
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (sorted_pair[mid] < p) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// The plan of the accumulating kernel: the rows of one block of tokens, experts
+// in order, in windows of 64; a window's rows reordered by (adapter, expert) and
+// cut into units.  Workgroup `part` of a block makes 8 windows.  It reads no
+// product, so it runs in the shrinking launch, behind its workgroups.
+constexpr int kPlanWindows = 8;
+struct PlanLds {
+  int lo[kLoraPlanMaxE], pos[kLoraPlanMaxE + 1], wave_sum[kWaves];
+};
+__device__ void make_plan(const LoraArgs& a, int b, int part, PlanLds& L) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int NE = a.E + a.n_shared;
+  const int t0 = b * a.block, t1 = min(a.T, t0 + a.block);
+  for (int e = tid; e < NE; e += kThreads) {
+    int lo, hi;
+    if (e < a.E) {
+      const int o0 = min(max(a.offsets[e], 0), a.P), o1 = min(max(a.offsets[e + 1], o0), a.P);
+      lo = first_pair(a.sorted_pair, o0, o1, t0 * a.k);
+      hi = first_pair(a.sorted_pair, lo, o1, t1 * a.k);
+    } else {
+      lo = a.P + (e - a.E) * a.T + t0;
+      hi = lo + t1 - t0;
+    }
+    L.lo[e] = lo;
+    L.pos[e] = hi - lo;
+  }
+  __syncthreads();
+  // exclusive sums: a thread owns PER experts
+  constexpr int PER = (kLoraPlanMaxE + kThreads - 1) / kThreads;
+  int cnt[PER], own = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = tid * PER + i;
+    cnt[i] = e < NE ? L.pos[e] : 0;
+    own += cnt[i];
+  }
+  int pre = own;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int v = __shfl_up(pre, d);
+    if (lane >= d) pre += v;
+  }
+  if (lane == 63) L.wave_sum[wave] = pre;
+  __syncthreads();
+  int total = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    if (w < wave) before += L.wave_sum[w];
+    total += L.wave_sum[w];
+  }
+  int at = before + pre - own;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = tid * PER + i;
+    if (e < NE) L.pos[e] = at;
+    at += cnt[i];
+  }
+  __syncthreads();
+  const size_t base = (size_t)b * a.win;
+  for (int i = wave; i < kPlanWindows; i += kWaves) {
+    const int w = part * kPlanWindows + i;
+    if (w >= a.win) break;
+    const int q = 64 * w + lane;
+    int key = -1, row = 0, token = 0, rank = 0;
+    const uint16_t* bp = nullptr;
+    if (q < total) {
+      int e = 0, hi = NE;   // the last expert whose rows start at q or before
+      while (hi - e > 1) {
+        const int mid = (e + hi) >> 1;
+        if (L.pos[mid] <= q) e = mid;
+        else hi = mid;
+      }
+      row = L.lo[e] + q - L.pos[e];
+      if (e < a.E) {
+        const int p = a.sorted_pair[row];
+        token = (unsigned)p < (unsigned)a.P ? p / a.k : -1;
+      } else {
+        token = row - a.P - (e - a.E) * a.T;
+      }
+      if (token >= t0 && token < t1) {
+        const int d = a.adapter[token];
+        if ((unsigned)d < (unsigned)a.n) {
+          const moe_lora m = a.table[(size_t)d * NE + e];
+          if (entry_ok(a, m, a.H, e < a.E ? a.I : a.I_sh)) {
+            key = d * NE + e;
+            rank = m.rank;
+            bp = m.b;
+          }
+        }
+      }
+    }
+    // a token that lists an expert twice has neighbouring rows: each time apart
+    const int token1 = __shfl_up(token, 1), key1 = __shfl_up(key, 1);
+    const bool same = lane > 0 && token1 == token && key1 == key;
+    const uint64_t first = ~__ballot(same) & ((2ull << lane) - 1);
+    const int again = lane - (63 - __builtin_clzll(first));
+    uint64_t todo = __ballot(key >= 0);
+    int units = 0;
+    while (todo) {
+      const int lead = __builtin_ctzll(todo);
+      const uint64_t rows = __ballot(key == __builtin_amdgcn_readlane(key, lead) &&
+                                     again == __builtin_amdgcn_readlane(again, lead));
+      todo &= ~rows;
+      const int n = __popcll(rows), nu = (n + 15) / 16;
+      const uint64_t bits = reinterpret_cast<uint64_t>(bp);
+      const uint32_t b_hi = (uint32_t)__builtin_amdgcn_readlane((int)(bits >> 32), lead);
+      const uint32_t b_lo = (uint32_t)__builtin_amdgcn_readlane((int)bits, lead);
+      const u32x4 u = {b_lo, b_hi, (uint32_t)__builtin_amdgcn_readlane(rank, lead) / 8, 0u};
+      const size_t first_unit = (base + w) * 64 + units;
+      if (lane < nu) reinterpret_cast<u32x4*>(a.plan)[first_unit + lane] = u;
+      if ((rows >> lane) & 1) {
+        const int t = token - t0;
+        const LoraUnitRow r = {(uint32_t)row, (uint32_t)(t * 256 + (t & 15) * 16)};
+        a.plan_rows[first_unit * 16 + __popcll(rows & ((1ull << lane) - 1))] = r;
+      }
+      // places without a row: any row's v, added behind the block
+      if (n + lane < 16 * nu)
+        a.plan_rows[first_unit * 16 + n + lane] =
+            LoraUnitRow{(uint32_t)__builtin_amdgcn_readlane(row, lead), (uint32_t)a.block * 256};
+      units += nu;
+    }
+    if (lane == 0) a.plan_count[base + w] = units;
+  }
+}
+
+template <int NW, int CT, bool F32, bool PARTS>
+__global__ __launch_bounds__(kThreads) void lora_shrink_kernel(LoraArgs a, int slots, int n_win) {
   constexpr int NFM = NW / 16;
   __shared__ int list[kWaves][64];
-  __shared__ __align__(16) float red[kWaves * NFM * CT * 256];
+  union Lds {
+    float red[kWaves * NFM * CT * 256];
+    PlanLds plan;
+  };
+  __shared__ __align__(16) typename std::conditional<PARTS, Lds, float[kWaves * NFM * CT * 256]>::type lds;
+  float* red = reinterpret_cast<float*>(&lds);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15;
   const int win = blockIdx.x / slots, slot = blockIdx.x - win * slots;
   const int ct0 = blockIdx.y * CT, split = blockIdx.z;
+  if constexpr (PARTS) {
+    if (win >= n_win) {
+      const int per = (a.win + kPlanWindows - 1) / kPlanWindows, q = win - n_win;
+      if (blockIdx.y == 0) make_plan(a, q / per, q % per, lds.plan);
+      return;
+    }
+  }
   const int r0 = win * NW;
-  const Row w = window_row(a, r0 + lane, lane < NW);
+  const Row w = window_row<PARTS>(a, r0 + lane, lane < NW);
   Groups gr;
   gr.init(w.key, 0);
   uint64_t rows;
@@ -275,17 +448,19 @@ __global__ __launch_bounds__(kThreads) void lora_shrink_kernel(LoraArgs a, int s
       constexpr int NF = decltype(nf)::value;
       const void* src[NF];
       int row[NF];
+      float weight[NF];
 #pragma unroll
       for (int f = 0; f < NF; ++f) {
         // fragments' rows past the group's end are computed and dropped
         const int l = list[wave][min(16 * f + c, n - 1)];
         row[f] = r0 + l;
         const int token = __shfl(w.token, l);
+        weight[f] = PARTS ? __shfl(w.weight, l) : 1.0f;
         if (a.halves == 2) src[f] = static_cast<const uint16_t*>(a.in) + (size_t)token * a.H;
         else if (F32) src[f] = static_cast<const float*>(a.in) + (size_t)row[f] * a.ld_h;
         else src[f] = static_cast<const uint16_t*>(a.in) + (size_t)row[f] * a.ld_h;
       }
-      shrink_group<NF, CT, F32>(a, p, K, C, ct0, split, src, row, n, red);
+      shrink_group<NF, CT, F32, PARTS>(a, p, K, C, ct0, split, src, row, weight, n, red);
     };
     if constexpr (NFM == 1) {
       run(std::integral_constant<int, 1>{});
@@ -410,7 +585,7 @@ __global__ __launch_bounds__(kThreads) void lora_expand_gateup_kernel(LoraArgs a
   const int win = blockIdx.x / slots, slot = blockIdx.x - win * slots;
   const int i0 = (blockIdx.y * kWaves + wave) * 32;
   const int r0 = win * NW;
-  const Row w = window_row(a, r0 + lane, lane < NW);
+  const Row w = window_row<false>(a, r0 + lane, lane < NW);
   Groups gr;
   gr.init(w.key, kBaseRouted);
   uint64_t rows;
@@ -534,18 +709,222 @@ __global__ __launch_bounds__(kThreads) void lora_expand_down_kernel(LoraArgs a) 
   }
 }
 
+// ---------------------------------------------------------------------
+// expand, down, of many tokens.  A workgroup owns 64 columns of a block of
+// tokens and keeps their sums in LDS (fp32), starting from base; it passes the
+// block's units (make_plan) and adds each unit's products B v to its tokens'.  A
+// wave owns 16 of the columns of all the tokens, so no two waves meet in a sum,
+// and a unit holds a token once, so no two lanes do: plain reads and writes in a
+// wave's own order, the same result every time (LDS additions without return were
+// ten times slower: 500 us for 4096 tokens, H 2048).  (Rows of y through memory as in the shared
+// projection would be 600 MB for 4096 tokens of 9 rows and H 2048; by tokens,
+// without any reuse of B between them, it took 381 us.)
+// A token's 64 sums are 16 chunks of 4; chunk q lies at q ^ (token % 16), so that
+// the 16 tokens of a unit spread over the banks.
+constexpr int kUnitsAtOnce = 96;   // in LDS
+
+template <int KB>   // steps of 32 ranks
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2)))
+void lora_accumulate_kernel(LoraArgs a, int n_slabs) {
+  extern __shared__ f32x4 sums[];                // [block + 1][16]
+  __shared__ u32x4 unit_mem[9 * kUnitsAtOnce];   // units, then their rows
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int c = lane & 15, g = lane >> 4;
+  // the workgroups of an XCD (b mod 8) share slabs: B's rows of a slab stay in its L2
+  const int xcd = blockIdx.x & 7, li = blockIdx.x >> 3;
+  const int slab = xcd + 8 * (li / a.n_blocks), b = li % a.n_blocks;
+  if (slab >= n_slabs) return;
+  const int n0 = slab * kLoraSlab, t0 = b * a.block, nt = min(a.block, a.T - t0);
+
+  // The units of a segment of windows, `first` on, on their way to LDS: thread t
+  // takes pieces t, t + 256, ... of 16 bytes (a unit has 9).
+  constexpr int kPer = (9 * kUnitsAtOnce + kThreads - 1) / kThreads;
+  const size_t base = (size_t)b * a.win;
+  struct Chunk {
+    u32x4 piece[kPer];
+    int n;   // units
+  };
+  auto load_counts = [&](int w0) { return a.plan_count[base + w0 + (lane & (kLoraSegment - 1))]; };
+  auto load_chunk = [&](int w0, int counts, int first, Chunk& x) {
+    int before[kLoraSegment + 1];   // units of the windows before
+    before[0] = 0;
+#pragma unroll
+    for (int w = 0; w < kLoraSegment; ++w)
+      before[w + 1] = before[w] + __builtin_amdgcn_readlane(counts, w);
+    x.n = min(before[kLoraSegment] - first, kUnitsAtOnce);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int p = tid + i * kThreads, u = min(p / 9, x.n - 1), q = p - p / 9 * 9, at = first + u;
+      int w = 0, start = 0;
+#pragma unroll
+      for (int k = 1; k < kLoraSegment; ++k)
+        if (at >= before[k]) {
+          w = k;
+          start = before[k];
+        }
+      const size_t slot = (base + w0 + w) * 64 + (at - start);
+      if (x.n > 0)
+        x.piece[i] = q == 0 ? reinterpret_cast<const u32x4*>(a.plan)[slot]
+                            : reinterpret_cast<const u32x4*>(a.plan_rows)[slot * 8 + q - 1];
+    }
+    return before[kLoraSegment];
+  };
+  Chunk next;
+  int w0 = 0, first = 0;
+  int counts = load_counts(0);
+  int counts1 = kLoraSegment < a.win ? load_counts(kLoraSegment) : 0;
+  int total = load_chunk(0, counts, 0, next);
+
+  const int q0 = tid & 15, nq = min(n0 + 4 * q0, a.H - 4);   // columns past H: never stored
+  for (int i0 = tid >> 4; i0 < nt; i0 += 8 * (kThreads / 16)) {
+    f32x4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = *reinterpret_cast<const f32x4*>(
+          a.base + (size_t)(t0 + min(i0 + i * (kThreads / 16), nt - 1)) * a.H + nq);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int t = i0 + i * (kThreads / 16);
+      if (t < nt) sums[t * 16 + (q0 ^ (t & 15))] = v[i];
+    }
+  }
+  const uint32_t col = min(n0 + 16 * wave + c, a.H - 1);   // B's row of the lane
+  const uint32_t mine = (uint32_t)(4 * wave + g);
+  const uint32_t part_bytes = (uint32_t)a.R * a.max_rank * 2;
+  const __amdgpu_buffer_rsrc_t vrs =
+      __builtin_amdgcn_make_buffer_rsrc(a.parts, 0, (int)(3 * part_bytes), 0x00020000);
+  // Nothing in a unit's way branches, so that the loads of later units stay in
+  // flight behind the products of earlier ones: places without a row repeat one
+  // and add behind the block, and ranks past the last are offsets out of range,
+  // which load zeros and touch no line.
+  constexpr int kBatch = 4 / KB;   // units fetched together
+  struct Data {
+    u32x4 b[KB], v[KB][3];
+    uint32_t place;
+  };
+  auto look = [&](int i, int n, u32x4& u, uint2& r) {
+    const int k = min(i, n - 1);
+    u = unit_mem[k];
+    r = reinterpret_cast<const uint2*>(unit_mem + kUnitsAtOnce + k * 8)[c];
+    r.y = (i < n ? r.y / 16 : (uint32_t)a.block * 16) ^ mine;
+  };
+  auto fetch = [&](const u32x4& u, const uint2& r, Data& d) {
+    const int r8 = __builtin_amdgcn_readfirstlane((int)u.z);
+    const uint64_t at = ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)u.y) << 32) |
+                        (uint32_t)__builtin_amdgcn_readfirstlane((int)u.x);
+    const __amdgpu_buffer_rsrc_t brs = __builtin_amdgcn_make_buffer_rsrc(
+        reinterpret_cast<void*>(at), 0, a.H * r8 * 16, 0x00020000);
+    d.place = r.y;
+#pragma unroll
+    for (int k = 0; k < KB; ++k) {
+      const int q = 4 * k + g;
+      const bool in = q < r8;
+      const uint32_t bo = in ? 16 * (col * r8 + q) : 0xFFFFFFFFu;
+      const uint32_t vo = in ? 16 * (q * a.R + r.x) : 0xFFFFFFFFu;
+      d.b[k] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(brs, bo, 0, 0));
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        d.v[k][e] = __builtin_bit_cast(
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(vrs, vo, e * part_bytes, 0));
+    }
+  };
+  auto add = [&](const Data (&d)[kBatch]) {
+    f32x4 acc[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < KB; ++k)
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) acc[i] = mfma(d[i].b[k], d[i].v[k][e], acc[i]);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) sums[d[i].place] += acc[i];
+  };
+  while (true) {
+    const int n = next.n;
+    __syncthreads();   // the last units have been read, base is in
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int p = tid + i * kThreads, u = p / 9, q = p - u * 9;
+      if (u < n) unit_mem[q == 0 ? u : kUnitsAtOnce + u * 8 + q - 1] = next.piece[i];
+    }
+    __syncthreads();
+    first += kUnitsAtOnce;
+    bool more = true;
+    if (first >= total) {
+      first = 0;
+      w0 += kLoraSegment;
+      counts = counts1;
+      more = w0 < a.win;
+      if (w0 + kLoraSegment < a.win) counts1 = load_counts(w0 + kLoraSegment);
+    }
+    if (more) total = load_chunk(w0, counts, first, next);
+    if (n > 0) {
+      u32x4 u[kBatch];
+      uint2 r[kBatch];
+      Data cur[kBatch], nxt[kBatch];
+      auto look_all = [&](int i0) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) look(i0 + i, n, u[i], r[i]);
+      };
+      auto fetch_all = [&](Data (&d)[kBatch]) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) fetch(u[i], r[i], d[i]);
+      };
+      look_all(0);
+      fetch_all(cur);
+      look_all(kBatch);
+      for (int i = 0; i < n; i += 2 * kBatch) {
+        fetch_all(nxt);
+        __builtin_amdgcn_sched_barrier(0);
+        look_all(i + 2 * kBatch);
+        add(cur);
+        __builtin_amdgcn_sched_barrier(0);
+        fetch_all(cur);
+        __builtin_amdgcn_sched_barrier(0);
+        look_all(i + 3 * kBatch);
+        add(nxt);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    if (!more) break;
+  }
+  __syncthreads();
+  for (int i = tid; i < nt * 16; i += kThreads) {
+    const int t = i >> 4, q = i & 15, n = n0 + 4 * q;
+    if (n >= a.H) continue;
+    const f32x4 v = sums[t * 16 + (q ^ (t & 15))];
+    const size_t o = (size_t)(t0 + t) * a.H + n;
+    if (a.out_f32) {
+      *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + o) = v;
+    } else {
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + o) =
+          make_uint2(mx_bf16(v[0]) | (mx_bf16(v[1]) << 16), mx_bf16(v[2]) | (mx_bf16(v[3]) << 16));
+    }
+  }
+}
+
 template <int CT>
 hipError_t launch_shrink(const LoraArgs& a, hipStream_t st) {
   const int tiles = (a.halves * a.max_rank + 15) / 16;
   const int rows = a.large ? kLoraLargeRows : kLoraSmallRows, slots = a.large ? 1 : kLoraSmallRows;
-  const dim3 grid((a.R + rows - 1) / rows * slots, (tiles + CT - 1) / CT, a.splits);
-  if (a.large) {
-    if (a.in_f32) lora_shrink_kernel<kLoraLargeRows, CT, true><<<grid, kThreads, 0, st>>>(a, slots);
-    else lora_shrink_kernel<kLoraLargeRows, CT, false><<<grid, kThreads, 0, st>>>(a, slots);
+  const int n_win = (a.R + rows - 1) / rows;
+  dim3 grid(n_win * slots, (tiles + CT - 1) / CT, a.splits);
+  if (a.block) grid.x += a.n_blocks * ((a.win + kPlanWindows - 1) / kPlanWindows);
+#define LORA_GO(NW, F32, PARTS) \
+  lora_shrink_kernel<NW, CT, F32, PARTS><<<grid, kThreads, 0, st>>>(a, slots, n_win)
+  if (a.block) {
+    if (a.in_f32) LORA_GO(kLoraLargeRows, true, true);
+    else LORA_GO(kLoraLargeRows, false, true);
+  } else if (a.large) {
+    if (a.in_f32) LORA_GO(kLoraLargeRows, true, false);
+    else LORA_GO(kLoraLargeRows, false, false);
   } else {
-    if (a.in_f32) lora_shrink_kernel<kLoraSmallRows, CT, true><<<grid, kThreads, 0, st>>>(a, slots);
-    else lora_shrink_kernel<kLoraSmallRows, CT, false><<<grid, kThreads, 0, st>>>(a, slots);
+    if (a.in_f32) LORA_GO(kLoraSmallRows, true, false);
+    else LORA_GO(kLoraSmallRows, false, false);
   }
+#undef LORA_GO
   return hipGetLastError();
 }
 
@@ -555,13 +934,54 @@ hipError_t shrink(const LoraArgs& a, hipStream_t st) {
   return launch_shrink<2>(a, st);
 }
 
+template <int KB>
+hipError_t launch_accumulate(const LoraArgs& a, hipStream_t st) {
+  const size_t lds = (size_t)(a.block + 1) * kLoraSlab * 4;
+  const int n_slabs = (a.H + kLoraSlab - 1) / kLoraSlab;
+  const int grid = 8 * ((n_slabs + 7) / 8) * a.n_blocks;
+  lora_accumulate_kernel<KB><<<grid, kThreads, lds, st>>>(a, n_slabs);
+  return hipGetLastError();
+}
+
 }  // namespace
 
-void lora_plan(int R, int halves, int max_rank, int& splits, bool& large) {
-  large = R > 2048;
-  splits = 1;
-  const int tiles = (halves * max_rank + 15) / 16;
-  while (!large && splits < kLoraMaxSplits && (long long)R * tiles * splits * 2 <= 512) splits *= 2;
+void lora_choose(LoraArgs& a) {
+  a.large = a.R > 2048;
+  a.splits = 1;
+  const int tiles = (a.halves * a.max_rank + 15) / 16;
+  while (!a.large && a.splits < kLoraMaxSplits && (long long)a.R * tiles * a.splits * 2 <= 512)
+    a.splits *= 2;
+  a.block = a.n_blocks = a.win = 0;
+  if (a.halves == 1 && a.large && a.E + a.n_shared <= kLoraPlanMaxE &&
+      (long long)a.R * a.max_rank * 6 < (1LL << 32)) {   // 32-bit offsets into parts
+    const int n_slabs = (a.H + kLoraSlab - 1) / kLoraSlab;
+    a.block = kLoraMaxBlock;
+    while (a.block > 64 && (long long)((a.T + a.block - 1) / a.block) * n_slabs < 256) a.block /= 2;
+    a.n_blocks = (a.T + a.block - 1) / a.block;
+    // whole segments
+    const long long windows = ((long long)a.block * (a.k + a.n_shared) + 63) / 64;
+    a.win = (int)((windows + kLoraSegment - 1) / kLoraSegment) * kLoraSegment;
+  }
+}
+
+size_t lora_carve(LoraArgs& a, char* ws) {
+  const auto up256 = [](size_t x) { return (x + 255) & ~size_t(255); };
+  size_t off = 0;
+  const auto take = [&](size_t bytes) {
+    char* p = ws ? ws + off : nullptr;
+    off += up256(bytes);
+    return p;
+  };
+  if (a.block) {
+    const size_t win = (size_t)a.n_blocks * a.win;
+    a.parts = reinterpret_cast<uint16_t*>(take((size_t)a.R * a.max_rank * 6));
+    a.plan_count = reinterpret_cast<int*>(take(win * 4));
+    a.plan = reinterpret_cast<LoraUnit*>(take(win * 64 * sizeof(LoraUnit)));
+    a.plan_rows = reinterpret_cast<LoraUnitRow*>(take(win * 64 * 16 * sizeof(LoraUnitRow)));
+  } else {
+    a.v = reinterpret_cast<float*>(take((size_t)a.splits * a.R * a.halves * a.max_rank * 4));
+  }
+  return off;
 }
 
 hipError_t launch_lora_gateup(const LoraArgs& a, hipStream_t st) {
@@ -577,6 +997,11 @@ hipError_t launch_lora_gateup(const LoraArgs& a, hipStream_t st) {
 hipError_t launch_lora_down(const LoraArgs& a, hipStream_t st) {
   hipError_t e = shrink(a, st);
   if (e != hipSuccess) return e;
+  if (a.block) {
+    if (a.max_rank <= 32) return launch_accumulate<1>(a, st);
+    if (a.max_rank <= 64) return launch_accumulate<2>(a, st);
+    return launch_accumulate<4>(a, st);
+  }
   const dim3 grid(a.T, (a.H + 16 * kWaves - 1) / (16 * kWaves));
   lora_expand_down_kernel<<<grid, kThreads, 0, st>>>(a);
   return hipGetLastError();

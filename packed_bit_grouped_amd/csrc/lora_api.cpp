@@ -19,40 +19,18 @@ int ld_h_of(int I, int n_shared, int I_shared) {
   return n_shared > 0 && I_shared > I ? I_shared : I;
 }
 
-size_t v_bytes(int R, int halves, int max_rank) {
-  int splits;
-  bool large;
-  lora_plan(R, halves, max_rank, splits, large);
-  return (size_t)splits * R * halves * max_rank * 4;
-}
-
-size_t workspace_bytes(int R, int max_rank) {
-  const size_t up = v_bytes(R, 2, max_rank), down = v_bytes(R, 1, max_rank);
-  return 256 + (up > down ? up : down);
-}
-
-moe_status check_rows(int T, int k, int n_shared, int max_rank) {
-  if (T < 0 || k <= 0 || n_shared < 0 || max_rank <= 0) return MOE_E_INVAL;
-  if (max_rank % 8) return MOE_E_INVAL;
-  if (max_rank > kLoraMaxRank || n_shared > 65535) return MOE_E_UNSUPPORTED;
-  if ((long long)T * k >= (1LL << 24)) return MOE_E_UNSUPPORTED;
-  if ((long long)T * ((long long)k + n_shared) >= (1LL << 26)) return MOE_E_UNSUPPORTED;
-  return MOE_OK;
-}
-
 moe_status check_shape(int T, int H, int I, int E, int k, int n_shared, int I_shared,
                        int n_adapters, int max_rank) {
-  const moe_status st = check_rows(T, k, n_shared, max_rank);
-  if (st != MOE_OK && st != MOE_E_UNSUPPORTED) return st;
-  if (H <= 0 || I <= 0 || E <= 0 || k > E || n_adapters < 0) return MOE_E_INVAL;
+  if (T < 0 || H <= 0 || I <= 0 || E <= 0 || k <= 0 || n_shared < 0) return MOE_E_INVAL;
+  if (k > E || n_adapters < 0 || max_rank <= 0 || max_rank % 8) return MOE_E_INVAL;
   if (n_shared > 0 && I_shared <= 0) return MOE_E_INVAL;
-  if (st != MOE_OK) return st;
   if (H % 32 || I % 32 || (n_shared > 0 && I_shared % 32)) return MOE_E_UNSUPPORTED;
   if (H > kLoraMaxLen || I > kLoraMaxLen || (n_shared > 0 && I_shared > kLoraMaxLen))
     return MOE_E_UNSUPPORTED;
-  if (E > kRouteMaxE) return MOE_E_UNSUPPORTED;
+  if (max_rank > kLoraMaxRank || E > kRouteMaxE || n_shared > 65535) return MOE_E_UNSUPPORTED;
   if ((long long)n_adapters * ((long long)E + n_shared) >= (1LL << 31)) return MOE_E_UNSUPPORTED;
   const long long rows = (long long)T * ((long long)k + n_shared);
+  if ((long long)T * k >= (1LL << 24) || rows >= (1LL << 26)) return MOE_E_UNSUPPORTED;
   if (rows * H >= (1LL << 31) || rows * ld_h_of(I, n_shared, I_shared) >= (1LL << 31))
     return MOE_E_UNSUPPORTED;
   return MOE_OK;
@@ -81,18 +59,32 @@ LoraArgs args_of(int T, int H, int I, int E, int k, int n_shared, int I_shared,
   a.I_sh = n_shared > 0 ? I_shared : I;
   a.ld_h = ld_h_of(I, n_shared, I_shared);
   a.err = reinterpret_cast<int32_t*>(ws);
-  a.v = reinterpret_cast<float*>(ws + 256);
-  lora_plan(a.R, halves, max_rank, a.splits, a.large);
+  lora_choose(a);
+  lora_carve(a, ws ? ws + 256 : nullptr);
   return a;
+}
+
+// The larger of the two calls' needs (neither depends on the table).
+size_t workspace_bytes(int T, int H, int I, int E, int k, int n_shared, int I_shared,
+                       int max_rank) {
+  size_t most = 0;
+  for (int halves = 1; halves <= 2; ++halves) {
+    LoraArgs a = args_of(T, H, I, E, k, n_shared, I_shared, nullptr, 0, max_rank, nullptr, nullptr,
+                         nullptr, nullptr, halves);
+    const size_t n = lora_carve(a, nullptr);
+    most = n > most ? n : most;
+  }
+  return 256 + most;
 }
 
 }  // namespace
 
 extern "C" {
 
-size_t moe_lora_workspace_bytes(int T, int k, int n_shared, int max_rank) {
-  if (check_rows(T, k, n_shared, max_rank) != MOE_OK) return 0;
-  return workspace_bytes(T * (k + n_shared), max_rank);
+size_t moe_lora_workspace_bytes(int T, int H, int I, int E, int k, int n_shared, int I_shared,
+                                int max_rank) {
+  if (check_shape(T, H, I, E, k, n_shared, I_shared, 0, max_rank) != MOE_OK) return 0;
+  return workspace_bytes(T, H, I, E, k, n_shared, I_shared, max_rank);
 }
 
 moe_status moe_lora_gateup_silu(const uint16_t* x, int T, int H, int I, int E, int k,
@@ -109,7 +101,7 @@ moe_status moe_lora_gateup_silu(const uint16_t* x, int T, int H, int I, int E, i
   if (n_adapters > 0 && (!table || !aligned(table, 8))) return MOE_E_INVAL;
   if (!aligned(x, 16) || !aligned(gu, 16) || !aligned(h, 16)) return MOE_E_INVAL;
   if (!workspace || !aligned(workspace, 256) ||
-      ws_bytes < workspace_bytes(T * (k + n_shared), max_rank))
+      ws_bytes < workspace_bytes(T, H, I, E, k, n_shared, I_shared, max_rank))
     return MOE_E_WORKSPACE;
   st = device_usable();
   if (st != MOE_OK) return st;
@@ -142,7 +134,7 @@ moe_status moe_lora_down_combine(const void* h, int T, int H, int I, int E, int 
   if (!aligned(h, 16) || !aligned(base, 16) || !aligned(out, (flags & MOE_OUT_F32) ? 16 : 8))
     return MOE_E_INVAL;
   if (!workspace || !aligned(workspace, 256) ||
-      ws_bytes < workspace_bytes(T * (k + n_shared), max_rank))
+      ws_bytes < workspace_bytes(T, H, I, E, k, n_shared, I_shared, max_rank))
     return MOE_E_WORKSPACE;
   st = device_usable();
   if (st != MOE_OK) return st;

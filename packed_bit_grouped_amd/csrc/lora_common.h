@@ -10,6 +10,21 @@ constexpr int kLoraMaxRank = 128;
 constexpr int kLoraSmallRows = 16;    // rows of a window, small calls
 constexpr int kLoraLargeRows = 64;    // and large ones
 constexpr int kLoraMaxSplits = 4;
+constexpr int kLoraPlanMaxE = 1088;   // routed and shared experts of a plan
+constexpr int kLoraSlab = 64;         // columns of a workgroup of the accumulating kernel
+constexpr int kLoraMaxBlock = 512;    // and tokens
+constexpr int kLoraSegment = 8;       // windows of 64 rows that it takes at a time
+
+// A unit: up to 16 rows of one (adapter, expert) with tokens of one block, and
+// its rows: the row of v, and the byte of LDS where chunk 0 of the token's sums
+// lies (behind the block's where there is no row).
+struct alignas(16) LoraUnit {
+  const uint16_t* b;
+  int rank8, unused;
+};
+struct alignas(8) LoraUnitRow {
+  uint32_t row, place;
+};
 
 // Rows of a layer (sorted pairs, then the shared experts' tokens) with their
 // tokens' adapters.
@@ -25,6 +40,15 @@ struct LoraArgs {
   const void* in;               // gate/up: x bf16 [T][H]; down: h [R][ld_h]
   int in_f32;
   float* v;                     // [splits][R][halves * max_rank]
+  // down, large calls: v times the gate weight as three bf16 parts that sum to
+  // it, zeros behind an entry's own rank; and the plan of the accumulating
+  // kernel, per block of `block` tokens: its rows in win windows of 64, each with
+  // its units
+  uint16_t* parts;              // [3][max_rank / 8][R][8]
+  int block, n_blocks, win;
+  int* plan_count;              // [n_blocks][win] units of a window
+  LoraUnit* plan;               // [n_blocks][win][64]
+  LoraUnitRow* plan_rows;       // [n_blocks][win][64][16]
   int splits;                   // parts of K
   bool large;                   // windows of 64 rows, one workgroup each
   const float* gu;              // gate/up: [R][2 ld_h]
@@ -37,8 +61,11 @@ struct LoraArgs {
   int32_t* err;
 };
 
-// Splits of K and the window size for R rows (the workspace is sized by it).
-void lora_plan(int R, int halves, int max_rank, int& splits, bool& large);
+// How a call of these sizes runs: fills splits, large and, for down, the
+// accumulating kernel's block (0: not taken), n_blocks and win.  Host only.
+void lora_choose(LoraArgs& a);
+// The workspace behind the error word, in bytes; with ws, sets the pointers.
+size_t lora_carve(LoraArgs& a, char* ws);
 
 hipError_t launch_lora_gateup(const LoraArgs& a, hipStream_t st);
 hipError_t launch_lora_down(const LoraArgs& a, hipStream_t st);

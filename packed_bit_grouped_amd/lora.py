@@ -124,10 +124,10 @@ class LoraBuffers:
         self.P = T * k
         self.R = self.P + n_shared * T
         self.ld_h = max(I, I_shared if n_shared else 0)
-        self.ws_bytes = L.moe_lora_workspace_bytes(T, k, n_shared, max_rank)
+        self.ws_bytes = L.moe_lora_workspace_bytes(T, H, I, E, k, n_shared, I_shared, max_rank)
         if self.ws_bytes == 0:
-            raise ValueError(f"unsupported sizes: T={T} k={k} n_shared={n_shared} "
-                             f"max_rank={max_rank}")
+            raise ValueError(f"unsupported sizes: T={T} H={H} I={I} E={E} k={k} n_shared={n_shared} "
+                             f"I_shared={I_shared} max_rank={max_rank}")
         dev = torch.device(device)
         if dev.type == "cuda" and dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())

@@ -506,3 +506,21 @@ def test_layer_in_a_graph(lora):
         torch.cuda.synchronize()
         got = d["B"].out.clone()
         assert torch.equal(got, go())
+
+
+@pytest.mark.parametrize("T", [6, 700, 2100])
+def test_a_token_that_lists_an_expert_twice(lora, T):
+    """Both of its rows count, alone and between others of their expert."""
+    d = make(lora, T, 64, 32, 4, 3, 0, 0, 2, (8, 16), out_f32=True, runs=True, none=0.0, seed=12)
+    rng = np.random.default_rng(12)
+    ids = d["ids"].copy()
+    ids[::2, 1] = ids[::2, 0]
+    ids[1::6, 2] = ids[1::6, 1] = ids[1::6, 0]
+    flat = ids.ravel()
+    order = np.argsort(flat, kind="stable").astype(np.int32)
+    d["ids"], d["sp"], d["pos"] = ids, order, np.argsort(order).astype(np.int32)
+    d["off"] = np.concatenate([[0], np.cumsum(np.bincount(flat, minlength=4))]).astype(np.int32)
+    d["rows"] = O.rows_of(d["sp"], ids, T, 3, 4, 0)
+    d["t"] = [dev(d[x]) for x in ("ids", "off", "sp", "pos")]
+    check_gateup(d, run_gateup(lora, d))
+    check_down(d, run_down(lora, d))

@@ -104,7 +104,7 @@ def test_invalid_arguments(call, more):
 def test_unsupported_sizes_and_workspace(call):
     for kw in UNSUPPORTED:
         assert call(**kw) == L.MOE_E_UNSUPPORTED, kw
-    need = L.moe_lora_workspace_bytes(4, 2, 0, 16)
+    need = L.moe_lora_workspace_bytes(4, 64, 32, 8, 2, 0, 0, 16)
     assert need >= 256 + 4 * 2 * 32 * 4
     assert call(ws_bytes=need - 1) == L.MOE_E_WORKSPACE
     assert call(workspace=None) == L.MOE_E_WORKSPACE
@@ -120,12 +120,10 @@ def test_down_in_place_is_for_fp32():
 
 
 def test_workspace_sizes():
-    assert L.moe_lora_workspace_bytes(4, 2, 0, 12) == 0
-    assert L.moe_lora_workspace_bytes(4, 2, 0, 136) == 0
-    assert L.moe_lora_workspace_bytes(-1, 2, 0, 16) == 0
-    assert L.moe_lora_workspace_bytes(4, 0, 0, 16) == 0
-    for T, k, s, r in ((1, 1, 0, 8), (64, 8, 1, 16), (4096, 8, 1, 16), (65535, 8, 0, 128)):
-        assert L.moe_lora_workspace_bytes(T, k, s, r) >= 256 + T * (k + s) * 2 * r * 4
+    size = lambda T, k, s, r: L.moe_lora_workspace_bytes(T, 64, 32, 64, k, s, 32, r)
+    assert size(4, 2, 0, 12) == size(4, 2, 0, 136) == size(-1, 2, 0, 16) == size(4, 0, 0, 16) == 0
+    for T, k, s, r in ((0, 1, 0, 8), (1, 1, 0, 8), (64, 8, 1, 16), (4096, 8, 1, 16), (65535, 8, 0, 128)):
+        assert size(T, k, s, r) >= 256 + T * (k + s) * 2 * r * 4
 
 
 def test_shared_sums_flag_belongs_to_gateup_alone():
