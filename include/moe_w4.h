@@ -768,12 +768,25 @@ moe_status moe_mx4_layer(int act, const float* logits, const uint16_t* x, int T,
  * MOE_OUT_F32 -> base, moe_lora_down_combine -> out.
  * ===================================================================== */
 
+/* moe_lora_tile -- n matrices [rows][cols] of plain bf16 rows to the layout that
+ * the calls below read, once per adapter, in pieces of 8 values along a row:
+ *   A (is_b = 0, rows % 8 == 0, cols % 32 == 0): tiles of 16 rows, one after the
+ *     other; in a tile, for every 32 columns, the pieces [4][16].  A last tile of
+ *     8 rows keeps its size; what lies behind its rows is neither written nor read
+ *   B (is_b = 1, rows % 32 == 0, cols % 8 == 0): tiles of 32 rows, one after the
+ *     other; in a tile the pieces [cols / 8][32]
+ * dst: n matrices of rows rounded up to whole tiles.  src, dst 16-byte aligned,
+ * no overlap.  Limits: those, rows *
+ * cols < 2^31, n * rows * cols < 2^34 (else MOE_E_UNSUPPORTED). */
+moe_status moe_lora_tile(const uint16_t* src, int n, int rows, int cols, int is_b, uint16_t* dst,
+                         void* stream);
+
 /* An adapter's matrices for one projection of one expert; tables of these live
  * in DEVICE memory, as [n_adapters][E + n_shared] (shared experts behind the
- * routed ones).
- *   gate/up: a bf16 [2*rank][K] (the gate's rows, then up's), K = H;
- *            b bf16 [N][rank], N = 2I (gate rows, then up rows)
- *   down:    a bf16 [rank][K], K = I;  b bf16 [N][rank], N = H
+ * routed ones).  a, b: as moe_lora_tile wrote them from
+ *   gate/up: A bf16 [2*rank][K] (the gate's rows, then up's), K = H;
+ *            B bf16 [N][rank], N = 2I (gate rows, then up rows)
+ *   down:    A bf16 [rank][K], K = I;  B bf16 [N][rank], N = H
  * (I_shared for shared experts.)  rank: a multiple of 8, 0 where the adapter
  * leaves the expert alone; ranks may differ from entry to entry.  a, b 16-byte
  * aligned.  An entry that the calls cannot use (other N or K, rank above
@@ -815,8 +828,8 @@ size_t moe_lora_workspace_bytes(int T, int H, int I, int E, int k, int n_shared,
  * MOE_H_F32, in down's A) may come out as NaN.
  * Limits: H, I, I_shared multiples of 32 and at most 2^20, E <= 1024, n_shared
  * <= 65535, n_adapters * (E + n_shared) < 2^31, max_rank a multiple of 8 up to
- * 128, T*k < 2^24, T*(k + n_shared) < 2^26 and times H or max(I, I_shared) <
- * 2^31; else MOE_E_UNSUPPORTED.  x, gu, h 16-byte aligned.  T = 0 launches nothing.
+ * 128, T <= 2^22, T*k < 2^24, T*(k + n_shared) < 2^26 and times H or
+ * max(I, I_shared) < 2^31; else MOE_E_UNSUPPORTED.  x, gu, h 16-byte aligned.  T = 0 launches nothing.
  * ------------------------------------------------------------------- */
 #define MOE_H_F32 512        /* moe_lora_* calls: h is fp32 (A8 layers) */
 moe_status moe_lora_gateup_silu(const uint16_t* x, int T, int H, int I, int E, int k,

@@ -129,6 +129,7 @@ _SIGS = {
                               c_void_p]),
     "moe_route_scored": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_int, c_int,
                                  c_int, c_int, c_float, c_void_p, c_void_p, c_void_p]),
+    "moe_lora_tile": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_void_p]),
     "moe_lora_workspace_bytes": (c_size_t, [c_int] * 8),
     "moe_lora_gateup_silu": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
                                      c_void_p, c_int, c_int, c_void_p, c_void_p, c_void_p,
@@ -459,6 +460,11 @@ def moe_mx4_layer(act, logits, x, T, H, I, E, k, renormalize, w13, w2, w13_share
                  _ptr(shared_gate), _ptr(topk_ids), _ptr(topk_w), _ptr(counts), _ptr(offsets),
                  _ptr(sorted_pair), _ptr(pair_pos), _ptr(h), _ptr(out), _ptr(workspace),
                  ws_bytes, flags, _stream(stream), check=check)
+
+
+def moe_lora_tile(src, n, rows, cols, is_b, dst, stream=None, check=True):
+    return _call("moe_lora_tile", _ptr(src), n, rows, cols, is_b, _ptr(dst), _stream(stream),
+                 check=check)
 
 
 def moe_lora_workspace_bytes(T, H, I, E, k, n_shared=0, I_shared=0, max_rank=16) -> int:

@@ -18,11 +18,15 @@
 // sorted pair -> token -> table entry -> matrix, a decode batch by reading each
 // (adapter, expert)'s matrices once, a prefill chunk by g, u and h.
 //
+// A and B are tiled (moe_lora_tile): a fragment's 64 loads of 16 bytes are
+// neighbours, a kilobyte together.  From plain rows every lane's load is a cache
+// access of its own: one token's A of 131 KB took 4.5 us in one compute unit.
+//
 // Windows.  A workgroup looks at a window of 16 or 64 neighbouring rows and
 // splits it into groups of rows of one (adapter, expert); each group runs as
 // fragments of 16 rows against that pair's matrices.  Sorted rows of a prompt
 // that share an expert are neighbours, so a window holds few groups; a decode
-// batch has up to one per row, and there a workgroup takes one group.
+// batch has up to one per row, and there a workgroup takes one group, from K to h.
 #include <type_traits>
 
 #include "lora_common.h"
@@ -78,14 +82,14 @@ struct Row {
   float weight;
 };
 template <bool WEIGHT>
-__device__ __forceinline__ Row window_row(const LoraArgs& a, int r, bool in) {
+__device__ __forceinline__ Row window_row(const LoraArgs& a, int r, int p, const int* topk_ids,
+                                          const int* adapter) {
   Row w = {0, kNoRow, 1.0f};
-  if (!in || r >= a.R) return w;
+  if (r >= a.R) return w;
   int e;
   if (r < a.P) {
-    const int p = a.sorted_pair[r];
     if ((unsigned)p >= (unsigned)a.P) return w;
-    e = a.topk_ids[p];
+    e = topk_ids[p];
     if ((unsigned)e >= (unsigned)a.E) return w;
     w.token = p / a.k;
     if (WEIGHT) w.weight = a.topk_w[p];
@@ -96,11 +100,22 @@ __device__ __forceinline__ Row window_row(const LoraArgs& a, int r, bool in) {
     if (WEIGHT && a.shared_gate)
       w.weight = shared_gate_weight(a.shared_gate[(size_t)w.token * a.n_shared + s]);
   }
-  const int d = a.adapter[w.token];
+  const int d = adapter[w.token];
   w.key = (unsigned)d < (unsigned)a.n ? d * (a.E + a.n_shared) + e
           : e < a.E                   ? kBaseRouted
                                       : kBaseShared;
   return w;
+}
+
+template <bool WEIGHT>
+__device__ __forceinline__ Row window_row(const LoraArgs& a, int r) {
+  return window_row<WEIGHT>(a, r, r < a.P ? a.sorted_pair[r] : 0, a.topk_ids, a.adapter);
+}
+
+// Columns of h of a key's rows.
+__device__ __forceinline__ int width_of(const LoraArgs& a, int key) {
+  const bool shared = key >= 0 ? key % (a.E + a.n_shared) >= a.E : key == kBaseShared;
+  return shared ? a.I_sh : a.I;
 }
 
 // The pair of matrices of a table entry; rank 0 where there is none.
@@ -131,23 +146,16 @@ __device__ __forceinline__ Pair pair_of(const LoraArgs& a, int key, int N, int K
   return p;
 }
 
-// The window's groups in turn, the same in every wave: the rows (bits) and key
-// of one; `slot` of `slots` workgroups takes every slots-th.
+// The window's groups in turn, the same in every wave: the rows (bits) and key of one.
 struct Groups {
   uint64_t todo;
-  int ord;
-  __device__ __forceinline__ void init(int key, int from) {
-    todo = __ballot(key >= from);
-    ord = 0;
-  }
-  __device__ __forceinline__ bool next(int key, int slot, int slots, uint64_t& rows, int& k) {
-    while (todo) {
-      k = __builtin_amdgcn_readlane(key, __builtin_ctzll(todo));
-      rows = __ballot(key == k);
-      todo &= ~rows;
-      if (ord++ % slots == slot) return true;
-    }
-    return false;
+  __device__ __forceinline__ void init(int key, int from) { todo = __ballot(key >= from); }
+  __device__ __forceinline__ bool next(int key, uint64_t& rows, int& k) {
+    if (!todo) return false;
+    k = __builtin_amdgcn_readlane(key, __builtin_ctzll(todo));
+    rows = __ballot(key == k);
+    todo &= ~rows;
+    return true;
   }
 };
 
@@ -163,57 +171,51 @@ __device__ __forceinline__ int list_rows(uint64_t rows, int* list) {
 // ---------------------------------------------------------------------
 // shrink: v[row][j] = scale sum_K A[j][K] in[row][K]
 //
-// The workgroup's waves (and, for few rows, `splits` workgroups) share K; a
-// wave's fragments go from memory to registers, 16 bytes per lane, since every
-// byte of A and of the rows is read by one wave only.
-//
-// PARTS: v goes out times the row's weight, as three bf16 parts (the accumulating
-// kernel's operand: it would else be split once per slab of columns).
-template <int NF, int CT, bool F32, bool PARTS>
-__device__ __forceinline__ void shrink_group(const LoraArgs& a, const Pair& p, int K, int C, int ct0,
-                                             int split, const void* const (&rows)[NF],
-                                             const int (&row)[NF], const float (&weight)[NF], int n,
-                                             float* red) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = lane & 15, g = lane >> 4;
-  const int steps = K >> 5, workers = kWaves * a.splits, me = split * kWaves + wave;
-  const int per = (steps + workers - 1) / workers;
+// The workgroup's waves share K; a wave's fragments go from memory to registers,
+// 16 bytes per lane, since every byte of A and of the rows is read by one wave only.
+template <int WORKERS, bool F32, int NF, int CT>
+__device__ __forceinline__ void shrink_part(const Pair& p, int K, int C, int ct0, int me,
+                                            const void* const (&rows)[NF], f32x4 (&acc)[NF][CT]) {
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  const int steps = K >> 5, per = (steps + WORKERS - 1) / WORKERS;
   const int s0 = min(me * per, steps), s1 = min(s0 + per, steps);
+  // tiles and steps are the same for all lanes, a lane's place in a step for all steps
   const uint16_t* pa[CT];
+  uint32_t mine[CT];
 #pragma unroll
-  for (int j = 0; j < CT; ++j)   // columns past the last are computed and dropped
-    pa[j] = p.a + (size_t)min(16 * (ct0 + j) + c, C - 1) * K + 8 * g;
-  f32x4 acc[NF][CT];
+  for (int j = 0; j < CT; ++j) {   // rows past the last are computed and dropped
+    const int t = min(ct0 + j, (C - 1) / 16), h = min(C - 16 * t, 16);
+    pa[j] = p.a + (size_t)16 * t * K + (size_t)s0 * 512;
+    mine[j] = 8 * (g * 16 + min(c, h - 1));
+  }
 #pragma unroll
   for (int f = 0; f < NF; ++f)
 #pragma unroll
     for (int j = 0; j < CT; ++j) acc[f][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  constexpr int U = F32 ? 2 : 4;
   int s = s0;
-  auto step = [&](int n_st) {
+  auto step = [&](auto n_steps) {   // their loads are in flight together
+    constexpr int U = decltype(n_steps)::value;
     u32x4 wa[U][CT], wx[U][NF][F32 ? 2 : 1];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      if (i >= n_st) break;
 #pragma unroll
       for (int j = 0; j < CT; ++j)
-        wa[i][j] = *reinterpret_cast<const u32x4*>(pa[j] + (size_t)(s + i) * 32);
+        wa[i][j] = *reinterpret_cast<const u32x4*>(pa[j] + i * 512 + mine[j]);
 #pragma unroll
       for (int f = 0; f < NF; ++f) {
         if constexpr (F32) {
           const u32x4* q = reinterpret_cast<const u32x4*>(static_cast<const float*>(rows[f]) +
-                                                          (size_t)(s + i) * 32 + 8 * g);
+                                                          (size_t)s * 32 + i * 32 + 8 * g);
           wx[i][f][0] = q[0];
           wx[i][f][1] = q[1];
         } else {
           wx[i][f][0] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(rows[f]) +
-                                                        (size_t)(s + i) * 32 + 8 * g);
+                                                        (size_t)s * 32 + i * 32 + 8 * g);
         }
       }
     }
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      if (i >= n_st) break;
+    for (int i = 0; i < U; ++i)
 #pragma unroll
       for (int f = 0; f < NF; ++f) {
         if constexpr (F32) {
@@ -231,11 +233,27 @@ __device__ __forceinline__ void shrink_group(const LoraArgs& a, const Pair& p, i
           for (int j = 0; j < CT; ++j) acc[f][j] = mfma(wa[i][j], wx[i][f][0], acc[f][j]);
         }
       }
-    }
+    s += U;
+#pragma unroll
+    for (int j = 0; j < CT; ++j) pa[j] += U * 512;
   };
-  for (; s + U <= s1; s += U) step(U);
-  for (; s < s1; ++s) step(1);
+  constexpr int U = F32 ? (NF * CT == 1 ? 4 : 2) : NF * CT == 1 ? 16 : NF * CT == 2 ? 8 : 4;
+  while (s + U <= s1) step(std::integral_constant<int, U>{});
+  if constexpr (U > 4)
+    while (s + 4 <= s1) step(std::integral_constant<int, 4>{});
+  while (s < s1) step(std::integral_constant<int, 1>{});
+}
 
+// PARTS: v goes out times the row's weight, as three bf16 parts (the accumulating
+// kernel's operand: it would else be split once per slab of columns).
+template <int NF, int CT, bool F32, bool PARTS>
+__device__ __forceinline__ void shrink_group(const LoraArgs& a, const Pair& p, int K, int C, int ct0,
+                                             const void* const (&rows)[NF], const int (&row)[NF],
+                                             const float (&weight)[NF], int n, float* red) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = lane & 15, g = lane >> 4;
+  f32x4 acc[NF][CT];
+  shrink_part<kWaves, F32>(p, K, C, ct0, wave, rows, acc);
   // the waves' parts meet: wave w adds those of tiles w, w + 4, ...
   __syncthreads();   // the last group's parts have been read
 #pragma unroll
@@ -245,7 +263,7 @@ __device__ __forceinline__ void shrink_group(const LoraArgs& a, const Pair& p, i
       *reinterpret_cast<f32x4*>(red + ((wave * NF * CT + f * CT + j) * 64 + lane) * 4) = acc[f][j];
   __syncthreads();
   const int VL = a.halves * a.max_rank;
-  float* v = a.v + (size_t)split * a.R * VL;
+  float* v = a.v;
 #pragma unroll
   for (int f = 0; f < NF; ++f)
 #pragma unroll
@@ -410,9 +428,9 @@ __device__ void make_plan(const LoraArgs& a, int b, int part, PlanLds& L) {
   }
 }
 
-template <int NW, int CT, bool F32, bool PARTS>
-__global__ __launch_bounds__(kThreads) void lora_shrink_kernel(LoraArgs a, int slots, int n_win) {
-  constexpr int NFM = NW / 16;
+template <int CT, bool F32, bool PARTS>
+__global__ __launch_bounds__(kThreads) void lora_shrink_kernel(LoraArgs a, int n_win) {
+  constexpr int NW = kLoraLargeRows, NFM = NW / 16;
   __shared__ int list[kWaves][64];
   union Lds {
     float red[kWaves * NFM * CT * 256];
@@ -421,8 +439,7 @@ __global__ __launch_bounds__(kThreads) void lora_shrink_kernel(LoraArgs a, int s
   __shared__ __align__(16) typename std::conditional<PARTS, Lds, float[kWaves * NFM * CT * 256]>::type lds;
   float* red = reinterpret_cast<float*>(&lds);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15;
-  const int win = blockIdx.x / slots, slot = blockIdx.x - win * slots;
-  const int ct0 = blockIdx.y * CT, split = blockIdx.z;
+  const int win = blockIdx.x, ct0 = blockIdx.y * CT;
   if constexpr (PARTS) {
     if (win >= n_win) {
       const int per = (a.win + kPlanWindows - 1) / kPlanWindows, q = win - n_win;
@@ -431,14 +448,13 @@ __global__ __launch_bounds__(kThreads) void lora_shrink_kernel(LoraArgs a, int s
     }
   }
   const int r0 = win * NW;
-  const Row w = window_row<PARTS>(a, r0 + lane, lane < NW);
+  const Row w = window_row<PARTS>(a, r0 + lane);
   Groups gr;
   gr.init(w.key, 0);
   uint64_t rows;
   int key;
-  while (gr.next(w.key, slot, slots, rows, key)) {
-    const int e = key % (a.E + a.n_shared);
-    const int width = e < a.E ? a.I : a.I_sh;
+  while (gr.next(w.key, rows, key)) {
+    const int width = width_of(a, key);
     const int K = a.halves == 2 ? a.H : width, N = a.halves == 2 ? 2 * width : a.H;
     const Pair p = pair_of(a, key, N, K);
     const int C = a.halves * p.rank;
@@ -460,31 +476,11 @@ __global__ __launch_bounds__(kThreads) void lora_shrink_kernel(LoraArgs a, int s
         else if (F32) src[f] = static_cast<const float*>(a.in) + (size_t)row[f] * a.ld_h;
         else src[f] = static_cast<const uint16_t*>(a.in) + (size_t)row[f] * a.ld_h;
       }
-      shrink_group<NF, CT, F32, PARTS>(a, p, K, C, ct0, split, src, row, weight, n, red);
+      shrink_group<NF, CT, F32, PARTS>(a, p, K, C, ct0, src, row, weight, n, red);
     };
-    if constexpr (NFM == 1) {
-      run(std::integral_constant<int, 1>{});
-    } else {
-      if (n <= 16) run(std::integral_constant<int, 1>{});
-      else if (n <= 32) run(std::integral_constant<int, 2>{});
-      else run(std::integral_constant<int, 4>{});
-    }
-  }
-}
-
-// The row's v from j on, 8 values: the parts of K added in order.
-__device__ __forceinline__ void load_v(const LoraArgs& a, size_t row, int j, float (&f)[8]) {
-  const int VL = a.halves * a.max_rank;
-  f32x4 lo = {0.0f, 0.0f, 0.0f, 0.0f}, hi = lo;
-  for (int s = 0; s < a.splits; ++s) {
-    const f32x4* q = reinterpret_cast<const f32x4*>(a.v + ((size_t)s * a.R + row) * VL + j);
-    lo += q[0];
-    hi += q[1];
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[i] = lo[i];
-    f[4 + i] = hi[i];
+    if (n <= 16) run(std::integral_constant<int, 1>{});
+    else if (n <= 32) run(std::integral_constant<int, 2>{});
+    else run(std::integral_constant<int, 4>{});
   }
 }
 
@@ -500,99 +496,120 @@ __device__ __forceinline__ float silu_mul_wide(float g, float u) {
 // expand, gate/up.  A wave owns 32 columns: two fragments of gate rows of B and
 // two of up rows, dealt so that a lane ends with 8 neighbouring columns of its
 // row: whole 16-byte loads of g and u and stores of h.
+__device__ __forceinline__ void load_gu(const LoraArgs& a, int row, int col, f32x4 (&gu)[4]) {
+  const float* q = a.gu + (size_t)row * 2 * a.ld_h + col;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)   // gate, gate, up, up
+    gu[i] = *reinterpret_cast<const f32x4*>(q + (i >> 1) * a.ld_h + 4 * (i & 1));
+}
+// Row `row` of a tiled B, ranks [j, j + 8).
+__device__ __forceinline__ size_t b_at(int row, int j, int rank) {
+  return (size_t)(row & ~31) * rank + 32 * j + 8 * (row & 31);
+}
+// B's fragments of ranks [k0, k0 + 32): the lane's row of each, zeros past the rank.
+__device__ __forceinline__ void load_b(const Pair& p, int width, int i0, int k0, u32x4 (&b)[4]) {
+  const int lane = threadIdx.x & 63, c = lane & 15, j = k0 + 8 * (lane >> 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int br = (i >> 1) * width + i0 + 8 * (c >> 2) + 4 * (i & 1) + (c & 3);
+    b[i] = u32x4{0u, 0u, 0u, 0u};
+    if (j < p.rank) b[i] = *reinterpret_cast<const u32x4*>(p.b + b_at(br, j, p.rank));
+  }
+}
+// v: 8 values each of the gate's and up's.
+__device__ __forceinline__ void expand_step(const u32x4 (&b)[4], const float (&vg)[8],
+                                            const float (&vu)[8], f32x4 (&acc)[4]) {
+  u32x4 g[3], u[3];
+  split3(vg, g);
+  split3(vu, u);
+#pragma unroll
+  for (int e = 0; e < 3; ++e) {
+    acc[0] = mfma(b[0], g[e], acc[0]);
+    acc[1] = mfma(b[1], g[e], acc[1]);
+    acc[2] = mfma(b[2], u[e], acc[2]);
+    acc[3] = mfma(b[3], u[e], acc[3]);
+  }
+}
+__device__ __forceinline__ void store_h(const LoraArgs& a, int row, int col, bool there,
+                                        const f32x4 (&gu)[4], f32x4 (&acc)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) mx_keep(acc[i]);
+  if (!there) return;
+  float gv[8], uv[8], hv[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    gv[i] = gu[i / 4][i % 4] + acc[i / 4][i % 4];
+    uv[i] = gu[2 + i / 4][i % 4] + acc[2 + i / 4][i % 4];
+  }
+  const size_t o = (size_t)row * a.ld_h + col;
+  if (a.out_f32) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) hv[i] = silu_mul_wide(gv[i], uv[i]);
+    float* h = static_cast<float*>(a.out) + o;
+    *reinterpret_cast<f32x4*>(h) = f32x4{hv[0], hv[1], hv[2], hv[3]};
+    *reinterpret_cast<f32x4*>(h + 4) = f32x4{hv[4], hv[5], hv[6], hv[7]};
+  } else {
+    mx_silu_mul(gv, uv, hv);
+    u32x4 s;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = mx_bf16(hv[2 * i]) | (mx_bf16(hv[2 * i + 1]) << 16);
+    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + o) = s;
+  }
+}
+
 template <int NF>
 __device__ __forceinline__ void expand_group(const LoraArgs& a, const Pair& p, int width, int i0,
                                              const int (&row)[NF], int n) {
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int col = i0 + 8 * g;
-  f32x4 gu[NF][4];   // gate, gate, up, up
+  f32x4 gu[NF][4], acc[NF][4];
 #pragma unroll
   for (int f = 0; f < NF; ++f) {
-    const float* q = a.gu + (size_t)row[f] * 2 * a.ld_h + col;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        gu[f][2 * h + i] = *reinterpret_cast<const f32x4*>(q + h * a.ld_h + 4 * i);
-  }
-  f32x4 acc[NF][4];
-#pragma unroll
-  for (int f = 0; f < NF; ++f)
+    load_gu(a, row[f], col, gu[f]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[f][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const u32x4 zero = {0u, 0u, 0u, 0u};
+  }
   for (int k0 = 0; k0 < p.rank; k0 += 32) {
     const int j = k0 + 8 * g;
-    const bool in = j < p.rank;
     u32x4 b[4];
+    load_b(p, width, i0, k0, b);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int br = h * width + i0 + 8 * (c >> 2) + 4 * i + (c & 3);
-        b[2 * h + i] =
-            in ? *reinterpret_cast<const u32x4*>(p.b + (size_t)br * p.rank + j) : zero;
-      }
-#pragma unroll
-    for (int f = 0; f < NF; ++f)
+    for (int f = 0; f < NF; ++f) {
+      float v[2][8];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float t[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (in) load_v(a, row[f], h * p.rank + j, t);
-        u32x4 sp[3];
-        split3(t, sp);
+        f32x4 lo = {0.0f, 0.0f, 0.0f, 0.0f}, hi = lo;
+        if (j < p.rank) {
+          const f32x4* q = reinterpret_cast<const f32x4*>(a.v + (size_t)row[f] * 2 * a.max_rank +
+                                                          h * p.rank + j);
+          lo = q[0];
+          hi = q[1];
+        }
 #pragma unroll
-        for (int e = 0; e < 3; ++e) {
-          acc[f][2 * h] = mfma(b[2 * h], sp[e], acc[f][2 * h]);
-          acc[f][2 * h + 1] = mfma(b[2 * h + 1], sp[e], acc[f][2 * h + 1]);
+        for (int i = 0; i < 4; ++i) {
+          v[h][i] = lo[i];
+          v[h][4 + i] = hi[i];
         }
       }
-  }
-#pragma unroll
-  for (int f = 0; f < NF; ++f)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) mx_keep(acc[f][i]);
-#pragma unroll
-  for (int f = 0; f < NF; ++f) {
-    float gv[8], uv[8], hv[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      gv[i] = gu[f][i / 4][i % 4] + acc[f][i / 4][i % 4];
-      uv[i] = gu[f][2 + i / 4][i % 4] + acc[f][2 + i / 4][i % 4];
-    }
-    if (16 * f + c >= n) continue;
-    const size_t o = (size_t)row[f] * a.ld_h + col;
-    if (a.out_f32) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) hv[i] = silu_mul_wide(gv[i], uv[i]);
-      float* h = static_cast<float*>(a.out) + o;
-      *reinterpret_cast<f32x4*>(h) = f32x4{hv[0], hv[1], hv[2], hv[3]};
-      *reinterpret_cast<f32x4*>(h + 4) = f32x4{hv[4], hv[5], hv[6], hv[7]};
-    } else {
-      mx_silu_mul(gv, uv, hv);
-      u32x4 s;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] = mx_bf16(hv[2 * i]) | (mx_bf16(hv[2 * i + 1]) << 16);
-      *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + o) = s;
+      expand_step(b, v[0], v[1], acc[f]);
     }
   }
+#pragma unroll
+  for (int f = 0; f < NF; ++f) store_h(a, row[f], col, 16 * f + c < n, gu[f], acc[f]);
 }
 
-template <int NW>
-__global__ __launch_bounds__(kThreads) void lora_expand_gateup_kernel(LoraArgs a, int slots) {
+__global__ __launch_bounds__(kThreads) void lora_expand_gateup_kernel(LoraArgs a) {
   __shared__ int list[kWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15;
-  const int win = blockIdx.x / slots, slot = blockIdx.x - win * slots;
   const int i0 = (blockIdx.y * kWaves + wave) * 32;
-  const int r0 = win * NW;
-  const Row w = window_row<false>(a, r0 + lane, lane < NW);
+  const int r0 = blockIdx.x * kLoraLargeRows;
+  const Row w = window_row<false>(a, r0 + lane);
   Groups gr;
   gr.init(w.key, kBaseRouted);
   uint64_t rows;
   int key;
-  while (gr.next(w.key, slot, slots, rows, key)) {
-    const bool sh = key >= 0 ? key % (a.E + a.n_shared) >= a.E : key == kBaseShared;
-    const int width = sh ? a.I_sh : a.I;
+  while (gr.next(w.key, rows, key)) {
+    const int width = width_of(a, key);
     const Pair p = pair_of(a, key, 2 * width, a.H);
     if (i0 >= width) continue;
     const int n = list_rows(rows, list[wave]);
@@ -603,109 +620,233 @@ __global__ __launch_bounds__(kThreads) void lora_expand_gateup_kernel(LoraArgs a
       for (int f = 0; f < NF; ++f) row[f] = r0 + list[wave][min(16 * f + c, n - 1)];
       expand_group<NF>(a, p, width, i0, row, n);
     };
-    if constexpr (NW == 16) {
-      run(std::integral_constant<int, 1>{});
-    } else {
-      if (n <= 16) run(std::integral_constant<int, 1>{});
-      else if (n <= 32) run(std::integral_constant<int, 2>{});
-      else run(std::integral_constant<int, 4>{});
-    }
+    if (n <= 16) run(std::integral_constant<int, 1>{});
+    else if (n <= 32) run(std::integral_constant<int, 2>{});
+    else run(std::integral_constant<int, 4>{});
   }
 }
 
 // ---------------------------------------------------------------------
-// expand, down, by tokens: out[t][n] = base + sum over the token's rows of
-// w B v.  The rows' ranks form one long axis, in pieces of 8 that each have a
-// matrix of their own; a matrix product over 32 of it takes four pieces, whatever
-// rows they are of.  The other operand's columns 0, 1, 2 are the three parts of w v.
-constexpr int kPieces = 128;   // of a pass
+// Few rows, gate/up: one launch.  A workgroup takes one group of a window of 16
+// rows; its waves share K, v stays in LDS, and each wave then takes blocks of 32
+// columns, the first one's g, u and B asked for before the products of K.  A few
+// tokens' time is trips to memory, so what depends on nothing is read at once:
+// the window's pairs with all tokens' experts and adapters, then the table's
+// entry, then the matrices.  Eight waves share the trips of a workgroup that has
+// a compute unit to itself, four leave room for three workgroups.
+constexpr int kSmallTiles = 2;   // of 16 ranks at a time
 
-__global__ __launch_bounds__(kThreads) void lora_expand_down_kernel(LoraArgs a) {
-  __shared__ const uint16_t* src[kPieces];   // B + the piece's first rank
-  __shared__ int stride[kPieces];            // the matrix's rank, 0: nothing
+template <int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void lora_gateup_small_kernel(LoraArgs a) {
+  constexpr int kVPitch = 2 * kLoraMaxRank + 4;
+  __shared__ int list[WAVES][64];
+  __shared__ int ids[kLoraManyRows], adapter[kLoraManyRows];
+  __shared__ __align__(16) float red[WAVES * kSmallTiles * 256];
+  __shared__ __align__(16) float v[16 * kVPitch];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, g = lane >> 4;
+  const int win = blockIdx.x / kLoraSmallRows, slot = blockIdx.x - win * kLoraSmallRows;
+  const int r0 = win * kLoraSmallRows, r = r0 + lane;
+  const int pr = lane < kLoraSmallRows && r < a.P ? a.sorted_pair[r] : 0;
+  for (int i = tid; i < a.P; i += 64 * WAVES) ids[i] = a.topk_ids[i];
+  for (int i = tid; i < a.T; i += 64 * WAVES) adapter[i] = a.adapter[i];
+  __syncthreads();
+  const Row w = window_row<false>(a, lane < kLoraSmallRows ? r : a.R, pr, ids, adapter);
+  Groups gr;
+  gr.init(w.key, kBaseRouted);
+  uint64_t rows;
+  int key;
+  for (int i = 0; i <= slot; ++i)   // its slot-th group
+    if (!gr.next(w.key, rows, key)) return;
+  const int width = width_of(a, key);
+  const Pair p = pair_of(a, key, 2 * width, a.H);
+  const int n = list_rows(rows, list[wave]);
+  const int l = list[wave][min(c, n - 1)];   // past the group's end: computed and dropped
+  const int row[1] = {r0 + l};
+  const void* src[1] = {static_cast<const uint16_t*>(a.in) + (size_t)__shfl(w.token, l) * a.H};
+
+  struct Block {
+    f32x4 gu[4];
+    u32x4 b[4];
+  };
+  Block cur, nxt;
+  auto load = [&](int i0, Block& x) {
+    if (i0 >= width) return;
+    load_gu(a, row[0], i0 + 8 * g, x.gu);
+    load_b(p, width, i0, 0, x.b);
+  };
+  load(wave * 32, cur);
+  const int C = 2 * p.rank;
+  for (int ct0 = 0; 16 * ct0 < C; ct0 += kSmallTiles) {
+    f32x4 acc[1][kSmallTiles];
+    shrink_part<WAVES, false>(p, a.H, C, ct0, wave, src, acc);
+    if (ct0) __syncthreads();   // the last tiles' parts have been read
+#pragma unroll
+    for (int j = 0; j < kSmallTiles; ++j)
+      *reinterpret_cast<f32x4*>(red + ((wave * kSmallTiles + j) * 64 + lane) * 4) = acc[0][j];
+    __syncthreads();
+    if (wave < kSmallTiles) {
+      f32x4 t = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int k = 0; k < WAVES; ++k)
+        t += *reinterpret_cast<const f32x4*>(red + ((k * kSmallTiles + wave) * 64 + lane) * 4);
+      const int col = 16 * (ct0 + wave) + 4 * g;
+      if (col < C) *reinterpret_cast<f32x4*>(v + c * kVPitch + col) = t * p.scale;
+    }
+  }
+  __syncthreads();
+  for (int i0 = wave * 32; i0 < width; i0 += WAVES * 32) {
+    load(i0 + WAVES * 32, nxt);
+    f32x4 acc[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int k0 = 0; k0 < p.rank; k0 += 32) {
+      const int j = k0 + 8 * g;
+      if (k0) load_b(p, width, i0, k0, cur.b);
+      float t[2][8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[h][i] = j < p.rank ? v[c * kVPitch + h * p.rank + j + i] : 0.0f;
+      expand_step(cur.b, t[0], t[1], acc);
+    }
+    store_h(a, row[0], i0 + 8 * g, c < n, cur.gu, acc);
+    cur = nxt;
+  }
+}
+
+// ---------------------------------------------------------------------
+// Few tokens, down: one launch.  A workgroup takes a token and 256 NT columns.
+// It makes v of all the token's rows (a wave a row; a row's h and A are small next
+// to B, and the other workgroups of the token find them in the cache), then
+// out[t][n] = base[t][n] + sum over the rows of w B v.  There the rows' ranks form
+// one long axis, in pieces of 8 that each have a matrix of their own; a matrix
+// product over 32 of it takes four pieces, whatever rows they are of.  The other
+// operand's columns 0, 1, 2 are the three parts of w v.  The first steps' B is
+// asked for with A, a trip to memory earlier.
+constexpr int kPieces = 128;      // of a pass
+constexpr int kDownWaves = 16;
+
+template <int NT, bool F32>
+__global__ __launch_bounds__(64 * kDownWaves) void lora_down_small_kernel(LoraArgs a) {
+  __shared__ Pair pair[kPieces];
+  __shared__ int row_of[kPieces];
+  __shared__ float weight_of[kPieces];
   __shared__ __align__(16) u32x4 vs[3][kPieces];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int c = lane & 15, g = lane >> 4;
   const int t = blockIdx.x;
-  const int n0 = (blockIdx.y * kWaves + wave) * 16;
+  const int n0 = (blockIdx.y * kDownWaves + wave) * 16 * NT;
   const int per = a.max_rank / 8;            // pieces of a row
-  const int choices = a.k + a.n_shared;
-  const int total = choices * per;
+  const int choices = a.k + a.n_shared, at_once = kPieces / per;
   const int d = a.adapter[t];
-  const bool has = (unsigned)d < (unsigned)a.n;
-  const int nc = min(n0 + c, a.H - 1);
-  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
   const u32x4 zero = {0u, 0u, 0u, 0u};
-  for (int q0 = 0; has && q0 < total; q0 += kPieces) {
-    const int m = min(total - q0, kPieces);
-    if (q0) __syncthreads();
-    if (tid < kPieces) {
-      const int q = q0 + tid, ch = q / per, j = 8 * (q - ch * per);
-      const uint16_t* sp = nullptr;
-      int rank = 0;
-      u32x4 parts[3] = {zero, zero, zero};
-      if (tid < m) {
-        int row, e;
-        float wt;
-        if (ch < a.k) {
-          row = a.pair_pos[t * a.k + ch];
-          e = a.topk_ids[t * a.k + ch];
-          wt = a.topk_w[t * a.k + ch];
-        } else {
-          const int s = ch - a.k;
-          row = a.P + s * a.T + t;
-          e = a.E + s;
-          wt = a.shared_gate ? shared_gate_weight(a.shared_gate[(size_t)t * a.n_shared + s]) : 1.0f;
-        }
-        const bool ok = (unsigned)row < (unsigned)a.R && (unsigned)e < (unsigned)(a.E + a.n_shared);
-        if (ok) {
-          const int width = e < a.E ? a.I : a.I_sh;
-          const moe_lora* dp = a.table + (size_t)d * (a.E + a.n_shared) + e;
-          const Pair p = pair_of(a, (int)(dp - a.table), a.H, width);
-          if (j < p.rank) {
-            rank = p.rank;
-            sp = p.b + j;
-            float f[8];
-            load_v(a, row, j, f);
+  constexpr int kAhead = 8 / NT;   // steps
+  f32x4 acc[NT];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] *= wt;
-            split3(f, parts);
-          }
-        }
+  for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int c0 = 0; c0 < choices; c0 += at_once) {
+    const int m = min(choices - c0, at_once), pieces = m * per;
+    int row = 0, e = -1;
+    float wt = 1.0f;
+    if (tid < m) {
+      const int ch = c0 + tid;
+      if (ch < a.k) {
+        row = a.pair_pos[(size_t)t * a.k + ch];
+        e = a.topk_ids[(size_t)t * a.k + ch];
+        wt = a.topk_w[(size_t)t * a.k + ch];
+      } else {
+        const int s = ch - a.k;
+        row = a.P + s * a.T + t;
+        e = a.E + s;
+        if (a.shared_gate) wt = shared_gate_weight(a.shared_gate[(size_t)t * a.n_shared + s]);
       }
-      src[tid] = sp;
-      stride[tid] = rank;
-#pragma unroll
-      for (int i = 0; i < 3; ++i) vs[i][tid] = parts[i];
+    }
+    if ((unsigned)d >= (unsigned)a.n) break;   // after the loads: one trip with d's
+    if (c0) __syncthreads();                   // the last pass is done
+    if (tid < m) {
+      const bool ok = (unsigned)row < (unsigned)a.R && (unsigned)e < (unsigned)(a.E + a.n_shared);
+      const int key = ok ? d * (a.E + a.n_shared) + e : kNoRow;
+      pair[tid] = pair_of(a, key, a.H, ok ? width_of(a, key) : 0);
+      row_of[tid] = ok ? row : 0;
+      weight_of[tid] = wt;
     }
     __syncthreads();
-    const int groups = (m + 3) / 4;
-#pragma unroll 4
-    for (int s = 0; s < groups; ++s) {
-      const int q = 4 * s + g, rank = stride[q];
-      const u32x4 b =
-          rank ? *reinterpret_cast<const u32x4*>(src[q] + (size_t)nc * rank) : zero;
-      const u32x4 v = c < 3 ? vs[c][q] : zero;
-      acc = mfma(b, v, acc);
+    auto load_b = [&](int s, u32x4 (&b)[NT]) {   // pieces s + g, s a multiple of 4
+      const int q = min(s + g, pieces - 1), ch = q / per, j = 8 * (q - ch * per);
+      const int rank = s + g < pieces ? pair[ch].rank : 0;
+      const auto* bp = (const __attribute__((address_space(1))) uint16_t*)pair[ch].b;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        b[i] = zero;
+        if (j < rank)
+          b[i] = *(const __attribute__((address_space(1))) u32x4*)(
+              bp + b_at(min(n0 + 16 * i + c, a.H - 1), j, rank));
+      }
+    };
+    u32x4 ahead[kAhead][NT];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load_b(4 * i, ahead[i]);
+    // v of the pass's rows
+    for (int ch = wave; ch < m; ch += kDownWaves) {
+      Pair p;
+      p.rank = __builtin_amdgcn_readfirstlane(pair[ch].rank);
+      const uint64_t at = reinterpret_cast<uint64_t>(pair[ch].a);
+      p.a = reinterpret_cast<const uint16_t*>(
+          ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(at >> 32)) << 32) |
+          (uint32_t)__builtin_amdgcn_readfirstlane((int)at));
+      const int r = __builtin_amdgcn_readfirstlane(row_of[ch]);
+      const int K = r < a.P ? a.I : a.I_sh;
+      const void* in[1] = {F32 ? (const void*)(static_cast<const float*>(a.in) + (size_t)r * a.ld_h)
+                               : (const void*)(static_cast<const uint16_t*>(a.in) + (size_t)r * a.ld_h)};
+      const float scale = pair[ch].scale, w = weight_of[ch];
+      for (int ct = 0; 16 * ct < 8 * per; ++ct) {
+        f32x4 x[1][1] = {{f32x4{0.0f, 0.0f, 0.0f, 0.0f}}};
+        if (16 * ct < p.rank) shrink_part<1, F32>(p, K, p.rank, ct, 0, in, x);
+        mx_keep(x[0][0]);
+        const int j = 16 * ct + 4 * g;   // every column of x is the same
+        if (c == 0 && j < 8 * per) {
+          uint32_t q[4][3];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            split3(j < p.rank ? x[0][0][i] * scale * w : 0.0f, q[i][0], q[i][1], q[i][2]);
+#pragma unroll
+          for (int i = 0; i < 3; ++i)
+            reinterpret_cast<uint2*>(&vs[i][ch * per + j / 8])[(j >> 2) & 1] =
+                make_uint2(q[0][i] | (q[1][i] << 16), q[2][i] | (q[3][i] << 16));
+        }
+      }
+    }
+    __syncthreads();
+    auto add = [&](int s, const u32x4 (&b)[NT]) {
+      const u32x4 x = c < 3 && s + g < pieces ? vs[c][s + g] : zero;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) acc[i] = mfma(b[i], x, acc[i]);
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) add(4 * i, ahead[i]);
+    for (int s = 4 * kAhead; s < pieces; s += 4) {
+      u32x4 b[NT];
+      load_b(s, b);
+      add(s, b);
     }
   }
-  // the three parts' sums: lanes 1 and 2 of the 16 to lane 0
-  f32x4 sum;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    sum[i] = acc[i] + (__shfl(acc[i], lane + 1) + __shfl(acc[i], lane + 2));
-  const int n = n0 + 4 * g;
-  if (c != 0 || n >= a.H) return;
-  const size_t o = (size_t)t * a.H + n;
-  const f32x4 b = *reinterpret_cast<const f32x4*>(a.base + o);
-  sum += b;
-  if (a.out_f32) {
-    *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + o) = sum;
-  } else {
-    uint2 s;
-    s.x = mx_bf16(sum[0]) | (mx_bf16(sum[1]) << 16);
-    s.y = mx_bf16(sum[2]) | (mx_bf16(sum[3]) << 16);
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + o) = s;
+  for (int i = 0; i < NT; ++i) {
+    // the three parts' sums: lanes 1 and 2 of the 16 to lane 0
+    f32x4 sum;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      sum[e] = acc[i][e] + (__shfl(acc[i][e], lane + 1) + __shfl(acc[i][e], lane + 2));
+    const int n = n0 + 16 * i + 4 * g;
+    if (c != 0 || n >= a.H) continue;
+    const size_t o = (size_t)t * a.H + n;
+    sum += *reinterpret_cast<const f32x4*>(a.base + o);
+    if (a.out_f32) {
+      *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + o) = sum;
+    } else {
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + o) =
+          make_uint2(mx_bf16(sum[0]) | (mx_bf16(sum[1]) << 16), mx_bf16(sum[2]) | (mx_bf16(sum[3]) << 16));
+    }
   }
 }
 
@@ -819,7 +960,7 @@ void lora_accumulate_kernel(LoraArgs a, int n_slabs) {
     for (int k = 0; k < KB; ++k) {
       const int q = 4 * k + g;
       const bool in = q < r8;
-      const uint32_t bo = in ? 16 * (col * r8 + q) : 0xFFFFFFFFu;
+      const uint32_t bo = in ? 16 * ((col & ~31u) * r8 + 32 * q + (col & 31)) : 0xFFFFFFFFu;
       const uint32_t vo = in ? 16 * (q * a.R + r.x) : 0xFFFFFFFFu;
       d.b[k] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(brs, bo, 0, 0));
 #pragma unroll
@@ -905,33 +1046,47 @@ void lora_accumulate_kernel(LoraArgs a, int n_slabs) {
   }
 }
 
+// One 16-byte piece of a matrix per thread, to its place in the tiled layout.
+__global__ __launch_bounds__(kThreads) void lora_tile_kernel(const uint16_t* __restrict__ src, long long pieces,
+                                                             int rows, int cols, int is_b,
+                                                             uint16_t* __restrict__ dst) {
+  const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= pieces) return;
+  const int per_row = cols / 8;
+  const long long m = i / ((long long)rows * per_row);
+  const int in = (int)(i - m * ((long long)rows * per_row)), r = in / per_row, q = in - r * per_row;
+  const size_t at = is_b ? b_at(r, 8 * q, cols)
+                         : (size_t)(r & ~15) * cols + (size_t)(q / 4) * 512 + 8 * ((q & 3) * 16 + (r & 15));
+  const int held = is_b ? rows : (rows + 15) & ~15;
+  *reinterpret_cast<u32x4*>(dst + (size_t)m * held * cols + at) =
+      reinterpret_cast<const u32x4*>(src)[i];
+}
+
 template <int CT>
 hipError_t launch_shrink(const LoraArgs& a, hipStream_t st) {
   const int tiles = (a.halves * a.max_rank + 15) / 16;
-  const int rows = a.large ? kLoraLargeRows : kLoraSmallRows, slots = a.large ? 1 : kLoraSmallRows;
-  const int n_win = (a.R + rows - 1) / rows;
-  dim3 grid(n_win * slots, (tiles + CT - 1) / CT, a.splits);
-  if (a.block) grid.x += a.n_blocks * ((a.win + kPlanWindows - 1) / kPlanWindows);
-#define LORA_GO(NW, F32, PARTS) \
-  lora_shrink_kernel<NW, CT, F32, PARTS><<<grid, kThreads, 0, st>>>(a, slots, n_win)
+  const int n_win = (a.R + kLoraLargeRows - 1) / kLoraLargeRows;
+  dim3 grid(n_win, (tiles + CT - 1) / CT);
   if (a.block) {
-    if (a.in_f32) LORA_GO(kLoraLargeRows, true, true);
-    else LORA_GO(kLoraLargeRows, false, true);
-  } else if (a.large) {
-    if (a.in_f32) LORA_GO(kLoraLargeRows, true, false);
-    else LORA_GO(kLoraLargeRows, false, false);
+    grid.x += a.n_blocks * ((a.win + kPlanWindows - 1) / kPlanWindows);
+    if (a.in_f32) lora_shrink_kernel<CT, true, true><<<grid, kThreads, 0, st>>>(a, n_win);
+    else lora_shrink_kernel<CT, false, true><<<grid, kThreads, 0, st>>>(a, n_win);
   } else {
-    if (a.in_f32) LORA_GO(kLoraSmallRows, true, false);
-    else LORA_GO(kLoraSmallRows, false, false);
+    lora_shrink_kernel<CT, false, false><<<grid, kThreads, 0, st>>>(a, n_win);
   }
-#undef LORA_GO
   return hipGetLastError();
 }
 
 hipError_t shrink(const LoraArgs& a, hipStream_t st) {
-  const int tiles = (a.halves * a.max_rank + 15) / 16;
-  if (!a.large || tiles == 1) return launch_shrink<1>(a, st);
-  return launch_shrink<2>(a, st);
+  return a.halves * a.max_rank <= 16 ? launch_shrink<1>(a, st) : launch_shrink<2>(a, st);
+}
+
+template <int NT>
+hipError_t launch_down_small(const LoraArgs& a, hipStream_t st) {
+  const dim3 grid(a.T, (a.H + 16 * kDownWaves * NT - 1) / (16 * kDownWaves * NT));
+  if (a.in_f32) lora_down_small_kernel<NT, true><<<grid, 64 * kDownWaves, 0, st>>>(a);
+  else lora_down_small_kernel<NT, false><<<grid, 64 * kDownWaves, 0, st>>>(a);
+  return hipGetLastError();
 }
 
 template <int KB>
@@ -946,11 +1101,7 @@ hipError_t launch_accumulate(const LoraArgs& a, hipStream_t st) {
 }  // namespace
 
 void lora_choose(LoraArgs& a) {
-  a.large = a.R > 2048;
-  a.splits = 1;
-  const int tiles = (a.halves * a.max_rank + 15) / 16;
-  while (!a.large && a.splits < kLoraMaxSplits && (long long)a.R * tiles * a.splits * 2 <= 512)
-    a.splits *= 2;
+  a.large = a.R > kLoraManyRows;
   a.block = a.n_blocks = a.win = 0;
   if (a.halves == 1 && a.large && a.E + a.n_shared <= kLoraPlanMaxE &&
       (long long)a.R * a.max_rank * 6 < (1LL << 32)) {   // 32-bit offsets into parts
@@ -962,6 +1113,15 @@ void lora_choose(LoraArgs& a) {
     const long long windows = ((long long)a.block * (a.k + a.n_shared) + 63) / 64;
     a.win = (int)((windows + kLoraSegment - 1) / kLoraSegment) * kLoraSegment;
   }
+}
+
+hipError_t launch_lora_tile(const uint16_t* src, int n, int rows, int cols, int is_b, uint16_t* dst,
+                            hipStream_t st) {
+  const long long pieces = (long long)n * rows * (cols / 8);
+  const long long grid = (pieces + kThreads - 1) / kThreads;
+  if (grid >= 1 << 24) return hipErrorInvalidValue;
+  lora_tile_kernel<<<(int)grid, kThreads, 0, st>>>(src, pieces, rows, cols, is_b, dst);
+  return hipGetLastError();
 }
 
 size_t lora_carve(LoraArgs& a, char* ws) {
@@ -978,33 +1138,38 @@ size_t lora_carve(LoraArgs& a, char* ws) {
     a.plan_count = reinterpret_cast<int*>(take(win * 4));
     a.plan = reinterpret_cast<LoraUnit*>(take(win * 64 * sizeof(LoraUnit)));
     a.plan_rows = reinterpret_cast<LoraUnitRow*>(take(win * 64 * 16 * sizeof(LoraUnitRow)));
-  } else {
-    a.v = reinterpret_cast<float*>(take((size_t)a.splits * a.R * a.halves * a.max_rank * 4));
+  } else if (a.halves == 2 && a.large) {
+    a.v = reinterpret_cast<float*>(take((size_t)a.R * 2 * a.max_rank * 4));
   }
   return off;
 }
 
 hipError_t launch_lora_gateup(const LoraArgs& a, hipStream_t st) {
-  hipError_t e = shrink(a, st);
+  if (!a.large) {
+    const int grid = (a.R + kLoraSmallRows - 1) / kLoraSmallRows * kLoraSmallRows;
+    if (a.R <= 256) lora_gateup_small_kernel<8><<<grid, 512, 0, st>>>(a);
+    else lora_gateup_small_kernel<4><<<grid, 256, 0, st>>>(a);
+    return hipGetLastError();
+  }
+  const hipError_t e = shrink(a, st);
   if (e != hipSuccess) return e;
-  const int rows = a.large ? kLoraLargeRows : kLoraSmallRows, slots = a.large ? 1 : kLoraSmallRows;
-  const dim3 grid((a.R + rows - 1) / rows * slots, (a.ld_h + 32 * kWaves - 1) / (32 * kWaves));
-  if (a.large) lora_expand_gateup_kernel<kLoraLargeRows><<<grid, kThreads, 0, st>>>(a, slots);
-  else lora_expand_gateup_kernel<kLoraSmallRows><<<grid, kThreads, 0, st>>>(a, slots);
+  const dim3 grid((a.R + kLoraLargeRows - 1) / kLoraLargeRows,
+                  (a.ld_h + 32 * kWaves - 1) / (32 * kWaves));
+  lora_expand_gateup_kernel<<<grid, kThreads, 0, st>>>(a);
   return hipGetLastError();
 }
 
 hipError_t launch_lora_down(const LoraArgs& a, hipStream_t st) {
-  hipError_t e = shrink(a, st);
-  if (e != hipSuccess) return e;
   if (a.block) {
+    const hipError_t e = shrink(a, st);
+    if (e != hipSuccess) return e;
     if (a.max_rank <= 32) return launch_accumulate<1>(a, st);
     if (a.max_rank <= 64) return launch_accumulate<2>(a, st);
     return launch_accumulate<4>(a, st);
   }
-  const dim3 grid(a.T, (a.H + 16 * kWaves - 1) / (16 * kWaves));
-  lora_expand_down_kernel<<<grid, kThreads, 0, st>>>(a);
-  return hipGetLastError();
+  // columns of a workgroup: few tokens are spread, more of them share v
+  if ((long long)a.T * a.H < (1 << 15)) return launch_down_small<1>(a, st);
+  return launch_down_small<2>(a, st);
 }
 
 }  // namespace moe

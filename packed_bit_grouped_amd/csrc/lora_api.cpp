@@ -30,7 +30,8 @@ moe_status check_shape(int T, int H, int I, int E, int k, int n_shared, int I_sh
   if (max_rank > kLoraMaxRank || E > kRouteMaxE || n_shared > 65535) return MOE_E_UNSUPPORTED;
   if ((long long)n_adapters * ((long long)E + n_shared) >= (1LL << 31)) return MOE_E_UNSUPPORTED;
   const long long rows = (long long)T * ((long long)k + n_shared);
-  if ((long long)T * k >= (1LL << 24) || rows >= (1LL << 26)) return MOE_E_UNSUPPORTED;
+  if (T > (1 << 22) || (long long)T * k >= (1LL << 24) || rows >= (1LL << 26))
+    return MOE_E_UNSUPPORTED;
   if (rows * H >= (1LL << 31) || rows * ld_h_of(I, n_shared, I_shared) >= (1LL << 31))
     return MOE_E_UNSUPPORTED;
   return MOE_OK;
@@ -85,6 +86,21 @@ size_t moe_lora_workspace_bytes(int T, int H, int I, int E, int k, int n_shared,
                                 int max_rank) {
   if (check_shape(T, H, I, E, k, n_shared, I_shared, 0, max_rank) != MOE_OK) return 0;
   return workspace_bytes(T, H, I, E, k, n_shared, I_shared, max_rank);
+}
+
+moe_status moe_lora_tile(const uint16_t* src, int n, int rows, int cols, int is_b, uint16_t* dst,
+                         void* stream) {
+  if (n < 0 || rows <= 0 || cols <= 0 || (is_b != 0 && is_b != 1)) return MOE_E_INVAL;
+  if (rows % (is_b ? 32 : 8) || cols % (is_b ? 8 : 32)) return MOE_E_UNSUPPORTED;
+  if ((long long)rows * cols >= (1LL << 31) ||
+      (__int128)n * rows * cols >= (__int128)(1LL << 34))
+    return MOE_E_UNSUPPORTED;
+  if (n == 0) return MOE_OK;
+  if (!src || !dst || src == dst || !aligned(src, 16) || !aligned(dst, 16)) return MOE_E_INVAL;
+  const moe_status st = device_usable();
+  if (st != MOE_OK) return st;
+  return from_hip(
+      launch_lora_tile(src, n, rows, cols, is_b, dst, static_cast<hipStream_t>(stream)));
 }
 
 moe_status moe_lora_gateup_silu(const uint16_t* x, int T, int H, int I, int E, int k,

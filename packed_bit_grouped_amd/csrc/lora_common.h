@@ -9,7 +9,7 @@ namespace moe {
 constexpr int kLoraMaxRank = 128;
 constexpr int kLoraSmallRows = 16;    // rows of a window, small calls
 constexpr int kLoraLargeRows = 64;    // and large ones
-constexpr int kLoraMaxSplits = 4;
+constexpr int kLoraManyRows = 2048;   // rows up to which a call is small
 constexpr int kLoraPlanMaxE = 1088;   // routed and shared experts of a plan
 constexpr int kLoraSlab = 64;         // columns of a workgroup of the accumulating kernel
 constexpr int kLoraMaxBlock = 512;    // and tokens
@@ -39,7 +39,7 @@ struct LoraArgs {
   int H, I, I_sh, ld_h;
   const void* in;               // gate/up: x bf16 [T][H]; down: h [R][ld_h]
   int in_f32;
-  float* v;                     // [splits][R][halves * max_rank]
+  float* v;                     // gate/up, large calls: [R][2 * max_rank]
   // down, large calls: v times the gate weight as three bf16 parts that sum to
   // it, zeros behind an entry's own rank; and the plan of the accumulating
   // kernel, per block of `block` tokens: its rows in win windows of 64, each with
@@ -49,8 +49,7 @@ struct LoraArgs {
   int* plan_count;              // [n_blocks][win] units of a window
   LoraUnit* plan;               // [n_blocks][win][64]
   LoraUnitRow* plan_rows;       // [n_blocks][win][64][16]
-  int splits;                   // parts of K
-  bool large;                   // windows of 64 rows, one workgroup each
+  bool large;                   // windows of 64 rows, two launches
   const float* gu;              // gate/up: [R][2 ld_h]
   const float* base;            // down: [T][H]
   const float* topk_w;          // down
@@ -61,12 +60,16 @@ struct LoraArgs {
   int32_t* err;
 };
 
-// How a call of these sizes runs: fills splits, large and, for down, the
-// accumulating kernel's block (0: not taken), n_blocks and win.  Host only.
+// How a call of these sizes runs: fills large and, for down, the accumulating
+// kernel's block (0: not taken), n_blocks and win.  Host only.
 void lora_choose(LoraArgs& a);
 // The workspace behind the error word, in bytes; with ws, sets the pointers.
 size_t lora_carve(LoraArgs& a, char* ws);
 
+// n matrices [rows][cols] to the layout of A (rows % 8 == 0, cols % 32 == 0) or of
+// B (rows % 32 == 0, cols % 8 == 0).
+hipError_t launch_lora_tile(const uint16_t* src, int n, int rows, int cols, int is_b, uint16_t* dst,
+                            hipStream_t st);
 hipError_t launch_lora_gateup(const LoraArgs& a, hipStream_t st);
 hipError_t launch_lora_down(const LoraArgs& a, hipStream_t st);
 

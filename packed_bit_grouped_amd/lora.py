@@ -16,8 +16,8 @@ projections a pair of low-rank matrices and a scale.
 ``stream`` as in mx.py: a torch stream, or a handle as a number, on which inputs,
 tables and buffers have to be ready.  Outputs are the buffers' own tensors,
 overwritten by the next call on them; calls that overlap in time need buffers
-each.  Adapters' matrices are kept by ``Adapters`` until their place is loaded
-anew or emptied: wait for the steps that still use them before doing so.
+each.  ``Adapters`` keeps its own copies of the matrices until their place is
+loaded anew or emptied: wait for the steps that still use them before doing so.
 """
 from __future__ import annotations
 
@@ -30,7 +30,7 @@ from . import _lib as L
 from . import layer as _w4
 from . import mx as _mx
 from . import router as _router
-from .mx import _BF16, _F32, _I32, _gate, _launch, _side, _want
+from .mx import _BF16, _F32, _I32, _empty, _gate, _gpu, _launch, _side, _used_on, _want
 
 
 class Adapters:
@@ -72,7 +72,8 @@ class Adapters:
         """Adapter `slot` for the experts first, first + 1, ... (shared experts
         are numbers E, ...; one call holds experts of one size): a13 bf16
         [m][2*rank][H] (the gate's rows, then up's) with b13 [m][2I][rank], and a2
-        [m][rank][I] with b2 [m][H][rank], or one of the pairs alone."""
+        [m][rank][I] with b2 [m][H][rank], or one of the pairs alone.  They are
+        laid out anew (moe_lora_tile) and not needed any more."""
         if not 0 <= slot < self.n:
             raise ValueError(f"slot: {slot}, expected one of {self.n}")
         if (a13 is None) != (b13 is None) or (a2 is None) != (b2 is None) or (a13 is None and a2 is None):
@@ -84,6 +85,7 @@ class Adapters:
         if len(widths) != 1:
             raise ValueError("first: routed and shared experts of different sizes in one call")
         width = widths.pop()
+        todo = []
         for tag, a, b, halves, N, K in (("13", a13, b13, 2, 2 * width, self.H),
                                         ("2", a2, b2, 1, self.H, width)):
             if a is None:
@@ -96,10 +98,20 @@ class Adapters:
             pb = _want("b" + tag, b, _BF16, (m, N, rank), self._dev)
             if (pa | pb) % 16:
                 raise ValueError(f"a{tag}, b{tag}: expected 16-byte aligned matrices")
+            todo.append((tag, a, b, rank, N, K))
+        for tag, a, b, rank, N, K in todo:
+            side = _side(_gpu(a), stream)
+            rows = (a.shape[1] + 15) // 16 * 16
+            ta = _empty((m, rows, K), torch.bfloat16, a.device, side)
+            tb = _empty(b.shape, torch.bfloat16, b.device, side)
+            _launch("moe_lora_tile", self._dev, stream, a.data_ptr(), m, a.shape[1], K, 0, ta.data_ptr())
+            _launch("moe_lora_tile", self._dev, stream, b.data_ptr(), m, N, rank, 1, tb.data_ptr())
+            _used_on(side, a, b)
             for i in range(m):
                 self._host[tag][slot * self.per + first + i] = L.LoraDesc(
-                    pa + i * halves * rank * K * 2, pb + i * N * rank * 2, rank, scale, N, K)
-                self._held[tag, slot, first + i] = (a, b)
+                    ta.data_ptr() + i * rows * K * 2, tb.data_ptr() + i * N * rank * 2, rank,
+                    scale, N, K)
+                self._held[tag, slot, first + i] = (ta, tb)
             self._put(tag, slot, first, m, stream)
 
     def unload(self, slot, stream=None):

@@ -31,6 +31,26 @@ def bf16(rng, *shape, scale=1.0):
     return torch.from_numpy((rng.standard_normal(shape) * scale).astype(np.float32)).bfloat16().to(DEV)
 
 
+def test_tiled_layouts_match_their_definition(lora):
+    from packed_bit_grouped_amd import _lib as L
+    rng = np.random.default_rng(0)
+    for n, rows, cols, is_b in ((1, 8, 32, 0), (3, 16, 96, 0), (2, 24, 64, 0), (2, 256, 160, 0), (1, 32, 8, 1),
+                                (3, 96, 24, 1), (2, 64, 128, 1)):
+        m = rng.integers(-30000, 30000, (n, rows, cols)).astype(np.int16)
+        held = rows if is_b else (rows + 15) // 16 * 16
+        dst = torch.zeros((n, held * cols), dtype=torch.int16, device=DEV)
+        L.moe_lora_tile(dev(m), n, rows, cols, is_b, dst)
+        want = np.zeros((n, held * cols), dtype=np.int16)
+        for i in range(n):
+            if is_b:
+                want[i] = m[i].reshape(rows // 32, 32, cols // 8, 8).transpose(0, 2, 1, 3).ravel()
+            else:
+                full = np.zeros((held, cols), dtype=np.int16)
+                full[:rows] = m[i]
+                want[i] = full.reshape(held // 16, 16, cols // 32, 4, 8).transpose(0, 2, 3, 1, 4).ravel()
+        assert np.array_equal(dst.cpu().numpy(), want)
+
+
 def tables(rng, T, k, E, gone=0.0):
     """Routing tables of random choices; gone: that share of pairs has no expert."""
     ids = np.array([rng.permutation(E)[:k] for _ in range(T)], dtype=np.int32).reshape(T, k)
