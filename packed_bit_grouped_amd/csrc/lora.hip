@@ -27,6 +27,7 @@
 // fragments of 16 rows against that pair's matrices.  Sorted rows of a prompt
 // that share an expert are neighbours, so a window holds few groups; a decode
 // batch has up to one per row, and there a workgroup takes one group, from K to h.
+#include <algorithm>
 #include <type_traits>
 
 #include "lora_common.h"
@@ -75,6 +76,12 @@ __device__ __forceinline__ void split3(const float (&f)[8], u32x4 (&s)[3]) {
 // of places without a row.
 constexpr int kBaseShared = -1, kBaseRouted = -2, kNoRow = -3;
 
+// The i-th of n workgroups as a place in order such that an XCD's (i mod 8) are neighbours.
+__device__ __forceinline__ int xcd_order(int i, int n) {
+  const int x = i & 7, per = n >> 3, more = n & 7;
+  return x * per + min(x, more) + (i >> 3);
+}
+
 // A lane's row of the window: its token and number in the adapters' table, and
 // (WEIGHT) what its output joins the token's with.
 struct Row {
@@ -113,9 +120,11 @@ __device__ __forceinline__ Row window_row(const LoraArgs& a, int r) {
 }
 
 // Columns of h of a key's rows.
+__device__ __forceinline__ bool width_is_shared(const LoraArgs& a, int key) {
+  return key >= 0 ? key % (a.E + a.n_shared) >= a.E : key == kBaseShared;
+}
 __device__ __forceinline__ int width_of(const LoraArgs& a, int key) {
-  const bool shared = key >= 0 ? key % (a.E + a.n_shared) >= a.E : key == kBaseShared;
-  return shared ? a.I_sh : a.I;
+  return width_is_shared(a, key) ? a.I_sh : a.I;
 }
 
 // The pair of matrices of a table entry; rank 0 where there is none.
@@ -169,15 +178,19 @@ __device__ __forceinline__ int list_rows(uint64_t rows, int* list) {
 }
 
 // ---------------------------------------------------------------------
+constexpr int kFragments = 2;                   // of 16 rows that run together
+constexpr int kUnitRows = 16 * kFragments;
+
 // shrink: v[row][j] = scale sum_K A[j][K] in[row][K]
 //
 // The workgroup's waves share K; a wave's fragments go from memory to registers,
 // 16 bytes per lane, since every byte of A and of the rows is read by one wave only.
-template <int WORKERS, bool F32, int NF, int CT>
-__device__ __forceinline__ void shrink_part(const Pair& p, int K, int C, int ct0, int me,
+// The loads of U steps are in flight together; what is left goes in 8, 4, 2, 1.
+template <int U, bool F32, int NF, int CT>
+__device__ __forceinline__ void shrink_part(const Pair& p, int K, int C, int ct0, int me, int workers,
                                             const void* const (&rows)[NF], f32x4 (&acc)[NF][CT]) {
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-  const int steps = K >> 5, per = (steps + WORKERS - 1) / WORKERS;
+  const int steps = K >> 5, per = (steps + workers - 1) / workers;
   const int s0 = min(me * per, steps), s1 = min(s0 + per, steps);
   // tiles and steps are the same for all lanes, a lane's place in a step for all steps
   const uint16_t* pa[CT];
@@ -193,11 +206,11 @@ __device__ __forceinline__ void shrink_part(const Pair& p, int K, int C, int ct0
 #pragma unroll
     for (int j = 0; j < CT; ++j) acc[f][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   int s = s0;
-  auto step = [&](auto n_steps) {   // their loads are in flight together
-    constexpr int U = decltype(n_steps)::value;
-    u32x4 wa[U][CT], wx[U][NF][F32 ? 2 : 1];
+  auto step = [&](auto n_steps) {
+    constexpr int N = decltype(n_steps)::value;
+    u32x4 wa[N][CT], wx[N][NF][F32 ? 2 : 1];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
+    for (int i = 0; i < N; ++i) {
 #pragma unroll
       for (int j = 0; j < CT; ++j)
         wa[i][j] = *reinterpret_cast<const u32x4*>(pa[j] + i * 512 + mine[j]);
@@ -215,7 +228,7 @@ __device__ __forceinline__ void shrink_part(const Pair& p, int K, int C, int ct0
       }
     }
 #pragma unroll
-    for (int i = 0; i < U; ++i)
+    for (int i = 0; i < N; ++i) {
 #pragma unroll
       for (int f = 0; f < NF; ++f) {
         if constexpr (F32) {
@@ -233,27 +246,34 @@ __device__ __forceinline__ void shrink_part(const Pair& p, int K, int C, int ct0
           for (int j = 0; j < CT; ++j) acc[f][j] = mfma(wa[i][j], wx[i][f][0], acc[f][j]);
         }
       }
-    s += U;
+    }
+    s += N;
 #pragma unroll
-    for (int j = 0; j < CT; ++j) pa[j] += U * 512;
+    for (int j = 0; j < CT; ++j) pa[j] += N * 512;
   };
-  constexpr int U = F32 ? (NF * CT == 1 ? 4 : 2) : NF * CT == 1 ? 16 : NF * CT == 2 ? 8 : 4;
   while (s + U <= s1) step(std::integral_constant<int, U>{});
+  if constexpr (U > 8)
+    if (s + 8 <= s1) step(std::integral_constant<int, 8>{});
   if constexpr (U > 4)
-    while (s + 4 <= s1) step(std::integral_constant<int, 4>{});
-  while (s < s1) step(std::integral_constant<int, 1>{});
+    if (s + 4 <= s1) step(std::integral_constant<int, 4>{});
+  if constexpr (U > 2)
+    if (s + 2 <= s1) step(std::integral_constant<int, 2>{});
+  if (s < s1) step(std::integral_constant<int, 1>{});
 }
 
-// PARTS: v goes out times the row's weight, as three bf16 parts (the accumulating
-// kernel's operand: it would else be split once per slab of columns).
-template <int NF, int CT, bool F32, bool PARTS>
+// v of the group goes out as three bf16 parts (it would else be split once per
+// slab of columns), in pieces of 8 ranks of neighbouring rows: what a fragment of
+// the expanding kernel loads.  `to` is a row's place among `places` of a piece.
+// Down's v goes out times the row's weight.
+template <int NF, int CT, bool F32, bool DOWN>
 __device__ __forceinline__ void shrink_group(const LoraArgs& a, const Pair& p, int K, int C, int ct0,
-                                             const void* const (&rows)[NF], const int (&row)[NF],
+                                             const void* const (&rows)[NF], uint16_t* parts,
+                                             int places, const int (&to)[NF],
                                              const float (&weight)[NF], int n, float* red) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = lane & 15, g = lane >> 4;
   f32x4 acc[NF][CT];
-  shrink_part<kWaves, F32>(p, K, C, ct0, wave, rows, acc);
+  shrink_part<F32 ? 2 : 8, F32>(p, K, C, ct0, wave, kWaves, rows, acc);
   // the waves' parts meet: wave w adds those of tiles w, w + 4, ...
   __syncthreads();   // the last group's parts have been read
 #pragma unroll
@@ -262,8 +282,6 @@ __device__ __forceinline__ void shrink_group(const LoraArgs& a, const Pair& p, i
     for (int j = 0; j < CT; ++j)
       *reinterpret_cast<f32x4*>(red + ((wave * NF * CT + f * CT + j) * 64 + lane) * 4) = acc[f][j];
   __syncthreads();
-  const int VL = a.halves * a.max_rank;
-  float* v = a.v;
 #pragma unroll
   for (int f = 0; f < NF; ++f)
 #pragma unroll
@@ -277,19 +295,16 @@ __device__ __forceinline__ void shrink_group(const LoraArgs& a, const Pair& p, i
       if (16 * f + c >= n) continue;
       if (col >= C) continue;
       t *= p.scale;
-      if constexpr (PARTS) {
-        uint32_t q[4][3];
+      uint32_t q[4][3];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) split3(t[i] * weight[f], q[i][0], q[i][1], q[i][2]);
-        // a piece of 8 ranks of neighbouring rows is contiguous: what a fragment loads
-        uint16_t* o = a.parts + ((size_t)(col >> 3) * a.R + row[f]) * 8 + (col & 7);
+      for (int i = 0; i < 4; ++i) split3(DOWN ? t[i] * weight[f] : t[i], q[i][0], q[i][1], q[i][2]);
+      // gate/up: up's ranks from max_rank on
+      const int at = DOWN || col < p.rank ? col : col - p.rank + a.max_rank;
+      uint16_t* o = parts + ((size_t)(at >> 3) * places + to[f]) * 8 + (at & 7);
 #pragma unroll
-        for (int e = 0; e < 3; ++e)
-          *reinterpret_cast<uint2*>(o + (size_t)e * a.R * a.max_rank) =
-              make_uint2(q[0][e] | (q[1][e] << 16), q[2][e] | (q[3][e] << 16));
-      } else {
-        *reinterpret_cast<f32x4*>(v + (size_t)row[f] * VL + col) = t;
-      }
+      for (int e = 0; e < 3; ++e)
+        *reinterpret_cast<uint2*>(o + (size_t)e * places * a.halves * a.max_rank) =
+            make_uint2(q[0][e] | (q[1][e] << 16), q[2][e] | (q[3][e] << 16));
     }
 }
 
@@ -428,39 +443,34 @@ __device__ void make_plan(const LoraArgs& a, int b, int part, PlanLds& L) {
   }
 }
 
-template <int CT, bool F32, bool PARTS>
-__global__ __launch_bounds__(kThreads) void lora_shrink_kernel(LoraArgs a, int n_win) {
-  constexpr int NW = kLoraLargeRows, NFM = NW / 16;
+// down, many tokens: v of a window of 64 rows, group after group, and the plan.
+template <int CT, bool F32>
+__global__ __launch_bounds__(kThreads) void lora_shrink_down_kernel(LoraArgs a, int n_win) {
   __shared__ int list[kWaves][64];
-  union Lds {
-    float red[kWaves * NFM * CT * 256];
+  __shared__ __align__(16) union {
+    float red[kWaves * kFragments * CT * 256];
     PlanLds plan;
-  };
-  __shared__ __align__(16) typename std::conditional<PARTS, Lds, float[kWaves * NFM * CT * 256]>::type lds;
-  float* red = reinterpret_cast<float*>(&lds);
+  } lds;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15;
-  const int win = blockIdx.x, ct0 = blockIdx.y * CT;
-  if constexpr (PARTS) {
-    if (win >= n_win) {
-      const int per = (a.win + kPlanWindows - 1) / kPlanWindows, q = win - n_win;
-      if (blockIdx.y == 0) make_plan(a, q / per, q % per, lds.plan);
-      return;
-    }
+  const int ct0 = blockIdx.y * CT;
+  if ((int)blockIdx.x >= n_win) {
+    const int per = (a.win + kPlanWindows - 1) / kPlanWindows, q = (int)blockIdx.x - n_win;
+    if (blockIdx.y == 0) make_plan(a, q / per, q % per, lds.plan);
+    return;
   }
-  const int r0 = win * NW;
-  const Row w = window_row<PARTS>(a, r0 + lane);
+  // neighbouring windows, which share matrices, on one XCD (workgroup mod 8)
+  const int r0 = xcd_order(blockIdx.x, n_win) * kLoraLargeRows;
+  const Row w = window_row<true>(a, r0 + lane);
   Groups gr;
   gr.init(w.key, 0);
   uint64_t rows;
   int key;
   while (gr.next(w.key, rows, key)) {
-    const int width = width_of(a, key);
-    const int K = a.halves == 2 ? a.H : width, N = a.halves == 2 ? 2 * width : a.H;
-    const Pair p = pair_of(a, key, N, K);
-    const int C = a.halves * p.rank;
-    if (16 * ct0 >= C) continue;   // no adapter, or a lower rank than the largest
+    const int K = width_of(a, key);
+    const Pair p = pair_of(a, key, a.H, K);
+    if (16 * ct0 >= p.rank) continue;   // no adapter, or a lower rank than the largest
     const int n = list_rows(rows, list[wave]);
-    auto run = [&](auto nf) {
+    auto run = [&](auto nf, int f0) {
       constexpr int NF = decltype(nf)::value;
       const void* src[NF];
       int row[NF];
@@ -468,19 +478,144 @@ __global__ __launch_bounds__(kThreads) void lora_shrink_kernel(LoraArgs a, int n
 #pragma unroll
       for (int f = 0; f < NF; ++f) {
         // fragments' rows past the group's end are computed and dropped
-        const int l = list[wave][min(16 * f + c, n - 1)];
+        const int l = list[wave][min(16 * (f0 + f) + c, n - 1)];
         row[f] = r0 + l;
-        const int token = __shfl(w.token, l);
-        weight[f] = PARTS ? __shfl(w.weight, l) : 1.0f;
-        if (a.halves == 2) src[f] = static_cast<const uint16_t*>(a.in) + (size_t)token * a.H;
-        else if (F32) src[f] = static_cast<const float*>(a.in) + (size_t)row[f] * a.ld_h;
-        else src[f] = static_cast<const uint16_t*>(a.in) + (size_t)row[f] * a.ld_h;
+        weight[f] = __shfl(w.weight, l);
+        src[f] = static_cast<const char*>(a.in) + (size_t)row[f] * a.ld_h * (F32 ? 4 : 2);
       }
-      shrink_group<NF, CT, F32, PARTS>(a, p, K, C, ct0, src, row, weight, n, red);
+      shrink_group<NF, CT, F32, true>(a, p, K, p.rank, ct0, src, a.parts, a.R, row, weight,
+                                      n - 16 * f0, lds.red);
     };
-    if (n <= 16) run(std::integral_constant<int, 1>{});
-    else if (n <= 32) run(std::integral_constant<int, 2>{});
-    else run(std::integral_constant<int, 4>{});
+    int f0 = 0;
+    for (; 16 * f0 + 16 < n; f0 += 2) run(std::integral_constant<int, 2>{}, f0);
+    if (16 * f0 < n) run(std::integral_constant<int, 1>{}, f0);
+  }
+}
+
+// ---------------------------------------------------------------------
+// gate/up, many rows: three launches.  The first sorts a window of 256 rows by
+// (adapter, expert) and cuts the groups into units of up to 32 rows; rows without
+// an adapter come last.  A unit's products of K and its expansion then read that
+// pair's matrices once, and what bounds both is the bytes that a compute unit
+// takes in (a unit streams about 30 bytes/ns): by windows of 64 rows A came in
+// 3300 times for 1028 pairs (4096 tokens of 9 rows, 4 adapters), by 256 1600
+// times.
+struct SortLds {
+  int2 group[kWaves][64];   // of a wave's rows: key, rows
+  int start[kWaves * 64], count[kWaves], wave_sum[2][kWaves];
+};
+__global__ __launch_bounds__(kLoraWindow) void lora_sort_kernel(LoraArgs a) {
+  static_assert(kLoraWindow == kThreads, "a thread per row");
+  __shared__ SortLds L;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r0 = blockIdx.x * kLoraWindow;
+  const Row w = window_row<false>(a, r0 + tid);
+  // groups of the wave's rows; a group's first lane stands for it
+  int lead = lane, before = 0, groups = 0;
+  uint64_t todo = __ballot(w.key != kNoRow);
+  while (todo) {
+    const int l = __builtin_ctzll(todo);
+    const uint64_t rows = __ballot(w.key == __builtin_amdgcn_readlane(w.key, l));
+    todo &= ~rows;
+    if ((rows >> lane) & 1) {
+      lead = l;
+      before = __popcll(rows & ((1ull << lane) - 1));
+    }
+    if (lane == l) L.group[wave][groups] = make_int2(w.key, __popcll(rows));
+    ++groups;
+  }
+  if (lane == 0) L.count[wave] = groups;
+  const bool stands = lead == lane && w.key != kNoRow;
+  Pair p = {nullptr, nullptr, 0, 0.0f};
+  int shared = 0;
+  if (stands) {
+    shared = width_is_shared(a, w.key);
+    if (w.key >= 0) {
+      const moe_lora d = a.table[w.key];
+      if (d.rank != 0) {
+        if (entry_ok(a, d, 2 * (shared ? a.I_sh : a.I), a.H)) p = Pair{d.a, d.b, d.rank, d.scale};
+        else atomicOr(a.err, 1);
+      }
+    }
+  }
+  __syncthreads();
+  // the same key in other waves: the first one's group holds all its rows
+  int n = 0, prior = 0, home = -1;
+  if (stands)
+    for (int v = 0; v < kWaves; ++v)
+      for (int i = 0; i < L.count[v]; ++i) {
+        const int2 q = L.group[v][i];
+        if (q.x != w.key) continue;
+        if (home < 0) home = 64 * v + i;
+        if (v < wave) prior += q.y;
+        n += q.y;
+      }
+  const bool first = stands && prior == 0;
+  // exclusive sums of rows and units, with an adapter and without
+  const int nu = first ? (n + kUnitRows - 1) / kUnitRows : 0, mine = first ? n | (nu << 16) : 0;
+  int sum[2] = {p.rank ? mine : 0, p.rank ? 0 : mine}, own[2] = {sum[0], sum[1]};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int v = __shfl_up(sum[h], d);
+      if (lane >= d) sum[h] += v;
+    }
+    if (lane == 63) L.wave_sum[h][wave] = sum[h];
+  }
+  __syncthreads();
+  int total[2] = {0, 0};
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int v = 0; v < kWaves; ++v) {
+      if (v < wave) sum[h] += L.wave_sum[h][v];
+      total[h] += L.wave_sum[h][v];
+    }
+  const int at = p.rank ? sum[0] - own[0] : total[0] + sum[1] - own[1];
+  const size_t base = (size_t)blockIdx.x * kLoraWindow;
+  if (first) {
+    L.start[home] = at & 0xFFFF;
+    for (int u = 0; u < nu; ++u)
+      a.units[base + (at >> 16) + u] =
+          LoraGroupUnit{p.a, p.b, p.scale, (uint16_t)p.rank, (uint16_t)shared,
+                        (uint16_t)((at & 0xFFFF) + u * kUnitRows), (uint16_t)min(n - u * kUnitRows, kUnitRows), 0};
+  }
+  if (tid == 0) a.unit_count[blockIdx.x] = make_int2(total[0] >> 16, (total[0] + total[1]) >> 16);
+  __syncthreads();
+  const int start = __shfl(stands ? L.start[home] + prior : 0, lead);
+  if (w.key != kNoRow) a.order[base + start + before] = (uint32_t)w.token | ((uint32_t)tid << 24);
+}
+
+template <int CT>
+__global__ __launch_bounds__(kThreads) void lora_shrink_gateup_kernel(LoraArgs a, int n_win, int slots) {
+  __shared__ __align__(16) float red[kWaves * kFragments * CT * 256];
+  const int c = threadIdx.x & 15;
+  const int ct0 = blockIdx.y * CT;
+  // neighbouring windows, which share matrices, on one XCD (workgroup mod 8)
+  const int i = xcd_order(blockIdx.x, n_win * slots), win = i / slots;
+  const size_t base = (size_t)win * kLoraWindow;
+  const int n_units = a.unit_count[win].x;
+  uint16_t* parts = a.parts + base * 6 * a.max_rank;
+  for (int u = i - win * slots; u < n_units; u += slots) {
+    const LoraGroupUnit m = a.units[base + u];
+    const Pair p = {m.a, m.b, m.rank, m.scale};
+    const int C = 2 * p.rank, n = m.n;
+    if (16 * ct0 >= C) continue;   // a lower rank than the largest
+    auto run = [&](auto nf) {
+      constexpr int NF = decltype(nf)::value;
+      const void* src[NF];
+      int to[NF];
+      const float weight[NF] = {};
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        // fragments' rows past the unit's end are computed and dropped
+        to[f] = m.first + min(16 * f + c, n - 1);
+        src[f] = static_cast<const uint16_t*>(a.in) + (size_t)(a.order[base + to[f]] & 0xFFFFFF) * a.H;
+      }
+      shrink_group<NF, CT, false, false>(a, p, a.H, C, ct0, src, parts, kLoraWindow, to, weight, n, red);
+    };
+    if (n > 16) run(std::integral_constant<int, 2>{});
+    else run(std::integral_constant<int, 1>{});
   }
 }
 
@@ -557,72 +692,94 @@ __device__ __forceinline__ void store_h(const LoraArgs& a, int row, int col, boo
   }
 }
 
-template <int NF>
-__device__ __forceinline__ void expand_group(const LoraArgs& a, const Pair& p, int width, int i0,
-                                             const int (&row)[NF], int n) {
-  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-  const int col = i0 + 8 * g;
-  f32x4 gu[NF][4], acc[NF][4];
+// Many rows: a wave takes 64 columns of every `slots`-th unit, 16 rows at a time,
+// and the fragments' parts are exchanged: a lane ends with four neighbouring
+// columns of four rows, so that loads of g and u are whole runs of 256 bytes.
+// Ranks, rows and columns past the last are offsets out of range: zeros that
+// touch no line.
+constexpr int kExpandCols = 64;
+constexpr uint32_t kOut = 0x80000000u;   // no buffer here is larger
+
+__global__ __launch_bounds__(kThreads) void lora_expand_gateup_kernel(LoraArgs a, int n_win, int slots) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
+  const int i0 = (blockIdx.y * kWaves + wave) * kExpandCols;
+  if (i0 >= a.ld_h) return;
+  const int idx = xcd_order(blockIdx.x, n_win * slots), win = idx / slots;
+  const size_t base = (size_t)win * kLoraWindow;
+  const int r0 = win * kLoraWindow, n_units = a.unit_count[win].y;
+  const int col = i0 + 4 * c;
+  const uint32_t v_part = (uint32_t)(a.max_rank * 2 * kLoraWindow * 2);   // bytes
+  const __amdgpu_buffer_rsrc_t vrs = __builtin_amdgcn_make_buffer_rsrc(
+      a.parts + base * 6 * a.max_rank, 0, (int)(3 * v_part), 0x00020000);
+  const __amdgpu_buffer_rsrc_t grs = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<float*>(a.gu) + (size_t)r0 * 2 * a.ld_h, 0,
+      (int)((uint32_t)min(kLoraWindow, a.R - r0) * 8u * a.ld_h), 0x00020000);
+  for (int u = idx - win * slots; u < n_units; u += slots) {
+    const LoraGroupUnit m = a.units[base + u];
+    const int rank = m.rank, width = m.shared ? a.I_sh : a.I;
+    if (i0 >= width) continue;
+    const __amdgpu_buffer_rsrc_t brs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint16_t*>(m.b), 0, 4 * width * rank, 0x00020000);
+    for (int f0 = 0; f0 < m.n; f0 += 16) {
+      const uint32_t* order = a.order + base + m.first + f0 + 4 * g;
+      int row[4];
+      f32x4 gu[4][2], acc[2][4];   // row 4 g + i; gate, up
 #pragma unroll
-  for (int f = 0; f < NF; ++f) {
-    load_gu(a, row[f], col, gu[f]);
+      for (int i = 0; i < 4; ++i) row[i] = (int)(order[i] >> 24);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[f][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  }
-  for (int k0 = 0; k0 < p.rank; k0 += 32) {
-    const int j = k0 + 8 * g;
-    u32x4 b[4];
-    load_b(p, width, i0, k0, b);
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int f = 0; f < NF; ++f) {
-      float v[2][8];
+        for (int h = 0; h < 2; ++h)
+          gu[i][h] = __builtin_bit_cast(
+              f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                         grs, f0 + 4 * g + i < m.n && col < width ? 4u * ((row[i] * 2 + h) * a.ld_h + col) : kOut, 0, 0));
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        f32x4 lo = {0.0f, 0.0f, 0.0f, 0.0f}, hi = lo;
-        if (j < p.rank) {
-          const f32x4* q = reinterpret_cast<const f32x4*>(a.v + (size_t)row[f] * 2 * a.max_rank +
-                                                          h * p.rank + j);
-          lo = q[0];
-          hi = q[1];
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[h][q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int k0 = 0; k0 < rank; k0 += 32) {
+        const int j = k0 + 8 * g;
+        u32x4 v[2][3], b[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t vo = j < rank ? 16u * ((h * a.max_rank + j) / 8 * kLoraWindow + m.first + f0 + c) : kOut;
+          const uint32_t br = h * width + col;
+          const uint32_t bo = j < rank && col < width ? 2u * ((br & ~31u) * rank + 32 * j + 8 * (br & 31)) : kOut;
+#pragma unroll
+          for (int e = 0; e < 3; ++e)
+            v[h][e] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(vrs, vo, e * v_part, 0));
+#pragma unroll
+          for (int q = 0; q < 4; ++q)   // column 4 c + q
+            b[h][q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(brs, bo + 16 * q, 0, 0));
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[h][i] = lo[i];
-          v[h][4 + i] = hi[i];
+        for (int e = 0; e < 3; ++e)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[h][q] = mfma(v[h][e], b[h][q], acc[h][q]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (f0 + 4 * g + i >= m.n || col >= width) continue;
+        float x[4], y[4], h[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          x[q] = gu[i][0][q] + acc[0][q][i];
+          y[q] = gu[i][1][q] + acc[1][q][i];
+        }
+        const size_t o = (size_t)(r0 + row[i]) * a.ld_h + col;
+        if (a.out_f32) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) h[q] = silu_mul_wide(x[q], y[q]);
+          *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + o) = f32x4{h[0], h[1], h[2], h[3]};
+        } else {
+          mx_silu_mul(x, y, h);
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + o) =
+              make_uint2(mx_bf16(h[0]) | (mx_bf16(h[1]) << 16), mx_bf16(h[2]) | (mx_bf16(h[3]) << 16));
         }
       }
-      expand_step(b, v[0], v[1], acc[f]);
     }
-  }
-#pragma unroll
-  for (int f = 0; f < NF; ++f) store_h(a, row[f], col, 16 * f + c < n, gu[f], acc[f]);
-}
-
-__global__ __launch_bounds__(kThreads) void lora_expand_gateup_kernel(LoraArgs a) {
-  __shared__ int list[kWaves][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15;
-  const int i0 = (blockIdx.y * kWaves + wave) * 32;
-  const int r0 = blockIdx.x * kLoraLargeRows;
-  const Row w = window_row<false>(a, r0 + lane);
-  Groups gr;
-  gr.init(w.key, kBaseRouted);
-  uint64_t rows;
-  int key;
-  while (gr.next(w.key, rows, key)) {
-    const int width = width_of(a, key);
-    const Pair p = pair_of(a, key, 2 * width, a.H);
-    if (i0 >= width) continue;
-    const int n = list_rows(rows, list[wave]);
-    auto run = [&](auto nf) {
-      constexpr int NF = decltype(nf)::value;
-      int row[NF];
-#pragma unroll
-      for (int f = 0; f < NF; ++f) row[f] = r0 + list[wave][min(16 * f + c, n - 1)];
-      expand_group<NF>(a, p, width, i0, row, n);
-    };
-    if (n <= 16) run(std::integral_constant<int, 1>{});
-    else if (n <= 32) run(std::integral_constant<int, 2>{});
-    else run(std::integral_constant<int, 4>{});
   }
 }
 
@@ -664,21 +821,23 @@ __global__ __launch_bounds__(64 * WAVES) void lora_gateup_small_kernel(LoraArgs 
   const int row[1] = {r0 + l};
   const void* src[1] = {static_cast<const uint16_t*>(a.in) + (size_t)__shfl(w.token, l) * a.H};
 
+  // blocks of columns: their g, u and first 32 ranks of B
   struct Block {
     f32x4 gu[4];
     u32x4 b[4];
   };
-  Block cur, nxt;
+  constexpr int kStep = WAVES * 32, kBlocks = WAVES == 8 ? 4 : 2;
+  Block blk[kBlocks];
   auto load = [&](int i0, Block& x) {
     if (i0 >= width) return;
     load_gu(a, row[0], i0 + 8 * g, x.gu);
     load_b(p, width, i0, 0, x.b);
   };
-  load(wave * 32, cur);
+  load(wave * 32, blk[0]);
   const int C = 2 * p.rank;
   for (int ct0 = 0; 16 * ct0 < C; ct0 += kSmallTiles) {
     f32x4 acc[1][kSmallTiles];
-    shrink_part<WAVES, false>(p, a.H, C, ct0, wave, src, acc);
+    shrink_part<8, false>(p, a.H, C, ct0, wave, WAVES, src, acc);
     if (ct0) __syncthreads();   // the last tiles' parts have been read
 #pragma unroll
     for (int j = 0; j < kSmallTiles; ++j)
@@ -693,29 +852,38 @@ __global__ __launch_bounds__(64 * WAVES) void lora_gateup_small_kernel(LoraArgs 
       if (col < C) *reinterpret_cast<f32x4*>(v + c * kVPitch + col) = t * p.scale;
     }
   }
+  __builtin_amdgcn_sched_barrier(0);   // the registers of A's loads are free
+#pragma unroll
+  for (int k = 1; k < kBlocks; ++k) load(wave * 32 + k * kStep, blk[k]);
   __syncthreads();
-  for (int i0 = wave * 32; i0 < width; i0 += WAVES * 32) {
-    load(i0 + WAVES * 32, nxt);
-    f32x4 acc[4];
+  for (int i0 = wave * 32; i0 < width; i0 += kBlocks * kStep) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int k0 = 0; k0 < p.rank; k0 += 32) {
-      const int j = k0 + 8 * g;
-      if (k0) load_b(p, width, i0, k0, cur.b);
-      float t[2][8];
+    for (int k = 0; k < kBlocks; ++k) {
+      const int col = i0 + k * kStep;
+      if (col >= width) break;
+      f32x4 acc[4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int i = 0; i < 4; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int k0 = 0; k0 < p.rank; k0 += 32) {
+        const int j = k0 + 8 * g;
+        if (k0) load_b(p, width, col, k0, blk[k].b);
+        float t[2][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t[h][i] = j < p.rank ? v[c * kVPitch + h * p.rank + j + i] : 0.0f;
-      expand_step(cur.b, t[0], t[1], acc);
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            t[h][i] = j < p.rank ? v[c * kVPitch + h * p.rank + j + i] : 0.0f;
+        expand_step(blk[k].b, t[0], t[1], acc);
+      }
+      store_h(a, row[0], col + 8 * g, c < n, blk[k].gu, acc);
     }
-    store_h(a, row[0], i0 + 8 * g, c < n, cur.gu, acc);
-    cur = nxt;
+#pragma unroll
+    for (int k = 0; k < kBlocks; ++k) load(i0 + (kBlocks + k) * kStep, blk[k]);
   }
 }
 
 // ---------------------------------------------------------------------
-// Few tokens, down: one launch.  A workgroup takes a token and 256 NT columns.
+// Few tokens, down: one launch.  A workgroup takes a token and 192 NT columns.
 // It makes v of all the token's rows (a wave a row; a row's h and A are small next
 // to B, and the other workgroups of the token find them in the cache), then
 // out[t][n] = base[t][n] + sum over the rows of w B v.  There the rows' ranks form
@@ -724,13 +892,16 @@ __global__ __launch_bounds__(64 * WAVES) void lora_gateup_small_kernel(LoraArgs 
 // operand's columns 0, 1, 2 are the three parts of w v.  The first steps' B is
 // asked for with A, a trip to memory earlier.
 constexpr int kPieces = 128;      // of a pass
-constexpr int kDownWaves = 16;
+constexpr int kDownWaves = 12;
 
 template <int NT, bool F32>
 __global__ __launch_bounds__(64 * kDownWaves) void lora_down_small_kernel(LoraArgs a) {
   __shared__ Pair pair[kPieces];
   __shared__ int row_of[kPieces];
   __shared__ float weight_of[kPieces];
+  // [part][row][rank]: one part, or no more than kDownWaves rows of them
+  __shared__ __align__(16) float sums[kDownWaves * kLoraMaxRank > 8 * kPieces ? kDownWaves * kLoraMaxRank
+                                                                              : 8 * kPieces];
   __shared__ __align__(16) u32x4 vs[3][kPieces];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int c = lane & 15, g = lane >> 4;
@@ -740,7 +911,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void lora_down_small_kernel(LoraAr
   const int choices = a.k + a.n_shared, at_once = kPieces / per;
   const int d = a.adapter[t];
   const u32x4 zero = {0u, 0u, 0u, 0u};
-  constexpr int kAhead = 8 / NT;   // steps
+  constexpr int kAhead = NT == 1 ? 5 : 8 / NT;   // steps of B asked for with A
   f32x4 acc[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -786,8 +957,11 @@ __global__ __launch_bounds__(64 * kDownWaves) void lora_down_small_kernel(LoraAr
     u32x4 ahead[kAhead][NT];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) load_b(4 * i, ahead[i]);
-    // v of the pass's rows
-    for (int ch = wave; ch < m; ch += kDownWaves) {
+    // v of the pass's rows: the waves share them, and a row's K where there are
+    // more waves than rows
+    const int parts = m < kDownWaves ? kDownWaves / m : 1;
+    for (int q = wave; q < m * parts; q += kDownWaves) {
+      const int ch = q / parts, part = q - ch * parts;
       Pair p;
       p.rank = __builtin_amdgcn_readfirstlane(pair[ch].rank);
       const uint64_t at = reinterpret_cast<uint64_t>(pair[ch].a);
@@ -798,23 +972,36 @@ __global__ __launch_bounds__(64 * kDownWaves) void lora_down_small_kernel(LoraAr
       const int K = r < a.P ? a.I : a.I_sh;
       const void* in[1] = {F32 ? (const void*)(static_cast<const float*>(a.in) + (size_t)r * a.ld_h)
                                : (const void*)(static_cast<const uint16_t*>(a.in) + (size_t)r * a.ld_h)};
-      const float scale = pair[ch].scale, w = weight_of[ch];
-      for (int ct = 0; 16 * ct < 8 * per; ++ct) {
-        f32x4 x[1][1] = {{f32x4{0.0f, 0.0f, 0.0f, 0.0f}}};
-        if (16 * ct < p.rank) shrink_part<1, F32>(p, K, p.rank, ct, 0, in, x);
-        mx_keep(x[0][0]);
-        const int j = 16 * ct + 4 * g;   // every column of x is the same
-        if (c == 0 && j < 8 * per) {
-          uint32_t q[4][3];
+      float* to = sums + (part * m + ch) * per * 8 + 4 * g;
+      auto tiles = [&](auto n, int ct) {
+        constexpr int CT = decltype(n)::value;
+        f32x4 x[1][CT];
+        shrink_part<(F32 ? 4 : 8) / CT, F32>(p, K, p.rank, ct, part, parts, in, x);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            split3(j < p.rank ? x[0][0][i] * scale * w : 0.0f, q[i][0], q[i][1], q[i][2]);
-#pragma unroll
-          for (int i = 0; i < 3; ++i)
-            reinterpret_cast<uint2*>(&vs[i][ch * per + j / 8])[(j >> 2) & 1] =
-                make_uint2(q[0][i] | (q[1][i] << 16), q[2][i] | (q[3][i] << 16));
+        for (int i = 0; i < CT; ++i) {
+          mx_keep(x[0][i]);
+          const int j = 16 * (ct + i);
+          // every column is the same; the last tile may be half
+          if (c == 0 && j + 4 * g < p.rank) *reinterpret_cast<f32x4*>(to + j) = x[0][i];
         }
+      };
+      int ct = 0;
+      for (; 16 * ct + 16 < p.rank; ct += 2) tiles(std::integral_constant<int, 2>{}, ct);
+      if (16 * ct < p.rank) tiles(std::integral_constant<int, 1>{}, ct);
+    }
+    __syncthreads();
+    for (int i = tid; i < 8 * pieces; i += 64 * kDownWaves) {
+      const int q = i / 8, ch = q / per, j = i - 8 * ch * per;
+      float x = 0.0f;
+      if (j < pair[ch].rank) {
+        for (int k = 0; k < parts; ++k) x += sums[8 * k * pieces + i];
+        x = x * pair[ch].scale * weight_of[ch];
       }
+      uint32_t f[3];
+      split3(x, f[0], f[1], f[2]);
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        reinterpret_cast<uint16_t*>(&vs[e][q])[i & 7] = (uint16_t)f[e];
     }
     __syncthreads();
     auto add = [&](int s, const u32x4 (&b)[NT]) {
@@ -1063,22 +1250,19 @@ __global__ __launch_bounds__(kThreads) void lora_tile_kernel(const uint16_t* __r
 }
 
 template <int CT>
-hipError_t launch_shrink(const LoraArgs& a, hipStream_t st) {
-  const int tiles = (a.halves * a.max_rank + 15) / 16;
-  const int n_win = (a.R + kLoraLargeRows - 1) / kLoraLargeRows;
-  dim3 grid(n_win, (tiles + CT - 1) / CT);
-  if (a.block) {
-    grid.x += a.n_blocks * ((a.win + kPlanWindows - 1) / kPlanWindows);
-    if (a.in_f32) lora_shrink_kernel<CT, true, true><<<grid, kThreads, 0, st>>>(a, n_win);
-    else lora_shrink_kernel<CT, false, true><<<grid, kThreads, 0, st>>>(a, n_win);
-  } else {
-    lora_shrink_kernel<CT, false, false><<<grid, kThreads, 0, st>>>(a, n_win);
-  }
+hipError_t launch_shrink_down(const LoraArgs& a, hipStream_t st) {
+  const int tiles = (a.max_rank + 15) / 16, n_win = (a.R + kLoraLargeRows - 1) / kLoraLargeRows;
+  const dim3 grid(n_win + a.n_blocks * ((a.win + kPlanWindows - 1) / kPlanWindows), (tiles + CT - 1) / CT);
+  if (a.in_f32) lora_shrink_down_kernel<CT, true><<<grid, kThreads, 0, st>>>(a, n_win);
+  else lora_shrink_down_kernel<CT, false><<<grid, kThreads, 0, st>>>(a, n_win);
   return hipGetLastError();
 }
 
-hipError_t shrink(const LoraArgs& a, hipStream_t st) {
-  return a.halves * a.max_rank <= 16 ? launch_shrink<1>(a, st) : launch_shrink<2>(a, st);
+template <int CT>
+hipError_t launch_shrink_gateup(const LoraArgs& a, int n_win, int slots, hipStream_t st) {
+  const dim3 grid(n_win * slots, ((2 * a.max_rank + 15) / 16 + CT - 1) / CT);
+  lora_shrink_gateup_kernel<CT><<<grid, kThreads, 0, st>>>(a, n_win, slots);
+  return hipGetLastError();
 }
 
 template <int NT>
@@ -1139,7 +1323,11 @@ size_t lora_carve(LoraArgs& a, char* ws) {
     a.plan = reinterpret_cast<LoraUnit*>(take(win * 64 * sizeof(LoraUnit)));
     a.plan_rows = reinterpret_cast<LoraUnitRow*>(take(win * 64 * 16 * sizeof(LoraUnitRow)));
   } else if (a.halves == 2 && a.large) {
-    a.v = reinterpret_cast<float*>(take((size_t)a.R * 2 * a.max_rank * 4));
+    const size_t win = (size_t)(a.R + kLoraWindow - 1) / kLoraWindow, rows = win * kLoraWindow;
+    a.parts = reinterpret_cast<uint16_t*>(take(rows * 2 * a.max_rank * 6));
+    a.unit_count = reinterpret_cast<int2*>(take(win * sizeof(int2)));
+    a.units = reinterpret_cast<LoraGroupUnit*>(take(rows * sizeof(LoraGroupUnit)));
+    a.order = reinterpret_cast<uint32_t*>(take((rows + 32) * 4));   // read past a unit's end
   }
   return off;
 }
@@ -1151,25 +1339,34 @@ hipError_t launch_lora_gateup(const LoraArgs& a, hipStream_t st) {
     else lora_gateup_small_kernel<4><<<grid, 256, 0, st>>>(a);
     return hipGetLastError();
   }
-  const hipError_t e = shrink(a, st);
+  const int n_win = (a.R + kLoraWindow - 1) / kLoraWindow;
+  lora_sort_kernel<<<n_win, kLoraWindow, 0, st>>>(a);
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const dim3 grid((a.R + kLoraLargeRows - 1) / kLoraLargeRows,
-                  (a.ld_h + 32 * kWaves - 1) / (32 * kWaves));
-  lora_expand_gateup_kernel<<<grid, kThreads, 0, st>>>(a);
+  // a window's units are dealt to as many workgroups as fill the device some times over
+  const int slots = std::min(kLoraWindow, std::max(8, 2048 / n_win));
+  e = a.max_rank <= 8 ? launch_shrink_gateup<1>(a, n_win, slots, st)
+                      : launch_shrink_gateup<2>(a, n_win, slots, st);
+  if (e != hipSuccess) return e;
+  constexpr int kCols = kExpandCols * kWaves;
+  const dim3 grid(n_win * slots, (a.ld_h + kCols - 1) / kCols);
+  lora_expand_gateup_kernel<<<grid, kThreads, 0, st>>>(a, n_win, slots);
   return hipGetLastError();
 }
 
 hipError_t launch_lora_down(const LoraArgs& a, hipStream_t st) {
   if (a.block) {
-    const hipError_t e = shrink(a, st);
+    const hipError_t e = a.max_rank <= 16 ? launch_shrink_down<1>(a, st) : launch_shrink_down<2>(a, st);
     if (e != hipSuccess) return e;
     if (a.max_rank <= 32) return launch_accumulate<1>(a, st);
     if (a.max_rank <= 64) return launch_accumulate<2>(a, st);
     return launch_accumulate<4>(a, st);
   }
-  // columns of a workgroup: few tokens are spread, more of them share v
-  if ((long long)a.T * a.H < (1 << 15)) return launch_down_small<1>(a, st);
-  return launch_down_small<2>(a, st);
+  // columns of a workgroup: as few as leave a compute unit to each
+  const auto groups = [&](int nt) { return (long long)a.T * ((a.H + 16 * kDownWaves * nt - 1) / (16 * kDownWaves * nt)); };
+  if (groups(1) <= 256) return launch_down_small<1>(a, st);
+  if (groups(2) <= 256) return launch_down_small<2>(a, st);
+  return launch_down_small<4>(a, st);
 }
 
 }  // namespace moe

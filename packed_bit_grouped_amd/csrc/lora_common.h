@@ -7,8 +7,9 @@
 namespace moe {
 
 constexpr int kLoraMaxRank = 128;
-constexpr int kLoraSmallRows = 16;    // rows of a window, small calls
-constexpr int kLoraLargeRows = 64;    // and large ones
+constexpr int kLoraSmallRows = 16;    // rows of a window: gate/up, small calls
+constexpr int kLoraWindow = 256;      // gate/up, large ones
+constexpr int kLoraLargeRows = 64;    // down, large ones
 constexpr int kLoraManyRows = 2048;   // rows up to which a call is small
 constexpr int kLoraPlanMaxE = 1088;   // routed and shared experts of a plan
 constexpr int kLoraSlab = 64;         // columns of a workgroup of the accumulating kernel
@@ -26,6 +27,16 @@ struct alignas(8) LoraUnitRow {
   uint32_t row, place;
 };
 
+// gate/up: up to 32 rows of one (adapter, expert) of a window, neighbours in the
+// window's order; rank 0 without an adapter.
+struct alignas(32) LoraGroupUnit {
+  const uint16_t* a;
+  const uint16_t* b;
+  float scale;
+  uint16_t rank, shared, first, n;
+  uint32_t unused;
+};
+
 // Rows of a layer (sorted pairs, then the shared experts' tokens) with their
 // tokens' adapters.
 struct LoraArgs {
@@ -39,17 +50,20 @@ struct LoraArgs {
   int H, I, I_sh, ld_h;
   const void* in;               // gate/up: x bf16 [T][H]; down: h [R][ld_h]
   int in_f32;
-  float* v;                     // gate/up, large calls: [R][2 * max_rank]
-  // down, large calls: v times the gate weight as three bf16 parts that sum to
-  // it, zeros behind an entry's own rank; and the plan of the accumulating
-  // kernel, per block of `block` tokens: its rows in win windows of 64, each with
-  // its units
-  uint16_t* parts;              // [3][max_rank / 8][R][8]
+  // large calls: v (down: times the gate weight) as three bf16 parts that sum to
+  // it; gate/up: [window][3][2 max_rank / 8][256][8], down: [3][max_rank / 8][R][8]
+  uint16_t* parts;
+  // gate/up, large calls: windows of 256 rows
+  int2* unit_count;             // [window] units with an adapter, and in all
+  LoraGroupUnit* units;         // [window][256], those with an adapter first
+  uint32_t* order;              // [window][256] token | row of the window << 24
+  // down, large calls: the plan of the accumulating kernel, per block of `block`
+  // tokens: its rows in win windows of 64, each with its units
   int block, n_blocks, win;
   int* plan_count;              // [n_blocks][win] units of a window
   LoraUnit* plan;               // [n_blocks][win][64]
   LoraUnitRow* plan_rows;       // [n_blocks][win][64][16]
-  bool large;                   // windows of 64 rows, two launches
+  bool large;                   // two launches
   const float* gu;              // gate/up: [R][2 ld_h]
   const float* base;            // down: [T][H]
   const float* topk_w;          // down
