@@ -261,19 +261,96 @@ __device__ __forceinline__ void shrink_part(const Pair& p, int K, int C, int ct0
   if (s < s1) step(std::integral_constant<int, 1>{});
 }
 
+// The same with the rows through LDS, a wave's own part of it: the lanes of a
+// fragment each hold another row, and read so every 16 bytes are an access of their
+// own to the cache.  Here a load takes 64 bytes of a row with neighbouring lanes;
+// rows[f] is row 16 f + lane / 4.
+constexpr int kStagedSteps = 2;
+constexpr int kStagedPitch = 80;   // bytes of a row's step: rows spread over the banks
+constexpr int kStagedBytes = 16 * kStagedPitch;
+template <int U, int NF, int CT>
+__device__ __forceinline__ void shrink_staged(const Pair& p, int K, int C, int ct0, int me, int workers,
+                                              const uint16_t* const (&rows)[NF], char* stage,
+                                              f32x4 (&acc)[NF][CT]) {
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  const int steps = K >> 5, per = (steps + workers - 1) / workers;
+  const int s0 = min(me * per, steps), s1 = min(s0 + per, steps);
+  const uint16_t* pa[CT];
+  uint32_t mine[CT];
+#pragma unroll
+  for (int j = 0; j < CT; ++j) {   // rows past the last are computed and dropped
+    const int t = min(ct0 + j, (C - 1) / 16), h = min(C - 16 * t, 16);
+    pa[j] = p.a + (size_t)16 * t * K + (size_t)s0 * 512;
+    mine[j] = 8 * (g * 16 + min(c, h - 1));
+  }
+  const uint16_t* px[NF];
+#pragma unroll
+  for (int f = 0; f < NF; ++f) px[f] = rows[f] + (size_t)s0 * 32 + 8 * (lane & 3);
+  char* put = stage + (lane >> 2) * kStagedPitch + 16 * (lane & 3);
+  const char* get = stage + c * kStagedPitch + 16 * g;
+#pragma unroll
+  for (int f = 0; f < NF; ++f)
+#pragma unroll
+    for (int j = 0; j < CT; ++j) acc[f][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  int s = s0;
+  auto step = [&](auto n_steps) {
+    constexpr int N = decltype(n_steps)::value;
+    u32x4 wa[N][CT], wx[N][NF];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+#pragma unroll
+      for (int f = 0; f < NF; ++f) wx[i][f] = *reinterpret_cast<const u32x4*>(px[f] + i * 32);
+#pragma unroll
+      for (int j = 0; j < CT; ++j)
+        wa[i][j] = *reinterpret_cast<const u32x4*>(pa[j] + i * 512 + mine[j]);
+    }
+    constexpr int kAt = N < kStagedSteps ? N : kStagedSteps;
+#pragma unroll
+    for (int i0 = 0; i0 < N; i0 += kAt) {
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int i = 0; i < kAt; ++i)
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+          *reinterpret_cast<u32x4*>(put + (i * NF + f) * kStagedBytes) = wx[i0 + i][f];
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int i = 0; i < kAt; ++i)
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+          const u32x4 w = *reinterpret_cast<const u32x4*>(get + (i * NF + f) * kStagedBytes);
+#pragma unroll
+          for (int j = 0; j < CT; ++j) acc[f][j] = mfma(wa[i0 + i][j], w, acc[f][j]);
+        }
+    }
+    s += N;
+#pragma unroll
+    for (int j = 0; j < CT; ++j) pa[j] += N * 512;
+#pragma unroll
+    for (int f = 0; f < NF; ++f) px[f] += N * 32;
+  };
+  while (s + U <= s1) step(std::integral_constant<int, U>{});
+  if constexpr (U > 4)
+    if (s + 4 <= s1) step(std::integral_constant<int, 4>{});
+  if constexpr (U > 2)
+    if (s + 2 <= s1) step(std::integral_constant<int, 2>{});
+  if (s < s1) step(std::integral_constant<int, 1>{});
+}
+
 // v of the group goes out as three bf16 parts (it would else be split once per
 // slab of columns), in pieces of 8 ranks of neighbouring rows: what a fragment of
 // the expanding kernel loads.  `to` is a row's place among `places` of a piece.
 // Down's v goes out times the row's weight.
 template <int NF, int CT, bool F32, bool DOWN>
 __device__ __forceinline__ void shrink_group(const LoraArgs& a, const Pair& p, int K, int C, int ct0,
-                                             const void* const (&rows)[NF], uint16_t* parts,
+                                             const typename std::conditional<DOWN, void, uint16_t>::type* const (&rows)[NF], uint16_t* parts,
                                              int places, const int (&to)[NF],
-                                             const float (&weight)[NF], int n, float* red) {
+                                             const float (&weight)[NF], int n, char* stage, float* red) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = lane & 15, g = lane >> 4;
   f32x4 acc[NF][CT];
-  shrink_part<F32 ? 2 : 8, F32>(p, K, C, ct0, wave, kWaves, rows, acc);
+  if constexpr (DOWN) shrink_part<F32 ? 2 : 8, F32>(p, K, C, ct0, wave, kWaves, rows, acc);
+  else shrink_staged<8>(p, K, C, ct0, wave, kWaves, rows, stage, acc);
   // the waves' parts meet: wave w adds those of tiles w, w + 4, ...
   __syncthreads();   // the last group's parts have been read
 #pragma unroll
@@ -484,7 +561,7 @@ __global__ __launch_bounds__(kThreads) void lora_shrink_down_kernel(LoraArgs a, 
         src[f] = static_cast<const char*>(a.in) + (size_t)row[f] * a.ld_h * (F32 ? 4 : 2);
       }
       shrink_group<NF, CT, F32, true>(a, p, K, p.rank, ct0, src, a.parts, a.R, row, weight,
-                                      n - 16 * f0, lds.red);
+                                      n - 16 * f0, nullptr, lds.red);
     };
     int f0 = 0;
     for (; 16 * f0 + 16 < n; f0 += 2) run(std::integral_constant<int, 2>{}, f0);
@@ -589,7 +666,8 @@ __global__ __launch_bounds__(kLoraWindow) void lora_sort_kernel(LoraArgs a) {
 template <int CT>
 __global__ __launch_bounds__(kThreads) void lora_shrink_gateup_kernel(LoraArgs a, int n_win, int slots) {
   __shared__ __align__(16) float red[kWaves * kFragments * CT * 256];
-  const int c = threadIdx.x & 15;
+  __shared__ __align__(16) char stage[kWaves][kStagedSteps * kFragments * kStagedBytes];
+  const int lane = threadIdx.x & 63, c = lane & 15;
   const int ct0 = blockIdx.y * CT;
   // neighbouring windows, which share matrices, on one XCD (workgroup mod 8)
   const int i = xcd_order(blockIdx.x, n_win * slots), win = i / slots;
@@ -603,16 +681,17 @@ __global__ __launch_bounds__(kThreads) void lora_shrink_gateup_kernel(LoraArgs a
     if (16 * ct0 >= C) continue;   // a lower rank than the largest
     auto run = [&](auto nf) {
       constexpr int NF = decltype(nf)::value;
-      const void* src[NF];
+      const uint16_t* src[NF];
       int to[NF];
       const float weight[NF] = {};
 #pragma unroll
       for (int f = 0; f < NF; ++f) {
         // fragments' rows past the unit's end are computed and dropped
         to[f] = m.first + min(16 * f + c, n - 1);
-        src[f] = static_cast<const uint16_t*>(a.in) + (size_t)(a.order[base + to[f]] & 0xFFFFFF) * a.H;
+        src[f] = static_cast<const uint16_t*>(a.in) + 
+                 (size_t)(a.order[base + m.first + min(16 * f + (lane >> 2), n - 1)] & 0xFFFFFF) * a.H;
       }
-      shrink_group<NF, CT, false, false>(a, p, a.H, C, ct0, src, parts, kLoraWindow, to, weight, n, red);
+      shrink_group<NF, CT, false, false>(a, p, a.H, C, ct0, src, parts, kLoraWindow, to, weight, n, stage[threadIdx.x >> 6], red);
     };
     if (n > 16) run(std::integral_constant<int, 2>{});
     else run(std::integral_constant<int, 1>{});
