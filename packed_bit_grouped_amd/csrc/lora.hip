@@ -22,12 +22,18 @@
 // neighbours, a kilobyte together.  From plain rows every lane's load is a cache
 // access of its own: one token's A of 131 KB took 4.5 us in one compute unit.
 //
-// Windows.  A workgroup looks at a window of 16 or 64 neighbouring rows and
-// splits it into groups of rows of one (adapter, expert); each group runs as
-// fragments of 16 rows against that pair's matrices.  Sorted rows of a prompt
-// that share an expert are neighbours, so a window holds few groups; a decode
-// batch has up to one per row, and there a workgroup takes one group, from K to h.
+// Windows.  The rows of a window of neighbours are split into groups of one
+// (adapter, expert); each group runs as fragments of 16 rows against that pair's
+// matrices.  Sorted rows of a prompt that share an expert are neighbours, so a
+// window of 256 holds few groups; a decode batch has up to one per row, and there
+// a workgroup takes one group of a window of 16, from K to h.
+//
+// What the calls measured (H 2048, I 512, 256 experts and a shared one, 8 a token,
+// rank 16; in a graph): one token gate/up 9.7 us, down 7.9; 64 tokens over 32
+// adapters 26 and 14.6 (the matrices at 3.5 and 3.1 TB/s); 4096 tokens over 4
+// adapters 111 (3.4 TB/s of what has to be moved) and 128.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "lora_common.h"
@@ -185,7 +191,9 @@ constexpr int kUnitRows = 16 * kFragments;
 //
 // The workgroup's waves share K; a wave's fragments go from memory to registers,
 // 16 bytes per lane, since every byte of A and of the rows is read by one wave only.
-// The loads of U steps are in flight together; what is left goes in 8, 4, 2, 1.
+// The loads of U steps are in flight together; what is left goes in 8, 4, 2, 1 (a
+// step count that varies in the loop made the compiler wait for each load: 22 us
+// became 50).
 template <int U, bool F32, int NF, int CT>
 __device__ __forceinline__ void shrink_part(const Pair& p, int K, int C, int ct0, int me, int workers,
                                             const void* const (&rows)[NF], f32x4 (&acc)[NF][CT]) {
@@ -264,7 +272,16 @@ __device__ __forceinline__ void shrink_part(const Pair& p, int K, int C, int ct0
 // The same with the rows through LDS, a wave's own part of it: the lanes of a
 // fragment each hold another row, and read so every 16 bytes are an access of their
 // own to the cache.  Here a load takes 64 bytes of a row with neighbouring lanes;
-// rows[f] is row 16 f + lane / 4.
+// rows[f] is row 16 f + lane / 4.  (Gate/up of 4096 tokens, H 2048: 55 us without,
+// 49 so.  fp32 rows go the other way: a lane's 32 bytes of a step are half a line.)
+template <bool F32>
+struct RowOf {
+  typedef uint16_t type;
+};
+template <>
+struct RowOf<true> {
+  typedef void type;
+};
 constexpr int kStagedSteps = 2;
 constexpr int kStagedPitch = 80;   // bytes of a row's step: rows spread over the banks
 constexpr int kStagedBytes = 16 * kStagedPitch;
@@ -337,19 +354,20 @@ __device__ __forceinline__ void shrink_staged(const Pair& p, int K, int C, int c
   if (s < s1) step(std::integral_constant<int, 1>{});
 }
 
-// v of the group goes out as three bf16 parts (it would else be split once per
-// slab of columns), in pieces of 8 ranks of neighbouring rows: what a fragment of
-// the expanding kernel loads.  `to` is a row's place among `places` of a piece.
-// Down's v goes out times the row's weight.
+// v of a unit goes out as three bf16 parts (it would else be split once per slab of
+// columns), in pieces of 8 ranks of the rows in a window's order: what a fragment of
+// the expanding kernels loads.  to[f]: a row's place in the first piece; a piece has
+// `places`.  Down's v goes out times the row's weight.
 template <int NF, int CT, bool F32, bool DOWN>
-__device__ __forceinline__ void shrink_group(const LoraArgs& a, const Pair& p, int K, int C, int ct0,
-                                             const typename std::conditional<DOWN, void, uint16_t>::type* const (&rows)[NF], uint16_t* parts,
-                                             int places, const int (&to)[NF],
-                                             const float (&weight)[NF], int n, char* stage, float* red) {
+__device__ __forceinline__ void shrink_unit(const LoraArgs& a, const Pair& p, int K, int C, int ct0,
+                                            const typename RowOf<F32>::type* const (&rows)[NF],
+                                            int places, uint16_t* const (&to)[NF],
+                                            const float (&weight)[NF], int n, char* stage,
+                                            float* red) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = lane & 15, g = lane >> 4;
   f32x4 acc[NF][CT];
-  if constexpr (DOWN) shrink_part<F32 ? 2 : 8, F32>(p, K, C, ct0, wave, kWaves, rows, acc);
+  if constexpr (F32) shrink_part<2, F32>(p, K, C, ct0, wave, kWaves, rows, acc);
   else shrink_staged<8>(p, K, C, ct0, wave, kWaves, rows, stage, acc);
   // the waves' parts meet: wave w adds those of tiles w, w + 4, ...
   __syncthreads();   // the last group's parts have been read
@@ -370,36 +388,44 @@ __device__ __forceinline__ void shrink_group(const LoraArgs& a, const Pair& p, i
         t += *reinterpret_cast<const f32x4*>(red + ((w * NF * CT + f * CT + j) * 64 + lane) * 4);
       const int col = 16 * (ct0 + j) + 4 * g;
       if (16 * f + c >= n) continue;
-      if (col >= C) continue;
+      if (col >= C || (DOWN && !to[f])) continue;
       t *= p.scale;
       uint32_t q[4][3];
 #pragma unroll
       for (int i = 0; i < 4; ++i) split3(DOWN ? t[i] * weight[f] : t[i], q[i][0], q[i][1], q[i][2]);
       // gate/up: up's ranks from max_rank on
       const int at = DOWN || col < p.rank ? col : col - p.rank + a.max_rank;
-      uint16_t* o = parts + ((size_t)(at >> 3) * places + to[f]) * 8 + (at & 7);
+      uint16_t* o = to[f] + (at >> 3) * places * 8 + (at & 7);
 #pragma unroll
       for (int e = 0; e < 3; ++e)
-        *reinterpret_cast<uint2*>(o + (size_t)e * places * a.halves * a.max_rank) =
+        *reinterpret_cast<uint2*>(o + e * places * (DOWN ? 1 : 2) * a.max_rank) =
             make_uint2(q[0][e] | (q[1][e] << 16), q[2][e] | (q[3][e] << 16));
     }
 }
 
-// First of [lo, hi) whose pair is at least p (an expert's rows are in the order
-// of their pairs).
-__device__ __forceinline__ int first_pair(const int32_t* sorted_pair, int lo, int hi, int p) {
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (sorted_pair[mid] < p) lo = mid + 1;
-    else hi = mid;
+// An expert's rows [lo, hi), in the order of their pairs: the first ones whose pair
+// is at least p and q.  Both searches at once, a trip to memory for each step.
+__device__ __forceinline__ int2 first_pairs(const int32_t* sorted_pair, int lo, int hi, int p, int q) {
+  int2 at = make_int2(lo, lo), end = make_int2(hi, hi);
+  while (at.x < end.x || at.y < end.y) {   // a search that is done stays where it is
+    const int i = (at.x + end.x) >> 1, j = (at.y + end.y) >> 1;
+    const int u = sorted_pair[min(i, hi - 1)], v = sorted_pair[min(j, hi - 1)];
+    if (at.x < end.x) {
+      if (u < p) at.x = i + 1;
+      else end.x = i;
+    }
+    if (at.y < end.y) {
+      if (v < q) at.y = j + 1;
+      else end.y = j;
+    }
   }
-  return lo;
+  return make_int2(at.x, max(at.x, at.y));
 }
 
 // The plan of the accumulating kernel: the rows of one block of tokens, experts
 // in order, in windows of 64; a window's rows reordered by (adapter, expert) and
-// cut into units.  Workgroup `part` of a block makes 8 windows.  It reads no
-// product, so it runs in the shrinking launch, behind its workgroups.
+// cut into units.  v lies in that order, so that a unit's rows are neighbours and a
+// unit is one place, not sixteen.  Workgroup `part` of a block makes 8 windows.
 constexpr int kPlanWindows = 8;
 struct PlanLds {
   int lo[kLoraPlanMaxE], pos[kLoraPlanMaxE + 1], wave_sum[kWaves];
@@ -412,8 +438,9 @@ __device__ void make_plan(const LoraArgs& a, int b, int part, PlanLds& L) {
     int lo, hi;
     if (e < a.E) {
       const int o0 = min(max(a.offsets[e], 0), a.P), o1 = min(max(a.offsets[e + 1], o0), a.P);
-      lo = first_pair(a.sorted_pair, o0, o1, t0 * a.k);
-      hi = first_pair(a.sorted_pair, lo, o1, t1 * a.k);
+      const int2 r = first_pairs(a.sorted_pair, o0, o1, t0 * a.k, t1 * a.k);
+      lo = r.x;
+      hi = r.y;
     } else {
       lo = a.P + (e - a.E) * a.T + t0;
       hi = lo + t1 - t0;
@@ -492,7 +519,7 @@ __device__ void make_plan(const LoraArgs& a, int b, int part, PlanLds& L) {
     const uint64_t first = ~__ballot(same) & ((2ull << lane) - 1);
     const int again = lane - (63 - __builtin_clzll(first));
     uint64_t todo = __ballot(key >= 0);
-    int units = 0;
+    int units = 0, placed = 0;
     while (todo) {
       const int lead = __builtin_ctzll(todo);
       const uint64_t rows = __ballot(key == __builtin_amdgcn_readlane(key, lead) &&
@@ -502,90 +529,58 @@ __device__ void make_plan(const LoraArgs& a, int b, int part, PlanLds& L) {
       const uint64_t bits = reinterpret_cast<uint64_t>(bp);
       const uint32_t b_hi = (uint32_t)__builtin_amdgcn_readlane((int)(bits >> 32), lead);
       const uint32_t b_lo = (uint32_t)__builtin_amdgcn_readlane((int)bits, lead);
-      const u32x4 u = {b_lo, b_hi, (uint32_t)__builtin_amdgcn_readlane(rank, lead) / 8, 0u};
+      const uint32_t rank8 = (uint32_t)__builtin_amdgcn_readlane(rank, lead) / 8;
       const size_t first_unit = (base + w) * 64 + units;
-      if (lane < nu) reinterpret_cast<u32x4*>(a.plan)[first_unit + lane] = u;
+      const uint32_t at = (uint32_t)(base + w) * 64 + placed;
+      const uint32_t place = ((uint32_t)(base + w) * 3 * (a.max_rank / 8) * 64 + placed) * 16;
+      if (lane < nu)
+        reinterpret_cast<u32x4*>(a.plan)[first_unit + lane] =
+            u32x4{b_lo, b_hi, rank8, place + 256u * lane};
       if ((rows >> lane) & 1) {
-        const int t = token - t0;
-        const LoraUnitRow r = {(uint32_t)row, (uint32_t)(t * 256 + (t & 15) * 16)};
-        a.plan_rows[first_unit * 16 + __popcll(rows & ((1ull << lane) - 1))] = r;
+        const int t = token - t0, i = __popcll(rows & ((1ull << lane) - 1));
+        a.plan_sums[first_unit * 16 + i] = (uint32_t)(t * 256 + (t & 15) * 16);
+        a.place[row] = at + i;
       }
-      // places without a row: any row's v, added behind the block
-      if (n + lane < 16 * nu)
-        a.plan_rows[first_unit * 16 + n + lane] =
-            LoraUnitRow{(uint32_t)__builtin_amdgcn_readlane(row, lead), (uint32_t)a.block * 256};
+      // lanes without a row add behind the block
+      if (n + lane < 16 * nu) a.plan_sums[first_unit * 16 + n + lane] = (uint32_t)a.block * 256;
       units += nu;
+      placed += n;
     }
     if (lane == 0) a.plan_count[base + w] = units;
   }
 }
 
-// down, many tokens: v of a window of 64 rows, group after group, and the plan.
-template <int CT, bool F32>
-__global__ __launch_bounds__(kThreads) void lora_shrink_down_kernel(LoraArgs a, int n_win) {
-  __shared__ int list[kWaves][64];
-  __shared__ __align__(16) union {
-    float red[kWaves * kFragments * CT * 256];
-    PlanLds plan;
-  } lds;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15;
-  const int ct0 = blockIdx.y * CT;
-  if ((int)blockIdx.x >= n_win) {
-    const int per = (a.win + kPlanWindows - 1) / kPlanWindows, q = (int)blockIdx.x - n_win;
-    if (blockIdx.y == 0) make_plan(a, q / per, q % per, lds.plan);
-    return;
-  }
-  // neighbouring windows, which share matrices, on one XCD (workgroup mod 8)
-  const int r0 = xcd_order(blockIdx.x, n_win) * kLoraLargeRows;
-  const Row w = window_row<true>(a, r0 + lane);
-  Groups gr;
-  gr.init(w.key, 0);
-  uint64_t rows;
-  int key;
-  while (gr.next(w.key, rows, key)) {
-    const int K = width_of(a, key);
-    const Pair p = pair_of(a, key, a.H, K);
-    if (16 * ct0 >= p.rank) continue;   // no adapter, or a lower rank than the largest
-    const int n = list_rows(rows, list[wave]);
-    auto run = [&](auto nf, int f0) {
-      constexpr int NF = decltype(nf)::value;
-      const void* src[NF];
-      int row[NF];
-      float weight[NF];
-#pragma unroll
-      for (int f = 0; f < NF; ++f) {
-        // fragments' rows past the group's end are computed and dropped
-        const int l = list[wave][min(16 * (f0 + f) + c, n - 1)];
-        row[f] = r0 + l;
-        weight[f] = __shfl(w.weight, l);
-        src[f] = static_cast<const char*>(a.in) + (size_t)row[f] * a.ld_h * (F32 ? 4 : 2);
-      }
-      shrink_group<NF, CT, F32, true>(a, p, K, p.rank, ct0, src, a.parts, a.R, row, weight,
-                                      n - 16 * f0, nullptr, lds.red);
-    };
-    int f0 = 0;
-    for (; 16 * f0 + 16 < n; f0 += 2) run(std::integral_constant<int, 2>{}, f0);
-    if (16 * f0 < n) run(std::integral_constant<int, 1>{}, f0);
-  }
-}
-
 // ---------------------------------------------------------------------
-// gate/up, many rows: three launches.  The first sorts a window of 256 rows by
+// Many rows: three launches.  The first sorts a window of 256 rows by
 // (adapter, expert) and cuts the groups into units of up to 32 rows; rows without
 // an adapter come last.  A unit's products of K and its expansion then read that
-// pair's matrices once, and what bounds both is the bytes that a compute unit
-// takes in (a unit streams about 30 bytes/ns): by windows of 64 rows A came in
-// 3300 times for 1028 pairs (4096 tokens of 9 rows, 4 adapters), by 256 1600
-// times.
+// pair's matrices once.  What bounded both was how often the matrices came in and
+// how few rows a fragment had: from windows of 64 rows, sorted by every workgroup
+// for itself, 4096 tokens of 9 rows over 4 adapters took 62 us of products of K and
+// 85 of expansion; so, 6.6 + 49 + 54 (the last two move their 151 and 230 MB at 3.1
+// and 4.3 TB/s).  A wave finds its groups with ballots, the four waves' lists are
+// then compared (every row with every other one: 10.7 us, so 6.6).
 struct SortLds {
   int2 group[kWaves][64];   // of a wave's rows: key, rows
   int start[kWaves * 64], count[kWaves], wave_sum[2][kWaves];
 };
-__global__ __launch_bounds__(kLoraWindow) void lora_sort_kernel(LoraArgs a) {
+template <bool DOWN>
+__global__ __launch_bounds__(kLoraWindow) void lora_sort_kernel(LoraArgs a, int n_win) {
   static_assert(kLoraWindow == kThreads, "a thread per row");
-  __shared__ SortLds L;
+  __shared__ union {
+    SortLds sort;
+    PlanLds plan;
+  } lds;
+  if constexpr (DOWN) {
+    if ((int)blockIdx.x >= n_win) {
+      const int per = (a.win + kPlanWindows - 1) / kPlanWindows, q = (int)blockIdx.x - n_win;
+      make_plan(a, q / per, q % per, lds.plan);
+      return;
+    }
+  }
+  SortLds& L = lds.sort;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r0 = blockIdx.x * kLoraWindow;
-  const Row w = window_row<false>(a, r0 + tid);
+  const Row w = window_row<DOWN>(a, r0 + tid);
   // groups of the wave's rows; a group's first lane stands for it
   int lead = lane, before = 0, groups = 0;
   uint64_t todo = __ballot(w.key != kNoRow);
@@ -609,7 +604,8 @@ __global__ __launch_bounds__(kLoraWindow) void lora_sort_kernel(LoraArgs a) {
     if (w.key >= 0) {
       const moe_lora d = a.table[w.key];
       if (d.rank != 0) {
-        if (entry_ok(a, d, 2 * (shared ? a.I_sh : a.I), a.H)) p = Pair{d.a, d.b, d.rank, d.scale};
+        const int width = shared ? a.I_sh : a.I;
+        if (entry_ok(a, d, DOWN ? a.H : 2 * width, DOWN ? width : a.H)) p = Pair{d.a, d.b, d.rank, d.scale};
         else atomicOr(a.err, 1);
       }
     }
@@ -660,38 +656,55 @@ __global__ __launch_bounds__(kLoraWindow) void lora_sort_kernel(LoraArgs a) {
   if (tid == 0) a.unit_count[blockIdx.x] = make_int2(total[0] >> 16, (total[0] + total[1]) >> 16);
   __syncthreads();
   const int start = __shfl(stands ? L.start[home] + prior : 0, lead);
-  if (w.key != kNoRow) a.order[base + start + before] = (uint32_t)w.token | ((uint32_t)tid << 24);
+  if (w.key != kNoRow) {
+    a.order[base + start + before] = (uint32_t)w.token | ((uint32_t)tid << 24);
+    if (DOWN) a.weight[base + start + before] = w.weight;
+  }
 }
 
-template <int CT>
-__global__ __launch_bounds__(kThreads) void lora_shrink_gateup_kernel(LoraArgs a, int n_win, int slots) {
+template <int CT, bool F32, bool DOWN>
+__global__ __launch_bounds__(kThreads) void lora_shrink_kernel(LoraArgs a, int n_win, int slots) {
   __shared__ __align__(16) float red[kWaves * kFragments * CT * 256];
-  __shared__ __align__(16) char stage[kWaves][kStagedSteps * kFragments * kStagedBytes];
+  __shared__ __align__(16) char stage[F32 ? 1 : kWaves][kStagedSteps * kFragments * kStagedBytes];
   const int lane = threadIdx.x & 63, c = lane & 15;
   const int ct0 = blockIdx.y * CT;
   // neighbouring windows, which share matrices, on one XCD (workgroup mod 8)
   const int i = xcd_order(blockIdx.x, n_win * slots), win = i / slots;
   const size_t base = (size_t)win * kLoraWindow;
   const int n_units = a.unit_count[win].x;
-  uint16_t* parts = a.parts + base * 6 * a.max_rank;
   for (int u = i - win * slots; u < n_units; u += slots) {
     const LoraGroupUnit m = a.units[base + u];
     const Pair p = {m.a, m.b, m.rank, m.scale};
-    const int C = 2 * p.rank, n = m.n;
+    const int C = (DOWN ? 1 : 2) * p.rank, n = m.n;
+    const int K = !DOWN ? a.H : m.shared ? a.I_sh : a.I;
     if (16 * ct0 >= C) continue;   // a lower rank than the largest
     auto run = [&](auto nf) {
       constexpr int NF = decltype(nf)::value;
-      const uint16_t* src[NF];
-      int to[NF];
-      const float weight[NF] = {};
+      const typename RowOf<F32>::type* src[NF];
+      uint16_t* to[NF];
+      float weight[NF];
 #pragma unroll
       for (int f = 0; f < NF; ++f) {
         // fragments' rows past the unit's end are computed and dropped
-        to[f] = m.first + min(16 * f + c, n - 1);
-        src[f] = static_cast<const uint16_t*>(a.in) + 
-                 (size_t)(a.order[base + m.first + min(16 * f + (lane >> 2), n - 1)] & 0xFFFFFF) * a.H;
+        const int at = m.first + min(16 * f + c, n - 1);
+        const int from = F32 ? at : m.first + min(16 * f + (lane >> 2), n - 1);
+        const uint32_t row = a.order[base + from];
+        const size_t off = DOWN ? (base + (row >> 24)) * a.ld_h : (size_t)(row & 0xFFFFFF) * a.H;
+        if constexpr (F32) src[f] = static_cast<const float*>(a.in) + off;
+        else src[f] = static_cast<const uint16_t*>(a.in) + off;
+        weight[f] = 1.0f;
+        if constexpr (DOWN) {
+          const uint32_t place = a.place[base + (a.order[base + at] >> 24)];
+          to[f] = a.parts + (size_t)(place >> 6) * 64 * 3 * a.max_rank + (place & 63) * 8;
+          weight[f] = a.weight[base + at];
+          // a list of pairs that contradicts itself: no place, nothing is stored
+          if (place >= (uint32_t)a.n_blocks * a.win * 64) to[f] = nullptr;
+        } else {
+          to[f] = a.parts + base * 6 * a.max_rank + at * 8;
+        }
       }
-      shrink_group<NF, CT, false, false>(a, p, a.H, C, ct0, src, parts, kLoraWindow, to, weight, n, stage[threadIdx.x >> 6], red);
+      shrink_unit<NF, CT, F32, DOWN>(a, p, K, C, ct0, src, DOWN ? 64 : kLoraWindow, to, weight, n,
+                                     stage[F32 ? 0 : threadIdx.x >> 6], red);
     };
     if (n > 16) run(std::integral_constant<int, 2>{});
     else run(std::integral_constant<int, 1>{});
@@ -869,7 +882,8 @@ __global__ __launch_bounds__(kThreads) void lora_expand_gateup_kernel(LoraArgs a
 // tokens' time is trips to memory, so what depends on nothing is read at once:
 // the window's pairs with all tokens' experts and adapters, then the table's
 // entry, then the matrices.  Eight waves share the trips of a workgroup that has
-// a compute unit to itself, four leave room for three workgroups.
+// a compute unit to itself, four leave room for three workgroups: 9 rows 9.7 us by
+// eight, 11.8 by four, 231 rows 11.6 and 14.4, 576 rows 32.6 and 26.4.
 constexpr int kSmallTiles = 2;   // of 16 ranks at a time
 
 template <int WAVES>
@@ -1122,19 +1136,23 @@ __global__ __launch_bounds__(64 * kDownWaves) void lora_down_small_kernel(LoraAr
 // block's units (make_plan) and adds each unit's products B v to its tokens'.  A
 // wave owns 16 of the columns of all the tokens, so no two waves meet in a sum,
 // and a unit holds a token once, so no two lanes do: plain reads and writes in a
-// wave's own order, the same result every time (LDS additions without return were
-// ten times slower: 500 us for 4096 tokens, H 2048).  (Rows of y through memory as in the shared
-// projection would be 600 MB for 4096 tokens of 9 rows and H 2048; by tokens,
-// without any reuse of B between them, it took 381 us.)
+// wave's own order, the same result every time.  4096 tokens, H 2048: 96 us, 15 of
+// them base and out; LDS additions without return were five times slower (500 us),
+// sums by tokens without any reuse of B four times (381), and rows of y through
+// memory as in the shared projection would be 600 MB.  What bounds it is none of
+// the rates but the way of a unit through a wave, 200 ns; neither 128 columns of 256
+// tokens (101 to 128 us), waves that share columns and split the adapters (104),
+// products over 16 ranks with 8-byte loads (119) nor deeper batches (116) shorten it.
 // A token's 64 sums are 16 chunks of 4; chunk q lies at q ^ (token % 16), so that
 // the 16 tokens of a unit spread over the banks.
 constexpr int kUnitsAtOnce = 96;   // in LDS
+constexpr int kUnitsAhead = 16;    // and behind them some that do nothing: what the loop reads past its end
 
 template <int KB>   // steps of 32 ranks
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2)))
 void lora_accumulate_kernel(LoraArgs a, int n_slabs) {
   extern __shared__ f32x4 sums[];                // [block + 1][16]
-  __shared__ u32x4 unit_mem[9 * kUnitsAtOnce];   // units, then their rows
+  __shared__ u32x4 unit_mem[5 * (kUnitsAtOnce + kUnitsAhead)];   // a unit, and its rows' places
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int c = lane & 15, g = lane >> 4;
   // the workgroups of an XCD (b mod 8) share slabs: B's rows of a slab stay in its L2
@@ -1144,8 +1162,8 @@ void lora_accumulate_kernel(LoraArgs a, int n_slabs) {
   const int n0 = slab * kLoraSlab, t0 = b * a.block, nt = min(a.block, a.T - t0);
 
   // The units of a segment of windows, `first` on, on their way to LDS: thread t
-  // takes pieces t, t + 256, ... of 16 bytes (a unit has 9).
-  constexpr int kPer = (9 * kUnitsAtOnce + kThreads - 1) / kThreads;
+  // takes pieces t, t + 256, ... of 16 bytes (a unit has 5).
+  constexpr int kPer = (5 * kUnitsAtOnce + kThreads - 1) / kThreads;
   const size_t base = (size_t)b * a.win;
   struct Chunk {
     u32x4 piece[kPer];
@@ -1161,7 +1179,7 @@ void lora_accumulate_kernel(LoraArgs a, int n_slabs) {
     x.n = min(before[kLoraSegment] - first, kUnitsAtOnce);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int p = tid + i * kThreads, u = min(p / 9, x.n - 1), q = p - p / 9 * 9, at = first + u;
+      const int p = tid + i * kThreads, u = min(p / 5, x.n - 1), q = p - p / 5 * 5, at = first + u;
       int w = 0, start = 0;
 #pragma unroll
       for (int k = 1; k < kLoraSegment; ++k)
@@ -1172,7 +1190,7 @@ void lora_accumulate_kernel(LoraArgs a, int n_slabs) {
       const size_t slot = (base + w0 + w) * 64 + (at - start);
       if (x.n > 0)
         x.piece[i] = q == 0 ? reinterpret_cast<const u32x4*>(a.plan)[slot]
-                            : reinterpret_cast<const u32x4*>(a.plan_rows)[slot * 8 + q - 1];
+                            : reinterpret_cast<const u32x4*>(a.plan_sums)[slot * 4 + q - 1];
     }
     return before[kLoraSegment];
   };
@@ -1196,38 +1214,39 @@ void lora_accumulate_kernel(LoraArgs a, int n_slabs) {
     }
   }
   const uint32_t col = min(n0 + 16 * wave + c, a.H - 1);   // B's row of the lane
-  const uint32_t mine = (uint32_t)(4 * wave + g);
-  const uint32_t part_bytes = (uint32_t)a.R * a.max_rank * 2;
-  const __amdgpu_buffer_rsrc_t vrs =
-      __builtin_amdgcn_make_buffer_rsrc(a.parts, 0, (int)(3 * part_bytes), 0x00020000);
-  // Nothing in a unit's way branches, so that the loads of later units stay in
-  // flight behind the products of earlier ones: places without a row repeat one
-  // and add behind the block, and ranks past the last are offsets out of range,
-  // which load zeros and touch no line.
+  const uint32_t mine = (uint32_t)(4 * wave + g) * 16;
+  const uint32_t part_bytes = 64 * a.max_rank * 2;   // of a window's v
+  const __amdgpu_buffer_rsrc_t vrs = __builtin_amdgcn_make_buffer_rsrc(
+      a.parts, 0, (int)((uint32_t)a.n_blocks * a.win * 3 * part_bytes), 0x00020000);
+  // One wave a SIMD: what bounds it is the instructions of a unit.  None branches, so
+  // that the loads of later units stay in flight behind the products of earlier
+  // ones.  Ranks past the last are offsets out of range, which load zeros and touch
+  // no line; lanes without a row load any and add behind the block.
   constexpr int kBatch = 4 / KB;   // units fetched together
   struct Data {
     u32x4 b[KB], v[KB][3];
     uint32_t place;
   };
-  auto look = [&](int i, int n, u32x4& u, uint2& r) {
-    const int k = min(i, n - 1);
-    u = unit_mem[k];
-    r = reinterpret_cast<const uint2*>(unit_mem + kUnitsAtOnce + k * 8)[c];
-    r.y = (i < n ? r.y / 16 : (uint32_t)a.block * 16) ^ mine;
+  struct Unit {
+    u32x4 u;
+    uint32_t place;
   };
-  auto fetch = [&](const u32x4& u, const uint2& r, Data& d) {
-    const int r8 = __builtin_amdgcn_readfirstlane((int)u.z);
-    const uint64_t at = ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)u.y) << 32) |
-                        (uint32_t)__builtin_amdgcn_readfirstlane((int)u.x);
-    const __amdgpu_buffer_rsrc_t brs = __builtin_amdgcn_make_buffer_rsrc(
-        reinterpret_cast<void*>(at), 0, a.H * r8 * 16, 0x00020000);
-    d.place = r.y;
+  auto look = [&](int i, Unit& m) {
+    m.u = unit_mem[5 * i];
+    m.place = reinterpret_cast<const uint32_t*>(unit_mem + 5 * i + 1)[c];
+  };
+  auto fetch = [&](const Unit& m, Data& d) {
+    const uint64_t at = ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)m.u.y) << 32) |
+                        (uint32_t)__builtin_amdgcn_readfirstlane((int)m.u.x);
+    const __amdgpu_buffer_rsrc_t brs =
+        __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(at), 0, (int)kOut, 0x00020000);
+    d.place = m.place ^ mine;
 #pragma unroll
     for (int k = 0; k < KB; ++k) {
-      const int q = 4 * k + g;
-      const bool in = q < r8;
-      const uint32_t bo = in ? 16 * ((col & ~31u) * r8 + 32 * q + (col & 31)) : 0xFFFFFFFFu;
-      const uint32_t vo = in ? 16 * (q * a.R + r.x) : 0xFFFFFFFFu;
+      const uint32_t q = 4 * k + g;
+      const bool in = q < m.u.z;
+      const uint32_t bo = in ? m.u.z * (16 * (col & ~31u)) + 16 * (32 * q + (col & 31)) : kOut;
+      const uint32_t vo = in ? m.u.w + 16 * (q * 64 + c) : kOut;
       d.b[k] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(brs, bo, 0, 0));
 #pragma unroll
       for (int e = 0; e < 3; ++e)
@@ -1246,16 +1265,20 @@ void lora_accumulate_kernel(LoraArgs a, int n_slabs) {
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) acc[i] = mfma(d[i].b[k], d[i].v[k][e], acc[i]);
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) sums[d[i].place] += acc[i];
+    for (int i = 0; i < kBatch; ++i)
+      *reinterpret_cast<f32x4*>(reinterpret_cast<char*>(sums) + d[i].place) += acc[i];
   };
   while (true) {
     const int n = next.n;
+    const uint32_t behind = (uint32_t)a.block * 256;
     __syncthreads();   // the last units have been read, base is in
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int p = tid + i * kThreads, u = p / 9, q = p - u * 9;
-      if (u < n) unit_mem[q == 0 ? u : kUnitsAtOnce + u * 8 + q - 1] = next.piece[i];
+      const int p = tid + i * kThreads;
+      if (p < 5 * n) unit_mem[p] = next.piece[i];
     }
+    if (tid < 5 * kUnitsAhead)   // no rank, behind the block
+      unit_mem[5 * n + tid] = tid % 5 ? u32x4{behind, behind, behind, behind} : u32x4{0u, 0u, 0u, 0u};
     __syncthreads();
     first += kUnitsAtOnce;
     bool more = true;
@@ -1268,16 +1291,15 @@ void lora_accumulate_kernel(LoraArgs a, int n_slabs) {
     }
     if (more) total = load_chunk(w0, counts, first, next);
     if (n > 0) {
-      u32x4 u[kBatch];
-      uint2 r[kBatch];
+      Unit u[kBatch];
       Data cur[kBatch], nxt[kBatch];
       auto look_all = [&](int i0) {
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) look(i0 + i, n, u[i], r[i]);
+        for (int i = 0; i < kBatch; ++i) look(i0 + i, u[i]);
       };
       auto fetch_all = [&](Data (&d)[kBatch]) {
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) fetch(u[i], r[i], d[i]);
+        for (int i = 0; i < kBatch; ++i) fetch(u[i], d[i]);
       };
       look_all(0);
       fetch_all(cur);
@@ -1328,20 +1350,31 @@ __global__ __launch_bounds__(kThreads) void lora_tile_kernel(const uint16_t* __r
       reinterpret_cast<const u32x4*>(src)[i];
 }
 
-template <int CT>
-hipError_t launch_shrink_down(const LoraArgs& a, hipStream_t st) {
-  const int tiles = (a.max_rank + 15) / 16, n_win = (a.R + kLoraLargeRows - 1) / kLoraLargeRows;
-  const dim3 grid(n_win + a.n_blocks * ((a.win + kPlanWindows - 1) / kPlanWindows), (tiles + CT - 1) / CT);
-  if (a.in_f32) lora_shrink_down_kernel<CT, true><<<grid, kThreads, 0, st>>>(a, n_win);
-  else lora_shrink_down_kernel<CT, false><<<grid, kThreads, 0, st>>>(a, n_win);
+template <bool DOWN>
+hipError_t launch_shrink(const LoraArgs& a, int n_win, int slots, hipStream_t st) {
+  const int plans = DOWN ? a.n_blocks * ((a.win + kPlanWindows - 1) / kPlanWindows) : 0;
+  lora_sort_kernel<DOWN><<<n_win + plans, kLoraWindow, 0, st>>>(a, n_win);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int tiles = ((DOWN ? 1 : 2) * a.max_rank + 15) / 16;
+  if (tiles == 1) {
+    const dim3 grid(n_win * slots);
+    if (DOWN && a.in_f32) lora_shrink_kernel<1, true, true><<<grid, kThreads, 0, st>>>(a, n_win, slots);
+    else lora_shrink_kernel<1, false, DOWN><<<grid, kThreads, 0, st>>>(a, n_win, slots);
+  } else {
+    const dim3 grid(n_win * slots, (tiles + 1) / 2);
+    if (DOWN && a.in_f32) lora_shrink_kernel<2, true, true><<<grid, kThreads, 0, st>>>(a, n_win, slots);
+    else lora_shrink_kernel<2, false, DOWN><<<grid, kThreads, 0, st>>>(a, n_win, slots);
+  }
   return hipGetLastError();
 }
 
-template <int CT>
-hipError_t launch_shrink_gateup(const LoraArgs& a, int n_win, int slots, hipStream_t st) {
-  const dim3 grid(n_win * slots, ((2 * a.max_rank + 15) / 16 + CT - 1) / CT);
-  lora_shrink_gateup_kernel<CT><<<grid, kThreads, 0, st>>>(a, n_win, slots);
-  return hipGetLastError();
+// A window's units are dealt to as many workgroups as fill the device some times
+// over: of 144 windows to 14 each 55 + 54 us (products of K, expansion), to 8 each
+// 61 + 59, to 28 each 55 + 56.
+int windows(const LoraArgs& a) { return (a.R + kLoraWindow - 1) / kLoraWindow; }
+int unit_slots(const LoraArgs& a) {
+  return std::min(kLoraWindow, std::max(8, 2048 / windows(a)));
 }
 
 template <int NT>
@@ -1363,19 +1396,47 @@ hipError_t launch_accumulate(const LoraArgs& a, hipStream_t st) {
 
 }  // namespace
 
-void lora_choose(LoraArgs& a) {
-  a.large = a.R > kLoraManyRows;
+// Three launches or one.
+//
+// gate/up: one reads a pair's matrices for every window of 16 rows that holds it.
+// Three cost about 45 us and read them far less often where rows share a pair:
+// 1026 rows of 4 adapters of rank 64 on 33 experts (H 2048, I 512) 48 us against 75,
+// 576 rows 62 against 51; without sharing (32 adapters of rank 16 on 257 experts)
+// 1440 rows 87 against 62, 2052 rows 109 against 83.
+//
+// down: one reads a row's matrices from the cache at 4.6 TB/s, whatever they share;
+// three cost about 40 us and 0.12 for each unit of a block of tokens.  32 adapters
+// on 257 experts: 4104 rows 103 us in one, 148 in three, 18432 rows 348 and 266,
+// 36864 rows 662 and 305; 4 adapters: 4104 rows 84 and 94, 8208 rows 138 and 110,
+// 36864 rows 590 and 126; on 33 experts, rank 64: 576 rows 38 and 68, 1026 rows 65
+// and 59, 4104 rows 157 and 53.
+void lora_choose(LoraArgs& a, bool most) {
   a.block = a.n_blocks = a.win = 0;
-  if (a.halves == 1 && a.large && a.E + a.n_shared <= kLoraPlanMaxE &&
-      (long long)a.R * a.max_rank * 6 < (1LL << 32)) {   // 32-bit offsets into parts
-    const int n_slabs = (a.H + kLoraSlab - 1) / kLoraSlab;
-    a.block = kLoraMaxBlock;
-    while (a.block > 64 && (long long)((a.T + a.block - 1) / a.block) * n_slabs < 256) a.block /= 2;
-    a.n_blocks = (a.T + a.block - 1) / a.block;
-    // whole segments
-    const long long windows = ((long long)a.block * (a.k + a.n_shared) + 63) / 64;
-    a.win = (int)((windows + kLoraSegment - 1) / kLoraSegment) * kLoraSegment;
+  a.large = a.R > kLoraFewRows;
+  const double experts = (double)a.E + a.n_shared;
+  if (a.halves == 2) {
+    const double pairs = experts * std::min(a.n, a.T);
+    const double bytes = 4.0 * a.R * a.max_rank * ((double)a.H + a.I);
+    if (!most && a.R <= kLoraManyRows && (a.R <= 5 * pairs || bytes < 450e6)) a.large = false;
+    return;
   }
+  if (a.E + a.n_shared > kLoraPlanMaxE) a.large = false;
+  if (!a.large) return;
+  const int n_slabs = (a.H + kLoraSlab - 1) / kLoraSlab;
+  a.block = kLoraMaxBlock;
+  while (a.block > 64 && (long long)((a.T + a.block - 1) / a.block) * n_slabs < 256) a.block /= 2;
+  a.n_blocks = (a.T + a.block - 1) / a.block;
+  // whole segments
+  const double rows = (double)a.block * (a.k + a.n_shared);
+  const long long windows = ((long long)a.block * (a.k + a.n_shared) + 63) / 64;
+  a.win = (int)((windows + kLoraSegment - 1) / kLoraSegment) * kLoraSegment;
+  // offsets into v: 31 bits
+  if ((long long)a.n_blocks * a.win * 64 * a.max_rank * 6 >= (1LL << 31)) a.large = false;
+  if (most || !a.large) return;
+  const double pairs = experts * std::min(a.n, std::min(a.T, a.block));
+  const double units = pairs * (1.0 - std::exp(-rows / std::max(pairs, 1.0))) + rows / 16;
+  const double one = 2.0 * a.R * a.max_rank * ((double)a.H + a.I) / 4.6e6;
+  if (a.n == 0 || one < 40.0 + 0.12 * std::min(units, 1200.0)) a.large = false;
 }
 
 hipError_t launch_lora_tile(const uint16_t* src, int n, int rows, int cols, int is_b, uint16_t* dst,
@@ -1395,18 +1456,21 @@ size_t lora_carve(LoraArgs& a, char* ws) {
     off += up256(bytes);
     return p;
   };
-  if (a.block) {
+  if (!a.large) return off;
+  const size_t n_win = (size_t)(a.R + kLoraWindow - 1) / kLoraWindow, rows = n_win * kLoraWindow;
+  a.unit_count = reinterpret_cast<int2*>(take(n_win * sizeof(int2)));
+  a.units = reinterpret_cast<LoraGroupUnit*>(take(rows * sizeof(LoraGroupUnit)));
+  a.order = reinterpret_cast<uint32_t*>(take((rows + kUnitRows) * 4));   // read past a unit's end
+  if (a.halves == 2) {
+    a.parts = reinterpret_cast<uint16_t*>(take(rows * 2 * a.max_rank * 6));
+  } else {
     const size_t win = (size_t)a.n_blocks * a.win;
-    a.parts = reinterpret_cast<uint16_t*>(take((size_t)a.R * a.max_rank * 6));
+    a.weight = reinterpret_cast<float*>(take(rows * 4));
+    a.place = reinterpret_cast<uint32_t*>(take(rows * 4));
+    a.parts = reinterpret_cast<uint16_t*>(take(win * 64 * a.max_rank * 6));
     a.plan_count = reinterpret_cast<int*>(take(win * 4));
     a.plan = reinterpret_cast<LoraUnit*>(take(win * 64 * sizeof(LoraUnit)));
-    a.plan_rows = reinterpret_cast<LoraUnitRow*>(take(win * 64 * 16 * sizeof(LoraUnitRow)));
-  } else if (a.halves == 2 && a.large) {
-    const size_t win = (size_t)(a.R + kLoraWindow - 1) / kLoraWindow, rows = win * kLoraWindow;
-    a.parts = reinterpret_cast<uint16_t*>(take(rows * 2 * a.max_rank * 6));
-    a.unit_count = reinterpret_cast<int2*>(take(win * sizeof(int2)));
-    a.units = reinterpret_cast<LoraGroupUnit*>(take(rows * sizeof(LoraGroupUnit)));
-    a.order = reinterpret_cast<uint32_t*>(take((rows + 32) * 4));   // read past a unit's end
+    a.plan_sums = reinterpret_cast<uint32_t*>(take(win * 64 * 16 * 4));
   }
   return off;
 }
@@ -1418,14 +1482,8 @@ hipError_t launch_lora_gateup(const LoraArgs& a, hipStream_t st) {
     else lora_gateup_small_kernel<4><<<grid, 256, 0, st>>>(a);
     return hipGetLastError();
   }
-  const int n_win = (a.R + kLoraWindow - 1) / kLoraWindow;
-  lora_sort_kernel<<<n_win, kLoraWindow, 0, st>>>(a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  // a window's units are dealt to as many workgroups as fill the device some times over
-  const int slots = std::min(kLoraWindow, std::max(8, 2048 / n_win));
-  e = a.max_rank <= 8 ? launch_shrink_gateup<1>(a, n_win, slots, st)
-                      : launch_shrink_gateup<2>(a, n_win, slots, st);
+  const int n_win = windows(a), slots = unit_slots(a);
+  const hipError_t e = launch_shrink<false>(a, n_win, slots, st);
   if (e != hipSuccess) return e;
   constexpr int kCols = kExpandCols * kWaves;
   const dim3 grid(n_win * slots, (a.ld_h + kCols - 1) / kCols);
@@ -1434,14 +1492,16 @@ hipError_t launch_lora_gateup(const LoraArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_lora_down(const LoraArgs& a, hipStream_t st) {
-  if (a.block) {
-    const hipError_t e = a.max_rank <= 16 ? launch_shrink_down<1>(a, st) : launch_shrink_down<2>(a, st);
+  if (a.large) {
+    const hipError_t e = launch_shrink<true>(a, windows(a), unit_slots(a), st);
     if (e != hipSuccess) return e;
     if (a.max_rank <= 32) return launch_accumulate<1>(a, st);
     if (a.max_rank <= 64) return launch_accumulate<2>(a, st);
     return launch_accumulate<4>(a, st);
   }
-  // columns of a workgroup: as few as leave a compute unit to each
+  // columns of a workgroup: as few as leave a compute unit to each (192, 384 or 768:
+  // one token 7.9 us by 192, 9.2 by 768; 64 tokens 24 and 14.6; 77 tokens, H 1056,
+  // fp32 15.8, 9.5 by 384, 10.7)
   const auto groups = [&](int nt) { return (long long)a.T * ((a.H + 16 * kDownWaves * nt - 1) / (16 * kDownWaves * nt)); };
   if (groups(1) <= 256) return launch_down_small<1>(a, st);
   if (groups(2) <= 256) return launch_down_small<2>(a, st);

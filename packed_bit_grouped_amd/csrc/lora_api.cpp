@@ -60,7 +60,7 @@ LoraArgs args_of(int T, int H, int I, int E, int k, int n_shared, int I_shared,
   a.I_sh = n_shared > 0 ? I_shared : I;
   a.ld_h = ld_h_of(I, n_shared, I_shared);
   a.err = reinterpret_cast<int32_t*>(ws);
-  lora_choose(a);
+  lora_choose(a, ws == nullptr);
   lora_carve(a, ws ? ws + 256 : nullptr);
   return a;
 }

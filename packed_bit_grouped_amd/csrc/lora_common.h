@@ -8,27 +8,23 @@ namespace moe {
 
 constexpr int kLoraMaxRank = 128;
 constexpr int kLoraSmallRows = 16;    // rows of a window: gate/up, small calls
-constexpr int kLoraWindow = 256;      // gate/up, large ones
-constexpr int kLoraLargeRows = 64;    // down, large ones
-constexpr int kLoraManyRows = 2048;   // rows up to which a call is small
+constexpr int kLoraWindow = 256;      // large ones
+constexpr int kLoraFewRows = 640;     // rows up to which a call is one launch
+constexpr int kLoraManyRows = 2048;   // gate/up: up to which it may be
 constexpr int kLoraPlanMaxE = 1088;   // routed and shared experts of a plan
 constexpr int kLoraSlab = 64;         // columns of a workgroup of the accumulating kernel
 constexpr int kLoraMaxBlock = 512;    // and tokens
 constexpr int kLoraSegment = 8;       // windows of 64 rows that it takes at a time
 
-// A unit: up to 16 rows of one (adapter, expert) with tokens of one block, and
-// its rows: the row of v, and the byte of LDS where chunk 0 of the token's sums
-// lies (behind the block's where there is no row).
+// A unit: up to 16 rows of one (adapter, expert) with tokens of one block; v: the
+// byte of parts where the first one's lies, the others' behind it.
 struct alignas(16) LoraUnit {
   const uint16_t* b;
-  int rank8, unused;
-};
-struct alignas(8) LoraUnitRow {
-  uint32_t row, place;
+  uint32_t rank8, v;
 };
 
-// gate/up: up to 32 rows of one (adapter, expert) of a window, neighbours in the
-// window's order; rank 0 without an adapter.
+// Up to 32 rows of one (adapter, expert) of a window, neighbours in the window's
+// order; rank 0 without an adapter.
 struct alignas(32) LoraGroupUnit {
   const uint16_t* a;
   const uint16_t* b;
@@ -50,20 +46,22 @@ struct LoraArgs {
   int H, I, I_sh, ld_h;
   const void* in;               // gate/up: x bf16 [T][H]; down: h [R][ld_h]
   int in_f32;
-  // large calls: v (down: times the gate weight) as three bf16 parts that sum to
-  // it; gate/up: [window][3][2 max_rank / 8][256][8], down: [3][max_rank / 8][R][8]
-  uint16_t* parts;
-  // gate/up, large calls: windows of 256 rows
+  // large calls: windows of 256 rows
   int2* unit_count;             // [window] units with an adapter, and in all
   LoraGroupUnit* units;         // [window][256], those with an adapter first
   uint32_t* order;              // [window][256] token | row of the window << 24
+  // v (down: times the gate weight) as three bf16 parts that sum to it; gate/up:
+  // [window][3][2 max_rank / 8][256][8], down: [plan's window][3][max_rank / 8][64][8]
+  uint16_t* parts;
   // down, large calls: the plan of the accumulating kernel, per block of `block`
   // tokens: its rows in win windows of 64, each with its units
+  float* weight;                // [window][256] in the window's order
+  uint32_t* place;              // [R] plan's window * 64 + place in it
   int block, n_blocks, win;
   int* plan_count;              // [n_blocks][win] units of a window
   LoraUnit* plan;               // [n_blocks][win][64]
-  LoraUnitRow* plan_rows;       // [n_blocks][win][64][16]
-  bool large;                   // two launches
+  uint32_t* plan_sums;          // [n_blocks][win][64][16] byte of a row's token's chunk 0 in LDS
+  bool large;                   // three launches
   const float* gu;              // gate/up: [R][2 ld_h]
   const float* base;            // down: [T][H]
   const float* topk_w;          // down
@@ -75,8 +73,9 @@ struct LoraArgs {
 };
 
 // How a call of these sizes runs: fills large and, for down, the accumulating
-// kernel's block (0: not taken), n_blocks and win.  Host only.
-void lora_choose(LoraArgs& a);
+// kernel's block, n_blocks and win.  most: of any adapters, the way that needs the
+// most workspace.  Host only.
+void lora_choose(LoraArgs& a, bool most);
 // The workspace behind the error word, in bytes; with ws, sets the pointers.
 size_t lora_carve(LoraArgs& a, char* ws);
 

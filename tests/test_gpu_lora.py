@@ -146,11 +146,16 @@ CASES = [  # T, H, I, E, k, n_shared, I_shared, adapters, ranks, runs
     (77, 1056, 352, 12, 3, 0, 0, 5, (24,), False),
     (130, 64, 32, 2, 2, 0, 0, 1, (8,), True),
     (33, 64, 64, 40, 20, 1, 64, 3, (128,), False),     # 336 pieces of rank 8 a token: several passes
-    # more than 2048 rows: windows of 64
+    # more than 2048 rows
     (700, 64, 64, 7, 3, 0, 0, 3, (8, 16), True),
     (700, 96, 32, 3, 3, 1, 64, 40, (16, 40), False),
     (1031, 160, 96, 5, 2, 1, 96, 2, (8, 72, 128), True),
     (2100, 32, 32, 4, 1, 1, 32, 1, (16,), True),
+    # the sums of a block of tokens in LDS: ranks up to 32, 64 and 128, blocks of 64 tokens and more
+    (1100, 2080, 384, 6, 3, 1, 416, 3, (8, 24, 32), False),
+    (900, 1056, 352, 12, 4, 0, 0, 2, (8, 64), True),
+    (1500, 992, 96, 5, 2, 1, 32, 40, (16, 72, 128), False),
+    (4200, 8224, 32, 3, 1, 0, 0, 1, (16,), False),
 ]
 
 
@@ -180,11 +185,12 @@ def test_down_matches_oracle(lora, case, wide, out_f32):
     assert d["B"].error_word() == 0
 
 
-@pytest.mark.parametrize("T", [5, 70, 900])
-def test_unrouted_pairs(lora, T):
+# tokens and ranks: one launch; three of gate/up; three of both
+@pytest.mark.parametrize("T,ranks", [(5, (8, 16)), (70, (8, 16)), (900, (8, 16)), (2000, (8, 128))])
+def test_unrouted_pairs(lora, T, ranks):
     """Pairs that no expert took: their rows of h stay as they were, and what
     lies in them reaches no output."""
-    d = make(lora, T, 96, 64, 6, 3, 1, 32, 3, (8, 16), gone=0.3, none=0.1, seed=T)
+    d = make(lora, T, 96, 64, 6, 3, 1, 32, 3, ranks, gone=0.3, none=0.1, seed=T)
     d["B"].h.fill_(3.0)
     h = run_gateup(lora, d)
     there = check_gateup(d, h)
@@ -196,33 +202,33 @@ def test_unrouted_pairs(lora, T):
     check_down(d, out)
 
 
-@pytest.mark.parametrize("T", [9, 800])
-def test_unrouted_tokens_without_shared_experts_give_base(lora, T):
-    d = make(lora, T, 64, 32, 4, 2, n=2, ranks=(8,), gone=1.0, out_f32=True, seed=1)
+@pytest.mark.parametrize("T,ranks", [(9, (8,)), (1200, (8,)), (4500, (128,))])
+def test_unrouted_tokens_without_shared_experts_give_base(lora, T, ranks):
+    d = make(lora, T, 64, 32, 4, 2, n=2, ranks=ranks, gone=1.0, out_f32=True, seed=1)
     assert torch.equal(run_down(lora, d), d["base"])
     d["B"].h.fill_(5.0)
     assert (run_gateup(lora, d) == 5.0).all()
 
 
-@pytest.mark.parametrize("T", [6, 1000])
+@pytest.mark.parametrize("T,rank", [(6, 8), (1000, 8), (3500, 128)])
 @pytest.mark.parametrize("n", [0, 3])
-def test_no_adapter_at_all(lora, T, n):
-    d = make(lora, T, 64, 32, 4, 2, 1, 64, n=max(n, 1), ranks=(8,), none=1.0, out_f32=True, seed=2)
+def test_no_adapter_at_all(lora, T, rank, n):
+    d = make(lora, T, 64, 32, 4, 2, 1, 64, n=max(n, 1), ranks=(rank,), none=1.0, out_f32=True, seed=2)
     if n == 0:
-        d["ad"] = lora.Adapters(0, 4, 64, 32, 1, 64, max_rank=8, device=DEV)
+        d["ad"] = lora.Adapters(0, 4, 64, 32, 1, 64, max_rank=rank, device=DEV)
         d["tad"] = torch.zeros(T, dtype=torch.int32, device=DEV)
     check_gateup(d, run_gateup(lora, d))
     assert torch.equal(run_down(lora, d), d["base"])
 
 
-@pytest.mark.parametrize("T", [8, 900])
-def test_unusable_entries_count_as_none_and_are_reported(lora, T):
-    d = make(lora, T, 64, 32, 3, 3, 0, 0, 1, (8, 16), none=0.0, seed=3)
+@pytest.mark.parametrize("T,ranks", [(8, (8, 16)), (900, (8, 16)), (3000, (8, 128))])
+def test_unusable_entries_count_as_none_and_are_reported(lora, T, ranks):
+    d = make(lora, T, 64, 32, 3, 3, 0, 0, 1, ranks, none=0.0, seed=3)
     a13, b13 = bf16(np.random.default_rng(0), 1, 16, 64), bf16(np.random.default_rng(0), 1, 64, 8)
     a2, b2 = bf16(np.random.default_rng(0), 1, 8, 32), bf16(np.random.default_rng(0), 1, 64, 8)
     d["ad"].load(0, a13, b13, a2, b2, first=1)
     d["up"][0][1] = d["dn"][0][1] = None
-    for change in (dict(N=32), dict(K=96), dict(rank=24), dict(rank=12), dict(rank=-8), dict(a=0), dict(b=0),
+    for change in (dict(N=32), dict(K=96), dict(rank=ranks[1] + 8), dict(rank=12), dict(rank=-8), dict(a=0), dict(b=0),
                    dict(a=a13.data_ptr() + 2)):
         for tag in ("13", "2"):
             d["ad"].load(0, a13, b13, a2, b2, first=1)
@@ -243,9 +249,9 @@ def test_unusable_entries_count_as_none_and_are_reported(lora, T):
     assert d["B"].error_word() == 0
 
 
-@pytest.mark.parametrize("T", [20, 900])
-def test_nan_and_inf_stay_in_their_rows(lora, T):
-    d = make(lora, T, 96, 64, 4, 2, 1, 64, 3, (8, 16), none=0.0, out_f32=True, seed=4)
+@pytest.mark.parametrize("T,ranks", [(20, (8, 16)), (900, (8, 16)), (2000, (8, 128))])
+def test_nan_and_inf_stay_in_their_rows(lora, T, ranks):
+    d = make(lora, T, 96, 64, 4, 2, 1, 64, 3, ranks, none=0.0, out_f32=True, seed=4)
     keep_h, keep_o = f64(run_gateup(lora, d)), f64(run_down(lora, d))
     d["x"][2, 9] = float("nan")
     d["x"][5, 1] = float("inf")
@@ -292,11 +298,11 @@ def test_down_in_place(lora):
     assert torch.equal(d["base"], want)
 
 
-@pytest.mark.parametrize("T", [30, 800])
-def test_same_results_every_time_on_streams_and_in_graphs(lora, T):
-    d = make(lora, T, 128, 64, 6, 3, 1, 64, 4, (8, 16), seed=7)
+@pytest.mark.parametrize("T,ranks", [(30, (8, 16)), (800, (8, 16)), (2000, (8, 128))])
+def test_same_results_every_time_on_streams_and_in_graphs(lora, T, ranks):
+    d = make(lora, T, 128, 64, 6, 3, 1, 64, 4, ranks, seed=7)
     h, o = run_gateup(lora, d).clone(), run_down(lora, d).clone()
-    e = make(lora, T, 128, 64, 6, 3, 1, 64, 4, (8, 16), seed=7)
+    e = make(lora, T, 128, 64, 6, 3, 1, 64, 4, ranks, seed=7)
     a, b = torch.cuda.Stream(), torch.cuda.Stream()
     torch.cuda.synchronize()
     for _ in range(3):                                # two at once, with buffers each
@@ -528,10 +534,10 @@ def test_layer_in_a_graph(lora):
         assert torch.equal(got, go())
 
 
-@pytest.mark.parametrize("T", [6, 700, 2100])
-def test_a_token_that_lists_an_expert_twice(lora, T):
+@pytest.mark.parametrize("T,ranks", [(6, (8, 16)), (700, (8, 16)), (2100, (8, 16)), (2100, (16, 128))])
+def test_a_token_that_lists_an_expert_twice(lora, T, ranks):
     """Both of its rows count, alone and between others of their expert."""
-    d = make(lora, T, 64, 32, 4, 3, 0, 0, 2, (8, 16), out_f32=True, runs=True, none=0.0, seed=12)
+    d = make(lora, T, 64, 32, 4, 3, 0, 0, 2, ranks, out_f32=True, runs=True, none=0.0, seed=12)
     rng = np.random.default_rng(12)
     ids = d["ids"].copy()
     ids[::2, 1] = ids[::2, 0]
@@ -544,3 +550,11 @@ def test_a_token_that_lists_an_expert_twice(lora, T):
     d["t"] = [dev(d[x]) for x in ("ids", "off", "sp", "pos")]
     check_gateup(d, run_gateup(lora, d))
     check_down(d, run_down(lora, d))
+
+
+def test_more_experts_than_the_sums_of_a_block_hold(lora):
+    """Shared experts beside 1024 routed ones: many rows, down in one launch."""
+    d = make(lora, 40, 256, 32, 1024, 2, 70, 32, 1, (128,), none=0.0, seed=13)
+    check_gateup(d, run_gateup(lora, d))
+    check_down(d, run_down(lora, d))
+    assert d["B"].error_word() == 0
