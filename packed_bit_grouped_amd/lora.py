@@ -32,6 +32,10 @@ from . import mx as _mx
 from . import router as _router
 from .mx import _BF16, _F32, _I32, _empty, _gate, _gpu, _launch, _side, _used_on, _want
 
+_DESC = np.dtype([("a", np.uint64), ("b", np.uint64), ("rank", np.int32), ("scale", np.float32),
+                  ("N", np.int32), ("K", np.int32)])   # struct moe_lora
+assert _DESC.itemsize == ctypes.sizeof(L.LoraDesc)
+
 
 class Adapters:
     """Tables of n adapters of a layer with E routed experts of H x I and
@@ -56,11 +60,14 @@ class Adapters:
                       for tag in self._host}
         self._held = {}
 
+    def _entries(self, tag, slot, first, count):
+        lo = slot * self.per + first
+        return np.frombuffer(self._host[tag], dtype=_DESC)[lo:lo + count]
+
     def _put(self, tag, slot, first, count, stream):
         size = ctypes.sizeof(L.LoraDesc)
         lo = (slot * self.per + first) * size
-        raw = np.frombuffer(self._host[tag], dtype=np.uint8)[lo:lo + count * size]
-        src = torch.from_numpy(raw.copy())
+        src = torch.from_numpy(self._entries(tag, slot, first, count).copy().view(np.uint8))
         side = _side(self._dev, stream) if self._dev >= 0 else None
         if side is None:
             self.table[tag][lo:lo + count * size].copy_(src)
@@ -107,11 +114,12 @@ class Adapters:
             _launch("moe_lora_tile", self._dev, stream, a.data_ptr(), m, a.shape[1], K, 0, ta.data_ptr())
             _launch("moe_lora_tile", self._dev, stream, b.data_ptr(), m, N, rank, 1, tb.data_ptr())
             _used_on(side, a, b)
-            for i in range(m):
-                self._host[tag][slot * self.per + first + i] = L.LoraDesc(
-                    ta.data_ptr() + i * rows * K * 2, tb.data_ptr() + i * N * rank * 2, rank,
-                    scale, N, K)
-                self._held[tag, slot, first + i] = (ta, tb)
+            d = self._entries(tag, slot, first, m)
+            i = np.arange(m, dtype=np.uint64)
+            d["a"] = ta.data_ptr() + i * np.uint64(rows * K * 2)
+            d["b"] = tb.data_ptr() + i * np.uint64(N * rank * 2)
+            d["rank"], d["scale"], d["N"], d["K"] = rank, scale, N, K
+            self._held.update({(tag, slot, first + i): (ta, tb) for i in range(m)})
             self._put(tag, slot, first, m, stream)
 
     def unload(self, slot, stream=None):
@@ -119,8 +127,8 @@ class Adapters:
         if not 0 <= slot < self.n:
             raise ValueError(f"slot: {slot}, expected one of {self.n}")
         for tag in self._host:
+            self._entries(tag, slot, 0, self.per)[:] = np.zeros((), _DESC)
             for e in range(self.per):
-                self._host[tag][slot * self.per + e] = L.LoraDesc()
                 self._held.pop((tag, slot, e), None)
             self._put(tag, slot, 0, self.per, stream)
 
