@@ -253,15 +253,25 @@ def run_layer(bank, M, adapters, B, x, adapter, logits, renormalize=1, routing=N
     router.route_scored.  The routing's results are in M.ids, M.w and M's tables.
     flags: MOE_PATH_* of the int4/int2 projections."""
     T, H, I, E, k = M.T, M.H, M.I, M.E, M.k
-    if (T, H, I, E, k, M.n_shared) != (B.T, B.H, B.I, B.E, B.k, B.n_shared):
+    if (T, H, I, E, k, M.n_shared) != (B.T, B.H, B.I, B.E, B.k, B.n_shared) or M.ld_h != B.ld_h or (
+            M.n_shared and M.I_shared != B.I_shared):
         raise ValueError("the shared projections' buffers and the adapters' are for different layers")
     wide = isinstance(M, _w4.LayerBuffers) and M.act == L.MOE_A8
     if wide != bool(B.h_flags):
         raise ValueError("h_f32: fp32 h goes with 8-bit activations, bf16 h with the others")
+    if flags and isinstance(M, _mx.MxBuffers):
+        raise ValueError("flags: MOE_PATH_* are of the int4/int2 projections")
+    if M.ids.device != B.device:
+        raise ValueError(f"the shared projections' buffers are on {M.ids.device}, the adapters' on {B.device}")
     if T == 0:
         return B.out
+    # before the first launch: what the calls read
     dev = B._dev
     _want("logits", logits, _F32, (T, E), dev)
+    _want("x", x, _BF16, (T, H), dev)
+    _want("adapter", adapter, _I32, (T,), dev)
+    _gate(shared_gate, B)
+    _table(adapters, "13", B)
     if stream is not None and not isinstance(stream, int):
         stream = _mx._here(dev, stream).cuda_stream
     if dev != torch.cuda.current_device():

@@ -534,6 +534,33 @@ def test_layer_in_a_graph(lora):
         assert torch.equal(got, go())
 
 
+def test_layer_refuses_what_does_not_fit_before_it_runs(lora):
+    T, H, I, E, k, Is = 6, 256, 128, 8, 2, 128
+    dl = w4_layer(T, H, I, E, k, 1, Is, "a16", 77)
+    M = dl.buffers("a16", 16)
+    ad = lora.Adapters(2, E, H, I, 1, Is, max_rank=8, device=DEV)
+    B = lora.LoraBuffers(T, H, I, E, k, 1, Is, 8, device=DEV)
+    x, tad = torch.zeros(T, H, dtype=torch.bfloat16, device=DEV), torch.zeros(T, dtype=torch.int32, device=DEV)
+    M.ids.fill_(-7)
+    go = lambda bank=dl.bank, M=M, ad=ad, B=B, x=x, tad=tad, logits=dl.logits, **kw: lora.run_layer(
+        bank, M, ad, B, x, tad, logits, **kw)
+    for kw, word in ((dict(x=x[:3]), "x"), (dict(x=x.float()), "x"), (dict(tad=tad[:2]), "adapter"),
+                     (dict(tad=tad.long()), "adapter"), (dict(logits=dl.logits[:, :4]), "logits"),
+                     (dict(shared_gate=torch.zeros(T, 2, device=DEV)), "shared_gate"),
+                     (dict(B=lora.LoraBuffers(T, H, I, E, k, 1, 2 * Is, 8, device=DEV)), "different layers"),
+                     (dict(B=lora.LoraBuffers(T, H, I, E, k, 1, 64, 8, device=DEV)), "different layers"),
+                     (dict(B=lora.LoraBuffers(T, H, I, E, k, 1, Is, 8, h_f32=True, device=DEV)), "h_f32"),
+                     (dict(ad=lora.Adapters(2, E, H, 64, 1, Is, max_rank=8, device=DEV)), "adapters"),
+                     (dict(ad=lora.Adapters(2, E, H, I, 1, Is, max_rank=16, device=DEV)), "ranks")):
+        with pytest.raises((ValueError, TypeError), match=word):
+            go(**kw)
+    bank, X = mx_layer(T, H, I, E, k, 1, Is, "a16", 1)
+    with pytest.raises(ValueError, match="flags"):
+        go(bank=bank, M=X, flags=1)
+    torch.cuda.synchronize()
+    assert (M.ids == -7).all()
+
+
 @pytest.mark.parametrize("T,ranks", [(6, (8, 16)), (700, (8, 16)), (2100, (8, 16)), (2100, (16, 128))])
 def test_a_token_that_lists_an_expert_twice(lora, T, ranks):
     """Both of its rows count, alone and between others of their expert."""
