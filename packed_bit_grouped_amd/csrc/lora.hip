@@ -1136,16 +1136,18 @@ __global__ __launch_bounds__(64 * kDownWaves) void lora_down_small_kernel(LoraAr
 // block's units (make_plan) and adds each unit's products B v to its tokens'.  A
 // wave owns 16 of the columns of all the tokens, so no two waves meet in a sum,
 // and a unit holds a token once, so no two lanes do: plain reads and writes in a
-// wave's own order, the same result every time.  4096 tokens, H 2048: 96 us, 15 of
-// them base and out; LDS additions without return were five times slower (500 us),
+// wave's own order, the same result every time.  4096 tokens, H 2048: 88 us, 17 of
+// them base, out and the units on their way; LDS additions without return were five times slower (500 us),
 // sums by tokens without any reuse of B four times (381), and rows of y through
-// memory as in the shared projection would be 600 MB.  What bounds it is none of
-// the rates but the way of a unit through a wave, 200 ns; neither 128 columns of 256
-// tokens (101 to 128 us), waves that share columns and split the adapters (104),
-// products over 16 ranks with 8-byte loads (119) nor deeper batches (116) shorten it.
+// memory as in the shared projection would be 600 MB.  What bounds it is no rate but
+// the way of a unit through a wave, about 200 ns: without B's loads, without v's or
+// without the sums' reads and writes it was 3 to 6 us shorter.  128 columns of 256
+// tokens (101 to 128 us), waves that divide the adapters (104), v through LDS once
+// for all waves (102), products over 16 ranks with 8-byte loads (119) and batches of
+// 8 units (99) were slower.
 // A token's 64 sums are 16 chunks of 4; chunk q lies at q ^ (token % 16), so that
 // the 16 tokens of a unit spread over the banks.
-constexpr int kUnitsAtOnce = 96;   // in LDS
+constexpr int kUnitsAtOnce = 128;  // in LDS; a segment of a prompt has about 75 (segments of 8 windows 96 us, 16 88, 32 95)
 constexpr int kUnitsAhead = 16;    // and behind them some that do nothing: what the loop reads past its end
 
 template <int KB>   // steps of 32 ranks

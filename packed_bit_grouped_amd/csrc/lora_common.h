@@ -14,7 +14,7 @@ constexpr int kLoraManyRows = 2048;   // gate/up: up to which it may be
 constexpr int kLoraPlanMaxE = 1088;   // routed and shared experts of a plan
 constexpr int kLoraSlab = 64;         // columns of a workgroup of the accumulating kernel
 constexpr int kLoraMaxBlock = 512;    // and tokens
-constexpr int kLoraSegment = 8;       // windows of 64 rows that it takes at a time
+constexpr int kLoraSegment = 16;      // windows of 64 rows that it takes at a time
 
 // A unit: up to 16 rows of one (adapter, expert) with tokens of one block; v: the
 // byte of parts where the first one's lies, the others' behind it.
