@@ -30,8 +30,8 @@
 //
 // What the calls measured (H 2048, I 512, 256 experts and a shared one, 8 a token,
 // rank 16; in a graph): one token gate/up 9.7 us, down 7.9; 64 tokens over 32
-// adapters 26 and 14.6 (the matrices at 3.5 and 3.1 TB/s); 4096 tokens over 4
-// adapters 111 (3.4 TB/s of what has to be moved) and 128.
+// adapters 26 and 14 (the matrices at 3.5 and 3.2 TB/s); 4096 tokens over 4
+// adapters 110 (3.4 TB/s of what has to be moved) and 115 (1.5).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -1407,11 +1407,12 @@ hipError_t launch_accumulate(const LoraArgs& a, hipStream_t st) {
 // 1440 rows 87 against 62, 2052 rows 109 against 83.
 //
 // down: one reads a row's matrices from the cache at 4.6 TB/s, whatever they share;
-// three cost about 40 us and 0.12 for each unit of a block of tokens.  32 adapters
-// on 257 experts: 4104 rows 103 us in one, 148 in three, 18432 rows 348 and 266,
-// 36864 rows 662 and 305; 4 adapters: 4104 rows 84 and 94, 8208 rows 138 and 110,
-// 36864 rows 590 and 126; on 33 experts, rank 64: 576 rows 38 and 68, 1026 rows 65
-// and 59, 4104 rows 157 and 53.
+// three cost about 35 us and 0.2 for each 32 ranks of a unit of a block of tokens
+// (a block has the adapters of its share of the tokens: a request's are neighbours).
+// 32 adapters on 257 experts: 4104 rows 102 us in one, 146 in three, 11700 rows 235
+// and 302, 18432 rows 348 and 261, 36864 rows 662 and 302; 4 adapters: 4104 rows 83
+// and 90, 8208 rows 138 and 106, 36864 rows 590 and 115; on 33 experts, rank 64: 576
+// rows 37 and 67, 1440 rows 71 and 53, 4104 rows 157 and 52.
 void lora_choose(LoraArgs& a, bool most) {
   a.block = a.n_blocks = a.win = 0;
   a.large = a.R > kLoraFewRows;
@@ -1435,10 +1436,12 @@ void lora_choose(LoraArgs& a, bool most) {
   // offsets into v: 31 bits
   if ((long long)a.n_blocks * a.win * 64 * a.max_rank * 6 >= (1LL << 31)) a.large = false;
   if (most || !a.large) return;
-  const double pairs = experts * std::min(a.n, std::min(a.T, a.block));
+  const double adapters = std::ceil((double)a.n * std::min(a.T, a.block) / a.T);
+  const double pairs = experts * std::min(adapters, (double)a.block);
   const double units = pairs * (1.0 - std::exp(-rows / std::max(pairs, 1.0))) + rows / 16;
   const double one = 2.0 * a.R * a.max_rank * ((double)a.H + a.I) / 4.6e6;
-  if (a.n == 0 || one < 40.0 + 0.12 * std::min(units, 1200.0)) a.large = false;
+  const double rounds = std::max(1.0, (double)a.n_blocks * n_slabs / 256);
+  if (a.n == 0 || one < 35.0 + 0.2 * ((a.max_rank + 31) / 32) * rounds * units) a.large = false;
 }
 
 hipError_t launch_lora_tile(const uint16_t* src, int n, int rows, int cols, int is_b, uint16_t* dst,

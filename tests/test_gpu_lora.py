@@ -561,7 +561,7 @@ def test_layer_refuses_what_does_not_fit_before_it_runs(lora):
     assert (M.ids == -7).all()
 
 
-@pytest.mark.parametrize("T,ranks", [(6, (8, 16)), (700, (8, 16)), (2100, (8, 16)), (2100, (16, 128))])
+@pytest.mark.parametrize("T,ranks", [(6, (8, 16)), (700, (8, 16)), (2100, (8, 16)), (4200, (16, 128))])
 def test_a_token_that_lists_an_expert_twice(lora, T, ranks):
     """Both of its rows count, alone and between others of their expert."""
     d = make(lora, T, 64, 32, 4, 3, 0, 0, 2, ranks, out_f32=True, runs=True, none=0.0, seed=12)
