@@ -151,7 +151,7 @@ __device__ __forceinline__ Pair pair_of(const LoraArgs& a, int key, int N, int K
   const moe_lora d = a.table[key];
   if (d.rank == 0) return p;
   if (!entry_ok(a, d, N, K)) {
-    if (threadIdx.x == 0) atomicOr(a.err, 1);
+    atomicOr(a.err, 1);
     return p;
   }
   p.a = d.a;
@@ -1028,7 +1028,9 @@ __global__ __launch_bounds__(64 * kDownWaves) void lora_down_small_kernel(LoraAr
     if ((unsigned)d >= (unsigned)a.n) break;   // after the loads: one trip with d's
     if (c0) __syncthreads();                   // the last pass is done
     if (tid < m) {
-      const bool ok = (unsigned)row < (unsigned)a.R && (unsigned)e < (unsigned)(a.E + a.n_shared);
+      // a routed choice has an expert and a row among the pairs
+      const bool ok = (unsigned)row < (unsigned)(c0 + tid < a.k ? a.P : a.R) &&
+                      (unsigned)e < (unsigned)(c0 + tid < a.k ? a.E : a.E + a.n_shared);
       const int key = ok ? d * (a.E + a.n_shared) + e : kNoRow;
       pair[tid] = pair_of(a, key, a.H, ok ? width_of(a, key) : 0);
       row_of[tid] = ok ? row : 0;

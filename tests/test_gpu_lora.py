@@ -249,6 +249,21 @@ def test_unusable_entries_count_as_none_and_are_reported(lora, T, ranks):
     assert d["B"].error_word() == 0
 
 
+@pytest.mark.parametrize("e", range(4))
+def test_an_unusable_entry_is_reported_whichever_choice_meets_it(lora, e):
+    d = make(lora, 1, 64, 32, 3, 3, 1, 32, 1, (8,), none=0.0, seed=14)
+    for tag, run in (("13", run_gateup), ("2", run_down)):
+        rng = np.random.default_rng(1)
+        d["ad"].load(0, bf16(rng, 1, 16, 64), bf16(rng, 1, 64, 8), bf16(rng, 1, 8, 32), bf16(rng, 1, 64, 8), first=e)
+        d["B"].ws[:4].zero_()
+        run(lora, d)
+        assert d["B"].error_word() == 0
+        d["ad"]._host[tag][e].rank = 24
+        d["ad"]._put(tag, 0, e, 1, None)
+        run(lora, d)
+        assert d["B"].error_word() == 1
+
+
 @pytest.mark.parametrize("T,ranks", [(20, (8, 16)), (900, (8, 16)), (2000, (8, 128))])
 def test_nan_and_inf_stay_in_their_rows(lora, T, ranks):
     d = make(lora, T, 96, 64, 4, 2, 1, 64, 3, ranks, none=0.0, out_f32=True, seed=4)
