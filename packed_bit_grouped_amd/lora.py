@@ -35,6 +35,7 @@ from .mx import _BF16, _F32, _I32, _empty, _gate, _gpu, _launch, _side, _used_on
 _DESC = np.dtype([("a", np.uint64), ("b", np.uint64), ("rank", np.int32), ("scale", np.float32),
                   ("N", np.int32), ("K", np.int32)])   # struct moe_lora
 assert _DESC.itemsize == ctypes.sizeof(L.LoraDesc)
+_TILE_M = 4096   # of a sort whose tiles nobody reads: as few as there can be
 
 
 class Adapters:
@@ -134,11 +135,15 @@ class Adapters:
 
 
 class LoraBuffers:
-    """Every per-step buffer of the adapters of one layer shape, allocated once.
-    h_f32: h in fp32 (layers with 8-bit activations), else bf16."""
+    """Every per-step buffer of the adapters of one layer shape, allocated once,
+    on the stream that is current then (other streams wait for it).
+    h_f32: h in fp32 (layers with 8-bit activations), else bf16.  layer: with
+    what run_layer keeps between the calls: the shared projections' sums gu fp32
+    [R][2 * ld_h] and base fp32 [T][H], and the sort's tile list; False for
+    callers of gateup_silu and down_combine that bring their own."""
 
     def __init__(self, T, H, I, E, k, n_shared=0, I_shared=0, max_rank=16, h_f32=False,
-                 out_f32=False, device="cuda"):
+                 out_f32=False, device="cuda", layer=True):
         self.T, self.H, self.I, self.E, self.k = T, H, I, E, k
         self.n_shared, self.I_shared, self.max_rank = n_shared, I_shared, max_rank
         self.P = T * k
@@ -161,29 +166,14 @@ class LoraBuffers:
         self.out = torch.empty((T, H), device=dev, dtype=torch.float32 if out_f32 else torch.bfloat16)
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=dev)
         self.ws[:256].zero_()
-        self._gu = self._base = self._tiles = None
-
-    @property
-    def gu(self):
-        """fp32 [R][2 * ld_h] for the shared gate/up sums (made when first asked for)."""
-        if self._gu is None:
-            self._gu = torch.zeros((self.R, 2 * self.ld_h), dtype=torch.float32, device=self.device)
-        return self._gu
-
-    @property
-    def base(self):
-        """fp32 [T][H] for the shared down projection's sum (made when first asked for)."""
-        if self._base is None:
-            self._base = torch.empty((self.T, self.H), dtype=torch.float32, device=self.device)
-        return self._base
-
-    def tiles(self, tile_m):
-        """The sort's tile list and count, where the projections do not bring one."""
-        if self._tiles is None:
-            m = max(L.moe_permute_max_tiles(self.T, self.k, self.E, tile_m), 1)
-            self._tiles = (torch.empty((m, 4), dtype=torch.int32, device=self.device),
-                           torch.zeros(1, dtype=torch.int32, device=self.device))
-        return self._tiles
+        self.gu = self.base = self.tiles = self.n_tiles = None
+        if layer:
+            self.gu = torch.zeros((self.R, 2 * self.ld_h), dtype=torch.float32, device=dev)
+            self.base = torch.empty((T, H), dtype=torch.float32, device=dev)
+            # for projections that bring no tile list of their own
+            m = max(L.moe_permute_max_tiles(T, k, E, _TILE_M), 1)
+            self.tiles = torch.empty((m, 4), dtype=torch.int32, device=dev)
+            self.n_tiles = torch.zeros(1, dtype=torch.int32, device=dev)
 
     def error_word(self) -> int:
         return int(self.ws[:4].view(torch.int32).item())
@@ -263,6 +253,8 @@ def run_layer(bank, M, adapters, B, x, adapter, logits, renormalize=1, routing=N
         raise ValueError("flags: MOE_PATH_* are of the int4/int2 projections")
     if M.ids.device != B.device:
         raise ValueError(f"the shared projections' buffers are on {M.ids.device}, the adapters' on {B.device}")
+    if B.gu is None:
+        raise ValueError("the adapters' buffers were made with layer=False")
     if T == 0:
         return B.out
     # before the first launch: what the calls read
@@ -285,8 +277,7 @@ def run_layer(bank, M, adapters, B, x, adapter, logits, renormalize=1, routing=N
     else:
         _router.route_scored(logits, k, ids=M.ids, w=M.w, stream=stream, **routing)
     if isinstance(M, _mx.MxBuffers):
-        tile_m = 4096
-        tiles, n_tiles = B.tiles(tile_m)
+        tile_m, tiles, n_tiles = _TILE_M, B.tiles, B.n_tiles
     else:
         tile_m, tiles, n_tiles = M.tile_m, M.tiles, M.n_tiles
     L.moe_permute(M.ids, T, k, E, tile_m, M.counts, M.offsets, M.sorted_pair, M.pair_pos, tiles,

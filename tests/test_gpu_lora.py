@@ -600,3 +600,33 @@ def test_more_experts_than_the_sums_of_a_block_hold(lora):
     check_gateup(d, run_gateup(lora, d))
     check_down(d, run_down(lora, d))
     assert d["B"].error_word() == 0
+
+
+@pytest.mark.parametrize("kind", ["mx", "w4"])
+def test_layer_on_another_stream_with_fresh_buffers(lora, kind):
+    """The first step on a stream of its own, while the current one is busy: nothing is
+    made in the step, and the result is the one of the current stream."""
+    T, H, I, E, k, Is = 300, 256, 128, 8, 2, 128
+    if kind == "mx":
+        bank, M = mx_layer(T, H, I, E, k, 1, Is, "a16", 21)
+        x, logits = torch.randn(T, H, device=DEV).bfloat16(), torch.randn(T, E, device=DEV)
+    else:
+        dl = w4_layer(T, H, I, E, k, 1, Is, "a16", 321)
+        bank, M, x, logits = dl.bank, dl.buffers("a16"), dl.x, dl.logits
+    d = make(lora, T, H, I, E, k, 1, Is, 3, (8, 16), seed=22)
+    sized = (T, H, I, E, k, 1, Is, 16)
+    want = lora.run_layer(bank, M, d["ad"], lora.LoraBuffers(*sized, device=DEV), x, d["tad"], logits).clone()
+    a, side = torch.randn(4096, 4096, device=DEV), torch.cuda.Stream()
+    for _ in range(3):
+        B = lora.LoraBuffers(*sized, device=DEV)
+        side.wait_stream(torch.cuda.current_stream())
+        for _ in range(5):
+            a @ a                                     # the current stream is busy
+        before = torch.cuda.memory_stats()["allocation.all.allocated"]
+        out = lora.run_layer(bank, M, d["ad"], B, x, d["tad"], logits, stream=side)
+        assert torch.cuda.memory_stats()["allocation.all.allocated"] == before
+        side.synchronize()
+        assert torch.equal(out, want) and B.error_word() == 0
+        torch.cuda.synchronize()
+    with pytest.raises(ValueError, match="layer=False"):
+        lora.run_layer(bank, M, d["ad"], lora.LoraBuffers(*sized, device=DEV, layer=False), x, d["tad"], logits)

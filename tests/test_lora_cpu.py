@@ -178,3 +178,17 @@ def test_tiling_refusals():
     for kw in (dict(), dict(rows=8), dict(is_b=1), dict(is_b=1, cols=8)):
         assert tile(**kw) == L.MOE_E_DEVICE, kw
     assert tile(n=0, src=None, dst=None) == L.MOE_OK
+
+
+def test_layer_buffers_are_all_there_from_the_start():
+    """Nothing is made in a step: a step's stream is not the one that memory would come from."""
+    torch = pytest.importorskip("torch")
+    from packed_bit_grouped_amd import lora
+    B = lora.LoraBuffers(5, 64, 32, 8, 2, 1, 96, device="cpu")
+    held = {name: id(v) for name, v in vars(B).items() if isinstance(v, torch.Tensor)}
+    assert {"h", "out", "ws", "gu", "base", "tiles", "n_tiles"} <= set(held)
+    assert B.gu.shape == (15, 192) and B.base.shape == (5, 64)
+    assert B.gu.dtype == B.base.dtype == torch.float32 and B.tiles.dtype == torch.int32
+    assert len(B.tiles) == L.moe_permute_max_tiles(5, 2, 8, 4096)
+    assert {name: id(getattr(B, name)) for name in held} == held
+    assert lora.LoraBuffers(5, 64, 32, 8, 2, 1, 96, device="cpu", layer=False).gu is None
