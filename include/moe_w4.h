@@ -60,7 +60,7 @@
 extern "C" {
 #endif
 
-#define MOE_W4_ABI_VERSION 7
+#define MOE_W4_ABI_VERSION 8
 
 /* Version of the compiled library.  The Python binding refuses to load a
  * library whose version differs from the header it was written for. */
@@ -807,6 +807,13 @@ typedef struct moe_lora {
  * Calls that overlap in time need a workspace each. */
 size_t moe_lora_workspace_bytes(int T, int H, int I, int E, int k, int n_shared, int I_shared,
                                 int max_rank);
+
+/* How the gate/up (down = 0) or the down call (1) of these sizes runs (host
+ * only): 0, in one launch; else in three, and gate/up sorts that many rows at a
+ * time, down keeps the sums of that many tokens together.  A status below 0 for
+ * sizes that they refuse. */
+int moe_lora_block(int T, int H, int I, int E, int k, int n_shared, int I_shared, int n_adapters,
+                   int max_rank, int down);
 
 /* ---------------------------------------------------------------------
  * moe_lora_gateup_silu -- h of every routed pair and shared-expert token from

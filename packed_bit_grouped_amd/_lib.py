@@ -14,7 +14,7 @@ from typing import Optional
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe_w4.so")
-ABI_VERSION = 7
+ABI_VERSION = 8
 
 MOE_OK, MOE_E_INVAL, MOE_E_UNSUPPORTED, MOE_E_DEVICE, MOE_E_WORKSPACE = 0, -1, -2, -3, -4
 MOE_A16, MOE_A8, MOE_A4 = 0, 1, 2
@@ -131,6 +131,7 @@ _SIGS = {
                                  c_int, c_int, c_float, c_void_p, c_void_p, c_void_p]),
     "moe_lora_tile": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_void_p]),
     "moe_lora_workspace_bytes": (c_size_t, [c_int] * 8),
+    "moe_lora_block": (c_int, [c_int] * 10),
     "moe_lora_gateup_silu": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
                                      c_void_p, c_int, c_int, c_void_p, c_void_p, c_void_p,
                                      c_void_p, c_void_p, c_void_p, c_size_t, c_int, c_void_p]),
@@ -469,6 +470,10 @@ def moe_lora_tile(src, n, rows, cols, is_b, dst, stream=None, check=True):
 
 def moe_lora_workspace_bytes(T, H, I, E, k, n_shared=0, I_shared=0, max_rank=16) -> int:
     return load().moe_lora_workspace_bytes(T, H, I, E, k, n_shared, I_shared, max_rank)
+
+
+def moe_lora_block(T, H, I, E, k, n_shared, I_shared, n_adapters, max_rank, down) -> int:
+    return load().moe_lora_block(T, H, I, E, k, n_shared, I_shared, n_adapters, max_rank, down)
 
 
 def moe_lora_gateup_silu(x, T, H, I, E, k, n_shared, I_shared, adapter, n_adapters, max_rank,

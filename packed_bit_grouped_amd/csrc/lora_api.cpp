@@ -88,6 +88,17 @@ size_t moe_lora_workspace_bytes(int T, int H, int I, int E, int k, int n_shared,
   return workspace_bytes(T, H, I, E, k, n_shared, I_shared, max_rank);
 }
 
+int moe_lora_block(int T, int H, int I, int E, int k, int n_shared, int I_shared, int n_adapters,
+                   int max_rank, int down) {
+  const moe_status st = check_shape(T, H, I, E, k, n_shared, I_shared, n_adapters, max_rank);
+  if (st != MOE_OK) return st;
+  if (down != 0 && down != 1) return MOE_E_INVAL;
+  LoraArgs a = args_of(T, H, I, E, k, n_shared, I_shared, nullptr, n_adapters, max_rank, nullptr,
+                       nullptr, nullptr, nullptr, down ? 1 : 2);
+  lora_choose(a, false);
+  return !a.large ? 0 : down ? a.block : kLoraWindow;
+}
+
 moe_status moe_lora_tile(const uint16_t* src, int n, int rows, int cols, int is_b, uint16_t* dst,
                          void* stream) {
   if (n < 0 || rows <= 0 || cols <= 0 || (is_b != 0 && is_b != 1)) return MOE_E_INVAL;

@@ -192,3 +192,17 @@ def test_layer_buffers_are_all_there_from_the_start():
     assert len(B.tiles) == L.moe_permute_max_tiles(5, 2, 8, 4096)
     assert {name: id(getattr(B, name)) for name in held} == held
     assert lora.LoraBuffers(5, 64, 32, 8, 2, 1, 96, device="cpu", layer=False).gu is None
+
+
+def test_how_a_call_runs():
+    """One launch of few rows, three of many; as many tokens a block as leave a
+    workgroup to each compute unit."""
+    block = lambda T, H=2048, I=512, E=256, k=8, s=1, n=4, rank=16, down=1: L.moe_lora_block(
+        T, H, I, E, k, s, I if s else 0, n, rank, down)
+    assert block(0) == block(1) == block(64) == 0 and block(1, down=0) == block(64, down=0) == 0
+    assert block(4096) == 512 and block(4096, down=0) == 256
+    assert block(4096, H=1024) == 256 and block(1100, H=2080) == 128 and block(2000, H=96, E=8) == 64
+    assert block(4096, n=0) == 0 and block(4096, E=1024, s=65) == 0      # more experts than a plan holds
+    assert block(4096, E=1024, s=65, down=0) == 256
+    assert block(4, H=48) == L.MOE_E_UNSUPPORTED and block(-1) == L.MOE_E_INVAL
+    assert block(4, rank=12) == L.MOE_E_INVAL and block(4, down=2) == L.MOE_E_INVAL
