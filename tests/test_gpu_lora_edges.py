@@ -1,12 +1,13 @@
 """The adapters' calls where their other tests do not go: the sums of a block of
-tokens over several segments of windows and more units than are taken at a time."""
+tokens over several segments of windows and more units than are taken at a time;
+fp32 operands to their last bit."""
 import numpy as np
 import pytest
 
 from packed_bit_grouped_amd import _lib as L
 
 torch = pytest.importorskip("torch")
-from test_gpu_lora import check_down, make, run_down  # noqa: E402
+from test_gpu_lora import DEV, check_down, dev, f64, make, run_down, run_gateup, tables  # noqa: E402,F401
 
 pytestmark = pytest.mark.gpu
 
@@ -93,3 +94,107 @@ def test_segments_without_units_between_others(lora, silent, empty):
     assert [i for i, u in enumerate(units[0]) if u == 0] == list(empty) and len(units[0]) == 5
     check_down(d, run_down(lora, d))
     assert d["B"].error_word() == 0
+
+
+# ---------------------------------------------------------------------------
+# Fp32 operands go into the matrix cores as three parts of 8 bits.  With matrices
+# whose rows hold powers of two a result has the 24 bits of one operand, and every
+# partial sum on the way is a run of its bits: nothing may be rounded, so the
+# calls have to be exact.  (A bound of worst-case sums of K products is above what
+# a lost third part changes.)
+
+
+def power(rng, *shape):
+    return 2.0 ** rng.integers(-3, 4, shape) * rng.choice([-1.0, 1.0], shape)
+
+
+def one_entry_rows(rng, n, K):
+    """[n][K] with a power of two in one column of each row; the columns, the entries."""
+    col, val = rng.integers(0, K, n), power(rng, n)
+    m = np.zeros((n, K))
+    m[np.arange(n), col] = val
+    return m, col, val
+
+
+def bits24(rng, *shape):
+    """Numbers of [1, 2) with 24 bits, the last one set."""
+    return 1.0 + (rng.integers(0, 1 << 22, shape) * 2 + 1) * 2.0 ** -23
+
+
+def two_parts(f):
+    """f without its last 8 bits."""
+    return (f.astype(np.float32).view(np.uint32) & 0xFFFFFF00).view(np.float32)
+
+
+def bf(a):
+    t = torch.from_numpy(np.ascontiguousarray(a).astype(np.float32)).bfloat16()
+    assert np.array_equal(t.double().numpy(), a)
+    return t.to(DEV)
+
+
+@pytest.mark.parametrize("T,H,I,rank,many", [
+    (1, 64, 32, 8, False), (40, 416, 96, 24, False), (300, 64, 64, 128, False), (9, 2048, 512, 40, False),
+    (20000, 512, 64, 16, True), (4000, 544, 96, 72, True), (4000, 512, 64, 128, True)])
+def test_down_keeps_every_bit_of_h_and_v(lora, T, H, I, rank, many):
+    rng = np.random.default_rng(T + rank)
+    E, scale = 3, 0.25
+    ids, off, sp, pos = tables(rng, T, 1, E)
+    assert (L.moe_lora_block(T, H, I, E, 1, 0, 0, 1, rank, 1) > 0) == many
+    ad, a2, b2 = lora.Adapters(1, E, H, I, max_rank=rank, device=DEV), [], []
+    for e in range(E):
+        a2.append(one_entry_rows(rng, rank, I))
+        b2.append(one_entry_rows(rng, H, rank))
+    ad.load(0, a2=bf(np.stack([m for m, _, _ in a2])), b2=bf(np.stack([m for m, _, _ in b2])), scale=scale)
+    h, w = bits24(rng, T, I) * power(rng, T, I), power(rng, T, 1)
+    want = np.zeros((T, H))
+    for t in range(T):
+        e = ids[t, 0]
+        v = scale * a2[e][2] * h[pos[t], a2[e][1]]
+        want[t] = w[t, 0] * b2[e][2] * v[b2[e][1]]
+    assert (two_parts(want) != want).all()
+    B = lora.LoraBuffers(T, H, I, E, 1, max_rank=rank, h_f32=True, out_f32=True, device=DEV)
+    out = lora.down_combine(ad, dev(h.astype(np.float32)), torch.zeros(T, H, device=DEV),
+                            torch.zeros(T, dtype=torch.int32, device=DEV), dev(w.astype(np.float32)),
+                            *map(dev, (ids, off, sp, pos)), B)
+    assert np.array_equal(f64(out), want)
+
+
+@pytest.mark.parametrize("T,I,rank,many", [
+    (1, 32, 8, False), (9, 160, 128, False), (300, 96, 40, False), (640, 64, 16, False),
+    (3000, 96, 8, True), (3000, 320, 40, True), (2100, 64, 128, True)])
+@pytest.mark.parametrize("half", ["gate", "up"])
+def test_gateup_keeps_every_bit_of_v(lora, T, I, rank, many, half):
+    """v of 24 bits from x of 8: columns 3 q, 3 q + 1 and 3 q + 2 hold 8 bits each, the
+    next ones behind the last.  Through up: SiLU(64) = 64 in fp32.  Through gate: SiLU(g)
+    = g for g >= 64, u = 1."""
+    rng = np.random.default_rng(T + rank)
+    E, H, scale = 3, 96, 2.0
+    ids, off, sp, pos = tables(rng, T, 1, E)
+    assert (L.moe_lora_block(T, H, I, E, 1, 0, 0, 1, rank, 0) > 0) == many
+    x = rng.integers(128, 256, (T, H)) * 2.0 ** (-8 * (np.arange(H) % 3))
+    x[:, 2::3] += 2.0 ** -16 * (x[:, 2::3] * 2 ** 16 % 2 == 0)        # the last bit set
+    a13, b13 = np.zeros((E, 2 * rank, H)), np.zeros((E, 2 * I, rank))
+    want = np.zeros((T, I))
+    for e in range(E):
+        q, pa = rng.integers(0, H // 3, rank), 2.0 ** rng.integers(0, 4, rank)
+        b, col, pb = one_entry_rows(rng, I, rank)
+        first = 0 if half == "gate" else rank
+        for i in range(3):
+            a13[e, first + np.arange(rank), 3 * q + i] = pa
+        if half == "gate":
+            b, pb = np.abs(b), np.abs(pb) * 8                            # g of 128 and more
+            b *= 8
+        b13[e, :I] = b if half == "gate" else 0.0
+        b13[e, I:] = b if half == "up" else 0.0
+        t = np.nonzero(ids[:, 0] == e)[0]
+        v = scale * pa * x[t].reshape(len(t), H // 3, 3).sum(2)[:, q]
+        want[pos[t]] = pb * v[:, col] * (64.0 if half == "up" else 1.0)
+    assert (two_parts(want) != want).all() and (half == "up" or (want >= 64).all())
+    ad = lora.Adapters(1, E, H, I, max_rank=rank, device=DEV)
+    ad.load(0, bf(a13), bf(b13), scale=scale)
+    gu = np.zeros((T, 2 * I), dtype=np.float32)
+    gu[:, :I], gu[:, I:] = (64.0, 0.0) if half == "up" else (0.0, 1.0)
+    B = lora.LoraBuffers(T, H, I, E, 1, max_rank=rank, h_f32=True, device=DEV)
+    h = lora.gateup_silu(ad, bf(x), torch.zeros(T, dtype=torch.int32, device=DEV), dev(gu),
+                         *map(dev, (ids, off, sp)), B)
+    assert np.array_equal(f64(h), want)
