@@ -241,16 +241,17 @@ def run_layer(bank, M, adapters, B, x, adapter, logits, renormalize=1, routing=N
     mx.MxBank with mx.MxBuffers; routing None: the softmax top-k of
     moe_route_topk (renormalize as there), else the keyword arguments of
     router.route_scored.  The routing's results are in M.ids, M.w and M's tables.
-    flags: MOE_PATH_* of the int4/int2 projections."""
+    flags: MOE_PATH_* (and MOE_QUANT_SEPARATE) of the int4/int2 projections."""
     T, H, I, E, k = M.T, M.H, M.I, M.E, M.k
     if (T, H, I, E, k, M.n_shared) != (B.T, B.H, B.I, B.E, B.k, B.n_shared) or M.ld_h != B.ld_h or (
             M.n_shared and M.I_shared != B.I_shared):
         raise ValueError("the shared projections' buffers and the adapters' are for different layers")
-    wide = isinstance(M, _w4.LayerBuffers) and M.act == L.MOE_A8
+    packed = isinstance(M, _w4.LayerBuffers)
+    wide = packed and M.act == L.MOE_A8
     if wide != bool(B.h_flags):
         raise ValueError("h_f32: fp32 h goes with 8-bit activations, bf16 h with the others")
-    if flags and isinstance(M, _mx.MxBuffers):
-        raise ValueError("flags: MOE_PATH_* are of the int4/int2 projections")
+    if flags & ~((L.MOE_PATH_MASK | L.MOE_QUANT_SEPARATE) if packed else 0):
+        raise ValueError(f"flags: {flags:#x}, expected MOE_PATH_* of the int4/int2 projections")
     if M.ids.device != B.device:
         raise ValueError(f"the shared projections' buffers are on {M.ids.device}, the adapters' on {B.device}")
     if B.gu is None:

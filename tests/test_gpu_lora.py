@@ -630,3 +630,22 @@ def test_layer_on_another_stream_with_fresh_buffers(lora, kind):
         torch.cuda.synchronize()
     with pytest.raises(ValueError, match="layer=False"):
         lora.run_layer(bank, M, d["ad"], lora.LoraBuffers(*sized, device=DEV, layer=False), x, d["tad"], logits)
+
+
+def test_layer_takes_no_flags_but_paths(lora):
+    """MOE_X_PREPARED would read a copy of x that no call of the layer makes."""
+    from packed_bit_grouped_amd import _lib as L
+    T, H, I, E, k, Is = 6, 256, 128, 8, 2, 128
+    dl = w4_layer(T, H, I, E, k, 1, Is, "a16", 78)
+    M = dl.buffers("a16", 16)
+    ad = lora.Adapters(2, E, H, I, 1, Is, max_rank=8, device=DEV)
+    B = lora.LoraBuffers(T, H, I, E, k, 1, Is, 8, device=DEV)
+    tad = torch.zeros(T, dtype=torch.int32, device=DEV)
+    M.ids.fill_(-7)
+    for flags in (L.MOE_X_PREPARED, L.MOE_LAYER_ONE_LAUNCH, L.MOE_OUT_F32, L.MOE_W_PREPACKED, L.MOE_GU_F32, L.MOE_H_F32):
+        with pytest.raises(ValueError, match="flags"):
+            lora.run_layer(dl.bank, M, ad, B, dl.x, tad, dl.logits, flags=flags)
+    torch.cuda.synchronize()
+    assert (M.ids == -7).all()
+    lora.run_layer(dl.bank, M, ad, B, dl.x, tad, dl.logits, flags=L.MOE_PATH_MFMA16 | L.MOE_QUANT_SEPARATE)
+    assert (M.ids >= 0).all()
