@@ -60,7 +60,7 @@
 extern "C" {
 #endif
 
-#define MOE_W4_ABI_VERSION 8
+#define MOE_W4_ABI_VERSION 9
 
 /* Version of the compiled library.  The Python binding refuses to load a
  * library whose version differs from the header it was written for. */
@@ -300,6 +300,13 @@ size_t moe_workspace_bytes(int act, int T, int H, int I, int E, int k,
                               /* SiLU: what moe_lora_gateup_silu joins with  */
                               /* the requests' adapters.  Other calls refuse */
                               /* it; not on the vector-ALU decode path       */
+
+/* Whether moe_w4_gateup_silu and moe_w4_down_combine take these sizes and flags
+ * (host only): MOE_OK, or what they would return.  A forced path that does not
+ * cover the shape and MOE_W_PREPACKED off the matrix-core path are refused by the
+ * one or the other, which a caller of both wants to know before the first. */
+moe_status moe_w4_covers(int act, int T, int H, int I, int E, int k, int n_shared, int I_shared,
+                         int tile_m, int flags);
 
 /* Tile height to pass as moe_permute's tile_m: 160 (the MFMA path's row
  * chunk: an expert with up to 160 pairs streams its weights once) when

@@ -14,7 +14,7 @@ from typing import Optional
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe_w4.so")
-ABI_VERSION = 8
+ABI_VERSION = 9
 
 MOE_OK, MOE_E_INVAL, MOE_E_UNSUPPORTED, MOE_E_DEVICE, MOE_E_WORKSPACE = 0, -1, -2, -3, -4
 MOE_A16, MOE_A8, MOE_A4 = 0, 1, 2
@@ -128,6 +128,7 @@ _SIGS = {
                               c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                               c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_int,
                               c_void_p]),
+    "moe_w4_covers": (c_int, [c_int] * 10),
     "moe_route_scored": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_int, c_int,
                                  c_int, c_int, c_float, c_void_p, c_void_p, c_void_p]),
     "moe_lora_tile": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_void_p]),
@@ -462,6 +463,11 @@ def moe_mx4_layer(act, logits, x, T, H, I, E, k, renormalize, w13, w2, w13_share
                  _ptr(shared_gate), _ptr(topk_ids), _ptr(topk_w), _ptr(counts), _ptr(offsets),
                  _ptr(sorted_pair), _ptr(pair_pos), _ptr(h), _ptr(out), _ptr(workspace),
                  ws_bytes, flags, _stream(stream), check=check)
+
+
+def moe_w4_covers(act, T, H, I, E, k, n_shared, I_shared, tile_m, flags, check=True):
+    return _call("moe_w4_covers", act, T, H, I, E, k, n_shared, I_shared, tile_m, flags,
+                 check=check)
 
 
 def moe_lora_tile(src, n, rows, cols, is_b, dst, stream=None, check=True):

@@ -109,6 +109,21 @@ bool use_mfma(int act, int T, int H, int I, int E, int k, int n_shared,
          (long long)T * k >= 32LL * E;
 }
 
+// Whether gate/up (mode 0) or down (1) has a kernel for these sizes and flags,
+// which check_layer took: a forced path covers its shapes only, and the prepacked
+// layout is read by the matrix-core path alone.
+moe_status check_path(int act, int mode, int T, int H, int I, int E, int k, int n_shared,
+                      int I_shared, int tile_m, int flags) {
+  const int path = flags & MOE_PATH_MASK, K = mode ? I : H;
+  const int K_sh = mode && n_shared > 0 ? I_shared : K;
+  if (path == MOE_PATH_MFMA16 && !m16_ok(act, mode, T, K, K_sh, tile_m)) return MOE_E_UNSUPPORTED;
+  if (path == MOE_PATH_MFMA && !mfma_shape_ok(act, T, H, I, k, n_shared, I_shared))
+    return MOE_E_UNSUPPORTED;
+  if ((flags & MOE_W_PREPACKED) && !use_mfma(act, T, H, I, E, k, n_shared, I_shared, flags))
+    return MOE_E_UNSUPPORTED;
+  return MOE_OK;
+}
+
 }  // namespace
 
 namespace moe {
@@ -335,11 +350,10 @@ static moe_status gateup_impl(int act, const uint16_t* x, int T, int H, int I,
   const WsLayout L = ws_layout(act, T, H, I, E, k, n_shared, I_shared);
   if (!workspace || !aligned(workspace, 256) || ws_bytes < L.total) return MOE_E_WORKSPACE;
   if (partials && ng_ld <= 0) return MOE_E_INVAL;
+  st = check_path(act, 0, T, H, I, E, k, n_shared, I_shared, tile_m, flags);
+  if (st != MOE_OK) return st;
   const int path = flags & MOE_PATH_MASK;
   const bool m16 = m16_ok(act, 0, T, H, H, tile_m);
-  if (path == MOE_PATH_MFMA16 && !m16) return MOE_E_UNSUPPORTED;
-  if (path == MOE_PATH_MFMA && !mfma_shape_ok(act, T, H, I, k, n_shared, I_shared))
-    return MOE_E_UNSUPPORTED;
   st = check_device();
   if (st != MOE_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -376,7 +390,6 @@ static moe_status gateup_impl(int act, const uint16_t* x, int T, int H, int I,
 
   const bool pp = (flags & MOE_W_PREPACKED) != 0;
   if (use_mfma(act, T, H, I, E, k, n_shared, I_shared, flags)) {
-    if (!mfma_shape_ok(act, T, H, I, k, n_shared, I_shared)) return MOE_E_UNSUPPORTED;
     a.in_bf16 = x;
     uint16_t* x16 = reinterpret_cast<uint16_t*>(ws + L.a16);
     // the routing launch of moe_w4_layer made the fp16 copy of x already
@@ -384,7 +397,6 @@ static moe_status gateup_impl(int act, const uint16_t* x, int T, int H, int I,
     if (stage_h16) a.out16 = reinterpret_cast<uint16_t*>(ws + L.h16);
     return from_hip(launch_proj_mfma8(a, x16, pp, s));
   }
-  if (pp) return MOE_E_UNSUPPORTED;   // the prepacked layout is read by the matrix-core path only
   const bool dec = act == MOE_A16 && !partials && !raw && dec_gateup_ok(T, H, tile_m);
   const bool on_m16 = path == MOE_PATH_MFMA16 ||
                       (path == MOE_PATH_AUTO && m16 && !(dec && (long long)T * k <= kDecPairs));
@@ -438,11 +450,10 @@ static moe_status down_impl(int act, const void* h, int T, int H, int I, int E,
   const WsLayout L = ws_layout(act, T, H, I, E, k, n_shared, I_shared);
   if (!workspace || !aligned(workspace, 256) || ws_bytes < L.total) return MOE_E_WORKSPACE;
   if (partials && ng_ld <= 0) return MOE_E_INVAL;
+  st = check_path(act, 1, T, H, I, E, k, n_shared, I_shared, tile_m, flags);
+  if (st != MOE_OK) return st;
   const int path = flags & MOE_PATH_MASK;
   const bool m16 = m16_ok(act, 1, T, I, n_shared > 0 ? I_shared : I, tile_m);
-  if (path == MOE_PATH_MFMA16 && !m16) return MOE_E_UNSUPPORTED;
-  if (path == MOE_PATH_MFMA && !mfma_shape_ok(act, T, H, I, k, n_shared, I_shared))
-    return MOE_E_UNSUPPORTED;
   st = check_device();
   if (st != MOE_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -480,7 +491,6 @@ static moe_status down_impl(int act, const void* h, int T, int H, int I, int E,
   hipError_t e;
   const bool pp = (flags & MOE_W_PREPACKED) != 0;
   if (use_mfma(act, T, H, I, E, k, n_shared, I_shared, flags)) {
-    if (!mfma_shape_ok(act, T, H, I, k, n_shared, I_shared)) return MOE_E_UNSUPPORTED;
     a.in_bf16 = static_cast<const uint16_t*>(h);
     if (h16_staged) {
       a.in_bf16 = reinterpret_cast<const uint16_t*>(ws + L.h16);
@@ -491,7 +501,6 @@ static moe_status down_impl(int act, const void* h, int T, int H, int I, int E,
     return from_hip(launch_combine(y, H, topk_w, pair_pos, T, k, H, T * k,
                                    n_shared, shared_gate, out, out_f32, s));
   }
-  if (pp) return MOE_E_UNSUPPORTED;   // the prepacked layout is read by the matrix-core path only
   if (act == MOE_A8) a.in_f32 = static_cast<const float*>(h);
   else a.in_bf16 = static_cast<const uint16_t*>(h);
   const bool dec = act == MOE_A16 && !partials &&
@@ -531,6 +540,14 @@ static moe_status down_impl(int act, const void* h, int T, int H, int I, int E,
   if (e != hipSuccess) return MOE_E_DEVICE;
   return from_hip(launch_combine(y, H, topk_w, pair_pos, T, k, H, T * k,
                                  n_shared, shared_gate, out, out_f32, s));
+}
+
+moe_status moe_w4_covers(int act, int T, int H, int I, int E, int k, int n_shared, int I_shared,
+                         int tile_m, int flags) {
+  const moe_status st = check_layer(act, T, H, I, E, k, n_shared, I_shared, tile_m, flags);
+  if (st != MOE_OK || T == 0) return st;
+  const moe_status g = check_path(act, 0, T, H, I, E, k, n_shared, I_shared, tile_m, flags);
+  return g != MOE_OK ? g : check_path(act, 1, T, H, I, E, k, n_shared, I_shared, tile_m, flags);
 }
 
 moe_status moe_w4_gateup_silu(int act, const uint16_t* x, int T, int H, int I,

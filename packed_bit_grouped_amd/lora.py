@@ -241,7 +241,8 @@ def run_layer(bank, M, adapters, B, x, adapter, logits, renormalize=1, routing=N
     mx.MxBank with mx.MxBuffers; routing None: the softmax top-k of
     moe_route_topk (renormalize as there), else the keyword arguments of
     router.route_scored.  The routing's results are in M.ids, M.w and M's tables.
-    flags: MOE_PATH_* (and MOE_QUANT_SEPARATE) of the int4/int2 projections."""
+    flags: MOE_PATH_* (and MOE_QUANT_SEPARATE) of the int4/int2 projections.  What
+    does not fit is refused before anything is launched."""
     T, H, I, E, k = M.T, M.H, M.I, M.E, M.k
     if (T, H, I, E, k, M.n_shared) != (B.T, B.H, B.I, B.E, B.k, B.n_shared) or M.ld_h != B.ld_h or (
             M.n_shared and M.I_shared != B.I_shared):
@@ -250,6 +251,8 @@ def run_layer(bank, M, adapters, B, x, adapter, logits, renormalize=1, routing=N
     wide = packed and M.act == L.MOE_A8
     if wide != bool(B.h_flags):
         raise ValueError("h_f32: fp32 h goes with 8-bit activations, bf16 h with the others")
+    if not isinstance(bank, _w4.Bank if packed else _mx.MxBank):
+        raise TypeError(f"bank: {type(bank).__name__} does not go with {type(M).__name__}")
     if flags & ~((L.MOE_PATH_MASK | L.MOE_QUANT_SEPARATE) if packed else 0):
         raise ValueError(f"flags: {flags:#x}, expected MOE_PATH_* of the int4/int2 projections")
     if M.ids.device != B.device:
@@ -258,10 +261,21 @@ def run_layer(bank, M, adapters, B, x, adapter, logits, renormalize=1, routing=N
         raise ValueError("the adapters' buffers were made with layer=False")
     if T == 0:
         return B.out
-    # before the first launch: what the calls read
     dev = B._dev
+    if packed:
+        w_flags = flags | (L.MOE_W_PREPACKED if bank.prepacked else 0)
+        for tag, n in (("w13", E), ("w2", E), ("w13_sh", M.n_shared), ("w2_sh", M.n_shared)):
+            table = getattr(bank, tag)
+            held = 0 if table is None else table.numel() // ctypes.sizeof(L.QMatDesc)
+            if held < n or (n and table.device != B.device):
+                raise ValueError(f"{tag}: the bank holds {held} matrices, the buffers are for {n} on {B.device}")
+        L.moe_w4_covers(M.act, T, H, I, E, k, M.n_shared, M.I_shared, M.tile_m, w_flags)
+    else:
+        for tag, shape in M.mats.items():
+            bank.need(tag, shape, dev)
     _want("logits", logits, _F32, (T, E), dev)
-    _want("x", x, _BF16, (T, H), dev)
+    if _want("x", x, _BF16, (T, H), dev) % 16:
+        raise ValueError("x: expected 16-byte aligned rows")
     _want("adapter", adapter, _I32, (T,), dev)
     _gate(shared_gate, B)
     _table(adapters, "13", B)
@@ -277,26 +291,25 @@ def run_layer(bank, M, adapters, B, x, adapter, logits, renormalize=1, routing=N
         L.moe_route_topk(logits, T, E, k, int(renormalize), M.ids, M.w, stream)
     else:
         _router.route_scored(logits, k, ids=M.ids, w=M.w, stream=stream, **routing)
-    if isinstance(M, _mx.MxBuffers):
-        tile_m, tiles, n_tiles = _TILE_M, B.tiles, B.n_tiles
-    else:
+    if packed:
         tile_m, tiles, n_tiles = M.tile_m, M.tiles, M.n_tiles
+    else:
+        tile_m, tiles, n_tiles = _TILE_M, B.tiles, B.n_tiles
     L.moe_permute(M.ids, T, k, E, tile_m, M.counts, M.offsets, M.sorted_pair, M.pair_pos, tiles,
                   n_tiles, stream)
-    if isinstance(M, _mx.MxBuffers):
+    if not packed:
         _mx.gateup_silu(bank, x, M.offsets, M.sorted_pair, M, stream, gu=B.gu)
     else:
-        flags |= L.MOE_W_PREPACKED if bank.prepacked else 0
         L.moe_w4_gateup_silu(M.act, x, T, H, I, E, k, bank.w13, bank.w13_sh, M.n_shared,
                              M.I_shared, M.offsets, M.sorted_pair, tiles, n_tiles, tile_m, B.gu,
-                             M.ws, M.ws_bytes, flags | L.MOE_GU_F32, stream)
+                             M.ws, M.ws_bytes, w_flags | L.MOE_GU_F32, stream)
     h = gateup_silu(adapters, x, adapter, B.gu, M.ids, M.offsets, M.sorted_pair, B, stream)
-    if isinstance(M, _mx.MxBuffers):
+    if not packed:
         _mx.down_combine(bank, h, M.w, M.offsets, M.pair_pos, M, shared_gate, stream, out=B.base)
     else:
         L.moe_w4_down_combine(M.act, h, T, H, I, E, k, bank.w2, bank.w2_sh, M.n_shared,
                               M.I_shared, M.w, M.offsets, M.sorted_pair, M.pair_pos, tiles,
-                              n_tiles, tile_m, B.base, M.ws, M.ws_bytes, flags | L.MOE_OUT_F32,
+                              n_tiles, tile_m, B.base, M.ws, M.ws_bytes, w_flags | L.MOE_OUT_F32,
                               stream, shared_gate=shared_gate)
     return down_combine(adapters, h, B.base, adapter, M.w, M.ids, M.offsets, M.sorted_pair,
                         M.pair_pos, B, shared_gate, stream)

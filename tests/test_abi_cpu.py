@@ -341,3 +341,39 @@ def test_prepack_scales_validation():
     assert call(K=8192, group=64) == L.MOE_E_UNSUPPORTED   # more than 64 groups
     assert call() == L.MOE_E_DEVICE
     assert call(gate_up=0, group=32) == L.MOE_E_DEVICE
+
+
+# ---------------------------------------------------------------------------
+# which sizes and flags the two projections take
+
+
+def test_covers_says_what_either_projection_refuses():
+    A8, ok, no = L.MOE_A8, L.MOE_OK, L.MOE_E_UNSUPPORTED
+    def covers(T=4, H=256, I=128, E=8, k=2, n_shared=0, I_shared=0, tile_m=16, flags=0, act=0):
+        return L.moe_w4_covers(act, T, H, I, E, k, n_shared, I_shared, tile_m, flags, check=False)
+    assert covers() == covers(act=A8) == covers(T=0, flags=L.MOE_W_PREPACKED) == ok
+    assert covers(flags=L.MOE_PATH_MFMA) == covers(flags=L.MOE_PATH_MFMA16) == ok
+    assert covers(flags=L.MOE_PATH_MFMA, act=A8) == covers(flags=L.MOE_PATH_MFMA, H=288) == no
+    assert covers(flags=L.MOE_PATH_MFMA, n_shared=1, I_shared=96) == no
+    assert covers(flags=L.MOE_PATH_MFMA16, tile_m=160) == no
+    assert covers(flags=L.MOE_PATH_MFMA16, H=8192) == no                 # gate/up's rows of 8192
+    assert covers(flags=L.MOE_PATH_MFMA16, I=8192) == no                 # down's
+    assert covers(flags=L.MOE_W_PREPACKED) == no                         # 8 pairs go elsewhere
+    assert covers(flags=L.MOE_W_PREPACKED, T=128) == ok
+    assert covers(flags=L.MOE_W_PREPACKED | L.MOE_PATH_MFMA) == ok
+    assert covers(flags=L.MOE_W_PREPACKED | L.MOE_PATH_GEMV, T=128) == no
+    assert covers(E=513) == covers(H=48) == covers(T=1 << 23) == no
+    for kw in (dict(T=-1), dict(k=9), dict(tile_m=0), dict(act=2), dict(flags=L.MOE_LAYER_ONE_LAUNCH),
+               dict(flags=L.MOE_GU_F32), dict(n_shared=1)):
+        assert covers(**kw) == L.MOE_E_INVAL, kw
+
+
+@pytest.mark.parametrize("kw", [dict(flags=L.MOE_PATH_MFMA16, tile_m=160), dict(flags=L.MOE_PATH_MFMA, H=288),
+                                dict(flags=L.MOE_W_PREPACKED)])
+def test_a_path_that_does_not_cover_the_shape_is_refused_on_the_host(kw):
+    assert _gateup(**kw) == L.MOE_E_UNSUPPORTED
+    a = dict(act=0, h=FAKE, T=4, H=256, I=128, E=8, k=2, w2=FAKE, w2_shared=None, n_shared=0, I_shared=0,
+             topk_w=FAKE, offsets=FAKE, sorted_pair=FAKE, pair_pos=FAKE, tiles=FAKE, n_tiles=FAKE, tile_m=16,
+             out=FAKE, workspace=FAKE, ws_bytes=1 << 30, flags=0)
+    a.update(kw)
+    assert L.moe_w4_down_combine(*a.values(), stream=0, check=False) == L.MOE_E_UNSUPPORTED

@@ -649,3 +649,40 @@ def test_layer_takes_no_flags_but_paths(lora):
     assert (M.ids == -7).all()
     lora.run_layer(dl.bank, M, ad, B, dl.x, tad, dl.logits, flags=L.MOE_PATH_MFMA16 | L.MOE_QUANT_SEPARATE)
     assert (M.ids >= 0).all()
+
+
+def test_layer_refuses_banks_paths_and_flags_before_it_runs(lora):
+    from packed_bit_grouped_amd import _lib as L
+    T, H, I, E, k, Is = 6, 256, 128, 8, 2, 128
+    dl = w4_layer(T, H, I, E, k, 1, Is, "a16", 78)
+    M = dl.buffers("a16", 16)
+    ad = lora.Adapters(2, E, H, I, 1, Is, max_rank=8, device=DEV)
+    B = lora.LoraBuffers(T, H, I, E, k, 1, Is, 8, device=DEV)
+    tad = torch.zeros(T, dtype=torch.int32, device=DEV)
+    bank, X = mx_layer(T, H, I, E, k, 1, Is, "a16", 2)
+    small = w4_layer(T, H, I, E - 4, k, 1, Is, "a16", 79).bank
+    bare = w4_layer(T, H, I, E, k, 0, 0, "a16", 79).bank
+    x = dl.x.view(torch.bfloat16)
+    odd = torch.zeros(T * H + 4, dtype=torch.bfloat16, device=DEV)[4:].view(T, H)
+    wide = dl.buffers("a16", 160)
+    M.ids.fill_(-7), X.ids.fill_(-7), wide.ids.fill_(-7)
+    go = lambda bank=dl.bank, M=M, x=x, **kw: lora.run_layer(bank, M, ad, B, x, tad, dl.logits, **kw)
+    for kw, kind, word in (
+            (dict(bank=bank), TypeError, "bank"), (dict(M=X), TypeError, "bank"), (dict(bank=small), ValueError, "w13"),
+            (dict(bank=bare), ValueError, "w13_sh"), (dict(x=odd), ValueError, "aligned"),
+            (dict(bank=mx_layer(T, H, I, E - 1, k, 1, Is, "a16", 3)[0], M=X), ValueError, "w13"),
+            (dict(bank=mx_layer(T, H, I + 32, E, k, 1, Is, "a16", 3)[0], M=X), ValueError, "w13"),
+            (dict(bank=mx_layer(T, H, I, E, k, 0, 0, "a16", 3)[0], M=X), ValueError, "w13_shared"),
+            (dict(flags=L.MOE_X_PREPARED), ValueError, "flags"), (dict(flags=L.MOE_LAYER_ONE_LAUNCH), ValueError, "flags"),
+            (dict(flags=L.MOE_OUT_F32), ValueError, "flags"), (dict(flags=L.MOE_H_F32), ValueError, "flags"),
+            (dict(flags=L.MOE_PATH_MFMA16, M=wide), L.MoeError, "moe_w4_covers"),
+            (dict(bank=dl.bank.prepack()), L.MoeError, "moe_w4_covers"),
+            (dict(routing=dict(n_group=3)), L.MoeError, "moe_route_scored"),
+            (dict(routing=dict(n_group=8, topk_group=1)), L.MoeError, "moe_route_scored")):
+        with pytest.raises(kind, match=word):
+            go(**kw)
+    torch.cuda.synchronize()
+    assert all((m.ids == -7).all() for m in (M, X, wide))
+    assert B.error_word() == M.error_word() == 0
+    go(), go(flags=L.MOE_PATH_MFMA16 | L.MOE_QUANT_SEPARATE)       # what fits runs
+    assert (M.ids >= 0).all()
