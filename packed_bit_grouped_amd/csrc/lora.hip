@@ -103,7 +103,8 @@ __device__ __forceinline__ Row window_row(const LoraArgs& a, int r, int p, const
   if (r < a.P) {
     if ((unsigned)p >= (unsigned)a.P) return w;
     e = topk_ids[p];
-    if ((unsigned)e >= (unsigned)a.E) return w;
+    const int back = WEIGHT ? a.pair_pos[p] : r;   // -1: the pair adds nothing
+    if ((unsigned)e >= (unsigned)a.E || back != r) return w;
     w.token = p / a.k;
     if (WEIGHT) w.weight = a.topk_w[p];
   } else {
@@ -485,23 +486,26 @@ __device__ void make_plan(const LoraArgs& a, int b, int part, PlanLds& L) {
     const int w = part * kPlanWindows + i;
     if (w >= a.win) break;
     const int q = 64 * w + lane;
-    int key = -1, row = 0, token = 0, rank = 0;
+    int key = -1, row = 0, token = 0, rank = 0, e = -1;
     const uint16_t* bp = nullptr;
     if (q < total) {
-      int e = 0, hi = NE;   // the last expert whose rows start at q or before
+      int hi = NE;   // the last expert whose rows start at q or before
+      e = 0;
       while (hi - e > 1) {
         const int mid = (e + hi) >> 1;
         if (L.pos[mid] <= q) e = mid;
         else hi = mid;
       }
       row = L.lo[e] + q - L.pos[e];
+      bool counts = true;
       if (e < a.E) {
         const int p = a.sorted_pair[row];
         token = (unsigned)p < (unsigned)a.P ? p / a.k : -1;
+        counts = token >= 0 && a.pair_pos[p] == row;   // -1: the pair adds nothing
       } else {
         token = row - a.P - (e - a.E) * a.T;
       }
-      if (token >= t0 && token < t1) {
+      if (counts && token >= t0 && token < t1) {
         const int d = a.adapter[token];
         if ((unsigned)d < (unsigned)a.n) {
           const moe_lora m = a.table[(size_t)d * NE + e];
@@ -514,8 +518,8 @@ __device__ void make_plan(const LoraArgs& a, int b, int part, PlanLds& L) {
       }
     }
     // a token that lists an expert twice has neighbouring rows: each time apart
-    const int token1 = __shfl_up(token, 1), key1 = __shfl_up(key, 1);
-    const bool same = lane > 0 && token1 == token && key1 == key;
+    const int token1 = __shfl_up(token, 1), e1 = __shfl_up(e, 1);
+    const bool same = lane > 0 && token1 == token && e1 == e;
     const uint64_t first = ~__ballot(same) & ((2ull << lane) - 1);
     const int again = lane - (63 - __builtin_clzll(first));
     uint64_t todo = __ballot(key >= 0);

@@ -198,3 +198,38 @@ def test_gateup_keeps_every_bit_of_v(lora, T, I, rank, many, half):
     h = lora.gateup_silu(ad, bf(x), torch.zeros(T, dtype=torch.int32, device=DEV), dev(gu),
                          *map(dev, (ids, off, sp)), B)
     assert np.array_equal(f64(h), want)
+
+
+# ---------------------------------------------------------------------------
+# the routing's tables
+
+
+@pytest.mark.parametrize("T,ranks", [(5, (8, 16)), (70, (8, 16)), (2400, (8, 16)), (2400, (8, 128))])
+@pytest.mark.parametrize("wide", [False, True])
+def test_a_pair_without_a_place_adds_nothing(lora, T, ranks, wide):
+    """pair_pos -1 takes a pair out of the sum whatever the other tables say, as in
+    the shared down projection."""
+    d = make(lora, T, 4096, 64, 6, 3, 1, 32, 3, ranks, h_f32=wide, out_f32=True, none=0.1, seed=T)
+    assert (block_of(d) > 0) == (T > 70)
+    d["pos"][np.random.default_rng(1).random(3 * T) < 0.3] = -1
+    d["pos"][:3] = -1
+    d["t"][3] = dev(d["pos"])
+    check_down(d, run_down(lora, d))
+    assert d["B"].error_word() == 0
+
+
+@pytest.mark.parametrize("T,ranks", [(6, (8, 16)), (2400, (8, 16)), (2400, (8, 128))])
+@pytest.mark.parametrize("gone", [0, 1, 2])
+def test_a_token_s_places_of_one_expert_one_of_them_taken_out(lora, T, ranks, gone):
+    """Three times the same expert, the first, second or third of them without a place."""
+    d = make(lora, T, 4096, 64, 4, 3, 0, 0, 2, ranks, out_f32=True, runs=True, none=0.0, seed=41)
+    ids = np.repeat(d["ids"][:, :1], 3, 1)
+    order = np.argsort(ids.ravel(), kind="stable").astype(np.int32)
+    pos = np.argsort(order).astype(np.int32).reshape(T, 3)
+    pos[::2, gone] = -1
+    d["ids"], d["sp"], d["pos"] = ids, order, pos.ravel()
+    d["off"] = np.concatenate([[0], np.cumsum(np.bincount(ids.ravel(), minlength=4))]).astype(np.int32)
+    d["rows"] = [(int(p) // 3, int(ids.ravel()[p])) for p in order]
+    d["t"] = [dev(d[x]) for x in ("ids", "off", "sp", "pos")]
+    assert (block_of(d) > 0) == (T > 6)
+    check_down(d, run_down(lora, d))
