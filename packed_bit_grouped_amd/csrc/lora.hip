@@ -544,6 +544,7 @@ __device__ void make_plan(const LoraArgs& a, int b, int part, PlanLds& L) {
         const int t = token - t0, i = __popcll(rows & ((1ull << lane) - 1));
         a.plan_sums[first_unit * 16 + i] = (uint32_t)(t * 256 + (t & 15) * 16);
         a.place[row] = at + i;
+        a.row_at[at + i] = (uint32_t)row;
       }
       // lanes without a row add behind the block
       if (n + lane < 16 * nu) a.plan_sums[first_unit * 16 + n + lane] = (uint32_t)a.block * 256;
@@ -701,8 +702,11 @@ __global__ __launch_bounds__(kThreads) void lora_shrink_kernel(LoraArgs a, int n
           const uint32_t place = a.place[base + (a.order[base + at] >> 24)];
           to[f] = a.parts + (size_t)(place >> 6) * 64 * 3 * a.max_rank + (place & 63) * 8;
           weight[f] = a.weight[base + at];
-          // a list of pairs that contradicts itself: no place, nothing is stored
-          if (place >= (uint32_t)a.n_blocks * a.win * 64) to[f] = nullptr;
+          // a row that the plan left out (lists that contradict each other) has
+          // whatever place an earlier call left: only a place of its own counts
+          const uint32_t places = (uint32_t)a.n_blocks * a.win * 64;
+          if (a.row_at[min(place, places - 1)] != (uint32_t)base + (a.order[base + at] >> 24) || place >= places)
+            to[f] = nullptr;
         } else {
           to[f] = a.parts + base * 6 * a.max_rank + at * 8;
         }
@@ -1478,6 +1482,7 @@ size_t lora_carve(LoraArgs& a, char* ws) {
     const size_t win = (size_t)a.n_blocks * a.win;
     a.weight = reinterpret_cast<float*>(take(rows * 4));
     a.place = reinterpret_cast<uint32_t*>(take(rows * 4));
+    a.row_at = reinterpret_cast<uint32_t*>(take(win * 64 * 4));
     a.parts = reinterpret_cast<uint16_t*>(take(win * 64 * a.max_rank * 6));
     a.plan_count = reinterpret_cast<int*>(take(win * 4));
     a.plan = reinterpret_cast<LoraUnit*>(take(win * 64 * sizeof(LoraUnit)));

@@ -57,6 +57,7 @@ struct LoraArgs {
   // tokens: its rows in win windows of 64, each with its units
   float* weight;                // [window][256] in the window's order
   uint32_t* place;              // [R] plan's window * 64 + place in it
+  uint32_t* row_at;             // [n_blocks][win][64] and back
   int block, n_blocks, win;
   int* plan_count;              // [n_blocks][win] units of a window
   LoraUnit* plan;               // [n_blocks][win][64]

@@ -4,6 +4,7 @@ fp32 operands to their last bit."""
 import numpy as np
 import pytest
 
+from oracle import lora_oracle as O
 from packed_bit_grouped_amd import _lib as L
 
 torch = pytest.importorskip("torch")
@@ -233,3 +234,26 @@ def test_a_token_s_places_of_one_expert_one_of_them_taken_out(lora, T, ranks, go
     d["t"] = [dev(d[x]) for x in ("ids", "off", "sp", "pos")]
     assert (block_of(d) > 0) == (T > 6)
     check_down(d, run_down(lora, d))
+
+
+@pytest.mark.parametrize("ranks", [(8, 16), (8, 128)])
+def test_rows_that_the_offsets_leave_out_touch_no_other_token(lora, ranks):
+    """Lists that contradict each other: rows of valid pairs that no expert's offsets
+    hold.  What an earlier call left in the workspace is not taken for their places."""
+    T, E = 2400, 6
+    d = make(lora, T, 4096, 64, E, 1, 0, 0, 3, ranks, out_f32=True, none=0.0, seed=43)
+    assert block_of(d) > 0
+    check_down(d, run_down(lora, d))                  # a place for every row
+    cut = int(d["off"][3] - 40)                       # expert 2 ends early: its last 40 rows are nobody's
+    d["off"][3] = cut
+    left = [d["rows"][r][0] for r in range(cut, cut + 40)]
+    rng = np.random.default_rng(44)
+    d["adapter"] = rng.integers(0, 3, T).astype(np.int32)      # other places than before
+    d["tad"], d["t"][1] = dev(d["adapter"]), dev(d["off"])
+    out = run_down(lora, d)
+    others = np.setdiff1d(np.arange(T), left)
+    pos = d["pos"].copy()
+    pos[left] = -1
+    want, bound = O.down(f64(d["base"]), f64(d["h"]), d["rows"], d["adapter"], d["dn"], d["widths"], f64(d["w"]), pos,
+                         np.ones((T, 0)), T, 1, False)
+    assert (np.abs(f64(out) - want)[others] <= bound[others]).all()
