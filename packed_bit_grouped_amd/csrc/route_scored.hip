@@ -11,6 +11,8 @@
 // (the largest power of two with LG * n_group <= 64), so that a group's best
 // two values are a butterfly over its own lanes, and no step needs LDS: lane l
 // holds the experts i = l % LG, + LG, ... of group l / LG.
+#include <algorithm>
+
 #include "route_common.h"
 
 namespace moe {
@@ -88,7 +90,7 @@ __device__ __forceinline__ void join2(double& a, double& b, double oa, double ob
 template <int NV>
 __global__ __launch_bounds__(64 * kScoredWaves) void route_scored_kernel(ScoredArgs a, int lg) {
   const int lane = threadIdx.x & 63;
-  const int t = blockIdx.x * kScoredWaves + (threadIdx.x >> 6);
+  const int t = (blockIdx.y * gridDim.x + blockIdx.x) * kScoredWaves + (threadIdx.x >> 6);
   if (t >= a.T) return;
   const int size = a.E / a.n_group, LG = 1 << lg;
   const int g = lane >> lg, i0 = lane & (LG - 1);
@@ -228,7 +230,9 @@ hipError_t launch_route_scored(const ScoredArgs& a, hipStream_t st) {
   int lg = 6;
   while (lg > 0 && (a.n_group << lg) > 64) --lg;
   const int size = a.E / a.n_group, nv = (size + (1 << lg) - 1) >> lg;
-  const int grid = (a.T + kScoredWaves - 1) / kScoredWaves, block = 64 * kScoredWaves;
+  const int wgs = (a.T + kScoredWaves - 1) / kScoredWaves, block = 64 * kScoredWaves;
+  // a launch has fewer than 2^32 lanes along x
+  const dim3 grid(std::min(wgs, 1 << 20), (wgs + (1 << 20) - 1) >> 20);
   if (nv <= 1) route_scored_kernel<1><<<grid, block, 0, st>>>(a, lg);
   else if (nv <= 2) route_scored_kernel<2><<<grid, block, 0, st>>>(a, lg);
   else if (nv <= 4) route_scored_kernel<4><<<grid, block, 0, st>>>(a, lg);

@@ -170,3 +170,15 @@ def test_no_tokens_and_refusals(router):
     from packed_bit_grouped_amd import _lib as L
     with pytest.raises(L.MoeError):
         router.route_scored(l, 17)
+
+
+@pytest.mark.parametrize("T", [(1 << 26) - 5, (1 << 26) - 1])
+def test_the_most_tokens(router, T):
+    """Workgroups of 256 lanes for four tokens each: 2^32 lanes and the most that are less."""
+    logits = torch.zeros((T, 1), device=DEV)
+    ids = torch.full((T, 1), -7, dtype=torch.int32, device=DEV)
+    w = torch.full((T, 1), -7.0, device=DEV)
+    router.route_scored(logits, 1, renormalize=False, scale=4.0, ids=ids, w=w)
+    assert (ids == 0).all() and (w == 2.0).all()
+    del logits, ids, w
+    torch.cuda.empty_cache()
