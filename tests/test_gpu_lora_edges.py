@@ -8,7 +8,7 @@ from oracle import lora_oracle as O
 from packed_bit_grouped_amd import _lib as L
 
 torch = pytest.importorskip("torch")
-from test_gpu_lora import DEV, check_down, dev, f64, make, run_down, run_gateup, tables  # noqa: E402,F401
+from test_gpu_lora import DEV, check_down, check_gateup, dev, f64, make, run_down, run_gateup, tables  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -257,3 +257,109 @@ def test_rows_that_the_offsets_leave_out_touch_no_other_token(lora, ranks):
     want, bound = O.down(f64(d["base"]), f64(d["h"]), d["rows"], d["adapter"], d["dn"], d["widths"], f64(d["w"]), pos,
                          np.ones((T, 0)), T, 1, False)
     assert (np.abs(f64(out) - want)[others] <= bound[others]).all()
+
+
+# ---------------------------------------------------------------------------
+# sizes, streams and graphs
+
+
+class Far:
+    """Rows of a device tensor, fetched one at a time, as the oracle indexes them."""
+
+    def __init__(self, t):
+        self.t = t
+
+    def __getitem__(self, at):
+        return f64(self.t[at[0], at[1]])
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_more_sums_and_rows_of_h_than_32_bits_count(lora, wide):
+    """gu of 2^31 values and more, h of 2^31 bytes and more."""
+    T, H, I, E, k, rank = 70000, 64, 2048, 8, 8, 8
+    rng = np.random.default_rng(51)
+    ids = rng.integers(0, E, (T, k)).astype(np.int32)
+    order = np.argsort(ids.ravel(), kind="stable").astype(np.int32)
+    pos = np.argsort(order).astype(np.int32)
+    off = np.concatenate([[0], np.cumsum(np.bincount(ids.ravel(), minlength=E))]).astype(np.int32)
+    adapter = rng.integers(-1, 2, T).astype(np.int32)
+    ad = lora.Adapters(2, E, H, I, max_rank=rank, device=DEV)
+    up, dn = [[None] * E for _ in range(2)], [[None] * E for _ in range(2)]
+    for i in range(2):
+        a13, b13, a2, b2 = (torch.randn(E, *s, device=DEV).bfloat16() * 0.3
+                            for s in ((2 * rank, H), (2 * I, rank), (rank, I), (H, rank)))
+        ad.load(i, a13, b13, a2, b2, scale=0.5)
+        for e in range(E):
+            up[i][e], dn[i][e] = (f64(a13[e]), f64(b13[e]), 0.5), (f64(a2[e]), f64(b2[e]), 0.5)
+    x, R = torch.randn(T, H, device=DEV).bfloat16(), T * k
+    t = list(map(dev, (ids, off, order, pos)))
+    tad, w = dev(adapter), torch.rand(T, k, device=DEV)
+    B = lora.LoraBuffers(T, H, I, E, k, max_rank=rank, h_f32=wide, out_f32=True, device=DEV)
+    assert B.gu.numel() > 1 << 31 and B.h.numel() * 2 > 1 << 31
+    for i in range(0, R, 1 << 17):
+        B.gu[i:i + (1 << 17)].normal_()
+    h = lora.gateup_silu(ad, x, tad, B.gu, *t[:3], B)
+    some = np.unique(np.concatenate([[0, R - 1], rng.integers(0, R, 60), rng.integers(R - 2000, R, 20)]))
+    rows = [(int(order[r]) // k, int(ids.ravel()[order[r]])) for r in some]
+    want, bound = O.gateup(f64(B.gu[some]), f64(x), rows, adapter, up, [I] * E, I, not wide)
+    assert (np.abs(f64(h[some]) - want) <= bound).all()
+    base = torch.randn(T, H, device=DEV)
+    out = lora.down_combine(ad, h, base, tad, w, *t, B)
+    tok = np.unique(np.concatenate([[0, T - 1], rng.integers(0, T, 20)]))
+    n = len(tok)
+    all_rows = {int(r): (i, int(ids[q, j])) for i, q in enumerate(tok) for j, r in enumerate(pos.reshape(T, k)[q])}
+    want, bound = O.down(f64(base[tok]), Far(h), all_rows, adapter[tok], dn, [I] * E, f64(w[tok]),
+                         pos.reshape(T, k)[tok].ravel(), np.ones((n, 0)), n, k, False)
+    assert (np.abs(f64(out[tok]) - want) <= bound).all()
+    assert B.error_word() == 0
+    del B, h, out
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("T", [20, 900])
+def test_two_graphs_share_buffers_and_adapters_change_between_replays(lora, T):
+    d = make(lora, T, 128, 64, 6, 3, 1, 64, 3, (8, 16), none=0.0, seed=61)
+    other = {**d, "x": torch.randn_like(d["x"]), "h": torch.randn(d["h"].shape, device=DEV).to(d["h"].dtype)}
+    graphs = []
+    torch.cuda.synchronize()
+    for q in (d, other):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run_gateup(lora, q)
+            run_down(lora, q)
+        graphs.append(g)
+    rng = np.random.default_rng(62)
+    for i in range(4):
+        for g, q in zip(graphs, (d, other)):
+            g.replay()
+            h, out = d["B"].h.clone(), d["B"].out.clone()
+            assert torch.equal(h, run_gateup(lora, q)) and torch.equal(out, run_down(lora, q))
+        torch.cuda.synchronize()
+        r = (8, 16)[i % 2]
+        bf = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32) * 0.2).bfloat16().to(DEV)
+        d["ad"].load(i % 3, bf(6, 2 * r, 128), bf(6, 128, r), bf(6, r, 64), bf(6, 128, r), scale=0.5)
+
+
+@pytest.mark.parametrize("kind", ["stream", "handle"])
+def test_adapters_are_loaded_on_the_stream_that_uses_them(lora, kind):
+    d = make(lora, 40, 128, 64, 4, 2, 0, 0, 2, (8,), none=0.0, seed=63)
+    side = torch.cuda.Stream()
+    arg = side if kind == "stream" else side.cuda_stream
+    busy = torch.randn(4096, 4096, device=DEV)
+    rng = np.random.default_rng(64)
+    for i in range(4):
+        m = [torch.from_numpy(rng.standard_normal(s).astype(np.float32) * 0.2).bfloat16().to(DEV)
+             for s in ((4, 16, 128), (4, 128, 8), (4, 8, 64), (4, 128, 8))]
+        side.wait_stream(torch.cuda.current_stream())
+        for _ in range(5):
+            busy @ busy                               # the current stream is behind
+        d["ad"].load(i % 2, *m, scale=0.5, stream=arg)
+        for e in range(4):
+            d["up"][i % 2][e] = (f64(m[0][e]), f64(m[1][e]), 0.5)
+            d["dn"][i % 2][e] = (f64(m[2][e]), f64(m[3][e]), 0.5)
+        del m                                         # its memory may go to the current stream's work
+        torch.randn(4, 128, 8, device=DEV)
+        h, out = run_gateup(lora, d, stream=arg), run_down(lora, d, stream=arg)
+        side.synchronize()
+        check_gateup(d, h)
+        check_down(d, out)
