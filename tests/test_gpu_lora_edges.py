@@ -363,3 +363,19 @@ def test_adapters_are_loaded_on_the_stream_that_uses_them(lora, kind):
         side.synchronize()
         check_gateup(d, h)
         check_down(d, out)
+
+
+@pytest.mark.parametrize("T,held,room", [(5, 8, 128), (60, 24, 40), (2400, 8, 40), (2400, 16, 128)])
+def test_buffers_for_higher_ranks_than_the_adapters_have(lora, T, held, room):
+    d = make(lora, T, 4096, 64, 5, 3, 1, 96, 3, (8, held), seed=71)
+    d["B"] = lora.LoraBuffers(T, 4096, 64, 5, 3, 1, 96, room, device=DEV)
+    assert (block_of(d) > 0) == (T > 60)
+    check_gateup(d, run_gateup(lora, d))
+    check_down(d, run_down(lora, d))
+    assert d["B"].error_word() == 0
+
+
+def test_no_tokens(lora):
+    d = make(lora, 0, 64, 32, 4, 2, 1, 64, 2, (8,), seed=72)
+    assert run_gateup(lora, d).shape == (0, 64) and run_down(lora, d).shape == (0, 64)
+    assert d["B"].error_word() == 0
