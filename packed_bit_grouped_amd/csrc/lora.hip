@@ -31,7 +31,8 @@
 // What the calls measured (H 2048, I 512, 256 experts and a shared one, 8 a token,
 // rank 16; in a graph): one token gate/up 9.7 us, down 7.9; 64 tokens over 32
 // adapters 26 and 14 (the matrices at 3.5 and 3.2 TB/s); 4096 tokens over 4
-// adapters 110 (3.4 TB/s of what has to be moved) and 115 (1.5).
+// adapters 110 (3.4 TB/s of what has to be moved) and 116 (1.5); with h in fp32 125
+// and 130.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -56,7 +57,8 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
 }
 
 // fp32 as three bf16 numbers that sum to it: cut off, cut off, the rest (8 bits
-// at most).  Infinities and NaN are in the first alone.
+// at most; below 2^-133, bf16's smallest step, it is dropped).  Infinities and NaN
+// are in the first alone.
 __device__ __forceinline__ void split3(float f, uint32_t& a, uint32_t& b, uint32_t& c) {
   uint32_t u = __float_as_uint(f);
   const uint32_t mag = u & 0x7FFFFFFFu;
@@ -1150,14 +1152,18 @@ __global__ __launch_bounds__(64 * kDownWaves) void lora_down_small_kernel(LoraAr
 // them base, out and the units on their way; LDS additions without return were five times slower (500 us),
 // sums by tokens without any reuse of B four times (381), and rows of y through
 // memory as in the shared projection would be 600 MB.  What bounds it is no rate but
-// the way of a unit through a wave, about 200 ns: without B's loads, without v's or
-// without the sums' reads and writes it was 3 to 6 us shorter.  128 columns of 256
-// tokens (101 to 128 us), waves that divide the adapters (104), v through LDS once
-// for all waves (102), products over 16 ranks with 8-byte loads (119) and batches of
-// 8 units (99) were slower.
+// the way of a unit through a wave, some 165 ns of 434 units a block: 80 MB at the
+// device's memory are 0.9 TB/s, LDS is busy for 31% of the cycles, the matrix cores
+// for 11%; a SIMD's one wave issues 25 vector instructions a unit, 24% of its cycles,
+// and waits in 41%.  Without B's loads it took 85 us, without v's 89, without either
+// 81, without the sums' reads and writes 86.  128 columns of 256 tokens (101 to 128
+// us), 64 columns of 256 with two workgroups a compute unit (114), waves that divide
+// the adapters (104), v through LDS once for all waves (102), products over 16 ranks
+// with 8-byte loads (119) and batches of 8 units (99) were slower; two parts of v in
+// one product for ranks up to 16 gained 2 us and is not worth a variant.
 // A token's 64 sums are 16 chunks of 4; chunk q lies at q ^ (token % 16), so that
 // the 16 tokens of a unit spread over the banks.
-constexpr int kUnitsAtOnce = 128;  // in LDS; a segment of a prompt has about 75 (segments of 8 windows 96 us, 16 88, 32 95)
+constexpr int kUnitsAtOnce = 128;  // in LDS; a segment of a prompt has about 100 (segments of 8 windows 96 us, 16 88, 32 95)
 constexpr int kUnitsAhead = 16;    // and behind them some that do nothing: what the loop reads past its end
 
 template <int KB>   // steps of 32 ranks
@@ -1423,6 +1429,13 @@ hipError_t launch_accumulate(const LoraArgs& a, hipStream_t st) {
 // and 302, 18432 rows 348 and 261, 36864 rows 662 and 302; 4 adapters: 4104 rows 83
 // and 90, 8208 rows 138 and 106, 36864 rows 590 and 115; on 33 experts, rank 64: 576
 // rows 37 and 67, 1440 rows 71 and 53, 4104 rows 157 and 52.
+//
+// The constants come from H 2048, I 512.  At H 4096 with I 1536 and 14336, 8 to 256
+// experts and ranks 16, 64 and 128 (22 sizes of 720 to 32768 rows) both rules took the
+// faster way, or one within 5% of it, at 20: 2000 rows of one adapter of rank 128 on
+// 8 experts 64 against 510 gate/up, 50 against 406 down.  They miss at 800 rows of rank
+// 16 on 8 experts (one launch: 68 and 60, three 31 and 22) and 2000 of rank 16 on
+// 256 (129 and 124, three 104 and 74).
 void lora_choose(LoraArgs& a, bool most) {
   a.block = a.n_blocks = a.win = 0;
   a.large = a.R > kLoraFewRows;
